@@ -17,5 +17,8 @@ from ._lib import (  # noqa: F401
     dak_probe_concurrent, dak_probe_read_bw, dak_selftest_link, dak_selftest_wait, dak_sm_count,
     dak_tune_attn, dak_tune_gemm, dak_tuning, host_requests_for_ratio, host_heads_for_ratio,
     host_tiles_for_ratio, lib, load_tuning, place_decoder_layer, save_tuning, tuning_to_dict,
+    ROPE_SCALINGS, dak_attn_acc, dak_attn_acc_workspace_bytes, dak_attn_prefix, dak_attn_prefix_workspace_bytes,
+    dak_kv_append_rope, dak_kv_evict, dak_kv_evict_workspace_bytes, dak_rope_config, dak_rope_from_freqs,
+    dak_rope_make, dak_rope_plan,
 )
 from .modules import SplitK_FlashAttn, SplitK_GEMM  # noqa: F401,E402

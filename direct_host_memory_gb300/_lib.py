@@ -32,8 +32,13 @@ EXPORTS = [
     "dak_place_matrix_glu", "dak_plan_units", "dak_gemm_workspace_bytes", "dak_gemm_ws", "dak_gemm_plan", "dak_gemm_launch_plan",
     "dak_attn_f32", "dak_inject_fault", "dak_fault_pending", "dak_alloc_counts", "dak_gemm_chain",
     "dak_gemm_chain_workspace_bytes", "dak_link_begin", "dak_link_timeouts", "dak_selftest_link",
-    "dak_place_kv_heads", "dak_kv_append", "dak_gemm_chain_plan",
+    "dak_place_kv_heads", "dak_kv_append", "dak_gemm_chain_plan", "dak_placement_data", "dak_rope_make",
+    "dak_rope_from_freqs", "dak_kv_append_rope", "dak_kv_evict_workspace_bytes", "dak_kv_evict",
+    "dak_attn_acc_workspace_bytes", "dak_attn_acc", "dak_attn_prefix_workspace_bytes", "dak_attn_prefix",
 ]
+
+# position scalings of dak_rope_make (DAK_ROPE_* in dak.h)
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 # host-side fault injection kinds (DAK_FAULT_* in dak.h)
 FAULT_HOST_ALLOC, FAULT_DEVICE_ALLOC, FAULT_TENSOR_MAP = 1, 2, 3
@@ -81,6 +86,17 @@ class dak_gemm_plan_info(ctypes.Structure):
         "tile_m", "cluster_slots")]
 
 
+class dak_rope_config(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("orig_len", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double), ("attn_scale", ctypes.c_double)]
+
+
+class dak_rope_plan(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("scale", ctypes.c_float), ("turns", ctypes.c_uint64 * 64)]
+
+
 class dak_decoder_config(ctypes.Structure):
     _fields_ = [("n_layers", ctypes.c_int), ("hidden", ctypes.c_int), ("n_heads", ctypes.c_int),
                 ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("ffn", ctypes.c_int),
@@ -125,6 +141,18 @@ def _load():
         "dak_attn_staged": (i32, [vp, vp, vp, vp, i32, ctypes.c_float, vp, vp, sz, P(dak_tuning), vp]),
         "dak_attn_f32": (i32, [vp, vp, vp, i32, ctypes.c_float, vp, vp, sz, P(dak_tuning), vp]),
         "dak_attn_default_split": (i32, [vp]),
+        "dak_placement_data": (i32, [vp, P(vp), P(vp)]),
+        "dak_rope_make": (i32, [i32, P(dak_rope_config), P(dak_rope_plan)]),
+        "dak_rope_from_freqs": (i32, [i32, P(dbl), i32, i32, dbl, P(dak_rope_plan)]),
+        "dak_kv_append_rope": (i32, [vp, P(dak_rope_plan), vp, vp, vp, i32, i32, i32, i64, i64, i64, vp, vp, vp, vp,
+                                     vp, vp]),
+        "dak_kv_evict_workspace_bytes": (sz, [vp]),
+        "dak_kv_evict": (i32, [vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "dak_attn_acc_workspace_bytes": (sz, [vp, i32, i32]),
+        "dak_attn_acc": (i32, [vp, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp, vp, sz, P(dak_tuning), vp]),
+        "dak_attn_prefix_workspace_bytes": (sz, [vp, vp, i32, i32, i32]),
+        "dak_attn_prefix": (i32, [vp, vp, vp, vp, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp, vp, sz, P(dak_tuning),
+                                  vp]),
         "dak_plan_ratios": (i32, [P(dak_op), i32, dbl, dbl, dbl, i32, P(dbl), P(dbl)]),
         "dak_plan_units": (i32, [P(dak_op), i32, dbl, dbl, dbl, P(i64), P(dbl)]),
         "dak_last_error": (i32, [vp, P(ctypes.c_uint64)]),
@@ -198,6 +226,14 @@ def _on_device(x) -> int:
     return 0 if isinstance(x, np.ndarray) else int(x.is_cuda)
 
 
+class _DeviceMemory:
+    """Device memory of a placement for torch.as_tensor (16-bit words; keeps the placement alive)."""
+
+    def __init__(self, placement, ptr, shape):
+        self._placement = placement
+        self.__cuda_array_interface__ = {"shape": shape, "typestr": "<i2", "data": (ptr, False), "version": 2}
+
+
 class Placement:
     """A library-owned placement (dak_placement*). Free with .free() or by dropping it."""
 
@@ -216,6 +252,31 @@ class Placement:
         if self._h is None:
             raise ValueError("placement already freed")
         return self._h
+
+    def slabs(self):
+        """The parts of a placed KV cache as bf16 tensors that share its memory: (host, hbm), the
+        pinned part on the CPU and the HBM part on the GPU, each [slabs of that tier][chunks of 64
+        tokens][K, V][64][D] (dak_placement_data in dak.h says how a row is laid out), or None
+        where the placement has none in that tier. The caller orders its reads after the work
+        that writes the cache, and drops them before the placement is freed by .free()."""
+        import torch
+        if self.kind != "kv":
+            raise ValueError("slabs() is for KV placements")
+        host, hbm = ctypes.c_void_p(), ctypes.c_void_p()
+        _check(lib.dak_placement_data(self.handle, ctypes.byref(host), ctypes.byref(hbm)), "dak_placement_data")
+        tail = (-(-self.meta["L"] // 64), 2, 64, self.meta["D"])
+        out = []
+        for ptr, n, on_gpu in ((host.value, self.host_units, False), (hbm.value, self.units - self.host_units, True)):
+            if not ptr or not n:
+                out.append(None)
+            elif on_gpu:
+                mem = _DeviceMemory(self, ptr, (n,) + tail)
+                out.append(torch.as_tensor(mem).view(torch.bfloat16))
+            else:
+                mem = (ctypes.c_int16 * (n * int(np.prod(tail)))).from_address(ptr)
+                mem._placement = self
+                out.append(torch.from_numpy(np.ctypeslib.as_array(mem)).view(torch.bfloat16).view((n,) + tail))
+        return tuple(out)
 
     def free(self):
         if self._h is not None:
@@ -532,6 +593,223 @@ def dak_attn_noalloc(Q, KV: Placement, O, seq_lens=None, scale: float = 0.0, tun
                           f"{NOALLOC_SCRATCH_BYTES}-byte array; use dak_attn with a workspace")
     _check(lib.dak_attn_noalloc(_ptr(Q), KV.handle, _ptr(seq_lens), Hq, float(scale), _ptr(O), _tuning(tuning),
                                 _stream_ptr(stream)), "dak_attn_noalloc")
+    return O
+
+
+# ------------------------------------------------------------------------------- rotation, append, eviction
+
+def dak_rope_make(head_dim: int, rot_dim: int = 0, theta: float = 0.0, interleaved: bool = False,
+                  scaling: str = "none", factor: float = 1.0, orig_len: float = 0.0, low_turns: float = 0.0,
+                  high_turns: float = 0.0, attn_scale: float = 1.0) -> dak_rope_plan:
+    """The rotation of dak_kv_append_rope for heads of head_dim elements of which the first
+    rot_dim (0 = all) turn, in halves or interleaved pairs, with scaling one of "none",
+    "linear", "ntk", "by_parts" (dak_rope_config in dak.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    c = dak_rope_config(rot_dim=int(rot_dim), interleaved=int(bool(interleaved)), scaling=ROPE_SCALINGS[scaling],
+                        theta=float(theta), factor=float(factor), orig_len=float(orig_len),
+                        low_turns=float(low_turns), high_turns=float(high_turns), attn_scale=float(attn_scale))
+    out = dak_rope_plan()
+    _check(lib.dak_rope_make(int(head_dim), ctypes.byref(c), ctypes.byref(out)), "dak_rope_make")
+    return out
+
+
+def dak_rope_from_freqs(head_dim: int, inv_freq, interleaved: bool = False, attn_scale: float = 1.0) -> dak_rope_plan:
+    """The same from given frequencies (radians per position, one per pair)."""
+    f = [float(x) for x in inv_freq]
+    out = dak_rope_plan()
+    _check(lib.dak_rope_from_freqs(int(head_dim), (ctypes.c_double * max(1, len(f)))(*f), len(f),
+                                   int(bool(interleaved)), float(attn_scale), ctypes.byref(out)), "dak_rope_from_freqs")
+    return out
+
+
+def _i32_cuda(t, name, shape):
+    """A contiguous int32 CUDA tensor of this shape (None stays None)."""
+    import torch
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32 and t.is_contiguous()
+            and tuple(t.shape) == shape):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)}")
+    return t
+
+
+def _f32_cuda(t, name, shape):
+    import torch
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.float32 and t.is_contiguous()
+            and tuple(t.shape) == shape):
+        raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor {list(shape)}")
+    return t
+
+
+def _token_rows(t, name, B, T, heads, D, dtype):
+    """Pitch in elements between the tokens of t [B][T][heads][D] (T = 1: also [B][heads][D]), whose
+    tokens lie at one pitch with each token's heads contiguous, as in a slice of a packed
+    projection."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
+    shape, st = tuple(t.shape), t.stride()
+    if T == 1 and shape == (B, heads, D):
+        row, head, el = st
+        ok = True
+    elif shape == (B, T, heads, D):
+        row, head, el = (st[1] if T > 1 else st[0]), st[2], st[3]
+        ok = T == 1 or B == 1 or st[0] == T * st[1]
+    else:
+        raise ValueError(f"{name} must be [B={B}][T={T}][{heads}][{D}]")
+    if not ok or el != 1 or (heads > 1 and head != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous and its tokens at one pitch")
+    return heads * D if B * T == 1 else row
+
+
+def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slots, positions=None, n_new=None,
+                       q_out=None, slot_pos=None, stream=None):
+    """Rotate new tokens and append them to a placed cache (dak.h): q [B][T][H_q][D] (or None),
+    k_new and v_new [B][T][H_kv][D], bf16 or fp32 CUDA, slices of one projection's output as
+    they are (T = 1: the T axis may be absent); slots, positions, n_new int32 CUDA [B];
+    slot_pos int32 CUDA [B][H_kv][L], updated in place. Returns q_out, bf16, shaped as q (None
+    without q)."""
+    import torch
+    B, Hkv, D, L = KV.meta["B"], KV.meta["H_kv"], KV.meta["D"], KV.meta["L"]
+    T = int(k_new.shape[1]) if k_new.ndim == 4 else 1
+    dtype = k_new.dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("k_new must be bf16 or fp32")
+    kp = _token_rows(k_new, "k_new", B, T, Hkv, D, dtype)
+    vp = _token_rows(v_new, "v_new", B, T, Hkv, D, dtype)
+    Hq = qp = 0
+    if q is not None:
+        Hq = int(q.shape[-2])
+        qp = _token_rows(q, "q", B, T, Hq, D, dtype)
+        if q_out is None:
+            q_out = torch.empty(tuple(q.shape), dtype=torch.bfloat16, device=q.device)
+        _check_bf16_cuda(q_out, "q_out")
+        if tuple(q_out.shape) != tuple(q.shape):
+            raise ValueError("q_out must be shaped as q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _i32_cuda(slots, "slots", (B,))
+    _i32_cuda(positions, "positions", (B,))
+    _i32_cuda(n_new, "n_new", (B,))
+    _i32_cuda(slot_pos, "slot_pos", (B, Hkv, L))
+    _check(lib.dak_kv_append_rope(KV.handle, ctypes.byref(rope), _ptr(q), _ptr(k_new), _ptr(v_new),
+                                  int(dtype == torch.float32), T, Hq, qp, kp, vp, _ptr(slots), _ptr(positions),
+                                  _ptr(n_new), _ptr(q_out), _ptr(slot_pos), _stream_ptr(stream)), "dak_kv_append_rope")
+    return q_out
+
+
+def dak_kv_evict_workspace_bytes(KV: Placement) -> int:
+    return int(lib.dak_kv_evict_workspace_bytes(KV.handle))
+
+
+def dak_kv_evict(KV: Placement, seq_lens, n_keep: int, n_recent: int, acc, slot_pos, acc_out=None, slot_pos_out=None,
+                 lens_out=None, src_out=None, workspace=None, stream=None):
+    """Keep n_keep slots of every (request, kv head) of a placed cache that holds more: the
+    n_recent newest positions, then the largest accumulated weights (dak.h). acc fp32 and
+    slot_pos int32 CUDA [B][H_kv][L], updated in place unless acc_out / slot_pos_out are
+    given; seq_lens int32 CUDA [B]. Returns (lens_out [B], src_out [B][H_kv][n_keep]), int32:
+    the new lengths, and the slot each kept row came from (-1 past the length)."""
+    import torch
+    B, Hkv, L = KV.meta["B"], KV.meta["H_kv"], KV.meta["L"]
+    acc_out = acc if acc_out is None else acc_out
+    slot_pos_out = slot_pos if slot_pos_out is None else slot_pos_out
+    _i32_cuda(seq_lens, "seq_lens", (B,))
+    _f32_cuda(acc, "acc", (B, Hkv, L))
+    _f32_cuda(acc_out, "acc_out", (B, Hkv, L))
+    _i32_cuda(slot_pos, "slot_pos", (B, Hkv, L))
+    _i32_cuda(slot_pos_out, "slot_pos_out", (B, Hkv, L))
+    if not 1 <= int(n_keep) <= L:
+        raise DakError(1, f"dak_kv_evict: n_keep {n_keep} outside 1..{L}")
+    if lens_out is None:
+        lens_out = torch.empty(B, dtype=torch.int32, device=acc.device)
+    if src_out is None:
+        src_out = torch.empty((B, Hkv, int(n_keep)), dtype=torch.int32, device=acc.device)
+    _i32_cuda(lens_out, "lens_out", (B,))
+    _i32_cuda(src_out, "src_out", (B, Hkv, int(n_keep)))
+    if workspace is None:
+        workspace = torch.empty(dak_kv_evict_workspace_bytes(KV), dtype=torch.uint8, device=acc.device)
+    _check(lib.dak_kv_evict(KV.handle, _ptr(seq_lens), int(n_keep), int(n_recent), _ptr(acc), _ptr(acc_out),
+                            _ptr(slot_pos), _ptr(slot_pos_out), _ptr(lens_out), _ptr(src_out), _ptr(workspace),
+                            workspace.numel() * workspace.element_size(), _stream_ptr(stream)), "dak_kv_evict")
+    return lens_out, src_out
+
+
+# ------------------------------------------------------------------------------- attention for serving
+
+def _n_split_of(tuning) -> int:
+    if isinstance(tuning, dak_tuning):
+        return int(tuning.n_split)
+    return int(dict(tuning or {}).get("n_split", 0) or 0)
+
+
+def _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out):
+    import torch
+    _check_bf16_cuda(Q, "Q")
+    B, Hkv, D, L = KV.meta["B"], KV.meta["H_kv"], KV.meta["D"], KV.meta["L"]
+    if Q.ndim != 3 or int(Q.shape[0]) != B or int(Q.shape[2]) != D:
+        raise ValueError("Q must be [B][H_q][D] of the KV placement's B and D")
+    dtype = torch.float32 if o_fp32 else torch.bfloat16
+    if O is None:
+        O = torch.empty(tuple(Q.shape), dtype=dtype, device=Q.device)
+    elif not (O.is_cuda and O.dtype == dtype and O.is_contiguous() and tuple(O.shape) == tuple(Q.shape)):
+        raise ValueError(f"O must be a contiguous {dtype} CUDA tensor shaped like Q")
+    _i32_cuda(seq_lens, "seq_lens", (B,))
+    _f32_cuda(acc_in, "acc_in", (B, Hkv, L))
+    _f32_cuda(acc_out, "acc_out", (B, Hkv, L))
+    return int(Q.shape[1]), O
+
+
+def dak_attn_acc_workspace_bytes(KV: Placement, H_q: int, n_split: int = 0) -> int:
+    return int(lib.dak_attn_acc_workspace_bytes(KV.handle, int(H_q), int(n_split)))
+
+
+def dak_attn_acc(Q, KV: Placement, acc_in=None, acc_out=None, seq_lens=None, scale: float = 0.0, O=None,
+                 o_fp32: bool = False, workspace=None, tuning=None, stream=None):
+    """dak_attn that adds every position's attention weight, summed over the query heads of its
+    kv head, to acc_in fp32 [B][H_kv][L] (None = zeros). Returns (O, acc_out); acc_out may be
+    acc_in; without one, a new tensor that is zero behind each request's tokens."""
+    import torch
+    if acc_out is None:
+        acc_out = torch.zeros((KV.meta["B"], KV.meta["H_kv"], KV.meta["L"]), dtype=torch.float32, device=Q.device)
+    Hq, O = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out)
+    if workspace is None:
+        workspace = torch.empty(dak_attn_acc_workspace_bytes(KV, Hq, _n_split_of(tuning)), dtype=torch.uint8,
+                                device=Q.device)
+    _check(lib.dak_attn_acc(_ptr(Q), KV.handle, _ptr(seq_lens), Hq, float(scale), _ptr(O), int(bool(o_fp32)),
+                            _ptr(acc_in), _ptr(acc_out), _ptr(workspace),
+                            workspace.numel() * workspace.element_size(), _tuning(tuning), _stream_ptr(stream)),
+           "dak_attn_acc")
+    return O, acc_out
+
+
+def dak_attn_prefix_workspace_bytes(KV: Placement, prefix: Placement, H_q: int, n_split: int = 0,
+                                    with_acc: bool = False) -> int:
+    return int(lib.dak_attn_prefix_workspace_bytes(KV.handle, prefix.handle, int(H_q), int(n_split), int(bool(with_acc))))
+
+
+def dak_attn_prefix(Q, KV: Placement, prefix: Placement, prefix_of=None, prefix_lens=None, seq_lens=None, acc_in=None,
+                    acc_out=None, scale: float = 0.0, O=None, o_fp32: bool = False, workspace=None, tuning=None,
+                    stream=None):
+    """Decode attention of requests that share prefixes: request b attends over the first
+    prefix_lens[prefix_of[b]] rows of prefix placement slab prefix_of[b] (negative: none; None:
+    prefix 0 for all) and over its own seq_lens[b] cached tokens. Each prefix is read once for
+    all its requests. acc_out, if given, takes acc_in (None = zeros) plus the weights of the own
+    cache's positions, as in dak_attn_acc. Returns O."""
+    import torch
+    Hq, O = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out)
+    if acc_in is not None and acc_out is None:
+        raise ValueError("acc_in without acc_out")
+    _i32_cuda(prefix_of, "prefix_of", (KV.meta["B"],))
+    _i32_cuda(prefix_lens, "prefix_lens", (prefix.meta["B"],))
+    if workspace is None:
+        workspace = torch.empty(dak_attn_prefix_workspace_bytes(KV, prefix, Hq, _n_split_of(tuning), acc_out is not None),
+                                dtype=torch.uint8, device=Q.device)
+    _check(lib.dak_attn_prefix(_ptr(Q), KV.handle, _ptr(seq_lens), prefix.handle, _ptr(prefix_lens), _ptr(prefix_of), Hq,
+                               float(scale), _ptr(O), int(bool(o_fp32)), _ptr(acc_in), _ptr(acc_out), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _tuning(tuning), _stream_ptr(stream)),
+           "dak_attn_prefix")
     return O
 
 

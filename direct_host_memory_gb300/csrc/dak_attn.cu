@@ -51,6 +51,13 @@ struct AttnParams {
     // host-link handoff of a decode step (link_wait / link_signal; null = off)
     unsigned* link;
     unsigned link_after;
+    // attn_kernel<.., EXT>: partials are always written; scores, if not null, takes every
+    // scaled score (log2 domain) [B][Hq][score_pitch]
+    float* scores;
+    int score_pitch;
+    // EXT over a shared prefix: unit (b, g, s) reads slab (prefix_of[b], g) of n_prefix
+    const int* prefix_of;
+    int n_prefix;
 };
 
 constexpr int kChunkTok = 64;
@@ -88,6 +95,26 @@ struct Unit {
     const uint8_t* base;  // the (request, kv head) slab
 };
 
+// The same for a pass over the requests' prefixes: slabs of either tier, each CTA taking any.
+__device__ __forceinline__ Unit decode_prefix_unit(const AttnParams& p, long long u) {
+    Unit x;
+    const int per_b = p.Hkv * p.n_split;
+    x.b = static_cast<int>(u / per_b);
+    const int rem = static_cast<int>(u - static_cast<long long>(x.b) * per_b);
+    x.g = rem / p.n_split;
+    x.s = rem - x.g * p.n_split;
+    const int e = p.prefix_of ? p.prefix_of[x.b] : 0;
+    const int f = e >= 0 && e < p.n_prefix ? e : -1;
+    if (e >= p.n_prefix) report(p.st, DAK_ERR_BOUNDS, (0x9F1Full << 32) | static_cast<unsigned>(x.b));
+    x.Lb = f < 0 ? 0 : p.L;
+    if (f >= 0 && p.seq_lens) x.Lb = min(max(p.seq_lens[f], 0), p.L);
+    x.t0 = x.s * p.split_len;
+    x.t1 = min(x.Lb, x.t0 + p.split_len);
+    const long long slab = static_cast<long long>(max(f, 0)) * p.Hkv + x.g;
+    x.base = slab < p.h_s ? p.kv[0] + slab * p.head_bytes : p.kv[1] + (slab - p.h_s) * p.head_bytes;
+    return x;
+}
+
 __device__ __forceinline__ Unit decode_unit(const AttnParams& p, long long u, int tier) {
     Unit x;
     const int per_b = p.Hkv * p.n_split;
@@ -123,11 +150,23 @@ __device__ __forceinline__ void split_bf16(float v0, float v1, uint32_t& hi, uin
     lo = pack_bf16(v0 - __bfloat162float(h0), v1 - __bfloat162float(h1));
 }
 
+// The bf16 pair of what hi and lo of split_bf16 leave of two fp32 values.
+__device__ __forceinline__ uint32_t third_bf16(float v0, float v1, uint32_t hi, uint32_t lo) {
+    return pack_bf16(v0 - bf_lo(hi) - bf_lo(lo), v1 - bf_hi(hi) - bf_hi(lo));
+}
+
+// Mask of a bf16 pair of which the first n elements count.
+__device__ __forceinline__ uint32_t pair_mask(int n) { return n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u; }
+
 __device__ __forceinline__ void named_bar_consumers() {
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttnConsumers) : "memory");
 }
 
-template <int D, bool SPLIT_P>
+// PARTS: bf16 parts of P that enter P.V. EXT: kExtNone = dak_attn; kExtOwn / kExtPrefix = the
+// passes of dak_attn_acc and dak_attn_prefix, which leave partials for their own merge.
+enum { kExtNone = 0, kExtOwn = 1, kExtPrefix = 2 };
+
+template <int D, int PARTS, int EXT>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
     constexpr int KS = D / 16;                       // k-steps of the score MMA
     constexpr int NB = D / 8;                        // 8-wide column blocks of O
@@ -162,7 +201,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
             long long i = 0;
             bool waited = false;
             for (long long u = ur.begin; u < ur.end && !*abort; ++u) {
-                const Unit x = decode_unit(p, u, ur.tier);
+                const Unit x = EXT == kExtPrefix ? decode_prefix_unit(p, u) : decode_unit(p, u, ur.tier);
                 for (int t = x.t0; t < x.t1; t += kChunkTok, ++i) {
                     const int s = static_cast<int>(i % W);
                     if (p.wait_newest && !waited && t + kChunkTok >= x.Lb) {
@@ -200,7 +239,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     long long i = 0;
     bool failed = false;  // a wait ran out: skip the math but keep meeting the named barriers
     for (long long u = ur.begin; u < ur.end; ++u) {
-        const Unit x = decode_unit(p, u, ur.tier);
+        const Unit x = EXT == kExtPrefix ? decode_prefix_unit(p, u) : decode_unit(p, u, ur.tier);
         // Q fragments (A operand), rows >= G are zero
         uint32_t qa[KS][4];
         {
@@ -258,6 +297,22 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                         mx_b = fmaxf(mx_b, sc[nb][2 + e]);
                     }
                 }
+                if (EXT == kExtOwn && p.scores) {
+                    // tokens past the valid ones hold -inf and lie inside the padded row
+                    float* row = p.scores + (static_cast<long long>(x.b) * p.Hq + static_cast<long long>(x.g) * p.G) *
+                                                p.score_pitch + t + 16 * w + 2 * q4;
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb) {
+                        if (ra < p.G) {
+                            *reinterpret_cast<float2*>(row + static_cast<long long>(ra) * p.score_pitch + nb * 8) =
+                                make_float2(sc[nb][0], sc[nb][1]);
+                        }
+                        if (ra + 8 < p.G) {
+                            *reinterpret_cast<float2*>(row + static_cast<long long>(ra + 8) * p.score_pitch + nb * 8) =
+                                make_float2(sc[nb][2], sc[nb][3]);
+                        }
+                    }
+                }
                 mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 1));
                 mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 2));
                 mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 1));
@@ -289,13 +344,21 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                     o[nb][2] *= corr_b;
                     o[nb][3] *= corr_b;
                 }
-                // P as the A operand (16 rows x 16 tokens): hi = bf16(P), and with SPLIT_P also
-                // lo = bf16(P - hi), both multiplied into the same accumulators
+                // P as the A operand (16 rows x 16 tokens): hi = bf16(P), with two parts also
+                // lo = bf16(P - hi) and with three bf16(P - hi - lo), all multiplied into the
+                // same accumulators
                 uint32_t pa0, pa1, pa2, pa3, pl0, pl1, pl2, pl3;
+                uint32_t pt0 = 0, pt1 = 0, pt2 = 0, pt3 = 0;
                 split_bf16(pr[0][0], pr[0][1], pa0, pl0);
                 split_bf16(pr[0][2], pr[0][3], pa1, pl1);
                 split_bf16(pr[1][0], pr[1][1], pa2, pl2);
                 split_bf16(pr[1][2], pr[1][3], pa3, pl3);
+                if (PARTS == 3) {
+                    pt0 = third_bf16(pr[0][0], pr[0][1], pa0, pl0);
+                    pt1 = third_bf16(pr[0][2], pr[0][3], pa1, pl1);
+                    pt2 = third_bf16(pr[1][0], pr[1][1], pa2, pl2);
+                    pt3 = third_bf16(pr[1][2], pr[1][3], pa3, pl3);
+                }
                 // ---- O += P V
                 {
                     const int tok = 16 * w + (mi & 1) * 8 + rr;
@@ -305,11 +368,24 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                         const uint32_t addr = vs_base + static_cast<uint32_t>(tok * D * 2 + ((c ^ (tok & 7)) << 4));
                         uint32_t b0, b1, b2, b3;
                         ldsm_x4_t(addr, b0, b1, b2, b3);
+                        if (EXT != kExtNone && valid < 16) {
+                            // rows past the valid tokens may hold anything, also infinities and
+                            // NaN, which a probability of zero would not cancel
+                            const uint32_t lo = pair_mask(valid - 2 * q4), hi = pair_mask(valid - 8 - 2 * q4);
+                            b0 &= lo;
+                            b1 &= hi;
+                            b2 &= lo;
+                            b3 &= hi;
+                        }
                         mma_bf16_16816(o[2 * db], pa0, pa1, pa2, pa3, b0, b1);
                         mma_bf16_16816(o[2 * db + 1], pa0, pa1, pa2, pa3, b2, b3);
-                        if (SPLIT_P) {
+                        if (PARTS >= 2) {
                             mma_bf16_16816(o[2 * db], pl0, pl1, pl2, pl3, b0, b1);
                             mma_bf16_16816(o[2 * db + 1], pl0, pl1, pl2, pl3, b2, b3);
+                        }
+                        if (PARTS == 3) {
+                            mma_bf16_16816(o[2 * db], pt0, pt1, pt2, pt3, b0, b1);
+                            mma_bf16_16816(o[2 * db + 1], pt0, pt1, pt2, pt3, b2, b3);
                         }
                     }
                 }
@@ -365,7 +441,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                 lsum += f * row[D + 1];
             }
             const long long orow = static_cast<long long>(x.b) * p.Hq + static_cast<long long>(x.g) * p.G + r;
-            if (p.n_split == 1) {
+            if (EXT == kExtNone && p.n_split == 1) {
                 store_out(p.O, p.o_fp32, orow * D + d, lsum > 0.f ? acc / lsum : 0.f);
             } else {
                 float* wr = p.ws + (orow * p.n_split + x.s) * (D + 2);
@@ -481,6 +557,77 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_cta_kernel(const
     }
 }
 
+// Merge of dak_attn_acc and dak_attn_prefix: the partials of the own cache's n_own splits and of
+// the prefix's n_pre (either may be 0), in that order, into O as attn_combine does, and the
+// accumulated weights acc_out = acc_in + sum_r 2^(s_r - M_r) / l_r from the scores s that the own
+// pass left. Block (b, g) x y: y < G merges query head g * G + y, later ones take
+// kMergePositions positions of the slab each.
+struct MergeParams {
+    const float* own;  // [B][Hq][n_own][D + 2]
+    const float* pre;  // [B][Hq][n_pre][D + 2]
+    int n_own, n_pre;
+    void* O;
+    int o_fp32;
+    const float* scores;  // [B][Hq][score_pitch], log2 domain
+    int score_pitch;
+    const float* acc_in;  // [B][Hkv][L] or null
+    float* acc_out;       // null: no accumulation
+    const int* seq_lens;
+    int Hq, Hkv, G, L;
+};
+constexpr int kMergeThreads = 128;
+constexpr int kMergePositions = 512;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const MergeParams p) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const int b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv;
+    const long long row0 = static_cast<long long>(b) * p.Hq + static_cast<long long>(g) * p.G;
+    const int n = p.n_own + p.n_pre;
+    const auto part = [&](long long row, int s) {
+        return s < p.n_own ? p.own + (row * p.n_own + s) * (D + 2) : p.pre + (row * p.n_pre + s - p.n_own) * (D + 2);
+    };
+    const int tid = threadIdx.x;
+    if (static_cast<int>(blockIdx.y) < p.G) {
+        const long long row = row0 + blockIdx.y;
+        float M = -INFINITY;
+        for (int s = 0; s < n; ++s) M = fmaxf(M, part(row, s)[D]);
+        const float base = M == -INFINITY ? 0.f : M;
+        if (tid < D) {
+            float acc = 0.f, lsum = 0.f;
+            for (int s = 0; s < n; ++s) {
+                const float* ps = part(row, s);
+                const float f = exp2f(ps[D] - base);
+                lsum += f * ps[D + 1];
+                acc += f * ps[tid];
+            }
+            store_out(p.O, p.o_fp32, row * D + tid, lsum > 0.f ? acc / lsum : 0.f);
+        }
+        return;
+    }
+    const int L = p.seq_lens ? min(max(p.seq_lens[b], 0), p.L) : p.L;
+    const int j0 = (blockIdx.y - p.G) * kMergePositions;
+    if (j0 >= L) return;
+    __shared__ float Ms[16], rl[16];
+    if (tid < p.G) {
+        const long long row = row0 + tid;
+        float M = -INFINITY, l = 0.f;
+        for (int s = 0; s < n; ++s) M = fmaxf(M, part(row, s)[D]);
+        const float base = M == -INFINITY ? 0.f : M;
+        for (int s = 0; s < n; ++s) l += exp2f(part(row, s)[D] - base) * part(row, s)[D + 1];
+        Ms[tid] = base;
+        rl[tid] = l > 0.f ? 1.f / l : 0.f;
+    }
+    __syncthreads();
+    const long long slab = static_cast<long long>(blockIdx.x) * p.L;
+    for (int j = j0 + tid; j < min(j0 + kMergePositions, L); j += kMergeThreads) {
+        float w = 0.f;
+        for (int r = 0; r < p.G; ++r) w += exp2f(p.scores[(row0 + r) * p.score_pitch + j] - Ms[r]) * rl[r];
+        p.acc_out[slab + j] = (p.acc_in ? p.acc_in[slab + j] : 0.f) + w;
+    }
+}
+
 constexpr int kAttnDefaultHostCtas = 32;
 constexpr int kAttnDefaultHostWindow = 4;
 // Default ring depth: 2 stages (64 KiB in flight per CTA; three CTAs fit on an SM). Measured
@@ -515,8 +662,8 @@ template <int D>
 static int attn_ctas_per_sm(int W, int G) {
     int n = 0;
     const int smem = attn_smem_bytes<D>(W, G);
-    if (cudaFuncSetAttribute(attn_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<D, false>, kAttnThreads, smem) != cudaSuccess) {
+    if (cudaFuncSetAttribute(attn_kernel<D, 1, kExtNone>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<D, 1, kExtNone>, kAttnThreads, smem) != cudaSuccess) {
         cudaGetLastError();
         return 1;
     }
@@ -541,10 +688,19 @@ static cudaError_t launch_maybe_pdl(Kernel k, int grid, int threads, int smem, b
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
+// The passes of dak_attn_acc / dak_attn_prefix: partials only.
+template <int D, int EXT>
+static cudaError_t launch_attn_ext_d(const AttnParams& p, int grid, int W, bool pdl, cudaStream_t s) {
+    const int smem = attn_smem_bytes<D>(W, p.G);
+    auto k = p.o_fp32 ? attn_kernel<D, 3, EXT> : attn_kernel<D, 2, EXT>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e == cudaSuccess ? launch_maybe_pdl(k, grid, kAttnThreads, smem, pdl, s, p) : e;
+}
+
 template <int D>
 static cudaError_t launch_attn_d(const AttnParams& p, int grid, int W, bool pdl, cudaStream_t s) {
     const int smem = attn_smem_bytes<D>(W, p.G);
-    auto k = p.o_fp32 ? attn_kernel<D, true> : attn_kernel<D, false>;
+    auto k = p.o_fp32 ? attn_kernel<D, 2, kExtNone> : attn_kernel<D, 1, kExtNone>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     e = launch_maybe_pdl(k, grid, kAttnThreads, smem, pdl, s, p);
@@ -558,9 +714,17 @@ static cudaError_t launch_attn_d(const AttnParams& p, int grid, int W, bool pdl,
                             static_cast<const float*>(p.ws), p.O, p.o_fp32, p.n_split);
 }
 
+// ext: the own-cache pass of dak_attn_acc / dak_attn_prefix (partials into ws, scores), with a
+// workspace that the caller has checked.
+struct AttnExt {
+    float* scores = nullptr;
+    int score_pitch = 0;
+};
+
 static dak_status launch_attn_kernels(const void* Q, const dak_placement* KV, const void* host_src,
                                       const int* seq_lens, int H_q, float scale, void* O, void* ws, size_t ws_bytes,
-                                      const dak_tuning* t, cudaStream_t stream, int o_fp32, const LinkHandoff* link) {
+                                      const dak_tuning* t, cudaStream_t stream, int o_fp32, const LinkHandoff* link,
+                                      const AttnExt* ext = nullptr) {
     if (link && link->signals) *link->signals = 0;
     if (!KV || KV->kind != 1 || !Q || !O) return DAK_ERR_INVALID;
     if (H_q <= 0 || H_q % KV->H_kv) return DAK_ERR_INVALID;
@@ -626,7 +790,15 @@ static dak_status launch_attn_kernels(const void* Q, const dak_placement* KV, co
         p.link = link->ctr;
         p.link_after = link->after;
     }
-    cudaError_t e = KV->D == 128 ? launch_attn_d<128>(p, grid, W, pdl, stream) : launch_attn_d<64>(p, grid, W, pdl, stream);
+    cudaError_t e;
+    if (ext) {
+        p.scores = ext->scores;
+        p.score_pitch = ext->score_pitch;
+        e = KV->D == 128 ? launch_attn_ext_d<128, kExtOwn>(p, grid, W, pdl, stream)
+                         : launch_attn_ext_d<64, kExtOwn>(p, grid, W, pdl, stream);
+    } else {
+        e = KV->D == 128 ? launch_attn_d<128>(p, grid, W, pdl, stream) : launch_attn_d<64>(p, grid, W, pdl, stream);
+    }
     if (e == cudaSuccess && link && link->signals && p.link) *link->signals = p.n_host_ctas;
     return cuda_status(e);
 }
@@ -646,6 +818,124 @@ dak_status launch_attn(const void* Q, const dak_placement* KV, const void* host_
         launch_attn_kernels(Q, KV, host_src, seq_lens, H_q, scale, O, ws, ws_bytes, t, stream, o_fp32, link);
     if (joined && r == DAK_OK) link_commit(t, own_signals);
     return r;
+}
+
+// The passes of dak_attn_acc (P null) and dak_attn_prefix. Workspace: the own pass's partials,
+// the prefix pass's partials and the scores, each rounded up to 256 bytes.
+struct ExtLayout {
+    int n_own, n_pre, score_pitch;
+    size_t own_bytes, pre_bytes, score_bytes;
+    size_t total() const { return own_bytes + pre_bytes + score_bytes; }
+};
+
+static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+static ExtLayout ext_layout(const dak_placement* KV, const dak_placement* P, int H_q, int n_split, bool with_acc) {
+    ExtLayout x{};
+    const size_t rows = static_cast<size_t>(KV->B) * H_q;
+    x.n_own = n_split > 0 ? n_split : default_split(KV->B, KV->H_kv, KV->L);
+    x.n_pre = P ? default_split(KV->B, P->H_kv, P->L) : 0;
+    x.own_bytes = round256(rows * x.n_own * (KV->D + 2) * sizeof(float));
+    x.pre_bytes = round256(rows * x.n_pre * (KV->D + 2) * sizeof(float));
+    x.score_pitch = (KV->L + kChunkTok - 1) / kChunkTok * kChunkTok;
+    x.score_bytes = with_acc ? round256(rows * x.score_pitch * sizeof(float)) : 0;
+    return x;
+}
+
+// Partial overlap of two arrays of n elements (the same array twice is none).
+static bool partly_overlaps(const void* a, const void* b, size_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x != y && x < y + bytes && y < x + bytes;
+}
+
+static dak_status launch_attn_ext(const void* Q, const dak_placement* KV, const int* seq_lens, const dak_placement* P,
+                                  const int* prefix_lens, const int* prefix_of, int H_q, float scale, void* O,
+                                  int o_fp32, const float* acc_in, float* acc_out, void* ws, size_t ws_bytes,
+                                  const dak_tuning* t, cudaStream_t stream, const LinkHandoff* link) {
+    if (!KV || KV->kind != 1 || !Q || !O || H_q <= 0 || H_q % KV->H_kv) return DAK_ERR_INVALID;
+    if (H_q / KV->H_kv > 16) return DAK_ERR_UNSUPPORTED;
+    if (P && (P->kind != 1 || P->D != KV->D || P->H_kv != KV->H_kv || P->device != KV->device)) return DAK_ERR_INVALID;
+    if (t && t->n_split > kMaxSplits) return DAK_ERR_INVALID;
+    if (acc_out && acc_in &&
+        partly_overlaps(acc_in, acc_out, static_cast<size_t>(KV->B) * KV->H_kv * KV->L * sizeof(float))) {
+        return DAK_ERR_INVALID;
+    }
+    if ((reinterpret_cast<uintptr_t>(Q) & 15) || (reinterpret_cast<uintptr_t>(O) & 15) ||
+        (reinterpret_cast<uintptr_t>(ws) & 15) || (reinterpret_cast<uintptr_t>(acc_in) & 3) ||
+        (reinterpret_cast<uintptr_t>(acc_out) & 3)) {
+        return DAK_ERR_ALIGN;
+    }
+    const ExtLayout x = ext_layout(KV, P, H_q, t ? t->n_split : 0, acc_out != nullptr);
+    if (!ws || ws_bytes < x.total()) return DAK_ERR_INVALID;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DAK_ERR_CUDA;
+    if (dev != KV->device) return DAK_ERR_INVALID;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    float* own = reinterpret_cast<float*>(w);
+    float* pre = reinterpret_cast<float*>(w + x.own_bytes);
+
+    dak_tuning tun = t ? *t : dak_tuning{};
+    tun.n_split = x.n_own;
+    AttnExt ext;
+    ext.scores = acc_out ? reinterpret_cast<float*>(w + x.own_bytes + x.pre_bytes) : nullptr;
+    ext.score_pitch = x.score_pitch;
+    dak_status r = launch_attn_kernels(Q, KV, KV->host_dev, seq_lens, H_q, scale, O, own, x.own_bytes, &tun, stream,
+                                       o_fp32, link, &ext);
+    if (r != DAK_OK) return r;
+    if (P) {
+        AttnParams p{};
+        p.Q = static_cast<const __nv_bfloat16*>(Q);
+        p.kv[0] = static_cast<const uint8_t*>(P->host_dev);
+        p.kv[1] = static_cast<const uint8_t*>(P->hbm_ptr);
+        p.seq_lens = prefix_lens;
+        p.o_fp32 = o_fp32 ? 1 : 0;
+        p.ws = pre;
+        p.B = KV->B;
+        p.Hq = H_q;
+        p.Hkv = KV->H_kv;
+        p.G = H_q / KV->H_kv;
+        p.L = P->L;
+        p.h_s = P->h_s;
+        p.n_split = x.n_pre;
+        p.split_len = ((P->L + x.n_pre - 1) / x.n_pre + kChunkTok - 1) / kChunkTok * kChunkTok;
+        p.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(KV->D))) * 1.4426950408889634f;
+        p.head_bytes = P->head_bytes;
+        p.st = status_ptr();
+        if (!p.st) return DAK_ERR_CUDA;
+        p.prefix_of = prefix_of;
+        p.n_prefix = P->B;
+        p.hbm_units = static_cast<long long>(KV->B) * KV->H_kv * x.n_pre;
+        p.host_window = p.hbm_window = kAttnStages;
+        const int per_sm = KV->D == 128 ? attn_ctas_per_sm<128>(kAttnStages, p.G) : attn_ctas_per_sm<64>(kAttnStages, p.G);
+        p.n_hbm_ctas = static_cast<int>(std::min<long long>(p.hbm_units, static_cast<long long>(per_sm) * device_sm_count()));
+        const cudaError_t e = KV->D == 128 ? launch_attn_ext_d<128, kExtPrefix>(p, p.n_hbm_ctas, kAttnStages, false, stream)
+                                           : launch_attn_ext_d<64, kExtPrefix>(p, p.n_hbm_ctas, kAttnStages, false, stream);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
+    MergeParams m{};
+    m.own = own;
+    m.pre = pre;
+    m.n_own = x.n_own;
+    m.n_pre = x.n_pre;
+    m.O = O;
+    m.o_fp32 = o_fp32 ? 1 : 0;
+    m.scores = ext.scores;
+    m.score_pitch = x.score_pitch;
+    m.acc_in = acc_in;
+    m.acc_out = acc_out;
+    m.seq_lens = seq_lens;
+    m.Hq = H_q;
+    m.Hkv = KV->H_kv;
+    m.G = H_q / KV->H_kv;
+    m.L = KV->L;
+    const dim3 grid(static_cast<unsigned>(KV->B) * KV->H_kv,
+                    static_cast<unsigned>(m.G + (acc_out ? (KV->L + kMergePositions - 1) / kMergePositions : 0)));
+    if (KV->D == 128) {
+        attn_merge_kernel<128><<<grid, kMergeThreads, 0, stream>>>(m);
+    } else {
+        attn_merge_kernel<64><<<grid, kMergeThreads, 0, stream>>>(m);
+    }
+    return cuda_status(cudaGetLastError());
 }
 
 }  // namespace dak
@@ -682,4 +972,39 @@ extern "C" dak_status dak_attn_staged(const void* Q, const dak_placement* KV, co
     if (reinterpret_cast<uintptr_t>(staging) & 15) return DAK_ERR_ALIGN;
     return dak::launch_attn(Q, KV, staging, seq_lens, H_q, scale, O, workspace, ws_bytes, tuning,
                             static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t dak_attn_acc_workspace_bytes(const dak_placement* KV, int H_q, int n_split) {
+    if (!KV || KV->kind != 1 || H_q <= 0 || H_q % KV->H_kv || n_split > dak::kMaxSplits) return 0;
+    return dak::ext_layout(KV, nullptr, H_q, n_split, true).total();
+}
+
+extern "C" dak_status dak_attn_acc(const void* Q, const dak_placement* KV, const int* seq_lens, int H_q, float scale,
+                                   void* O, int o_fp32, const float* acc_in, float* acc_out, void* workspace,
+                                   size_t ws_bytes, const dak_tuning* tuning, void* stream) {
+    if (!acc_out) return DAK_ERR_INVALID;
+    dak::LinkHandoff lk;
+    int signals = 0;
+    const bool joined = dak::link_join(tuning, &lk);
+    if (joined) lk.signals = &signals;
+    const dak_status r =
+        dak::launch_attn_ext(Q, KV, seq_lens, nullptr, nullptr, nullptr, H_q, scale, O, o_fp32, acc_in, acc_out,
+                             workspace, ws_bytes, tuning, static_cast<cudaStream_t>(stream), joined ? &lk : nullptr);
+    if (joined && r == DAK_OK) dak::link_commit(tuning, signals);
+    return r;
+}
+
+extern "C" size_t dak_attn_prefix_workspace_bytes(const dak_placement* KV, const dak_placement* P, int H_q,
+                                                  int n_split, int with_acc) {
+    if (!KV || KV->kind != 1 || !P || P->kind != 1 || H_q <= 0 || H_q % KV->H_kv || n_split > dak::kMaxSplits) return 0;
+    return dak::ext_layout(KV, P, H_q, n_split, with_acc != 0).total();
+}
+
+extern "C" dak_status dak_attn_prefix(const void* Q, const dak_placement* KV, const int* seq_lens,
+                                      const dak_placement* P, const int* prefix_lens, const int* prefix_of, int H_q,
+                                      float scale, void* O, int o_fp32, const float* acc_in, float* acc_out,
+                                      void* workspace, size_t ws_bytes, const dak_tuning* tuning, void* stream) {
+    if (!P) return DAK_ERR_INVALID;
+    return dak::launch_attn_ext(Q, KV, seq_lens, P, prefix_lens, prefix_of, H_q, scale, O, o_fp32, acc_in, acc_out,
+                                workspace, ws_bytes, tuning, static_cast<cudaStream_t>(stream), nullptr);
 }

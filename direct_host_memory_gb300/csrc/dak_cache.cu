@@ -1,0 +1,527 @@
+// What changes the contents of a placed KV cache between attention calls: new tokens rotated
+// and appended (dak_kv_append_rope), and the least attended tokens evicted (dak_kv_evict).
+// The cache layout is the one of dak_attn.cu: a (request, kv head) slab is ceil(L/64) chunks
+// [K 64 x D][V 64 x D] bf16, the 16-byte piece c of token t's row stored at c ^ (t & 7).
+#include <climits>
+#include <cmath>
+
+#include "dak_device.cuh"
+
+namespace dak {
+
+// ------------------------------------------------------------------------------------
+// rotation and append
+// ------------------------------------------------------------------------------------
+struct RopeParams {
+    dak_rope_plan rope;
+    const void* q;
+    const void* k;
+    const void* v;
+    long long q_pitch, k_pitch, v_pitch;  // elements from token to token
+    const int* slots;
+    const int* positions;
+    const int* n_new;
+    __nv_bfloat16* q_out;
+    int* slot_pos;
+    uint8_t* host;
+    uint8_t* hbm;
+    long long head_bytes;
+    int T, Hq, Hkv, L, h_s;
+    DevStatus* st;
+};
+
+constexpr int kRopeThreads = 128;
+
+template <bool F32>
+__device__ __forceinline__ float load_elem(const void* p, long long i) {
+    if (F32) return static_cast<const float*>(p)[i];
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// Eight consecutive elements at i (16-byte aligned in bf16, 32 bytes in fp32).
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, long long i, float (&x)[8]) {
+    if (F32) {
+        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        const float4 a = s[0], b = s[1];
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+        x[0] = bf_lo(a.x), x[1] = bf_hi(a.x), x[2] = bf_lo(a.y), x[3] = bf_hi(a.y);
+        x[4] = bf_lo(a.z), x[5] = bf_hi(a.z), x[6] = bf_lo(a.w), x[7] = bf_hi(a.w);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
+    return make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+}
+
+// One block per (token, share of its heads). The first threads turn the position into the
+// pairs' cos and sin: position x turns modulo 2^64 is the angle as a binary fraction of a
+// turn, exact at any distance; its upper 32 bits, signed, are half-turns * 2^-31. Then each
+// thread makes one 16-byte piece of one head's output row. Memory bound: every element is read
+// and written once (a pair's partner comes from the L1 line that the neighbour loads).
+template <int D, bool F32>
+__global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int PIECES = D / 8;
+    __shared__ float2 cs[D / 2];
+    const int b = blockIdx.x / p.T, t = blockIdx.x - b * p.T;
+    if (p.n_new && t >= p.n_new[b]) return;
+    const int R = p.rope.rot_dim, half = R / 2;
+    const long long row = static_cast<long long>(p.slots[b]) + t;
+    const long long pos = p.positions ? static_cast<long long>(p.positions[b]) + t : row;
+    if (static_cast<int>(threadIdx.x) < half) {
+        const uint64_t turn = static_cast<uint64_t>(pos) * p.rope.turns[threadIdx.x];
+        const float x = static_cast<float>(static_cast<int>(static_cast<uint32_t>(turn >> 32))) * 0x1p-31f;
+        float s, c;
+        sincospif(x, &s, &c);
+        cs[threadIdx.x] = make_float2(c * p.rope.scale, s * p.rope.scale);
+    }
+    __syncthreads();
+    const bool in_range = row >= 0 && row < p.L;
+    if (!in_range && blockIdx.y == 0 && threadIdx.x == 0) {
+        report(p.st, DAK_ERR_BOUNDS, 0xA9901000ull << 32 | static_cast<unsigned>(b));
+    }
+    const long long token = blockIdx.x;
+    const int heads = p.Hq + 2 * p.Hkv;
+    for (int task = blockIdx.y * kRopeThreads + threadIdx.x; task < heads * PIECES; task += gridDim.y * kRopeThreads) {
+        const int h = task / PIECES, c = task - h * PIECES;
+        const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+        if (!is_q && !in_range) continue;
+        const int g = is_q ? h : is_v ? h - p.Hq - p.Hkv : h - p.Hq;
+        const void* src = is_q ? p.q : is_v ? p.v : p.k;
+        const long long at = token * (is_q ? p.q_pitch : is_v ? p.v_pitch : p.k_pitch) + g * D;
+        const int e0 = c * 8;
+        float x[8], y[8];
+        load8<F32>(src, at + e0, x);
+        if (is_v || e0 >= R) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = x[i];
+        } else if (p.rope.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                if (e0 + i < R) {
+                    const float2 f = cs[(e0 + i) >> 1];
+                    y[i] = x[i] * f.x - x[i + 1] * f.y;
+                    y[i + 1] = x[i + 1] * f.x + x[i] * f.y;
+                } else {
+                    y[i] = x[i];
+                    y[i + 1] = x[i + 1];
+                }
+            }
+        } else if ((half & 7) == 0) {
+            const bool low = e0 < half;
+            float o[8];
+            load8<F32>(src, at + (low ? e0 + half : e0 - half), o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = cs[(low ? e0 : e0 - half) + i];
+                y[i] = low ? x[i] * f.x - o[i] * f.y : x[i] * f.x + o[i] * f.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = e0 + i;
+                if (e < half) {
+                    y[i] = x[i] * cs[e].x - load_elem<F32>(src, at + e + half) * cs[e].y;
+                } else if (e < R) {
+                    y[i] = x[i] * cs[e - half].x + load_elem<F32>(src, at + e - half) * cs[e - half].y;
+                } else {
+                    y[i] = x[i];
+                }
+            }
+        }
+        const uint4 out = pack8(y);
+        if (is_q) {
+            *reinterpret_cast<uint4*>(p.q_out + (token * p.Hq + h) * D + e0) = out;
+        } else {
+            const long long slab = static_cast<long long>(b) * p.Hkv + g;
+            uint4* base =
+                reinterpret_cast<uint4*>(slab < p.h_s ? p.host + slab * p.head_bytes : p.hbm + (slab - p.h_s) * p.head_bytes);
+            base[(row >> 6) * (2 * 64 * PIECES) + (is_v ? 64 * PIECES : 0) + (row & 63) * PIECES + (c ^ (row & 7))] = out;
+            if (p.slot_pos && !is_v && c == 0) p.slot_pos[slab * p.L + row] = static_cast<int>(pos);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// eviction
+// ------------------------------------------------------------------------------------
+struct EvictParams {
+    const int* seq_lens;
+    const float* acc;
+    float* acc_out;
+    const int* pos;
+    int* pos_out;
+    int* lens_out;
+    int* src_out;
+    int* moves;   // [slabs][2][list]: the holes and the movers of each slab, in ascending order
+    int* n_moves; // [slabs]
+    int list;     // longest list: min(n_keep, L - n_keep)
+    int Hkv, L, n_keep, n_recent;
+    uint8_t* host;
+    uint8_t* hbm;
+    long long head_bytes;
+    int h_s;
+};
+
+constexpr int kEvictThreads = 512;
+constexpr int kMoveThreads = 256;
+
+// Order of eviction as an unsigned key: protected slots highest, then the weight, NaN lowest;
+// -0 equals +0.
+__device__ __forceinline__ uint32_t evict_key(float w, bool newest) {
+    if (newest) return 0xFFFFFFFFu;
+    if (isnan(w)) return 0u;
+    const uint32_t u = __float_as_uint(w + 0.0f);
+    return u >> 31 ? ~u : u | 0x80000000u;
+}
+
+// One block per slab: the n_keep-th largest key by a radix select over bytes, then one pass over
+// the slots in order that gives every slot its fate and every hole and mover its rank.
+__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const EvictParams p) {
+    constexpr int NW = kEvictThreads / 32;
+    __shared__ int hist[256];
+    __shared__ int red[NW];
+    __shared__ int sh_a, sh_b;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long slab = blockIdx.x;
+    const int b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv;
+    const int n = min(max(p.seq_lens[b], 0), p.L), keep = p.n_keep;
+    const float* acc = p.acc + slab * p.L;
+    const int* pos = p.pos + slab * p.L;
+    float* acc_out = p.acc_out + slab * p.L;
+    int* pos_out = p.pos_out + slab * p.L;
+    int* src = p.src_out ? p.src_out + slab * keep : nullptr;
+    const bool copy = p.acc_out != p.acc, copy_pos = p.pos_out != p.pos;
+    if (g == 0 && tid == 0) p.lens_out[b] = min(n, keep);
+    if (n <= keep) {
+        for (int i = tid; i < n; i += kEvictThreads) {
+            if (copy) acc_out[i] = acc[i];
+            if (copy_pos) pos_out[i] = pos[i];
+        }
+        if (src) {
+            for (int i = tid; i < keep; i += kEvictThreads) src[i] = i < n ? i : -1;
+        }
+        if (tid == 0) p.n_moves[slab] = 0;
+        return;
+    }
+    // newest position
+    int m = INT_MIN;
+    for (int i = tid; i < n; i += kEvictThreads) m = max(m, pos[i]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+    m = red[0];
+    for (int w = 1; w < NW; ++w) m = max(m, red[w]);
+    const long long oldest = static_cast<long long>(m) - p.n_recent;  // newer than this: protected
+    // the keep-th largest key, a byte at a time from the top: prefix = its leading bytes,
+    // want = how many of the keys that share them are kept
+    uint32_t prefix = 0;
+    int want = keep;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kEvictThreads) {
+            const uint32_t k = evict_key(acc[i], pos[i] > oldest);
+            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+        }
+        __syncthreads();
+        if (tid == 0) {
+            int left = want, d = 255;
+            while (d > 0 && hist[d] < left) left -= hist[d--];
+            sh_a = d;
+            sh_b = left;
+        }
+        __syncthreads();
+        prefix |= static_cast<uint32_t>(sh_a) << shift;
+        want = sh_b;
+        __syncthreads();
+    }
+    // slots in order: above the threshold kept, at it the first `want`
+    int eq_seen = 0, n_holes = 0, n_movers = 0;
+    int* holes = p.moves + slab * 2 * p.list;
+    int* movers = holes + p.list;
+    const uint32_t below = (1u << lane) - 1;
+    // a block-wide exclusive rank of `mine`, and the tile's count added to `total`
+    const auto rank_of = [&](bool mine, int& total) {
+        const uint32_t bal = __ballot_sync(0xffffffffu, mine);
+        if (lane == 0) red[warp] = __popc(bal);
+        __syncthreads();
+        int before = total + __popc(bal & below), all = 0;
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += red[w];
+            all += red[w];
+        }
+        total += all;
+        __syncthreads();
+        return before;
+    };
+    for (int i0 = 0; i0 < n; i0 += kEvictThreads) {
+        const int i = i0 + tid;
+        const uint32_t k = i < n ? evict_key(acc[i], pos[i] > oldest) : 0u;
+        const bool eq = i < n && k == prefix;
+        const int at = rank_of(eq, eq_seen);
+        const bool kept = i < n && (k > prefix || (eq && at < want));
+        const bool hole = i < keep && !kept, mover = i >= keep && kept;
+        const int hr = rank_of(hole, n_holes), mr = rank_of(mover, n_movers);
+        if (hole) holes[hr] = i;
+        if (mover) movers[mr] = i;
+        if (kept && i < keep) {
+            if (copy) acc_out[i] = acc[i];
+            if (copy_pos) pos_out[i] = pos[i];
+            if (src) src[i] = i;
+        }
+    }
+    __syncthreads();
+    const int cnt = n_holes;  // as many holes as movers
+    if (tid == 0) p.n_moves[slab] = cnt;
+    for (int r = tid; r < cnt; r += kEvictThreads) {
+        const int to = holes[r], from = movers[r];
+        acc_out[to] = acc[from];
+        pos_out[to] = pos[from];
+        if (src) src[to] = from;
+    }
+    __syncthreads();
+    for (int i = keep + tid; i < n; i += kEvictThreads) {
+        acc_out[i] = 0.f;
+        pos_out[i] = -1;
+    }
+}
+
+// One warp per moved row: K and V from slot `from` to slot `to`.
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+    constexpr int PIECES = D / 8;
+    const long long slab = blockIdx.x;
+    const int cnt = p.n_moves[slab];
+    const int* holes = p.moves + slab * 2 * p.list;
+    const int* movers = holes + p.list;
+    uint4* base =
+        reinterpret_cast<uint4*>(slab < p.h_s ? p.host + slab * p.head_bytes : p.hbm + (slab - p.h_s) * p.head_bytes);
+    constexpr int PER_ROW = 2 * PIECES;  // 16-byte pieces of a K row and a V row
+    const long long total = static_cast<long long>(cnt) * PER_ROW;
+    for (long long e = blockIdx.y * static_cast<long long>(kMoveThreads) + threadIdx.x; e < total;
+         e += static_cast<long long>(gridDim.y) * kMoveThreads) {
+        const int r = static_cast<int>(e / PER_ROW), q = static_cast<int>(e % PER_ROW);
+        const int c = q % PIECES, v = q / PIECES;
+        const int from = movers[r], to = holes[r];
+        base[static_cast<long long>(to >> 6) * (128 * PIECES) + v * 64 * PIECES + (to & 63) * PIECES + (c ^ (to & 7))] =
+            base[static_cast<long long>(from >> 6) * (128 * PIECES) + v * 64 * PIECES + (from & 63) * PIECES +
+                 (c ^ (from & 7))];
+    }
+}
+
+static bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+static bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+static dak_status device_matches(const dak_placement* p) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DAK_ERR_CUDA;
+    return dev == p->device ? DAK_OK : DAK_ERR_INVALID;
+}
+
+}  // namespace dak
+
+using namespace dak;
+
+extern "C" dak_status dak_placement_data(const dak_placement* p, void** host, void** hbm) {
+    if (!p) return DAK_ERR_INVALID;
+    if (host) *host = p->host_ptr;
+    if (hbm) *hbm = p->hbm_ptr;
+    return DAK_OK;
+}
+
+extern "C" dak_status dak_rope_from_freqs(int head_dim, const double* inv_freq, int n_pairs, int interleaved,
+                                          double attn_scale, dak_rope_plan* out) {
+    if (!inv_freq || !out) return DAK_ERR_INVALID;
+    if (head_dim != 64 && head_dim != 128) return DAK_ERR_UNSUPPORTED;
+    if (n_pairs < 1 || n_pairs > head_dim / 2 || !std::isfinite(attn_scale) || attn_scale > 1e30) return DAK_ERR_INVALID;
+    dak_rope_plan r{};
+    r.head_dim = head_dim;
+    r.rot_dim = 2 * n_pairs;
+    r.interleaved = interleaved ? 1 : 0;
+    r.scale = attn_scale > 0 ? static_cast<float>(attn_scale) : 1.0f;
+    for (int i = 0; i < n_pairs; ++i) {
+        if (!std::isfinite(inv_freq[i])) return DAK_ERR_INVALID;
+        const double t = std::fmod(inv_freq[i] / 6.283185307179586476925, 1.0);  // exact, sign kept
+        const double f = std::floor(std::ldexp(std::fabs(t), 64) + 0.5);
+        const uint64_t u = f >= 0x1p64 ? 0 : static_cast<uint64_t>(f);
+        r.turns[i] = t < 0 ? 0 - u : u;  // a turn backwards is its complement
+    }
+    *out = r;
+    return DAK_OK;
+}
+
+extern "C" dak_status dak_rope_make(int head_dim, const dak_rope_config* cfg, dak_rope_plan* out) {
+    if (!cfg || !out) return DAK_ERR_INVALID;
+    if (head_dim != 64 && head_dim != 128) return DAK_ERR_UNSUPPORTED;
+    const int R = cfg->rot_dim > 0 ? cfg->rot_dim : head_dim;
+    const double theta = cfg->theta > 0 ? cfg->theta : 500000.0;
+    const double s = cfg->factor > 0 ? cfg->factor : 1.0;
+    double low = cfg->low_turns, high = cfg->high_turns;
+    if (low <= 0 && high <= 0) low = 1.0, high = 32.0;
+    if (R % 2 || R > head_dim || !std::isfinite(theta) || !std::isfinite(s) || std::isnan(cfg->theta) ||
+        std::isnan(cfg->factor)) {
+        return DAK_ERR_INVALID;
+    }
+    double inv[64];
+    for (int i = 0; i < R / 2; ++i) {
+        const double e = -2.0 * i / R;
+        const double f = std::pow(theta, e);
+        switch (cfg->scaling) {
+            case DAK_ROPE_PLAIN:
+                inv[i] = f;
+                break;
+            case DAK_ROPE_LINEAR:
+                inv[i] = f / s;
+                break;
+            case DAK_ROPE_NTK:
+                inv[i] = R > 2 ? std::pow(theta * std::pow(s, static_cast<double>(R) / (R - 2)), e) : f;
+                break;
+            case DAK_ROPE_BY_PARTS: {
+                if (!(cfg->orig_len > 0) || !std::isfinite(cfg->orig_len) || !(low >= 0) || !(high > low) ||
+                    !std::isfinite(high)) {
+                    return DAK_ERR_INVALID;
+                }
+                const double turns = cfg->orig_len * f / 6.283185307179586476925;
+                const double mix = std::fmin(1.0, std::fmax(0.0, (turns - low) / (high - low)));
+                inv[i] = f / s * (1 - mix) + f * mix;
+                break;
+            }
+            default:
+                return DAK_ERR_INVALID;
+        }
+    }
+    return dak_rope_from_freqs(head_dim, inv, R / 2, cfg->interleaved, cfg->attn_scale, out);
+}
+
+extern "C" dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope_plan* rope, const void* q,
+                                         const void* k, const void* v, int in_fp32, int T, int H_q, int64_t q_pitch,
+                                         int64_t k_pitch, int64_t v_pitch, const int* slots, const int* positions,
+                                         const int* n_new, void* q_out, int* slot_pos, void* stream) {
+    if (!KV || KV->kind != 1 || !rope || !k || !v || !slots || T < 1 || H_q < 0) return DAK_ERR_INVALID;
+    if (H_q > 0 && (!q || !q_out)) return DAK_ERR_INVALID;
+    const int D = KV->D;
+    if (rope->head_dim != D || rope->rot_dim < 2 || rope->rot_dim > D || rope->rot_dim % 2) return DAK_ERR_INVALID;
+    const int64_t kv_row = static_cast<int64_t>(KV->H_kv) * D, q_row = static_cast<int64_t>(H_q) * D;
+    if (k_pitch < kv_row || v_pitch < kv_row || (H_q > 0 && q_pitch < q_row)) return DAK_ERR_INVALID;
+    const int64_t tokens = static_cast<int64_t>(KV->B) * T;
+    if (tokens > 0x7FFFFFFF || static_cast<int64_t>(H_q) + 2ll * KV->H_kv > (1 << 24)) return DAK_ERR_INVALID;
+    const int size = in_fp32 ? 4 : 2, per16 = 16 / size;
+    if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(q_out, 16) || misaligned(slots, 4) ||
+        misaligned(positions, 4) || misaligned(n_new, 4) || misaligned(slot_pos, 4) || k_pitch % per16 ||
+        v_pitch % per16 || (H_q > 0 && q_pitch % per16)) {
+        return DAK_ERR_ALIGN;
+    }
+    if (H_q > 0) {
+        const size_t out_bytes = static_cast<size_t>(tokens) * q_row * 2;
+        const auto span = [&](int64_t pitch, int64_t row) { return static_cast<size_t>((tokens - 1) * pitch + row) * size; };
+        if (ranges_overlap(q_out, out_bytes, q, span(q_pitch, q_row)) ||
+            ranges_overlap(q_out, out_bytes, k, span(k_pitch, kv_row)) ||
+            ranges_overlap(q_out, out_bytes, v, span(v_pitch, kv_row))) {
+            return DAK_ERR_INVALID;
+        }
+    }
+    const dak_status m = device_matches(KV);
+    if (m != DAK_OK) return m;
+    RopeParams p{};
+    p.rope = *rope;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_pitch = q_pitch;
+    p.k_pitch = k_pitch;
+    p.v_pitch = v_pitch;
+    p.slots = slots;
+    p.positions = positions;
+    p.n_new = n_new;
+    p.q_out = static_cast<__nv_bfloat16*>(q_out);
+    p.slot_pos = slot_pos;
+    p.host = static_cast<uint8_t*>(KV->host_dev);
+    p.hbm = static_cast<uint8_t*>(KV->hbm_ptr);
+    p.head_bytes = KV->head_bytes;
+    p.T = T;
+    p.Hq = H_q;
+    p.Hkv = KV->H_kv;
+    p.L = KV->L;
+    p.h_s = KV->h_s;
+    p.st = status_ptr();
+    if (!p.st) return DAK_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>(tokens), 1);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (D == 128) {
+        in_fp32 ? append_rope_kernel<128, true><<<grid, kRopeThreads, 0, s>>>(p)
+                : append_rope_kernel<128, false><<<grid, kRopeThreads, 0, s>>>(p);
+    } else {
+        in_fp32 ? append_rope_kernel<64, true><<<grid, kRopeThreads, 0, s>>>(p)
+                : append_rope_kernel<64, false><<<grid, kRopeThreads, 0, s>>>(p);
+    }
+    return cuda_status(cudaGetLastError());
+}
+
+// Workspace: per slab a count and the holes and movers, of which there are at most
+// min(n_keep, L - n_keep) <= L / 2 each.
+extern "C" size_t dak_kv_evict_workspace_bytes(const dak_placement* KV) {
+    if (!KV || KV->kind != 1) return 0;
+    const size_t slabs = static_cast<size_t>(KV->B) * KV->H_kv;
+    return (slabs * (1 + 2 * static_cast<size_t>(KV->L / 2)) * sizeof(int) + 15) / 16 * 16;
+}
+
+extern "C" dak_status dak_kv_evict(const dak_placement* KV, const int* seq_lens, int n_keep, int n_recent,
+                                   const float* acc, float* acc_out, const int* slot_pos, int* slot_pos_out,
+                                   int* lens_out, int* src_out, void* workspace, size_t ws_bytes, void* stream) {
+    if (!KV || KV->kind != 1 || !seq_lens || !acc || !acc_out || !slot_pos || !slot_pos_out || !lens_out || !workspace) {
+        return DAK_ERR_INVALID;
+    }
+    if (n_keep < 1 || n_keep > KV->L || n_recent < 0 || n_recent > n_keep) return DAK_ERR_INVALID;
+    if (misaligned(seq_lens, 4) || misaligned(acc, 4) || misaligned(acc_out, 4) || misaligned(slot_pos, 4) ||
+        misaligned(slot_pos_out, 4) || misaligned(lens_out, 4) || misaligned(src_out, 4) || misaligned(workspace, 16)) {
+        return DAK_ERR_ALIGN;
+    }
+    if (ws_bytes < dak_kv_evict_workspace_bytes(KV)) return DAK_ERR_INVALID;
+    const size_t slabs = static_cast<size_t>(KV->B) * KV->H_kv;
+    const size_t table = slabs * KV->L * 4, lens = static_cast<size_t>(KV->B) * 4;
+    if ((acc_out != acc && ranges_overlap(acc_out, table, acc, table)) ||
+        (slot_pos_out != slot_pos && ranges_overlap(slot_pos_out, table, slot_pos, table)) ||
+        ranges_overlap(lens_out, lens, seq_lens, lens)) {
+        return DAK_ERR_INVALID;
+    }
+    const dak_status m = device_matches(KV);
+    if (m != DAK_OK) return m;
+    EvictParams p{};
+    p.seq_lens = seq_lens;
+    p.acc = acc;
+    p.acc_out = acc_out;
+    p.pos = slot_pos;
+    p.pos_out = slot_pos_out;
+    p.lens_out = lens_out;
+    p.src_out = src_out;
+    p.n_moves = static_cast<int*>(workspace);
+    p.moves = p.n_moves + slabs;
+    p.list = n_keep < KV->L - n_keep ? n_keep : KV->L - n_keep;
+    p.Hkv = KV->H_kv;
+    p.L = KV->L;
+    p.n_keep = n_keep;
+    p.n_recent = n_recent;
+    p.host = static_cast<uint8_t*>(KV->host_dev);
+    p.hbm = static_cast<uint8_t*>(KV->hbm_ptr);
+    p.head_bytes = KV->head_bytes;
+    p.h_s = KV->h_s;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    evict_select_kernel<<<static_cast<unsigned>(slabs), kEvictThreads, 0, s>>>(p);
+    if (p.list > 0) {
+        const dim3 grid(static_cast<unsigned>(slabs), 8);
+        if (KV->D == 128) {
+            evict_move_kernel<128><<<grid, kMoveThreads, 0, s>>>(p);
+        } else {
+            evict_move_kernel<64><<<grid, kMoveThreads, 0, s>>>(p);
+        }
+    }
+    return cuda_status(cudaGetLastError());
+}

@@ -179,6 +179,107 @@ dak_status dak_place_kv_heads(const void* K_src, const void* V_src, int src_on_d
 dak_status dak_kv_append(const dak_placement* KV, const void* k_new, const void* v_new, const int* positions,
                          void* stream);
 
+/* Rotary positions for dak_kv_append_rope: how a head's first rot_dim elements are turned in
+ * pairs. Pair i of a token at position p turns by the angle p * f_i:
+ *     y1 = (x1 cos - x2 sin) * attn_scale,  y2 = (x2 cos + x1 sin) * attn_scale.
+ *   rot_dim    : elements turned, even, 2..D; the rest of the head passes through. <= 0: D.
+ *   interleaved: 0 = pair i is (x[i], x[i + rot_dim/2]); 1 = (x[2i], x[2i + 1]).
+ *   theta      : base, f_i = theta^(-2i/rot_dim). <= 0: 500000, the decoder's default.
+ *   scaling    : DAK_ROPE_PLAIN;
+ *                DAK_ROPE_LINEAR, every f_i divided by factor (position interpolation);
+ *                DAK_ROPE_NTK, theta replaced by theta * factor^(rot_dim / (rot_dim - 2)), which
+ *                leaves the fastest pair alone and divides the slowest by factor;
+ *                DAK_ROPE_BY_PARTS, per pair by the turns r = orig_len * f_i / 2 pi that it
+ *                makes over the original context: f_i / factor for r <= low_turns, f_i for
+ *                r >= high_turns, between them mixed linearly in r.
+ *   factor     : context extension, > 0 (<= 0: 1). orig_len: > 0 for BY_PARTS.
+ *   low_turns, high_turns: 0 <= low < high; both <= 0: 1 and 32.
+ *   attn_scale : factor on cos and sin; <= 0: 1. */
+typedef enum { DAK_ROPE_PLAIN = 0, DAK_ROPE_LINEAR = 1, DAK_ROPE_NTK = 2, DAK_ROPE_BY_PARTS = 3 } dak_rope_scaling;
+typedef struct {
+    int rot_dim;
+    int interleaved;
+    int scaling;
+    double theta;
+    double factor;
+    double orig_len;
+    double low_turns;
+    double high_turns;
+    double attn_scale;
+} dak_rope_config;
+
+/* A rotation ready for use: plain data made by dak_rope_make or dak_rope_from_freqs, kept by
+ * the caller. turns[i] is f_i / 2 pi modulo 1 as a 64-bit binary fraction, so that position
+ * times turns modulo 2^64 is the angle in turns, exact to 2^-33 for any int32 position. */
+typedef struct {
+    int head_dim;
+    int rot_dim;
+    int interleaved;
+    float scale;
+    uint64_t turns[64];
+} dak_rope_plan;
+
+/* Host arithmetic only. DAK_ERR_UNSUPPORTED: head_dim not 64 or 128; DAK_ERR_INVALID: null
+ * pointers, rot_dim odd or above head_dim, an unknown scaling, values that are not finite or
+ * out of the ranges above. */
+dak_status dak_rope_make(int head_dim, const dak_rope_config* cfg, dak_rope_plan* out);
+
+/* The same from given frequencies inv_freq[n_pairs] (radians per position, finite), for any
+ * other scheme: rot_dim = 2 n_pairs, 1 <= n_pairs <= head_dim / 2; attn_scale as above. */
+dak_status dak_rope_from_freqs(int head_dim, const double* inv_freq, int n_pairs, int interleaved, double attn_scale,
+                               dak_rope_plan* out);
+
+/* Rotate new tokens and append them to a placed KV cache, dak_kv_append's step for unrotated
+ * projections and for one token or many: token t < n_new[b] of request b has position
+ * positions[b] + t; its query heads are rotated into q_out, its key heads are rotated into
+ * row slots[b] + t of their (request, kv head) slabs, in whichever tier holds them, and its
+ * value heads are stored there as they are. Rows and positions differ once rows have been
+ * evicted (dak_kv_evict).
+ *   q, k, v  : [B][T] tokens at q_pitch, k_pitch, v_pitch elements from one token to the next,
+ *              each [H_q][D] or [H_kv][D] (device): bf16, or fp32 with in_fp32 (a projection's
+ *              c_fp32 output); they may lie side by side in one buffer. Rotated in fp32 and
+ *              rounded once. q NULL with H_q 0: keys and values only.
+ *   slots    : int32 [B]. positions: int32 [B], or NULL = slots. n_new: int32 [B], clamped to
+ *              [0, T], or NULL = T (device).
+ *   q_out    : bf16 [B][T][H_q][D]; the rows of tokens t >= n_new[b] are left as they were. Must
+ *              not overlap q, k or v (DAK_ERR_INVALID).
+ *   slot_pos : int32 [B][H_kv][L] or NULL: slot_pos[b][g][slots[b] + t] = positions[b] + t, the
+ *              table dak_kv_evict goes by.
+ * Pointers 16-byte aligned (int32 arrays 4), pitches multiples of 16 bytes (DAK_ERR_ALIGN).
+ * A row outside [0, L) is skipped (its query is still rotated) and reported by
+ * dak_last_error as DAK_ERR_BOUNDS. Stream-ordered; a following dak_attn as after
+ * dak_kv_append. */
+dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope_plan* rope, const void* q, const void* k,
+                              const void* v, int in_fp32, int T, int H_q, int64_t q_pitch, int64_t k_pitch,
+                              int64_t v_pitch, const int* slots, const int* positions, const int* n_new, void* q_out,
+                              int* slot_pos, void* stream);
+
+/* Evict the least attended tokens of a placed KV cache, each (request, kv head) for itself.
+ * Where a request holds L_b = seq_lens[b] (clamped to [0, L]) > n_keep tokens, n_keep slots
+ * stay:
+ *   first the newest, slot_pos > max(slot_pos[0 .. L_b-1]) - n_recent, then the largest acc
+ *   (accumulated attention weights, dak_attn_acc); equal ones by the lower slot, NaN last.
+ * The kept rows in slots >= n_keep move into the slots < n_keep that were not kept, the i-th
+ * to the i-th in ascending order; no other row of the cache moves, so at most L_b - n_keep
+ * rows per kv head are copied, within the tier that holds them. Slots are then in no order of
+ * position, which attention does not need; slot_pos says which token a slot holds. A request
+ * with L_b <= n_keep keeps every row.
+ *   acc, slot_pos         : fp32 and int32 [B][H_kv][L] (device).
+ *   acc_out, slot_pos_out : the same after the eviction: entries below min(L_b, n_keep) follow
+ *              their rows, the entries from there to L_b become 0 and -1, those behind L_b
+ *              are left as they were. Each may be its input (in place) but must not overlap
+ *              it otherwise.
+ *   lens_out : int32 [B], min(L_b, n_keep); must not overlap seq_lens (DAK_ERR_INVALID).
+ *   src_out  : int32 [B][H_kv][n_keep] or NULL: the slot that slot i's row came from, -1 for
+ *              i >= L_b.
+ *   workspace: dak_kv_evict_workspace_bytes(KV) bytes of device memory, 16-byte aligned,
+ *              contents on entry do not matter; calls that share one must not overlap.
+ * 1 <= n_keep <= L, 0 <= n_recent <= n_keep (DAK_ERR_INVALID). Stream-ordered. */
+size_t dak_kv_evict_workspace_bytes(const dak_placement* KV);
+dak_status dak_kv_evict(const dak_placement* KV, const int* seq_lens, int n_keep, int n_recent, const float* acc,
+                        float* acc_out, const int* slot_pos, int* slot_pos_out, int* lens_out, int* src_out,
+                        void* workspace, size_t ws_bytes, void* stream);
+
 /* Release a placement (host and HBM parts). NULL is accepted. */
 dak_status dak_free(dak_placement* p);
 
@@ -187,6 +288,16 @@ dak_status dak_free(dak_placement* p);
  * output pointer may be NULL. */
 dak_status dak_placement_info(const dak_placement* p, int64_t* host_bytes, int64_t* hbm_bytes, int64_t* units,
                               int64_t* host_units);
+
+/* Addresses of a placement's two parts, for a caller that saves, checks or migrates what the
+ * library updates in place: *host is the pinned part's host address, *hbm the HBM part's
+ * device address (NULL where the placement has none in that tier; either output may be
+ * NULL). The memory stays the library's and is valid until dak_free. A KV cache is laid out
+ * by slab (the first host_units of dak_placement_info on the host, the rest in HBM, in
+ * request-major order): ceil(L/64) chunks of 64 tokens, each [K 64 x D][V 64 x D] bf16, and
+ * inside the row of token t the 8-element piece c is stored at piece c ^ (t % 8). Rows past
+ * L are zero. A matrix's tiles are laid out as dak_place_matrix says. */
+dak_status dak_placement_data(const dak_placement* p, void** host, void** hbm);
 
 /* ---------------------------------------------------------------------------------- *
  * Hot path
@@ -352,6 +463,48 @@ dak_status dak_attn(const void* Q, const dak_placement* KV, const int* seq_lens,
  * workspace and errors as dak_attn. */
 dak_status dak_attn_f32(const void* Q, const dak_placement* KV, const int* seq_lens, int H_q, float scale, void* O,
                         void* workspace, size_t ws_bytes, const dak_tuning* tuning, void* stream);
+
+/* dak_attn that also accumulates every position's attention weight, for dak_kv_evict:
+ *     acc_out[b][g][j] = acc_in[b][g][j] + sum over the query heads h of kv head g of p[b,h,j],
+ *     p[b,h,:] = softmax_j(scale * q[b,h] . k[b,g,j]),  j < L_b,
+ * in fp32; entries j >= L_b are left as they were.
+ *   seq_lens: as dak_attn, but L_b = 0 is allowed (a request without tokens: O = 0); values are
+ *             clamped to [0, L].
+ *   O       : [B][H_q][D], bf16 or (o_fp32) fp32. The probabilities enter P.V as two bf16 parts
+ *             (three with o_fp32).
+ *   acc_in  : fp32 [B][H_kv][L] (device), or NULL = zeros. acc_out: the same shape; it may be
+ *             acc_in (in place) but must not overlap it otherwise.
+ *   workspace: dak_attn_acc_workspace_bytes(KV, H_q, n_split) bytes (n_split <= 0: the default),
+ *             16-byte aligned device memory: the splits' partial results and the scores.
+ * Everything else as dak_attn. */
+size_t dak_attn_acc_workspace_bytes(const dak_placement* KV, int H_q, int n_split);
+dak_status dak_attn_acc(const void* Q, const dak_placement* KV, const int* seq_lens, int H_q, float scale, void* O,
+                        int o_fp32, const float* acc_in, float* acc_out, void* workspace, size_t ws_bytes,
+                        const dak_tuning* tuning, void* stream);
+
+/* Decode attention of a batch whose requests share prefixes (a system prompt, a document):
+ * request b attends over the rows of prefix prefix_of[b] and then over its own cache,
+ *     o[b,h] = softmax over j of scale * q[b,h] . k_j, applied to v_j,
+ *     (k_j, v_j) in P[prefix_of[b]][g][0 .. prefix_lens-1] and KV[b][g][0 .. L_b-1].
+ * Every prefix is read once for all its requests' query heads instead of once per request.
+ *   P          : a KV placement holding the prefixes, [n_prefix][H_kv][L_p][D], with KV's H_kv, D
+ *                and device; its own split between the tiers.
+ *   prefix_lens: int32 [n_prefix] (device), clamped to [0, L_p], or NULL = L_p.
+ *   prefix_of  : int32 [B] (device), or NULL = prefix 0 for all. Negative: no prefix. A value
+ *                >= n_prefix counts as none and is reported by dak_last_error (DAK_ERR_BOUNDS).
+ *   seq_lens   : as dak_attn_acc. A request with neither prefix nor own tokens gives O = 0.
+ *   acc_in, acc_out: as dak_attn_acc, over the own cache's positions (the softmax runs over
+ *                prefix and own cache together); acc_out NULL = not accumulated.
+ *   workspace  : dak_attn_prefix_workspace_bytes(KV, P, H_q, n_split, acc_out != NULL) bytes,
+ *                16-byte aligned.
+ *   tuning     : applies to the pass over the own caches; link is not taken.
+ * Requires H_q / H_kv <= 16, as dak_attn. */
+size_t dak_attn_prefix_workspace_bytes(const dak_placement* KV, const dak_placement* P, int H_q, int n_split,
+                                       int with_acc);
+dak_status dak_attn_prefix(const void* Q, const dak_placement* KV, const int* seq_lens, const dak_placement* P,
+                           const int* prefix_lens, const int* prefix_of, int H_q, float scale, void* O, int o_fp32,
+                           const float* acc_in, float* acc_out, void* workspace, size_t ws_bytes,
+                           const dak_tuning* tuning, void* stream);
 
 /* The n_split dak_attn uses for a placement when tuning->n_split <= 0. */
 int dak_attn_default_split(const dak_placement* KV);
