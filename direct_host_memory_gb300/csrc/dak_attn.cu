@@ -55,9 +55,6 @@ struct AttnParams {
     // scaled score (log2 domain) [B][Hq][score_pitch]
     float* scores;
     int score_pitch;
-    // EXT over a shared prefix: unit (b, g, s) reads slab (prefix_of[b], g) of n_prefix
-    const int* prefix_of;
-    int n_prefix;
 };
 
 constexpr int kChunkTok = 64;
@@ -94,26 +91,6 @@ struct Unit {
     int Lb;      // tokens of the request
     const uint8_t* base;  // the (request, kv head) slab
 };
-
-// The same for a pass over the requests' prefixes: slabs of either tier, each CTA taking any.
-__device__ __forceinline__ Unit decode_prefix_unit(const AttnParams& p, long long u) {
-    Unit x;
-    const int per_b = p.Hkv * p.n_split;
-    x.b = static_cast<int>(u / per_b);
-    const int rem = static_cast<int>(u - static_cast<long long>(x.b) * per_b);
-    x.g = rem / p.n_split;
-    x.s = rem - x.g * p.n_split;
-    const int e = p.prefix_of ? p.prefix_of[x.b] : 0;
-    const int f = e >= 0 && e < p.n_prefix ? e : -1;
-    if (e >= p.n_prefix) report(p.st, DAK_ERR_BOUNDS, (0x9F1Full << 32) | static_cast<unsigned>(x.b));
-    x.Lb = f < 0 ? 0 : p.L;
-    if (f >= 0 && p.seq_lens) x.Lb = min(max(p.seq_lens[f], 0), p.L);
-    x.t0 = x.s * p.split_len;
-    x.t1 = min(x.Lb, x.t0 + p.split_len);
-    const long long slab = static_cast<long long>(max(f, 0)) * p.Hkv + x.g;
-    x.base = slab < p.h_s ? p.kv[0] + slab * p.head_bytes : p.kv[1] + (slab - p.h_s) * p.head_bytes;
-    return x;
-}
 
 __device__ __forceinline__ Unit decode_unit(const AttnParams& p, long long u, int tier) {
     Unit x;
@@ -162,11 +139,9 @@ __device__ __forceinline__ void named_bar_consumers() {
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttnConsumers) : "memory");
 }
 
-// PARTS: bf16 parts of P that enter P.V. EXT: kExtNone = dak_attn; kExtOwn / kExtPrefix = the
-// passes of dak_attn_acc and dak_attn_prefix, which leave partials for their own merge.
-enum { kExtNone = 0, kExtOwn = 1, kExtPrefix = 2 };
-
-template <int D, int PARTS, int EXT>
+// PARTS: bf16 parts of P that enter P.V. EXT: the pass over the own caches of dak_attn_acc and
+// dak_attn_prefix, which leaves partials for their merge (attn_merge_kernel) and may keep scores.
+template <int D, int PARTS, bool EXT>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
     constexpr int KS = D / 16;                       // k-steps of the score MMA
     constexpr int NB = D / 8;                        // 8-wide column blocks of O
@@ -201,7 +176,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
             long long i = 0;
             bool waited = false;
             for (long long u = ur.begin; u < ur.end && !*abort; ++u) {
-                const Unit x = EXT == kExtPrefix ? decode_prefix_unit(p, u) : decode_unit(p, u, ur.tier);
+                const Unit x = decode_unit(p, u, ur.tier);
                 for (int t = x.t0; t < x.t1; t += kChunkTok, ++i) {
                     const int s = static_cast<int>(i % W);
                     if (p.wait_newest && !waited && t + kChunkTok >= x.Lb) {
@@ -239,7 +214,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     long long i = 0;
     bool failed = false;  // a wait ran out: skip the math but keep meeting the named barriers
     for (long long u = ur.begin; u < ur.end; ++u) {
-        const Unit x = EXT == kExtPrefix ? decode_prefix_unit(p, u) : decode_unit(p, u, ur.tier);
+        const Unit x = decode_unit(p, u, ur.tier);
         // Q fragments (A operand), rows >= G are zero
         uint32_t qa[KS][4];
         {
@@ -297,7 +272,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                         mx_b = fmaxf(mx_b, sc[nb][2 + e]);
                     }
                 }
-                if (EXT == kExtOwn && p.scores) {
+                if (EXT && p.scores) {
                     // tokens past the valid ones hold -inf and lie inside the padded row
                     float* row = p.scores + (static_cast<long long>(x.b) * p.Hq + static_cast<long long>(x.g) * p.G) *
                                                 p.score_pitch + t + 16 * w + 2 * q4;
@@ -368,7 +343,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                         const uint32_t addr = vs_base + static_cast<uint32_t>(tok * D * 2 + ((c ^ (tok & 7)) << 4));
                         uint32_t b0, b1, b2, b3;
                         ldsm_x4_t(addr, b0, b1, b2, b3);
-                        if (EXT != kExtNone && valid < 16) {
+                        if (EXT && valid < 16) {
                             // rows past the valid tokens may hold anything, also infinities and
                             // NaN, which a probability of zero would not cancel
                             const uint32_t lo = pair_mask(valid - 2 * q4), hi = pair_mask(valid - 8 - 2 * q4);
@@ -441,7 +416,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                 lsum += f * row[D + 1];
             }
             const long long orow = static_cast<long long>(x.b) * p.Hq + static_cast<long long>(x.g) * p.G + r;
-            if (EXT == kExtNone && p.n_split == 1) {
+            if (!EXT && p.n_split == 1) {
                 store_out(p.O, p.o_fp32, orow * D + d, lsum > 0.f ? acc / lsum : 0.f);
             } else {
                 float* wr = p.ws + (orow * p.n_split + x.s) * (D + 2);
@@ -558,14 +533,20 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_cta_kernel(const
 }
 
 // Merge of dak_attn_acc and dak_attn_prefix: the partials of the own cache's n_own splits and of
-// the prefix's n_pre (either may be 0), in that order, into O as attn_combine does, and the
-// accumulated weights acc_out = acc_in + sum_r 2^(s_r - M_r) / l_r from the scores s that the own
-// pass left. Block (b, g) x y: y < G merges query head g * G + y, later ones take
-// kMergePositions positions of the slab each.
+// the prefix's ranges, in that order, into O as attn_combine does, and the accumulated weights
+// acc_out = acc_in + sum_r 2^(s_r - M_r) / l_r from the scores s that the own pass left. Block
+// (b, g) x y: y < G merges query head g * G + y, later ones take kMergePositions positions of
+// the slab each.
 struct MergeParams {
     const float* own;  // [B][Hq][n_own][D + 2]
-    const float* pre;  // [B][Hq][n_pre][D + 2]
-    int n_own, n_pre;
+    int n_own;
+    // prefix pass (launch_prefix); n_pre 0: none
+    const float* pre_o;
+    const float2* pre_ml;
+    const int* n_ranges;
+    const int* prefix_of;
+    const int* prefix_lens;
+    int n_pre, n_prefix, prefix_L;
     void* O;
     int o_fp32;
     const float* scores;  // [B][Hq][score_pitch], log2 domain
@@ -580,27 +561,35 @@ constexpr int kMergePositions = 512;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const MergeParams p) {
-    grid_dep_launch();
-    grid_dep_wait();
     const int b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv;
     const long long row0 = static_cast<long long>(b) * p.Hq + static_cast<long long>(g) * p.G;
-    const int n = p.n_own + p.n_pre;
-    const auto part = [&](long long row, int s) {
-        return s < p.n_own ? p.own + (row * p.n_own + s) * (D + 2) : p.pre + (row * p.n_pre + s - p.n_own) * (D + 2);
+    int n_pre = 0;
+    if (p.n_pre > 0) {
+        const int f = p.prefix_of ? p.prefix_of[b] : 0;
+        if (f >= 0 && f < p.n_prefix && (p.prefix_lens ? p.prefix_lens[f] : p.prefix_L) > 0) n_pre = p.n_ranges[f];
+    }
+    const int n = p.n_own + n_pre;
+    const auto ml = [&](long long row, int s) {
+        if (s >= p.n_own) return p.pre_ml[row * p.n_pre + s - p.n_own];
+        const float* q = p.own + (row * p.n_own + s) * (D + 2) + D;
+        return make_float2(q[0], q[1]);
+    };
+    const auto o_of = [&](long long row, int s) {
+        return s < p.n_own ? p.own + (row * p.n_own + s) * (D + 2) : p.pre_o + (row * p.n_pre + s - p.n_own) * D;
     };
     const int tid = threadIdx.x;
     if (static_cast<int>(blockIdx.y) < p.G) {
         const long long row = row0 + blockIdx.y;
         float M = -INFINITY;
-        for (int s = 0; s < n; ++s) M = fmaxf(M, part(row, s)[D]);
+        for (int s = 0; s < n; ++s) M = fmaxf(M, ml(row, s).x);
         const float base = M == -INFINITY ? 0.f : M;
         if (tid < D) {
             float acc = 0.f, lsum = 0.f;
             for (int s = 0; s < n; ++s) {
-                const float* ps = part(row, s);
-                const float f = exp2f(ps[D] - base);
-                lsum += f * ps[D + 1];
-                acc += f * ps[tid];
+                const float2 v = ml(row, s);
+                const float f = exp2f(v.x - base);
+                lsum += f * v.y;
+                acc += f * o_of(row, s)[tid];
             }
             store_out(p.O, p.o_fp32, row * D + tid, lsum > 0.f ? acc / lsum : 0.f);
         }
@@ -613,9 +602,9 @@ __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const MergePa
     if (tid < p.G) {
         const long long row = row0 + tid;
         float M = -INFINITY, l = 0.f;
-        for (int s = 0; s < n; ++s) M = fmaxf(M, part(row, s)[D]);
+        for (int s = 0; s < n; ++s) M = fmaxf(M, ml(row, s).x);
         const float base = M == -INFINITY ? 0.f : M;
-        for (int s = 0; s < n; ++s) l += exp2f(part(row, s)[D] - base) * part(row, s)[D + 1];
+        for (int s = 0; s < n; ++s) l += exp2f(ml(row, s).x - base) * ml(row, s).y;
         Ms[tid] = base;
         rl[tid] = l > 0.f ? 1.f / l : 0.f;
     }
@@ -662,8 +651,8 @@ template <int D>
 static int attn_ctas_per_sm(int W, int G) {
     int n = 0;
     const int smem = attn_smem_bytes<D>(W, G);
-    if (cudaFuncSetAttribute(attn_kernel<D, 1, kExtNone>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<D, 1, kExtNone>, kAttnThreads, smem) != cudaSuccess) {
+    if (cudaFuncSetAttribute(attn_kernel<D, 1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<D, 1, false>, kAttnThreads, smem) != cudaSuccess) {
         cudaGetLastError();
         return 1;
     }
@@ -688,11 +677,11 @@ static cudaError_t launch_maybe_pdl(Kernel k, int grid, int threads, int smem, b
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
-// The passes of dak_attn_acc / dak_attn_prefix: partials only.
-template <int D, int EXT>
+// The own-cache pass of dak_attn_acc / dak_attn_prefix: partials only.
+template <int D>
 static cudaError_t launch_attn_ext_d(const AttnParams& p, int grid, int W, bool pdl, cudaStream_t s) {
     const int smem = attn_smem_bytes<D>(W, p.G);
-    auto k = p.o_fp32 ? attn_kernel<D, 3, EXT> : attn_kernel<D, 2, EXT>;
+    auto k = p.o_fp32 ? attn_kernel<D, 3, true> : attn_kernel<D, 2, true>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     return e == cudaSuccess ? launch_maybe_pdl(k, grid, kAttnThreads, smem, pdl, s, p) : e;
 }
@@ -700,7 +689,7 @@ static cudaError_t launch_attn_ext_d(const AttnParams& p, int grid, int W, bool 
 template <int D>
 static cudaError_t launch_attn_d(const AttnParams& p, int grid, int W, bool pdl, cudaStream_t s) {
     const int smem = attn_smem_bytes<D>(W, p.G);
-    auto k = p.o_fp32 ? attn_kernel<D, 2, kExtNone> : attn_kernel<D, 1, kExtNone>;
+    auto k = p.o_fp32 ? attn_kernel<D, 2, false> : attn_kernel<D, 1, false>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     e = launch_maybe_pdl(k, grid, kAttnThreads, smem, pdl, s, p);
@@ -794,8 +783,8 @@ static dak_status launch_attn_kernels(const void* Q, const dak_placement* KV, co
     if (ext) {
         p.scores = ext->scores;
         p.score_pitch = ext->score_pitch;
-        e = KV->D == 128 ? launch_attn_ext_d<128, kExtOwn>(p, grid, W, pdl, stream)
-                         : launch_attn_ext_d<64, kExtOwn>(p, grid, W, pdl, stream);
+        e = KV->D == 128 ? launch_attn_ext_d<128>(p, grid, W, pdl, stream)
+                         : launch_attn_ext_d<64>(p, grid, W, pdl, stream);
     } else {
         e = KV->D == 128 ? launch_attn_d<128>(p, grid, W, pdl, stream) : launch_attn_d<64>(p, grid, W, pdl, stream);
     }
@@ -821,11 +810,12 @@ dak_status launch_attn(const void* Q, const dak_placement* KV, const void* host_
 }
 
 // The passes of dak_attn_acc (P null) and dak_attn_prefix. Workspace: the own pass's partials,
-// the prefix pass's partials and the scores, each rounded up to 256 bytes.
+// the prefix pass's (o, then maxima and sums, then the ranges' counts) and the scores, each
+// rounded up to 256 bytes.
 struct ExtLayout {
     int n_own, n_pre, score_pitch;
-    size_t own_bytes, pre_bytes, score_bytes;
-    size_t total() const { return own_bytes + pre_bytes + score_bytes; }
+    size_t own_bytes, pre_o_bytes, pre_ml_bytes, ranges_bytes, score_bytes;
+    size_t total() const { return own_bytes + pre_o_bytes + pre_ml_bytes + ranges_bytes + score_bytes; }
 };
 
 static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -834,9 +824,11 @@ static ExtLayout ext_layout(const dak_placement* KV, const dak_placement* P, int
     ExtLayout x{};
     const size_t rows = static_cast<size_t>(KV->B) * H_q;
     x.n_own = n_split > 0 ? n_split : default_split(KV->B, KV->H_kv, KV->L);
-    x.n_pre = P ? default_split(KV->B, P->H_kv, P->L) : 0;
+    x.n_pre = P ? prefix_max_ranges(P) : 0;
     x.own_bytes = round256(rows * x.n_own * (KV->D + 2) * sizeof(float));
-    x.pre_bytes = round256(rows * x.n_pre * (KV->D + 2) * sizeof(float));
+    x.pre_o_bytes = round256(rows * x.n_pre * KV->D * sizeof(float));
+    x.pre_ml_bytes = round256(rows * x.n_pre * sizeof(float2));
+    x.ranges_bytes = P ? round256(static_cast<size_t>(P->B) * sizeof(int)) : 0;
     x.score_pitch = (KV->L + kChunkTok - 1) / kChunkTok * kChunkTok;
     x.score_bytes = with_acc ? round256(rows * x.score_pitch * sizeof(float)) : 0;
     return x;
@@ -855,6 +847,7 @@ static dak_status launch_attn_ext(const void* Q, const dak_placement* KV, const 
     if (!KV || KV->kind != 1 || !Q || !O || H_q <= 0 || H_q % KV->H_kv) return DAK_ERR_INVALID;
     if (H_q / KV->H_kv > 16) return DAK_ERR_UNSUPPORTED;
     if (P && (P->kind != 1 || P->D != KV->D || P->H_kv != KV->H_kv || P->device != KV->device)) return DAK_ERR_INVALID;
+    if (P && P->B > kMaxPrefixes) return DAK_ERR_UNSUPPORTED;
     if (t && t->n_split > kMaxSplits) return DAK_ERR_INVALID;
     if (acc_out && acc_in &&
         partly_overlaps(acc_in, acc_out, static_cast<size_t>(KV->B) * KV->H_kv * KV->L * sizeof(float))) {
@@ -871,52 +864,40 @@ static dak_status launch_attn_ext(const void* Q, const dak_placement* KV, const 
     if (cudaGetDevice(&dev) != cudaSuccess) return DAK_ERR_CUDA;
     if (dev != KV->device) return DAK_ERR_INVALID;
     uint8_t* w = static_cast<uint8_t*>(ws);
-    float* own = reinterpret_cast<float*>(w);
-    float* pre = reinterpret_cast<float*>(w + x.own_bytes);
-
+    const auto take = [&](size_t bytes) {
+        uint8_t* at = w;
+        w += bytes;
+        return at;
+    };
+    MergeParams m{};
+    float* own = reinterpret_cast<float*>(take(x.own_bytes));
+    float* pre_o = reinterpret_cast<float*>(take(x.pre_o_bytes));
+    float* pre_ml = reinterpret_cast<float*>(take(x.pre_ml_bytes));
+    int* n_ranges = reinterpret_cast<int*>(take(x.ranges_bytes));
+    AttnExt ext;
+    ext.scores = acc_out ? reinterpret_cast<float*>(w) : nullptr;
+    ext.score_pitch = x.score_pitch;
+    if (P) {
+        const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(KV->D));
+        const dak_status r = launch_prefix(Q, P, prefix_lens, prefix_of, KV->B, H_q, sc * 1.4426950408889634f, o_fp32,
+                                           pre_o, pre_ml, n_ranges, stream);
+        if (r != DAK_OK) return r;
+        m.pre_o = pre_o;
+        m.pre_ml = reinterpret_cast<const float2*>(pre_ml);
+        m.n_ranges = n_ranges;
+        m.prefix_of = prefix_of;
+        m.prefix_lens = prefix_lens;
+        m.n_pre = x.n_pre;
+        m.n_prefix = P->B;
+        m.prefix_L = P->L;
+    }
     dak_tuning tun = t ? *t : dak_tuning{};
     tun.n_split = x.n_own;
-    AttnExt ext;
-    ext.scores = acc_out ? reinterpret_cast<float*>(w + x.own_bytes + x.pre_bytes) : nullptr;
-    ext.score_pitch = x.score_pitch;
-    dak_status r = launch_attn_kernels(Q, KV, KV->host_dev, seq_lens, H_q, scale, O, own, x.own_bytes, &tun, stream,
-                                       o_fp32, link, &ext);
+    const dak_status r = launch_attn_kernels(Q, KV, KV->host_dev, seq_lens, H_q, scale, O, own, x.own_bytes, &tun, stream,
+                                             o_fp32, link, &ext);
     if (r != DAK_OK) return r;
-    if (P) {
-        AttnParams p{};
-        p.Q = static_cast<const __nv_bfloat16*>(Q);
-        p.kv[0] = static_cast<const uint8_t*>(P->host_dev);
-        p.kv[1] = static_cast<const uint8_t*>(P->hbm_ptr);
-        p.seq_lens = prefix_lens;
-        p.o_fp32 = o_fp32 ? 1 : 0;
-        p.ws = pre;
-        p.B = KV->B;
-        p.Hq = H_q;
-        p.Hkv = KV->H_kv;
-        p.G = H_q / KV->H_kv;
-        p.L = P->L;
-        p.h_s = P->h_s;
-        p.n_split = x.n_pre;
-        p.split_len = ((P->L + x.n_pre - 1) / x.n_pre + kChunkTok - 1) / kChunkTok * kChunkTok;
-        p.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(KV->D))) * 1.4426950408889634f;
-        p.head_bytes = P->head_bytes;
-        p.st = status_ptr();
-        if (!p.st) return DAK_ERR_CUDA;
-        p.prefix_of = prefix_of;
-        p.n_prefix = P->B;
-        p.hbm_units = static_cast<long long>(KV->B) * KV->H_kv * x.n_pre;
-        p.host_window = p.hbm_window = kAttnStages;
-        const int per_sm = KV->D == 128 ? attn_ctas_per_sm<128>(kAttnStages, p.G) : attn_ctas_per_sm<64>(kAttnStages, p.G);
-        p.n_hbm_ctas = static_cast<int>(std::min<long long>(p.hbm_units, static_cast<long long>(per_sm) * device_sm_count()));
-        const cudaError_t e = KV->D == 128 ? launch_attn_ext_d<128, kExtPrefix>(p, p.n_hbm_ctas, kAttnStages, false, stream)
-                                           : launch_attn_ext_d<64, kExtPrefix>(p, p.n_hbm_ctas, kAttnStages, false, stream);
-        if (e != cudaSuccess) return cuda_status(e);
-    }
-    MergeParams m{};
     m.own = own;
-    m.pre = pre;
     m.n_own = x.n_own;
-    m.n_pre = x.n_pre;
     m.O = O;
     m.o_fp32 = o_fp32 ? 1 : 0;
     m.scores = ext.scores;

@@ -4,6 +4,7 @@
 // library's device status word.
 #pragma once
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -11,6 +12,9 @@
 #include "dak_internal.h"
 
 namespace dak {
+
+// The driver's tensor-map encoder (null if it cannot be found).
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 // ------------------------------------------------------------------------------------
 // status word: kernels never trap; a failed wait or a bad index records a code in the

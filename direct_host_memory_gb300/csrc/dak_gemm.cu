@@ -1570,7 +1570,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 // ======================================================================================
 using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
 
-static EncodeTiledFn encode_fn() {
+EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
