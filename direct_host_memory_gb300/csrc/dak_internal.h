@@ -141,7 +141,7 @@ dak_status launch_attn(const void* Q, const dak_placement* KV, const void* host_
 // [rows][ranges][D] and ml_part [rows][ranges][2] (maximum in the log2 domain, sum), and in
 // n_ranges [n_prefix] how many of them a prefix's rows have (not written for a prefix without
 // members or rows). Arguments are checked by the caller.
-constexpr int kMaxPrefixes = 2048;
+constexpr int kMaxPrefixes = 1024;
 int prefix_max_ranges(const dak_placement* P);
 dak_status launch_prefix(const void* Q, const dak_placement* P, const int* lens, const int* of, int B, int H_q,
                          float scale_log2, int o_fp32, float* o_part, float* ml_part, int* n_ranges, cudaStream_t s);

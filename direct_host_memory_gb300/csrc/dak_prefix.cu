@@ -29,7 +29,7 @@
 
 namespace dak {
 
-constexpr int kPrefixThreads = 10 * 32;  // two softmax warpgroups, copies, MMAs
+constexpr int kPrefixThreads = 11 * 32;  // two softmax warpgroups, copies, each stream's products
 constexpr int kPrefixMinChunks = 2;      // chunks of 64 keys in a range, at least
 
 struct PrefixMaps {
@@ -45,11 +45,12 @@ struct PrefixParams {
     float2* ml_part;   // [B * Hq][n_pre]: m (log2 domain), l
     int* n_ranges;     // [n_prefix]: key ranges of a prefix that has members and rows
     int B, Hq, Hkv, G, L, n_prefix, n_pre, h_s, slab_chunks;
+    int mpt;  // members of a 128-row tile: 128 / G
     float scale_log2;
     DevStatus* st;
 };
 
-enum : uint32_t { X_PROD_EMPTY = 0x51, X_MMA_FULL, X_MMA_P, X_MMA_PV, X_SM_S, X_SM_V, X_SM_O, X_DRAIN };
+enum : uint32_t { X_PROD_EMPTY = 0x51, X_PROD_FULL, X_MMA_FULL, X_MMA_P, X_MMA_PV, X_MMA_GO, X_SM_S, X_SM_V, X_SM_O, X_DRAIN };
 
 // What a CTA works on.
 struct PrefixUnit {
@@ -61,11 +62,12 @@ struct PrefixUnit {
     int units;         // units of the whole launch
 };
 
-__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int kv, int chunk, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int kv, int chunk, uint64_t* bar,
+                                            uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4, "
-        "%2}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(0), "r"(kv), "r"(chunk), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
+        "%2, %3, %4, %2}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(0), "r"(kv), "r"(chunk), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
 
@@ -78,43 +80,43 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-    uint32_t r[32];
+// 16 columns of this thread's lane; the values are there after tmem_wait(v).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Waits for every load of this thread; the registers pass through so that no use of them moves up.
+__device__ __forceinline__ void tmem_wait(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                   "+f"(v[15])
+                 :
+                 : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
-    uint32_t r[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
             taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 bytes global -> shared, `bytes` (16 or 0) of them from src and zeros for the rest.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ float exp2_ftz(float x) {
     float y;
@@ -122,65 +124,129 @@ __device__ __forceinline__ float exp2_ftz(float x) {
     return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+          "l"(*reinterpret_cast<unsigned long long*>(&c)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return *reinterpret_cast<float2*>(&r);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 template <int ID, int THREADS>
 __device__ __forceinline__ void prefix_bar() {
     asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
 }
 
-__device__ __forceinline__ int prefix_chunks(const PrefixParams& p, int f) {
-    const int n = p.lens ? min(max(p.lens[f], 0), p.L) : p.L;
-    return (n + 63) >> 6;
+__device__ __forceinline__ void report_prefix(const PrefixParams& p, int b) {
+    report(p.st, DAK_ERR_BOUNDS, (0x9F1Full << 32) | static_cast<unsigned>(b));
 }
 
-// Unit u of the launch into *unit (units == 0: none at all) and its members' requests. All threads
-// call it; scratch: n_prefix int2 of shared memory, free until the next barrier.
-__device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int2* scratch, PrefixUnit* unit, int* member) {
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int mpt = 128 / p.G;  // members of a 128-row tile
-    for (int f = tid; f < p.n_prefix; f += kPrefixThreads) scratch[f] = make_int2(p.of ? 0 : f == 0 ? p.B : 0, 0);
-    __syncthreads();
-    if (p.of) {
-        for (int b = tid; b < p.B; b += kPrefixThreads) {
-            const int e = p.of[b];
-            if (e >= 0 && e < p.n_prefix) atomicAdd(&scratch[e].x, 1);
-            if (e >= p.n_prefix && blockIdx.x == 0) report(p.st, DAK_ERR_BOUNDS, (0x9F1Full << 32) | static_cast<unsigned>(b));
+// Unit u of the launch into *unit (units == 0: none at all) and its members' requests, by one warp.
+// Every CTA waits for this before its first copy, so it is built for latency: the map and the
+// lengths are loaded side by side (the first 128 requests' map stays in registers), counting and
+// searching run in shared memory, scratch[f] (n_prefix int4, free until the next barrier): requests,
+// 256-row tiles, chunks, rows; divisions are 32-bit.
+__device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* scratch, PrefixUnit* unit, int* member) {
+    constexpr unsigned all = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    const int per_tile = 2 * p.mpt;  // members of a 256-row tile
+    const int ctas = static_cast<int>(gridDim.x);
+    int map[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) map[k] = p.of && k * 32 + lane < p.B ? p.of[k * 32 + lane] : -1;
+    const auto map_of = [&](int b0) {  // the map of requests b0 + lane, in steps of 32 from 0
+        return b0 == 0 ? map[0] : b0 == 32 ? map[1] : b0 == 64 ? map[2] : b0 == 96 ? map[3]
+               : b0 + lane < p.B ? p.of[b0 + lane] : -1;
+    };
+    const auto ranges = [&](int c, int T) { return min((c + T - 1) / T, p.n_pre); };
+    int f = -1, start = 0, base = 0, n = 0;
+    int4 e;
+    if (p.n_prefix == 1) {
+        const int len = p.lens ? min(max(p.lens[0], 0), p.L) : p.L;
+        int cnt = p.B;
+        if (p.of) {
+            cnt = 0;
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                const int v = map_of(b0);
+                if (v > 0 && blockIdx.x == 0) report_prefix(p, b0 + lane);
+                cnt += __popc(__ballot_sync(all, v == 0));
+            }
         }
-        __syncthreads();
-    }
-    if (tid < 32) {
-        const unsigned all = 0xffffffffu;
-        int cmax = 1;
-        for (int f = lane; f < p.n_prefix; f += 32) {
-            const int c = prefix_chunks(p, f);
-            const int tiles = c > 0 ? (scratch[f].x + 2 * mpt - 1) / (2 * mpt) : 0;
-            scratch[f].y = tiles;
-            if (tiles) cmax = max(cmax, c);
+        e = make_int4(cnt, (cnt + per_tile - 1) / per_tile, (len + 63) >> 6, len);
+        if (e.y > 0 && e.z > 0) {
+            const int n_tiles = e.y * p.Hkv, each = n_tiles < ctas ? ctas / n_tiles : 1;
+            n = ranges(e.z, max(min(kPrefixMinChunks, e.z), (e.z + each - 1) / each));
+            base = n_tiles * n;
+            if (u < base) f = 0;
+        }
+    } else {
+        for (int i = lane; i < p.n_prefix; i += 32) {
+            const int len = p.lens ? min(max(p.lens[i], 0), p.L) : p.L;
+            scratch[i] = make_int4(p.of || i > 0 ? 0 : p.B, 0, (len + 63) >> 6, len);
+        }
+        __syncwarp();
+        if (p.of) {
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                const int v = map_of(b0);
+                const bool in = v >= 0 && v < p.n_prefix;
+                if (v >= p.n_prefix && blockIdx.x == 0) report_prefix(p, b0 + lane);
+                const unsigned same = __match_any_sync(all, in ? v : -1);
+                if (in && lane == __ffs(same) - 1) scratch[v].x += __popc(same);
+                __syncwarp();
+            }
+        }
+        int cmax = 1, n_tiles = 0;
+        float work = 0.f;
+        for (int i = lane; i < p.n_prefix; i += 32) {
+            const int4 q = scratch[i];
+            const int tiles = q.z > 0 ? (q.x + per_tile - 1) / per_tile : 0;
+            scratch[i].y = tiles;
+            n_tiles += tiles;
+            work += static_cast<float>(tiles) * static_cast<float>(q.z);
+            if (tiles) cmax = max(cmax, q.z);
         }
         __syncwarp();
         cmax = __reduce_max_sync(all, cmax);
-        const auto ranges = [&](int c, int T) { return min((c + T - 1) / T, p.n_pre); };
-        const auto total = [&](int T) {
-            int n = 0;
-            for (int f = lane; f < p.n_prefix; f += 32) {
-                if (scratch[f].y) n += scratch[f].y * ranges(prefix_chunks(p, f), T);
-            }
-            return __reduce_add_sync(all, n) * p.Hkv;
-        };
-        int lo = min(kPrefixMinChunks, cmax), hi = cmax;
-        if (total(hi) < static_cast<int>(gridDim.x)) {
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (total(mid) <= static_cast<int>(gridDim.x)) hi = mid;
+        n_tiles = __reduce_add_sync(all, n_tiles) * p.Hkv;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(all, work, o);
+        work *= static_cast<float>(p.Hkv);
+        int T = cmax;
+        if (n_tiles < ctas) {
+            // sum tiles ceil(c / T) lies between work / T and work / T + n_tiles
+            const auto total = [&](int t) {
+                int k = 0;
+                for (int i = lane; i < p.n_prefix; i += 32) k += scratch[i].y * ranges(scratch[i].z, t);
+                return __reduce_add_sync(all, k) * p.Hkv;
+            };
+            int lo = max(min(kPrefixMinChunks, cmax), static_cast<int>(min(work / static_cast<float>(ctas), 1e9f)) - 1);
+            lo = min(lo, cmax);
+            T = max(lo, min(cmax, static_cast<int>(min(work / static_cast<float>(ctas - n_tiles), 1e9f)) + 2));
+            while (lo < T) {
+                const int mid = (lo + T) >> 1;
+                if (total(mid) <= ctas) T = mid;
                 else lo = mid + 1;
             }
         }
-        const int T = hi;
-        int base = 0, f = -1, start = 0;
         for (int f0 = 0; f0 < p.n_prefix; f0 += 32) {
             const int ff = f0 + lane;
-            int n = 0;
-            if (ff < p.n_prefix && scratch[ff].y) n = scratch[ff].y * ranges(prefix_chunks(p, ff), T) * p.Hkv;
-            int incl = n;
+            const int k = ff < p.n_prefix ? scratch[ff].y * ranges(scratch[ff].z, T) * p.Hkv : 0;
+            int incl = k;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(all, incl, o);
@@ -190,53 +256,213 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int2* sc
             if (f < 0 && hit) {
                 const int l = __ffs(hit) - 1;
                 f = f0 + l;
-                start = base + __shfl_sync(all, incl - n, l);
+                start = base + __shfl_sync(all, incl - k, l);
             }
             base += __shfl_sync(all, incl, 31);
         }
-        if (f < 0) {
-            if (lane == 0) unit->units = 0;
-        } else {
-            const int c = prefix_chunks(p, f), n = ranges(c, T), tiles = scratch[f].y, cnt = scratch[f].x;
-            const int rem = u - start;
-            const int g = rem / (tiles * n), t = rem / n % tiles, s = rem % n;
-            const int r0 = t * 2 * mpt, here = min(2 * mpt, cnt - r0);
-            if (lane == 0) {
-                unit->f = f;
-                unit->g = g;
-                unit->s = s;
-                unit->c0 = static_cast<int>(static_cast<long long>(c) * s / n);
-                unit->c1 = static_cast<int>(static_cast<long long>(c) * (s + 1) / n);
-                unit->len = p.lens ? min(max(p.lens[f], 0), p.L) : p.L;
-                unit->members = here;
-                unit->two = here > mpt;
-                unit->units = base;
-                if (g == 0 && t == 0 && s == 0) p.n_ranges[f] = n;
-            }
-            if (!p.of) {
-                for (int i = lane; i < here; i += 32) member[i] = r0 + i;
-            } else {
-                int seen = 0;
-                for (int b0 = 0; b0 < p.B && seen < r0 + here; b0 += 32) {
-                    const bool mine = b0 + lane < p.B && p.of[b0 + lane] == f;
-                    const unsigned m = __ballot_sync(all, mine);
-                    const int rank = seen + __popc(m & ((1u << lane) - 1)) - r0;
-                    if (mine && rank >= 0 && rank < here) member[rank] = b0 + lane;
-                    seen += __popc(m);
-                }
-            }
+        if (f >= 0) {
+            e = scratch[f];
+            n = ranges(e.z, T);
         }
     }
-    __syncthreads();
+    if (f < 0) {
+        if (lane == 0) unit->units = 0;
+        return;
+    }
+    const int c = e.z, rem = u - start;
+    const int gt = rem / n, s = rem - gt * n, g = gt / e.y, t = gt - g * e.y;
+    const int r0 = t * per_tile, here = min(per_tile, e.x - r0);
+    if (lane == 0) {
+        const int each = c / n, more = c - each * n;  // the first `more` ranges get a chunk more
+        unit->f = f;
+        unit->g = g;
+        unit->s = s;
+        unit->c0 = s * each + min(s, more);
+        unit->c1 = unit->c0 + each + (s < more);
+        unit->len = e.w;
+        unit->members = here;
+        unit->two = here > p.mpt;
+        unit->units = base;
+        if (gt == 0 && s == 0) p.n_ranges[f] = n;
+    }
+    if (!p.of) {
+        for (int i = lane; i < here; i += 32) member[i] = r0 + i;
+        return;
+    }
+    int seen = 0;
+    for (int b0 = 0; b0 < p.B && seen < r0 + here; b0 += 32) {
+        const int v = map_of(b0);
+        const unsigned m = __ballot_sync(all, v == f);
+        const int rank = seen + __popc(m & ((1u << lane) - 1)) - r0;
+        if (v == f && rank >= 0 && rank < here) member[rank] = b0 + lane;
+        seen += __popc(m);
+    }
 }
+
+// The products of a step of nk chunks of 64 keys, one thread. Descriptors differ in their start
+// address alone, which is the low word's. This and all code that a CTA runs only a few times is kept
+// small: a first run fetches its instructions through the memory system that K and V saturate, at 10
+// cycles an instruction and more, which set the time of short prefixes.
+//
+// S (128 rows x 64 nk keys) = Q . K^T: both K-major, 128-byte rows in 8-row groups 1024 bytes apart,
+// 32 bytes further per 16 columns and a half further per 64.
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_addr, uint32_t k_addr, int nk) {
+    const uint32_t idesc = idesc_bf16_f32(128, static_cast<uint32_t>(64 * nk));
+    uint64_t qd = smem_desc(q_addr, 16, 1024, 2), kd = smem_desc(k_addr, 16, 1024, 2);
+#pragma unroll 1
+    for (int h = 0; h < D / 64; ++h) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) umma_bf16(d_tmem, qd + k * 2, kd + k * 2, idesc, h > 0 || k > 0);
+        qd += 16384 >> 4;
+        kd += static_cast<uint64_t>(8192 * nk) >> 4;
+    }
+}
+
+// O (128 rows x D) += P . V: P from TMEM in PARTS bf16 parts, two keys a column, where the softmax
+// put them; V MN-major (idesc bit 16): N = D along a row's halves, 8192 nk bytes apart, K = the
+// keys in groups of eight, 1024 bytes apart.
+template <int D, int PARTS>
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_addr, int nk, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, D) | (1u << 16);
+    uint64_t vd = smem_desc(v_addr, static_cast<uint32_t>(8192 * nk), 1024, 2);
+    uint32_t acc = accumulate;
+#pragma unroll 1
+    for (int k = 0; k < 4 * nk; ++k) {  // 16 keys: columns 16 k + 8 q of P's part q, the third at 64 + 8 k
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+            umma_bf16_ts(d_tmem, p_tmem + (q < 2 ? k * 16 + q * 8 : 64 + k * 8), vd, idesc, acc);
+            acc = 1;
+        }
+        vd += 2048 >> 4;
+    }
+}
+
+// One step of a row: S (nk chunks of 64 keys, the first `valid` of them real) into P over it in TMEM,
+// with the running maximum (of the reference, log2 domain) and sum. S is read twice, once for the
+// maximum and once for the exponentials, 32 columns a turn.
+template <int D, int KEYS>
+__device__ __forceinline__ void softmax_step(uint32_t s_addr, uint32_t o_addr, int nk, int valid, float scale_log2,
+                                             float& m_ref, float& l, bool first) {
+    const auto load = [&](int q, float(&v)[2][16]) {
+        tmem_ld16(s_addr + q * 32, v[0]);
+        tmem_ld16(s_addr + q * 32 + 16, v[1]);
+        tmem_wait(v[0]);
+        tmem_wait(v[1]);
+        if (valid < 32 * q + 32) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                if (32 * q + k >= valid) v[k >> 4][k & 15] = -INFINITY;
+            }
+        }
+    };
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+    for (int q = 0; q < 2 * nk; ++q) {
+        float v[2][16];
+        load(q, v);
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+            mx[0] = max3(mx[0], v[0][k], v[0][k + 1]);
+            mx[1] = max3(mx[1], v[1][k], v[1][k + 1]);
+        }
+    }
+    const float m_new = fmaxf(mx[0], mx[1]) * scale_log2;
+    // the reference only moves when a row's maximum outgrows it by 2^8: until then the sums just
+    // grow, which fp32 holds
+    if (first) {
+        m_ref = m_new;
+    } else if (__any_sync(0xffffffffu, m_new > m_ref + 8.f)) {
+        const float m2 = fmaxf(m_ref, m_new);
+        const float f = m2 == -INFINITY ? 1.f : exp2_ftz(m_ref - m2);
+        m_ref = m2;
+        l *= f;
+#pragma unroll 1
+        for (int q = 0; q < D / 16; ++q) {
+            float o[16];
+            tmem_ld16(o_addr + q * 16, o);
+            tmem_wait(o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] *= f;
+            tmem_st16(o_addr + q * 16, o);
+        }
+    }
+    const float base = m_ref == -INFINITY ? 0.f : m_ref;
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    const float2 scale2 = make_float2(scale_log2, scale_log2), base2 = make_float2(-base, -base);
+    const float2 minus = make_float2(-1.f, -1.f);
+#pragma unroll 1
+    for (int q = 0; q < 2 * nk; ++q) {
+        float v[2][16];
+        load(q, v);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t hi[8], lo[8], th[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 e = fma2(make_float2(v[h][2 * k], v[h][2 * k + 1]), scale2, base2);
+                const float2 w = make_float2(exp2_ftz(e.x), exp2_ftz(e.y));
+                sum[k & 1] = add2(sum[k & 1], w);
+                hi[k] = pack_bf16(w.x, w.y);
+                float2 r = fma2(make_float2(bf_lo(hi[k]), bf_hi(hi[k])), minus, w);
+                lo[k] = pack_bf16(r.x, r.y);
+                if (KEYS == 64) {
+                    r = fma2(make_float2(bf_lo(lo[k]), bf_hi(lo[k])), minus, r);
+                    th[k] = pack_bf16(r.x, r.y);
+                }
+            }
+            // P goes over the 16 scores that it was made from, part by part; the third part has the
+            // columns behind a step of 64
+            tmem_st8(s_addr + q * 32 + h * 16, hi);
+            tmem_st8(s_addr + q * 32 + h * 16 + 8, lo);
+            if (KEYS == 64) tmem_st8(s_addr + 64 + q * 16 + h * 8, th);
+        }
+    }
+    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
+// The 32 rows of HALF columns that a warp put into `stage` (piece c of row r at c ^ (r & 7)) to rows
+// `at` of each lane (negative: none) of out, `pitch` apart; neighbouring lanes on neighbouring
+// addresses (each thread storing its own row took 4 us for a tile).
+template <int HALF>
+__device__ __forceinline__ void store_rows(const uint8_t* stage, float* out, int pitch, long long at) {
+    constexpr int HP = HALF / 4;
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll 4
+    for (int e = lane; e < 32 * HP; e += 32) {
+        const int row = e / HP, c = e % HP;
+        const long long to = __shfl_sync(0xffffffffu, at, row);
+        const float4 v = *reinterpret_cast<const float4*>(stage + row * (HALF * 4) + ((c ^ (row & 7)) << 4));
+        if (to >= 0) *reinterpret_cast<float4*>(out + to * pitch + c * 4) = v;
+    }
+    __syncwarp();
+}
+
+// Where a count of K and V stages lies in the ring.
+template <int NS>
+struct RingPos {
+    int slot;
+    uint32_t phase;
+    __device__ __forceinline__ explicit RingPos(int n) : slot(n % NS), phase(static_cast<uint32_t>(n / NS) & 1u) {}
+    __device__ __forceinline__ void advance(int by) {  // by < NS
+        slot += by;
+        if (slot >= NS) {
+            slot -= NS;
+            phase ^= 1u;
+        }
+    }
+};
 
 // KEYS: keys of a step, 128 (bf16 output, P in two bf16 parts) or 64 (fp32 output, three).
 template <int D, int KEYS>
 struct PrefixCfg {
-    static constexpr int kHalves = D / 64;
     static constexpr int kTileBytes = 128 * D * 2;  // one Q tile
     static constexpr int kStage = KEYS * D * 2;     // K or V of a step
     static constexpr int kStages = std::min(12, (224 * 1024 - 2 * kTileBytes) / kStage);
+    // copies of a CTA that have not landed yet: enough for the memory system's latency; more only
+    // queue in it and hold up everything else that comes that way
+    static constexpr int kInFlight = std::min(kStages, 96 * 1024 / kStage);
     static constexpr int kSmem = 2 * kTileBytes + kStages * kStage + 1024;
 };
 
@@ -246,10 +472,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     using C = PrefixCfg<D, KEYS>;
     constexpr int NS = C::kStages;
     constexpr int SMAX = KEYS / 64;  // chunks of a whole step
+    constexpr int parts = KEYS == 64 ? 3 : 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     uint8_t* ring = smem + 2 * C::kTileBytes;
-    __shared__ uint64_t full[NS], empty[NS], s_full[2], p_ready[2], pv_done[2];
+    __shared__ uint64_t full[NS], empty[NS], s_full[2], p_ready[2], pv_done[2], go;
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_flag;
     __shared__ PrefixUnit unit;
@@ -259,12 +486,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     volatile int* abort = &abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 32) {
         abort_flag = 0;
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);
         }
+        mbar_init(&go, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&p_ready[s], 4);
@@ -276,133 +504,141 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         tmem_alloc(&tmem_sh, 512);
         tmem_relinquish();
     }
+    // warp 0 goes straight to the plan and meets the others after it
     tc_fence_before();
-    __syncthreads();
+    if (warp == 0) asm volatile("bar.arrive 5, %0;" ::"n"(kPrefixThreads) : "memory");
+    else prefix_bar<5, kPrefixThreads>();
     tc_fence_after();
-    const uint32_t tmem = tmem_sh;
     // TMEM columns: S (and P over it) of the two streams at 0 and 128, O at 256 and 256 + D
-    long long it0 = 0;        // K and V stages used by earlier units
+    int it0 = 0;              // K and V stages used by earlier units
     int used[2] = {0, 0};     // steps each stream did in earlier units
+    int paired = 0;           // earlier units with two row tiles
     for (int u = blockIdx.x;; u += gridDim.x) {
-        plan_unit(p, u, reinterpret_cast<int2*>(smem), &unit, member);
+        if (warp == 0) plan_unit(p, u, reinterpret_cast<int4*>(smem), &unit, member);
+        __syncthreads();
+        tc_fence_after();
+        const uint32_t tmem = tmem_sh;
         const PrefixUnit x = unit;
         if (x.units == 0) break;
         const int steps = (x.c1 - x.c0 + SMAX - 1) / SMAX;
         const int items = x.two ? 2 * steps : steps;  // item i: stream i & 1, step i / 2 or i
-        constexpr int parts = KEYS == 64 ? 3 : 2;
         const long long slab = static_cast<long long>(x.f) * p.Hkv + x.g;
         const int tier = slab < p.h_s ? 0 : 1;
         const int step_of_shift = x.two ? 1 : 0;
-        __syncthreads();  // the scratch that the plan used is Q's memory
-
         if (warp == 8) {
             // ------------------------------------------------------------ copies
+            prefix_bar<4, 288>();  // Q's loads are on their way, ahead of the stream of K and V
             if (lane == 0) {
+                const uint64_t policy = policy_evict_first();
+                const auto wait_landed = [&](int i) {
+                    return mbar_wait(&full[i % NS], static_cast<uint32_t>((i / NS) & 1), abort, p.st, DAK_ERR_TIMEOUT,
+                                     X_PROD_FULL);
+                };
                 const int chunk0 = static_cast<int>((tier ? slab - p.h_s : slab) * p.slab_chunks);
-                long long it = it0;
+                int it = it0;
                 for (int j = 0; j < steps; ++j) {
                     const int c = x.c0 + j * SMAX, nk = min(SMAX, x.c1 - c);
                     const CUtensorMap* map = nk == SMAX ? &maps.step[tier] : &maps.tail[tier];
                     for (int kv = 0; kv < 2; ++kv, ++it) {
-                        const int s = static_cast<int>(it % NS);
+                        const int s = it % NS;
                         if (it >= NS && !mbar_wait(&empty[s], static_cast<uint32_t>((it / NS - 1) & 1), abort, p.st,
                                                    DAK_ERR_TIMEOUT, X_PROD_EMPTY)) {
                             goto copies_done;
                         }
+                        if (it >= it0 + C::kInFlight && !wait_landed(it - C::kInFlight)) goto copies_done;
                         mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nk * 64 * D * 2));
-                        tma_load_5d(ring + static_cast<size_t>(s) * C::kStage, map, kv, chunk0 + c, &full[s]);
+                        tma_load_5d(ring + static_cast<size_t>(s) * C::kStage, map, kv, chunk0 + c, &full[s], policy);
                     }
                 }
             copies_done:
                 if (*abort) {  // copies in flight land before the CTA may leave
                     volatile int dummy = 0;
                     for (int s = 0; s < NS && s < it; ++s) {
-                        const long long last = ((it - 1 - s) / NS) * NS + s;
+                        const int last = ((it - 1 - s) / NS) * NS + s;
                         mbar_wait(&full[s], static_cast<uint32_t>((last / NS) & 1), &dummy, p.st, DAK_ERR_TIMEOUT, X_DRAIN);
                     }
                 }
             }
             __syncwarp();
-        } else if (warp == 9) {
-            // ------------------------------------------------------------ products
-            prefix_bar<2, 288>();  // Q lies in shared memory
+        } else if (warp >= 9) {
+            // ------------------------------------------------------------ products, a warp per stream
+            // The whole warp runs the loop, so that its state and the descriptors stay warp-uniform;
+            // one elected lane issues. With one warp for both streams, what lies between the products
+            // (waits, address arithmetic) added up: 2.6k cycles a step of both at 1.5k of products.
+            const int st = warp - 9, stride = x.two ? 1 : 2;
+            prefix_bar<2, 320>();  // Q lies in shared memory
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t q_addr = smem_u32(smem), ring_addr = smem_u32(ring);
-                const auto stage_at = [&](int j, int kv) { return static_cast<int>((it0 + 2 * j + kv) % NS); };
-                const auto wait_full = [&](int j, int kv) {
-                    const long long it = it0 + 2 * j + kv;
-                    return mbar_wait(&full[it % NS], static_cast<uint32_t>((it / NS) & 1), abort, p.st, DAK_ERR_TIMEOUT,
-                                     X_MMA_FULL);
-                };
-                const auto qk = [&](int i) {
-                    const int st = i & 1, j = i >> step_of_shift;
-                    const int nk = min(SMAX, x.c1 - x.c0 - j * SMAX);
-                    if (!wait_full(j, 0)) return false;
-                    // S's columns still hold the P that the stream's last product reads
-                    if (i >= 2 && !mbar_wait(&pv_done[st], static_cast<uint32_t>((used[st] + (i >> 1) - 1) & 1), abort,
-                                             p.st, DAK_ERR_TIMEOUT, X_MMA_PV)) {
-                        return false;
-                    }
-                    tc_fence_after();
-                    const uint32_t a = q_addr + (x.two ? st * C::kTileBytes : 0);
-                    const uint32_t b = ring_addr + stage_at(j, 0) * C::kStage;
-                    const uint32_t idesc = idesc_bf16_f32(128, static_cast<uint32_t>(64 * nk));
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t h = k >> 2, in = (k & 3) * 32;
-                        umma_bf16(tmem + st * 128, smem_desc(a + h * 16384 + in, 16, 1024, 2),
-                                  smem_desc(b + h * (8192 * nk) + in, 16, 1024, 2), idesc, k > 0);
-                    }
+            const bool leader = elect_one();
+            const uint32_t q_addr = smem_u32(smem) + (x.two ? st * C::kTileBytes : 0), ring_addr = smem_u32(ring);
+            const uint32_t s_tmem = tmem + st * 128, o_tmem = tmem + 256 + st * D;
+            int j = x.two ? 0 : st, n = used[st];
+            RingPos<NS> pos(it0 + 2 * j);  // K of step j; V follows
+            const auto wait_full = [&](RingPos<NS> r) {
+                return mbar_wait(&full[r.slot], r.phase, abort, p.st, DAK_ERR_TIMEOUT, X_MMA_FULL);
+            };
+            // a stage is free when both streams have used it, or the one that does has said so twice
+            const auto release = [&](int slot) {
+                umma_commit(&empty[slot]);
+                if (!x.two) umma_commit(&empty[slot]);
+            };
+            const auto qk = [&]() {
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t b = ring_addr + pos.slot * C::kStage;
+                    issue_qk<D>(s_tmem, q_addr, b, min(SMAX, x.c1 - x.c0 - j * SMAX));
                     umma_commit(&s_full[st]);
-                    if (!x.two || st == 1) umma_commit(&empty[stage_at(j, 0)]);
-                    return true;
-                };
-                const auto pv = [&](int i) {
-                    const int st = i & 1, j = i >> step_of_shift;
-                    const int nk = min(SMAX, x.c1 - x.c0 - j * SMAX);
-                    if (!wait_full(j, 1) || !mbar_wait(&p_ready[st], static_cast<uint32_t>((used[st] + (i >> 1)) & 1),
-                                                       abort, p.st, DAK_ERR_TIMEOUT, X_MMA_P)) {
-                        return false;
-                    }
-                    tc_fence_after();
-                    const uint32_t v = ring_addr + stage_at(j, 1) * C::kStage;
-                    // V: N = D along a row's halves (8192 nk bytes apart), K = the keys, in groups of
-                    // eight 1024 bytes apart; bit 16: B is MN-major
-                    const uint32_t idesc = idesc_bf16_f32(128, D) | (1u << 16);
-                    for (int q = 0; q < parts; ++q) {
-                        for (int k = 0; k < 4 * nk; ++k) {
-                            umma_bf16_ts(tmem + 256 + st * D, tmem + st * 128 + q * (KEYS / 2) + k * 8,
-                                         smem_desc(v + k * 2048, 8192 * nk, 1024, 2), idesc, i >= 2 || q > 0 || k > 0);
-                        }
-                    }
+                    release(pos.slot);
+                }
+                __syncwarp();
+            };
+            // Two row tiles: the second stream starts once the first one's softmax is done, so that from
+            // then on each one's softmax runs under the other's products (in step they waited for the
+            // tensor cores together and then left them idle together).
+            bool ok = j < steps && wait_full(pos);
+            if (ok && x.two && st == 1) ok = mbar_wait(&go, paired & 1, abort, p.st, DAK_ERR_TIMEOUT, X_MMA_GO);
+            if (ok) qk();
+            for (bool first = true; ok; first = false, ++n) {
+                RingPos<NS> v = pos;
+                v.advance(1);
+                ok = wait_full(v) && mbar_wait(&p_ready[st], n & 1, abort, p.st, DAK_ERR_TIMEOUT, X_MMA_P);
+                if (!ok) break;
+                if (first && x.two && st == 0 && lane == 0) mbar_arrive(&go);
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t b = ring_addr + v.slot * C::kStage;
+                    issue_pv<D, parts>(o_tmem, s_tmem, b, min(SMAX, x.c1 - x.c0 - j * SMAX), !first);
                     umma_commit(&pv_done[st]);
-                    if (!x.two || st == 1) umma_commit(&empty[stage_at(j, 1)]);
-                    return true;
-                };
-                bool ok = qk(0) && (items < 2 || qk(1));
-                for (int i = 0; i < items && ok; ++i) ok = pv(i) && (i + 2 >= items || qk(i + 2));
+                    release(v.slot);
+                }
+                __syncwarp();
+                j += stride;
+                if (j >= steps) break;
+                pos.advance(2 * stride);
+                // S's columns hold the P that the product just issued reads: it finishes first
+                ok = wait_full(pos) && mbar_wait(&pv_done[st], n & 1, abort, p.st, DAK_ERR_TIMEOUT, X_MMA_PV);
+                if (ok) qk();
             }
             __syncwarp();
-        } else {
+        } else if (warp < 8) {
             // ------------------------------------------------------------ softmax, one row a thread
             const int st = warp >> 2, r = (warp & 3) * 32 + lane;
-            const int mpt = 128 / p.G;
+            const int mpt = p.mpt;
             {   // Q rows into the 128-byte swizzled K-major layout, rows without a member zero
-                const int n_rows = x.two ? 256 : 128;
-                for (int e = threadIdx.x; e < n_rows * (D / 8); e += 256) {
-                    const int row = e / (D / 8), c = e % (D / 8);
-                    const int tile = row >> 7, rr = row & 127, m = rr / p.G;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (m < mpt && tile * mpt + m < x.members) {
-                        const long long qrow = static_cast<long long>(member[tile * mpt + m]) * p.Hq + x.g * p.G + rr - m * p.G;
-                        v = *reinterpret_cast<const uint4*>(p.Q + qrow * D + c * 8);
-                    }
-                    *reinterpret_cast<uint4*>(smem + tile * C::kTileBytes + (c >> 3) * 16384 + rr * 128 +
-                                              (((c & 7) ^ (rr & 7)) << 4)) = v;
+                constexpr int PIECES = D / 8;  // 16-byte pieces of a row
+                const int n = (x.two ? 256 : 128) * PIECES;
+#pragma unroll 1
+                for (int e = threadIdx.x; e < n; e += 256) {
+                    const int rr = (e / PIECES) & 127, tile = e / (128 * PIECES), c = e % PIECES, m = rr / p.G;
+                    const bool there = m < mpt && tile * mpt + m < x.members;
+                    const __nv_bfloat16* src = p.Q + c * 8;
+                    if (there) src += (static_cast<long long>(member[tile * mpt + m]) * p.Hq + x.g * p.G + rr - m * p.G) * D;
+                    cp_async16(smem + tile * C::kTileBytes + (c >> 3) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), src,
+                               there ? 16 : 0);
                 }
+                asm volatile("bar.arrive 4, 288;" ::: "memory");  // K and V may start behind these copies
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();
-                prefix_bar<2, 288>();
+                prefix_bar<2, 320>();
             }
             const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
             const uint32_t s_addr = tmem + lanes + st * 128, o_addr = tmem + lanes + 256 + st * D;
@@ -420,79 +656,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                float s[KEYS];
-#pragma unroll
-                for (int q = 0; q < KEYS / 32; ++q) {
-                    if (q < 2 * nk) tmem_ld32(s_addr + q * 32, s + q * 32);
-                }
-                tmem_wait_ld();
-                if (valid < KEYS) {
-                    if (!x.two || st == 0) {
-                        // rows of V past the prefix may hold anything, also infinities and NaN,
-                        // which a probability of zero would not cancel
-                        const long long vit = it0 + 2 * j + 1;
-                        mbar_wait(&full[vit % NS], static_cast<uint32_t>((vit / NS) & 1), abort, p.st, DAK_ERR_TIMEOUT,
-                                  X_SM_V);
-                        uint8_t* v = ring + static_cast<size_t>(vit % NS) * C::kStage;
-                        for (int e = (warp & 3) * 32 + lane; e < (64 * nk - valid) * (D / 8); e += 128) {
-                            const int row = valid + e / (D / 8), c = e % (D / 8);
-                            *reinterpret_cast<uint4*>(v + (c >> 3) * (8192 * nk) + row * 128 + ((c & 7) << 4)) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
+                if (valid < 64 * nk && (!x.two || st == 0)) {
+                    // rows of V past the prefix may hold anything, also infinities and NaN, which a
+                    // probability of zero would not cancel
+                    const int vit = it0 + 2 * j + 1;
+                    mbar_wait(&full[vit % NS], static_cast<uint32_t>((vit / NS) & 1), abort, p.st, DAK_ERR_TIMEOUT, X_SM_V);
+                    uint8_t* v = ring + static_cast<size_t>(vit % NS) * C::kStage;
+                    for (int e = r; e < (64 * nk - valid) * (D / 8); e += 128) {
+                        const int row = valid + e / (D / 8), c = e % (D / 8);
+                        *reinterpret_cast<uint4*>(v + (c >> 3) * (8192 * nk) + row * 128 + ((c & 7) << 4)) =
+                            make_uint4(0, 0, 0, 0);
                     }
-#pragma unroll
-                    for (int k = 0; k < KEYS; ++k) {
-                        if (k >= valid) s[k] = -INFINITY;
-                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < KEYS; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
-                const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-                // the reference only moves when a row's maximum outgrows it by 2^8: until then the
-                // sums just grow, which fp32 holds
-                if (mine == 0) {
-                    m_ref = m_new;
-                } else if (__any_sync(0xffffffffu, m_new > m_ref + 8.f)) {
-                    const float m2 = fmaxf(m_ref, m_new);
-                    const float f = m2 == -INFINITY ? 1.f : exp2_ftz(m_ref - m2);
-                    m_ref = m2;
-                    l *= f;
-#pragma unroll
-                    for (int q = 0; q < D / 32; ++q) {
-                        float o[32];
-                        tmem_ld32(o_addr + q * 32, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= f;
-                        tmem_st32(o_addr + q * 32, o);
-                    }
-                }
-                const float base = m_ref == -INFINITY ? 0.f : m_ref;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int q = 0; q < KEYS / 32; ++q) {
-                    if (q < 2 * nk) {
-                        uint32_t hi[16], lo[16], th[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float a = exp2_ftz(fmaf(s[q * 32 + 2 * k], p.scale_log2, -base));
-                            const float b = exp2_ftz(fmaf(s[q * 32 + 2 * k + 1], p.scale_log2, -base));
-                            sum[(2 * k) & 3] += a;
-                            sum[(2 * k + 1) & 3] += b;
-                            hi[k] = pack_bf16(a, b);
-                            const float ra = a - bf_lo(hi[k]), rb = b - bf_hi(hi[k]);
-                            lo[k] = pack_bf16(ra, rb);
-                            if (KEYS == 64) th[k] = pack_bf16(ra - bf_lo(lo[k]), rb - bf_hi(lo[k]));
-                        }
-                        tmem_st16(s_addr + q * 16, hi);
-                        if (parts > 1) tmem_st16(s_addr + KEYS / 2 + q * 16, lo);
-                        if (KEYS == 64) tmem_st16(s_addr + KEYS + q * 16, th);
-                    }
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                softmax_step<D, KEYS>(s_addr, o_addr, nk, valid, p.scale_log2, m_ref, l, mine == 0);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -510,20 +688,29 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             if (valid_row) {
                 at = (static_cast<long long>(member[tile * mpt + m]) * p.Hq + x.g * p.G + r - m * p.G) * p.n_pre + x.s;
             }
+            // half a row's columns at a time go through this stream's Q tile, which is free now
+            constexpr int HALF = D / 2;
+            uint8_t* stage = smem + st * C::kTileBytes + (warp & 3) * 32 * HALF * 4;
+            const auto put = [&](const float(&o)[16], int q) {  // 16 columns from q * 16 of the half
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    *reinterpret_cast<float4*>(stage + lane * (HALF * 4) + (((q * 4 + k) ^ (lane & 7)) << 4)) =
+                        make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+            };
+            const auto flush = [&](int col) { store_rows<HALF>(stage, p.o_part + col, D, valid_row ? at : -1ll); };
             if (x.two) {
                 tc_fence_after();
-#pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    float o[32];
-                    tmem_ld32(o_addr + q * 32, o);
-                    tmem_wait_ld();
-                    if (valid_row) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            *reinterpret_cast<float4*>(p.o_part + at * D + q * 32 + k) =
-                                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                        }
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+                    for (int q = 0; q < HALF / 16; ++q) {
+                        float o[16];
+                        tmem_ld16(o_addr + h * HALF + q * 16, o);
+                        tmem_wait(o);
+                        put(o, q);
                     }
+                    flush(h * HALF);
                 }
                 if (valid_row) p.ml_part[at] = make_float2(m_ref, l);
             } else {
@@ -532,32 +719,29 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 prefix_bar<3, 256>();
                 tc_fence_after();
                 const float2 e0 = ex[0][r], e1 = ex[1][r];
+                prefix_bar<3, 256>();  // ex lies in what is written next
                 const float M = fmaxf(e0.x, e1.x), base = M == -INFINITY ? 0.f : M;
                 const float f0 = exp2_ftz(e0.x - base), f1 = exp2_ftz(e1.x - base);
                 const bool both = items > 1;  // the second stream had a step
+#pragma unroll 1
+                for (int q = 0; q < HALF / 16; ++q) {  // stream 0 the first half of the columns
+                    float a[16], b[16];
+                    tmem_ld16(tmem + lanes + 256 + st * HALF + q * 16, a);
+                    tmem_ld16(tmem + lanes + 256 + D + st * HALF + q * 16, b);
+                    tmem_wait(a);
+                    tmem_wait(b);
 #pragma unroll
-                for (int q = 0; q < D / 64; ++q) {
-                    const int col = st * (D / 2) + q * 32;
-                    float a[32], b[32];
-                    tmem_ld32(tmem + lanes + 256 + col, a);
-                    tmem_ld32(tmem + lanes + 256 + D + col, b);
-                    tmem_wait_ld();
-                    if (valid_row) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) a[k] = both ? a[k] * f0 + b[k] * f1 : a[k] * f0;
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            *reinterpret_cast<float4*>(p.o_part + at * D + col + k) =
-                                make_float4(a[k], a[k + 1], a[k + 2], a[k + 3]);
-                        }
-                    }
+                    for (int k = 0; k < 16; ++k) a[k] = both ? a[k] * f0 + b[k] * f1 : a[k] * f0;
+                    put(a, q);
                 }
+                flush(st * HALF);
                 if (valid_row && st == 0) p.ml_part[at] = make_float2(M, e0.y * f0 + (both ? e1.y * f1 : 0.f));
             }
         }
         it0 += 2 * steps;
         used[0] += (items + 1) / 2;
         used[1] += items / 2;
+        paired += x.two;
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
@@ -567,7 +751,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     __syncthreads();
     if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem_sh, 512);
     }
 }
 
@@ -613,6 +797,7 @@ dak_status launch_prefix(const void* Q, const dak_placement* P, const int* lens,
     p.Hq = H_q;
     p.Hkv = P->H_kv;
     p.G = H_q / P->H_kv;
+    p.mpt = 128 / p.G;
     p.L = P->L;
     p.n_prefix = P->B;
     p.n_pre = prefix_max_ranges(P);

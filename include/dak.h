@@ -500,7 +500,7 @@ dak_status dak_attn_acc(const void* Q, const dak_placement* KV, const int* seq_l
  *   tuning     : applies to the pass over the own caches; link is not taken.
  * The prefixes are read by tcgen05 tensor-core tiles of up to 256 query rows (requests x H_q /
  * H_kv); a prefix with more rows than that is streamed once per 256.
- * Requires H_q / H_kv <= 16, as dak_attn, and at most 2048 prefixes (DAK_ERR_UNSUPPORTED). */
+ * Requires H_q / H_kv <= 16, as dak_attn, and at most 1024 prefixes (DAK_ERR_UNSUPPORTED). */
 size_t dak_attn_prefix_workspace_bytes(const dak_placement* KV, const dak_placement* P, int H_q, int n_split,
                                        int with_acc);
 dak_status dak_attn_prefix(const void* Q, const dak_placement* KV, const int* seq_lens, const dak_placement* P,
