@@ -241,6 +241,8 @@ class Placement:
         self._h = handle
         self.kind = kind
         self.meta = meta
+        self.shape = (meta["B"], meta["H_kv"], meta["D"], meta["L"]) if kind == "kv" else None
+        self._cache = {}
         hb, gb, u, hu = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64()
         _check(lib.dak_placement_info(handle, ctypes.byref(hb), ctypes.byref(gb), ctypes.byref(u),
                                       ctypes.byref(hu)), "dak_placement_info")
@@ -252,6 +254,13 @@ class Placement:
         if self._h is None:
             raise ValueError("placement already freed")
         return self._h
+
+    def cached(self, key, make):
+        """make() once per key: sizes that depend on the placement and the key alone."""
+        v = self._cache.get(key)
+        if v is None:
+            v = self._cache[key] = make()
+        return v
 
     def slabs(self):
         """The parts of a placed KV cache as bf16 tensors that share its memory: (host, hbm), the
@@ -623,34 +632,42 @@ def dak_rope_from_freqs(head_dim: int, inv_freq, interleaved: bool = False, attn
     return out
 
 
-def _i32_cuda(t, name, shape):
-    """A contiguous int32 CUDA tensor of this shape (None stays None)."""
+# The calls below are made once per layer and token, so that their host time counts: tensors are
+# checked in one place each and handed over as plain addresses.
+
+def _t():
+    global _torch
     import torch
-    if t is None:
-        return None
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32 and t.is_contiguous()
-            and tuple(t.shape) == shape):
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)}")
-    return t
+    _torch = torch
+    return torch
 
 
-def _f32_cuda(t, name, shape):
-    import torch
+_torch = None
+
+
+def _raw_stream(stream):
+    """Address of the stream (None: the current one of the current device)."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _arg(t, name, dtype, shape):
+    """Address of a contiguous CUDA tensor of this type and shape (None: none)."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.float32 and t.is_contiguous()
-            and tuple(t.shape) == shape):
-        raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor {list(shape)}")
-    return t
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != _torch._C._cuda_getDevice() or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on the current CUDA device")
+    return t.data_ptr()
 
 
 def _token_rows(t, name, B, T, heads, D, dtype):
-    """Pitch in elements between the tokens of t [B][T][heads][D] (T = 1: also [B][heads][D]), whose
-    tokens lie at one pitch with each token's heads contiguous, as in a slice of a packed
-    projection."""
-    if not t.is_cuda or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
-    shape, st = tuple(t.shape), t.stride()
+    """Address of t [B][T][heads][D] (T = 1: also [B][heads][D]) and the pitch in elements between
+    its tokens, which lie at one pitch with each token's heads contiguous, as in a slice of a
+    packed projection."""
+    if t.dtype is not dtype or t.get_device() != _torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be a {dtype} tensor on the current CUDA device")
+    shape, st = t.shape, t.stride()
     if T == 1 and shape == (B, heads, D):
         row, head, el = st
         ok = True
@@ -661,7 +678,7 @@ def _token_rows(t, name, B, T, heads, D, dtype):
         raise ValueError(f"{name} must be [B={B}][T={T}][{heads}][{D}]")
     if not ok or el != 1 or (heads > 1 and head != D):
         raise ValueError(f"{name}: a token's heads must be contiguous and its tokens at one pitch")
-    return heads * D if B * T == 1 else row
+    return t.data_ptr(), heads * D if B * T == 1 else row
 
 
 def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slots, positions=None, n_new=None,
@@ -671,32 +688,30 @@ def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slot
     they are (T = 1: the T axis may be absent); slots, positions, n_new int32 CUDA [B];
     slot_pos int32 CUDA [B][H_kv][L], updated in place. Returns q_out, bf16, shaped as q (None
     without q)."""
-    import torch
-    B, Hkv, D, L = KV.meta["B"], KV.meta["H_kv"], KV.meta["D"], KV.meta["L"]
-    T = int(k_new.shape[1]) if k_new.ndim == 4 else 1
+    torch = _torch or _t()
+    B, Hkv, D, L = KV.shape
+    T = k_new.shape[1] if k_new.ndim == 4 else 1
     dtype = k_new.dtype
-    if dtype not in (torch.bfloat16, torch.float32):
+    fp32 = dtype is torch.float32
+    if not fp32 and dtype is not torch.bfloat16:
         raise ValueError("k_new must be bf16 or fp32")
-    kp = _token_rows(k_new, "k_new", B, T, Hkv, D, dtype)
-    vp = _token_rows(v_new, "v_new", B, T, Hkv, D, dtype)
+    ka, kp = _token_rows(k_new, "k_new", B, T, Hkv, D, dtype)
+    va, vp = _token_rows(v_new, "v_new", B, T, Hkv, D, dtype)
     Hq = qp = 0
+    qa = oa = None
     if q is not None:
-        Hq = int(q.shape[-2])
-        qp = _token_rows(q, "q", B, T, Hq, D, dtype)
+        Hq = q.shape[-2]
+        qa, qp = _token_rows(q, "q", B, T, Hq, D, dtype)
         if q_out is None:
-            q_out = torch.empty(tuple(q.shape), dtype=torch.bfloat16, device=q.device)
-        _check_bf16_cuda(q_out, "q_out")
-        if tuple(q_out.shape) != tuple(q.shape):
-            raise ValueError("q_out must be shaped as q")
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        oa = _arg(q_out, "q_out", torch.bfloat16, q.shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _i32_cuda(slots, "slots", (B,))
-    _i32_cuda(positions, "positions", (B,))
-    _i32_cuda(n_new, "n_new", (B,))
-    _i32_cuda(slot_pos, "slot_pos", (B, Hkv, L))
-    _check(lib.dak_kv_append_rope(KV.handle, ctypes.byref(rope), _ptr(q), _ptr(k_new), _ptr(v_new),
-                                  int(dtype == torch.float32), T, Hq, qp, kp, vp, _ptr(slots), _ptr(positions),
-                                  _ptr(n_new), _ptr(q_out), _ptr(slot_pos), _stream_ptr(stream)), "dak_kv_append_rope")
+    i32, per_request = torch.int32, (B,)
+    _check(lib.dak_kv_append_rope(KV.handle, rope, qa, ka, va, fp32, T, Hq, qp, kp, vp,
+                                  _arg(slots, "slots", i32, per_request), _arg(positions, "positions", i32, per_request),
+                                  _arg(n_new, "n_new", i32, per_request), oa,
+                                  _arg(slot_pos, "slot_pos", i32, (B, Hkv, L)), _raw_stream(stream)), "dak_kv_append_rope")
     return q_out
 
 
@@ -711,28 +726,25 @@ def dak_kv_evict(KV: Placement, seq_lens, n_keep: int, n_recent: int, acc, slot_
     slot_pos int32 CUDA [B][H_kv][L], updated in place unless acc_out / slot_pos_out are
     given; seq_lens int32 CUDA [B]. Returns (lens_out [B], src_out [B][H_kv][n_keep]), int32:
     the new lengths, and the slot each kept row came from (-1 past the length)."""
-    import torch
-    B, Hkv, L = KV.meta["B"], KV.meta["H_kv"], KV.meta["L"]
-    acc_out = acc if acc_out is None else acc_out
-    slot_pos_out = slot_pos if slot_pos_out is None else slot_pos_out
-    _i32_cuda(seq_lens, "seq_lens", (B,))
-    _f32_cuda(acc, "acc", (B, Hkv, L))
-    _f32_cuda(acc_out, "acc_out", (B, Hkv, L))
-    _i32_cuda(slot_pos, "slot_pos", (B, Hkv, L))
-    _i32_cuda(slot_pos_out, "slot_pos_out", (B, Hkv, L))
-    if not 1 <= int(n_keep) <= L:
+    torch = _torch or _t()
+    B, Hkv, _, L = KV.shape
+    n_keep = int(n_keep)
+    if not 1 <= n_keep <= L:
         raise DakError(1, f"dak_kv_evict: n_keep {n_keep} outside 1..{L}")
+    table, per_request, kept = (B, Hkv, L), (B,), (B, Hkv, n_keep)
+    i32, f32, dev = torch.int32, torch.float32, acc.device
     if lens_out is None:
-        lens_out = torch.empty(B, dtype=torch.int32, device=acc.device)
+        lens_out = torch.empty(B, dtype=i32, device=dev)
     if src_out is None:
-        src_out = torch.empty((B, Hkv, int(n_keep)), dtype=torch.int32, device=acc.device)
-    _i32_cuda(lens_out, "lens_out", (B,))
-    _i32_cuda(src_out, "src_out", (B, Hkv, int(n_keep)))
+        src_out = torch.empty(kept, dtype=i32, device=dev)
     if workspace is None:
-        workspace = torch.empty(dak_kv_evict_workspace_bytes(KV), dtype=torch.uint8, device=acc.device)
-    _check(lib.dak_kv_evict(KV.handle, _ptr(seq_lens), int(n_keep), int(n_recent), _ptr(acc), _ptr(acc_out),
-                            _ptr(slot_pos), _ptr(slot_pos_out), _ptr(lens_out), _ptr(src_out), _ptr(workspace),
-                            workspace.numel() * workspace.element_size(), _stream_ptr(stream)), "dak_kv_evict")
+        workspace = torch.empty(KV.cached("evict", lambda: dak_kv_evict_workspace_bytes(KV)), dtype=torch.uint8, device=dev)
+    aa, pa = _arg(acc, "acc", f32, table), _arg(slot_pos, "slot_pos", i32, table)
+    _check(lib.dak_kv_evict(KV.handle, _arg(seq_lens, "seq_lens", i32, per_request), n_keep, int(n_recent), aa,
+                            aa if acc_out is None else _arg(acc_out, "acc_out", f32, table), pa,
+                            pa if slot_pos_out is None else _arg(slot_pos_out, "slot_pos_out", i32, table),
+                            _arg(lens_out, "lens_out", i32, per_request), _arg(src_out, "src_out", i32, kept),
+                            workspace.data_ptr(), workspace.nbytes, _raw_stream(stream)), "dak_kv_evict")
     return lens_out, src_out
 
 
@@ -745,20 +757,19 @@ def _n_split_of(tuning) -> int:
 
 
 def _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out):
-    import torch
-    _check_bf16_cuda(Q, "Q")
-    B, Hkv, D, L = KV.meta["B"], KV.meta["H_kv"], KV.meta["D"], KV.meta["L"]
-    if Q.ndim != 3 or int(Q.shape[0]) != B or int(Q.shape[2]) != D:
+    """Addresses of Q, O, seq_lens, acc_in, acc_out, with O made where there is none."""
+    torch = _torch or _t()
+    B, Hkv, D, L = KV.shape
+    shape = Q.shape
+    if len(shape) != 3 or shape[0] != B or shape[2] != D:
         raise ValueError("Q must be [B][H_q][D] of the KV placement's B and D")
     dtype = torch.float32 if o_fp32 else torch.bfloat16
     if O is None:
-        O = torch.empty(tuple(Q.shape), dtype=dtype, device=Q.device)
-    elif not (O.is_cuda and O.dtype == dtype and O.is_contiguous() and tuple(O.shape) == tuple(Q.shape)):
-        raise ValueError(f"O must be a contiguous {dtype} CUDA tensor shaped like Q")
-    _i32_cuda(seq_lens, "seq_lens", (B,))
-    _f32_cuda(acc_in, "acc_in", (B, Hkv, L))
-    _f32_cuda(acc_out, "acc_out", (B, Hkv, L))
-    return int(Q.shape[1]), O
+        O = torch.empty(shape, dtype=dtype, device=Q.device)
+    table = (B, Hkv, L)
+    return (O, _arg(Q, "Q", torch.bfloat16, shape), _arg(O, "O", dtype, shape),
+            _arg(seq_lens, "seq_lens", torch.int32, (B,)), _arg(acc_in, "acc_in", torch.float32, table),
+            _arg(acc_out, "acc_out", torch.float32, table))
 
 
 def dak_attn_acc_workspace_bytes(KV: Placement, H_q: int, n_split: int = 0) -> int:
@@ -770,17 +781,18 @@ def dak_attn_acc(Q, KV: Placement, acc_in=None, acc_out=None, seq_lens=None, sca
     """dak_attn that adds every position's attention weight, summed over the query heads of its
     kv head, to acc_in fp32 [B][H_kv][L] (None = zeros). Returns (O, acc_out); acc_out may be
     acc_in; without one, a new tensor that is zero behind each request's tokens."""
-    import torch
+    torch = _torch or _t()
     if acc_out is None:
-        acc_out = torch.zeros((KV.meta["B"], KV.meta["H_kv"], KV.meta["L"]), dtype=torch.float32, device=Q.device)
-    Hq, O = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out)
+        B, Hkv, _, L = KV.shape
+        acc_out = torch.zeros((B, Hkv, L), dtype=torch.float32, device=Q.device)
+    O, qa, oa, la, ia, aa = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out)
+    Hq = Q.shape[1]
     if workspace is None:
-        workspace = torch.empty(dak_attn_acc_workspace_bytes(KV, Hq, _n_split_of(tuning)), dtype=torch.uint8,
-                                device=Q.device)
-    _check(lib.dak_attn_acc(_ptr(Q), KV.handle, _ptr(seq_lens), Hq, float(scale), _ptr(O), int(bool(o_fp32)),
-                            _ptr(acc_in), _ptr(acc_out), _ptr(workspace),
-                            workspace.numel() * workspace.element_size(), _tuning(tuning), _stream_ptr(stream)),
-           "dak_attn_acc")
+        n = _n_split_of(tuning) if tuning else 0
+        workspace = torch.empty(KV.cached(("acc", Hq, n), lambda: dak_attn_acc_workspace_bytes(KV, Hq, n)),
+                                dtype=torch.uint8, device=Q.device)
+    _check(lib.dak_attn_acc(qa, KV.handle, la, Hq, scale, oa, bool(o_fp32), ia, aa, workspace.data_ptr(), workspace.nbytes,
+                            _tuning(tuning), _raw_stream(stream)), "dak_attn_acc")
     return O, acc_out
 
 
@@ -797,18 +809,20 @@ def dak_attn_prefix(Q, KV: Placement, prefix: Placement, prefix_of=None, prefix_
     prefix 0 for all) and over its own seq_lens[b] cached tokens. Each prefix is read once for
     all its requests. acc_out, if given, takes acc_in (None = zeros) plus the weights of the own
     cache's positions, as in dak_attn_acc. Returns O."""
-    import torch
-    Hq, O = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out)
+    torch = _torch or _t()
     if acc_in is not None and acc_out is None:
         raise ValueError("acc_in without acc_out")
-    _i32_cuda(prefix_of, "prefix_of", (KV.meta["B"],))
-    _i32_cuda(prefix_lens, "prefix_lens", (prefix.meta["B"],))
+    O, qa, oa, la, ia, aa = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out)
+    Hq = Q.shape[1]
     if workspace is None:
-        workspace = torch.empty(dak_attn_prefix_workspace_bytes(KV, prefix, Hq, _n_split_of(tuning), acc_out is not None),
-                                dtype=torch.uint8, device=Q.device)
-    _check(lib.dak_attn_prefix(_ptr(Q), KV.handle, _ptr(seq_lens), prefix.handle, _ptr(prefix_lens), _ptr(prefix_of), Hq,
-                               float(scale), _ptr(O), int(bool(o_fp32)), _ptr(acc_in), _ptr(acc_out), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), _tuning(tuning), _stream_ptr(stream)),
+        n = _n_split_of(tuning) if tuning else 0
+        size = KV.cached(("prefix", prefix.shape, Hq, n, aa is None),
+                         lambda: dak_attn_prefix_workspace_bytes(KV, prefix, Hq, n, aa is not None))
+        workspace = torch.empty(size, dtype=torch.uint8, device=Q.device)
+    _check(lib.dak_attn_prefix(qa, KV.handle, la, prefix.handle,
+                               _arg(prefix_lens, "prefix_lens", torch.int32, (prefix.shape[0],)),
+                               _arg(prefix_of, "prefix_of", torch.int32, (KV.shape[0],)), Hq, scale, oa, bool(o_fp32), ia, aa,
+                               workspace.data_ptr(), workspace.nbytes, _tuning(tuning), _raw_stream(stream)),
            "dak_attn_prefix")
     return O
 

@@ -28,6 +28,7 @@
 // brings a whole stage; inside every token row the 16-byte piece c sits at c ^ (token & 7)
 // so that ldmatrix reads of 8 consecutive tokens hit 8 different bank groups.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "dak_device.cuh"
@@ -55,6 +56,8 @@ struct AttnParams {
     // scaled score (log2 domain) [B][Hq][score_pitch]
     float* scores;
     int score_pitch;
+    int deal;       // units dealt round the CTAs of a tier, empty ones skipped
+    int wait_late;  // the previous kernel is the call's prefix pass: only this grid's end waits for it
 };
 
 constexpr int kChunkTok = 64;
@@ -64,12 +67,24 @@ constexpr int kAttnThreads = 32 * (1 + kAttnConsumers);
 struct UnitRange {
     int tier;
     long long begin, end;  // global unit indices
+    int step;
     int window;
 };
 
 __device__ __forceinline__ UnitRange units_of_cta(const AttnParams& p) {
     UnitRange u;
     const int b = blockIdx.x;
+    u.step = 1;
+    if (p.deal) {
+        // EXT: the splits of a slab go to different CTAs, so that ragged lengths even out
+        const bool host = b < p.n_host_ctas;
+        u.tier = host ? 0 : 1;
+        u.step = host ? p.n_host_ctas : p.n_hbm_ctas;
+        u.begin = host ? b : p.host_units + b - p.n_host_ctas;
+        u.end = p.host_units + (host ? 0 : p.hbm_units);
+        u.window = host ? p.host_window : p.hbm_window;
+        return u;
+    }
     if (b < p.n_host_ctas) {
         u.tier = 0;
         u.begin = p.host_units * b / p.n_host_ctas;
@@ -175,7 +190,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
             if (link) link_wait(p.link, p.link_after, p.st);
             long long i = 0;
             bool waited = false;
-            for (long long u = ur.begin; u < ur.end && !*abort; ++u) {
+            for (long long u = ur.begin; u < ur.end && !*abort; u += EXT ? ur.step : 1) {
                 const Unit x = decode_unit(p, u, ur.tier);
                 for (int t = x.t0; t < x.t1; t += kChunkTok, ++i) {
                     const int s = static_cast<int>(i % W);
@@ -206,15 +221,16 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     // ---------------------------------------------------------------- consumers
     // Q (and the outputs) may belong to the previous kernel of the stream; the KV cache
     // streamed above is, with programmatic launch, taken to be written earlier than that
-    grid_dep_wait();
+    if (!EXT || !p.wait_late) grid_dep_wait();
     const int w = warp - 1;
     const int q4 = lane & 3;      // column pair within an 8-wide block
     const int ra = lane >> 2;     // MMA row of c0/c1 (c2/c3: ra + 8)
     const int mi = lane >> 3, rr = lane & 7;  // ldmatrix: matrix index, row within it
     long long i = 0;
     bool failed = false;  // a wait ran out: skip the math but keep meeting the named barriers
-    for (long long u = ur.begin; u < ur.end; ++u) {
+    for (long long u = ur.begin; u < ur.end; u += EXT ? ur.step : 1) {
         const Unit x = decode_unit(p, u, ur.tier);
+        if (EXT && x.t0 >= x.t1) continue;
         // Q fragments (A operand), rows >= G are zero
         uint32_t qa[KS][4];
         {
@@ -429,6 +445,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         }
         named_bar_consumers();  // comb is rewritten by the next unit
     }
+    // this grid's end stands for the prefix pass's too
+    if (EXT && p.wait_late) grid_dep_wait();
 }
 
 // Merge the context splits of every (request, query head) row in split order:
@@ -535,15 +553,15 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_cta_kernel(const
 // Merge of dak_attn_acc and dak_attn_prefix: the partials of the own cache's n_own splits and of
 // the prefix's ranges, in that order, into O as attn_combine does, and the accumulated weights
 // acc_out = acc_in + sum_r 2^(s_r - M_r) / l_r from the scores s that the own pass left. Block
-// (b, g) x y: y < G merges query head g * G + y, later ones take kMergePositions positions of
-// the slab each.
+// (b, g) x y: the first ones merge a query head a warp, later ones take kMergePositions positions
+// of the slab each. Splits behind a request's tokens have no partials.
 struct MergeParams {
     const float* own;  // [B][Hq][n_own][D + 2]
-    int n_own;
+    int n_own, split_len;
     // prefix pass (launch_prefix); n_pre 0: none
     const float* pre_o;
     const float2* pre_ml;
-    const int* n_ranges;
+    const int* n_ranges;  // [B]
     const int* prefix_of;
     const int* prefix_lens;
     int n_pre, n_prefix, prefix_L;
@@ -557,63 +575,106 @@ struct MergeParams {
     int Hq, Hkv, G, L;
 };
 constexpr int kMergeThreads = 128;
+constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMergePositions = 512;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const MergeParams p) {
+    constexpr int V = D / 32;  // columns of a lane
+    grid_dep_wait();
     const int b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv;
-    const long long row0 = static_cast<long long>(b) * p.Hq + static_cast<long long>(g) * p.G;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int L = p.seq_lens ? min(max(p.seq_lens[b], 0), p.L) : p.L;
+    const int o_blocks = (p.G + kMergeWarps - 1) / kMergeWarps;
+    const int j0 = (static_cast<int>(blockIdx.y) - o_blocks) * kMergePositions;
+    if (j0 >= L) return;
     int n_pre = 0;
     if (p.n_pre > 0) {
         const int f = p.prefix_of ? p.prefix_of[b] : 0;
-        if (f >= 0 && f < p.n_prefix && (p.prefix_lens ? p.prefix_lens[f] : p.prefix_L) > 0) n_pre = p.n_ranges[f];
+        if (f >= 0 && f < p.n_prefix && (p.prefix_lens ? p.prefix_lens[f] : p.prefix_L) > 0) n_pre = p.n_ranges[b];
     }
-    const int n = p.n_own + n_pre;
+    const int n_own = (L + p.split_len - 1) / p.split_len, n = n_own + n_pre;
+    const long long row0 = static_cast<long long>(b) * p.Hq + static_cast<long long>(g) * p.G;
     const auto ml = [&](long long row, int s) {
-        if (s >= p.n_own) return p.pre_ml[row * p.n_pre + s - p.n_own];
-        const float* q = p.own + (row * p.n_own + s) * (D + 2) + D;
-        return make_float2(q[0], q[1]);
+        if (s >= n_own) return p.pre_ml[row * p.n_pre + s - n_own];
+        return *reinterpret_cast<const float2*>(p.own + (row * p.n_own + s) * (D + 2) + D);
     };
-    const auto o_of = [&](long long row, int s) {
-        return s < p.n_own ? p.own + (row * p.n_own + s) * (D + 2) : p.pre_o + (row * p.n_pre + s - p.n_own) * D;
-    };
-    const int tid = threadIdx.x;
-    if (static_cast<int>(blockIdx.y) < p.G) {
-        const long long row = row0 + blockIdx.y;
-        float M = -INFINITY;
-        for (int s = 0; s < n; ++s) M = fmaxf(M, ml(row, s).x);
+    // maximum and denominator of a row, on every lane of its warp
+    const auto total = [&](long long row) {
+        float M = -INFINITY, l = 0.f;
+        for (int s = lane; s < n; s += 32) M = fmaxf(M, ml(row, s).x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         const float base = M == -INFINITY ? 0.f : M;
-        if (tid < D) {
-            float acc = 0.f, lsum = 0.f;
-            for (int s = 0; s < n; ++s) {
-                const float2 v = ml(row, s);
-                const float f = exp2f(v.x - base);
-                lsum += f * v.y;
-                acc += f * o_of(row, s)[tid];
+        for (int s = lane; s < n; s += 32) {
+            const float2 v = ml(row, s);
+            l += exp2f(v.x - base) * v.y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        return make_float2(base, l);
+    };
+    if (static_cast<int>(blockIdx.y) < o_blocks) {  // a warp per query head
+        const int r = static_cast<int>(blockIdx.y) * kMergeWarps + warp;
+        if (r >= p.G) return;
+        const long long row = row0 + r;
+        const float2 t = total(row);
+        float acc[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        for (int s0 = 0; s0 < n; s0 += 32) {
+            const float f = s0 + lane < n ? exp2f(ml(row, s0 + lane).x - t.x) : 0.f;
+            const int m = min(32, n - s0);
+#pragma unroll 8
+            for (int k = 0; k < m; ++k) {
+                const int s = s0 + k;
+                const float w = __shfl_sync(0xffffffffu, f, k);
+                const float* o = s < n_own ? p.own + (row * p.n_own + s) * (D + 2)
+                                           : p.pre_o + (row * p.n_pre + s - n_own) * D;
+#pragma unroll
+                for (int c = 0; c < V; c += 2) {  // the own partials' rows are 8-byte aligned
+                    const float2 v = *reinterpret_cast<const float2*>(o + (c >> 1) * 64 + lane * 2);
+                    acc[c] += w * v.x;
+                    acc[c + 1] += w * v.y;
+                }
             }
-            store_out(p.O, p.o_fp32, row * D + tid, lsum > 0.f ? acc / lsum : 0.f);
+        }
+        const float inv = t.y > 0.f ? 1.f / t.y : 0.f;
+#pragma unroll
+        for (int c = 0; c < V; c += 2) {
+            const long long at = row * D + (c >> 1) * 64 + lane * 2;
+            store_out(p.O, p.o_fp32, at, acc[c] * inv);
+            store_out(p.O, p.o_fp32, at + 1, acc[c + 1] * inv);
         }
         return;
     }
-    const int L = p.seq_lens ? min(max(p.seq_lens[b], 0), p.L) : p.L;
-    const int j0 = (blockIdx.y - p.G) * kMergePositions;
-    if (j0 >= L) return;
-    __shared__ float Ms[16], rl[16];
-    if (tid < p.G) {
-        const long long row = row0 + tid;
-        float M = -INFINITY, l = 0.f;
-        for (int s = 0; s < n; ++s) M = fmaxf(M, ml(row, s).x);
-        const float base = M == -INFINITY ? 0.f : M;
-        for (int s = 0; s < n; ++s) l += exp2f(ml(row, s).x - base) * ml(row, s).y;
-        Ms[tid] = base;
-        rl[tid] = l > 0.f ? 1.f / l : 0.f;
+    __shared__ float2 rows[16];  // maximum, 1 / denominator
+    for (int r = warp; r < p.G; r += kMergeWarps) {
+        const float2 t = total(row0 + r);
+        if (lane == 0) rows[r] = make_float2(t.x, t.y > 0.f ? 1.f / t.y : 0.f);
     }
     __syncthreads();
     const long long slab = static_cast<long long>(blockIdx.x) * p.L;
-    for (int j = j0 + tid; j < min(j0 + kMergePositions, L); j += kMergeThreads) {
-        float w = 0.f;
-        for (int r = 0; r < p.G; ++r) w += exp2f(p.scores[(row0 + r) * p.score_pitch + j] - Ms[r]) * rl[r];
-        p.acc_out[slab + j] = (p.acc_in ? p.acc_in[slab + j] : 0.f) + w;
+    const float* sc = p.scores + row0 * p.score_pitch;
+    float w[kMergePositions / kMergeThreads];
+#pragma unroll
+    for (int k = 0; k < kMergePositions / kMergeThreads; ++k) {
+        const int j = j0 + tid + k * kMergeThreads;
+        w[k] = p.acc_in && j < L ? p.acc_in[slab + j] : 0.f;
+    }
+    float add[kMergePositions / kMergeThreads] = {};
+    for (int r = 0; r < p.G; ++r) {
+        const float2 t = rows[r];
+#pragma unroll
+        for (int k = 0; k < kMergePositions / kMergeThreads; ++k) {
+            const int j = j0 + tid + k * kMergeThreads;
+            if (j < L) add[k] += exp2f(sc[static_cast<long long>(r) * p.score_pitch + j] - t.x) * t.y;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kMergePositions / kMergeThreads; ++k) {
+        const int j = j0 + tid + k * kMergeThreads;
+        if (j < L) p.acc_out[slab + j] = w[k] + add[k];
     }
 }
 
@@ -649,14 +710,18 @@ static int attn_smem_bytes(int W, int G) {
 // copies, so two per SM double the copy streams an SM keeps in flight).
 template <int D>
 static int attn_ctas_per_sm(int W, int G) {
-    int n = 0;
+    static std::atomic<int> known[kAttnMaxStages + 1][17];  // 0 = not asked yet
+    int n = known[W][G].load(std::memory_order_relaxed);
+    if (n) return n;
     const int smem = attn_smem_bytes<D>(W, G);
     if (cudaFuncSetAttribute(attn_kernel<D, 1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<D, 1, false>, kAttnThreads, smem) != cudaSuccess) {
         cudaGetLastError();
         return 1;
     }
-    return std::max(1, n);
+    n = std::max(1, n);
+    known[W][G].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 // Launch with or without programmatic dependent launch (the kernel may start while the
@@ -681,8 +746,10 @@ static cudaError_t launch_maybe_pdl(Kernel k, int grid, int threads, int smem, b
 template <int D>
 static cudaError_t launch_attn_ext_d(const AttnParams& p, int grid, int W, bool pdl, cudaStream_t s) {
     const int smem = attn_smem_bytes<D>(W, p.G);
+    static SmemLimit limit[2];
     auto k = p.o_fp32 ? attn_kernel<D, 3, true> : attn_kernel<D, 2, true>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e =
+        limit[p.o_fp32 ? 1 : 0].raise(reinterpret_cast<const void*>(k), attn_smem_bytes<D>(kAttnMaxStages, 16));
     return e == cudaSuccess ? launch_maybe_pdl(k, grid, kAttnThreads, smem, pdl, s, p) : e;
 }
 
@@ -703,11 +770,16 @@ static cudaError_t launch_attn_d(const AttnParams& p, int grid, int W, bool pdl,
                             static_cast<const float*>(p.ws), p.O, p.o_fp32, p.n_split);
 }
 
+static int split_tokens(int L, int n_split) {
+    return ((L + n_split - 1) / n_split + kChunkTok - 1) / kChunkTok * kChunkTok;
+}
+
 // ext: the own-cache pass of dak_attn_acc / dak_attn_prefix (partials into ws, scores), with a
 // workspace that the caller has checked.
 struct AttnExt {
     float* scores = nullptr;
     int score_pitch = 0;
+    bool after_prefix = false;
 };
 
 static dak_status launch_attn_kernels(const void* Q, const dak_placement* KV, const void* host_src,
@@ -745,7 +817,7 @@ static dak_status launch_attn_kernels(const void* Q, const dak_placement* KV, co
     p.L = KV->L;
     p.h_s = KV->h_s;
     p.n_split = n_split;
-    p.split_len = ((KV->L + n_split - 1) / n_split + kChunkTok - 1) / kChunkTok * kChunkTok;
+    p.split_len = split_tokens(KV->L, n_split);
     const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(KV->D));
     p.scale_log2 = sc * 1.4426950408889634f;
     p.head_bytes = KV->head_bytes;
@@ -783,6 +855,9 @@ static dak_status launch_attn_kernels(const void* Q, const dak_placement* KV, co
     if (ext) {
         p.scores = ext->scores;
         p.score_pitch = ext->score_pitch;
+        p.deal = 1;
+        p.wait_late = ext->after_prefix;
+        const bool pdl = (t && t->pdl > 0) || ext->after_prefix;
         e = KV->D == 128 ? launch_attn_ext_d<128>(p, grid, W, pdl, stream)
                          : launch_attn_ext_d<64>(p, grid, W, pdl, stream);
     } else {
@@ -818,17 +893,25 @@ struct ExtLayout {
     size_t total() const { return own_bytes + pre_o_bytes + pre_ml_bytes + ranges_bytes + score_bytes; }
 };
 
+// Splits of a cache for the passes that deal units round the CTAs: at most 256 tokens each, so that
+// requests of different lengths fill the SMs alike (the partials are 2% of the cache's bytes), and
+// more where default_split fills the SMs better.
+constexpr int kExtSplitTokens = 256;
+static int ext_default_split(int B, int Hkv, int L) {
+    return std::min(kMaxSplits, std::max(default_split(B, Hkv, L), (L + kExtSplitTokens - 1) / kExtSplitTokens));
+}
+
 static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 static ExtLayout ext_layout(const dak_placement* KV, const dak_placement* P, int H_q, int n_split, bool with_acc) {
     ExtLayout x{};
     const size_t rows = static_cast<size_t>(KV->B) * H_q;
-    x.n_own = n_split > 0 ? n_split : default_split(KV->B, KV->H_kv, KV->L);
+    x.n_own = n_split > 0 ? n_split : ext_default_split(KV->B, KV->H_kv, KV->L);
     x.n_pre = P ? prefix_max_ranges(P) : 0;
     x.own_bytes = round256(rows * x.n_own * (KV->D + 2) * sizeof(float));
     x.pre_o_bytes = round256(rows * x.n_pre * KV->D * sizeof(float));
     x.pre_ml_bytes = round256(rows * x.n_pre * sizeof(float2));
-    x.ranges_bytes = P ? round256(static_cast<size_t>(P->B) * sizeof(int)) : 0;
+    x.ranges_bytes = P ? round256(static_cast<size_t>(KV->B) * sizeof(int)) : 0;
     x.score_pitch = (KV->L + kChunkTok - 1) / kChunkTok * kChunkTok;
     x.score_bytes = with_acc ? round256(rows * x.score_pitch * sizeof(float)) : 0;
     return x;
@@ -893,6 +976,7 @@ static dak_status launch_attn_ext(const void* Q, const dak_placement* KV, const 
     }
     dak_tuning tun = t ? *t : dak_tuning{};
     tun.n_split = x.n_own;
+    ext.after_prefix = P != nullptr;
     const dak_status r = launch_attn_kernels(Q, KV, KV->host_dev, seq_lens, H_q, scale, O, own, x.own_bytes, &tun, stream,
                                              o_fp32, link, &ext);
     if (r != DAK_OK) return r;
@@ -909,14 +993,20 @@ static dak_status launch_attn_ext(const void* Q, const dak_placement* KV, const 
     m.Hkv = KV->H_kv;
     m.G = H_q / KV->H_kv;
     m.L = KV->L;
-    const dim3 grid(static_cast<unsigned>(KV->B) * KV->H_kv,
-                    static_cast<unsigned>(m.G + (acc_out ? (KV->L + kMergePositions - 1) / kMergePositions : 0)));
-    if (KV->D == 128) {
-        attn_merge_kernel<128><<<grid, kMergeThreads, 0, stream>>>(m);
-    } else {
-        attn_merge_kernel<64><<<grid, kMergeThreads, 0, stream>>>(m);
-    }
-    return cuda_status(cudaGetLastError());
+    m.split_len = split_tokens(KV->L, x.n_own);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(KV->B) * KV->H_kv,
+                       static_cast<unsigned>((m.G + kMergeWarps - 1) / kMergeWarps +
+                                             (acc_out ? (KV->L + kMergePositions - 1) / kMergePositions : 0)));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(KV->D == 128 ? cudaLaunchKernelEx(&cfg, attn_merge_kernel<128>, m)
+                                    : cudaLaunchKernelEx(&cfg, attn_merge_kernel<64>, m));
 }
 
 }  // namespace dak

@@ -2,6 +2,7 @@
 // and appended (dak_kv_append_rope), and the least attended tokens evicted (dak_kv_evict).
 // The cache layout is the one of dak_attn.cu: a (request, kv head) slab is ceil(L/64) chunks
 // [K 64 x D][V 64 x D] bf16, the 16-byte piece c of token t's row stored at c ^ (t & 7).
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -178,9 +179,10 @@ __device__ __forceinline__ uint32_t evict_key(float w, bool newest) {
     return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-// One block per slab: the n_keep-th largest key by a radix select over bytes, then one pass over
-// the slots in order that gives every slot its fate and every hole and mover its rank.
-__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const EvictParams p) {
+// Caches longer than a cluster's registers hold (kEvictMaxSlots): one block per slab that reads the
+// tables again for every pass. The n_keep-th largest key by a radix select over bytes, then one
+// pass over the slots in order that gives every slot its fate and every hole and mover its rank.
+__global__ void __launch_bounds__(kEvictThreads) evict_select_long_kernel(const EvictParams p) {
     constexpr int NW = kEvictThreads / 32;
     __shared__ int hist[256];
     __shared__ int red[NW];
@@ -290,27 +292,328 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
     }
 }
 
-// One warp per moved row: K and V from slot `from` to slot `to`.
+// The moved rows of a slab, K and V, from slots movers[r] to holes[r], by `threads` threads of which
+// this is `self`. Every thread has four 16-byte pieces in flight; a row's pieces lie on
+// neighbouring threads.
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
-    constexpr int PIECES = D / 8;
-    const long long slab = blockIdx.x;
-    const int cnt = p.n_moves[slab];
-    const int* holes = p.moves + slab * 2 * p.list;
-    const int* movers = holes + p.list;
+__device__ __forceinline__ void move_rows(const EvictParams& p, long long slab, const int* holes, const int* movers, int cnt,
+                                          int self, int threads) {
+    constexpr int PIECES = D / 8, PER_ROW = 2 * PIECES;
     uint4* base =
         reinterpret_cast<uint4*>(slab < p.h_s ? p.host + slab * p.head_bytes : p.hbm + (slab - p.h_s) * p.head_bytes);
-    constexpr int PER_ROW = 2 * PIECES;  // 16-byte pieces of a K row and a V row
-    const long long total = static_cast<long long>(cnt) * PER_ROW;
-    for (long long e = blockIdx.y * static_cast<long long>(kMoveThreads) + threadIdx.x; e < total;
-         e += static_cast<long long>(gridDim.y) * kMoveThreads) {
-        const int r = static_cast<int>(e / PER_ROW), q = static_cast<int>(e % PER_ROW);
-        const int c = q % PIECES, v = q / PIECES;
-        const int from = movers[r], to = holes[r];
-        base[static_cast<long long>(to >> 6) * (128 * PIECES) + v * 64 * PIECES + (to & 63) * PIECES + (c ^ (to & 7))] =
-            base[static_cast<long long>(from >> 6) * (128 * PIECES) + v * 64 * PIECES + (from & 63) * PIECES +
-                 (c ^ (from & 7))];
+    const auto piece_of = [](int row, int v, int c) {
+        return static_cast<long long>(row >> 6) * (128 * PIECES) + v * 64 * PIECES + (row & 63) * PIECES + (c ^ (row & 7));
+    };
+    const int q = self % PER_ROW, c = q % PIECES, v = q / PIECES;  // the same piece of every row it takes
+    const int step = threads / PER_ROW;
+    for (int r0 = self / PER_ROW; r0 < cnt; r0 += 4 * step) {
+        uint4 x[4];
+        int to[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = r0 + k * step;
+            to[k] = -1;
+            if (r < cnt) {
+                to[k] = holes[r];
+                x[k] = base[piece_of(movers[r], v, c)];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (to[k] >= 0) base[piece_of(to[k], v, c)] = x[k];
+        }
     }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+    grid_dep_wait();
+    const long long slab = blockIdx.x;
+    const int* holes = p.moves + slab * 2 * p.list;
+    move_rows<D>(p, slab, holes, holes + p.list, p.n_moves[slab], blockIdx.y * kMoveThreads + threadIdx.x,
+                 gridDim.y * kMoveThreads);
+}
+
+// The eviction of one slab by a cluster of 1 to 8 CTAs, the slots' weights and positions in
+// registers: CTA c holds slots [c, c + 1) * 1024 R, thread t the slots r * 1024 + t of them. Reading
+// the tables costs one pass; everything after is counting:
+//   newest position -> key of every slot (evict_key) -> the n_keep-th largest key by a radix select
+//   (11, 11 and 10 bits, histograms in shared memory added up over the cluster) -> kept slots (at
+//   the threshold key the lowest ones) -> ranks of holes and movers -> lists, tables, and with MOVE
+//   the rows themselves.
+// Ranks in slot order: ballots per (r, warp), whose counts are scanned in that order, offset by the
+// cluster's earlier CTAs.
+constexpr int kClusterThreads = 1024;
+constexpr int kEvictMaxCluster = 8;
+constexpr int kEvictMaxSlots = kEvictMaxCluster * kClusterThreads * 16;
+constexpr int kBins = 2048;
+
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+    return v;
+}
+
+template <int D, int R, bool MOVE>
+__global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictParams p, const int cluster) {
+    constexpr int NW = kClusterThreads / 32;
+    constexpr int ENTRIES = R * NW;  // (r, warp) pairs
+    __shared__ int hist[3][kBins];
+    __shared__ int cnt[ENTRIES];
+    __shared__ int wsum[NW];
+    __shared__ int share[4];  // read by the cluster: newest position, equals, holes and movers
+    __shared__ int pick[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const long long slab = blockIdx.x / cluster;
+    const int b = static_cast<int>(slab / p.Hkv), g = static_cast<int>(slab - static_cast<long long>(b) * p.Hkv);
+    const int n = min(max(p.seq_lens[b], 0), p.L), keep = p.n_keep;
+    const float* acc = p.acc + slab * p.L;
+    const int* pos = p.pos + slab * p.L;
+    float* acc_out = p.acc_out + slab * p.L;
+    int* pos_out = p.pos_out + slab * p.L;
+    int* src = p.src_out ? p.src_out + slab * keep : nullptr;
+    const bool copy = p.acc_out != p.acc, copy_pos = p.pos_out != p.pos;
+    const int s0 = rank * R * kClusterThreads + tid;  // slot of r: s0 + r * 1024
+    const auto sync = [&] {
+        if (cluster > 1) cluster_sync_all();
+        else __syncthreads();
+    };
+    grid_dep_launch();
+    if (g == 0 && rank == 0 && tid == 0) p.lens_out[b] = min(n, keep);
+    if (n <= keep) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = s0 + r * kClusterThreads;
+            if (copy && i < n) acc_out[i] = acc[i];
+            if (copy_pos && i < n) pos_out[i] = pos[i];
+            if (src && i < keep) src[i] = i < n ? i : -1;
+        }
+        if (rank == 0 && tid == 0) p.n_moves[slab] = 0;
+        return;
+    }
+    float w[R];
+    int q[R];
+    int newest = INT_MIN;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = s0 + r * kClusterThreads;
+        w[r] = i < n ? acc[i] : 0.f;
+        q[r] = i < n ? pos[i] : INT_MIN;
+        newest = max(newest, q[r]);
+    }
+    for (int i = tid; i < 3 * kBins; i += kClusterThreads) (&hist[0][0])[i] = 0;
+    newest = __reduce_max_sync(0xffffffffu, newest);
+    if (lane == 0) wsum[warp] = newest;
+    __syncthreads();
+    if (warp == 0) {
+        const int m = __reduce_max_sync(0xffffffffu, wsum[lane]);
+        if (lane == 0) share[0] = m;
+    }
+    sync();
+    newest = share[0];
+    for (int c = 0; c < cluster; ++c) {
+        if (c != rank) newest = max(newest, ld_cluster(&share[0], c));
+    }
+    // a position above `oldest` is protected; in 64 bits, as positions may be any int32
+    const long long oldest = static_cast<long long>(newest) - p.n_recent;
+    const auto key_of = [&](int r) { return evict_key(w[r], q[r] > oldest); };
+    uint32_t prefix = 0;  // leading bits of the threshold key
+    int want = keep;      // how many of the keys that share them are kept
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+        const uint32_t digits = pass == 2 ? 1023u : 2047u;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t k = key_of(r);
+            if (s0 + r * kClusterThreads < n && (pass == 0 || (k >> above) == (prefix >> above))) {
+                atomicAdd(&hist[pass][(k >> shift) & digits], 1);
+            }
+        }
+        sync();
+        // thread t: bins 2047 - 2t and 2046 - 2t, so that a scan by thread runs from the top
+        const int hi = kBins - 1 - 2 * tid;
+        int c1 = hist[pass][hi], c0 = hist[pass][hi - 1];
+        for (int c = 0; c < cluster; ++c) {
+            if (c == rank) continue;
+            c1 += ld_cluster(&hist[pass][hi], c);
+            c0 += ld_cluster(&hist[pass][hi - 1], c);
+        }
+        int incl = c1 + c0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+        int before = lane < warp ? wsum[lane] : 0;
+        before = __reduce_add_sync(0xffffffffu, before) + incl - c1 - c0;  // keys above this thread's bins
+        if (before < want && want <= before + c1) {
+            pick[0] = hi;
+            pick[1] = want - before;
+        } else if (before + c1 < want && want <= before + c1 + c0) {
+            pick[0] = hi - 1;
+            pick[1] = want - before - c1;
+        }
+        __syncthreads();
+        prefix |= static_cast<uint32_t>(pick[0]) << shift;
+        want = pick[1];
+    }
+    // exclusive scan of cnt over its entries in order; returns the sum
+    const auto scan = [&]() {
+        int v = tid < ENTRIES ? cnt[tid] : 0, incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+        const int mine = wsum[lane];
+        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
+        const int all = __reduce_add_sync(0xffffffffu, mine);
+        if (tid < ENTRIES) cnt[tid] = before + incl - v;
+        __syncthreads();
+        return all;
+    };
+    const uint32_t below = (1u << lane) - 1;
+    // the lowest `want` of the keys at the threshold
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const bool eq = s0 + r * kClusterThreads < n && key_of(r) == prefix;
+        const uint32_t bal = __ballot_sync(0xffffffffu, eq);
+        if (lane == 0) cnt[r * NW + warp] = __popc(bal);
+    }
+    __syncthreads();
+    int all = scan();
+    int eq_before = 0;
+    if (cluster > 1) {
+        if (tid == 0) share[1] = all;
+        sync();
+        for (int c = 0; c < rank; ++c) eq_before += ld_cluster(&share[1], c);
+    }
+    uint32_t kept = 0;  // bit r
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const bool in = s0 + r * kClusterThreads < n;
+        const uint32_t k = key_of(r);
+        const bool eq = in && k == prefix;
+        const uint32_t bal = __ballot_sync(0xffffffffu, eq);
+        const bool low = eq_before + cnt[r * NW + warp] + __popc(bal & below) < want;
+        if (in && (k > prefix || (eq && low))) kept |= 1u << r;
+    }
+    __syncthreads();
+    // holes (low half of a count) and movers (high half); both fit: a CTA has at most 16384 slots
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = s0 + r * kClusterThreads;
+        const bool k = kept >> r & 1u;
+        const uint32_t bh = __ballot_sync(0xffffffffu, i < keep && !k), bm = __ballot_sync(0xffffffffu, i >= keep && k);
+        if (lane == 0) cnt[r * NW + warp] = __popc(bh) | (__popc(bm) << 16);
+    }
+    __syncthreads();
+    all = scan();
+    int h_before = 0, m_before = 0, total = all & 0xFFFF;
+    if (cluster > 1) {
+        if (tid == 0) share[2] = all;
+        sync();
+        for (int c = 0; c < cluster; ++c) {
+            const int v = c == rank ? all : ld_cluster(&share[2], c);
+            if (c < rank) {
+                h_before += v & 0xFFFF;
+                m_before += v >> 16;
+            }
+            if (c != rank) total += v & 0xFFFF;
+        }
+    }
+    int* holes = p.moves + slab * 2 * p.list;
+    int* movers = holes + p.list;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = s0 + r * kClusterThreads;
+        const bool k = kept >> r & 1u, hole = i < keep && !k, mover = i >= keep && k;
+        const uint32_t bh = __ballot_sync(0xffffffffu, hole), bm = __ballot_sync(0xffffffffu, mover);
+        const int at = cnt[r * NW + warp];
+        if (hole) holes[h_before + (at & 0xFFFF) + __popc(bh & below)] = i;
+        if (mover) movers[m_before + (at >> 16) + __popc(bm & below)] = i;
+        if (k && i < keep) {
+            if (copy) acc_out[i] = w[r];
+            if (copy_pos) pos_out[i] = q[r];
+            if (src) src[i] = i;
+        }
+    }
+    sync();  // the lists are whole, and every slot of the slab has been read
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = s0 + r * kClusterThreads;
+        const bool mover = i >= keep && (kept >> r & 1u);
+        const uint32_t bm = __ballot_sync(0xffffffffu, mover);
+        if (mover) {
+            const int to = holes[m_before + (cnt[r * NW + warp] >> 16) + __popc(bm & below)];
+            acc_out[to] = w[r];
+            pos_out[to] = q[r];
+            if (src) src[to] = i;
+        }
+        if (i >= keep && i < n) {
+            acc_out[i] = 0.f;
+            pos_out[i] = -1;
+        }
+    }
+    if (rank == 0 && tid == 0) p.n_moves[slab] = total;
+    if (MOVE) move_rows<D>(p, slab, holes, movers, total, rank * kClusterThreads + tid, cluster * kClusterThreads);
+}
+
+template <int D, int R>
+static cudaError_t launch_evict(const EvictParams& p, unsigned slabs, int cluster, bool move, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(slabs * static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(kClusterThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return move ? cudaLaunchKernelEx(&cfg, evict_kernel<D, R, true>, p, cluster)
+                : cudaLaunchKernelEx(&cfg, evict_kernel<D, R, false>, p, cluster);
+}
+
+template <int D>
+static cudaError_t launch_evict_d(const EvictParams& p, unsigned slabs, cudaStream_t s) {
+    const int sms = device_sm_count();
+    cudaError_t e;
+    bool move = false;
+    if (p.L > kEvictMaxSlots) {
+        evict_select_long_kernel<<<slabs, kEvictThreads, 0, s>>>(p);
+        e = cudaGetLastError();
+    } else {
+        // as few CTAs as hold a slab; more while SMs are idle and each keeps a few thousand slots
+        int cluster = 1;
+        while (cluster * kClusterThreads * 16 < p.L) cluster *= 2;
+        while (cluster < kEvictMaxCluster && static_cast<int64_t>(slabs) * cluster * 2 <= sms &&
+               p.L > cluster * kClusterThreads * 4) {
+            cluster *= 2;
+        }
+        // few slabs leave SMs without a CTA: a second launch moves their rows with all of them
+        move = static_cast<int64_t>(slabs) * cluster * 4 >= 3ll * sms || p.list <= 256;
+        e = p.L <= cluster * kClusterThreads * 4 ? launch_evict<D, 4>(p, slabs, cluster, move, s)
+                                                 : launch_evict<D, 16>(p, slabs, cluster, move, s);
+    }
+    if (e != cudaSuccess || move || p.list == 0) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(slabs, static_cast<unsigned>(std::max<int64_t>(1, 8ll * sms / slabs)));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel<D>, p);
 }
 
 static bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -514,14 +817,7 @@ extern "C" dak_status dak_kv_evict(const dak_placement* KV, const int* seq_lens,
     p.head_bytes = KV->head_bytes;
     p.h_s = KV->h_s;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    evict_select_kernel<<<static_cast<unsigned>(slabs), kEvictThreads, 0, s>>>(p);
-    if (p.list > 0) {
-        const dim3 grid(static_cast<unsigned>(slabs), 8);
-        if (KV->D == 128) {
-            evict_move_kernel<128><<<grid, kMoveThreads, 0, s>>>(p);
-        } else {
-            evict_move_kernel<64><<<grid, kMoveThreads, 0, s>>>(p);
-        }
-    }
-    return cuda_status(cudaGetLastError());
+    const cudaError_t e = KV->D == 128 ? launch_evict_d<128>(p, static_cast<unsigned>(slabs), s)
+                                       : launch_evict_d<64>(p, static_cast<unsigned>(slabs), s);
+    return cuda_status(e);
 }

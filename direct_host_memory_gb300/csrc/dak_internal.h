@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/dak.h"
 
 struct dak_placement {
@@ -64,6 +66,26 @@ dak_status cuda_status(cudaError_t e);
 // device address looked up with cudaGetSymbolAddress is kept together with it, so that the
 // address is looked up again after the context was destroyed and made anew.
 unsigned long long current_context_id();
+
+// Raises a kernel's limit of dynamic shared memory to `bytes` once per context and device (a call
+// costs the host a microsecond, and the cache operators are called per layer and token).
+class SmemLimit {
+public:
+    cudaError_t raise(const void* kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long id = current_context_id();
+        if (dev < kDevices && id != 0 && done_[dev].load(std::memory_order_relaxed) == id) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && dev < kDevices) done_[dev].store(current_context_id(), std::memory_order_relaxed);
+        return e;
+    }
+
+private:
+    static constexpr int kDevices = 64;
+    std::atomic<unsigned long long> done_[kDevices] = {};
+};
 
 // The library's allocations go through these wrappers, which count the live allocations
 // (dak_alloc_counts) and take the host-side fault injection of dak_inject_fault: an injected
@@ -139,8 +161,8 @@ dak_status launch_attn(const void* Q, const dak_placement* KV, const void* host_
 // The prefix pass of dak_attn_prefix (dak_prefix.cu) over the placement P of shared prefixes: for
 // every row of Q [B][H_q][D] up to prefix_max_ranges(P) partials, unnormalised o_part
 // [rows][ranges][D] and ml_part [rows][ranges][2] (maximum in the log2 domain, sum), and in
-// n_ranges [n_prefix] how many of them a prefix's rows have (not written for a prefix without
-// members or rows). Arguments are checked by the caller.
+// n_ranges [B] how many of them a request's rows have (not written for a request without a prefix or
+// with an empty one). Arguments are checked by the caller.
 constexpr int kMaxPrefixes = 1024;
 int prefix_max_ranges(const dak_placement* P);
 dak_status launch_prefix(const void* Q, const dak_placement* P, const int* lens, const int* of, int B, int H_q,

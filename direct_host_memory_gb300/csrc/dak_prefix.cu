@@ -43,7 +43,7 @@ struct PrefixParams {
     const int* of;     // [B] or null
     float* o_part;     // [B * Hq][n_pre][D]
     float2* ml_part;   // [B * Hq][n_pre]: m (log2 domain), l
-    int* n_ranges;     // [n_prefix]: key ranges of a prefix that has members and rows
+    int* n_ranges;     // [B]: key ranges that a request's rows have partials of (not written without any)
     int B, Hq, Hkv, G, L, n_prefix, n_pre, h_s, slab_chunks;
     int mpt;  // members of a 128-row tile: 128 / G
     float scale_log2;
@@ -160,7 +160,7 @@ __device__ __forceinline__ void report_prefix(const PrefixParams& p, int b) {
 // Every CTA waits for this before its first copy, so it is built for latency: the map and the
 // lengths are loaded side by side (the first 128 requests' map stays in registers), counting and
 // searching run in shared memory, scratch[f] (n_prefix int4, free until the next barrier): requests,
-// 256-row tiles, chunks, rows; divisions are 32-bit.
+// halves (see below), chunks, rows; divisions are 32-bit.
 __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* scratch, PrefixUnit* unit, int* member) {
     constexpr unsigned all = 0xffffffffu;
     const int lane = threadIdx.x & 31;
@@ -173,8 +173,20 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         return b0 == 0 ? map[0] : b0 == 32 ? map[1] : b0 == 64 ? map[2] : b0 == 96 ? map[3]
                : b0 + lane < p.B ? p.of[b0 + lane] : -1;
     };
-    const auto ranges = [&](int c, int T) { return min((c + T - 1) / T, p.n_pre); };
-    int f = -1, start = 0, base = 0, n = 0;
+    // Requests' rows make full tiles of two 128-row halves and one more of one or two. A half over a
+    // chunk is a unit of work, so that a tile of two is cut into twice the ranges; `halves` holds
+    // both kinds: tiles of two in its upper bits, one of one in bit 0.
+    const auto halves_of = [&](int cnt) {
+        const int full = cnt / per_tile, rest = cnt - full * per_tile;
+        return rest > p.mpt ? 2 * full + 2 : 2 * full + (rest > 0);
+    };
+    const auto ranges = [&](int work, int c, int T) {
+        return max(1, min(min((work + T - 1) / T, p.n_pre), c / kPrefixMinChunks));
+    };
+    const auto units_of = [&](int halves, int c, int T) {  // per kv head
+        return halves == 0 || c == 0 ? 0 : (halves >> 1) * ranges(2 * c, c, T) + (halves & 1) * ranges(c, c, T);
+    };
+    int f = -1, start = 0, base = 0, T = 1;
     int4 e;
     if (p.n_prefix == 1) {
         const int len = p.lens ? min(max(p.lens[0], 0), p.L) : p.L;
@@ -187,11 +199,24 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
                 cnt += __popc(__ballot_sync(all, v == 0));
             }
         }
-        e = make_int4(cnt, (cnt + per_tile - 1) / per_tile, (len + 63) >> 6, len);
-        if (e.y > 0 && e.z > 0) {
-            const int n_tiles = e.y * p.Hkv, each = n_tiles < ctas ? ctas / n_tiles : 1;
-            n = ranges(e.z, max(min(kPrefixMinChunks, e.z), (e.z + each - 1) / each));
-            base = n_tiles * n;
+        e = make_int4(cnt, halves_of(cnt), (len + 63) >> 6, len);
+        const int tiles = ((e.y + 1) >> 1) * p.Hkv;
+        if (tiles > 0 && e.z > 0) {
+            T = 2 * e.z;
+            if (tiles < ctas) {
+                if (e.y == 1 || (e.y & 1) == 0) {  // tiles of one kind: each the same share of the CTAs
+                    const int each = ctas / tiles, work = e.y == 1 ? e.z : 2 * e.z;
+                    T = (work + each - 1) / each;
+                } else {
+                    int lo = 1;
+                    while (lo < T) {
+                        const int mid = (lo + T) >> 1;
+                        if (units_of(e.y, e.z, mid) * p.Hkv <= ctas) T = mid;
+                        else lo = mid + 1;
+                    }
+                }
+            }
+            base = units_of(e.y, e.z, T) * p.Hkv;
             if (u < base) f = 0;
         }
     } else {
@@ -214,11 +239,11 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         float work = 0.f;
         for (int i = lane; i < p.n_prefix; i += 32) {
             const int4 q = scratch[i];
-            const int tiles = q.z > 0 ? (q.x + per_tile - 1) / per_tile : 0;
-            scratch[i].y = tiles;
-            n_tiles += tiles;
-            work += static_cast<float>(tiles) * static_cast<float>(q.z);
-            if (tiles) cmax = max(cmax, q.z);
+            const int halves = q.z > 0 ? halves_of(q.x) : 0;
+            scratch[i].y = halves;
+            n_tiles += (halves + 1) >> 1;
+            work += static_cast<float>(halves) * static_cast<float>(q.z);
+            if (halves) cmax = max(cmax, q.z);
         }
         __syncwarp();
         cmax = __reduce_max_sync(all, cmax);
@@ -226,17 +251,16 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(all, work, o);
         work *= static_cast<float>(p.Hkv);
-        int T = cmax;
+        T = 2 * cmax;
         if (n_tiles < ctas) {
-            // sum tiles ceil(c / T) lies between work / T and work / T + n_tiles
+            // the units lie between work / T and work / T + n_tiles
             const auto total = [&](int t) {
                 int k = 0;
-                for (int i = lane; i < p.n_prefix; i += 32) k += scratch[i].y * ranges(scratch[i].z, t);
+                for (int i = lane; i < p.n_prefix; i += 32) k += units_of(scratch[i].y, scratch[i].z, t);
                 return __reduce_add_sync(all, k) * p.Hkv;
             };
-            int lo = max(min(kPrefixMinChunks, cmax), static_cast<int>(min(work / static_cast<float>(ctas), 1e9f)) - 1);
-            lo = min(lo, cmax);
-            T = max(lo, min(cmax, static_cast<int>(min(work / static_cast<float>(ctas - n_tiles), 1e9f)) + 2));
+            int lo = min(T, max(1, static_cast<int>(min(work / static_cast<float>(ctas), 1e9f)) - 1));
+            T = max(lo, min(T, static_cast<int>(min(work / static_cast<float>(ctas - n_tiles), 1e9f)) + 2));
             while (lo < T) {
                 const int mid = (lo + T) >> 1;
                 if (total(mid) <= ctas) T = mid;
@@ -245,7 +269,7 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         }
         for (int f0 = 0; f0 < p.n_prefix; f0 += 32) {
             const int ff = f0 + lane;
-            const int k = ff < p.n_prefix ? scratch[ff].y * ranges(scratch[ff].z, T) * p.Hkv : 0;
+            const int k = ff < p.n_prefix ? units_of(scratch[ff].y, scratch[ff].z, T) * p.Hkv : 0;
             int incl = k;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -260,17 +284,17 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
             }
             base += __shfl_sync(all, incl, 31);
         }
-        if (f >= 0) {
-            e = scratch[f];
-            n = ranges(e.z, T);
-        }
+        if (f >= 0) e = scratch[f];
     }
     if (f < 0) {
         if (lane == 0) unit->units = 0;
         return;
     }
-    const int c = e.z, rem = u - start;
-    const int gt = rem / n, s = rem - gt * n, g = gt / e.y, t = gt - g * e.y;
+    // units of a prefix: by kv head, in it the tiles of two and then the one of one, by range
+    const int c = e.z, twos = e.y >> 1, r2 = ranges(2 * c, c, T), per_g = units_of(e.y, c, T);
+    const int rem = u - start, g = rem / per_g, rg = rem - g * per_g;
+    const bool two = rg < twos * r2;
+    const int n = two ? r2 : ranges(c, c, T), t = two ? rg / r2 : twos, s = rg - t * r2;
     const int r0 = t * per_tile, here = min(per_tile, e.x - r0);
     if (lane == 0) {
         const int each = c / n, more = c - each * n;  // the first `more` ranges get a chunk more
@@ -281,21 +305,24 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         unit->c1 = unit->c0 + each + (s < more);
         unit->len = e.w;
         unit->members = here;
-        unit->two = here > p.mpt;
+        unit->two = two;
         unit->units = base;
-        if (gt == 0 && s == 0) p.n_ranges[f] = n;
     }
     if (!p.of) {
         for (int i = lane; i < here; i += 32) member[i] = r0 + i;
-        return;
+    } else {
+        int seen = 0;
+        for (int b0 = 0; b0 < p.B && seen < r0 + here; b0 += 32) {
+            const int v = map_of(b0);
+            const unsigned m = __ballot_sync(all, v == f);
+            const int rank = seen + __popc(m & ((1u << lane) - 1)) - r0;
+            if (v == f && rank >= 0 && rank < here) member[rank] = b0 + lane;
+            seen += __popc(m);
+        }
     }
-    int seen = 0;
-    for (int b0 = 0; b0 < p.B && seen < r0 + here; b0 += 32) {
-        const int v = map_of(b0);
-        const unsigned m = __ballot_sync(all, v == f);
-        const int rank = seen + __popc(m & ((1u << lane) - 1)) - r0;
-        if (v == f && rank >= 0 && rank < here) member[rank] = b0 + lane;
-        seen += __popc(m);
+    __syncwarp();
+    if (g == 0 && s == 0) {
+        for (int i = lane; i < here; i += 32) p.n_ranges[member[i]] = n;
     }
 }
 
@@ -319,18 +346,17 @@ __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_addr, uint3
     }
 }
 
-// O (128 rows x D) += P . V: P from TMEM in PARTS bf16 parts, two keys a column, where the softmax
+// O (128 rows x D) += P . V: P from TMEM in `parts` bf16 parts, two keys a column, where the softmax
 // put them; V MN-major (idesc bit 16): N = D along a row's halves, 8192 nk bytes apart, K = the
 // keys in groups of eight, 1024 bytes apart.
-template <int D, int PARTS>
-__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_addr, int nk, bool accumulate) {
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_addr, int nk, int parts, bool accumulate) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, D) | (1u << 16);
     uint64_t vd = smem_desc(v_addr, static_cast<uint32_t>(8192 * nk), 1024, 2);
     uint32_t acc = accumulate;
 #pragma unroll 1
     for (int k = 0; k < 4 * nk; ++k) {  // 16 keys: columns 16 k + 8 q of P's part q, the third at 64 + 8 k
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q) {
+        for (int q = 0; q < parts; ++q) {
             umma_bf16_ts(d_tmem, p_tmem + (q < 2 ? k * 16 + q * 8 : 64 + k * 8), vd, idesc, acc);
             acc = 1;
         }
@@ -341,7 +367,7 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
 // One step of a row: S (nk chunks of 64 keys, the first `valid` of them real) into P over it in TMEM,
 // with the running maximum (of the reference, log2 domain) and sum. S is read twice, once for the
 // maximum and once for the exponentials, 32 columns a turn.
-template <int D, int KEYS>
+template <int D, int PARTS>
 __device__ __forceinline__ void softmax_step(uint32_t s_addr, uint32_t o_addr, int nk, int valid, float scale_log2,
                                              float& m_ref, float& l, bool first) {
     const auto load = [&](int q, float(&v)[2][16]) {
@@ -404,9 +430,10 @@ __device__ __forceinline__ void softmax_step(uint32_t s_addr, uint32_t o_addr, i
                 const float2 w = make_float2(exp2_ftz(e.x), exp2_ftz(e.y));
                 sum[k & 1] = add2(sum[k & 1], w);
                 hi[k] = pack_bf16(w.x, w.y);
+                if (PARTS == 1) continue;
                 float2 r = fma2(make_float2(bf_lo(hi[k]), bf_hi(hi[k])), minus, w);
                 lo[k] = pack_bf16(r.x, r.y);
-                if (KEYS == 64) {
+                if (PARTS == 3) {
                     r = fma2(make_float2(bf_lo(lo[k]), bf_hi(lo[k])), minus, r);
                     th[k] = pack_bf16(r.x, r.y);
                 }
@@ -414,8 +441,8 @@ __device__ __forceinline__ void softmax_step(uint32_t s_addr, uint32_t o_addr, i
             // P goes over the 16 scores that it was made from, part by part; the third part has the
             // columns behind a step of 64
             tmem_st8(s_addr + q * 32 + h * 16, hi);
-            tmem_st8(s_addr + q * 32 + h * 16 + 8, lo);
-            if (KEYS == 64) tmem_st8(s_addr + 64 + q * 16 + h * 8, th);
+            if (PARTS >= 2) tmem_st8(s_addr + q * 32 + h * 16 + 8, lo);
+            if (PARTS == 3) tmem_st8(s_addr + 64 + q * 16 + h * 8, th);
         }
     }
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -454,7 +481,7 @@ struct RingPos {
     }
 };
 
-// KEYS: keys of a step, 128 (bf16 output, P in two bf16 parts) or 64 (fp32 output, three).
+// KEYS: keys of a step, 128 (bf16 output, P in one or two bf16 parts) or 64 (fp32 output, three).
 template <int D, int KEYS>
 struct PrefixCfg {
     static constexpr int kTileBytes = 128 * D * 2;  // one Q tile
@@ -472,7 +499,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     using C = PrefixCfg<D, KEYS>;
     constexpr int NS = C::kStages;
     constexpr int SMAX = KEYS / 64;  // chunks of a whole step
-    constexpr int parts = KEYS == 64 ? 3 : 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     uint8_t* ring = smem + 2 * C::kTileBytes;
@@ -485,6 +511,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     float2(*ex)[128] = reinterpret_cast<float2(*)[128]>(smem + C::kTileBytes);
     volatile int* abort = &abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dep_launch();  // the pass over the own caches fills SMs as they become free
 
     if (threadIdx.x == 32) {
         abort_flag = 0;
@@ -521,6 +548,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const PrefixUnit x = unit;
         if (x.units == 0) break;
         const int steps = (x.c1 - x.c0 + SMAX - 1) / SMAX;
+        // bf16 parts of P. With two row tiles the products and the softmax set the pace, not K and V:
+        // one part, as in dak_attn (its rounding stays below that of a bf16 output); with one the
+        // second part's products are free.
+        const int parts = KEYS == 64 ? 3 : x.two ? 1 : 2;
         const int items = x.two ? 2 * steps : steps;  // item i: stream i & 1, step i / 2 or i
         const long long slab = static_cast<long long>(x.f) * p.Hkv + x.g;
         const int tier = slab < p.h_s ? 0 : 1;
@@ -606,7 +637,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 tc_fence_after();
                 if (leader) {
                     const uint32_t b = ring_addr + v.slot * C::kStage;
-                    issue_pv<D, parts>(o_tmem, s_tmem, b, min(SMAX, x.c1 - x.c0 - j * SMAX), !first);
+                    issue_pv<D>(o_tmem, s_tmem, b, min(SMAX, x.c1 - x.c0 - j * SMAX), parts, !first);
                     umma_commit(&pv_done[st]);
                     release(v.slot);
                 }
@@ -670,7 +701,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                softmax_step<D, KEYS>(s_addr, o_addr, nk, valid, p.scale_log2, m_ref, l, mine == 0);
+                if (KEYS == 64) softmax_step<D, 3>(s_addr, o_addr, nk, valid, p.scale_log2, m_ref, l, mine == 0);
+                else if (x.two) softmax_step<D, 1>(s_addr, o_addr, nk, valid, p.scale_log2, m_ref, l, mine == 0);
+                else softmax_step<D, 2>(s_addr, o_addr, nk, valid, p.scale_log2, m_ref, l, mine == 0);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -777,7 +810,8 @@ int prefix_max_ranges(const dak_placement* P) {
 template <int D, int KEYS>
 static cudaError_t launch_prefix_d(const PrefixParams& p, const PrefixMaps& maps, int grid, cudaStream_t s) {
     auto k = prefix_kernel<D, KEYS>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixCfg<D, KEYS>::kSmem);
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(k), PrefixCfg<D, KEYS>::kSmem);
     if (e != cudaSuccess) return e;
     k<<<grid, kPrefixThreads, PrefixCfg<D, KEYS>::kSmem, s>>>(p, maps);
     return cudaGetLastError();
