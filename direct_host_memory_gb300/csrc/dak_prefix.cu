@@ -3,19 +3,21 @@
 // request's query head). Partial results go to the merge of dak_attn.cu.
 //
 // The contraction is GEMM-shaped (rows x keys x D twice), so it runs on the tcgen05 tensor cores
-// as the usual two products with an online softmax between them:
-//   S  = Q (128 rows x D, shared memory) . K^T (D x 128 keys, shared memory) -> TMEM, fp32
-//   P  = 2^(S * scale log2 e - m), written back into S's TMEM columns as bf16
-//   O += P (TMEM) . V (128 keys x D, shared memory) -> TMEM, fp32
-// A CTA has two streams, each a warpgroup of 128 threads (thread = row) with its own S, P and O
-// in TMEM, so that one stream's softmax runs under the other's products. With more than 128
-// rows the streams hold two row tiles and both go through every key; with fewer they hold the
-// same rows and take the 128-key steps in turn, and their results are merged in the CTA.
+// as the usual two products with an online softmax between them, 64 keys a step:
+//   S  = Q (128 rows x D, shared memory) . K^T (D x 64 keys, shared memory) -> TMEM, fp32
+//   P  = 2^(S * scale log2 e - m), written to TMEM as bf16
+//   O += P (TMEM) . V (64 keys x D, shared memory) -> TMEM, fp32
+// A CTA has two streams, each 128 threads (thread = row) and a warp that issues its products, with S,
+// P and O in TMEM. S is free as soon as its row is in a thread's registers, so that the next step's
+// scores are computed under the softmax, and P has two buffers where it fits.
+// With more than 128 rows the streams hold two row tiles and both go through every key; with fewer
+// they hold the same rows and take the steps in turn, and their results are merged in the CTA.
 //
 // The cache stores piece c of token t at c ^ (t & 7), which is the tensor cores' 128-byte swizzle
-// once a row's two 128-byte halves lie apart; a 5-D tensor map (64 elements, 64 tokens, K or V,
-// chunk, half) brings a step's K or V so in one copy. K is then a K-major operand; V, whose rows
-// are keys, an MN-major one.
+// once a row's two 128-byte halves lie apart; a 5-D tensor map (64 elements, 64 tokens, K and V,
+// chunk, half) brings a chunk so in one copy of up to 32 KiB (issuing a copy takes its thread 0.3 us
+// whatever its size, which held K and V apart to 20 bytes a cycle and SM). K is then a K-major
+// operand; V, whose rows are keys, an MN-major one.
 //
 // Which CTA works on what is planned on the device from the prefixes' lengths and the requests'
 // map, so that a captured call follows them: units (prefix, kv head, 256-row tile, key range),
@@ -29,12 +31,13 @@
 
 namespace dak {
 
-constexpr int kPrefixThreads = 11 * 32;  // two softmax warpgroups, copies, each stream's products
+constexpr int kSoftmaxThreads = 2 * 128;  // two streams, a thread a row
+constexpr int kPrefixThreads = kSoftmaxThreads + 3 * 32;  // and copies, each stream's products
+constexpr int kPrefixTwoCost = 5, kPrefixOneCost = 4;  // of a chunk, by a tile's 128-row halves
 constexpr int kPrefixMinChunks = 2;      // chunks of 64 keys in a range, at least
 
 struct PrefixMaps {
-    CUtensorMap step[2];  // [host, HBM]: a whole step (KEYS keys)
-    CUtensorMap tail[2];  // one chunk of 64 keys
+    CUtensorMap tier[2];  // host, HBM: chunks of 64 keys
 };
 
 struct PrefixParams {
@@ -50,7 +53,7 @@ struct PrefixParams {
     DevStatus* st;
 };
 
-enum : uint32_t { X_PROD_EMPTY = 0x51, X_PROD_FULL, X_MMA_FULL, X_MMA_P, X_MMA_PV, X_MMA_GO, X_SM_S, X_SM_V, X_SM_O, X_DRAIN };
+enum : uint32_t { X_PROD_EMPTY = 0x51, X_PROD_FULL, X_MMA_FULL, X_MMA_P, X_MMA_PV, X_SM_S, X_SM_O, X_DRAIN };
 
 // What a CTA works on.
 struct PrefixUnit {
@@ -60,15 +63,27 @@ struct PrefixUnit {
     int members;       // requests of this tile
     int two;           // the members fill more than one 128-row tile
     int units;         // units of the whole launch
+    int shared;        // other tiles read the same chunks
 };
 
-__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int kv, int chunk, uint64_t* bar,
-                                            uint64_t policy) {
+__device__ __forceinline__ void tma_load_chunk(void* dst, const CUtensorMap* map, int chunk, uint64_t* bar, uint64_t policy) {
     asm volatile(
         "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
-        "%2, %3, %4, %2}], [%5], %6;" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(0), "r"(kv), "r"(chunk), "r"(smem_u32(bar)), "l"(policy)
+        "%2, %2, %3, %2}], [%4], %5;" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(0), "r"(chunk), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
+}
+
+// mbar_wait with a plain test first: where the phase is long over, as it mostly is for the warps that
+// issue products, the suspending form takes twice the time.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort, DevStatus* st, uint32_t where) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok || mbar_wait(bar, parity, abort, st, DAK_ERR_TIMEOUT, where);
 }
 
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -173,9 +188,9 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         return b0 == 0 ? map[0] : b0 == 32 ? map[1] : b0 == 64 ? map[2] : b0 == 96 ? map[3]
                : b0 + lane < p.B ? p.of[b0 + lane] : -1;
     };
-    // Requests' rows make full tiles of two 128-row halves and one more of one or two. A half over a
-    // chunk is a unit of work, so that a tile of two is cut into twice the ranges; `halves` holds
-    // both kinds: tiles of two in its upper bits, one of one in bit 0.
+    // Requests' rows make full tiles of two 128-row halves and one more of one or two; `halves` holds
+    // both kinds: tiles of two in its upper bits, one of one in bit 0. A chunk costs a tile of two
+    // 1.25 times what it costs one of one (measured 1.9k and 1.55k cycles), and the ranges are cut so.
     const auto halves_of = [&](int cnt) {
         const int full = cnt / per_tile, rest = cnt - full * per_tile;
         return rest > p.mpt ? 2 * full + 2 : 2 * full + (rest > 0);
@@ -184,7 +199,7 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         return max(1, min(min((work + T - 1) / T, p.n_pre), c / kPrefixMinChunks));
     };
     const auto units_of = [&](int halves, int c, int T) {  // per kv head
-        return halves == 0 || c == 0 ? 0 : (halves >> 1) * ranges(2 * c, c, T) + (halves & 1) * ranges(c, c, T);
+        return halves == 0 || c == 0 ? 0 : (halves >> 1) * ranges(kPrefixTwoCost * c, c, T) + (halves & 1) * ranges(kPrefixOneCost * c, c, T);
     };
     int f = -1, start = 0, base = 0, T = 1;
     int4 e;
@@ -202,10 +217,10 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         e = make_int4(cnt, halves_of(cnt), (len + 63) >> 6, len);
         const int tiles = ((e.y + 1) >> 1) * p.Hkv;
         if (tiles > 0 && e.z > 0) {
-            T = 2 * e.z;
+            T = kPrefixTwoCost * e.z;
             if (tiles < ctas) {
                 if (e.y == 1 || (e.y & 1) == 0) {  // tiles of one kind: each the same share of the CTAs
-                    const int each = ctas / tiles, work = e.y == 1 ? e.z : 2 * e.z;
+                    const int each = ctas / tiles, work = (e.y == 1 ? kPrefixOneCost : kPrefixTwoCost) * e.z;
                     T = (work + each - 1) / each;
                 } else {
                     int lo = 1;
@@ -242,7 +257,7 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
             const int halves = q.z > 0 ? halves_of(q.x) : 0;
             scratch[i].y = halves;
             n_tiles += (halves + 1) >> 1;
-            work += static_cast<float>(halves) * static_cast<float>(q.z);
+            work += static_cast<float>((halves >> 1) * kPrefixTwoCost + (halves & 1) * kPrefixOneCost) * static_cast<float>(q.z);
             if (halves) cmax = max(cmax, q.z);
         }
         __syncwarp();
@@ -251,7 +266,7 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(all, work, o);
         work *= static_cast<float>(p.Hkv);
-        T = 2 * cmax;
+        T = kPrefixTwoCost * cmax;
         if (n_tiles < ctas) {
             // the units lie between work / T and work / T + n_tiles
             const auto total = [&](int t) {
@@ -291,10 +306,10 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         return;
     }
     // units of a prefix: by kv head, in it the tiles of two and then the one of one, by range
-    const int c = e.z, twos = e.y >> 1, r2 = ranges(2 * c, c, T), per_g = units_of(e.y, c, T);
+    const int c = e.z, twos = e.y >> 1, r2 = ranges(kPrefixTwoCost * c, c, T), per_g = units_of(e.y, c, T);
     const int rem = u - start, g = rem / per_g, rg = rem - g * per_g;
     const bool two = rg < twos * r2;
-    const int n = two ? r2 : ranges(c, c, T), t = two ? rg / r2 : twos, s = rg - t * r2;
+    const int n = two ? r2 : ranges(kPrefixOneCost * c, c, T), t = two ? rg / r2 : twos, s = rg - t * r2;
     const int r0 = t * per_tile, here = min(per_tile, e.x - r0);
     if (lane == 0) {
         const int each = c / n, more = c - each * n;  // the first `more` ranges get a chunk more
@@ -307,6 +322,7 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         unit->members = here;
         unit->two = two;
         unit->units = base;
+        unit->shared = e.y > 2;
     }
     if (!p.of) {
         for (int i = lane; i < here; i += 32) member[i] = r0 + i;
@@ -326,74 +342,74 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
     }
 }
 
-// The products of a step of nk chunks of 64 keys, one thread. Descriptors differ in their start
-// address alone, which is the low word's. This and all code that a CTA runs only a few times is kept
-// small: a first run fetches its instructions through the memory system that K and V saturate, at 10
-// cycles an instruction and more, which set the time of short prefixes.
+// The products of a step, one thread. Descriptors differ in their start address alone, which is the
+// low word's. This and all code that a CTA runs only a few times is kept small: a first run fetches
+// its instructions through the memory system that K and V saturate, at 10 cycles an instruction and
+// more, which set the time of short prefixes.
 //
-// S (128 rows x 64 nk keys) = Q . K^T: both K-major, 128-byte rows in 8-row groups 1024 bytes apart,
-// 32 bytes further per 16 columns and a half further per 64.
+// S (128 rows x 64 keys) = Q . K^T: both K-major, 128-byte rows in 8-row groups 1024 bytes apart, 32
+// bytes further per 16 columns and a half further per 64.
 template <int D>
-__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_addr, uint32_t k_addr, int nk) {
-    const uint32_t idesc = idesc_bf16_f32(128, static_cast<uint32_t>(64 * nk));
-    uint64_t qd = smem_desc(q_addr, 16, 1024, 2), kd = smem_desc(k_addr, 16, 1024, 2);
-#pragma unroll 1
-    for (int h = 0; h < D / 64; ++h) {
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_addr, uint32_t k_addr) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, 64);
+    const uint64_t qd = smem_desc(q_addr, 16, 1024, 2), kd = smem_desc(k_addr, 16, 1024, 2);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) umma_bf16(d_tmem, qd + k * 2, kd + k * 2, idesc, h > 0 || k > 0);
-        qd += 16384 >> 4;
-        kd += static_cast<uint64_t>(8192 * nk) >> 4;
+    for (int k = 0; k < D / 16; ++k) {
+        umma_bf16(d_tmem, qd + (k >> 2) * (16384 >> 4) + (k & 3) * 2, kd + (k >> 2) * (16384 >> 4) + (k & 3) * 2, idesc, k > 0);
     }
 }
 
-// O (128 rows x D) += P . V: P from TMEM in `parts` bf16 parts, two keys a column, where the softmax
-// put them; V MN-major (idesc bit 16): N = D along a row's halves, 8192 nk bytes apart, K = the
-// keys in groups of eight, 1024 bytes apart.
-template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_addr, int nk, int parts, bool accumulate) {
-    constexpr uint32_t idesc = idesc_bf16_f32(128, D) | (1u << 16);
-    uint64_t vd = smem_desc(v_addr, static_cast<uint32_t>(8192 * nk), 1024, 2);
-    uint32_t acc = accumulate;
-#pragma unroll 1
-    for (int k = 0; k < 4 * nk; ++k) {  // 16 keys: columns 16 k + 8 q of P's part q, the third at 64 + 8 k
-        for (int q = 0; q < parts; ++q) {
-            umma_bf16_ts(d_tmem, p_tmem + (q < 2 ? k * 16 + q * 8 : 64 + k * 8), vd, idesc, acc);
-            acc = 1;
-        }
-        vd += 2048 >> 4;
-    }
+// Columns of the 16 keys k of part q of P, from where P begins: with three parts they lie over S (the
+// first two) and behind it.
+template <int PARTS>
+__device__ __forceinline__ constexpr uint32_t p_column(int k, int q) {
+    return PARTS == 1 ? k * 8 : q < 2 ? k * 16 + q * 8 : 64 + k * 8;
 }
 
-// One step of a row: S (nk chunks of 64 keys, the first `valid` of them real) into P over it in TMEM,
-// with the running maximum (of the reference, log2 domain) and sum. S is read twice, once for the
-// maximum and once for the exponentials, 32 columns a turn.
+// O (128 rows x D) += P . V: P from TMEM in PARTS bf16 parts, two keys a column, where the softmax
+// put them; V MN-major (idesc bit 16): N = D along a row's halves, 16384 bytes apart, K = the keys in
+// groups of eight, 1024 bytes apart.
 template <int D, int PARTS>
-__device__ __forceinline__ void softmax_step(uint32_t s_addr, uint32_t o_addr, int nk, int valid, float scale_log2,
-                                             float& m_ref, float& l, bool first) {
-    const auto load = [&](int q, float(&v)[2][16]) {
-        tmem_ld16(s_addr + q * 32, v[0]);
-        tmem_ld16(s_addr + q * 32 + 16, v[1]);
-        tmem_wait(v[0]);
-        tmem_wait(v[1]);
-        if (valid < 32 * q + 32) {
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_addr, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, D) | (1u << 16);
+    const uint64_t vd = smem_desc(v_addr, 16384, 1024, 2);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                if (32 * q + k >= valid) v[k >> 4][k & 15] = -INFINITY;
-            }
-        }
-    };
-    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
-    for (int q = 0; q < 2 * nk; ++q) {
-        float v[2][16];
-        load(q, v);
+    for (int k = 0; k < 4; ++k) {  // 16 keys: 8 columns of each part (p_column)
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-            mx[0] = max3(mx[0], v[0][k], v[0][k + 1]);
-            mx[1] = max3(mx[1], v[1][k], v[1][k + 1]);
+        for (int q = 0; q < PARTS; ++q) {
+            umma_bf16_ts(d_tmem, p_tmem + p_column<PARTS>(k, q), vd + k * (2048 >> 4), idesc,
+                         k > 0 || q > 0 ? 1u : static_cast<uint32_t>(accumulate));
         }
     }
-    const float m_new = fmaxf(mx[0], mx[1]) * scale_log2;
+}
+
+// One step of a row: its 64 scores (from `valid` on not real) into P in PARTS bf16 parts, with the row's
+// running sum and the reference that its exponents are taken against (log2 domain). `taken` is called
+// once the scores are in registers, `grown` when a row of the warp outgrows its reference, with the
+// factor for O, and `room` before P is written.
+template <int PARTS, class Taken, class Grown, class Room>
+__device__ __forceinline__ void softmax_step(uint32_t s_addr, uint32_t p_addr, int valid, float scale_log2, float& m_ref,
+                                             float& l, bool first, const Taken& taken, const Grown& grown, const Room& room) {
+    float v[4][16];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tmem_ld16(s_addr + q * 16, v[q]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tmem_wait(v[q]);
+    taken();
+    if (valid < 64) {
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+            if (k >= valid) v[k >> 4][k & 15] = -INFINITY;
+        }
+    }
+    float mx[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        mx[q] = fmaxf(v[q][0], v[q][1]);
+#pragma unroll
+        for (int k = 2; k < 16; k += 2) mx[q] = max3(mx[q], v[q][k], v[q][k + 1]);
+    }
+    const float m_new = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale_log2;
     // the reference only moves when a row's maximum outgrows it by 2^8: until then the sums just
     // grow, which fp32 holds
     if (first) {
@@ -403,70 +419,61 @@ __device__ __forceinline__ void softmax_step(uint32_t s_addr, uint32_t o_addr, i
         const float f = m2 == -INFINITY ? 1.f : exp2_ftz(m_ref - m2);
         m_ref = m2;
         l *= f;
-#pragma unroll 1
-        for (int q = 0; q < D / 16; ++q) {
-            float o[16];
-            tmem_ld16(o_addr + q * 16, o);
-            tmem_wait(o);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] *= f;
-            tmem_st16(o_addr + q * 16, o);
-        }
+        grown(f);
     }
     const float base = m_ref == -INFINITY ? 0.f : m_ref;
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float2 scale2 = make_float2(scale_log2, scale_log2), base2 = make_float2(-base, -base);
     const float2 minus = make_float2(-1.f, -1.f);
-#pragma unroll 1
-    for (int q = 0; q < 2 * nk; ++q) {
-        float v[2][16];
-        load(q, v);
+    room();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t hi[8], lo[8], th[8];
+    for (int q = 0; q < 4; ++q) {
+        uint32_t hi[8], lo[8], th[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float2 e = fma2(make_float2(v[h][2 * k], v[h][2 * k + 1]), scale2, base2);
-                const float2 w = make_float2(exp2_ftz(e.x), exp2_ftz(e.y));
-                sum[k & 1] = add2(sum[k & 1], w);
-                hi[k] = pack_bf16(w.x, w.y);
-                if (PARTS == 1) continue;
-                float2 r = fma2(make_float2(bf_lo(hi[k]), bf_hi(hi[k])), minus, w);
-                lo[k] = pack_bf16(r.x, r.y);
-                if (PARTS == 3) {
-                    r = fma2(make_float2(bf_lo(lo[k]), bf_hi(lo[k])), minus, r);
-                    th[k] = pack_bf16(r.x, r.y);
-                }
+        for (int k = 0; k < 8; ++k) {
+            const float2 e = fma2(make_float2(v[q][2 * k], v[q][2 * k + 1]), scale2, base2);
+            const float2 w = make_float2(exp2_ftz(e.x), exp2_ftz(e.y));
+            sum[k & 1] = add2(sum[k & 1], w);
+            hi[k] = pack_bf16(w.x, w.y);
+            if (PARTS == 1) continue;
+            float2 r = fma2(make_float2(bf_lo(hi[k]), bf_hi(hi[k])), minus, w);
+            lo[k] = pack_bf16(r.x, r.y);
+            if (PARTS == 3) {
+                r = fma2(make_float2(bf_lo(lo[k]), bf_hi(lo[k])), minus, r);
+                th[k] = pack_bf16(r.x, r.y);
             }
-            // P goes over the 16 scores that it was made from, part by part; the third part has the
-            // columns behind a step of 64
-            tmem_st8(s_addr + q * 32 + h * 16, hi);
-            if (PARTS >= 2) tmem_st8(s_addr + q * 32 + h * 16 + 8, lo);
-            if (PARTS == 3) tmem_st8(s_addr + 64 + q * 16 + h * 8, th);
         }
+        tmem_st8(p_addr + p_column<PARTS>(q, 0), hi);
+        if (PARTS >= 2) tmem_st8(p_addr + p_column<PARTS>(q, 1), lo);
+        if (PARTS == 3) tmem_st8(p_addr + p_column<PARTS>(q, 2), th);
     }
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// The 32 rows of HALF columns that a warp put into `stage` (piece c of row r at c ^ (r & 7)) to rows
+// The 32 rows of COLS columns that a warp put into `stage` (piece c of row r at stage_piece) to rows
 // `at` of each lane (negative: none) of out, `pitch` apart; neighbouring lanes on neighbouring
 // addresses (each thread storing its own row took 4 us for a tile).
-template <int HALF>
-__device__ __forceinline__ void store_rows(const uint8_t* stage, float* out, int pitch, long long at) {
-    constexpr int HP = HALF / 4;
+template <int COLS>
+__device__ __forceinline__ int stage_piece(int row, int c) {
+    return row * (COLS / 4) + (c ^ (row & (COLS / 4 - 1)));
+}
+
+template <int COLS>
+__device__ __forceinline__ void store_rows(const float4* stage, float* out, int pitch, long long at) {
+    constexpr int PIECES = COLS / 4;
     const int lane = threadIdx.x & 31;
     __syncwarp();
 #pragma unroll 4
-    for (int e = lane; e < 32 * HP; e += 32) {
-        const int row = e / HP, c = e % HP;
+    for (int e = lane; e < 32 * PIECES; e += 32) {
+        const int row = e / PIECES, c = e % PIECES;
         const long long to = __shfl_sync(0xffffffffu, at, row);
-        const float4 v = *reinterpret_cast<const float4*>(stage + row * (HALF * 4) + ((c ^ (row & 7)) << 4));
+        const float4 v = stage[stage_piece<COLS>(row, c)];
         if (to >= 0) *reinterpret_cast<float4*>(out + to * pitch + c * 4) = v;
     }
     __syncwarp();
 }
 
-// Where a count of K and V stages lies in the ring.
+// Where a count of stages (chunks) lies in the ring.
 template <int NS>
 struct RingPos {
     int slot;
@@ -481,34 +488,33 @@ struct RingPos {
     }
 };
 
-// KEYS: keys of a step, 128 (bf16 output, P in one or two bf16 parts) or 64 (fp32 output, three).
-template <int D, int KEYS>
+template <int D>
 struct PrefixCfg {
     static constexpr int kTileBytes = 128 * D * 2;  // one Q tile
-    static constexpr int kStage = KEYS * D * 2;     // K or V of a step
-    static constexpr int kStages = std::min(12, (224 * 1024 - 2 * kTileBytes) / kStage);
+    static constexpr int kStage = 2 * 64 * D * 2;   // a chunk: per half row, K's 64 rows and then V's
+    static constexpr int kV = 64 * 128;             // V behind K
+    static constexpr int kStages = (224 * 1024 - 2 * kTileBytes) / kStage;
     // copies of a CTA that have not landed yet: enough for the memory system's latency; more only
     // queue in it and hold up everything else that comes that way
-    static constexpr int kInFlight = std::min(kStages, 96 * 1024 / kStage);
+    static constexpr int kInFlight = 96 * 1024 / kStage;
     static constexpr int kSmem = 2 * kTileBytes + kStages * kStage + 1024;
 };
 
-template <int D, int KEYS>
+// F32: fp32 output, P in three bf16 parts, which leave S no columns of its own.
+template <int D, bool F32>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const PrefixParams p, const __grid_constant__ PrefixMaps maps) {
-    using C = PrefixCfg<D, KEYS>;
+    using C = PrefixCfg<D>;
     constexpr int NS = C::kStages;
-    constexpr int SMAX = KEYS / 64;  // chunks of a whole step
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     uint8_t* ring = smem + 2 * C::kTileBytes;
-    __shared__ uint64_t full[NS], empty[NS], s_full[2], p_ready[2], pv_done[2], go;
+    __shared__ uint64_t full[NS], empty[NS], s_full[2], s_free[2], p_ready[2][2], pv_done[2][2];
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_flag;
     __shared__ PrefixUnit unit;
-    __shared__ int member[256];
-    // (m, l) of a row in each stream, where the streams share one Q tile: in the other's memory
-    float2(*ex)[128] = reinterpret_cast<float2(*)[128]>(smem + C::kTileBytes);
+    // the tile's requests, in the ring: K and V come in once their rows are known
+    int* member = reinterpret_cast<int*>(ring);
     volatile int* abort = &abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dep_launch();  // the pass over the own caches fills SMs as they become free
@@ -519,11 +525,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 2);
         }
-        mbar_init(&go, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
-            mbar_init(&p_ready[s], 4);
-            mbar_init(&pv_done[s], 1);
+            mbar_init(&s_free[s], 4);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&p_ready[s][b], 4);
+                mbar_init(&pv_done[s][b], 1);
+            }
         }
         fence_mbar_init();
     }
@@ -536,10 +544,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     if (warp == 0) asm volatile("bar.arrive 5, %0;" ::"n"(kPrefixThreads) : "memory");
     else prefix_bar<5, kPrefixThreads>();
     tc_fence_after();
-    // TMEM columns: S (and P over it) of the two streams at 0 and 128, O at 256 and 256 + D
-    int it0 = 0;              // K and V stages used by earlier units
-    int used[2] = {0, 0};     // steps each stream did in earlier units
-    int paired = 0;           // earlier units with two row tiles
+    // TMEM columns: stream s has S at 128 s, P behind it (one part: two buffers of 32 columns; two parts:
+    // one of 64; three: over S and behind it) and O at 256 + D s
+    int it0 = 0;  // stages used by earlier units
+    int used[2] = {0, 0}, filled[2][2] = {{0, 0}, {0, 0}};  // steps of a stream, and of each of its P buffers
     for (int u = blockIdx.x;; u += gridDim.x) {
         if (warp == 0) plan_unit(p, u, reinterpret_cast<int4*>(smem), &unit, member);
         __syncthreads();
@@ -547,46 +555,47 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const uint32_t tmem = tmem_sh;
         const PrefixUnit x = unit;
         if (x.units == 0) break;
-        const int steps = (x.c1 - x.c0 + SMAX - 1) / SMAX;
-        // bf16 parts of P. With two row tiles the products and the softmax set the pace, not K and V:
-        // one part, as in dak_attn (its rounding stays below that of a bf16 output); with one the
-        // second part's products are free.
-        const int parts = KEYS == 64 ? 3 : x.two ? 1 : 2;
-        const int items = x.two ? 2 * steps : steps;  // item i: stream i & 1, step i / 2 or i
+        // Steps are chunks. Two row tiles: both streams take every step; one: they take turns.
+        // P has one bf16 part where two row tiles make the products and the softmax set the pace, not K
+        // and V (as in dak_attn: its rounding stays below that of a bf16 output); with one tile a
+        // second part's products are free. An fp32 output takes three.
+        const int steps = x.c1 - x.c0;
+        const int stride = x.two ? 1 : 2;
+        const int p_bufs = !F32 && x.two ? 2 : 1;
+        const auto p_begin = [&](int i) { return F32 ? 0 : 64 + (p_bufs == 2 ? (i & 1) * 32 : 0); };  // of P of a step i
+        // P buffer of a stream's step i of this unit, and the parity of its barriers' phase
+        const auto buf = [&](int i) { return p_bufs == 2 ? i & 1 : 0; };
+        const auto par = [&](int f0, int f1, int i) {
+            return static_cast<uint32_t>((buf(i) ? f1 : f0) + (p_bufs == 2 ? i >> 1 : i)) & 1u;
+        };
         const long long slab = static_cast<long long>(x.f) * p.Hkv + x.g;
         const int tier = slab < p.h_s ? 0 : 1;
-        const int step_of_shift = x.two ? 1 : 0;
+
         if (warp == 8) {
             // ------------------------------------------------------------ copies
-            prefix_bar<4, 288>();  // Q's loads are on their way, ahead of the stream of K and V
+            prefix_bar<4, kSoftmaxThreads + 32>();  // Q's loads are on their way, ahead of the stream of K and V
             if (lane == 0) {
-                const uint64_t policy = policy_evict_first();
-                const auto wait_landed = [&](int i) {
-                    return mbar_wait(&full[i % NS], static_cast<uint32_t>((i / NS) & 1), abort, p.st, DAK_ERR_TIMEOUT,
-                                     X_PROD_FULL);
-                };
-                const int chunk0 = static_cast<int>((tier ? slab - p.h_s : slab) * p.slab_chunks);
-                int it = it0;
-                for (int j = 0; j < steps; ++j) {
-                    const int c = x.c0 + j * SMAX, nk = min(SMAX, x.c1 - c);
-                    const CUtensorMap* map = nk == SMAX ? &maps.step[tier] : &maps.tail[tier];
-                    for (int kv = 0; kv < 2; ++kv, ++it) {
-                        const int s = it % NS;
-                        if (it >= NS && !mbar_wait(&empty[s], static_cast<uint32_t>((it / NS - 1) & 1), abort, p.st,
-                                                   DAK_ERR_TIMEOUT, X_PROD_EMPTY)) {
-                            goto copies_done;
-                        }
-                        if (it >= it0 + C::kInFlight && !wait_landed(it - C::kInFlight)) goto copies_done;
-                        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nk * 64 * D * 2));
-                        tma_load_5d(ring + static_cast<size_t>(s) * C::kStage, map, kv, chunk0 + c, &full[s], policy);
+                const uint64_t policy = x.shared ? policy_evict_last() : policy_evict_first();
+                const int chunk0 = static_cast<int>((tier ? slab - p.h_s : slab) * p.slab_chunks) + x.c0;
+                RingPos<NS> pos(it0), landed(it0);
+                int i = 0;
+                bool ok = true;
+                for (; i < steps; ++i) {
+                    if (it0 + i >= NS) ok = wait_phase(&empty[pos.slot], pos.phase ^ 1u, abort, p.st, X_PROD_EMPTY);
+                    if (ok && i >= C::kInFlight) {
+                        ok = wait_phase(&full[landed.slot], landed.phase, abort, p.st, X_PROD_FULL);
+                        landed.advance(1);
                     }
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&full[pos.slot], C::kStage);
+                    tma_load_chunk(ring + pos.slot * C::kStage, &maps.tier[tier], chunk0 + i, &full[pos.slot], policy);
+                    pos.advance(1);
                 }
-            copies_done:
-                if (*abort) {  // copies in flight land before the CTA may leave
+                if (!ok) {  // copies in flight land before the CTA may leave
                     volatile int dummy = 0;
-                    for (int s = 0; s < NS && s < it; ++s) {
-                        const int last = ((it - 1 - s) / NS) * NS + s;
-                        mbar_wait(&full[s], static_cast<uint32_t>((last / NS) & 1), &dummy, p.st, DAK_ERR_TIMEOUT, X_DRAIN);
+                    for (int k = max(0, i - C::kInFlight); k < i; ++k) {
+                        const RingPos<NS> r(it0 + k);
+                        wait_phase(&full[r.slot], r.phase, &dummy, p.st, X_DRAIN);
                     }
                 }
             }
@@ -594,187 +603,200 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         } else if (warp >= 9) {
             // ------------------------------------------------------------ products, a warp per stream
             // The whole warp runs the loop, so that its state and the descriptors stay warp-uniform;
-            // one elected lane issues. With one warp for both streams, what lies between the products
-            // (waits, address arithmetic) added up: 2.6k cycles a step of both at 1.5k of products.
-            const int st = warp - 9, stride = x.two ? 1 : 2;
-            prefix_bar<2, 320>();  // Q lies in shared memory
+            // one elected lane issues.
+            const int st = warp - 9;
+            prefix_bar<2, kSoftmaxThreads + 64>();  // Q lies in shared memory
             tc_fence_after();
             const bool leader = elect_one();
             const uint32_t q_addr = smem_u32(smem) + (x.two ? st * C::kTileBytes : 0), ring_addr = smem_u32(ring);
             const uint32_t s_tmem = tmem + st * 128, o_tmem = tmem + 256 + st * D;
-            int j = x.two ? 0 : st, n = used[st];
-            RingPos<NS> pos(it0 + 2 * j);  // K of step j; V follows
-            const auto wait_full = [&](RingPos<NS> r) {
-                return mbar_wait(&full[r.slot], r.phase, abort, p.st, DAK_ERR_TIMEOUT, X_MMA_FULL);
-            };
-            // a stage is free when both streams have used it, or the one that does has said so twice
-            const auto release = [&](int slot) {
-                umma_commit(&empty[slot]);
-                if (!x.two) umma_commit(&empty[slot]);
-            };
-            const auto qk = [&]() {
+            const int first = x.two ? 0 : st, mine = first < steps ? (steps - first + stride - 1) / stride : 0;
+            const int n0 = used[st], f0 = filled[st][0], f1 = filled[st][1];
+            RingPos<NS> kpos(it0 + first), vpos(it0 + first);
+            const auto qk = [&](int i) {  // S of this stream's step i
+                if (!wait_phase(&full[kpos.slot], kpos.phase, abort, p.st, X_MMA_FULL)) return false;
+                // S's columns are free: read, or with P over them read as P too
+                if (i > 0 && !(F32 ? wait_phase(&pv_done[st][0], par(f0, f1, i - 1), abort, p.st, X_MMA_PV)
+                                   : wait_phase(&s_free[st], (n0 + i - 1) & 1, abort, p.st, X_MMA_PV))) {
+                    return false;
+                }
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t b = ring_addr + pos.slot * C::kStage;
-                    issue_qk<D>(s_tmem, q_addr, b, min(SMAX, x.c1 - x.c0 - j * SMAX));
+                    issue_qk<D>(s_tmem, q_addr, ring_addr + kpos.slot * C::kStage);
                     umma_commit(&s_full[st]);
-                    release(pos.slot);
                 }
                 __syncwarp();
+                kpos.advance(stride);
+                return true;
             };
-            // Two row tiles: the second stream starts once the first one's softmax is done, so that from
-            // then on each one's softmax runs under the other's products (in step they waited for the
-            // tensor cores together and then left them idle together).
-            bool ok = j < steps && wait_full(pos);
-            if (ok && x.two && st == 1) ok = mbar_wait(&go, paired & 1, abort, p.st, DAK_ERR_TIMEOUT, X_MMA_GO);
-            if (ok) qk();
-            for (bool first = true; ok; first = false, ++n) {
-                RingPos<NS> v = pos;
-                v.advance(1);
-                ok = wait_full(v) && mbar_wait(&p_ready[st], n & 1, abort, p.st, DAK_ERR_TIMEOUT, X_MMA_P);
-                if (!ok) break;
-                if (first && x.two && st == 0 && lane == 0) mbar_arrive(&go);
+            bool ok = mine == 0 || qk(0);
+            for (int i = 0; i < mine && ok; ++i) {
+                if (!F32 && i + 1 < mine && !qk(i + 1)) break;
+                if (!wait_phase(&p_ready[st][buf(i)], par(f0, f1, i), abort, p.st, X_MMA_P)) break;
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t b = ring_addr + v.slot * C::kStage;
-                    issue_pv<D>(o_tmem, s_tmem, b, min(SMAX, x.c1 - x.c0 - j * SMAX), parts, !first);
-                    umma_commit(&pv_done[st]);
-                    release(v.slot);
+                    const uint32_t p_tmem = s_tmem + p_begin(i), v = ring_addr + vpos.slot * C::kStage + C::kV;
+                    if (F32) issue_pv<D, 3>(o_tmem, p_tmem, v, i > 0);
+                    else if (x.two) issue_pv<D, 1>(o_tmem, p_tmem, v, i > 0);
+                    else issue_pv<D, 2>(o_tmem, p_tmem, v, i > 0);
+                    umma_commit(&pv_done[st][buf(i)]);
+                    // a stage is free when both streams have used it, or the one that does has said so twice
+                    umma_commit(&empty[vpos.slot]);
+                    if (!x.two) umma_commit(&empty[vpos.slot]);
                 }
                 __syncwarp();
-                j += stride;
-                if (j >= steps) break;
-                pos.advance(2 * stride);
-                // S's columns hold the P that the product just issued reads: it finishes first
-                ok = wait_full(pos) && mbar_wait(&pv_done[st], n & 1, abort, p.st, DAK_ERR_TIMEOUT, X_MMA_PV);
-                if (ok) qk();
+                vpos.advance(stride);
+                if (F32 && i + 1 < mine) ok = qk(i + 1);
             }
             __syncwarp();
-        } else if (warp < 8) {
-            // ------------------------------------------------------------ softmax, one row a thread
-            const int st = warp >> 2, r = (warp & 3) * 32 + lane;
+        } else {
+            // ------------------------------------------------------------ softmax, a thread a row
+            const int st = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
             const int mpt = p.mpt;
-            {   // Q rows into the 128-byte swizzled K-major layout, rows without a member zero
-                constexpr int PIECES = D / 8;  // 16-byte pieces of a row
-                const int n = (x.two ? 256 : 128) * PIECES;
-#pragma unroll 1
-                for (int e = threadIdx.x; e < n; e += 256) {
-                    const int rr = (e / PIECES) & 127, tile = e / (128 * PIECES), c = e % PIECES, m = rr / p.G;
-                    const bool there = m < mpt && tile * mpt + m < x.members;
-                    const __nv_bfloat16* src = p.Q + c * 8;
-                    if (there) src += (static_cast<long long>(member[tile * mpt + m]) * p.Hq + x.g * p.G + rr - m * p.G) * D;
-                    cp_async16(smem + tile * C::kTileBytes + (c >> 3) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), src,
-                               there ? 16 : 0);
-                }
-                asm volatile("bar.arrive 4, 288;" ::: "memory");  // K and V may start behind these copies
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                fence_proxy_async_smem();
-                prefix_bar<2, 320>();
-            }
-            const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-            const uint32_t s_addr = tmem + lanes + st * 128, o_addr = tmem + lanes + 256 + st * D;
-            float m_ref = -INFINITY, l = 0.f;
-            bool ok = true;
-            int mine = 0;
-            for (int i = st; i < items; i += 2, ++mine) {
-                const int j = i >> step_of_shift;
-                const int k0 = (x.c0 + j * SMAX) * 64;  // first key of the step
-                const int nk = min(SMAX, x.c1 - x.c0 - j * SMAX), valid = min(64 * nk, x.len - k0);
-                ok = mbar_wait(&s_full[st], static_cast<uint32_t>((used[st] + mine) & 1), abort, p.st, DAK_ERR_TIMEOUT,
-                               X_SM_S);
-                if (!__all_sync(0xffffffffu, ok)) {  // a wait ran out: the whole warp stops
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (valid < 64 * nk && (!x.two || st == 0)) {
-                    // rows of V past the prefix may hold anything, also infinities and NaN, which a
-                    // probability of zero would not cancel
-                    const int vit = it0 + 2 * j + 1;
-                    mbar_wait(&full[vit % NS], static_cast<uint32_t>((vit / NS) & 1), abort, p.st, DAK_ERR_TIMEOUT, X_SM_V);
-                    uint8_t* v = ring + static_cast<size_t>(vit % NS) * C::kStage;
-                    for (int e = r; e < (64 * nk - valid) * (D / 8); e += 128) {
-                        const int row = valid + e / (D / 8), c = e % (D / 8);
-                        *reinterpret_cast<uint4*>(v + (c >> 3) * (8192 * nk) + row * 128 + ((c & 7) << 4)) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (KEYS == 64) softmax_step<D, 3>(s_addr, o_addr, nk, valid, p.scale_log2, m_ref, l, mine == 0);
-                else if (x.two) softmax_step<D, 1>(s_addr, o_addr, nk, valid, p.scale_log2, m_ref, l, mine == 0);
-                else softmax_step<D, 2>(s_addr, o_addr, nk, valid, p.scale_log2, m_ref, l, mine == 0);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready[st]);
-            }
-            if (ok && mine > 0) {
-                mbar_wait(&pv_done[st], static_cast<uint32_t>((used[st] + mine - 1) & 1), abort, p.st, DAK_ERR_TIMEOUT,
-                          X_SM_O);
-            }
-            __syncwarp();
-            // ---- results: row r of this stream's tile, or of the tile that the streams share
+            // where row r of this stream's tile, or of the tile that the streams share, has its results
             const int tile = x.two ? st : 0, m = r / p.G;
             const bool valid_row = m < mpt && tile * mpt + m < x.members;
             long long at = 0;
             if (valid_row) {
                 at = (static_cast<long long>(member[tile * mpt + m]) * p.Hq + x.g * p.G + r - m * p.G) * p.n_pre + x.s;
             }
-            // half a row's columns at a time go through this stream's Q tile, which is free now
-            constexpr int HALF = D / 2;
-            uint8_t* stage = smem + st * C::kTileBytes + (warp & 3) * 32 * HALF * 4;
-            const auto put = [&](const float(&o)[16], int q) {  // 16 columns from q * 16 of the half
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    *reinterpret_cast<float4*>(stage + lane * (HALF * 4) + (((q * 4 + k) ^ (lane & 7)) << 4)) =
-                        make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                }
-            };
-            const auto flush = [&](int col) { store_rows<HALF>(stage, p.o_part + col, D, valid_row ? at : -1ll); };
-            if (x.two) {
-                tc_fence_after();
+            {   // Q rows into the 128-byte swizzled K-major layout, rows without a member zero
+                constexpr int PIECES = D / 8;  // 16-byte pieces of a row
+                const int n = (x.two ? 256 : 128) * PIECES;
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll 1
-                    for (int q = 0; q < HALF / 16; ++q) {
-                        float o[16];
-                        tmem_ld16(o_addr + h * HALF + q * 16, o);
-                        tmem_wait(o);
-                        put(o, q);
-                    }
-                    flush(h * HALF);
+                for (int e = threadIdx.x; e < n; e += kSoftmaxThreads) {
+                    const int rr = (e / PIECES) & 127, t = e / (128 * PIECES), c = e % PIECES, mm = rr / p.G;
+                    const bool there = mm < mpt && t * mpt + mm < x.members;
+                    const __nv_bfloat16* src = p.Q + c * 8;
+                    if (there) src += (static_cast<long long>(member[t * mpt + mm]) * p.Hq + x.g * p.G + rr - mm * p.G) * D;
+                    cp_async16(smem + t * C::kTileBytes + (c >> 3) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), src,
+                               there ? 16 : 0);
                 }
-                if (valid_row) p.ml_part[at] = make_float2(m_ref, l);
-            } else {
-                ex[st][r] = make_float2(m_ref, l);
-                tc_fence_before();
-                prefix_bar<3, 256>();
-                tc_fence_after();
-                const float2 e0 = ex[0][r], e1 = ex[1][r];
-                prefix_bar<3, 256>();  // ex lies in what is written next
-                const float M = fmaxf(e0.x, e1.x), base = M == -INFINITY ? 0.f : M;
-                const float f0 = exp2_ftz(e0.x - base), f1 = exp2_ftz(e1.x - base);
-                const bool both = items > 1;  // the second stream had a step
-#pragma unroll 1
-                for (int q = 0; q < HALF / 16; ++q) {  // stream 0 the first half of the columns
-                    float a[16], b[16];
-                    tmem_ld16(tmem + lanes + 256 + st * HALF + q * 16, a);
-                    tmem_ld16(tmem + lanes + 256 + D + st * HALF + q * 16, b);
-                    tmem_wait(a);
-                    tmem_wait(b);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) a[k] = both ? a[k] * f0 + b[k] * f1 : a[k] * f0;
-                    put(a, q);
-                }
-                flush(st * HALF);
-                if (valid_row && st == 0) p.ml_part[at] = make_float2(M, e0.y * f0 + (both ? e1.y * f1 : 0.f));
+                asm volatile("bar.arrive 4, %0;" ::"n"(kSoftmaxThreads + 32) : "memory");  // K and V may start behind these copies
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_proxy_async_smem();
+                prefix_bar<2, kSoftmaxThreads + 64>();
             }
+            const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+            const uint32_t s_addr = tmem + lanes + st * 128, o_addr = tmem + lanes + 256 + st * D;
+            const int n0 = used[st], f0 = filled[st][0], f1 = filled[st][1];
+            float m_ref = -INFINITY, l = 0.f;
+            bool ok = true;
+            int i = 0;
+            for (int j = x.two ? 0 : st; j < steps; j += stride, ++i) {
+                const int valid = min(64, x.len - (x.c0 + j) * 64);
+                ok = mbar_wait(&s_full[st], (n0 + i) & 1, abort, p.st, DAK_ERR_TIMEOUT, X_SM_S);
+                if (!__all_sync(0xffffffffu, ok)) {  // a wait ran out: the whole warp stops
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (valid < 64) {
+                    // Rows of V past the prefix may hold anything, also infinities and NaN, which a
+                    // probability of zero would not cancel. Both streams of a step clear them, as either
+                    // one's product may be first.
+                    // (The scores say that the chunk is there.)
+                    uint8_t* rows = ring + RingPos<NS>(it0 + j).slot * C::kStage + C::kV;
+                    for (int e = r; e < (64 - valid) * (D / 8); e += 128) {
+                        const int row = valid + e / (D / 8), c = e % (D / 8);
+                        *reinterpret_cast<uint4*>(rows + (c >> 3) * 16384 + row * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                const auto taken = [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_free[st]);
+                };
+                const auto done = [&](int k) {  // the product of this stream's step k
+                    mbar_wait(&pv_done[st][buf(k)], par(f0, f1, k), abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);
+                    __syncwarp();
+                    tc_fence_after();
+                };
+                // P's buffer is free; every product's end is waited for once and in order (a wait for one
+                // phase of a barrier says nothing while the phase before may be open)
+                const auto room = [&] {
+                    if (i >= p_bufs) done(i - p_bufs);
+                };
+                const auto grown = [&](float f) {  // O so far, its last product done, to the new reference
+                    if (p_bufs == 2 && i >= 2) done(i - 2);
+                    done(i - 1);
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        float o[16];
+                        tmem_ld16(o_addr + q * 16, o);
+                        tmem_wait(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] *= f;
+                        tmem_st16(o_addr + q * 16, o);
+                    }
+                };
+                const uint32_t p_addr = s_addr + p_begin(i);
+                if (F32) softmax_step<3>(s_addr, p_addr, valid, p.scale_log2, m_ref, l, i == 0, taken, grown, room);
+                else if (x.two) softmax_step<1>(s_addr, p_addr, valid, p.scale_log2, m_ref, l, i == 0, taken, grown, room);
+                else softmax_step<2>(s_addr, p_addr, valid, p.scale_log2, m_ref, l, i == 0, taken, grown, room);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[st][buf(i)]);
+            }
+            for (int k = max(0, i - p_bufs); ok && k < i; ++k) {
+                ok = mbar_wait(&pv_done[st][buf(k)], par(f0, f1, k), abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);
+            }
+            __syncwarp();
+            // ---- results
+            // Q's memory, no longer read, takes the streams' (m, l) where they share a tile, and then, half
+            // a row's columns at a time, the results on their way out.
+            constexpr int COLS = D / 2;
+            float M = m_ref, total = l, w0 = 1.f, w1 = 0.f;
+            const bool both = !x.two && steps > 1;  // the streams' rows are the same and both had a step
+            tc_fence_before();
+            if (!x.two) {
+                float2(*ex)[128] = reinterpret_cast<float2(*)[128]>(smem + C::kTileBytes);
+                ex[st][r] = make_float2(m_ref, l);
+                prefix_bar<3, kSoftmaxThreads>();
+                const float2 e0 = ex[0][r], e1 = ex[1][r];
+                prefix_bar<3, kSoftmaxThreads>();  // ex lies in what is written next
+                M = fmaxf(e0.x, e1.x);
+                const float base = M == -INFINITY ? 0.f : M;
+                w0 = exp2_ftz(e0.x - base);
+                w1 = both ? exp2_ftz(e1.x - base) : 0.f;
+                total = w0 * e0.y + (both ? w1 * e1.y : 0.f);
+            }
+            tc_fence_after();
+            float4* stage = reinterpret_cast<float4*>(smem + st * C::kTileBytes + quad * 32 * COLS * 4);
+#pragma unroll 1
+            for (int col = x.two ? 0 : st * COLS; col < (x.two ? D : (st + 1) * COLS); col += COLS) {
+#pragma unroll 1
+                for (int q = 0; q < COLS / 16; ++q) {
+                    float o[16];
+                    tmem_ld16(tmem + lanes + 256 + (x.two ? st * D : 0) + col + q * 16, o);
+                    tmem_wait(o);
+                    if (!x.two) {
+                        float b[16];
+                        tmem_ld16(tmem + lanes + 256 + D + col + q * 16, b);
+                        tmem_wait(b);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = both ? o[k] * w0 + b[k] * w1 : o[k] * w0;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        stage[stage_piece<COLS>(lane, q * 4 + k)] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                }
+                store_rows<COLS>(stage, p.o_part + col, D, valid_row ? at : -1ll);
+            }
+            if (valid_row && (x.two || st == 0)) p.ml_part[at] = make_float2(M, total);
         }
-        it0 += 2 * steps;
-        used[0] += (items + 1) / 2;
-        used[1] += items / 2;
-        paired += x.two;
+        it0 += steps;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            const int n = x.two ? steps : (steps + 1 - st) / 2;
+            used[st] += n;
+            filled[st][0] += p_bufs == 2 ? (n + 1) / 2 : n;
+            filled[st][1] += p_bufs == 2 ? n / 2 : 0;
+        }
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
@@ -788,14 +810,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     }
 }
 
-// The prefix's chunks of one tier as the kernel copies them, nk chunks at a time.
-static bool make_prefix_map(CUtensorMap* map, const void* base, int64_t chunks, int D, int nk) {
+// The prefix's chunks of one tier as the kernel copies them: (64 elements, 64 tokens, K and V, chunk,
+// half of a row).
+static bool make_prefix_map(CUtensorMap* map, const void* base, int64_t chunks, int D) {
     const auto enc = encode_fn();
     if (!enc || fault_due(DAK_FAULT_TENSOR_MAP)) return false;
     const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
     const cuuint64_t dims[5] = {64, 64, 2, static_cast<cuuint64_t>(chunks), static_cast<cuuint64_t>(D / 64)};
     const cuuint64_t strides[4] = {row, 64 * row, 128 * row, 128};
-    const cuuint32_t box[5] = {64, 64, 1, static_cast<cuuint32_t>(nk), static_cast<cuuint32_t>(D / 64)};
+    const cuuint32_t box[5] = {64, 64, 2, 1, static_cast<cuuint32_t>(D / 64)};
     const cuuint32_t one[5] = {1, 1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, one,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -807,19 +830,19 @@ int prefix_max_ranges(const dak_placement* P) {
     return std::max(1, std::min(device_sm_count() / P->H_kv, (chunks + kPrefixMinChunks - 1) / kPrefixMinChunks));
 }
 
-template <int D, int KEYS>
+template <int D, bool F32>
 static cudaError_t launch_prefix_d(const PrefixParams& p, const PrefixMaps& maps, int grid, cudaStream_t s) {
-    auto k = prefix_kernel<D, KEYS>;
+    auto k = prefix_kernel<D, F32>;
     static SmemLimit limit;
-    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(k), PrefixCfg<D, KEYS>::kSmem);
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(k), PrefixCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
-    k<<<grid, kPrefixThreads, PrefixCfg<D, KEYS>::kSmem, s>>>(p, maps);
+    k<<<grid, kPrefixThreads, PrefixCfg<D>::kSmem, s>>>(p, maps);
     return cudaGetLastError();
 }
 
 dak_status launch_prefix(const void* Q, const dak_placement* P, const int* lens, const int* of, int B, int H_q,
                          float scale_log2, int o_fp32, float* o_part, float* ml_part, int* n_ranges, cudaStream_t s) {
-    const int D = P->D, keys = o_fp32 ? 64 : 128;
+    const int D = P->D;
     PrefixParams p{};
     p.Q = static_cast<const __nv_bfloat16*>(Q);
     p.lens = lens;
@@ -846,10 +869,7 @@ dak_status launch_prefix(const void* Q, const dak_placement* P, const int* lens,
         const int64_t n = tier ? slabs - P->h_s : P->h_s;
         const void* base = tier ? P->hbm_ptr : P->host_dev;
         if (n == 0) continue;
-        if (!make_prefix_map(&maps.step[tier], base, n * p.slab_chunks, D, keys / 64) ||
-            !make_prefix_map(&maps.tail[tier], base, n * p.slab_chunks, D, 1)) {
-            return DAK_ERR_CUDA;
-        }
+        if (!make_prefix_map(&maps.tier[tier], base, n * p.slab_chunks, D)) return DAK_ERR_CUDA;
     }
     // no more CTAs than units can come out: every tile with members in every range
     const int per_tile = 2 * (128 / p.G);
@@ -857,9 +877,9 @@ dak_status launch_prefix(const void* Q, const dak_placement* P, const int* lens,
     const int grid = static_cast<int>(std::min<int64_t>(device_sm_count(), tiles * p.Hkv * p.n_pre));
     cudaError_t e;
     if (D == 128) {
-        e = o_fp32 ? launch_prefix_d<128, 64>(p, maps, grid, s) : launch_prefix_d<128, 128>(p, maps, grid, s);
+        e = o_fp32 ? launch_prefix_d<128, true>(p, maps, grid, s) : launch_prefix_d<128, false>(p, maps, grid, s);
     } else {
-        e = o_fp32 ? launch_prefix_d<64, 64>(p, maps, grid, s) : launch_prefix_d<64, 128>(p, maps, grid, s);
+        e = o_fp32 ? launch_prefix_d<64, true>(p, maps, grid, s) : launch_prefix_d<64, false>(p, maps, grid, s);
     }
     return cuda_status(e);
 }
