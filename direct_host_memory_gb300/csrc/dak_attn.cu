@@ -28,7 +28,6 @@
 // brings a whole stage; inside every token row the 16-byte piece c sits at c ^ (token & 7)
 // so that ldmatrix reads of 8 consecutive tokens hit 8 different bank groups.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include "dak_device.cuh"
@@ -52,12 +51,6 @@ struct AttnParams {
     // host-link handoff of a decode step (link_wait / link_signal; null = off)
     unsigned* link;
     unsigned link_after;
-    // attn_kernel<.., EXT>: partials are always written; scores, if not null, takes every
-    // scaled score (log2 domain) [B][Hq][score_pitch]
-    float* scores;
-    int score_pitch;
-    int deal;       // units dealt round the CTAs of a tier, empty ones skipped
-    int wait_late;  // the previous kernel is the call's prefix pass: only this grid's end waits for it
 };
 
 constexpr int kChunkTok = 64;
@@ -67,24 +60,12 @@ constexpr int kAttnThreads = 32 * (1 + kAttnConsumers);
 struct UnitRange {
     int tier;
     long long begin, end;  // global unit indices
-    int step;
     int window;
 };
 
 __device__ __forceinline__ UnitRange units_of_cta(const AttnParams& p) {
     UnitRange u;
     const int b = blockIdx.x;
-    u.step = 1;
-    if (p.deal) {
-        // EXT: the splits of a slab go to different CTAs, so that ragged lengths even out
-        const bool host = b < p.n_host_ctas;
-        u.tier = host ? 0 : 1;
-        u.step = host ? p.n_host_ctas : p.n_hbm_ctas;
-        u.begin = host ? b : p.host_units + b - p.n_host_ctas;
-        u.end = p.host_units + (host ? 0 : p.hbm_units);
-        u.window = host ? p.host_window : p.hbm_window;
-        return u;
-    }
     if (b < p.n_host_ctas) {
         u.tier = 0;
         u.begin = p.host_units * b / p.n_host_ctas;
@@ -142,21 +123,11 @@ __device__ __forceinline__ void split_bf16(float v0, float v1, uint32_t& hi, uin
     lo = pack_bf16(v0 - __bfloat162float(h0), v1 - __bfloat162float(h1));
 }
 
-// The bf16 pair of what hi and lo of split_bf16 leave of two fp32 values.
-__device__ __forceinline__ uint32_t third_bf16(float v0, float v1, uint32_t hi, uint32_t lo) {
-    return pack_bf16(v0 - bf_lo(hi) - bf_lo(lo), v1 - bf_hi(hi) - bf_hi(lo));
-}
-
-// Mask of a bf16 pair of which the first n elements count.
-__device__ __forceinline__ uint32_t pair_mask(int n) { return n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u; }
-
 __device__ __forceinline__ void named_bar_consumers() {
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttnConsumers) : "memory");
 }
 
-// PARTS: bf16 parts of P that enter P.V. EXT: the pass over the own caches of dak_attn_acc and
-// dak_attn_prefix, which leaves partials for their merge (attn_merge_kernel) and may keep scores.
-template <int D, int PARTS, bool EXT>
+template <int D, bool SPLIT_P>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
     constexpr int KS = D / 16;                       // k-steps of the score MMA
     constexpr int NB = D / 8;                        // 8-wide column blocks of O
@@ -190,7 +161,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
             if (link) link_wait(p.link, p.link_after, p.st);
             long long i = 0;
             bool waited = false;
-            for (long long u = ur.begin; u < ur.end && !*abort; u += EXT ? ur.step : 1) {
+            for (long long u = ur.begin; u < ur.end && !*abort; ++u) {
                 const Unit x = decode_unit(p, u, ur.tier);
                 for (int t = x.t0; t < x.t1; t += kChunkTok, ++i) {
                     const int s = static_cast<int>(i % W);
@@ -221,16 +192,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     // ---------------------------------------------------------------- consumers
     // Q (and the outputs) may belong to the previous kernel of the stream; the KV cache
     // streamed above is, with programmatic launch, taken to be written earlier than that
-    if (!EXT || !p.wait_late) grid_dep_wait();
+    grid_dep_wait();
     const int w = warp - 1;
     const int q4 = lane & 3;      // column pair within an 8-wide block
     const int ra = lane >> 2;     // MMA row of c0/c1 (c2/c3: ra + 8)
     const int mi = lane >> 3, rr = lane & 7;  // ldmatrix: matrix index, row within it
     long long i = 0;
     bool failed = false;  // a wait ran out: skip the math but keep meeting the named barriers
-    for (long long u = ur.begin; u < ur.end; u += EXT ? ur.step : 1) {
+    for (long long u = ur.begin; u < ur.end; ++u) {
         const Unit x = decode_unit(p, u, ur.tier);
-        if (EXT && x.t0 >= x.t1) continue;
         // Q fragments (A operand), rows >= G are zero
         uint32_t qa[KS][4];
         {
@@ -288,22 +258,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                         mx_b = fmaxf(mx_b, sc[nb][2 + e]);
                     }
                 }
-                if (EXT && p.scores) {
-                    // tokens past the valid ones hold -inf and lie inside the padded row
-                    float* row = p.scores + (static_cast<long long>(x.b) * p.Hq + static_cast<long long>(x.g) * p.G) *
-                                                p.score_pitch + t + 16 * w + 2 * q4;
-#pragma unroll
-                    for (int nb = 0; nb < 2; ++nb) {
-                        if (ra < p.G) {
-                            *reinterpret_cast<float2*>(row + static_cast<long long>(ra) * p.score_pitch + nb * 8) =
-                                make_float2(sc[nb][0], sc[nb][1]);
-                        }
-                        if (ra + 8 < p.G) {
-                            *reinterpret_cast<float2*>(row + static_cast<long long>(ra + 8) * p.score_pitch + nb * 8) =
-                                make_float2(sc[nb][2], sc[nb][3]);
-                        }
-                    }
-                }
                 mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 1));
                 mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 2));
                 mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 1));
@@ -335,21 +289,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                     o[nb][2] *= corr_b;
                     o[nb][3] *= corr_b;
                 }
-                // P as the A operand (16 rows x 16 tokens): hi = bf16(P), with two parts also
-                // lo = bf16(P - hi) and with three bf16(P - hi - lo), all multiplied into the
-                // same accumulators
+                // P as the A operand (16 rows x 16 tokens): hi = bf16(P), and with SPLIT_P also
+                // lo = bf16(P - hi), both multiplied into the same accumulators
                 uint32_t pa0, pa1, pa2, pa3, pl0, pl1, pl2, pl3;
-                uint32_t pt0 = 0, pt1 = 0, pt2 = 0, pt3 = 0;
                 split_bf16(pr[0][0], pr[0][1], pa0, pl0);
                 split_bf16(pr[0][2], pr[0][3], pa1, pl1);
                 split_bf16(pr[1][0], pr[1][1], pa2, pl2);
                 split_bf16(pr[1][2], pr[1][3], pa3, pl3);
-                if (PARTS == 3) {
-                    pt0 = third_bf16(pr[0][0], pr[0][1], pa0, pl0);
-                    pt1 = third_bf16(pr[0][2], pr[0][3], pa1, pl1);
-                    pt2 = third_bf16(pr[1][0], pr[1][1], pa2, pl2);
-                    pt3 = third_bf16(pr[1][2], pr[1][3], pa3, pl3);
-                }
                 // ---- O += P V
                 {
                     const int tok = 16 * w + (mi & 1) * 8 + rr;
@@ -359,24 +305,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                         const uint32_t addr = vs_base + static_cast<uint32_t>(tok * D * 2 + ((c ^ (tok & 7)) << 4));
                         uint32_t b0, b1, b2, b3;
                         ldsm_x4_t(addr, b0, b1, b2, b3);
-                        if (EXT && valid < 16) {
-                            // rows past the valid tokens may hold anything, also infinities and
-                            // NaN, which a probability of zero would not cancel
-                            const uint32_t lo = pair_mask(valid - 2 * q4), hi = pair_mask(valid - 8 - 2 * q4);
-                            b0 &= lo;
-                            b1 &= hi;
-                            b2 &= lo;
-                            b3 &= hi;
-                        }
                         mma_bf16_16816(o[2 * db], pa0, pa1, pa2, pa3, b0, b1);
                         mma_bf16_16816(o[2 * db + 1], pa0, pa1, pa2, pa3, b2, b3);
-                        if (PARTS >= 2) {
+                        if (SPLIT_P) {
                             mma_bf16_16816(o[2 * db], pl0, pl1, pl2, pl3, b0, b1);
                             mma_bf16_16816(o[2 * db + 1], pl0, pl1, pl2, pl3, b2, b3);
-                        }
-                        if (PARTS == 3) {
-                            mma_bf16_16816(o[2 * db], pt0, pt1, pt2, pt3, b0, b1);
-                            mma_bf16_16816(o[2 * db + 1], pt0, pt1, pt2, pt3, b2, b3);
                         }
                     }
                 }
@@ -432,7 +365,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                 lsum += f * row[D + 1];
             }
             const long long orow = static_cast<long long>(x.b) * p.Hq + static_cast<long long>(x.g) * p.G + r;
-            if (!EXT && p.n_split == 1) {
+            if (p.n_split == 1) {
                 store_out(p.O, p.o_fp32, orow * D + d, lsum > 0.f ? acc / lsum : 0.f);
             } else {
                 float* wr = p.ws + (orow * p.n_split + x.s) * (D + 2);
@@ -445,8 +378,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         }
         named_bar_consumers();  // comb is rewritten by the next unit
     }
-    // this grid's end stands for the prefix pass's too
-    if (EXT && p.wait_late) grid_dep_wait();
 }
 
 // Merge the context splits of every (request, query head) row in split order:
@@ -550,134 +481,6 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_cta_kernel(const
     }
 }
 
-// Merge of dak_attn_acc and dak_attn_prefix: the partials of the own cache's n_own splits and of
-// the prefix's ranges, in that order, into O as attn_combine does, and the accumulated weights
-// acc_out = acc_in + sum_r 2^(s_r - M_r) / l_r from the scores s that the own pass left. Block
-// (b, g) x y: the first ones merge a query head a warp, later ones take kMergePositions positions
-// of the slab each. Splits behind a request's tokens have no partials.
-struct MergeParams {
-    const float* own;  // [B][Hq][n_own][D + 2]
-    int n_own, split_len;
-    // prefix pass (launch_prefix); n_pre 0: none
-    const float* pre_o;
-    const float2* pre_ml;
-    const int* n_ranges;  // [B]
-    const int* prefix_of;
-    const int* prefix_lens;
-    int n_pre, n_prefix, prefix_L;
-    void* O;
-    int o_fp32;
-    const float* scores;  // [B][Hq][score_pitch], log2 domain
-    int score_pitch;
-    const float* acc_in;  // [B][Hkv][L] or null
-    float* acc_out;       // null: no accumulation
-    const int* seq_lens;
-    int Hq, Hkv, G, L;
-};
-constexpr int kMergeThreads = 128;
-constexpr int kMergeWarps = kMergeThreads / 32;
-constexpr int kMergePositions = 512;
-
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const MergeParams p) {
-    constexpr int V = D / 32;  // columns of a lane
-    grid_dep_wait();
-    const int b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int L = p.seq_lens ? min(max(p.seq_lens[b], 0), p.L) : p.L;
-    const int o_blocks = (p.G + kMergeWarps - 1) / kMergeWarps;
-    const int j0 = (static_cast<int>(blockIdx.y) - o_blocks) * kMergePositions;
-    if (j0 >= L) return;
-    int n_pre = 0;
-    if (p.n_pre > 0) {
-        const int f = p.prefix_of ? p.prefix_of[b] : 0;
-        if (f >= 0 && f < p.n_prefix && (p.prefix_lens ? p.prefix_lens[f] : p.prefix_L) > 0) n_pre = p.n_ranges[b];
-    }
-    const int n_own = (L + p.split_len - 1) / p.split_len, n = n_own + n_pre;
-    const long long row0 = static_cast<long long>(b) * p.Hq + static_cast<long long>(g) * p.G;
-    const auto ml = [&](long long row, int s) {
-        if (s >= n_own) return p.pre_ml[row * p.n_pre + s - n_own];
-        return *reinterpret_cast<const float2*>(p.own + (row * p.n_own + s) * (D + 2) + D);
-    };
-    // maximum and denominator of a row, on every lane of its warp
-    const auto total = [&](long long row) {
-        float M = -INFINITY, l = 0.f;
-        for (int s = lane; s < n; s += 32) M = fmaxf(M, ml(row, s).x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float base = M == -INFINITY ? 0.f : M;
-        for (int s = lane; s < n; s += 32) {
-            const float2 v = ml(row, s);
-            l += exp2f(v.x - base) * v.y;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        return make_float2(base, l);
-    };
-    if (static_cast<int>(blockIdx.y) < o_blocks) {  // a warp per query head
-        const int r = static_cast<int>(blockIdx.y) * kMergeWarps + warp;
-        if (r >= p.G) return;
-        const long long row = row0 + r;
-        const float2 t = total(row);
-        float acc[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = 0.f;
-        for (int s0 = 0; s0 < n; s0 += 32) {
-            const float f = s0 + lane < n ? exp2f(ml(row, s0 + lane).x - t.x) : 0.f;
-            const int m = min(32, n - s0);
-#pragma unroll 8
-            for (int k = 0; k < m; ++k) {
-                const int s = s0 + k;
-                const float w = __shfl_sync(0xffffffffu, f, k);
-                const float* o = s < n_own ? p.own + (row * p.n_own + s) * (D + 2)
-                                           : p.pre_o + (row * p.n_pre + s - n_own) * D;
-#pragma unroll
-                for (int c = 0; c < V; c += 2) {  // the own partials' rows are 8-byte aligned
-                    const float2 v = *reinterpret_cast<const float2*>(o + (c >> 1) * 64 + lane * 2);
-                    acc[c] += w * v.x;
-                    acc[c + 1] += w * v.y;
-                }
-            }
-        }
-        const float inv = t.y > 0.f ? 1.f / t.y : 0.f;
-#pragma unroll
-        for (int c = 0; c < V; c += 2) {
-            const long long at = row * D + (c >> 1) * 64 + lane * 2;
-            store_out(p.O, p.o_fp32, at, acc[c] * inv);
-            store_out(p.O, p.o_fp32, at + 1, acc[c + 1] * inv);
-        }
-        return;
-    }
-    __shared__ float2 rows[16];  // maximum, 1 / denominator
-    for (int r = warp; r < p.G; r += kMergeWarps) {
-        const float2 t = total(row0 + r);
-        if (lane == 0) rows[r] = make_float2(t.x, t.y > 0.f ? 1.f / t.y : 0.f);
-    }
-    __syncthreads();
-    const long long slab = static_cast<long long>(blockIdx.x) * p.L;
-    const float* sc = p.scores + row0 * p.score_pitch;
-    float w[kMergePositions / kMergeThreads];
-#pragma unroll
-    for (int k = 0; k < kMergePositions / kMergeThreads; ++k) {
-        const int j = j0 + tid + k * kMergeThreads;
-        w[k] = p.acc_in && j < L ? p.acc_in[slab + j] : 0.f;
-    }
-    float add[kMergePositions / kMergeThreads] = {};
-    for (int r = 0; r < p.G; ++r) {
-        const float2 t = rows[r];
-#pragma unroll
-        for (int k = 0; k < kMergePositions / kMergeThreads; ++k) {
-            const int j = j0 + tid + k * kMergeThreads;
-            if (j < L) add[k] += exp2f(sc[static_cast<long long>(r) * p.score_pitch + j] - t.x) * t.y;
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < kMergePositions / kMergeThreads; ++k) {
-        const int j = j0 + tid + k * kMergeThreads;
-        if (j < L) p.acc_out[slab + j] = w[k] + add[k];
-    }
-}
-
 constexpr int kAttnDefaultHostCtas = 32;
 constexpr int kAttnDefaultHostWindow = 4;
 // Default ring depth: 2 stages (64 KiB in flight per CTA; three CTAs fit on an SM). Measured
@@ -710,18 +513,14 @@ static int attn_smem_bytes(int W, int G) {
 // copies, so two per SM double the copy streams an SM keeps in flight).
 template <int D>
 static int attn_ctas_per_sm(int W, int G) {
-    static std::atomic<int> known[kAttnMaxStages + 1][17];  // 0 = not asked yet
-    int n = known[W][G].load(std::memory_order_relaxed);
-    if (n) return n;
+    int n = 0;
     const int smem = attn_smem_bytes<D>(W, G);
-    if (cudaFuncSetAttribute(attn_kernel<D, 1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<D, 1, false>, kAttnThreads, smem) != cudaSuccess) {
+    if (cudaFuncSetAttribute(attn_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<D, false>, kAttnThreads, smem) != cudaSuccess) {
         cudaGetLastError();
         return 1;
     }
-    n = std::max(1, n);
-    known[W][G].store(n, std::memory_order_relaxed);
-    return n;
+    return std::max(1, n);
 }
 
 // Launch with or without programmatic dependent launch (the kernel may start while the
@@ -742,21 +541,10 @@ static cudaError_t launch_maybe_pdl(Kernel k, int grid, int threads, int smem, b
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
-// The own-cache pass of dak_attn_acc / dak_attn_prefix: partials only.
-template <int D>
-static cudaError_t launch_attn_ext_d(const AttnParams& p, int grid, int W, bool pdl, cudaStream_t s) {
-    const int smem = attn_smem_bytes<D>(W, p.G);
-    static SmemLimit limit[2];
-    auto k = p.o_fp32 ? attn_kernel<D, 3, true> : attn_kernel<D, 2, true>;
-    const cudaError_t e =
-        limit[p.o_fp32 ? 1 : 0].raise(reinterpret_cast<const void*>(k), attn_smem_bytes<D>(kAttnMaxStages, 16));
-    return e == cudaSuccess ? launch_maybe_pdl(k, grid, kAttnThreads, smem, pdl, s, p) : e;
-}
-
 template <int D>
 static cudaError_t launch_attn_d(const AttnParams& p, int grid, int W, bool pdl, cudaStream_t s) {
     const int smem = attn_smem_bytes<D>(W, p.G);
-    auto k = p.o_fp32 ? attn_kernel<D, 2, false> : attn_kernel<D, 1, false>;
+    auto k = p.o_fp32 ? attn_kernel<D, true> : attn_kernel<D, false>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     e = launch_maybe_pdl(k, grid, kAttnThreads, smem, pdl, s, p);
@@ -770,22 +558,9 @@ static cudaError_t launch_attn_d(const AttnParams& p, int grid, int W, bool pdl,
                             static_cast<const float*>(p.ws), p.O, p.o_fp32, p.n_split);
 }
 
-static int split_tokens(int L, int n_split) {
-    return ((L + n_split - 1) / n_split + kChunkTok - 1) / kChunkTok * kChunkTok;
-}
-
-// ext: the own-cache pass of dak_attn_acc / dak_attn_prefix (partials into ws, scores), with a
-// workspace that the caller has checked.
-struct AttnExt {
-    float* scores = nullptr;
-    int score_pitch = 0;
-    bool after_prefix = false;
-};
-
 static dak_status launch_attn_kernels(const void* Q, const dak_placement* KV, const void* host_src,
                                       const int* seq_lens, int H_q, float scale, void* O, void* ws, size_t ws_bytes,
-                                      const dak_tuning* t, cudaStream_t stream, int o_fp32, const LinkHandoff* link,
-                                      const AttnExt* ext = nullptr) {
+                                      const dak_tuning* t, cudaStream_t stream, int o_fp32, const LinkHandoff* link) {
     if (link && link->signals) *link->signals = 0;
     if (!KV || KV->kind != 1 || !Q || !O) return DAK_ERR_INVALID;
     if (H_q <= 0 || H_q % KV->H_kv) return DAK_ERR_INVALID;
@@ -817,7 +592,7 @@ static dak_status launch_attn_kernels(const void* Q, const dak_placement* KV, co
     p.L = KV->L;
     p.h_s = KV->h_s;
     p.n_split = n_split;
-    p.split_len = split_tokens(KV->L, n_split);
+    p.split_len = ((KV->L + n_split - 1) / n_split + kChunkTok - 1) / kChunkTok * kChunkTok;
     const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(KV->D));
     p.scale_log2 = sc * 1.4426950408889634f;
     p.head_bytes = KV->head_bytes;
@@ -851,18 +626,7 @@ static dak_status launch_attn_kernels(const void* Q, const dak_placement* KV, co
         p.link = link->ctr;
         p.link_after = link->after;
     }
-    cudaError_t e;
-    if (ext) {
-        p.scores = ext->scores;
-        p.score_pitch = ext->score_pitch;
-        p.deal = 1;
-        p.wait_late = ext->after_prefix;
-        const bool pdl = (t && t->pdl > 0) || ext->after_prefix;
-        e = KV->D == 128 ? launch_attn_ext_d<128>(p, grid, W, pdl, stream)
-                         : launch_attn_ext_d<64>(p, grid, W, pdl, stream);
-    } else {
-        e = KV->D == 128 ? launch_attn_d<128>(p, grid, W, pdl, stream) : launch_attn_d<64>(p, grid, W, pdl, stream);
-    }
+    cudaError_t e = KV->D == 128 ? launch_attn_d<128>(p, grid, W, pdl, stream) : launch_attn_d<64>(p, grid, W, pdl, stream);
     if (e == cudaSuccess && link && link->signals && p.link) *link->signals = p.n_host_ctas;
     return cuda_status(e);
 }
@@ -882,131 +646,6 @@ dak_status launch_attn(const void* Q, const dak_placement* KV, const void* host_
         launch_attn_kernels(Q, KV, host_src, seq_lens, H_q, scale, O, ws, ws_bytes, t, stream, o_fp32, link);
     if (joined && r == DAK_OK) link_commit(t, own_signals);
     return r;
-}
-
-// The passes of dak_attn_acc (P null) and dak_attn_prefix. Workspace: the own pass's partials,
-// the prefix pass's (o, then maxima and sums, then the ranges' counts) and the scores, each
-// rounded up to 256 bytes.
-struct ExtLayout {
-    int n_own, n_pre, score_pitch;
-    size_t own_bytes, pre_o_bytes, pre_ml_bytes, ranges_bytes, score_bytes;
-    size_t total() const { return own_bytes + pre_o_bytes + pre_ml_bytes + ranges_bytes + score_bytes; }
-};
-
-// Splits of a cache for the passes that deal units round the CTAs: at most 256 tokens each, so that
-// requests of different lengths fill the SMs alike (the partials are 2% of the cache's bytes), and
-// more where default_split fills the SMs better.
-constexpr int kExtSplitTokens = 256;
-static int ext_default_split(int B, int Hkv, int L) {
-    return std::min(kMaxSplits, std::max(default_split(B, Hkv, L), (L + kExtSplitTokens - 1) / kExtSplitTokens));
-}
-
-static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-
-static ExtLayout ext_layout(const dak_placement* KV, const dak_placement* P, int H_q, int n_split, bool with_acc) {
-    ExtLayout x{};
-    const size_t rows = static_cast<size_t>(KV->B) * H_q;
-    x.n_own = n_split > 0 ? n_split : ext_default_split(KV->B, KV->H_kv, KV->L);
-    x.n_pre = P ? prefix_max_ranges(P) : 0;
-    x.own_bytes = round256(rows * x.n_own * (KV->D + 2) * sizeof(float));
-    x.pre_o_bytes = round256(rows * x.n_pre * KV->D * sizeof(float));
-    x.pre_ml_bytes = round256(rows * x.n_pre * sizeof(float2));
-    x.ranges_bytes = P ? round256(static_cast<size_t>(KV->B) * sizeof(int)) : 0;
-    x.score_pitch = (KV->L + kChunkTok - 1) / kChunkTok * kChunkTok;
-    x.score_bytes = with_acc ? round256(rows * x.score_pitch * sizeof(float)) : 0;
-    return x;
-}
-
-// Partial overlap of two arrays of n elements (the same array twice is none).
-static bool partly_overlaps(const void* a, const void* b, size_t bytes) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x != y && x < y + bytes && y < x + bytes;
-}
-
-static dak_status launch_attn_ext(const void* Q, const dak_placement* KV, const int* seq_lens, const dak_placement* P,
-                                  const int* prefix_lens, const int* prefix_of, int H_q, float scale, void* O,
-                                  int o_fp32, const float* acc_in, float* acc_out, void* ws, size_t ws_bytes,
-                                  const dak_tuning* t, cudaStream_t stream, const LinkHandoff* link) {
-    if (!KV || KV->kind != 1 || !Q || !O || H_q <= 0 || H_q % KV->H_kv) return DAK_ERR_INVALID;
-    if (H_q / KV->H_kv > 16) return DAK_ERR_UNSUPPORTED;
-    if (P && (P->kind != 1 || P->D != KV->D || P->H_kv != KV->H_kv || P->device != KV->device)) return DAK_ERR_INVALID;
-    if (P && P->B > kMaxPrefixes) return DAK_ERR_UNSUPPORTED;
-    if (t && t->n_split > kMaxSplits) return DAK_ERR_INVALID;
-    if (acc_out && acc_in &&
-        partly_overlaps(acc_in, acc_out, static_cast<size_t>(KV->B) * KV->H_kv * KV->L * sizeof(float))) {
-        return DAK_ERR_INVALID;
-    }
-    if ((reinterpret_cast<uintptr_t>(Q) & 15) || (reinterpret_cast<uintptr_t>(O) & 15) ||
-        (reinterpret_cast<uintptr_t>(ws) & 15) || (reinterpret_cast<uintptr_t>(acc_in) & 3) ||
-        (reinterpret_cast<uintptr_t>(acc_out) & 3)) {
-        return DAK_ERR_ALIGN;
-    }
-    const ExtLayout x = ext_layout(KV, P, H_q, t ? t->n_split : 0, acc_out != nullptr);
-    if (!ws || ws_bytes < x.total()) return DAK_ERR_INVALID;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return DAK_ERR_CUDA;
-    if (dev != KV->device) return DAK_ERR_INVALID;
-    uint8_t* w = static_cast<uint8_t*>(ws);
-    const auto take = [&](size_t bytes) {
-        uint8_t* at = w;
-        w += bytes;
-        return at;
-    };
-    MergeParams m{};
-    float* own = reinterpret_cast<float*>(take(x.own_bytes));
-    float* pre_o = reinterpret_cast<float*>(take(x.pre_o_bytes));
-    float* pre_ml = reinterpret_cast<float*>(take(x.pre_ml_bytes));
-    int* n_ranges = reinterpret_cast<int*>(take(x.ranges_bytes));
-    AttnExt ext;
-    ext.scores = acc_out ? reinterpret_cast<float*>(w) : nullptr;
-    ext.score_pitch = x.score_pitch;
-    if (P) {
-        const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(KV->D));
-        const dak_status r = launch_prefix(Q, P, prefix_lens, prefix_of, KV->B, H_q, sc * 1.4426950408889634f, o_fp32,
-                                           pre_o, pre_ml, n_ranges, stream);
-        if (r != DAK_OK) return r;
-        m.pre_o = pre_o;
-        m.pre_ml = reinterpret_cast<const float2*>(pre_ml);
-        m.n_ranges = n_ranges;
-        m.prefix_of = prefix_of;
-        m.prefix_lens = prefix_lens;
-        m.n_pre = x.n_pre;
-        m.n_prefix = P->B;
-        m.prefix_L = P->L;
-    }
-    dak_tuning tun = t ? *t : dak_tuning{};
-    tun.n_split = x.n_own;
-    ext.after_prefix = P != nullptr;
-    const dak_status r = launch_attn_kernels(Q, KV, KV->host_dev, seq_lens, H_q, scale, O, own, x.own_bytes, &tun, stream,
-                                             o_fp32, link, &ext);
-    if (r != DAK_OK) return r;
-    m.own = own;
-    m.n_own = x.n_own;
-    m.O = O;
-    m.o_fp32 = o_fp32 ? 1 : 0;
-    m.scores = ext.scores;
-    m.score_pitch = x.score_pitch;
-    m.acc_in = acc_in;
-    m.acc_out = acc_out;
-    m.seq_lens = seq_lens;
-    m.Hq = H_q;
-    m.Hkv = KV->H_kv;
-    m.G = H_q / KV->H_kv;
-    m.L = KV->L;
-    m.split_len = split_tokens(KV->L, x.n_own);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(KV->B) * KV->H_kv,
-                       static_cast<unsigned>((m.G + kMergeWarps - 1) / kMergeWarps +
-                                             (acc_out ? (KV->L + kMergePositions - 1) / kMergePositions : 0)));
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cuda_status(KV->D == 128 ? cudaLaunchKernelEx(&cfg, attn_merge_kernel<128>, m)
-                                    : cudaLaunchKernelEx(&cfg, attn_merge_kernel<64>, m));
 }
 
 }  // namespace dak
@@ -1043,39 +682,4 @@ extern "C" dak_status dak_attn_staged(const void* Q, const dak_placement* KV, co
     if (reinterpret_cast<uintptr_t>(staging) & 15) return DAK_ERR_ALIGN;
     return dak::launch_attn(Q, KV, staging, seq_lens, H_q, scale, O, workspace, ws_bytes, tuning,
                             static_cast<cudaStream_t>(stream));
-}
-
-extern "C" size_t dak_attn_acc_workspace_bytes(const dak_placement* KV, int H_q, int n_split) {
-    if (!KV || KV->kind != 1 || H_q <= 0 || H_q % KV->H_kv || n_split > dak::kMaxSplits) return 0;
-    return dak::ext_layout(KV, nullptr, H_q, n_split, true).total();
-}
-
-extern "C" dak_status dak_attn_acc(const void* Q, const dak_placement* KV, const int* seq_lens, int H_q, float scale,
-                                   void* O, int o_fp32, const float* acc_in, float* acc_out, void* workspace,
-                                   size_t ws_bytes, const dak_tuning* tuning, void* stream) {
-    if (!acc_out) return DAK_ERR_INVALID;
-    dak::LinkHandoff lk;
-    int signals = 0;
-    const bool joined = dak::link_join(tuning, &lk);
-    if (joined) lk.signals = &signals;
-    const dak_status r =
-        dak::launch_attn_ext(Q, KV, seq_lens, nullptr, nullptr, nullptr, H_q, scale, O, o_fp32, acc_in, acc_out,
-                             workspace, ws_bytes, tuning, static_cast<cudaStream_t>(stream), joined ? &lk : nullptr);
-    if (joined && r == DAK_OK) dak::link_commit(tuning, signals);
-    return r;
-}
-
-extern "C" size_t dak_attn_prefix_workspace_bytes(const dak_placement* KV, const dak_placement* P, int H_q,
-                                                  int n_split, int with_acc) {
-    if (!KV || KV->kind != 1 || !P || P->kind != 1 || H_q <= 0 || H_q % KV->H_kv || n_split > dak::kMaxSplits) return 0;
-    return dak::ext_layout(KV, P, H_q, n_split, with_acc != 0).total();
-}
-
-extern "C" dak_status dak_attn_prefix(const void* Q, const dak_placement* KV, const int* seq_lens,
-                                      const dak_placement* P, const int* prefix_lens, const int* prefix_of, int H_q,
-                                      float scale, void* O, int o_fp32, const float* acc_in, float* acc_out,
-                                      void* workspace, size_t ws_bytes, const dak_tuning* tuning, void* stream) {
-    if (!P) return DAK_ERR_INVALID;
-    return dak::launch_attn_ext(Q, KV, seq_lens, P, prefix_lens, prefix_of, H_q, scale, O, o_fp32, acc_in, acc_out,
-                                workspace, ws_bytes, tuning, static_cast<cudaStream_t>(stream), nullptr);
 }

@@ -1,6 +1,6 @@
 // The prefix pass of dak_attn_prefix: attention of all requests that share a prefix over the
 // prefix's rows, each (prefix, kv head) slab streamed once for up to 256 query rows (a row = one
-// request's query head). Partial results go to the merge of dak_attn.cu.
+// request's query head). Partial results go to the merge of dak_serve.cu.
 //
 // The contraction is GEMM-shaped (rows x keys x D twice), so it runs on the tcgen05 tensor cores
 // as the usual two products with an online softmax between them, 64 keys a step:
@@ -131,12 +131,6 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // 16 bytes global -> shared, `bytes` (16 or 0) of them from src and zeros for the rest.
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ float exp2_ftz(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // Two fp32 operations in one instruction.
@@ -827,7 +821,7 @@ static bool make_prefix_map(CUtensorMap* map, const void* base, int64_t chunks, 
 
 int prefix_max_ranges(const dak_placement* P) {
     const int chunks = (P->L + 63) / 64;
-    return std::max(1, std::min(device_sm_count() / P->H_kv, (chunks + kPrefixMinChunks - 1) / kPrefixMinChunks));
+    return std::max(1, std::min(std::min(device_sm_count(), 256) / P->H_kv, (chunks + kPrefixMinChunks - 1) / kPrefixMinChunks));
 }
 
 template <int D, bool F32>
