@@ -39,111 +39,169 @@ __device__ __forceinline__ float load_elem(const void* p, long long i) {
     return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
 
-// Eight consecutive elements at i (16-byte aligned in bf16, 32 bytes in fp32).
+// Eight consecutive elements at i as they lie in memory (16-byte aligned), and as fp32.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, long long i, float (&x)[8]) {
-    if (F32) {
-        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        const float4 a = s[0], b = s[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
-        x[0] = bf_lo(a.x), x[1] = bf_hi(a.x), x[2] = bf_lo(a.y), x[3] = bf_hi(a.y);
-        x[4] = bf_lo(a.z), x[5] = bf_hi(a.z), x[6] = bf_lo(a.w), x[7] = bf_hi(a.w);
+struct Piece;
+template <>
+struct Piece<false> {
+    uint4 v;
+    __device__ __forceinline__ void load(const void* p, long long i) {
+        v = ld_nc_v4(static_cast<const __nv_bfloat16*>(p) + i);
     }
-}
+    __device__ __forceinline__ void get(float* x) const {
+        x[0] = bf_lo(v.x), x[1] = bf_hi(v.x), x[2] = bf_lo(v.y), x[3] = bf_hi(v.y);
+        x[4] = bf_lo(v.z), x[5] = bf_hi(v.z), x[6] = bf_lo(v.w), x[7] = bf_hi(v.w);
+    }
+};
+template <>
+struct Piece<true> {
+    uint4 v[2];
+    __device__ __forceinline__ void load(const void* p, long long i) {
+        v[0] = ld_nc_v4(static_cast<const float*>(p) + i);
+        v[1] = ld_nc_v4(static_cast<const float*>(p) + i + 4);
+    }
+    __device__ __forceinline__ void get(float* x) const {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            x[4 * k] = __uint_as_float(v[k].x), x[4 * k + 1] = __uint_as_float(v[k].y);
+            x[4 * k + 2] = __uint_as_float(v[k].z), x[4 * k + 3] = __uint_as_float(v[k].w);
+        }
+    }
+};
 
-__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
+__device__ __forceinline__ uint4 pack8(const float* y) {
     return make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
 }
 
-// One block per (token, share of its heads). The first threads turn the position into the
-// pairs' cos and sin: position x turns modulo 2^64 is the angle as a binary fraction of a
-// turn, exact at any distance; its upper 32 bits, signed, are half-turns * 2^-31. Then each
-// thread makes one 16-byte piece of one head's output row. Memory bound: every element is read
-// and written once (a pair's partner comes from the L1 line that the neighbour loads).
-template <int D, bool F32>
-__global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int PIECES = D / 8;
+// One block per token (or a share of its heads, where tokens are few). A thread's unit is a pair of
+// 16-byte output pieces: of a query or key head the two that hold the same pairs' halves, or where
+// pairs do not lie so (interleaved, a share of pieces that turn, halves not of whole pieces) and in
+// value heads two pieces side by side. Its inputs are asked for first; the position, its angles and
+// the table of cos and sin come under those loads. Position x turns modulo 2^64 is the angle as a
+// binary fraction of a turn, exact at any distance; its upper 32 bits, signed, are half-turns *
+// 2^-31. Memory bound: every element is read and written once.
+enum { kRopeSplit = 0, kRopeInterleaved = 1, kRopePart = 2 };  // PART: halves of a part of the head
+
+template <int D, bool F32, int KIND>
+__global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8) append_rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int PAIRS = D / 16;  // units of a head
+    constexpr int PER = 3;         // units in flight per thread (a token of the 8B shape: all of them)
     __shared__ float2 cs[D / 2];
     const int b = blockIdx.x / p.T, t = blockIdx.x - b * p.T;
-    if (p.n_new && t >= p.n_new[b]) return;
-    const int R = p.rope.rot_dim, half = R / 2;
-    const long long row = static_cast<long long>(p.slots[b]) + t;
-    const long long pos = p.positions ? static_cast<long long>(p.positions[b]) + t : row;
-    if (static_cast<int>(threadIdx.x) < half) {
-        const uint64_t turn = static_cast<uint64_t>(pos) * p.rope.turns[threadIdx.x];
-        const float x = static_cast<float>(static_cast<int>(static_cast<uint32_t>(turn >> 32))) * 0x1p-31f;
-        float s, c;
-        sincospif(x, &s, &c);
-        cs[threadIdx.x] = make_float2(c * p.rope.scale, s * p.rope.scale);
-    }
-    __syncthreads();
-    const bool in_range = row >= 0 && row < p.L;
-    if (!in_range && blockIdx.y == 0 && threadIdx.x == 0) {
-        report(p.st, DAK_ERR_BOUNDS, 0xA9901000ull << 32 | static_cast<unsigned>(b));
-    }
     const long long token = blockIdx.x;
-    const int heads = p.Hq + 2 * p.Hkv;
-    for (int task = blockIdx.y * kRopeThreads + threadIdx.x; task < heads * PIECES; task += gridDim.y * kRopeThreads) {
-        const int h = task / PIECES, c = task - h * PIECES;
-        const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-        if (!is_q && !in_range) continue;
-        const int g = is_q ? h : is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-        const void* src = is_q ? p.q : is_v ? p.v : p.k;
-        const long long at = token * (is_q ? p.q_pitch : is_v ? p.v_pitch : p.k_pitch) + g * D;
-        const int e0 = c * 8;
-        float x[8], y[8];
-        load8<F32>(src, at + e0, x);
-        if (is_v || e0 >= R) {
+    const int R = p.rope.rot_dim, half = R / 2;
+    const int heads = p.Hq + 2 * p.Hkv, n_units = heads * PAIRS, stride = gridDim.y * kRopeThreads;
+    const int n_new = p.n_new ? p.n_new[b] : p.T, slot = p.slots[b], first = p.positions ? p.positions[b] : slot;
+    bool ready = false, in_range = false;
+    long long row = 0, pos = 0;
+    for (int u0 = blockIdx.y * kRopeThreads + threadIdx.x; u0 - static_cast<int>(threadIdx.x) < n_units; u0 += PER * stride) {
+        Piece<F32> raw[PER][2];
+        // unit u: its head, where its pieces begin in it
+        const auto place = [&](int u, int& h, int& e0, int& e1, bool& is_q, bool& is_v, int& g) {
+            h = u / PAIRS;
+            is_q = h < p.Hq;
+            is_v = h >= p.Hq + p.Hkv;
+            g = is_q ? h : is_v ? h - p.Hq - p.Hkv : h - p.Hq;
+            const int c = u - h * PAIRS;
+            const bool apart = KIND == kRopeSplit && !is_v;
+            e0 = apart ? c * 8 : c * 16;
+            e1 = apart ? e0 + D / 2 : e0 + 8;
+        };
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[i];
-        } else if (p.rope.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                if (e0 + i < R) {
-                    const float2 f = cs[(e0 + i) >> 1];
-                    y[i] = x[i] * f.x - x[i + 1] * f.y;
-                    y[i + 1] = x[i + 1] * f.x + x[i] * f.y;
-                } else {
-                    y[i] = x[i];
-                    y[i + 1] = x[i + 1];
-                }
-            }
-        } else if ((half & 7) == 0) {
-            const bool low = e0 < half;
-            float o[8];
-            load8<F32>(src, at + (low ? e0 + half : e0 - half), o);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f = cs[(low ? e0 : e0 - half) + i];
-                y[i] = low ? x[i] * f.x - o[i] * f.y : x[i] * f.x + o[i] * f.y;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int e = e0 + i;
-                if (e < half) {
-                    y[i] = x[i] * cs[e].x - load_elem<F32>(src, at + e + half) * cs[e].y;
-                } else if (e < R) {
-                    y[i] = x[i] * cs[e - half].x + load_elem<F32>(src, at + e - half) * cs[e - half].y;
-                } else {
-                    y[i] = x[i];
-                }
-            }
+        for (int k = 0; k < PER; ++k) {
+            const int u = u0 + k * stride;
+            if (u >= n_units) continue;
+            int h, e0, e1, g;
+            bool is_q, is_v;
+            place(u, h, e0, e1, is_q, is_v, g);
+            const void* src = is_q ? p.q : is_v ? p.v : p.k;
+            const long long at = token * (is_q ? p.q_pitch : is_v ? p.v_pitch : p.k_pitch) + static_cast<long long>(g) * D;
+            raw[k][0].load(src, at + e0);
+            raw[k][1].load(src, at + e1);
         }
-        const uint4 out = pack8(y);
-        if (is_q) {
-            *reinterpret_cast<uint4*>(p.q_out + (token * p.Hq + h) * D + e0) = out;
-        } else {
-            const long long slab = static_cast<long long>(b) * p.Hkv + g;
-            uint4* base =
-                reinterpret_cast<uint4*>(slab < p.h_s ? p.host + slab * p.head_bytes : p.hbm + (slab - p.h_s) * p.head_bytes);
-            base[(row >> 6) * (2 * 64 * PIECES) + (is_v ? 64 * PIECES : 0) + (row & 63) * PIECES + (c ^ (row & 7))] = out;
-            if (p.slot_pos && !is_v && c == 0) p.slot_pos[slab * p.L + row] = static_cast<int>(pos);
+        if (!ready) {
+            if (t >= n_new) return;
+            row = static_cast<long long>(slot) + t;
+            pos = static_cast<long long>(first) + t;
+            in_range = row >= 0 && row < p.L;
+            if (static_cast<int>(threadIdx.x) < half) {
+                const uint64_t turn = static_cast<uint64_t>(pos) * p.rope.turns[threadIdx.x];
+                const float a = static_cast<float>(static_cast<int>(static_cast<uint32_t>(turn >> 32))) * 0x1p-31f;
+                float s, c;
+                sincospif(a, &s, &c);
+                cs[threadIdx.x] = make_float2(c * p.rope.scale, s * p.rope.scale);
+            }
+            if (!in_range && blockIdx.y == 0 && threadIdx.x == 0) {
+                report(p.st, DAK_ERR_BOUNDS, 0xA9901000ull << 32 | static_cast<unsigned>(b));
+            }
+            __syncthreads();
+            ready = true;
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int u = u0 + k * stride;
+            if (u >= n_units) continue;
+            int h, e0, e1, g;
+            bool is_q, is_v;
+            place(u, h, e0, e1, is_q, is_v, g);
+            if (!is_q && !in_range) continue;
+            float x[16];
+            raw[k][0].get(x);
+            raw[k][1].get(x + 8);
+            if (!is_v) {
+                if (KIND == kRopeSplit) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 f = cs[e0 + i];
+                        const float a = x[i], c = x[8 + i];
+                        x[i] = a * f.x - c * f.y;
+                        x[8 + i] = c * f.x + a * f.y;
+                    }
+                } else if (KIND == kRopeInterleaved) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        if (e0 + i >= R) continue;
+                        const float2 f = cs[(e0 + i) >> 1];
+                        const float a = x[i], c = x[i + 1];
+                        x[i] = a * f.x - c * f.y;
+                        x[i + 1] = c * f.x + a * f.y;
+                    }
+                } else {  // a pair's other half by a load of its own
+                    const void* src = is_q ? p.q : p.k;
+                    const long long at = token * (is_q ? p.q_pitch : p.k_pitch) + static_cast<long long>(g) * D;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int e = e0 + i;
+                        if (e >= R) continue;
+                        const float2 f = cs[e < half ? e : e - half];
+                        const float o = load_elem<F32>(src, at + (e < half ? e + half : e - half));
+                        x[i] = x[i] * f.x + (e < half ? -o : o) * f.y;
+                    }
+                }
+            }
+            const uint4 y0 = pack8(x), y1 = pack8(x + 8);
+            if (is_q) {
+                __nv_bfloat16* out = p.q_out + (token * p.Hq + h) * D;
+                *reinterpret_cast<uint4*>(out + e0) = y0;
+                *reinterpret_cast<uint4*>(out + e1) = y1;
+            } else {
+                const long long slab = static_cast<long long>(b) * p.Hkv + g;
+                uint4* base =
+                    reinterpret_cast<uint4*>(slab < p.h_s ? p.host + slab * p.head_bytes : p.hbm + (slab - p.h_s) * p.head_bytes);
+                base += (row >> 6) * (16 * D) + (is_v ? 8 * D : 0) + (row & 63) * (D / 8);
+                base[(e0 >> 3) ^ (row & 7)] = y0;
+                base[(e1 >> 3) ^ (row & 7)] = y1;
+                if (p.slot_pos && !is_v && e0 == 0) p.slot_pos[slab * p.L + row] = static_cast<int>(pos);
+            }
         }
     }
+}
+
+template <int D, bool F32>
+static void launch_append_rope(const RopeParams& p, dim3 grid, cudaStream_t s) {
+    if (p.rope.interleaved) append_rope_kernel<D, F32, kRopeInterleaved><<<grid, kRopeThreads, 0, s>>>(p);
+    else if (p.rope.rot_dim == D) append_rope_kernel<D, F32, kRopeSplit><<<grid, kRopeThreads, 0, s>>>(p);
+    else append_rope_kernel<D, F32, kRopePart><<<grid, kRopeThreads, 0, s>>>(p);
 }
 
 // ------------------------------------------------------------------------------------
@@ -334,15 +392,15 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
                  gridDim.y * kMoveThreads);
 }
 
-// The eviction of one slab by a cluster of 1 to 8 CTAs, the slots' weights and positions in
-// registers: CTA c holds slots [c, c + 1) * 1024 R, thread t the slots r * 1024 + t of them. Reading
-// the tables costs one pass; everything after is counting:
+// The eviction of one slab by a cluster of 1 to 8 CTAs, the slots' keys in registers: CTA c holds slots
+// [c, c + 1) * 1024 R, thread t the slots r * 1024 + t of them. Reading the tables costs one pass;
+// everything after is counting:
 //   newest position -> key of every slot (evict_key) -> the n_keep-th largest key by a radix select
-//   (11, 11 and 10 bits, histograms in shared memory added up over the cluster) -> kept slots (at
-//   the threshold key the lowest ones) -> ranks of holes and movers -> lists, tables, and with MOVE
-//   the rows themselves.
+//   (11, 11 and 10 bits, histograms in shared memory, of the whole cluster added up by every CTA) ->
+//   kept slots (at the threshold key the lowest ones) -> ranks of holes and movers -> lists, tables,
+//   and with MOVE the rows themselves.
 // Ranks in slot order: ballots per (r, warp), whose counts are scanned in that order, offset by the
-// cluster's earlier CTAs.
+// cluster's earlier CTAs. What one CTA needs of each other one, the lanes of a warp read at once.
 constexpr int kClusterThreads = 1024;
 constexpr int kEvictMaxCluster = 8;
 constexpr int kEvictMaxSlots = kEvictMaxCluster * kClusterThreads * 16;
@@ -354,17 +412,26 @@ __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
     return v;
 }
 
-template <int D, int R, bool MOVE>
-__global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictParams p, const int cluster) {
+__device__ __forceinline__ int2 ld_cluster2(const int* p, uint32_t rank) {
+    int2 v;
+    asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+                 : "=r"(v.x), "=r"(v.y)
+                 : "r"(mapa_shared(smem_u32(p), rank))
+                 : "memory");
+    return v;
+}
+
+template <int D, int R, bool CLUSTER, bool MOVE>
+__global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictParams p, const int n_cluster) {
     constexpr int NW = kClusterThreads / 32;
     constexpr int ENTRIES = R * NW;  // (r, warp) pairs
-    __shared__ int hist[3][kBins];
+    __shared__ __align__(8) int hist[3][kBins];
     __shared__ int cnt[ENTRIES];
     __shared__ int wsum[NW];
     __shared__ int share[4];  // read by the cluster: newest position, equals, holes and movers
     __shared__ int pick[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int cluster = CLUSTER ? n_cluster : 1, rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
     const long long slab = blockIdx.x / cluster;
     const int b = static_cast<int>(slab / p.Hkv), g = static_cast<int>(slab - static_cast<long long>(b) * p.Hkv);
     const int n = min(max(p.seq_lens[b], 0), p.L), keep = p.n_keep;
@@ -375,10 +442,12 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
     int* src = p.src_out ? p.src_out + slab * keep : nullptr;
     const bool copy = p.acc_out != p.acc, copy_pos = p.pos_out != p.pos;
     const int s0 = rank * R * kClusterThreads + tid;  // slot of r: s0 + r * 1024
-    const auto sync = [&] {
-        if (cluster > 1) cluster_sync_all();
+    const auto sync = [] {
+        if (CLUSTER) cluster_sync_all();
         else __syncthreads();
     };
+    // the `what` of every CTA of the cluster, CTA c's on lane c
+    const auto of_cluster = [&](const int* what, int none) { return lane < cluster ? ld_cluster(what, lane) : none; };
     grid_dep_launch();
     if (g == 0 && rank == 0 && tid == 0) p.lens_out[b] = min(n, keep);
     if (n <= keep) {
@@ -392,32 +461,36 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
         if (rank == 0 && tid == 0) p.n_moves[slab] = 0;
         return;
     }
-    float w[R];
-    int q[R];
-    int newest = INT_MIN;
+    uint32_t key[R];
+    {
+        float w[R];
+        int q[R];
+        int newest = INT_MIN;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int i = s0 + r * kClusterThreads;
-        w[r] = i < n ? acc[i] : 0.f;
-        q[r] = i < n ? pos[i] : INT_MIN;
-        newest = max(newest, q[r]);
+        for (int r = 0; r < R; ++r) {
+            const int i = s0 + r * kClusterThreads;
+            w[r] = i < n ? acc[i] : 0.f;
+            q[r] = i < n ? pos[i] : INT_MIN;
+            newest = max(newest, q[r]);
+        }
+        for (int i = tid; i < 3 * kBins; i += kClusterThreads) {
+            (&hist[0][0])[i] = 0;
+        }
+        newest = __reduce_max_sync(0xffffffffu, newest);
+        if (lane == 0) wsum[warp] = newest;
+        __syncthreads();
+        newest = __reduce_max_sync(0xffffffffu, wsum[lane]);
+        if (CLUSTER) {
+            if (tid == 0) share[0] = newest;
+            sync();
+            newest = __reduce_max_sync(0xffffffffu, of_cluster(&share[0], INT_MIN));
+        }
+        // protected: a position above newest - n_recent (which may lie below every int32)
+        const bool every = static_cast<long long>(newest) - p.n_recent < INT_MIN;
+        const int oldest = every ? INT_MIN : newest - p.n_recent;
+#pragma unroll
+        for (int r = 0; r < R; ++r) key[r] = evict_key(w[r], every || q[r] > oldest);
     }
-    for (int i = tid; i < 3 * kBins; i += kClusterThreads) (&hist[0][0])[i] = 0;
-    newest = __reduce_max_sync(0xffffffffu, newest);
-    if (lane == 0) wsum[warp] = newest;
-    __syncthreads();
-    if (warp == 0) {
-        const int m = __reduce_max_sync(0xffffffffu, wsum[lane]);
-        if (lane == 0) share[0] = m;
-    }
-    sync();
-    newest = share[0];
-    for (int c = 0; c < cluster; ++c) {
-        if (c != rank) newest = max(newest, ld_cluster(&share[0], c));
-    }
-    // a position above `oldest` is protected; in 64 bits, as positions may be any int32
-    const long long oldest = static_cast<long long>(newest) - p.n_recent;
-    const auto key_of = [&](int r) { return evict_key(w[r], q[r] > oldest); };
     uint32_t prefix = 0;  // leading bits of the threshold key
     int want = keep;      // how many of the keys that share them are kept
 #pragma unroll
@@ -426,19 +499,30 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
         const uint32_t digits = pass == 2 ? 1023u : 2047u;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint32_t k = key_of(r);
-            if (s0 + r * kClusterThreads < n && (pass == 0 || (k >> above) == (prefix >> above))) {
-                atomicAdd(&hist[pass][(k >> shift) & digits], 1);
+            if (s0 + r * kClusterThreads < n && (pass == 0 || (key[r] >> above) == (prefix >> above))) {
+                atomicAdd(&hist[pass][(key[r] >> shift) & digits], 1);
             }
         }
         sync();
         // thread t: bins 2047 - 2t and 2046 - 2t, so that a scan by thread runs from the top
         const int hi = kBins - 1 - 2 * tid;
-        int c1 = hist[pass][hi], c0 = hist[pass][hi - 1];
-        for (int c = 0; c < cluster; ++c) {
-            if (c == rank) continue;
-            c1 += ld_cluster(&hist[pass][hi], c);
-            c0 += ld_cluster(&hist[pass][hi - 1], c);
+        int c1, c0;
+        if (CLUSTER) {  // of all CTAs, the loads in flight together
+            int2 v[kEvictMaxCluster];
+#pragma unroll
+            for (int c = 0; c < kEvictMaxCluster; ++c) {
+                v[c] = make_int2(0, 0);
+                if (c < cluster) v[c] = ld_cluster2(&hist[pass][hi - 1], c);
+            }
+            c1 = c0 = 0;
+#pragma unroll
+            for (int c = 0; c < kEvictMaxCluster; ++c) {
+                c0 += v[c].x;
+                c1 += v[c].y;
+            }
+        } else {
+            c1 = hist[pass][hi];
+            c0 = hist[pass][hi - 1];
         }
         int incl = c1 + c0;
 #pragma unroll
@@ -482,27 +566,26 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
     // the lowest `want` of the keys at the threshold
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const bool eq = s0 + r * kClusterThreads < n && key_of(r) == prefix;
-        const uint32_t bal = __ballot_sync(0xffffffffu, eq);
+        const uint32_t bal = __ballot_sync(0xffffffffu, s0 + r * kClusterThreads < n && key[r] == prefix);
         if (lane == 0) cnt[r * NW + warp] = __popc(bal);
     }
     __syncthreads();
     int all = scan();
     int eq_before = 0;
-    if (cluster > 1) {
+    if (CLUSTER) {
         if (tid == 0) share[1] = all;
         sync();
-        for (int c = 0; c < rank; ++c) eq_before += ld_cluster(&share[1], c);
+        const int v = of_cluster(&share[1], 0);
+        eq_before = __reduce_add_sync(0xffffffffu, lane < rank ? v : 0);
     }
     uint32_t kept = 0;  // bit r
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const bool in = s0 + r * kClusterThreads < n;
-        const uint32_t k = key_of(r);
-        const bool eq = in && k == prefix;
+        const bool in = s0 + r * kClusterThreads < n, eq = in && key[r] == prefix;
         const uint32_t bal = __ballot_sync(0xffffffffu, eq);
-        const bool low = eq_before + cnt[r * NW + warp] + __popc(bal & below) < want;
-        if (in && (k > prefix || (eq && low))) kept |= 1u << r;
+        bool k = in && key[r] > prefix;
+        if (bal && eq) k = eq_before + cnt[r * NW + warp] + __popc(bal & below) < want;
+        kept |= static_cast<uint32_t>(k) << r;
     }
     __syncthreads();
     // holes (low half of a count) and movers (high half); both fit: a CTA has at most 16384 slots
@@ -516,17 +599,13 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
     __syncthreads();
     all = scan();
     int h_before = 0, m_before = 0, total = all & 0xFFFF;
-    if (cluster > 1) {
+    if (CLUSTER) {
         if (tid == 0) share[2] = all;
         sync();
-        for (int c = 0; c < cluster; ++c) {
-            const int v = c == rank ? all : ld_cluster(&share[2], c);
-            if (c < rank) {
-                h_before += v & 0xFFFF;
-                m_before += v >> 16;
-            }
-            if (c != rank) total += v & 0xFFFF;
-        }
+        const int v = of_cluster(&share[2], 0), mine = lane < rank ? v : 0;
+        h_before = __reduce_add_sync(0xffffffffu, mine & 0xFFFF);
+        m_before = __reduce_add_sync(0xffffffffu, mine >> 16);
+        total = __reduce_add_sync(0xffffffffu, v & 0xFFFF);
     }
     int* holes = p.moves + slab * 2 * p.list;
     int* movers = holes + p.list;
@@ -535,25 +614,30 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
         const int i = s0 + r * kClusterThreads;
         const bool k = kept >> r & 1u, hole = i < keep && !k, mover = i >= keep && k;
         const uint32_t bh = __ballot_sync(0xffffffffu, hole), bm = __ballot_sync(0xffffffffu, mover);
-        const int at = cnt[r * NW + warp];
-        if (hole) holes[h_before + (at & 0xFFFF) + __popc(bh & below)] = i;
-        if (mover) movers[m_before + (at >> 16) + __popc(bm & below)] = i;
+        if (bh | bm) {
+            const int at = cnt[r * NW + warp];
+            if (hole) holes[h_before + (at & 0xFFFF) + __popc(bh & below)] = i;
+            if (mover) movers[m_before + (at >> 16) + __popc(bm & below)] = i;
+        }
         if (k && i < keep) {
-            if (copy) acc_out[i] = w[r];
-            if (copy_pos) pos_out[i] = q[r];
+            if (copy) acc_out[i] = acc[i];
+            if (copy_pos) pos_out[i] = pos[i];
             if (src) src[i] = i;
         }
     }
-    sync();  // the lists are whole, and every slot of the slab has been read
+    sync();  // the lists are whole
+    // A mover's entries go to its hole's slot, below n_keep, where nothing is read any more; the
+    // tables behind n_keep are read and then cleared by the thread that has the slot.
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int i = s0 + r * kClusterThreads;
+        if (i - lane + 32 <= keep) continue;  // the whole warp
         const bool mover = i >= keep && (kept >> r & 1u);
         const uint32_t bm = __ballot_sync(0xffffffffu, mover);
         if (mover) {
             const int to = holes[m_before + (cnt[r * NW + warp] >> 16) + __popc(bm & below)];
-            acc_out[to] = w[r];
-            pos_out[to] = q[r];
+            acc_out[to] = acc[i];
+            pos_out[to] = pos[i];
             if (src) src[to] = i;
         }
         if (i >= keep && i < n) {
@@ -571,15 +655,19 @@ static cudaError_t launch_evict(const EvictParams& p, unsigned slabs, int cluste
     cfg.gridDim = dim3(slabs * static_cast<unsigned>(cluster));
     cfg.blockDim = dim3(kClusterThreads);
     cfg.stream = s;
+    if (cluster == 1) {
+        return move ? cudaLaunchKernelEx(&cfg, evict_kernel<D, R, false, true>, p, 1)
+                    : cudaLaunchKernelEx(&cfg, evict_kernel<D, R, false, false>, p, 1);
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return move ? cudaLaunchKernelEx(&cfg, evict_kernel<D, R, true>, p, cluster)
-                : cudaLaunchKernelEx(&cfg, evict_kernel<D, R, false>, p, cluster);
+    cfg.numAttrs = 1;
+    return move ? cudaLaunchKernelEx(&cfg, evict_kernel<D, R, true, true>, p, cluster)
+                : cudaLaunchKernelEx(&cfg, evict_kernel<D, R, true, false>, p, cluster);
 }
 
 template <int D>
@@ -594,14 +682,15 @@ static cudaError_t launch_evict_d(const EvictParams& p, unsigned slabs, cudaStre
         // as few CTAs as hold a slab; more while SMs are idle and each keeps a few thousand slots
         int cluster = 1;
         while (cluster * kClusterThreads * 16 < p.L) cluster *= 2;
-        while (cluster < kEvictMaxCluster && static_cast<int64_t>(slabs) * cluster * 2 <= sms &&
-               p.L > cluster * kClusterThreads * 4) {
+        while (cluster < kEvictMaxCluster && static_cast<int64_t>(slabs) * cluster * 2 <= sms && p.L > cluster * kClusterThreads * 4) {
             cluster *= 2;
         }
         // few slabs leave SMs without a CTA: a second launch moves their rows with all of them
         move = static_cast<int64_t>(slabs) * cluster * 4 >= 3ll * sms || p.list <= 256;
-        e = p.L <= cluster * kClusterThreads * 4 ? launch_evict<D, 4>(p, slabs, cluster, move, s)
-                                                 : launch_evict<D, 16>(p, slabs, cluster, move, s);
+        const int per_thread = (p.L + cluster * kClusterThreads - 1) / (cluster * kClusterThreads);
+        e = per_thread <= 4   ? launch_evict<D, 4>(p, slabs, cluster, move, s)
+            : per_thread <= 8 ? launch_evict<D, 8>(p, slabs, cluster, move, s)
+                              : launch_evict<D, 16>(p, slabs, cluster, move, s);
     }
     if (e != cudaSuccess || move || p.list == 0) return e;
     cudaLaunchConfig_t cfg{};
@@ -756,15 +845,13 @@ extern "C" dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope
     p.h_s = KV->h_s;
     p.st = status_ptr();
     if (!p.st) return DAK_ERR_CUDA;
-    const dim3 grid(static_cast<unsigned>(tokens), 1);
+    // few tokens: their heads over several blocks, up to eight blocks an SM
+    const int units = (H_q + 2 * KV->H_kv) * (D / 16), blocks = (units + kRopeThreads - 1) / kRopeThreads;
+    const int64_t room = std::max<int64_t>(1, 8ll * device_sm_count() / tokens);
+    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(std::min<int64_t>(std::min(blocks, 16), room)));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (D == 128) {
-        in_fp32 ? append_rope_kernel<128, true><<<grid, kRopeThreads, 0, s>>>(p)
-                : append_rope_kernel<128, false><<<grid, kRopeThreads, 0, s>>>(p);
-    } else {
-        in_fp32 ? append_rope_kernel<64, true><<<grid, kRopeThreads, 0, s>>>(p)
-                : append_rope_kernel<64, false><<<grid, kRopeThreads, 0, s>>>(p);
-    }
+    if (D == 128) in_fp32 ? launch_append_rope<128, true>(p, grid, s) : launch_append_rope<128, false>(p, grid, s);
+    else in_fp32 ? launch_append_rope<64, true>(p, grid, s) : launch_append_rope<64, false>(p, grid, s);
     return cuda_status(cudaGetLastError());
 }
 
