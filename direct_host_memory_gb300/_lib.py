@@ -652,6 +652,27 @@ def _raw_stream(stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _kv_shape(KV, name="KV"):
+    """[B, H_kv, D, L] of a KV placement."""
+    if KV.shape is None:
+        raise ValueError(f"{name} must be a KV placement")
+    return KV.shape
+
+
+def _workspace(given, nbytes, stream):
+    """The caller's workspace, or one of this call's. The allocator hands a call's own memory out
+    again, in the order of the current stream, once the call has returned: on another stream it is
+    told so."""
+    if given is not None:
+        if given.get_device() != _torch._C._cuda_getDevice() or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
+        return given
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device="cuda")
+    if stream is not None:
+        ws.record_stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return ws
+
+
 def _arg(t, name, dtype, shape):
     """Address of a contiguous CUDA tensor of this type and shape (None: none)."""
     if t is None:
@@ -689,7 +710,7 @@ def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slot
     slot_pos int32 CUDA [B][H_kv][L], updated in place. Returns q_out, bf16, shaped as q (None
     without q)."""
     torch = _torch or _t()
-    B, Hkv, D, L = KV.shape
+    B, Hkv, D, L = _kv_shape(KV)
     T = k_new.shape[1] if k_new.ndim == 4 else 1
     dtype = k_new.dtype
     fp32 = dtype is torch.float32
@@ -727,7 +748,7 @@ def dak_kv_evict(KV: Placement, seq_lens, n_keep: int, n_recent: int, acc, slot_
     given; seq_lens int32 CUDA [B]. Returns (lens_out [B], src_out [B][H_kv][n_keep]), int32:
     the new lengths, and the slot each kept row came from (-1 past the length)."""
     torch = _torch or _t()
-    B, Hkv, _, L = KV.shape
+    B, Hkv, _, L = _kv_shape(KV)
     n_keep = int(n_keep)
     if not 1 <= n_keep <= L:
         raise DakError(1, f"dak_kv_evict: n_keep {n_keep} outside 1..{L}")
@@ -737,8 +758,7 @@ def dak_kv_evict(KV: Placement, seq_lens, n_keep: int, n_recent: int, acc, slot_
         lens_out = torch.empty(B, dtype=i32, device=dev)
     if src_out is None:
         src_out = torch.empty(kept, dtype=i32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(KV.cached("evict", lambda: dak_kv_evict_workspace_bytes(KV)), dtype=torch.uint8, device=dev)
+    workspace = _workspace(workspace, KV.cached("evict", lambda: dak_kv_evict_workspace_bytes(KV)), stream)
     aa, pa = _arg(acc, "acc", f32, table), _arg(slot_pos, "slot_pos", i32, table)
     _check(lib.dak_kv_evict(KV.handle, _arg(seq_lens, "seq_lens", i32, per_request), n_keep, int(n_recent), aa,
                             aa if acc_out is None else _arg(acc_out, "acc_out", f32, table), pa,
@@ -759,7 +779,7 @@ def _n_split_of(tuning) -> int:
 def _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out):
     """Addresses of Q, O, seq_lens, acc_in, acc_out, with O made where there is none."""
     torch = _torch or _t()
-    B, Hkv, D, L = KV.shape
+    B, Hkv, D, L = _kv_shape(KV)
     shape = Q.shape
     if len(shape) != 3 or shape[0] != B or shape[2] != D:
         raise ValueError("Q must be [B][H_q][D] of the KV placement's B and D")
@@ -783,14 +803,12 @@ def dak_attn_acc(Q, KV: Placement, acc_in=None, acc_out=None, seq_lens=None, sca
     acc_in; without one, a new tensor that is zero behind each request's tokens."""
     torch = _torch or _t()
     if acc_out is None:
-        B, Hkv, _, L = KV.shape
+        B, Hkv, _, L = _kv_shape(KV)
         acc_out = torch.zeros((B, Hkv, L), dtype=torch.float32, device=Q.device)
     O, qa, oa, la, ia, aa = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out)
     Hq = Q.shape[1]
-    if workspace is None:
-        n = _n_split_of(tuning) if tuning else 0
-        workspace = torch.empty(KV.cached(("acc", Hq, n), lambda: dak_attn_acc_workspace_bytes(KV, Hq, n)),
-                                dtype=torch.uint8, device=Q.device)
+    n = _n_split_of(tuning) if tuning else 0
+    workspace = _workspace(workspace, KV.cached(("acc", Hq, n), lambda: dak_attn_acc_workspace_bytes(KV, Hq, n)), stream)
     _check(lib.dak_attn_acc(qa, KV.handle, la, Hq, scale, oa, bool(o_fp32), ia, aa, workspace.data_ptr(), workspace.nbytes,
                             _tuning(tuning), _raw_stream(stream)), "dak_attn_acc")
     return O, acc_out
@@ -814,11 +832,10 @@ def dak_attn_prefix(Q, KV: Placement, prefix: Placement, prefix_of=None, prefix_
         raise ValueError("acc_in without acc_out")
     O, qa, oa, la, ia, aa = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out)
     Hq = Q.shape[1]
-    if workspace is None:
-        n = _n_split_of(tuning) if tuning else 0
-        size = KV.cached(("prefix", prefix.shape, Hq, n, aa is None),
-                         lambda: dak_attn_prefix_workspace_bytes(KV, prefix, Hq, n, aa is not None))
-        workspace = torch.empty(size, dtype=torch.uint8, device=Q.device)
+    n = _n_split_of(tuning) if tuning else 0
+    workspace = _workspace(workspace, KV.cached(("prefix", _kv_shape(prefix, "prefix"), Hq, n, aa is None),
+                                                lambda: dak_attn_prefix_workspace_bytes(KV, prefix, Hq, n, aa is not None)),
+                           stream)
     _check(lib.dak_attn_prefix(qa, KV.handle, la, prefix.handle,
                                _arg(prefix_lens, "prefix_lens", torch.int32, (prefix.shape[0],)),
                                _arg(prefix_of, "prefix_of", torch.int32, (KV.shape[0],)), Hq, scale, oa, bool(o_fp32), ia, aa,

@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
     };
     // the `what` of every CTA of the cluster, CTA c's on lane c
     const auto of_cluster = [&](const int* what, int none) { return lane < cluster ? ld_cluster(what, lane) : none; };
-    grid_dep_launch();
+    if (!MOVE) grid_dep_launch();
     if (g == 0 && rank == 0 && tid == 0) p.lens_out[b] = min(n, keep);
     if (n <= keep) {
 #pragma unroll

@@ -247,8 +247,8 @@ dak_status dak_rope_from_freqs(int head_dim, const double* inv_freq, int n_pairs
  *              table dak_kv_evict goes by.
  * Pointers 16-byte aligned (int32 arrays 4), pitches multiples of 16 bytes (DAK_ERR_ALIGN).
  * A row outside [0, L) is skipped (its query is still rotated) and reported by
- * dak_last_error as DAK_ERR_BOUNDS. Stream-ordered; a following dak_attn as after
- * dak_kv_append. */
+ * dak_last_error as DAK_ERR_BOUNDS. Stream-ordered; a following dak_attn or dak_attn_acc as
+ * after dak_kv_append (several tokens at once: without programmatic launch). */
 dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope_plan* rope, const void* q, const void* k,
                               const void* v, int in_fp32, int T, int H_q, int64_t q_pitch, int64_t k_pitch,
                               int64_t v_pitch, const int* slots, const int* positions, const int* n_new, void* q_out,
@@ -274,7 +274,8 @@ dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope_plan* rope
  *              i >= L_b.
  *   workspace: dak_kv_evict_workspace_bytes(KV) bytes of device memory, 16-byte aligned,
  *              contents on entry do not matter; calls that share one must not overlap.
- * 1 <= n_keep <= L, 0 <= n_recent <= n_keep (DAK_ERR_INVALID). Stream-ordered. */
+ * 1 <= n_keep <= L, 0 <= n_recent <= n_keep (DAK_ERR_INVALID). Stream-ordered; a following
+ * attention is launched without programmatic launch. */
 size_t dak_kv_evict_workspace_bytes(const dak_placement* KV);
 dak_status dak_kv_evict(const dak_placement* KV, const int* seq_lens, int n_keep, int n_recent, const float* acc,
                         float* acc_out, const int* slot_pos, int* slot_pos_out, int* lens_out, int* src_out,

@@ -264,3 +264,5 @@ def test_serving_attention_refusals(dak, no_gpu):
                dict(acc_out=0x300000)):  # the scores need more workspace
         assert prefix(**kw) == INVALID, kw
     assert prefix(acc_out=0x300000, n=dak.lib.dak_attn_prefix_workspace_bytes(r(kv), r(pre), 8, 0, 1)) == CUDA
+    assert prefix(P=r(_kv(B=1025, L=64)), n=1 << 40) == UNSUPPORTED
+    assert prefix(P=r(_kv(B=1024, L=64)), n=1 << 40) == CUDA

@@ -457,6 +457,171 @@ def test_evict_repeats_and_refuses(dak):
     kv.free()
 
 
+# ---------------------------------------------------------------- sizes, streams and graphs
+
+def _prefix_run(dak, B, Hq, Hkv, D, L, lens, plens, of, fp32):
+    import torch
+    q, k, v = synth.attn_inputs(B, Hq, Hkv, D, L, seed=B + D)
+    _, pk, pv = synth.attn_inputs(len(plens), Hq, Hkv, D, max(plens), seed=B + D + 1)
+    o, w, spread, reach = oc.attention(q, k, v, lens, (pk, pv), of, plens)
+    kv, pre = dak.dak_place_kv_heads(k, v, 3), dak.dak_place_kv_heads(pk, pv, min(5, len(plens) * Hkv - 1))
+    acc = torch.zeros(B, Hkv, L, device="cuda")
+    O = dak.dak_attn_prefix(to_dev(q), kv, pre, prefix_of=_i32(of), prefix_lens=_i32(plens), seq_lens=_i32(lens),
+                            acc_out=acc, o_fp32=fp32)
+    _ok(dak)
+    n = L + max(plens)
+    _check_attn(O, o, spread, reach, D, n, fp32, parts=None if fp32 else 1)
+    _check_weights(acc, None, w, np.zeros(w.shape, np.float32), lens, reach, Hq // Hkv, D, n)
+    kv.free()
+    pre.free()
+
+
+@pytest.mark.parametrize("P,B,Hq,Hkv,D,fp32", [
+    (60, 170, 8, 4, 64, False),    # more tiles than the GPU has SMs, more than 128 requests
+    (45, 300, 32, 4, 128, False),  # of one and of two 128-row halves, some prefixes with no request
+    (70, 140, 6, 3, 128, True),
+    (200, 210, 1, 1, 64, False),   # more prefixes than tiles
+])
+def test_attn_prefix_of_many(dak, P, B, Hq, Hkv, D, fp32):
+    rng = np.random.default_rng(P)
+    plens = rng.integers(0, 200, P)
+    plens[:3] = [0, 1, 200]
+    of = np.where(rng.random(B) < 0.25, 4, rng.integers(-1, P, B))  # one prefix with many requests
+    lens = rng.integers(0, 6, B)
+    _prefix_run(dak, B, Hq, Hkv, D, 5, lens.tolist(), plens.tolist(), of.tolist(), fp32)
+
+
+def test_attn_prefix_long_in_many_ranges(dak):
+    """One kv head: a prefix is cut into as many ranges as the GPU has SMs."""
+    _prefix_run(dak, 3, 4, 1, 64, 700, [700, 0, 3], [30001, 20], [0, 0, 1], False)
+    _prefix_run(dak, 40, 4, 1, 128, 9, [k % 9 for k in range(40)], [20000, 9000], [k % 3 - 1 for k in range(40)], True)
+
+
+def test_attn_acc_in_many_splits(dak):
+    import torch
+    B, Hq, Hkv, D, L = 2, 3, 1, 64, 66001
+    q, k, v = synth.attn_inputs(B, Hq, Hkv, D, L, seed=4)
+    lens = [L, 40000]
+    o, w, spread, reach = oc.attention(q, k, v, lens)
+    kv = dak.dak_place_kv_heads(k, v, 0)
+    for split in (1024, 300, 0):
+        O, acc = dak.dak_attn_acc(to_dev(q), kv, seq_lens=_i32(lens), tuning=dict(n_split=split))
+        _ok(dak)
+        _check_attn(O, o, spread, reach, D, L, False)
+        _check_weights(acc, None, w, np.zeros(w.shape, np.float32), lens, reach, Hq // Hkv, D, L)
+    kv.free()
+
+
+def test_a_cache_past_32_bit_offsets(dak):
+    """The last request of a cache of more than 4 GiB a tier against the same request alone."""
+    import torch
+    B, Hq, Hkv, D, L = 34, 4, 4, 128, 65600
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.zeros(B, Hkv, L, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for t in (k, v):
+        t[-1].normal_(generator=gen)
+    big, one = dak.dak_place_kv_heads(k, v, 0), dak.dak_place_kv_heads(k[-1:].contiguous(), v[-1:].contiguous(), 0)
+    del k, v
+    assert big.hbm_bytes > 1 << 32
+    rope = dak.dak_rope_make(D)
+    x = torch.randn(B, Hq + 2 * Hkv, D, device="cuda", generator=gen)
+    slots = torch.full((B,), L - 1, dtype=torch.int32, device="cuda")
+    acc = torch.rand(B, Hkv, L, device="cuda", generator=gen)
+    sp = torch.arange(L, dtype=torch.int32, device="cuda").repeat(B, Hkv, 1)
+    out = []
+    for kv, sel in ((big, slice(None)), (one, slice(-1, None))):
+        xx, a, p = x[sel].contiguous(), acc[sel].clone(), sp[sel].clone()
+        q = dak.dak_kv_append_rope(kv, rope, xx[:, :Hq], xx[:, Hq:2 * Hq], xx[:, 2 * Hq:], slots[sel], slot_pos=p)
+        lens = slots[sel] + 1
+        O, a = dak.dak_attn_acc(q, kv, acc_in=a, acc_out=a, seq_lens=lens, tuning=dict(n_split=8))
+        lens, src = dak.dak_kv_evict(kv, lens, 30000, 100, a, p)
+        O2 = dak.dak_attn_prefix(q, kv, kv, prefix_of=slots[sel] * 0 + kv.shape[0] - 1, seq_lens=lens,
+                                 prefix_lens=torch.full((kv.shape[0],), 30000, dtype=torch.int32, device="cuda"),
+                                 tuning=dict(n_split=8))
+        _ok(dak)
+        out.append([t[-1].clone() for t in (q, O, a, p, src)] + [lens[-1:], kv.slabs()[1][-Hkv:].clone()])
+        # the prefix of 34 requests is cut elsewhere than that of one: another order of the sums
+        out[-1].append(O2[-1].float())
+    for a, b in zip(out[0][:-1], out[1][:-1]):
+        assert torch.equal(a, b)
+    # |o| <= max |v| < 8 and each side is off by at most 2^-8 of the weighted |v| (one bf16 part) and
+    # 2^-9 of the output; both outputs lie far below 1
+    assert (out[0][-1] - out[1][-1]).abs().max().item() <= 2 * (U16 + U16) * 1.0
+    big.free()
+    one.free()
+
+
+def test_graphs_and_streams_with_memory_of_their_own(dak):
+    """Two graphs that were captured without a workspace replay in turn and beside eager calls; calls
+    on another stream take their memory with them."""
+    import torch
+    B, Hq, Hkv, D, L = 4, 8, 2, 64, 1500
+    q, k, v = synth.attn_inputs(B, Hq, Hkv, D, L, seed=21)
+    _, pk, pv = synth.attn_inputs(1, Hq, Hkv, D, 900, seed=22)
+    kv, pre = dak.dak_place_kv_heads(k, v, 2), dak.dak_place_kv_heads(pk, pv, 1)
+    Q = to_dev(q)
+    lens = [_i32([1500, 700, 0, 3]), _i32([9, 1400, 64, 65])]
+    calls = [lambda: dak.dak_attn_acc(Q, kv, seq_lens=lens[0], tuning=dict(n_split=20)),
+             lambda: (dak.dak_attn_prefix(Q, kv, pre, seq_lens=lens[1]),)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c())
+        graphs.append(g)
+    for _ in range(3):
+        for g, o in zip(graphs, outs):
+            for t in o:
+                t.fill_(-1.0)
+            if len(o) == 2:
+                o[1].zero_()
+            g.replay()
+        eager = [c() for c in calls]
+        torch.cuda.synchronize()
+        for o, e, w in zip(outs, eager, want):
+            assert torch.equal(o[0], w[0]) and torch.equal(e[0], w[0])
+            if len(o) == 2:
+                assert torch.equal(o[1], w[1]) and torch.equal(e[1], w[1])
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        s.wait_stream(torch.cuda.current_stream())
+        O, acc = torch.empty_like(want[0][0]), torch.zeros_like(want[0][1])
+        O2 = torch.empty_like(want[1][0])
+        torch.cuda.synchronize()
+        dak.dak_attn_acc(Q, kv, acc_out=acc, seq_lens=lens[0], O=O, tuning=dict(n_split=20), stream=stream)
+        junk = [torch.full((1 << 22,), 1e30, device="cuda") for _ in range(4)]  # on the current stream
+        dak.dak_attn_prefix(Q, kv, pre, seq_lens=lens[1], O=O2, stream=stream)
+        junk += [torch.full((1 << 22,), 1e30, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(O, want[0][0]) and torch.equal(acc, want[0][1]) and torch.equal(O2, want[1][0])
+    _ok(dak)
+    kv.free()
+    pre.free()
+
+
+def test_calls_refused_before_a_launch(dak):
+    import torch
+    q, k, v = synth.attn_inputs(2, 4, 2, 64, 64, seed=1)
+    kv, Q = dak.dak_place_kv_heads(k, v, 0), to_dev(q)
+    W = dak.dak_place_matrix(synth.normal_bf16(1, 1, 64 * 64).reshape(64, 64), 0)
+    lens = _i32([3, 4])
+    acc, sp = torch.zeros(2, 2, 64, device="cuda"), torch.zeros(2, 2, 64, dtype=torch.int32, device="cuda")
+    host = torch.empty(1 << 22, dtype=torch.uint8)
+    for call in (lambda: dak.dak_attn_acc(Q, W), lambda: dak.dak_attn_prefix(Q, W, kv), lambda: dak.dak_attn_prefix(Q, kv, W),
+                 lambda: dak.dak_kv_evict(W, lens, 2, 0, acc, sp), lambda: dak.dak_attn_acc(Q, kv, workspace=host),
+                 lambda: dak.dak_attn_prefix(Q, kv, kv, workspace=host),
+                 lambda: dak.dak_kv_evict(kv, lens, 2, 0, acc, sp, workspace=host),
+                 lambda: dak.dak_kv_append_rope(W, dak.dak_rope_make(64), None, Q, Q, lens),
+                 lambda: dak.dak_attn_acc(Q, kv, seq_lens=lens.cpu()), lambda: dak.dak_attn_acc(Q.cpu(), kv),
+                 lambda: dak.dak_attn_acc(Q, kv, acc_out=acc[:, :1]), lambda: dak.dak_attn_acc(Q, kv, seq_lens=lens.long())):
+        with pytest.raises(ValueError):
+            call()
+    _ok(dak)
+    kv.free()
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("use_prefix", [False, True])
