@@ -63,9 +63,13 @@ class SplitK_FlashAttn(torch.nn.Module):
     scale 1/sqrt(D) unless given, positions past seq_lens[b] masked), over a static KV cache
     K, V [B][H_kv][L][D] bf16 placed across host memory and HBM ([DAK] section 5): the first
     n_host_heads (request, kv head) slabs on the host. The cache is copied into the placement
-    at construction; append(k, v, positions) writes each step's new token into it.
-    forward(query [B][H_q][D] or [B][H_q][1][D], seq_lens int32 [B]) returns the same shape,
-    bf16 (or fp32 with fp32_out)."""
+    at construction; append(k, v, positions) writes each step's new token into it, and
+    append_rope(...) rotates one or many first. forward(query [B][H_q][D] or [B][H_q][1][D],
+    seq_lens int32 [B]) returns the same shape, bf16 (or fp32 with fp32_out).
+    For chats that outgrow the cache, track() keeps every token's accumulated attention weight
+    (self.weights, fp32 [B][H_kv][L]) and position (self.slot_pos, int32 of the same shape),
+    which evict(...) goes by. For requests that share prefixes, forward takes the KV placement
+    that holds those."""
 
     def __init__(self, k_cache, v_cache, offload_ratio: float = 0.0, n_host_heads: int = None,
                  n_split: int = 0, fp32_out: bool = False, tuning=None):
@@ -78,24 +82,67 @@ class SplitK_FlashAttn(torch.nn.Module):
         self.placement = _lib.dak_place_kv_heads(k_cache, v_cache, int(n_host_heads))
         self.batch, self.n_kv_heads, self.capacity, self.head_dim = B, Hkv, L, D
         self.n_split = int(n_split) or _lib.dak_attn_default_split(self.placement)
+        self._given_split = int(n_split)
         self.fp32_out = bool(fp32_out)
         self.tuning = dict(tuning or {})
         self._ws = None
+        self.weights = self.slot_pos = None
 
     @property
     def host_bytes(self) -> int:
         return self.placement.host_bytes
 
+    def track(self):
+        """From now on accumulate attention weights and keep positions: a token that the cache
+        holds already has its slot as its position and no weight yet."""
+        shape = (self.batch, self.n_kv_heads, self.capacity)
+        self.weights = torch.zeros(shape, dtype=torch.float32, device="cuda")
+        at = torch.arange(self.capacity, dtype=torch.int32, device="cuda")
+        self.slot_pos = at.expand(shape).contiguous()
+
     def append(self, k_new, v_new, positions):
         """Write one token per request: k_new, v_new bf16 CUDA [B][H_kv][D] (or [B][H_kv][1][D]),
-        positions int32 CUDA [B]."""
+        positions int32 CUDA [B]. A cache that is tracked appends by append_rope, which knows a
+        token's slot and its position."""
+        if self.slot_pos is not None:
+            raise ValueError("a tracked cache appends by append_rope")
         shape = (self.batch, self.n_kv_heads, self.head_dim)
         n = self.batch * self.n_kv_heads * self.head_dim
         if k_new.numel() != n or v_new.numel() != n:
             raise ValueError(f"k_new / v_new must hold {list(shape)}")
         _lib.dak_kv_append(self.placement, k_new.reshape(shape), v_new.reshape(shape), positions)
 
-    def forward(self, query, seq_lens=None, scale: float = None):
+    def append_rope(self, rope, q, k_new, v_new, slots, positions=None, n_new=None):
+        """Rotate new tokens and write them from row slots[b] on (dak_kv_append_rope): q
+        [B][T][H_q][D] or None, k_new and v_new [B][T][H_kv][D], bf16 or fp32 CUDA (T = 1: the
+        axis may be absent), rope by dak_rope_make; rope None: as they are. Returns the rotated
+        q in bf16."""
+        if rope is None:
+            rope = _lib.dak_rope_from_freqs(self.head_dim, [0.0])
+        return _lib.dak_kv_append_rope(self.placement, rope, q, k_new, v_new, slots, positions=positions, n_new=n_new,
+                                       slot_pos=self.slot_pos)
+
+    def evict(self, seq_lens, n_keep: int, n_recent: int = 0):
+        """Keep n_keep tokens of every (request, kv head) of a tracked cache that holds more: the
+        n_recent newest, then the most attended (dak_kv_evict). Returns the new seq_lens."""
+        if self.slot_pos is None:
+            raise ValueError("evict needs a tracked cache: call track() first")
+        return _lib.dak_kv_evict(self.placement, seq_lens, n_keep, n_recent, self.weights, self.slot_pos)[0]
+
+    def _serve(self, q, seq_lens, scale, prefix, prefix_of, prefix_lens):
+        tun = dict(self.tuning, n_split=self._given_split) if self._given_split else self.tuning
+        kw = dict(acc_in=self.weights, acc_out=self.weights, seq_lens=seq_lens, scale=scale, o_fp32=self.fp32_out,
+                  tuning=tun or None)
+        if prefix is None:
+            return _lib.dak_attn_acc(q, self.placement, **kw)[0]
+        return _lib.dak_attn_prefix(q, self.placement, prefix, prefix_of=prefix_of, prefix_lens=prefix_lens, **kw)
+
+    def forward(self, query, seq_lens=None, scale: float = None, prefix=None, prefix_of=None, prefix_lens=None):
+        """prefix: a KV placement of shared prefixes that requests attend over before their own
+        tokens, prefix_of int32 [B] which one (None: the first) and prefix_lens how long they are
+        (dak_attn_prefix)."""
+        if prefix is None and (prefix_of is not None or prefix_lens is not None):
+            raise ValueError("prefix_of and prefix_lens need a prefix")
         squeeze = query.ndim == 4
         if squeeze:
             if query.shape[2] != 1:
@@ -103,6 +150,9 @@ class SplitK_FlashAttn(torch.nn.Module):
             q = query.reshape(query.shape[0], query.shape[1], query.shape[3])
         else:
             q = query
+        if prefix is not None or self.weights is not None:
+            o = self._serve(q, seq_lens, float(scale or 0.0), prefix, prefix_of, prefix_lens)
+            return o.view(query.shape) if squeeze else o
         Hq = int(q.shape[1])
         need = _lib.dak_attn_workspace_bytes(self.batch, Hq, self.head_dim, self.n_split)
         if need and (self._ws is None or self._ws.numel() * 4 < need or self._ws.device != q.device):
