@@ -636,19 +636,20 @@ def dak_rope_from_freqs(head_dim: int, inv_freq, interleaved: bool = False, attn
 # checked in one place each and handed over as plain addresses.
 
 def _t():
-    global _torch
+    global _torch, _get_device, _get_stream
     import torch
+    _get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _torch = torch
     return torch
 
 
-_torch = None
+_torch = _get_device = _get_stream = None
 
 
-def _raw_stream(stream):
-    """Address of the stream (None: the current one of the current device)."""
+def _raw_stream(stream, dev):
+    """Address of the stream (None: the current one of the current device, which is dev)."""
     if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+        return _get_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -659,34 +660,34 @@ def _kv_shape(KV, name="KV"):
     return KV.shape
 
 
-def _workspace(given, nbytes, stream):
+def _workspace(given, nbytes, stream, dev, device):
     """The caller's workspace, or one of this call's. The allocator hands a call's own memory out
     again, in the order of the current stream, once the call has returned: on another stream it is
     told so."""
     if given is not None:
-        if given.get_device() != _torch._C._cuda_getDevice() or not given.is_contiguous():
+        if given.get_device() != dev or not given.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
         return given
-    ws = _torch.empty(nbytes, dtype=_torch.uint8, device="cuda")
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
     if stream is not None:
         ws.record_stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
     return ws
 
 
-def _arg(t, name, dtype, shape):
-    """Address of a contiguous CUDA tensor of this type and shape (None: none)."""
+def _arg(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of this type and shape on the current device dev (None: none)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != _torch._C._cuda_getDevice() or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on the current CUDA device")
     return t.data_ptr()
 
 
-def _token_rows(t, name, B, T, heads, D, dtype):
+def _token_rows(t, name, B, T, heads, D, dtype, dev):
     """Address of t [B][T][heads][D] (T = 1: also [B][heads][D]) and the pitch in elements between
     its tokens, which lie at one pitch with each token's heads contiguous, as in a slice of a
     packed projection."""
-    if t.dtype is not dtype or t.get_device() != _torch._C._cuda_getDevice():
+    if t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{name} must be a {dtype} tensor on the current CUDA device")
     shape, st = t.shape, t.stride()
     if T == 1 and shape == (B, heads, D):
@@ -712,27 +713,27 @@ def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slot
     torch = _torch or _t()
     B, Hkv, D, L = _kv_shape(KV)
     T = k_new.shape[1] if k_new.ndim == 4 else 1
-    dtype = k_new.dtype
+    dtype, dev = k_new.dtype, _get_device()
     fp32 = dtype is torch.float32
     if not fp32 and dtype is not torch.bfloat16:
         raise ValueError("k_new must be bf16 or fp32")
-    ka, kp = _token_rows(k_new, "k_new", B, T, Hkv, D, dtype)
-    va, vp = _token_rows(v_new, "v_new", B, T, Hkv, D, dtype)
+    ka, kp = _token_rows(k_new, "k_new", B, T, Hkv, D, dtype, dev)
+    va, vp = _token_rows(v_new, "v_new", B, T, Hkv, D, dtype, dev)
     Hq = qp = 0
     qa = oa = None
     if q is not None:
         Hq = q.shape[-2]
-        qa, qp = _token_rows(q, "q", B, T, Hq, D, dtype)
+        qa, qp = _token_rows(q, "q", B, T, Hq, D, dtype, dev)
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        oa = _arg(q_out, "q_out", torch.bfloat16, q.shape)
+        oa = _arg(q_out, "q_out", torch.bfloat16, q.shape, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     i32, per_request = torch.int32, (B,)
     _check(lib.dak_kv_append_rope(KV.handle, rope, qa, ka, va, fp32, T, Hq, qp, kp, vp,
-                                  _arg(slots, "slots", i32, per_request), _arg(positions, "positions", i32, per_request),
-                                  _arg(n_new, "n_new", i32, per_request), oa,
-                                  _arg(slot_pos, "slot_pos", i32, (B, Hkv, L)), _raw_stream(stream)), "dak_kv_append_rope")
+                                  _arg(slots, "slots", i32, per_request, dev), _arg(positions, "positions", i32, per_request, dev),
+                                  _arg(n_new, "n_new", i32, per_request, dev), oa,
+                                  _arg(slot_pos, "slot_pos", i32, (B, Hkv, L), dev), _raw_stream(stream, dev)), "dak_kv_append_rope")
     return q_out
 
 
@@ -753,18 +754,18 @@ def dak_kv_evict(KV: Placement, seq_lens, n_keep: int, n_recent: int, acc, slot_
     if not 1 <= n_keep <= L:
         raise DakError(1, f"dak_kv_evict: n_keep {n_keep} outside 1..{L}")
     table, per_request, kept = (B, Hkv, L), (B,), (B, Hkv, n_keep)
-    i32, f32, dev = torch.int32, torch.float32, acc.device
+    i32, f32, device, dev = torch.int32, torch.float32, acc.device, _get_device()
     if lens_out is None:
-        lens_out = torch.empty(B, dtype=i32, device=dev)
+        lens_out = torch.empty(B, dtype=i32, device=device)
     if src_out is None:
-        src_out = torch.empty(kept, dtype=i32, device=dev)
-    workspace = _workspace(workspace, KV.cached("evict", lambda: dak_kv_evict_workspace_bytes(KV)), stream)
-    aa, pa = _arg(acc, "acc", f32, table), _arg(slot_pos, "slot_pos", i32, table)
-    _check(lib.dak_kv_evict(KV.handle, _arg(seq_lens, "seq_lens", i32, per_request), n_keep, int(n_recent), aa,
-                            aa if acc_out is None else _arg(acc_out, "acc_out", f32, table), pa,
-                            pa if slot_pos_out is None else _arg(slot_pos_out, "slot_pos_out", i32, table),
-                            _arg(lens_out, "lens_out", i32, per_request), _arg(src_out, "src_out", i32, kept),
-                            workspace.data_ptr(), workspace.nbytes, _raw_stream(stream)), "dak_kv_evict")
+        src_out = torch.empty(kept, dtype=i32, device=device)
+    workspace = _workspace(workspace, KV.cached("evict", lambda: dak_kv_evict_workspace_bytes(KV)), stream, dev, device)
+    aa, pa = _arg(acc, "acc", f32, table, dev), _arg(slot_pos, "slot_pos", i32, table, dev)
+    _check(lib.dak_kv_evict(KV.handle, _arg(seq_lens, "seq_lens", i32, per_request, dev), n_keep, int(n_recent), aa,
+                            aa if acc_out is None else _arg(acc_out, "acc_out", f32, table, dev), pa,
+                            pa if slot_pos_out is None else _arg(slot_pos_out, "slot_pos_out", i32, table, dev),
+                            _arg(lens_out, "lens_out", i32, per_request, dev), _arg(src_out, "src_out", i32, kept, dev),
+                            workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev)), "dak_kv_evict")
     return lens_out, src_out
 
 
@@ -776,7 +777,7 @@ def _n_split_of(tuning) -> int:
     return int(dict(tuning or {}).get("n_split", 0) or 0)
 
 
-def _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out):
+def _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out, dev):
     """Addresses of Q, O, seq_lens, acc_in, acc_out, with O made where there is none."""
     torch = _torch or _t()
     B, Hkv, D, L = _kv_shape(KV)
@@ -787,9 +788,9 @@ def _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out):
     if O is None:
         O = torch.empty(shape, dtype=dtype, device=Q.device)
     table = (B, Hkv, L)
-    return (O, _arg(Q, "Q", torch.bfloat16, shape), _arg(O, "O", dtype, shape),
-            _arg(seq_lens, "seq_lens", torch.int32, (B,)), _arg(acc_in, "acc_in", torch.float32, table),
-            _arg(acc_out, "acc_out", torch.float32, table))
+    return (O, _arg(Q, "Q", torch.bfloat16, shape, dev), _arg(O, "O", dtype, shape, dev),
+            _arg(seq_lens, "seq_lens", torch.int32, (B,), dev), _arg(acc_in, "acc_in", torch.float32, table, dev),
+            _arg(acc_out, "acc_out", torch.float32, table, dev))
 
 
 def dak_attn_acc_workspace_bytes(KV: Placement, H_q: int, n_split: int = 0) -> int:
@@ -802,15 +803,17 @@ def dak_attn_acc(Q, KV: Placement, acc_in=None, acc_out=None, seq_lens=None, sca
     kv head, to acc_in fp32 [B][H_kv][L] (None = zeros). Returns (O, acc_out); acc_out may be
     acc_in; without one, a new tensor that is zero behind each request's tokens."""
     torch = _torch or _t()
+    dev = _get_device()
     if acc_out is None:
         B, Hkv, _, L = _kv_shape(KV)
         acc_out = torch.zeros((B, Hkv, L), dtype=torch.float32, device=Q.device)
-    O, qa, oa, la, ia, aa = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out)
+    O, qa, oa, la, ia, aa = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out, dev)
     Hq = Q.shape[1]
     n = _n_split_of(tuning) if tuning else 0
-    workspace = _workspace(workspace, KV.cached(("acc", Hq, n), lambda: dak_attn_acc_workspace_bytes(KV, Hq, n)), stream)
+    workspace = _workspace(workspace, KV.cached(("acc", Hq, n), lambda: dak_attn_acc_workspace_bytes(KV, Hq, n)), stream,
+                           dev, Q.device)
     _check(lib.dak_attn_acc(qa, KV.handle, la, Hq, scale, oa, bool(o_fp32), ia, aa, workspace.data_ptr(), workspace.nbytes,
-                            _tuning(tuning), _raw_stream(stream)), "dak_attn_acc")
+                            _tuning(tuning), _raw_stream(stream, dev)), "dak_attn_acc")
     return O, acc_out
 
 
@@ -828,18 +831,19 @@ def dak_attn_prefix(Q, KV: Placement, prefix: Placement, prefix_of=None, prefix_
     all its requests. acc_out, if given, takes acc_in (None = zeros) plus the weights of the own
     cache's positions, as in dak_attn_acc. Returns O."""
     torch = _torch or _t()
+    dev = _get_device()
     if acc_in is not None and acc_out is None:
         raise ValueError("acc_in without acc_out")
-    O, qa, oa, la, ia, aa = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out)
+    O, qa, oa, la, ia, aa = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out, dev)
     Hq = Q.shape[1]
     n = _n_split_of(tuning) if tuning else 0
     workspace = _workspace(workspace, KV.cached(("prefix", _kv_shape(prefix, "prefix"), Hq, n, aa is None),
                                                 lambda: dak_attn_prefix_workspace_bytes(KV, prefix, Hq, n, aa is not None)),
-                           stream)
+                           stream, dev, Q.device)
     _check(lib.dak_attn_prefix(qa, KV.handle, la, prefix.handle,
-                               _arg(prefix_lens, "prefix_lens", torch.int32, (prefix.shape[0],)),
-                               _arg(prefix_of, "prefix_of", torch.int32, (KV.shape[0],)), Hq, scale, oa, bool(o_fp32), ia, aa,
-                               workspace.data_ptr(), workspace.nbytes, _tuning(tuning), _raw_stream(stream)),
+                               _arg(prefix_lens, "prefix_lens", torch.int32, (prefix.shape[0],), dev),
+                               _arg(prefix_of, "prefix_of", torch.int32, (KV.shape[0],), dev), Hq, scale, oa, bool(o_fp32), ia, aa,
+                               workspace.data_ptr(), workspace.nbytes, _tuning(tuning), _raw_stream(stream, dev)),
            "dak_attn_prefix")
     return O
 
