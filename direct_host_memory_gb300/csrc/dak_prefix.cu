@@ -49,6 +49,7 @@ struct PrefixParams {
     int* n_ranges;     // [B]: key ranges that a request's rows have partials of (not written without any)
     int B, Hq, Hkv, G, L, n_prefix, n_pre, h_s, slab_chunks;
     int mpt;  // members of a 128-row tile: 128 / G
+    int inv_G;  // 2^16 / G rounded up: (r * inv_G) >> 16 is r / G for any row r of a tile
     float scale_log2;
     DevStatus* st;
 };
@@ -165,6 +166,13 @@ __device__ __forceinline__ void report_prefix(const PrefixParams& p, int b) {
     report(p.st, DAK_ERR_BOUNDS, (0x9F1Full << 32) | static_cast<unsigned>(b));
 }
 
+// n / d for 0 <= n < 2^21 (a count of requests or units: their rows' partials alone would take more
+// memory than there is), a few instructions where the integer division is dozens.
+__device__ __forceinline__ int quotient(int n, int d) {
+    const int q = static_cast<int>(static_cast<float>(n) * __fdividef(1.f, static_cast<float>(d))), r = n - q * d;
+    return q + (r >= d) - (r < 0);
+}
+
 // Unit u of the launch into *unit (units == 0: none at all) and its members' requests, by one warp.
 // Every CTA waits for this before its first copy, so it is built for latency: the map and the
 // lengths are loaded side by side (the first 128 requests' map stays in registers), counting and
@@ -186,15 +194,18 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
     // both kinds: tiles of two in its upper bits, one of one in bit 0. A chunk costs a tile of two
     // 1.25 times what it costs one of one (measured 1.9k and 1.55k cycles), and the ranges are cut so.
     const auto halves_of = [&](int cnt) {
-        const int full = cnt / per_tile, rest = cnt - full * per_tile;
+        const int full = quotient(cnt, per_tile), rest = cnt - full * per_tile;
         return rest > p.mpt ? 2 * full + 2 : 2 * full + (rest > 0);
     };
-    const auto ranges = [&](int work, int c, int T) {
-        return max(1, min(min((work + T - 1) / T, p.n_pre), c / kPrefixMinChunks));
+    // Ranges of a tile: its work over T, rounded up. (Any number from 1 to the limits is a valid cut;
+    // what it takes is the same one everywhere, so a reciprocal does.)
+    const auto ranges = [&](int cost, int c, float inv) {
+        return max(1, min(min(__float2int_ru(static_cast<float>(cost * c) * inv - 1e-3f), p.n_pre), c / kPrefixMinChunks));
     };
-    const auto units_of = [&](int halves, int c, int T) {  // per kv head
-        return halves == 0 || c == 0 ? 0 : (halves >> 1) * ranges(kPrefixTwoCost * c, c, T) + (halves & 1) * ranges(kPrefixOneCost * c, c, T);
+    const auto units_of = [&](int halves, int c, float inv) {  // per kv head
+        return halves == 0 || c == 0 ? 0 : (halves >> 1) * ranges(kPrefixTwoCost, c, inv) + (halves & 1) * ranges(kPrefixOneCost, c, inv);
     };
+    const auto inverse = [](int t) { return __fdividef(1.f, static_cast<float>(t)); };
     int f = -1, start = 0, base = 0, T = 1;
     int4 e;
     if (p.n_prefix == 1) {
@@ -202,6 +213,7 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         int cnt = p.B;
         if (p.of) {
             cnt = 0;
+#pragma unroll 1
             for (int b0 = 0; b0 < p.B; b0 += 32) {
                 const int v = map_of(b0);
                 if (v > 0 && blockIdx.x == 0) report_prefix(p, b0 + lane);
@@ -214,38 +226,41 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
             T = kPrefixTwoCost * e.z;
             if (tiles < ctas) {
                 if (e.y == 1 || (e.y & 1) == 0) {  // tiles of one kind: each the same share of the CTAs
-                    const int each = ctas / tiles, work = (e.y == 1 ? kPrefixOneCost : kPrefixTwoCost) * e.z;
-                    T = (work + each - 1) / each;
+                    const int each = quotient(ctas, tiles), work = (e.y == 1 ? kPrefixOneCost : kPrefixTwoCost) * e.z;
+                    T = quotient(work + each - 1, each);
                 } else {
                     int lo = 1;
+#pragma unroll 1
                     while (lo < T) {
                         const int mid = (lo + T) >> 1;
-                        if (units_of(e.y, e.z, mid) * p.Hkv <= ctas) T = mid;
+                        if (units_of(e.y, e.z, inverse(mid)) * p.Hkv <= ctas) T = mid;
                         else lo = mid + 1;
                     }
                 }
             }
-            base = units_of(e.y, e.z, T) * p.Hkv;
+            base = units_of(e.y, e.z, inverse(T)) * p.Hkv;
             if (u < base) f = 0;
         }
     } else {
+#pragma unroll 1
         for (int i = lane; i < p.n_prefix; i += 32) {
             const int len = p.lens ? min(max(p.lens[i], 0), p.L) : p.L;
             scratch[i] = make_int4(p.of || i > 0 ? 0 : p.B, 0, (len + 63) >> 6, len);
         }
         __syncwarp();
         if (p.of) {
+#pragma unroll 1
             for (int b0 = 0; b0 < p.B; b0 += 32) {
                 const int v = map_of(b0);
                 const bool in = v >= 0 && v < p.n_prefix;
                 if (v >= p.n_prefix && blockIdx.x == 0) report_prefix(p, b0 + lane);
-                const unsigned same = __match_any_sync(all, in ? v : -1);
-                if (in && lane == __ffs(same) - 1) scratch[v].x += __popc(same);
-                __syncwarp();
+                if (in) atomicAdd(&scratch[v].x, 1);
             }
+            __syncwarp();
         }
         int cmax = 1, n_tiles = 0;
         float work = 0.f;
+#pragma unroll 1
         for (int i = lane; i < p.n_prefix; i += 32) {
             const int4 q = scratch[i];
             const int halves = q.z > 0 ? halves_of(q.x) : 0;
@@ -263,22 +278,42 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         T = kPrefixTwoCost * cmax;
         if (n_tiles < ctas) {
             // the units lie between work / T and work / T + n_tiles
-            const auto total = [&](int t) {
+            const auto sum_on_lanes = [&](int t) {
                 int k = 0;
-                for (int i = lane; i < p.n_prefix; i += 32) k += units_of(scratch[i].y, scratch[i].z, t);
+                const float inv = inverse(t);
+#pragma unroll 1
+                for (int i = lane; i < p.n_prefix; i += 32) k += units_of(scratch[i].y, scratch[i].z, inv);
                 return __reduce_add_sync(all, k) * p.Hkv;
             };
             int lo = min(T, max(1, static_cast<int>(min(work / static_cast<float>(ctas), 1e9f)) - 1));
             T = max(lo, min(T, static_cast<int>(min(work / static_cast<float>(ctas - n_tiles), 1e9f)) + 2));
-            while (lo < T) {
-                const int mid = (lo + T) >> 1;
-                if (total(mid) <= ctas) T = mid;
-                else lo = mid + 1;
+            if (p.n_prefix <= 32) {  // a lane a candidate
+#pragma unroll 1
+                while (lo < T) {
+                    const int step = (T - lo + 31) >> 5, t = min(T, lo + lane * step);
+                    const float inv = inverse(t);
+                    int k = 0;
+#pragma unroll 1
+                    for (int i = 0; i < p.n_prefix; ++i) k += units_of(scratch[i].y, scratch[i].z, inv);
+                    // the lowest that fits (T does, or is the most there is); all below do not
+                    const int at = __ffs(__ballot_sync(all, k * p.Hkv <= ctas || t == T)) - 1;
+                    T = min(T, lo + at * step);
+                    lo = at > 0 ? min(T, lo + (at - 1) * step + 1) : T;
+                }
+            } else {
+#pragma unroll 1
+                while (lo < T) {
+                    const int mid = (lo + T) >> 1;
+                    if (sum_on_lanes(mid) <= ctas) T = mid;
+                    else lo = mid + 1;
+                }
             }
         }
+        const float inv = inverse(T);
+#pragma unroll 1
         for (int f0 = 0; f0 < p.n_prefix; f0 += 32) {
             const int ff = f0 + lane;
-            const int k = ff < p.n_prefix ? units_of(scratch[ff].y, scratch[ff].z, T) * p.Hkv : 0;
+            const int k = ff < p.n_prefix ? units_of(scratch[ff].y, scratch[ff].z, inv) * p.Hkv : 0;
             int incl = k;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -300,13 +335,14 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         return;
     }
     // units of a prefix: by kv head, in it the tiles of two and then the one of one, by range
-    const int c = e.z, twos = e.y >> 1, r2 = ranges(kPrefixTwoCost * c, c, T), per_g = units_of(e.y, c, T);
-    const int rem = u - start, g = rem / per_g, rg = rem - g * per_g;
+    const float inv = inverse(T);
+    const int c = e.z, twos = e.y >> 1, r2 = ranges(kPrefixTwoCost, c, inv), per_g = units_of(e.y, c, inv);
+    const int rem = u - start, g = quotient(rem, per_g), rg = rem - g * per_g;
     const bool two = rg < twos * r2;
-    const int n = two ? r2 : ranges(kPrefixOneCost * c, c, T), t = two ? rg / r2 : twos, s = rg - t * r2;
+    const int n = two ? r2 : ranges(kPrefixOneCost, c, inv), t = two ? quotient(rg, r2) : twos, s = rg - t * r2;
     const int r0 = t * per_tile, here = min(per_tile, e.x - r0);
     if (lane == 0) {
-        const int each = c / n, more = c - each * n;  // the first `more` ranges get a chunk more
+        const int each = quotient(c, n), more = c - each * n;  // the first `more` ranges get a chunk more
         unit->f = f;
         unit->g = g;
         unit->s = s;
@@ -319,9 +355,11 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
         unit->shared = e.y > 2;
     }
     if (!p.of) {
+#pragma unroll 1
         for (int i = lane; i < here; i += 32) member[i] = r0 + i;
     } else {
         int seen = 0;
+#pragma unroll 1
         for (int b0 = 0; b0 < p.B && seen < r0 + here; b0 += 32) {
             const int v = map_of(b0);
             const unsigned m = __ballot_sync(all, v == f);
@@ -332,6 +370,7 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
     }
     __syncwarp();
     if (g == 0 && s == 0) {
+#pragma unroll 1
         for (int i = lane; i < here; i += 32) p.n_ranges[member[i]] = n;
     }
 }
@@ -648,7 +687,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             const int st = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
             const int mpt = p.mpt;
             // where row r of this stream's tile, or of the tile that the streams share, has its results
-            const int tile = x.two ? st : 0, m = r / p.G;
+            const int tile = x.two ? st : 0, m = (r * p.inv_G) >> 16;
             const bool valid_row = m < mpt && tile * mpt + m < x.members;
             long long at = 0;
             if (valid_row) {
@@ -657,9 +696,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             {   // Q rows into the 128-byte swizzled K-major layout, rows without a member zero
                 constexpr int PIECES = D / 8;  // 16-byte pieces of a row
                 const int n = (x.two ? 256 : 128) * PIECES;
-#pragma unroll 1
+#pragma unroll 4
                 for (int e = threadIdx.x; e < n; e += kSoftmaxThreads) {
-                    const int rr = (e / PIECES) & 127, t = e / (128 * PIECES), c = e % PIECES, mm = rr / p.G;
+                    const int rr = (e / PIECES) & 127, t = e / (128 * PIECES), c = e % PIECES, mm = (rr * p.inv_G) >> 16;
                     const bool there = mm < mpt && t * mpt + mm < x.members;
                     const __nv_bfloat16* src = p.Q + c * 8;
                     if (there) src += (static_cast<long long>(member[t * mpt + mm]) * p.Hq + x.g * p.G + rr - mm * p.G) * D;
@@ -849,6 +888,7 @@ dak_status launch_prefix(const void* Q, const dak_placement* P, const int* lens,
     p.Hkv = P->H_kv;
     p.G = H_q / P->H_kv;
     p.mpt = 128 / p.G;
+    p.inv_G = (65536 + p.G - 1) / p.G;
     p.L = P->L;
     p.n_prefix = P->B;
     p.n_pre = prefix_max_ranges(P);
