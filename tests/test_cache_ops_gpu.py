@@ -188,10 +188,12 @@ ACC_CASES = [
     (1, 32, 8, 128, 2049, [2049], False, 0, 0),
     (1, 1, 1, 128, 1, [1], True, 0, 0),
     (1, 7, 7, 64, 64, [64], False, 2, 64),
+    (170, 15, 3, 128, 70, [(7 * b) % 71 for b in range(170)], False, 3, 2),  # many heads, few splits each
+    (340, 16, 4, 64, 20, None, True, 0, 0),
 ]
 
 
-@pytest.mark.parametrize("case", ACC_CASES, ids=str)
+@pytest.mark.parametrize("case", ACC_CASES, ids=lambda c: str(c) if c[0] < 100 else f"{c[:5]}")
 def test_attn_acc(dak, case):
     import torch
     B, Hq, Hkv, D, L, lens, fp32, host, n_split = case
@@ -481,12 +483,13 @@ def _prefix_run(dak, B, Hq, Hkv, D, L, lens, plens, of, fp32):
     (45, 300, 32, 4, 128, False),  # of one and of two 128-row halves, some prefixes with no request
     (70, 140, 6, 3, 128, True),
     (200, 210, 1, 1, 64, False),   # more prefixes than tiles
+    (3, 180, 16, 2, 64, True),     # the merge by warps
 ])
 def test_attn_prefix_of_many(dak, P, B, Hq, Hkv, D, fp32):
     rng = np.random.default_rng(P)
     plens = rng.integers(0, 200, P)
     plens[:3] = [0, 1, 200]
-    of = np.where(rng.random(B) < 0.25, 4, rng.integers(-1, P, B))  # one prefix with many requests
+    of = np.where(rng.random(B) < 0.25, min(4, P - 1), rng.integers(-1, P, B))  # one prefix with many requests
     lens = rng.integers(0, 6, B)
     _prefix_run(dak, B, Hq, Hkv, D, 5, lens.tolist(), plens.tolist(), of.tolist(), fp32)
 
