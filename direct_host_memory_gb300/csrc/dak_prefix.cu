@@ -7,9 +7,9 @@
 //   S  = Q (128 rows x D, shared memory) . K^T (D x 64 keys, shared memory) -> TMEM, fp32
 //   P  = 2^(S * scale log2 e - m), written to TMEM as bf16
 //   O += P (TMEM) . V (64 keys x D, shared memory) -> TMEM, fp32
-// A CTA has two streams, each 128 threads (thread = row) and a warp that issues its products, with S,
-// P and O in TMEM. S is free as soon as its row is in a thread's registers, so that the next step's
-// scores are computed under the softmax, and P has two buffers where it fits.
+// A CTA has two streams, each 128 threads (thread = row) and a warp that issues its products, with S
+// and O in TMEM and P written over the S that it comes from. S has two buffers, so that the next
+// step's scores are there when a step's softmax ends.
 // With more than 128 rows the streams hold two row tiles and both go through every key; with fewer
 // they hold the same rows and take the steps in turn, and their results are merged in the CTA.
 //
@@ -392,8 +392,7 @@ __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_addr, uint3
     }
 }
 
-// Columns of the 16 keys k of part q of P, from where P begins: with three parts they lie over S (the
-// first two) and behind it.
+// Columns of the 16 keys k of part q of P, from where its S begins: three parts reach beyond it.
 template <int PARTS>
 __device__ __forceinline__ constexpr uint32_t p_column(int k, int q) {
     return PARTS == 1 ? k * 8 : q < 2 ? k * 16 + q * 8 : 64 + k * 8;
@@ -416,19 +415,17 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
     }
 }
 
-// One step of a row: its 64 scores (from `valid` on not real) into P in PARTS bf16 parts, with the row's
-// running sum and the reference that its exponents are taken against (log2 domain). `taken` is called
-// once the scores are in registers, `grown` when a row of the warp outgrows its reference, with the
-// factor for O, and `room` before P is written.
-template <int PARTS, class Taken, class Grown, class Room>
-__device__ __forceinline__ void softmax_step(uint32_t s_addr, uint32_t p_addr, int valid, float scale_log2, float& m_ref,
-                                             float& l, bool first, const Taken& taken, const Grown& grown, const Room& room) {
+// One step of a row: its 64 scores (from `valid` on not real) into P in PARTS bf16 parts, over them, with
+// the row's running sum and the reference that its exponents are taken against (log2 domain). `grown`
+// is called when a row of the warp outgrows its reference, with the factor for O.
+template <int PARTS, class Grown>
+__device__ __forceinline__ void softmax_step(uint32_t s_addr, int valid, float scale_log2, float& m_ref, float& l, bool first,
+                                             const Grown& grown) {
     float v[4][16];
 #pragma unroll
     for (int q = 0; q < 4; ++q) tmem_ld16(s_addr + q * 16, v[q]);
 #pragma unroll
     for (int q = 0; q < 4; ++q) tmem_wait(v[q]);
-    taken();
     if (valid < 64) {
 #pragma unroll
         for (int k = 0; k < 64; ++k) {
@@ -458,7 +455,6 @@ __device__ __forceinline__ void softmax_step(uint32_t s_addr, uint32_t p_addr, i
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float2 scale2 = make_float2(scale_log2, scale_log2), base2 = make_float2(-base, -base);
     const float2 minus = make_float2(-1.f, -1.f);
-    room();
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         uint32_t hi[8], lo[8], th[8];
@@ -476,9 +472,9 @@ __device__ __forceinline__ void softmax_step(uint32_t s_addr, uint32_t p_addr, i
                 th[k] = pack_bf16(r.x, r.y);
             }
         }
-        tmem_st8(p_addr + p_column<PARTS>(q, 0), hi);
-        if (PARTS >= 2) tmem_st8(p_addr + p_column<PARTS>(q, 1), lo);
-        if (PARTS == 3) tmem_st8(p_addr + p_column<PARTS>(q, 2), th);
+        tmem_st8(s_addr + p_column<PARTS>(q, 0), hi);
+        if (PARTS >= 2) tmem_st8(s_addr + p_column<PARTS>(q, 1), lo);
+        if (PARTS == 3) tmem_st8(s_addr + p_column<PARTS>(q, 2), th);
     }
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
@@ -533,7 +529,7 @@ struct PrefixCfg {
     static constexpr int kSmem = 2 * kTileBytes + kStages * kStage + 1024;
 };
 
-// F32: fp32 output, P in three bf16 parts, which leave S no columns of its own.
+// F32: fp32 output, P in three bf16 parts, which leave no room for a second S.
 template <int D, bool F32>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const PrefixParams p, const __grid_constant__ PrefixMaps maps) {
@@ -542,7 +538,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     uint8_t* ring = smem + 2 * C::kTileBytes;
-    __shared__ uint64_t full[NS], empty[NS], s_full[2], s_free[2], p_ready[2][2], pv_done[2][2];
+    __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_ready[2][2], pv_done[2];
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_flag;
     __shared__ PrefixUnit unit;
@@ -559,11 +555,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             mbar_init(&empty[s], 2);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&s_full[s], 1);
-            mbar_init(&s_free[s], 4);
+            mbar_init(&pv_done[s], 1);
             for (int b = 0; b < 2; ++b) {
+                mbar_init(&s_full[s][b], 1);
                 mbar_init(&p_ready[s][b], 4);
-                mbar_init(&pv_done[s][b], 1);
             }
         }
         fence_mbar_init();
@@ -577,10 +572,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     if (warp == 0) asm volatile("bar.arrive 5, %0;" ::"n"(kPrefixThreads) : "memory");
     else prefix_bar<5, kPrefixThreads>();
     tc_fence_after();
-    // TMEM columns: stream s has S at 128 s, P behind it (one part: two buffers of 32 columns; two parts:
-    // one of 64; three: over S and behind it) and O at 256 + D s
+    // TMEM columns: stream s has S at 128 s + 64 b (buffer b) with P over it, and O at 256 + D s
+    constexpr int SB = F32 ? 1 : 2;  // buffers of S
     int it0 = 0;  // stages used by earlier units
-    int used[2] = {0, 0}, filled[2][2] = {{0, 0}, {0, 0}};  // steps of a stream, and of each of its P buffers
+    int used[2] = {0, 0}, filled[2][2] = {{0, 0}, {0, 0}};  // steps of a stream, and of each of its S buffers
     for (int u = blockIdx.x;; u += gridDim.x) {
         if (warp == 0) plan_unit(p, u, reinterpret_cast<int4*>(smem), &unit, member);
         __syncthreads();
@@ -594,13 +589,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         // second part's products are free. An fp32 output takes three.
         const int steps = x.c1 - x.c0;
         const int stride = x.two ? 1 : 2;
-        const int p_bufs = !F32 && x.two ? 2 : 1;
-        const auto p_begin = [&](int i) { return F32 ? 0 : 64 + (p_bufs == 2 ? (i & 1) * 32 : 0); };  // of P of a step i
-        // P buffer of a stream's step i of this unit, and the parity of its barriers' phase
-        const auto buf = [&](int i) { return p_bufs == 2 ? i & 1 : 0; };
-        const auto par = [&](int f0, int f1, int i) {
-            return static_cast<uint32_t>((buf(i) ? f1 : f0) + (p_bufs == 2 ? i >> 1 : i)) & 1u;
-        };
+        // S buffer of a stream's step i of this unit, and the parity of its barriers' phase
+        const auto buf = [&](int i) { return i & (SB - 1); };
+        const auto par = [&](int f0, int f1, int i) { return static_cast<uint32_t>((buf(i) ? f1 : f0) + i / SB) & 1u; };
         const long long slab = static_cast<long long>(x.f) * p.Hkv + x.g;
         const int tier = slab < p.h_s ? 0 : 1;
 
@@ -648,15 +639,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             RingPos<NS> kpos(it0 + first), vpos(it0 + first);
             const auto qk = [&](int i) {  // S of this stream's step i
                 if (!wait_phase(&full[kpos.slot], kpos.phase, abort, p.st, X_MMA_FULL)) return false;
-                // S's columns are free: read, or with P over them read as P too
-                if (i > 0 && !(F32 ? wait_phase(&pv_done[st][0], par(f0, f1, i - 1), abort, p.st, X_MMA_PV)
-                                   : wait_phase(&s_free[st], (n0 + i - 1) & 1, abort, p.st, X_MMA_PV))) {
-                    return false;
-                }
+                // the product that read P in these columns is done
+                if (i >= SB && !wait_phase(&pv_done[st], (n0 + i - SB) & 1, abort, p.st, X_MMA_PV)) return false;
                 tc_fence_after();
                 if (leader) {
-                    issue_qk<D>(s_tmem, q_addr, ring_addr + kpos.slot * C::kStage);
-                    umma_commit(&s_full[st]);
+                    issue_qk<D>(s_tmem + buf(i) * 64, q_addr, ring_addr + kpos.slot * C::kStage);
+                    umma_commit(&s_full[st][buf(i)]);
                 }
                 __syncwarp();
                 kpos.advance(stride);
@@ -668,11 +656,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 if (!wait_phase(&p_ready[st][buf(i)], par(f0, f1, i), abort, p.st, X_MMA_P)) break;
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t p_tmem = s_tmem + p_begin(i), v = ring_addr + vpos.slot * C::kStage + C::kV;
+                    const uint32_t p_tmem = s_tmem + buf(i) * 64, v = ring_addr + vpos.slot * C::kStage + C::kV;
                     if (F32) issue_pv<D, 3>(o_tmem, p_tmem, v, i > 0);
                     else if (x.two) issue_pv<D, 1>(o_tmem, p_tmem, v, i > 0);
                     else issue_pv<D, 2>(o_tmem, p_tmem, v, i > 0);
-                    umma_commit(&pv_done[st][buf(i)]);
+                    umma_commit(&pv_done[st]);
                     // a stage is free when both streams have used it, or the one that does has said so twice
                     umma_commit(&empty[vpos.slot]);
                     if (!x.two) umma_commit(&empty[vpos.slot]);
@@ -718,7 +706,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             int i = 0;
             for (int j = x.two ? 0 : st; j < steps; j += stride, ++i) {
                 const int valid = min(64, x.len - (x.c0 + j) * 64);
-                ok = mbar_wait(&s_full[st], (n0 + i) & 1, abort, p.st, DAK_ERR_TIMEOUT, X_SM_S);
+                ok = mbar_wait(&s_full[st][buf(i)], par(f0, f1, i), abort, p.st, DAK_ERR_TIMEOUT, X_SM_S);
                 if (!__all_sync(0xffffffffu, ok)) {  // a wait ran out: the whole warp stops
                     ok = false;
                     break;
@@ -737,24 +725,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                const auto taken = [&] {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_free[st]);
-                };
-                const auto done = [&](int k) {  // the product of this stream's step k
-                    mbar_wait(&pv_done[st][buf(k)], par(f0, f1, k), abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);
+                // O so far, its last product done, to the new reference (of the product before that this
+                // step's scores tell that it is done, so that the phase waited for is the next one)
+                const auto grown = [&](float f) {
+                    mbar_wait(&pv_done[st], (n0 + i - 1) & 1, abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);
                     __syncwarp();
                     tc_fence_after();
-                };
-                // P's buffer is free; every product's end is waited for once and in order (a wait for one
-                // phase of a barrier says nothing while the phase before may be open)
-                const auto room = [&] {
-                    if (i >= p_bufs) done(i - p_bufs);
-                };
-                const auto grown = [&](float f) {  // O so far, its last product done, to the new reference
-                    if (p_bufs == 2 && i >= 2) done(i - 2);
-                    done(i - 1);
 #pragma unroll 1
                     for (int q = 0; q < D / 16; ++q) {
                         float o[16];
@@ -765,17 +741,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                         tmem_st16(o_addr + q * 16, o);
                     }
                 };
-                const uint32_t p_addr = s_addr + p_begin(i);
-                if (F32) softmax_step<3>(s_addr, p_addr, valid, p.scale_log2, m_ref, l, i == 0, taken, grown, room);
-                else if (x.two) softmax_step<1>(s_addr, p_addr, valid, p.scale_log2, m_ref, l, i == 0, taken, grown, room);
-                else softmax_step<2>(s_addr, p_addr, valid, p.scale_log2, m_ref, l, i == 0, taken, grown, room);
+                const uint32_t at_s = s_addr + buf(i) * 64;
+                if (F32) softmax_step<3>(at_s, valid, p.scale_log2, m_ref, l, i == 0, grown);
+                else if (x.two) softmax_step<1>(at_s, valid, p.scale_log2, m_ref, l, i == 0, grown);
+                else softmax_step<2>(at_s, valid, p.scale_log2, m_ref, l, i == 0, grown);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_ready[st][buf(i)]);
             }
-            for (int k = max(0, i - p_bufs); ok && k < i; ++k) {
-                ok = mbar_wait(&pv_done[st][buf(k)], par(f0, f1, k), abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);
+            for (int k = max(0, i - 2); ok && k < i; ++k) {  // in order: a wait for one phase says nothing
+                ok = mbar_wait(&pv_done[st], (n0 + k) & 1, abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);  // while the one before is open
             }
             __syncwarp();
             // ---- results
@@ -827,8 +803,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         for (int st = 0; st < 2; ++st) {
             const int n = x.two ? steps : (steps + 1 - st) / 2;
             used[st] += n;
-            filled[st][0] += p_bufs == 2 ? (n + 1) / 2 : n;
-            filled[st][1] += p_bufs == 2 ? n / 2 : 0;
+            filled[st][0] += (n + SB - 1) / SB;
+            filled[st][1] += SB == 2 ? n / 2 : 0;
         }
         tc_fence_before();
         __syncthreads();
