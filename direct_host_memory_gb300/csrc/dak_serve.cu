@@ -37,7 +37,10 @@ struct ServeParams {
 constexpr int kChunk = 64;
 constexpr int kConsumers = 4;
 constexpr int kServeThreads = 32 * (1 + kConsumers);
-constexpr int kServeStages = 2;
+// Chunks in flight of a CTA, by D: three CTAs an SM keep 192 or 144 KiB on their way. More queue in the
+// memory system (32 requests over 8K, D 128: 2 or 3 169 us, 4 185 us), fewer leave it idle (12 requests of
+// 16 kv heads over up to 2.5K, D 64: 18.8 us with 2, 17.2 with 3).
+constexpr int serve_stages(int D) { return D == 128 ? 2 : 3; }
 constexpr int kServeMaxStages = 5;
 
 enum : uint32_t { V_PROD_EMPTY = 0x61, V_CONS_FULL, V_DRAIN };
@@ -613,10 +616,14 @@ __global__ void __launch_bounds__(kMergeThreads) serve_merge_kernel(const MergeP
 constexpr int kServeHostCtas = 32, kServeHostWindow = 4;
 
 // Splits of a cache: at most 512 tokens each, so that requests of different lengths fill the SMs
-// alike and their tails are short, and more where dak_attn's rule fills the SMs better.
+// alike and their tails are short; 256 where that leaves the CTAs fewer than about four units each
+// (own caches of up to 1024 tokens behind a prefix, 32 requests: 34.5 -> 32.4 us for the whole call,
+// and 128 tokens 34.5 again); and more where dak_attn's rule fills the SMs better.
 constexpr int kServeSplitTokens = 512;
 static int serve_default_split(const dak_placement* KV) {
-    return std::min(kMaxSplits, std::max(dak_attn_default_split(KV), (KV->L + kServeSplitTokens - 1) / kServeSplitTokens));
+    const int64_t units = static_cast<int64_t>(KV->B) * KV->H_kv * ((KV->L + kServeSplitTokens - 1) / kServeSplitTokens);
+    const int tokens = units < 4ll * 3 * device_sm_count() ? kServeSplitTokens / 2 : kServeSplitTokens;
+    return std::min(kMaxSplits, std::max(dak_attn_default_split(KV), (KV->L + tokens - 1) / tokens));
 }
 
 static int split_tokens(int L, int n_split) { return ((L + n_split - 1) / n_split + kChunk - 1) / kChunk * kChunk; }
@@ -774,7 +781,7 @@ static dak_status serve_attention(const void* Q, const dak_placement* KV, const 
     if (!p.st) return DAK_ERR_CUDA;
     p.host_units = static_cast<unsigned>(static_cast<int64_t>(KV->h_s) * x.n_own);
     p.hbm_units = static_cast<unsigned>((slabs - KV->h_s) * x.n_own);
-    int W = (t && t->hbm_window > 0) ? std::min(t->hbm_window, kServeMaxStages) : kServeStages;
+    int W = (t && t->hbm_window > 0) ? std::min(t->hbm_window, kServeMaxStages) : serve_stages(D);
     if (!(t && t->hbm_window > 0) && slabs * x.n_own <= device_sm_count()) {
         W = std::max(W, std::min(p.split_len / kChunk, kServeMaxStages));  // a unit's chunks in flight at once
     }
