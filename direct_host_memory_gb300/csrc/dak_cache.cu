@@ -429,7 +429,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
     __shared__ int cnt[ENTRIES];
     __shared__ int wsum[NW];
     __shared__ int share[4];  // read by the cluster: newest position, equals, holes and movers
-    __shared__ int pick[2];
+    __shared__ int coarse[3][NW];  // read by the cluster: sums of 64 bins, from the top
+    __shared__ int pick[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cluster = CLUSTER ? n_cluster : 1, rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
     const long long slab = blockIdx.x / cluster;
@@ -503,43 +504,76 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
                 atomicAdd(&hist[pass][(key[r] >> shift) & digits], 1);
             }
         }
-        sync();
         // thread t: bins 2047 - 2t and 2046 - 2t, so that a scan by thread runs from the top
+        __syncthreads();
         const int hi = kBins - 1 - 2 * tid;
-        int c1, c0;
-        if (CLUSTER) {  // of all CTAs, the loads in flight together
-            int2 v[kEvictMaxCluster];
+        const int c1 = hist[pass][hi], c0 = hist[pass][hi - 1];
+        if (CLUSTER) {
+            // the warp of bins that the threshold lies in by the cluster's coarse sums, then its bins: all
+            // CTAs' 2048 bins by every CTA were three quarters of a pass's time
+            const int sum = __reduce_add_sync(0xffffffffu, c1 + c0);
+            if (lane == 0) coarse[pass][warp] = sum;
+            sync();
+            if (warp == 0) {
+                const auto scan_from_top = [&](int v) {  // inclusive
 #pragma unroll
-            for (int c = 0; c < kEvictMaxCluster; ++c) {
-                v[c] = make_int2(0, 0);
-                if (c < cluster) v[c] = ld_cluster2(&hist[pass][hi - 1], c);
-            }
-            c1 = c0 = 0;
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int u = __shfl_up_sync(0xffffffffu, v, o);
+                        if (lane >= o) v += u;
+                    }
+                    return v;
+                };
+                int v[kEvictMaxCluster], all = 0;
 #pragma unroll
-            for (int c = 0; c < kEvictMaxCluster; ++c) {
-                c0 += v[c].x;
-                c1 += v[c].y;
+                for (int c = 0; c < kEvictMaxCluster; ++c) v[c] = c < cluster ? ld_cluster(&coarse[pass][lane], c) : 0;
+#pragma unroll
+                for (int c = 0; c < kEvictMaxCluster; ++c) all += v[c];
+                const int upto = scan_from_top(all);
+                const int at = __ffs(__ballot_sync(0xffffffffu, upto >= want)) - 1;  // its warp
+                const int above_it = __shfl_sync(0xffffffffu, upto - all, at);
+                const int top = kBins - 1 - 2 * (at * 32 + lane);
+                int2 w[kEvictMaxCluster];
+#pragma unroll
+                for (int c = 0; c < kEvictMaxCluster; ++c) {
+                    w[c] = c < cluster ? ld_cluster2(&hist[pass][top - 1], c) : make_int2(0, 0);
+                }
+                int d1 = 0, d0 = 0;
+#pragma unroll
+                for (int c = 0; c < kEvictMaxCluster; ++c) {
+                    d0 += w[c].x;
+                    d1 += w[c].y;
+                }
+                const int before = above_it + scan_from_top(d1 + d0) - d1 - d0;
+                if (before < want && want <= before + d1) {
+                    pick[0] = top;
+                    pick[1] = want - before;
+                    pick[2] = d1;
+                } else if (before + d1 < want && want <= before + d1 + d0) {
+                    pick[0] = top - 1;
+                    pick[1] = want - before - d1;
+                    pick[2] = d0;
+                }
             }
         } else {
-            c1 = hist[pass][hi];
-            c0 = hist[pass][hi - 1];
-        }
-        int incl = c1 + c0;
+            int incl = c1 + c0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) wsum[warp] = incl;
-        __syncthreads();
-        int before = lane < warp ? wsum[lane] : 0;
-        before = __reduce_add_sync(0xffffffffu, before) + incl - c1 - c0;  // keys above this thread's bins
-        if (before < want && want <= before + c1) {
-            pick[0] = hi;
-            pick[1] = want - before;
-        } else if (before + c1 < want && want <= before + c1 + c0) {
-            pick[0] = hi - 1;
-            pick[1] = want - before - c1;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (lane == 31) wsum[warp] = incl;
+            __syncthreads();
+            int before = lane < warp ? wsum[lane] : 0;
+            before = __reduce_add_sync(0xffffffffu, before) + incl - c1 - c0;  // keys above this thread's bins
+            if (before < want && want <= before + c1) {
+                pick[0] = hi;
+                pick[1] = want - before;
+                pick[2] = c1;
+            } else if (before + c1 < want && want <= before + c1 + c0) {
+                pick[0] = hi - 1;
+                pick[1] = want - before - c1;
+                pick[2] = c0;
+            }
         }
         __syncthreads();
         prefix |= static_cast<uint32_t>(pick[0]) << shift;
@@ -563,29 +597,35 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
         return all;
     };
     const uint32_t below = (1u << lane) - 1;
-    // the lowest `want` of the keys at the threshold
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const uint32_t bal = __ballot_sync(0xffffffffu, s0 + r * kClusterThreads < n && key[r] == prefix);
-        if (lane == 0) cnt[r * NW + warp] = __popc(bal);
-    }
-    __syncthreads();
-    int all = scan();
-    int eq_before = 0;
-    if (CLUSTER) {
-        if (tid == 0) share[1] = all;
-        sync();
-        const int v = of_cluster(&share[1], 0);
-        eq_before = __reduce_add_sync(0xffffffffu, lane < rank ? v : 0);
-    }
     uint32_t kept = 0;  // bit r
+    if (pick[2] == want) {  // every key at the threshold is kept, as where it is no other's
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const bool in = s0 + r * kClusterThreads < n, eq = in && key[r] == prefix;
-        const uint32_t bal = __ballot_sync(0xffffffffu, eq);
-        bool k = in && key[r] > prefix;
-        if (bal && eq) k = eq_before + cnt[r * NW + warp] + __popc(bal & below) < want;
-        kept |= static_cast<uint32_t>(k) << r;
+        for (int r = 0; r < R; ++r) {
+            kept |= static_cast<uint32_t>(s0 + r * kClusterThreads < n && key[r] >= prefix) << r;
+        }
+    } else {  // the lowest `want` of them
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t bal = __ballot_sync(0xffffffffu, s0 + r * kClusterThreads < n && key[r] == prefix);
+            if (lane == 0) cnt[r * NW + warp] = __popc(bal);
+        }
+        __syncthreads();
+        const int all = scan();
+        int eq_before = 0;
+        if (CLUSTER) {
+            if (tid == 0) share[1] = all;
+            sync();
+            const int v = of_cluster(&share[1], 0);
+            eq_before = __reduce_add_sync(0xffffffffu, lane < rank ? v : 0);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = s0 + r * kClusterThreads < n, eq = in && key[r] == prefix;
+            const uint32_t bal = __ballot_sync(0xffffffffu, eq);
+            bool k = in && key[r] > prefix;
+            if (bal && eq) k = eq_before + cnt[r * NW + warp] + __popc(bal & below) < want;
+            kept |= static_cast<uint32_t>(k) << r;
+        }
     }
     __syncthreads();
     // holes (low half of a count) and movers (high half); both fit: a CTA has at most 16384 slots
@@ -597,7 +637,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
         if (lane == 0) cnt[r * NW + warp] = __popc(bh) | (__popc(bm) << 16);
     }
     __syncthreads();
-    all = scan();
+    const int all = scan();
     int h_before = 0, m_before = 0, total = all & 0xFFFF;
     if (CLUSTER) {
         if (tid == 0) share[2] = all;
