@@ -173,8 +173,8 @@ __device__ __forceinline__ void report_prefix(const PrefixParams& p, int b) {
     report(p.st, DAK_ERR_BOUNDS, (0x9F1Full << 32) | static_cast<unsigned>(b));
 }
 
-// n / d for 0 <= n < 2^21 (a count of requests or units: their rows' partials alone would take more
-// memory than there is), a few instructions where the integer division is dozens.
+// n / d for n >= 0 and quotients below 2^21 (the float quotient is off by less than one, which the
+// remainder puts right), a few instructions where the integer division is dozens.
 __device__ __forceinline__ int quotient(int n, int d) {
     const int q = static_cast<int>(static_cast<float>(n) * __fdividef(1.f, static_cast<float>(d))), r = n - q * d;
     return q + (r >= d) - (r < 0);
@@ -298,7 +298,7 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
             if (p.n_prefix <= 32) {  // a lane a candidate
 #pragma unroll 1
                 while (lo < T) {
-                    const int step = (T - lo + 31) >> 5, t = min(T, lo + lane * step);
+                    const int step = (T - lo + 30) / 31, t = min(T, lo + lane * step);
                     const float inv = inverse(t);
                     int k = 0;
 #pragma unroll 1

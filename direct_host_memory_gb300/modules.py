@@ -130,7 +130,10 @@ class SplitK_FlashAttn(torch.nn.Module):
         return _lib.dak_kv_evict(self.placement, seq_lens, n_keep, n_recent, self.weights, self.slot_pos)[0]
 
     def _serve(self, q, seq_lens, scale, prefix, prefix_of, prefix_lens):
-        tun = dict(self.tuning, n_split=self._given_split) if self._given_split else self.tuning
+        # whether the kernel before writes the cache is not known here: no programmatic launch
+        tun = {k: v for k, v in self.tuning.items() if k not in ("pdl", "link")}
+        if self._given_split:
+            tun["n_split"] = self._given_split
         kw = dict(acc_in=self.weights, acc_out=self.weights, seq_lens=seq_lens, scale=scale, o_fp32=self.fp32_out,
                   tuning=tun or None)
         if prefix is None:

@@ -621,6 +621,13 @@ def test_calls_refused_before_a_launch(dak):
                  lambda: dak.dak_attn_acc(Q, kv, acc_out=acc[:, :1]), lambda: dak.dak_attn_acc(Q, kv, seq_lens=lens.long())):
         with pytest.raises(ValueError):
             call()
+    for heads, status in ((3, 1), (34, 7)):  # not a multiple of the kv heads; 17 query heads a kv head
+        with pytest.raises(dak.DakError) as e:
+            dak.dak_attn_acc(torch.zeros(2, heads, 64, dtype=torch.bfloat16, device="cuda"), kv)
+        assert e.value.status == status
+        with pytest.raises(dak.DakError) as e:
+            dak.dak_attn_prefix(torch.zeros(2, heads, 64, dtype=torch.bfloat16, device="cuda"), kv, kv)
+        assert e.value.status == status
     _ok(dak)
     kv.free()
 
