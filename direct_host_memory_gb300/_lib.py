@@ -657,11 +657,10 @@ def _t():
 _torch = _get_device = _get_stream = _alloc = _free = _empty = None
 
 
-def _raw_stream(stream, dev):
-    """Address of the stream (None: the current one of the current device, which is dev)."""
-    if stream is None:
-        return _get_stream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+def _current(stream):
+    """The stream as the current one: a call that is given a stream makes its results and its
+    workspace for that stream too."""
+    return _torch.cuda.stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 def _kv_shape(KV, name="KV"):
@@ -715,6 +714,9 @@ def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slot
     slot_pos int32 CUDA [B][H_kv][L], updated in place. Returns q_out, bf16, shaped as q (None
     without q)."""
     torch = _torch or _t()
+    if stream is not None:
+        with _current(stream):
+            return dak_kv_append_rope(KV, rope, q, k_new, v_new, slots, positions, n_new, q_out, slot_pos)
     B, Hkv, D, L = _kv_shape(KV)
     T = k_new.shape[1] if k_new.ndim == 4 else 1
     dtype, dev = k_new.dtype, _get_device()
@@ -740,7 +742,7 @@ def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slot
     _check(lib.dak_kv_append_rope(KV.handle, rope, qa, ka, va, fp32, T, Hq, qp, kp, vp,
                                   _arg(slots, "slots", i32, per_request, dev), _arg(positions, "positions", i32, per_request, dev),
                                   _arg(n_new, "n_new", i32, per_request, dev), oa,
-                                  _arg(slot_pos, "slot_pos", i32, (B, Hkv, L), dev), _raw_stream(stream, dev)), "dak_kv_append_rope")
+                                  _arg(slot_pos, "slot_pos", i32, (B, Hkv, L), dev), _get_stream(dev)), "dak_kv_append_rope")
     return q_out
 
 
@@ -756,6 +758,10 @@ def dak_kv_evict(KV: Placement, seq_lens, n_keep: int, n_recent: int, acc, slot_
     given; seq_lens int32 CUDA [B]. Returns (lens_out [B], src_out [B][H_kv][n_keep]), int32:
     the new lengths, and the slot each kept row came from (-1 past the length)."""
     torch = _torch or _t()
+    if stream is not None:
+        with _current(stream):
+            return dak_kv_evict(KV, seq_lens, n_keep, n_recent, acc, slot_pos, acc_out, slot_pos_out, lens_out, src_out,
+                                workspace)
     B, Hkv, _, L = _kv_shape(KV)
     n_keep = int(n_keep)
     if not 1 <= n_keep <= L:
@@ -771,7 +777,7 @@ def dak_kv_evict(KV: Placement, seq_lens, n_keep: int, n_recent: int, acc, slot_
             aa if acc_out is None else _arg(acc_out, "acc_out", f32, table, dev), pa,
             pa if slot_pos_out is None else _arg(slot_pos_out, "slot_pos_out", i32, table, dev),
             _arg(lens_out, "lens_out", i32, per_request, dev), _arg(src_out, "src_out", i32, kept, dev))
-    st = _raw_stream(stream, dev)
+    st = _get_stream(dev)
     if workspace is not None:
         _check(lib.dak_kv_evict(KV.handle, *args, *_given(workspace, dev), st), "dak_kv_evict")
         return lens_out, src_out
@@ -819,13 +825,16 @@ def dak_attn_acc(Q, KV: Placement, acc_in=None, acc_out=None, seq_lens=None, sca
     kv head, to acc_in fp32 [B][H_kv][L] (None = zeros). Returns (O, acc_out); acc_out may be
     acc_in; without one, a new tensor that is zero behind each request's tokens."""
     torch = _torch or _t()
+    if stream is not None:
+        with _current(stream):
+            return dak_attn_acc(Q, KV, acc_in, acc_out, seq_lens, scale, O, o_fp32, workspace, tuning)
     dev = _get_device()
     if acc_out is None:
         B, Hkv, _, L = _kv_shape(KV)
         acc_out = torch.zeros((B, Hkv, L), dtype=torch.float32, device=Q.device)
     O, qa, oa, la, ia, aa = _serve_args(Q, KV, O, o_fp32, seq_lens, acc_in, acc_out, dev)
     Hq = Q.shape[1]
-    st, tun = _raw_stream(stream, dev), _tuning(tuning)
+    st, tun = _get_stream(dev), _tuning(tuning)
     if workspace is not None:
         _check(lib.dak_attn_acc(qa, KV.handle, la, Hq, scale, oa, bool(o_fp32), ia, aa, *_given(workspace, dev), tun, st),
                "dak_attn_acc")
@@ -854,6 +863,10 @@ def dak_attn_prefix(Q, KV: Placement, prefix: Placement, prefix_of=None, prefix_
     all its requests. acc_out, if given, takes acc_in (None = zeros) plus the weights of the own
     cache's positions, as in dak_attn_acc. Returns O."""
     torch = _torch or _t()
+    if stream is not None:
+        with _current(stream):
+            return dak_attn_prefix(Q, KV, prefix, prefix_of, prefix_lens, seq_lens, acc_in, acc_out, scale, O, o_fp32,
+                                   workspace, tuning)
     dev = _get_device()
     if acc_in is not None and acc_out is None:
         raise ValueError("acc_in without acc_out")
@@ -862,7 +875,7 @@ def dak_attn_prefix(Q, KV: Placement, prefix: Placement, prefix_of=None, prefix_
     pshape = _kv_shape(prefix, "prefix")
     args = (qa, KV.handle, la, prefix.handle, _arg(prefix_lens, "prefix_lens", torch.int32, (pshape[0],), dev),
             _arg(prefix_of, "prefix_of", torch.int32, (Q.shape[0],), dev), Hq, scale, oa, bool(o_fp32), ia, aa)
-    st, tun = _raw_stream(stream, dev), _tuning(tuning)
+    st, tun = _get_stream(dev), _tuning(tuning)
     if workspace is not None:
         _check(lib.dak_attn_prefix(*args, *_given(workspace, dev), tun, st), "dak_attn_prefix")
         return O

@@ -599,6 +599,20 @@ def test_graphs_and_streams_with_memory_of_their_own(dak):
         junk += [torch.full((1 << 22,), 1e30, device="cuda") for _ in range(4)]
         torch.cuda.synchronize()
         assert torch.equal(O, want[0][0]) and torch.equal(acc, want[0][1]) and torch.equal(O2, want[1][0])
+        # results that a call makes itself are made for its stream
+        junk += [torch.full((1 << 22,), 1e30, device="cuda") for _ in range(4)]
+        got = dak.dak_attn_acc(Q, kv, seq_lens=lens[0], tuning=dict(n_split=20), stream=stream)
+        got2 = dak.dak_attn_prefix(Q, kv, pre, seq_lens=lens[1], stream=stream)
+        assert torch.cuda.current_stream() != s
+        s.synchronize()
+        assert torch.equal(got[0], want[0][0]) and torch.equal(got[1], want[0][1]) and torch.equal(got2, want[1][0])
+    with torch.cuda.stream(s):
+        tab = torch.arange(L, dtype=torch.int32, device="cuda").repeat(B, Hkv, 1)
+        keep, src = dak.dak_kv_evict(kv, lens[0], 600, 10, want[0][1].clone(), tab.clone())
+        apart = (want[0][1].clone(), torch.empty_like(tab), torch.empty_like(want[0][1]))
+    again, src2 = dak.dak_kv_evict(kv, lens[0], 600, 10, apart[0], tab, slot_pos_out=apart[1], acc_out=apart[2], stream=s)
+    s.synchronize()
+    assert torch.equal(keep, again) and torch.equal(src, src2) and keep.tolist() == [600, 600, 0, 3]
     _ok(dak)
     kv.free()
     pre.free()
