@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8) append_rope_kernel(
     const long long token = blockIdx.x;
     const int R = p.rope.rot_dim, half = R / 2;
     const int heads = p.Hq + 2 * p.Hkv, n_units = heads * PAIRS, stride = gridDim.y * kRopeThreads;
+    grid_dep_wait();  // launched while the previous kernel ends
     const int n_new = p.n_new ? p.n_new[b] : p.T, slot = p.slots[b], first = p.positions ? p.positions[b] : slot;
     bool ready = false, in_range = false;
     long long row = 0, pos = 0;
@@ -201,10 +202,19 @@ __global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8) append_rope_kernel(
 }
 
 template <int D, bool F32>
-static void launch_append_rope(const RopeParams& p, dim3 grid, cudaStream_t s) {
-    if (p.rope.interleaved) append_rope_kernel<D, F32, kRopeInterleaved><<<grid, kRopeThreads, 0, s>>>(p);
-    else if (p.rope.rot_dim == D) append_rope_kernel<D, F32, kRopeSplit><<<grid, kRopeThreads, 0, s>>>(p);
-    else append_rope_kernel<D, F32, kRopePart><<<grid, kRopeThreads, 0, s>>>(p);
+static cudaError_t launch_append_rope(const RopeParams& p, dim3 grid, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kRopeThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (p.rope.interleaved) return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopeInterleaved>, p);
+    if (p.rope.rot_dim == D) return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopeSplit>, p);
+    return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopePart>, p);
 }
 
 // ------------------------------------------------------------------------------------
@@ -442,6 +452,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) evict_kernel(const EvictPa
     const int cluster = CLUSTER ? n_cluster : 1, rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
     const long long slab = blockIdx.x / cluster;
     const int b = static_cast<int>(slab / p.Hkv), g = static_cast<int>(slab - static_cast<long long>(b) * p.Hkv);
+    grid_dep_wait();  // launched while the previous kernel ends
     const int n = min(max(p.seq_lens[b], 0), p.L), keep = p.n_keep;
     const float* acc = p.acc + slab * p.L;
     const int* pos = p.pos + slab * p.L;
@@ -734,17 +745,20 @@ static cudaError_t launch_evict(const EvictParams& p, unsigned slabs, int cluste
     cfg.gridDim = dim3(slabs * static_cast<unsigned>(cluster));
     cfg.blockDim = dim3(kClusterThreads);
     cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     if (cluster == 1) {
         return move ? cudaLaunchKernelEx(&cfg, evict_kernel<D, R, false, true>, p, 1)
                     : cudaLaunchKernelEx(&cfg, evict_kernel<D, R, false, false>, p, 1);
     }
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
     return move ? cudaLaunchKernelEx(&cfg, evict_kernel<D, R, true, true>, p, cluster)
                 : cudaLaunchKernelEx(&cfg, evict_kernel<D, R, true, false>, p, cluster);
 }
@@ -932,9 +946,8 @@ extern "C" dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope
     const int64_t room = std::max<int64_t>(1, 8ll * device_sm_count() / tokens);
     const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(std::min<int64_t>(std::min(blocks, 16), room)));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (D == 128) in_fp32 ? launch_append_rope<128, true>(p, grid, s) : launch_append_rope<128, false>(p, grid, s);
-    else in_fp32 ? launch_append_rope<64, true>(p, grid, s) : launch_append_rope<64, false>(p, grid, s);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(D == 128 ? (in_fp32 ? launch_append_rope<128, true>(p, grid, s) : launch_append_rope<128, false>(p, grid, s))
+                                : (in_fp32 ? launch_append_rope<64, true>(p, grid, s) : launch_append_rope<64, false>(p, grid, s)));
 }
 
 // Workspace: per slab a count and the holes and movers, of which there are at most

@@ -554,8 +554,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     int* member = reinterpret_cast<int*>(ring);
     volatile int* abort = &abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    grid_dep_launch();  // the pass over the own caches fills SMs as they become free
-
     if (threadIdx.x == 32) {
         abort_flag = 0;
         for (int s = 0; s < NS; ++s) {
@@ -580,6 +578,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     if (warp == 0) asm volatile("bar.arrive 5, %0;" ::"n"(kPrefixThreads) : "memory");
     else prefix_bar<5, kPrefixThreads>();
     tc_fence_after();
+    grid_dep_wait();  // launched while the previous kernel ends
+    grid_dep_launch();  // the pass over the own caches fills SMs as they become free
     // TMEM columns: stream s has S at 128 s + 64 b (buffer b) with P over it, and O at 256 + D s
     constexpr int SB = F32 ? 1 : 2;  // buffers of S
     int it0 = 0;  // stages used by earlier units
@@ -853,8 +853,17 @@ static cudaError_t launch_prefix_d(const PrefixParams& p, const PrefixMaps& maps
     static SmemLimit limit;
     const cudaError_t e = limit.raise(reinterpret_cast<const void*>(k), PrefixCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
-    k<<<grid, kPrefixThreads, PrefixCfg<D>::kSmem, s>>>(p, maps);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kPrefixThreads);
+    cfg.dynamicSmemBytes = PrefixCfg<D>::kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, p, maps);
 }
 
 dak_status launch_prefix(const void* Q, const dak_placement* P, const int* lens, const int* of, int B, int H_q,

@@ -28,6 +28,7 @@ struct ServeParams {
     int n_host_ctas, n_hbm_ctas, host_window, hbm_window;
     unsigned host_units, hbm_units;
     int wait_newest;  // as in dak_attn (tuning pdl 2)
+    int wait_first;   // without programmatic launch asked for: the previous kernel may write anything
     int wait_late;    // the previous kernel is the call's prefix pass: only this grid's end waits for it
     DevStatus* st;
     unsigned* link;
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(kServeThreads, NB == 1 ? 3 : 2) serve_kernel(c
         fence_mbar_init();
     }
     __syncthreads();
+    if (p.wait_first) grid_dep_wait();
     grid_dep_launch();
 
     if (warp == 0) {
@@ -636,7 +638,7 @@ static int serve_smem_bytes(int W, int G) {
 }
 
 template <int D, int NB, int PARTS>
-static cudaError_t launch_serve(const ServeParams& p, int W, bool pdl, cudaStream_t s) {
+static cudaError_t launch_serve(const ServeParams& p, int W, cudaStream_t s) {
     static SmemLimit limit;
     auto k = serve_kernel<D, NB, PARTS>;
     const cudaError_t e = limit.raise(reinterpret_cast<const void*>(k), serve_smem_bytes<D>(kServeMaxStages, 8 * NB));
@@ -650,7 +652,7 @@ static cudaError_t launch_serve(const ServeParams& p, int W, bool pdl, cudaStrea
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, p);
 }
 
@@ -797,7 +799,7 @@ static dak_status serve_attention(const void* Q, const dak_placement* KV, const 
     p.n_hbm_ctas = sc.n_hbm_ctas;
     p.host_window = sc.host_window;
     p.hbm_window = sc.hbm_window;
-    const bool pdl = P || (t && t->pdl > 0);
+    p.wait_first = !P && !(t && t->pdl > 0);
     p.wait_newest = !P && t && t->pdl == 2;
     p.wait_late = P != nullptr;
     if (link && link->ctr) {
@@ -807,11 +809,11 @@ static dak_status serve_attention(const void* Q, const dak_placement* KV, const 
     const int Wl = std::max(p.host_window, p.hbm_window);
     cudaError_t e;
     if (D == 128) {
-        e = G <= 8 ? (o_fp32 ? launch_serve<128, 1, 3>(p, Wl, pdl, stream) : launch_serve<128, 1, 2>(p, Wl, pdl, stream))
-                   : (o_fp32 ? launch_serve<128, 2, 3>(p, Wl, pdl, stream) : launch_serve<128, 2, 2>(p, Wl, pdl, stream));
+        e = G <= 8 ? (o_fp32 ? launch_serve<128, 1, 3>(p, Wl, stream) : launch_serve<128, 1, 2>(p, Wl, stream))
+                   : (o_fp32 ? launch_serve<128, 2, 3>(p, Wl, stream) : launch_serve<128, 2, 2>(p, Wl, stream));
     } else {
-        e = G <= 8 ? (o_fp32 ? launch_serve<64, 1, 3>(p, Wl, pdl, stream) : launch_serve<64, 1, 2>(p, Wl, pdl, stream))
-                   : (o_fp32 ? launch_serve<64, 2, 3>(p, Wl, pdl, stream) : launch_serve<64, 2, 2>(p, Wl, pdl, stream));
+        e = G <= 8 ? (o_fp32 ? launch_serve<64, 1, 3>(p, Wl, stream) : launch_serve<64, 1, 2>(p, Wl, stream))
+                   : (o_fp32 ? launch_serve<64, 2, 3>(p, Wl, stream) : launch_serve<64, 2, 2>(p, Wl, stream));
     }
     if (e != cudaSuccess) return cuda_status(e);
     if (link && link->signals && p.link) *link->signals = p.n_host_ctas;
