@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     uint8_t* ring = smem + 2 * C::kTileBytes;
-    __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_ready[2][2], pv_done[2];
+    __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_ready[2][2], pv_done[2][2];
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_flag;
     __shared__ PrefixUnit unit;
@@ -561,10 +561,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             mbar_init(&empty[s], 2);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&pv_done[s], 1);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&s_full[s][b], 1);
                 mbar_init(&p_ready[s][b], 4);
+                mbar_init(&pv_done[s][b], 1);
             }
         }
         fence_mbar_init();
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     // TMEM columns: stream s has S at 128 s + 64 b (buffer b) with P over it, and O at 256 + D s
     constexpr int SB = F32 ? 1 : 2;  // buffers of S
     int it0 = 0;  // stages used by earlier units
-    int used[2] = {0, 0}, filled[2][2] = {{0, 0}, {0, 0}};  // steps of a stream, and of each of its S buffers
+    int filled[2][2] = {{0, 0}, {0, 0}};  // steps of each stream by its S buffers
     for (int u = blockIdx.x;; u += gridDim.x) {
         if (warp == 0) plan_unit(p, u, reinterpret_cast<int4*>(smem), &unit, member);
         __syncthreads();
@@ -597,7 +597,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         // second part's products are free. An fp32 output takes three.
         const int steps = x.c1 - x.c0;
         const int stride = x.two ? 1 : 2;
-        // S buffer of a stream's step i of this unit, and the parity of its barriers' phase
+        // S buffer of a stream's step i of this unit, and the parity of its barriers' phase. Each buffer
+        // has barriers of its own: a wait by parity is right only where the phase before is known to be
+        // over and the one after not to be, and steps i and i + 2 of a buffer wait for each other.
         const auto buf = [&](int i) { return i & (SB - 1); };
         const auto par = [&](int f0, int f1, int i) { return static_cast<uint32_t>((buf(i) ? f1 : f0) + i / SB) & 1u; };
         const long long slab = static_cast<long long>(x.f) * p.Hkv + x.g;
@@ -643,12 +645,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             const uint32_t q_addr = smem_u32(smem) + (x.two ? st * C::kTileBytes : 0), ring_addr = smem_u32(ring);
             const uint32_t s_tmem = tmem + st * 128, o_tmem = tmem + 256 + st * D;
             const int first = x.two ? 0 : st, mine = first < steps ? (steps - first + stride - 1) / stride : 0;
-            const int n0 = used[st], f0 = filled[st][0], f1 = filled[st][1];
+            const int f0 = filled[st][0], f1 = filled[st][1];
             RingPos<NS> kpos(it0 + first), vpos(it0 + first);
             const auto qk = [&](int i) {  // S of this stream's step i
                 if (!wait_phase(&full[kpos.slot], kpos.phase, abort, p.st, X_MMA_FULL)) return false;
                 // the product that read P in these columns is done
-                if (i >= SB && !wait_phase(&pv_done[st], (n0 + i - SB) & 1, abort, p.st, X_MMA_PV)) return false;
+                if (i >= SB && !wait_phase(&pv_done[st][buf(i)], par(f0, f1, i - SB), abort, p.st, X_MMA_PV)) return false;
                 tc_fence_after();
                 if (leader) {
                     issue_qk<D>(s_tmem + buf(i) * 64, q_addr, ring_addr + kpos.slot * C::kStage);
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     if (F32) issue_pv<D, 3>(o_tmem, p_tmem, v, i > 0);
                     else if (x.two) issue_pv<D, 1>(o_tmem, p_tmem, v, i > 0);
                     else issue_pv<D, 2>(o_tmem, p_tmem, v, i > 0);
-                    umma_commit(&pv_done[st]);
+                    umma_commit(&pv_done[st][buf(i)]);
                     // a stage is free when both streams have used it, or the one that does has said so twice
                     umma_commit(&empty[vpos.slot]);
                     if (!x.two) umma_commit(&empty[vpos.slot]);
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             }
             const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
             const uint32_t s_addr = tmem + lanes + st * 128, o_addr = tmem + lanes + 256 + st * D;
-            const int n0 = used[st], f0 = filled[st][0], f1 = filled[st][1];
+            const int f0 = filled[st][0], f1 = filled[st][1];
             float m_ref = -INFINITY, l = 0.f;
             bool ok = true;
             int i = 0;
@@ -733,10 +735,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                // O so far, its last product done, to the new reference (of the product before that this
-                // step's scores tell that it is done, so that the phase waited for is the next one)
+                // O so far, its last product done, to the new reference
                 const auto grown = [&](float f) {
-                    mbar_wait(&pv_done[st], (n0 + i - 1) & 1, abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);
+                    mbar_wait(&pv_done[st][buf(i - 1)], par(f0, f1, i - 1), abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
@@ -758,8 +759,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_ready[st][buf(i)]);
             }
-            for (int k = max(0, i - 2); ok && k < i; ++k) {  // in order: a wait for one phase says nothing
-                ok = mbar_wait(&pv_done[st], (n0 + k) & 1, abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);  // while the one before is open
+            for (int k = max(0, i - SB); ok && k < i; ++k) {  // one phase of each buffer's
+                ok = mbar_wait(&pv_done[st][buf(k)], par(f0, f1, k), abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);
             }
             __syncwarp();
             // ---- results
@@ -810,7 +811,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
             const int n = x.two ? steps : (steps + 1 - st) / 2;
-            used[st] += n;
             filled[st][0] += (n + SB - 1) / SB;
             filled[st][1] += SB == 2 ? n / 2 : 0;
         }
