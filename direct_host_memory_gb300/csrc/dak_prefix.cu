@@ -429,23 +429,38 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
 template <int PARTS, class Grown>
 __device__ __forceinline__ void softmax_step(uint32_t s_addr, int valid, float scale_log2, float& m_ref, float& l, bool first,
                                              const Grown& grown) {
-    float v[4][16];
+    // with three parts O is in registers too, which leaves none for all scores: they are read twice
+    constexpr bool TWICE = PARTS == 3;
+    float v[TWICE ? 1 : 4][16];
+    const auto mask = [&](int q) {
+        if (valid < 64) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) tmem_ld16(s_addr + q * 16, v[q]);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) tmem_wait(v[q]);
-    if (valid < 64) {
-#pragma unroll
-        for (int k = 0; k < 64; ++k) {
-            if (k >= valid) v[k >> 4][k & 15] = -INFINITY;
+            for (int k = 0; k < 16; ++k) {
+                if (q * 16 + k >= valid) v[TWICE ? 0 : q][k] = -INFINITY;
+            }
         }
+    };
+    const auto read_again = [&](int q) {
+        tmem_ld16(s_addr + q * 16, v[0]);
+        tmem_wait(v[0]);
+        mask(q);
+    };
+    if (!TWICE) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld16(s_addr + q * 16, v[TWICE ? 0 : q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_wait(v[TWICE ? 0 : q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mask(q);
     }
     float mx[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        mx[q] = fmaxf(v[q][0], v[q][1]);
+        if (TWICE) read_again(q);
+        const float(&x)[16] = v[TWICE ? 0 : q];
+        mx[q] = fmaxf(x[0], x[1]);
 #pragma unroll
-        for (int k = 2; k < 16; k += 2) mx[q] = max3(mx[q], v[q][k], v[q][k + 1]);
+        for (int k = 2; k < 16; k += 2) mx[q] = max3(mx[q], x[k], x[k + 1]);
     }
     const float m_new = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale_log2;
     // the reference only moves when a row's maximum outgrows it by 2^8: until then the sums just
@@ -466,9 +481,11 @@ __device__ __forceinline__ void softmax_step(uint32_t s_addr, int valid, float s
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         uint32_t hi[8], lo[8], th[8];
+        if (TWICE) read_again(q);
+        const float(&x)[16] = v[TWICE ? 0 : q];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float2 e = fma2(make_float2(v[q][2 * k], v[q][2 * k + 1]), scale2, base2);
+            const float2 e = fma2(make_float2(x[2 * k], x[2 * k + 1]), scale2, base2);
             const float2 w = make_float2(exp2_ftz(e.x), exp2_ftz(e.y));
             sum[k & 1] = add2(sum[k & 1], w);
             hi[k] = pack_bf16(w.x, w.y);
@@ -667,7 +684,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 tc_fence_after();
                 if (leader) {
                     const uint32_t p_tmem = s_tmem + buf(i) * 64, v = ring_addr + vpos.slot * C::kStage + C::kV;
-                    if (F32) issue_pv<D, 3>(o_tmem, p_tmem, v, i > 0);
+                    if (F32) issue_pv<D, 3>(o_tmem, p_tmem, v, false);
                     else if (x.two) issue_pv<D, 1>(o_tmem, p_tmem, v, i > 0);
                     else issue_pv<D, 2>(o_tmem, p_tmem, v, i > 0);
                     umma_commit(&pv_done[st][buf(i)]);
@@ -712,6 +729,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             const uint32_t s_addr = tmem + lanes + st * 128, o_addr = tmem + lanes + 256 + st * D;
             const int f0 = filled[st][0], f1 = filled[st][1];
             float m_ref = -INFINITY, l = 0.f;
+            // An fp32 output's O is summed here, a step's product at a time: the tensor cores cut off what
+            // they add to a sum, about 2^-26 of it an instruction, twelve a step and always towards zero
+            // (100 requests of 64 query heads over 8000 rows: relative error 5.4e-6 so and 75 us, 4.0e-7
+            // and 92 us with the sums here).
+            float sum[F32 ? D / 16 : 1][16] = {};
+            const auto add_product = [&] {
+#pragma unroll
+                for (int q = 0; q < (F32 ? D / 16 : 0); ++q) {
+                    float o[16];
+                    tmem_ld16(o_addr + q * 16, o);
+                    tmem_wait(o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) sum[q][k] += o[k];
+                }
+            };
             bool ok = true;
             int i = 0;
             for (int j = x.two ? 0 : st; j < steps; j += stride, ++i) {
@@ -737,6 +769,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 }
                 // O so far, its last product done, to the new reference
                 const auto grown = [&](float f) {
+                    if (F32) {
+#pragma unroll
+                        for (int q = 0; q < (F32 ? D / 16 : 0); ++q) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) sum[q][k] *= f;
+                        }
+                        return;
+                    }
                     mbar_wait(&pv_done[st][buf(i - 1)], par(f0, f1, i - 1), abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);
                     __syncwarp();
                     tc_fence_after();
@@ -751,6 +791,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     }
                 };
                 const uint32_t at_s = s_addr + buf(i) * 64;
+                if (F32 && i > 0) add_product();  // the last step's: its scores' columns are these
                 if (F32) softmax_step<3>(at_s, valid, p.scale_log2, m_ref, l, i == 0, grown);
                 else if (x.two) softmax_step<1>(at_s, valid, p.scale_log2, m_ref, l, i == 0, grown);
                 else softmax_step<2>(at_s, valid, p.scale_log2, m_ref, l, i == 0, grown);
@@ -763,6 +804,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 ok = mbar_wait(&pv_done[st][buf(k)], par(f0, f1, k), abort, p.st, DAK_ERR_TIMEOUT, X_SM_O);
             }
             __syncwarp();
+            if (F32) {  // back to where the results are read from
+                tc_fence_after();
+                if (i > 0) add_product();
+#pragma unroll
+                for (int q = 0; q < (F32 ? D / 16 : 0); ++q) tmem_st16(o_addr + q * 16, sum[q]);
+                tmem_wait_st();
+            }
             // ---- results
             // Q's memory, no longer read, takes the streams' (m, l) where they share a tile, and then, half
             // a row's columns at a time, the results on their way out.

@@ -500,6 +500,25 @@ def test_attn_prefix_long_in_many_ranges(dak):
     _prefix_run(dak, 40, 4, 1, 128, 9, [k % 9 for k in range(40)], [20000, 9000], [k % 3 - 1 for k in range(40)], True)
 
 
+def test_attn_prefix_fp32_sums_do_not_drift(dak):
+    """Over values of one the output is one: the weights' sum by the products against their sum by the
+    softmax, for so many rows that every CTA sums a whole prefix of 512 steps."""
+    import torch
+    B, Hq, Hkv, D, Lp = 640, 64, 8, 64, 32768
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    k = torch.randn(1, Hkv, Lp, D, device="cuda", generator=gen).to(torch.bfloat16)
+    q = torch.randn(B, Hq, D, device="cuda", generator=gen).to(torch.bfloat16)
+    own = torch.zeros(B, Hkv, 1, D, dtype=torch.bfloat16, device="cuda")
+    kv, pre = dak.dak_place_kv_heads(own, own, 0), dak.dak_place_kv_heads(k, torch.ones_like(k), 0)
+    O = dak.dak_attn_prefix(q, kv, pre, seq_lens=torch.zeros(B, dtype=torch.int32, device="cuda"), o_fp32=True)
+    _ok(dak)
+    # the three parts of a weight 1; a step's 12 instructions cut off at most 2 each; 512 steps' products
+    # added; the softmax's sum of a step's weights 18 and of the steps 512; rescales, merge, division 10
+    assert (O - 1.0).abs().max().item() <= (1 + 24 + 512 + 18 + 512 + 10) * U32
+    kv.free()
+    pre.free()
+
+
 def test_attn_acc_in_many_splits(dak):
     import torch
     B, Hq, Hkv, D, L = 2, 3, 1, 64, 66001
