@@ -733,6 +733,7 @@ static dak_status serve_attention(const void* Q, const dak_placement* KV, const 
     if (P && (P->kind != 1 || P->D != D || P->H_kv != KV->H_kv || P->device != KV->device)) return DAK_ERR_INVALID;
     if (P && P->B > kMaxPrefixes) return DAK_ERR_UNSUPPORTED;
     if (t && t->n_split > kMaxSplits) return DAK_ERR_INVALID;
+    if (acc_out && G + (KV->L + kMergePositions - 1ll) / kMergePositions > 65535) return DAK_ERR_UNSUPPORTED;  // the merge's grid
     const int64_t slabs = static_cast<int64_t>(KV->B) * KV->H_kv;
     if (acc_out && acc_in && partly_overlaps(acc_in, acc_out, static_cast<size_t>(slabs) * KV->L * sizeof(float))) {
         return DAK_ERR_INVALID;

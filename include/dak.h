@@ -477,7 +477,7 @@ dak_status dak_attn_f32(const void* Q, const dak_placement* KV, const int* seq_l
  *             acc_in (in place) but must not overlap it otherwise.
  *   workspace: dak_attn_acc_workspace_bytes(KV, H_q, n_split) bytes (n_split <= 0: the default),
  *             16-byte aligned device memory: the splits' partial results and the scores.
- * Everything else as dak_attn. */
+ * L up to 33 million (DAK_ERR_UNSUPPORTED). Everything else as dak_attn. */
 size_t dak_attn_acc_workspace_bytes(const dak_placement* KV, int H_q, int n_split);
 dak_status dak_attn_acc(const void* Q, const dak_placement* KV, const int* seq_lens, int H_q, float scale, void* O,
                         int o_fp32, const float* acc_in, float* acc_out, void* workspace, size_t ws_bytes,

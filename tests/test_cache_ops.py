@@ -246,6 +246,8 @@ def test_serving_attention_refusals(dak, no_gpu):
                dict(tun=r(dak.dak_tuning(n_split=1025)))):
         assert acc(**kw) == INVALID, kw
     assert acc(Hq=68, n=1 << 40) == UNSUPPORTED  # 17 query heads a kv head
+    assert acc(KV=r(_kv(L=34_000_000)), n=1 << 50, acc_in=None, acc_out=1 << 40) == UNSUPPORTED
+    assert acc(KV=r(_kv(L=33_000_000)), n=1 << 50, acc_in=None, acc_out=1 << 40) == CUDA
     for kw in (dict(Q=0x100008), dict(O=0x200008), dict(ws=0x400008), dict(acc_in=0x500002), dict(acc_out=0x500001)):
         assert acc(**kw) == ALIGN, kw
 

@@ -637,6 +637,29 @@ def test_graphs_and_streams_with_memory_of_their_own(dak):
     pre.free()
 
 
+def test_attn_acc_in_a_handoff_sequence(dak):
+    """Launches of a host-link handoff sequence give the bits of launches by themselves."""
+    import torch
+    B, Hq, Hkv, D, L = 4, 8, 2, 128, 700
+    q, k, v = synth.attn_inputs(B, Hq, Hkv, D, L, seed=31)
+    Q, lens = to_dev(q), _i32([700, 64, 0, 333])
+    kvs = [dak.dak_place_kv_heads(k, v, h) for h in (3, 8, 0)]
+    want = dak.dak_attn_acc(Q, kvs[0], seq_lens=lens)
+    dak.dak_link_timeouts()
+    for slot in (0, 2, 2):
+        if slot:
+            dak.dak_link_begin(slot)
+        acc = [torch.zeros(B, Hkv, L, device="cuda") for _ in kvs]
+        out = [dak.dak_attn_acc(Q, kv, acc_out=a, seq_lens=lens, tuning=dict(pdl=1, link=slot))[0]
+               for kv, a in zip(kvs, acc)]
+        torch.cuda.synchronize()
+        _ok(dak)
+        assert all(torch.equal(o, want[0]) for o in out) and all(torch.equal(a, want[1]) for a in acc)
+    assert dak.dak_link_timeouts() == 0
+    for kv in kvs:
+        kv.free()
+
+
 def test_calls_refused_before_a_launch(dak):
     import torch
     q, k, v = synth.attn_inputs(2, 4, 2, 64, 64, seed=1)
