@@ -836,14 +836,14 @@ def dak_attn_acc(Q, KV: Placement, acc_in=None, acc_out=None, seq_lens=None, sca
     Hq = Q.shape[1]
     st, tun = _get_stream(dev), _tuning(tuning)
     if workspace is not None:
-        _check(lib.dak_attn_acc(qa, KV.handle, la, Hq, scale, oa, bool(o_fp32), ia, aa, *_given(workspace, dev), tun, st),
+        _check(lib.dak_attn_acc(qa, KV.handle, la, Hq, float(scale), oa, bool(o_fp32), ia, aa, *_given(workspace, dev), tun, st),
                "dak_attn_acc")
         return O, acc_out
     split = _n_split_of(tuning) if tuning else 0
     n = KV.cached(("acc", Hq, split), lambda: dak_attn_acc_workspace_bytes(KV, Hq, split))
     ws = _alloc(n, st)
     try:
-        _check(lib.dak_attn_acc(qa, KV.handle, la, Hq, scale, oa, bool(o_fp32), ia, aa, ws, n, tun, st), "dak_attn_acc")
+        _check(lib.dak_attn_acc(qa, KV.handle, la, Hq, float(scale), oa, bool(o_fp32), ia, aa, ws, n, tun, st), "dak_attn_acc")
     finally:
         _free(ws)
     return O, acc_out
@@ -874,7 +874,7 @@ def dak_attn_prefix(Q, KV: Placement, prefix: Placement, prefix_of=None, prefix_
     Hq = Q.shape[1]
     pshape = _kv_shape(prefix, "prefix")
     args = (qa, KV.handle, la, prefix.handle, _arg(prefix_lens, "prefix_lens", torch.int32, (pshape[0],), dev),
-            _arg(prefix_of, "prefix_of", torch.int32, (Q.shape[0],), dev), Hq, scale, oa, bool(o_fp32), ia, aa)
+            _arg(prefix_of, "prefix_of", torch.int32, (Q.shape[0],), dev), Hq, float(scale), oa, bool(o_fp32), ia, aa)
     st, tun = _get_stream(dev), _tuning(tuning)
     if workspace is not None:
         _check(lib.dak_attn_prefix(*args, *_given(workspace, dev), tun, st), "dak_attn_prefix")
