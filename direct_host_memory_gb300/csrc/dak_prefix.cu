@@ -5,7 +5,7 @@
 // The contraction is GEMM-shaped (rows x keys x D twice), so it runs on the tcgen05 tensor cores
 // as the usual two products with an online softmax between them, 64 keys a step:
 //   S  = Q (128 rows x D, shared memory) . K^T (D x 64 keys, shared memory) -> TMEM, fp32
-//   P  = 2^(S * scale log2 e - m), written to TMEM as bf16
+//   P  = 2^(S * scale log2 e - m), written to TMEM in two bf16 parts (three for an fp32 output)
 //   O += P (TMEM) . V (64 keys x D, shared memory) -> TMEM, fp32
 // A CTA has two streams, each 128 threads (thread = row) and a warp that issues its products, with S
 // and O in TMEM and P written over the S that it comes from. S has two buffers, so that the next
@@ -19,12 +19,13 @@
 // whatever its size, which held K and V apart to 20 bytes a cycle and SM). K is then a K-major
 // operand; V, whose rows are keys, an MN-major one.
 //
-// What bounds it: with two row tiles the products, 1328 of a step's 1490 cycles (the scores' N is 64, at
-// which an MMA takes 50 cycles where 32 would be its share of N 128's); with one the arrival of K and V,
-// 23 bytes a cycle and SM, about what L2 delivers to all SMs at once; short prefixes the start (plan,
-// Q, first chunks: 5 to 12 thousand cycles, most of them code that runs for the first time). 128
-// requests of 64 query and 8 kv heads, D 128, over 16K, 9K and 130 rows: 48 us; 32 of 32 heads over 8K:
-// 17 us.
+// What bounds it: with two row tiles the products, 2310 cycles a step (1640 with P in one part, half a bit
+// of the output for speed, which is not taken; the scores' N is 64, at which an MMA takes 50 cycles where
+// 32 would be its share of N 128's); with one the arrival of K and V, 23 bytes a cycle and SM, about what
+// L2 delivers to all SMs at once; short prefixes the start (plan, Q, first chunks: 5 to 12 thousand cycles,
+// most of them code that runs for the first time). 128 requests of 64 query and 8 kv heads, D 128, over
+// 16K, 9K and 130 rows and up to 256 own ones: 75.6 us for the whole call; 32 of 32 heads over 8K and up to
+// 1024 own ones: 31.7 us.
 //
 // Which CTA works on what is planned on the device from the prefixes' lengths and the requests'
 // map, so that a captured call follows them: units (prefix, kv head, 256-row tile, key range),
@@ -40,7 +41,7 @@ namespace dak {
 
 constexpr int kSoftmaxThreads = 2 * 128;  // two streams, a thread a row
 constexpr int kPrefixThreads = kSoftmaxThreads + 3 * 32;  // and copies, each stream's products
-constexpr int kPrefixTwoCost = 5, kPrefixOneCost = 4;  // of a chunk, by a tile's 128-row halves
+constexpr int kPrefixTwoCost = 3, kPrefixOneCost = 2;  // of a chunk, by a tile's 128-row halves
 constexpr int kPrefixMinChunks = 2;      // chunks of 64 keys in a range, at least
 
 struct PrefixMaps {
@@ -199,8 +200,9 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
     };
     // Requests' rows make full tiles of two 128-row halves and one more of one or two; `halves` holds
     // both kinds: tiles of two in its upper bits, one of one in bit 0. The ranges are cut as if a chunk
-    // cost a tile of two 1.25 times what it costs one of one (1.05 times where L2 has it, more where it
-    // comes from memory; cut by 8 to 7 or 4 to 3 the whole takes the same time).
+    // cost a tile of two 1.5 times what it costs one of one (2310 cycles of products to about 1450 of its
+    // bytes' arrival; 128 requests over 16K, 9K and 130 rows, from a cold L2: 81 us so, 85 by 5 to 4 or 8 to 7,
+    // 86 by 4 to 3; one prefix alone takes the same time by all of them).
     const auto halves_of = [&](int cnt) {
         const int full = quotient(cnt, per_tile), rest = cnt - full * per_tile;
         return rest > p.mpt ? 2 * full + 2 : 2 * full + (rest > 0);
@@ -400,11 +402,8 @@ __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_addr, uint3
     }
 }
 
-// Columns of the 16 keys k of part q of P, from where its S begins: three parts reach beyond it.
-template <int PARTS>
-__device__ __forceinline__ constexpr uint32_t p_column(int k, int q) {
-    return PARTS == 1 ? k * 8 : q < 2 ? k * 16 + q * 8 : 64 + k * 8;
-}
+// Columns of the 16 keys k of part q of P, from where its S begins: a third part lies beyond it.
+__device__ __forceinline__ constexpr uint32_t p_column(int k, int q) { return q < 2 ? k * 16 + q * 8 : 64 + k * 8; }
 
 // O (128 rows x D) += P . V: P from TMEM in PARTS bf16 parts, two keys a column, where the softmax
 // put them; V MN-major (idesc bit 16): N = D along a row's halves, 16384 bytes apart, K = the keys in
@@ -417,7 +416,7 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
     for (int k = 0; k < 4; ++k) {  // 16 keys: 8 columns of each part (p_column)
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) {
-            umma_bf16_ts(d_tmem, p_tmem + p_column<PARTS>(k, q), vd + k * (2048 >> 4), idesc,
+            umma_bf16_ts(d_tmem, p_tmem + p_column(k, q), vd + k * (2048 >> 4), idesc,
                          k > 0 || q > 0 ? 1u : static_cast<uint32_t>(accumulate));
         }
     }
@@ -489,7 +488,6 @@ __device__ __forceinline__ void softmax_step(uint32_t s_addr, int valid, float s
             const float2 w = make_float2(exp2_ftz(e.x), exp2_ftz(e.y));
             sum[k & 1] = add2(sum[k & 1], w);
             hi[k] = pack_bf16(w.x, w.y);
-            if (PARTS == 1) continue;
             float2 r = fma2(make_float2(bf_lo(hi[k]), bf_hi(hi[k])), minus, w);
             lo[k] = pack_bf16(r.x, r.y);
             if (PARTS == 3) {
@@ -497,9 +495,9 @@ __device__ __forceinline__ void softmax_step(uint32_t s_addr, int valid, float s
                 th[k] = pack_bf16(r.x, r.y);
             }
         }
-        tmem_st8(s_addr + p_column<PARTS>(q, 0), hi);
-        if (PARTS >= 2) tmem_st8(s_addr + p_column<PARTS>(q, 1), lo);
-        if (PARTS == 3) tmem_st8(s_addr + p_column<PARTS>(q, 2), th);
+        tmem_st8(s_addr + p_column(q, 0), hi);
+        tmem_st8(s_addr + p_column(q, 1), lo);
+        if (PARTS == 3) tmem_st8(s_addr + p_column(q, 2), th);
     }
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
@@ -609,9 +607,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const PrefixUnit x = unit;
         if (x.units == 0) break;
         // Steps are chunks. Two row tiles: both streams take every step; one: they take turns.
-        // P has one bf16 part where two row tiles make the products and the softmax set the pace, not K
-        // and V (as in dak_attn: its rounding stays below that of a bf16 output); with one tile a
-        // second part's products are free. An fp32 output takes three.
+        // P has two bf16 parts (2^-16), whatever the number of rows, so that a request's error does not
+        // depend on how many others share its prefix: of one part (2^-8) alone the error would be as large
+        // as the output's rounding. An fp32 output takes three (2^-24).
         const int steps = x.c1 - x.c0;
         const int stride = x.two ? 1 : 2;
         // S buffer of a stream's step i of this unit, and the parity of its barriers' phase. Each buffer
@@ -685,7 +683,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 if (leader) {
                     const uint32_t p_tmem = s_tmem + buf(i) * 64, v = ring_addr + vpos.slot * C::kStage + C::kV;
                     if (F32) issue_pv<D, 3>(o_tmem, p_tmem, v, false);
-                    else if (x.two) issue_pv<D, 1>(o_tmem, p_tmem, v, i > 0);
                     else issue_pv<D, 2>(o_tmem, p_tmem, v, i > 0);
                     umma_commit(&pv_done[st][buf(i)]);
                     // a stage is free when both streams have used it, or the one that does has said so twice
@@ -793,7 +790,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 const uint32_t at_s = s_addr + buf(i) * 64;
                 if (F32 && i > 0) add_product();  // the last step's: its scores' columns are these
                 if (F32) softmax_step<3>(at_s, valid, p.scale_log2, m_ref, l, i == 0, grown);
-                else if (x.two) softmax_step<1>(at_s, valid, p.scale_log2, m_ref, l, i == 0, grown);
                 else softmax_step<2>(at_s, valid, p.scale_log2, m_ref, l, i == 0, grown);
                 tmem_wait_st();
                 tc_fence_before();

@@ -500,9 +500,8 @@ dak_status dak_attn_acc(const void* Q, const dak_placement* KV, const int* seq_l
  *                16-byte aligned.
  *   tuning     : applies to the pass over the own caches; pdl and link are not taken.
  * The prefixes are read by tcgen05 tensor-core tiles of up to 256 query rows (requests x H_q /
- * H_kv); a prefix with more rows than that is streamed once per 256. The probabilities over a
- * prefix enter P.V as two bf16 parts where its rows fill one 128-row tile, as one where they fill
- * more (there the products bound the time; three with o_fp32).
+ * H_kv); a prefix with more rows than that is streamed once per 256. The probabilities enter P.V
+ * as two bf16 parts (three with o_fp32), however many requests share a prefix.
  * Requires H_q / H_kv <= 16, as dak_attn, and at most 1024 prefixes (DAK_ERR_UNSUPPORTED). */
 size_t dak_attn_prefix_workspace_bytes(const dak_placement* KV, const dak_placement* P, int H_q, int n_split,
                                        int with_acc);
