@@ -33,7 +33,7 @@ EXPORTS = [
     "dak_attn_f32", "dak_inject_fault", "dak_fault_pending", "dak_alloc_counts", "dak_gemm_chain",
     "dak_gemm_chain_workspace_bytes", "dak_link_begin", "dak_link_timeouts", "dak_selftest_link",
     "dak_place_kv_heads", "dak_kv_append", "dak_gemm_chain_plan", "dak_placement_data", "dak_rope_make",
-    "dak_rope_from_freqs", "dak_kv_append_rope", "dak_kv_evict_workspace_bytes", "dak_kv_evict",
+    "dak_rope_from_freqs", "dak_kv_append_rope", "dak_kv_append_rope_acc", "dak_kv_evict_workspace_bytes", "dak_kv_evict",
     "dak_attn_acc_workspace_bytes", "dak_attn_acc", "dak_attn_prefix_workspace_bytes", "dak_attn_prefix",
 ]
 
@@ -146,6 +146,8 @@ def _load():
         "dak_rope_from_freqs": (i32, [i32, P(dbl), i32, i32, dbl, P(dak_rope_plan)]),
         "dak_kv_append_rope": (i32, [vp, P(dak_rope_plan), vp, vp, vp, i32, i32, i32, i64, i64, i64, vp, vp, vp, vp,
                                      vp, vp]),
+        "dak_kv_append_rope_acc": (i32, [vp, P(dak_rope_plan), vp, vp, vp, i32, i32, i32, i64, i64, i64, vp, vp, vp, vp,
+                                         vp, vp, vp]),
         "dak_kv_evict_workspace_bytes": (sz, [vp]),
         "dak_kv_evict": (i32, [vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "dak_attn_acc_workspace_bytes": (sz, [vp, i32, i32]),
@@ -707,16 +709,17 @@ def _token_rows(t, name, B, T, heads, D, dtype, dev):
 
 
 def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slots, positions=None, n_new=None,
-                       q_out=None, slot_pos=None, stream=None):
+                       q_out=None, slot_pos=None, stream=None, acc=None):
     """Rotate new tokens and append them to a placed cache (dak.h): q [B][T][H_q][D] (or None),
     k_new and v_new [B][T][H_kv][D], bf16 or fp32 CUDA, slices of one projection's output as
     they are (T = 1: the T axis may be absent); slots, positions, n_new int32 CUDA [B];
-    slot_pos int32 CUDA [B][H_kv][L], updated in place. Returns q_out, bf16, shaped as q (None
+    slot_pos int32 and acc fp32 CUDA [B][H_kv][L], updated in place: a written row's position,
+    and 0 for its accumulated weight (the table of dak_attn_acc). Returns q_out, bf16, shaped as q (None
     without q)."""
     torch = _torch or _t()
     if stream is not None:
         with _current(stream):
-            return dak_kv_append_rope(KV, rope, q, k_new, v_new, slots, positions, n_new, q_out, slot_pos)
+            return dak_kv_append_rope(KV, rope, q, k_new, v_new, slots, positions, n_new, q_out, slot_pos, acc=acc)
     B, Hkv, D, L = _kv_shape(KV)
     T = k_new.shape[1] if k_new.ndim == 4 else 1
     dtype, dev = k_new.dtype, _get_device()
@@ -738,11 +741,13 @@ def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slot
         oa = _arg(q_out, "q_out", torch.bfloat16, q.shape, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    i32, per_request = torch.int32, (B,)
-    _check(lib.dak_kv_append_rope(KV.handle, rope, qa, ka, va, fp32, T, Hq, qp, kp, vp,
-                                  _arg(slots, "slots", i32, per_request, dev), _arg(positions, "positions", i32, per_request, dev),
-                                  _arg(n_new, "n_new", i32, per_request, dev), oa,
-                                  _arg(slot_pos, "slot_pos", i32, (B, Hkv, L), dev), _get_stream(dev)), "dak_kv_append_rope")
+    i32, per_request, table = torch.int32, (B,), (B, Hkv, L)
+    _check(lib.dak_kv_append_rope_acc(KV.handle, rope, qa, ka, va, fp32, T, Hq, qp, kp, vp,
+                                      _arg(slots, "slots", i32, per_request, dev),
+                                      _arg(positions, "positions", i32, per_request, dev),
+                                      _arg(n_new, "n_new", i32, per_request, dev), oa,
+                                      _arg(slot_pos, "slot_pos", i32, table, dev),
+                                      _arg(acc, "acc", torch.float32, table, dev), _get_stream(dev)), "dak_kv_append_rope")
     return q_out
 
 

@@ -24,6 +24,7 @@ struct RopeParams {
     const int* n_new;
     __nv_bfloat16* q_out;
     int* slot_pos;
+    float* acc;
     uint8_t* host;
     uint8_t* hbm;
     long long head_bytes;
@@ -195,7 +196,10 @@ __global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8) append_rope_kernel(
                 base += (row >> 6) * (16 * D) + (is_v ? 8 * D : 0) + (row & 63) * (D / 8);
                 base[(e0 >> 3) ^ (row & 7)] = y0;
                 base[(e1 >> 3) ^ (row & 7)] = y1;
-                if (p.slot_pos && !is_v && e0 == 0) p.slot_pos[slab * p.L + row] = static_cast<int>(pos);
+                if (!is_v && e0 == 0) {
+                    if (p.slot_pos) p.slot_pos[slab * p.L + row] = static_cast<int>(pos);
+                    if (p.acc) p.acc[slab * p.L + row] = 0.f;
+                }
             }
         }
     }
@@ -889,10 +893,10 @@ extern "C" dak_status dak_rope_make(int head_dim, const dak_rope_config* cfg, da
     return dak_rope_from_freqs(head_dim, inv, R / 2, cfg->interleaved, cfg->attn_scale, out);
 }
 
-extern "C" dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope_plan* rope, const void* q,
-                                         const void* k, const void* v, int in_fp32, int T, int H_q, int64_t q_pitch,
-                                         int64_t k_pitch, int64_t v_pitch, const int* slots, const int* positions,
-                                         const int* n_new, void* q_out, int* slot_pos, void* stream) {
+extern "C" dak_status dak_kv_append_rope_acc(const dak_placement* KV, const dak_rope_plan* rope, const void* q,
+                                             const void* k, const void* v, int in_fp32, int T, int H_q, int64_t q_pitch,
+                                             int64_t k_pitch, int64_t v_pitch, const int* slots, const int* positions,
+                                             const int* n_new, void* q_out, int* slot_pos, float* acc, void* stream) {
     if (!KV || KV->kind != 1 || !rope || !k || !v || !slots || T < 1 || H_q < 0) return DAK_ERR_INVALID;
     if (H_q > 0 && (!q || !q_out)) return DAK_ERR_INVALID;
     const int D = KV->D;
@@ -903,8 +907,8 @@ extern "C" dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope
     if (tokens > 0x7FFFFFFF || static_cast<int64_t>(H_q) + 2ll * KV->H_kv > (1 << 24)) return DAK_ERR_INVALID;
     const int size = in_fp32 ? 4 : 2, per16 = 16 / size;
     if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(q_out, 16) || misaligned(slots, 4) ||
-        misaligned(positions, 4) || misaligned(n_new, 4) || misaligned(slot_pos, 4) || k_pitch % per16 ||
-        v_pitch % per16 || (H_q > 0 && q_pitch % per16)) {
+        misaligned(positions, 4) || misaligned(n_new, 4) || misaligned(slot_pos, 4) || misaligned(acc, 4) ||
+        k_pitch % per16 || v_pitch % per16 || (H_q > 0 && q_pitch % per16)) {
         return DAK_ERR_ALIGN;
     }
     if (H_q > 0) {
@@ -931,6 +935,7 @@ extern "C" dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope
     p.n_new = n_new;
     p.q_out = static_cast<__nv_bfloat16*>(q_out);
     p.slot_pos = slot_pos;
+    p.acc = acc;
     p.host = static_cast<uint8_t*>(KV->host_dev);
     p.hbm = static_cast<uint8_t*>(KV->hbm_ptr);
     p.head_bytes = KV->head_bytes;
@@ -948,6 +953,14 @@ extern "C" dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(D == 128 ? (in_fp32 ? launch_append_rope<128, true>(p, grid, s) : launch_append_rope<128, false>(p, grid, s))
                                 : (in_fp32 ? launch_append_rope<64, true>(p, grid, s) : launch_append_rope<64, false>(p, grid, s)));
+}
+
+extern "C" dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope_plan* rope, const void* q,
+                                         const void* k, const void* v, int in_fp32, int T, int H_q, int64_t q_pitch,
+                                         int64_t k_pitch, int64_t v_pitch, const int* slots, const int* positions,
+                                         const int* n_new, void* q_out, int* slot_pos, void* stream) {
+    return dak_kv_append_rope_acc(KV, rope, q, k, v, in_fp32, T, H_q, q_pitch, k_pitch, v_pitch, slots, positions,
+                                  n_new, q_out, slot_pos, nullptr, stream);
 }
 
 // Workspace: per slab a count and the holes and movers, of which there are at most

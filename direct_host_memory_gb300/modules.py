@@ -115,12 +115,13 @@ class SplitK_FlashAttn(torch.nn.Module):
     def append_rope(self, rope, q, k_new, v_new, slots, positions=None, n_new=None):
         """Rotate new tokens and write them from row slots[b] on (dak_kv_append_rope): q
         [B][T][H_q][D] or None, k_new and v_new [B][T][H_kv][D], bf16 or fp32 CUDA (T = 1: the
-        axis may be absent), rope by dak_rope_make; rope None: as they are. Returns the rotated
-        q in bf16."""
+        axis may be absent), rope by dak_rope_make; rope None: as they are. In a tracked cache a
+        row's new token starts with its own position and no weight, whatever the row held before
+        (a draft taken back, a chat that ended). Returns the rotated q in bf16."""
         if rope is None:
             rope = _lib.dak_rope_from_freqs(self.head_dim, [0.0])
         return _lib.dak_kv_append_rope(self.placement, rope, q, k_new, v_new, slots, positions=positions, n_new=n_new,
-                                       slot_pos=self.slot_pos)
+                                       slot_pos=self.slot_pos, acc=self.weights)
 
     def evict(self, seq_lens, n_keep: int, n_recent: int = 0):
         """Keep n_keep tokens of every (request, kv head) of a tracked cache that holds more: the

@@ -254,6 +254,15 @@ dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope_plan* rope
                               int64_t v_pitch, const int* slots, const int* positions, const int* n_new, void* q_out,
                               int* slot_pos, void* stream);
 
+/* The same for a cache whose attention weights are accumulated (dak_attn_acc, dak_attn_prefix):
+ * acc, fp32 [B][H_kv][L] (device, 4-byte aligned) or NULL, is set to 0 where a row is written,
+ * acc[b][g][slots[b] + t] = 0. A row may have held another token (a draft taken back, a request
+ * that ended), whose weight the new one must not inherit: dak_kv_evict would go by it. */
+dak_status dak_kv_append_rope_acc(const dak_placement* KV, const dak_rope_plan* rope, const void* q, const void* k,
+                                  const void* v, int in_fp32, int T, int H_q, int64_t q_pitch, int64_t k_pitch,
+                                  int64_t v_pitch, const int* slots, const int* positions, const int* n_new,
+                                  void* q_out, int* slot_pos, float* acc, void* stream);
+
 /* Evict the least attended tokens of a placed KV cache, each (request, kv head) for itself.
  * Where a request holds L_b = seq_lens[b] (clamped to [0, L]) > n_keep tokens, n_keep slots
  * stay:
