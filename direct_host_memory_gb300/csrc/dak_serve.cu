@@ -401,6 +401,8 @@ __global__ void __launch_bounds__(kServeThreads, NB == 1 ? 3 : 2) serve_kernel(c
 //   call; 1024 heads: 35.4 -> 37.0, so that few heads keep the blocks). Later blocks take
 //   kMergePositions positions of the slab each,
 //   acc_out = acc_in + sum_r 2^(score_r - M_r) / l_r.
+// A request without any token has zeros; scores of NaN, or of infinity throughout, have NaN as their
+// softmax, in O and in the weights.
 // What a block waits for are loads, so that the partials or scores it will need are asked for before
 // the maxima they are taken against are known. Splits behind a request's tokens have no partials.
 struct MergeParams {
@@ -502,8 +504,7 @@ __global__ void __launch_bounds__(kMergeThreads) serve_merge_kernel(const MergeP
             acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
         }
         if (grp == 0) {
-            if (l > 0.f) acc.x /= l, acc.y /= l, acc.z /= l, acc.w /= l;
-            else acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (n > 0) acc.x /= l, acc.y /= l, acc.z /= l, acc.w /= l;  // no tokens at all: zeros
             if (p.o_fp32) {
                 *reinterpret_cast<float4*>(static_cast<float*>(p.O) + row * D + c * 4) = acc;
             } else {
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(kMergeThreads) serve_merge_kernel(const MergeP
             float v = 0.f;
 #pragma unroll
             for (int k = 0; k < GROUPS; ++k) v += red[k][tid];
-            v = l > 0.f ? v / l : 0.f;
+            v = n > 0 ? v / l : 0.f;  // no tokens at all: zeros
             if (p.o_fp32) static_cast<float*>(p.O)[row * D + tid] = v;
             else static_cast<__nv_bfloat16*>(p.O)[row * D + tid] = __float2bfloat16_rn(v);
         }
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(kMergeThreads) serve_merge_kernel(const MergeP
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (lane == 0) rows[r] = make_float2(base, l > 0.f ? 1.f / l : 0.f);
+        if (lane == 0) rows[r] = make_float2(base, 1.f / l);
     }
     __syncthreads();
 #pragma unroll

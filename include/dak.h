@@ -481,7 +481,8 @@ dak_status dak_attn_f32(const void* Q, const dak_placement* KV, const int* seq_l
  *   seq_lens: as dak_attn, but L_b = 0 is allowed (a request without tokens: O = 0); values are
  *             clamped to [0, L].
  *   O       : [B][H_q][D], bf16 or (o_fp32) fp32. The probabilities enter P.V as two bf16 parts
- *             (three with o_fp32).
+ *             (three with o_fp32). A score of NaN or +infinity makes its head's O and its kv
+ *             head's weights NaN, as the softmax of such a row is.
  *   acc_in  : fp32 [B][H_kv][L] (device), or NULL = zeros. acc_out: the same shape; it may be
  *             acc_in (in place) but must not overlap it otherwise.
  *   workspace: dak_attn_acc_workspace_bytes(KV, H_q, n_split) bytes (n_split <= 0: the default),
