@@ -87,6 +87,7 @@ class SplitK_FlashAttn(torch.nn.Module):
         self.tuning = dict(tuning or {})
         self._ws = None
         self.weights = self.slot_pos = None
+        self._several_new = False  # rows other than the newest were written since the last forward
 
     @property
     def host_bytes(self) -> int:
@@ -117,9 +118,13 @@ class SplitK_FlashAttn(torch.nn.Module):
         [B][T][H_q][D] or None, k_new and v_new [B][T][H_kv][D], bf16 or fp32 CUDA (T = 1: the
         axis may be absent), rope by dak_rope_make; rope None: as they are. In a tracked cache a
         row's new token starts with its own position and no weight, whatever the row held before
-        (a draft taken back, a chat that ended). Returns the rotated q in bf16."""
+        (a draft taken back, a chat that ended). Returns the rotated q in bf16. Where the module's
+        tuning sets pdl, a single token is the newest one of seq_lens at the next forward, as after
+        append; after several the next forward is launched without pdl."""
         if rope is None:
             rope = _lib.dak_rope_from_freqs(self.head_dim, [0.0])
+        if k_new.ndim == 4 and k_new.shape[1] > 1:
+            self._several_new = True
         return _lib.dak_kv_append_rope(self.placement, rope, q, k_new, v_new, slots, positions=positions, n_new=n_new,
                                        slot_pos=self.slot_pos, acc=self.weights)
 
@@ -154,6 +159,7 @@ class SplitK_FlashAttn(torch.nn.Module):
             q = query.reshape(query.shape[0], query.shape[1], query.shape[3])
         else:
             q = query
+        several_new, self._several_new = self._several_new, False
         if prefix is not None or self.weights is not None:
             o = self._serve(q, seq_lens, float(scale or 0.0), prefix, prefix_of, prefix_lens)
             return o.view(query.shape) if squeeze else o
@@ -162,6 +168,8 @@ class SplitK_FlashAttn(torch.nn.Module):
         if need and (self._ws is None or self._ws.numel() * 4 < need or self._ws.device != q.device):
             self._ws = torch.empty((need + 3) // 4, dtype=torch.float32, device=q.device)
         tun = dict(self.tuning, n_split=self.n_split)
+        if several_new:  # programmatic launch holds back the newest token's rows alone
+            tun.pop("pdl", None)
         fn = _lib.dak_attn_f32 if self.fp32_out else _lib.dak_attn
         o = fn(q, self.placement, seq_lens=seq_lens, scale=float(scale or 0.0), workspace=self._ws, tuning=tun)
         return o.view(query.shape) if squeeze else o

@@ -21,3 +21,47 @@ def test_append_rope_acc_refusals(dak, no_gpu):  # noqa: F811
     assert call() == CUDA and call(acc=None) == CUDA and call(slot_pos=None) == CUDA
     assert call(acc=0x8002) == ALIGN
     assert call(KV=None) == INVALID and call(slots=None) == INVALID and call(T=0) == INVALID
+
+
+class _Placement:
+    host_bytes = 0
+
+
+def test_forward_after_several_new_tokens_is_launched_without_pdl(dak, monkeypatch):  # noqa: F811
+    """Programmatic launch lets attention read all rows but the newest before the kernel in front of it has
+    ended: after append_rope of more than one token the next forward, and only that one, is launched
+    without it."""
+    import torch
+    from direct_host_memory_gb300 import _lib
+    seen = []
+
+    def attn(q, KV, **kw):
+        seen.append(kw["tuning"].get("pdl", 0))
+        return q
+
+    for name, fake in (("dak_place_kv_heads", lambda *a: _Placement()), ("dak_attn_default_split", lambda p: 1),
+                       ("dak_attn_workspace_bytes", lambda *a: 0), ("dak_attn", attn),
+                       ("dak_attn_prefix", lambda q, *a, **kw: q), ("dak_kv_append", lambda *a: None),
+                       ("dak_kv_append_rope", lambda *a, **kw: None)):
+        monkeypatch.setattr(_lib, name, fake)
+    B, Hkv, D = 2, 2, 64
+    z = torch.zeros(B, Hkv, 96, D, dtype=torch.bfloat16)
+    q, one, many = torch.zeros(B, 4, D), torch.zeros(B, Hkv, D), torch.zeros(B, 3, Hkv, D)
+    at = torch.zeros(B, dtype=torch.int32)
+    m = dak.SplitK_FlashAttn(z, z, tuning=dict(pdl=2, hbm_window=3))
+    m(q)
+    m.append(one, one, at)
+    m(q)
+    m.append_rope(None, None, one, one, at)
+    m.append_rope(None, None, one[:, None], one[:, None], at)
+    m(q)
+    assert seen == [2, 2, 2]
+    m.append_rope(None, None, many, many, at)
+    m.append_rope(None, None, one, one, at)
+    m(q)
+    m(q)
+    assert seen[3:] == [0, 2]
+    m.append_rope(None, None, many, many, at)
+    m(q, prefix=_Placement())  # waits for the rows itself
+    m(q)
+    assert seen[5:] == [2] and m.tuning == dict(pdl=2, hbm_window=3)
