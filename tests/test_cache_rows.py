@@ -65,3 +65,22 @@ def test_forward_after_several_new_tokens_is_launched_without_pdl(dak, monkeypat
     m(q, prefix=_Placement())  # waits for the rows itself
     m(q)
     assert seen[5:] == [2] and m.tuning == dict(pdl=2, hbm_window=3)
+
+
+@pytest.mark.parametrize("theta", [500000.0, 10000.0])
+def test_rope_turns_are_as_good_as_the_header_says(dak, theta):  # noqa: F811
+    """position * turns mod 2^64 within |position| (|f| 2^-55 + 2^-65) turns of the double frequency's angle, by
+    rational arithmetic; and no bound that does not grow with the position holds."""
+    from fractions import Fraction
+    two_pi = Fraction(6.283185307179586) + Fraction(2.4492935982947064e-16)  # 2 pi to 2^-105
+    f = [theta ** (-2.0 * i / 128) for i in range(64)] + [-0.75, 3.5]
+    worst = 0.0
+    for r, part in ((dak.dak_rope_from_freqs(128, f[:64]), f[:64]), (dak.dak_rope_from_freqs(128, f[64:]), f[64:])):
+        for i, x in enumerate(part):
+            for pos in (1, 4095, 1000000, 2 ** 31 - 1, -2 ** 31):
+                want = (Fraction(x) * pos / two_pi) % 1
+                gap = abs(Fraction((pos * r.turns[i]) % 2 ** 64, 2 ** 64) - want)
+                gap = min(gap, 1 - gap)
+                assert gap <= abs(pos) * (abs(Fraction(x)) / 2 ** 55 + Fraction(1, 2 ** 65)) + Fraction(1, 2 ** 80)
+                worst = max(worst, float(gap))
+    assert worst > 2.0 ** -33
