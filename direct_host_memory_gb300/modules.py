@@ -95,7 +95,9 @@ class SplitK_FlashAttn(torch.nn.Module):
 
     def track(self):
         """From now on accumulate attention weights and keep positions: a token that the cache
-        holds already has its slot as its position and no weight yet."""
+        holds already has its slot as its position (add to self.slot_pos where positions begin
+        later, as behind a shared prefix) and no weight yet, nor has one that append_rope writes,
+        until a query attends to it."""
         shape = (self.batch, self.n_kv_heads, self.capacity)
         self.weights = torch.zeros(shape, dtype=torch.float32, device="cuda")
         at = torch.arange(self.capacity, dtype=torch.int32, device="cuda")

@@ -191,7 +191,8 @@ dak_status dak_kv_append(const dak_placement* KV, const void* k_new, const void*
  *                leaves the fastest pair alone and divides the slowest by factor;
  *                DAK_ROPE_BY_PARTS, per pair by the turns r = orig_len * f_i / 2 pi that it
  *                makes over the original context: f_i / factor for r <= low_turns, f_i for
- *                r >= high_turns, between them mixed linearly in r.
+ *                r >= high_turns, between them mixed linearly in r. (Models trained with a mix
+ *                linear in the pair's index instead take dak_rope_from_freqs.)
  *   factor     : context extension, > 0 (<= 0: 1). orig_len: > 0 for BY_PARTS.
  *   low_turns, high_turns: 0 <= low < high; both <= 0: 1 and 32.
  *   attn_scale : factor on cos and sin; <= 0: 1. */
@@ -286,7 +287,8 @@ dak_status dak_kv_append_rope_acc(const dak_placement* KV, const dak_rope_plan* 
  *   workspace: dak_kv_evict_workspace_bytes(KV) bytes of device memory, 16-byte aligned,
  *              contents on entry do not matter; calls that share one must not overlap.
  * 1 <= n_keep <= L, 0 <= n_recent <= n_keep (DAK_ERR_INVALID). Stream-ordered; a following
- * attention is launched without programmatic launch. */
+ * attention is launched without programmatic launch. dak_decoder_step takes one position per
+ * request as row, angle and length and does not run over an evicted cache. */
 size_t dak_kv_evict_workspace_bytes(const dak_placement* KV);
 dak_status dak_kv_evict(const dak_placement* KV, const int* seq_lens, int n_keep, int n_recent, const float* acc,
                         float* acc_out, const int* slot_pos, int* slot_pos_out, int* lens_out, int* src_out,
