@@ -63,3 +63,44 @@ def test_attn_prefix_weights_at_any_number_of_rows(dak, B, Hq, Hkv, D, fp32):
     _check(O, c, ref, fp32)
     kv.free()
     pre.free()
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("B,Hq,Hkv,D", [(3, 8, 2, 128), (40, 6, 2, 64), (5, 16, 1, 64), (4, 24, 2, 128)])
+def test_attn_acc_weights(dak, B, Hq, Hkv, D, fp32):
+    """The same over the own caches, and the accumulated weights beside it."""
+    import torch
+    q, k, v, c, ref = _two_rows(B, Hq, Hkv, D)
+    kv = dak.dak_place_kv_heads(k.expand(B, -1, -1, -1).contiguous(), v.expand(B, -1, -1, -1).contiguous(), 1)
+    O, acc = dak.dak_attn_acc(q, kv, o_fp32=fp32)
+    assert dak.dak_last_error()[0] == 0
+    _check(O, c, ref, fp32)
+    # fp32 weights: c's 6 units, the denominator's 8, the product with its reciprocal 2, G of them added
+    w = np.concatenate([1 / (1 + c), c / (1 + c)], -1).reshape(B, Hkv, Hq // Hkv, 2).sum(2)
+    assert (np.abs(to_np(acc) - w) <= (16 + Hq // Hkv) * U32 * w).all()
+    kv.free()
+
+
+def test_attn_acc_fp32_sums_have_no_bias(dak):
+    """Equal scores over positive values: the weights are one and their sum the row count, both exact, so
+    that an output's error is that of its numerator's sum. Rounded to nearest, each of a warp's 1024
+    additions of a chunk's product is off by at most half a unit in the last place either way: the mean over
+    1024 outputs stays below 2 units of 2^-24 (6 standard deviations of 0.29 units in the last place, at most
+    2 of 2^-24, a third of them weighing in by the growing sum: sqrt(1024 / 3) * 0.58 / sqrt(1024) * 6).
+    A chunk's product itself may lose 16 (its sixteen terms cut off below the largest's 2^-24), the merge
+    and the division 4. Summed in the tensor cores, which cut off towards zero each time, the mean is below
+    by dozens of units."""
+    import torch
+    B, Hkv, D, L = 8, 2, 64, 65536
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    v = torch.rand(B, Hkv, L, D, device="cuda", generator=gen) + 1.0
+    v = (v * torch.exp2(-12.0 * torch.rand(B, Hkv, L, D, device="cuda", generator=gen))).to(torch.bfloat16)
+    kv = dak.dak_place_kv_heads(torch.zeros_like(v), v, 0)
+    q = torch.randn(B, Hkv, D, device="cuda", generator=gen).to(torch.bfloat16)
+    O, _ = dak.dak_attn_acc(q, kv, o_fp32=True, tuning=dict(n_split=1))
+    assert dak.dak_last_error()[0] == 0
+    ref = v.double().mean(2)
+    rel = ((O.double() - ref) / ref).flatten() / U32
+    assert abs(rel.mean().item()) <= 2 + 16 + 4, f"mean error {rel.mean().item():.1f} units of 2^-24"
+    assert rel.abs().max().item() <= 1024 + 16 + 4
+    kv.free()
