@@ -451,7 +451,8 @@ __global__ void __launch_bounds__(kMergeThreads) serve_merge_kernel(const MergeP
     }
     const int n_own = (L + p.split_len - 1) / p.split_len;
     grid_dep_wait();
-    const int n = n_own + (prefixed ? p.n_ranges[b] : 0);
+    // the limits: where a wait of the prefix pass ran out, its later units' counts were never written
+    const int n = n_own + (prefixed ? min(max(p.n_ranges[b], 0), p.n_pre) : 0);
     const long long row0 = static_cast<long long>(b) * p.Hq + static_cast<long long>(g) * p.G;
     const auto ml = [&](long long row, int s) {
         return s < n_own ? p.own_ml[row * p.n_own + s] : p.pre_ml[row * p.n_pre + s - n_own];
