@@ -159,12 +159,12 @@ dak_status launch_attn(const void* Q, const dak_placement* KV, const void* host_
                        int o_fp32 = 0, const LinkHandoff* link = nullptr);
 
 // The prefix pass of dak_attn_prefix (dak_prefix.cu) over the placement P of shared prefixes: for
-// every row of Q [B][H_q][D] up to prefix_max_ranges(P) partials, unnormalised o_part
+// every row of Q [B][H_q][D] up to prefix_max_ranges(P, B * H_q) partials, unnormalised o_part
 // [rows][ranges][D] and ml_part [rows][ranges][2] (maximum in the log2 domain, sum), and in
 // n_ranges [B] how many of them a request's rows have (not written for a request without a prefix or
 // with an empty one). Arguments are checked by the caller.
 constexpr int kMaxPrefixes = 1024;
-int prefix_max_ranges(const dak_placement* P);
+int prefix_max_ranges(const dak_placement* P, int64_t rows);
 dak_status launch_prefix(const void* Q, const dak_placement* P, const int* lens, const int* of, int B, int H_q,
                          float scale_log2, int o_fp32, float* o_part, float* ml_part, int* n_ranges, cudaStream_t s);
 

@@ -43,6 +43,7 @@ constexpr int kSoftmaxThreads = 2 * 128;  // two streams, a thread a row
 constexpr int kPrefixThreads = kSoftmaxThreads + 3 * 32;  // and copies, each stream's products
 constexpr int kPrefixTwoCost = 3, kPrefixOneCost = 2;  // of a chunk, by a tile's 128-row halves
 constexpr int kPrefixMinChunks = 2;      // chunks of 64 keys in a range, at least
+constexpr int64_t kPrefixPartialBytes = 64ll << 20;  // of partials in the workspace (prefix_max_ranges)
 
 struct PrefixMaps {
     CUtensorMap tier[2];  // host, HBM: chunks of 64 keys
@@ -886,9 +887,15 @@ static bool make_prefix_map(CUtensorMap* map, const void* base, int64_t chunks, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int prefix_max_ranges(const dak_placement* P) {
+// Every row has a place in the workspace for each range that its prefix may be cut into. As many ranges as a
+// kv head has SMs, so that one request alone fills them, are 545 MB for 512 requests of 16 query heads on one
+// kv head, whose prefix is cut into a few: past kPrefixPartialBytes there are fewer. Those 512 over 16K rows
+// 105.6 us so, 116.9 without the limit (fewer partials are merged by warps); one of them alone over
+// 16K 42 us, 51 without, 38 with 128 MiB, 54 with 32; one of 256 requests of 32 and 8 heads 52, 51, 49, 60.
+int prefix_max_ranges(const dak_placement* P, int64_t rows) {
     const int chunks = (P->L + 63) / 64;
-    return std::max(1, std::min(std::min(device_sm_count(), 256) / P->H_kv, (chunks + kPrefixMinChunks - 1) / kPrefixMinChunks));
+    const int most = std::min(std::min(device_sm_count(), 256) / P->H_kv, (chunks + kPrefixMinChunks - 1) / kPrefixMinChunks);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, kPrefixPartialBytes / (rows * (P->D + 2) * 4))));
 }
 
 template <int D, bool F32>
@@ -928,7 +935,7 @@ dak_status launch_prefix(const void* Q, const dak_placement* P, const int* lens,
     p.inv_G = (65536 + p.G - 1) / p.G;
     p.L = P->L;
     p.n_prefix = P->B;
-    p.n_pre = prefix_max_ranges(P);
+    p.n_pre = prefix_max_ranges(P, static_cast<int64_t>(B) * H_q);
     p.h_s = P->h_s;
     p.slab_chunks = (P->L + 63) / 64;
     p.scale_log2 = scale_log2;

@@ -706,7 +706,7 @@ static ServeLayout serve_layout(const dak_placement* KV, const dak_placement* P,
     const size_t rows = static_cast<size_t>(KV->B) * H_q, slabs = static_cast<size_t>(KV->B) * KV->H_kv;
     const int G = H_q / KV->H_kv;
     x.n_own = n_split > 0 ? n_split : serve_default_split(KV);
-    x.n_pre = P ? prefix_max_ranges(P) : 0;
+    x.n_pre = P ? prefix_max_ranges(P, static_cast<int64_t>(rows)) : 0;
     x.own_o = round256(rows * x.n_own * KV->D * sizeof(float));
     x.own_ml = round256(rows * x.n_own * sizeof(float2));
     x.pre_o = round256(rows * x.n_pre * KV->D * sizeof(float));

@@ -145,3 +145,50 @@ def test_attn_acc_launched_while_the_append_runs(dak, host, n_split):  # noqa: F
     _ok(dak)
     ref.free()
     kv.free()
+
+
+@pytest.mark.parametrize("B,Hq,H,D,P,Lp", [(512, 16, 1, 128, 1, 16384), (128, 64, 8, 128, 3, 16384), (1, 32, 8, 128, 1, 9000),
+                                           (1000, 8, 8, 64, 900, 500), (4, 32, 8, 128, 1, 257)])
+def test_prefix_workspace_is_in_proportion(dak, B, Hq, H, D, P, Lp):  # noqa: F811
+    """A wide batch's partials over a prefix do not take a place for every row in as many ranges as there are
+    SMs (545 MB for the first case)."""
+    import torch
+    kv, pre = (dak.dak_place_kv_heads(z, z, 0) for z in (
+        torch.zeros(n, H, rows, D, dtype=torch.bfloat16, device="cuda") for n, rows in ((B, 64), (P, Lp))))
+    got = dak.dak_attn_prefix_workspace_bytes(kv, pre, Hq, 1)
+    sms, rows, place = dak.dak_sm_count(), B * Hq, (D + 2) * 4
+    # a place a row is D + 2 floats; the own pass takes one, as it is in one split; the prefix one for each
+    # range, but no more than 64 MiB where one range takes less
+    most = max(rows * place, min(rows * place * max(1, sms // H), 64 << 20))
+    assert rows * 2 * place <= got <= rows * place + most + B * 4 + 5 * 256
+    kv.free()
+    pre.free()
+
+
+@pytest.mark.parametrize("P,B,Hq,Hkv,D", [(3, 128, 64, 8, 128), (1, 300, 16, 1, 64), (90, 400, 8, 8, 64), (33, 60, 32, 4, 128),
+                                          (1, 97, 20, 2, 128), (200, 50, 4, 2, 64)])
+def test_prefix_call_stays_inside_its_workspace(dak, P, B, Hq, Hkv, D):  # noqa: F811
+    """What lies right behind the workspace is left as it was, for prefixes of every length and tile kind,
+    and the result does not depend on where it lies."""
+    import torch
+    rng = np.random.default_rng(P + B)
+    gen = torch.Generator(device="cuda").manual_seed(P)
+    L, Lp = 3, 2500
+
+    def rand(*s):
+        return torch.randn(*s, device="cuda", generator=gen).to(torch.bfloat16)
+
+    kv = dak.dak_place_kv_heads(rand(B, Hkv, L, D), rand(B, Hkv, L, D), 0)
+    pre = dak.dak_place_kv_heads(rand(P, Hkv, Lp, D), rand(P, Hkv, Lp, D), 0)
+    n = dak.dak_attn_prefix_workspace_bytes(kv, pre, Hq)
+    q = rand(B, Hq, D)
+    for rep in range(6):
+        plens = np.exp(rng.uniform(0, np.log(Lp + 1), P)).astype(int).clip(0, Lp)
+        of = rng.integers(-1, P, B) if rep % 2 else np.where(rng.random(B) < 0.7, 0, rng.integers(-1, P, B))
+        ws = torch.full((n + (1 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+        O = dak.dak_attn_prefix(q, kv, pre, prefix_of=_i32(of), prefix_lens=_i32(plens), workspace=ws[:n])
+        one = dak.dak_attn_prefix(q, kv, pre, prefix_of=_i32(of), prefix_lens=_i32(plens))
+        _ok(dak)
+        assert (ws[n:] == 0x5A).all() and torch.equal(O, one)
+    kv.free()
+    pre.free()
