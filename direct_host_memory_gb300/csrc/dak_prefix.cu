@@ -19,13 +19,14 @@
 // whatever its size, which held K and V apart to 20 bytes a cycle and SM). K is then a K-major
 // operand; V, whose rows are keys, an MN-major one.
 //
-// What bounds it: with two row tiles the products, 2310 cycles a step (1640 with P in one part, half a bit
-// of the output for speed, which is not taken; the scores' N is 64, at which an MMA takes 50 cycles where
-// 32 would be its share of N 128's); with one the arrival of K and V, 23 bytes a cycle and SM, about what
-// L2 delivers to all SMs at once; short prefixes the start (plan, Q, first chunks: 5 to 12 thousand cycles,
-// most of them code that runs for the first time). 128 requests of 64 query and 8 kv heads, D 128, over
-// 16K, 9K and 130 rows and up to 256 own ones: 75.6 us for the whole call; 32 of 32 heads over 8K and up to
-// 1024 own ones: 31.7 us.
+// What bounds it: with two row tiles a step's chain from S through the softmax to P and P.V, 2310 cycles
+// (1640 with P in one part, half a bit of the output for speed, which is not taken). No pipe is full: the
+// tensor cores are active 40% of the time, instructions issue in 29% of the cycles, exp2 and conversions 13%;
+// a sub-partition has two softmax warps, one of each stream, to cover their latencies, and registers for no
+// more. With one the arrival of K and V, 23 bytes a cycle and SM, about what L2 delivers to all SMs at
+// once; short prefixes the start (plan, Q, first chunks: 5 to 12 thousand cycles, most of them code that
+// runs for the first time). 128 requests of 64 query and 8 kv heads, D 128, over 16K, 9K and 130 rows and
+// up to 256 own ones: 75.6 us for the whole call; 32 of 32 heads over 8K and up to 1024 own ones: 31.7 us.
 //
 // Which CTA works on what is planned on the device from the prefixes' lengths and the requests'
 // map, so that a captured call follows them: units (prefix, kv head, 256-row tile, key range),
@@ -201,9 +202,9 @@ __device__ __forceinline__ void plan_unit(const PrefixParams& p, int u, int4* sc
     };
     // Requests' rows make full tiles of two 128-row halves and one more of one or two; `halves` holds
     // both kinds: tiles of two in its upper bits, one of one in bit 0. The ranges are cut as if a chunk
-    // cost a tile of two 1.5 times what it costs one of one (2310 cycles of products to about 1450 of its
-    // bytes' arrival; 128 requests over 16K, 9K and 130 rows, from a cold L2: 81 us so, 85 by 5 to 4 or 8 to 7,
-    // 86 by 4 to 3; one prefix alone takes the same time by all of them).
+    // cost a tile of two 1.5 times what it costs one of one (2310 cycles to about 1450 of its bytes' arrival;
+    // 128 requests over 16K, 9K and 130 rows, from a cold L2: 81 us so, 85 by 5 to 4 or 8 to 7, 86 by 4 to 3;
+    // one prefix alone takes the same time by all of them).
     const auto halves_of = [&](int cnt) {
         const int full = quotient(cnt, per_tile), rest = cnt - full * per_tile;
         return rest > p.mpt ? 2 * full + 2 : 2 * full + (rest > 0);
