@@ -567,8 +567,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_flag;
     __shared__ PrefixUnit unit;
-    // the tile's requests, in the ring: K and V come in once their rows are known
-    int* member = reinterpret_cast<int*>(ring);
+    // the tile's requests: not in the ring, where copies by another proxy would follow these writes
+    __shared__ int member[256];
     volatile int* abort = &abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 32) {
