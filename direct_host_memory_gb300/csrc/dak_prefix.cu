@@ -26,7 +26,7 @@
 // more. With one the arrival of K and V, 23 bytes a cycle and SM, about what L2 delivers to all SMs at
 // once; short prefixes the start (plan, Q, first chunks: 5 to 12 thousand cycles, most of them code that
 // runs for the first time). 128 requests of 64 query and 8 kv heads, D 128, over 16K, 9K and 130 rows and
-// up to 256 own ones: 75.6 us for the whole call; 32 of 32 heads over 8K and up to 1024 own ones: 31.7 us.
+// up to 256 own ones: 76.3 us for the whole call; 32 of 32 heads over 8K and up to 1024 own ones: 31.7 us.
 //
 // Which CTA works on what is planned on the device from the prefixes' lengths and the requests'
 // map, so that a captured call follows them: units (prefix, kv head, 256-row tile, key range),
