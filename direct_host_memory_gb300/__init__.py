@@ -19,6 +19,7 @@ from ._lib import (  # noqa: F401
     host_tiles_for_ratio, lib, load_tuning, place_decoder_layer, save_tuning, tuning_to_dict,
     ROPE_SCALINGS, dak_attn_acc, dak_attn_acc_workspace_bytes, dak_attn_prefix, dak_attn_prefix_workspace_bytes,
     dak_kv_append_rope, dak_kv_evict, dak_kv_evict_workspace_bytes, dak_rope_config, dak_rope_from_freqs,
-    dak_rope_make, dak_rope_plan,
+    dak_rope_make, dak_rope_plan, MAX_TREE, dak_attn_tree, dak_attn_tree_workspace_bytes, dak_kv_append_rope_axes,
+    dak_kv_commit, dak_kv_fork, dak_rope_axes_make, dak_rope_axes_plan, dak_tree_mask,
 )
 from .modules import SplitK_FlashAttn, SplitK_GEMM  # noqa: F401,E402

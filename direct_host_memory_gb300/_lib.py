@@ -35,6 +35,8 @@ EXPORTS = [
     "dak_place_kv_heads", "dak_kv_append", "dak_gemm_chain_plan", "dak_placement_data", "dak_rope_make",
     "dak_rope_from_freqs", "dak_kv_append_rope", "dak_kv_append_rope_acc", "dak_kv_evict_workspace_bytes", "dak_kv_evict",
     "dak_attn_acc_workspace_bytes", "dak_attn_acc", "dak_attn_prefix_workspace_bytes", "dak_attn_prefix",
+    "dak_rope_axes_make", "dak_kv_append_rope_axes", "dak_attn_tree_workspace_bytes", "dak_attn_tree", "dak_kv_commit",
+    "dak_kv_fork",
 ]
 
 # position scalings of dak_rope_make (DAK_ROPE_* in dak.h)
@@ -97,6 +99,10 @@ class dak_rope_plan(ctypes.Structure):
                 ("scale", ctypes.c_float), ("turns", ctypes.c_uint64 * 64)]
 
 
+class dak_rope_axes_plan(ctypes.Structure):
+    _fields_ = [("rope", dak_rope_plan), ("n_axes", ctypes.c_int), ("axis", ctypes.c_ubyte * 64)]
+
+
 class dak_decoder_config(ctypes.Structure):
     _fields_ = [("n_layers", ctypes.c_int), ("hidden", ctypes.c_int), ("n_heads", ctypes.c_int),
                 ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("ffn", ctypes.c_int),
@@ -155,6 +161,13 @@ def _load():
         "dak_attn_prefix_workspace_bytes": (sz, [vp, vp, i32, i32, i32]),
         "dak_attn_prefix": (i32, [vp, vp, vp, vp, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp, vp, sz, P(dak_tuning),
                                   vp]),
+        "dak_rope_axes_make": (i32, [P(dak_rope_plan), i32, P(i32), P(dak_rope_axes_plan)]),
+        "dak_kv_append_rope_axes": (i32, [vp, P(dak_rope_axes_plan), vp, vp, vp, i32, i32, i32, i64, i64, i64, vp, vp, vp,
+                                          vp, vp, vp, vp]),
+        "dak_attn_tree_workspace_bytes": (sz, [vp, i32, i32]),
+        "dak_attn_tree": (i32, [vp, vp, vp, i32, vp, i64, vp, i32, ctypes.c_float, vp, i32, vp, sz, P(dak_tuning), vp]),
+        "dak_kv_commit": (i32, [vp, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp]),
+        "dak_kv_fork": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         "dak_plan_ratios": (i32, [P(dak_op), i32, dbl, dbl, dbl, i32, P(dbl), P(dbl)]),
         "dak_plan_units": (i32, [P(dak_op), i32, dbl, dbl, dbl, P(i64), P(dbl)]),
         "dak_last_error": (i32, [vp, P(ctypes.c_uint64)]),
@@ -708,18 +721,9 @@ def _token_rows(t, name, B, T, heads, D, dtype, dev):
     return t.data_ptr(), heads * D if B * T == 1 else row
 
 
-def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slots, positions=None, n_new=None,
-                       q_out=None, slot_pos=None, stream=None, acc=None):
-    """Rotate new tokens and append them to a placed cache (dak.h): q [B][T][H_q][D] (or None),
-    k_new and v_new [B][T][H_kv][D], bf16 or fp32 CUDA, slices of one projection's output as
-    they are (T = 1: the T axis may be absent); slots, positions, n_new int32 CUDA [B];
-    slot_pos int32 and acc fp32 CUDA [B][H_kv][L], updated in place: a written row's position,
-    and 0 for its accumulated weight (the table of dak_attn_acc). Returns q_out, bf16, shaped as q (None
-    without q)."""
+def _append_rope(KV, rope, axes, q, k_new, v_new, slots, positions, n_new, q_out, slot_pos, acc):
+    """dak_kv_append_rope_acc, or with axes (the axes of each token's own positions) dak_kv_append_rope_axes."""
     torch = _torch or _t()
-    if stream is not None:
-        with _current(stream):
-            return dak_kv_append_rope(KV, rope, q, k_new, v_new, slots, positions, n_new, q_out, slot_pos, acc=acc)
     B, Hkv, D, L = _kv_shape(KV)
     T = k_new.shape[1] if k_new.ndim == 4 else 1
     dtype, dev = k_new.dtype, _get_device()
@@ -742,13 +746,54 @@ def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slot
     elif q_out is not None:
         raise ValueError("q_out without q")
     i32, per_request, table = torch.int32, (B,), (B, Hkv, L)
-    _check(lib.dak_kv_append_rope_acc(KV.handle, rope, qa, ka, va, fp32, T, Hq, qp, kp, vp,
-                                      _arg(slots, "slots", i32, per_request, dev),
-                                      _arg(positions, "positions", i32, per_request, dev),
-                                      _arg(n_new, "n_new", i32, per_request, dev), oa,
-                                      _arg(slot_pos, "slot_pos", i32, table, dev),
-                                      _arg(acc, "acc", torch.float32, table, dev), _get_stream(dev)), "dak_kv_append_rope")
+    fn, name = (lib.dak_kv_append_rope_axes, "dak_kv_append_rope_axes") if axes else (lib.dak_kv_append_rope_acc, "dak_kv_append_rope")
+    _check(fn(KV.handle, rope, qa, ka, va, fp32, T, Hq, qp, kp, vp, _arg(slots, "slots", i32, per_request, dev),
+              _arg(positions, "positions", i32, (B, T, axes) if axes else per_request, dev),
+              _arg(n_new, "n_new", i32, per_request, dev), oa, _arg(slot_pos, "slot_pos", i32, table, dev),
+              _arg(acc, "acc", torch.float32, table, dev), _get_stream(dev)), name)
     return q_out
+
+
+def dak_kv_append_rope(KV: Placement, rope: dak_rope_plan, q, k_new, v_new, slots, positions=None, n_new=None,
+                       q_out=None, slot_pos=None, stream=None, acc=None):
+    """Rotate new tokens and append them to a placed cache (dak.h): q [B][T][H_q][D] (or None),
+    k_new and v_new [B][T][H_kv][D], bf16 or fp32 CUDA, slices of one projection's output as
+    they are (T = 1: the T axis may be absent); slots, positions, n_new int32 CUDA [B];
+    slot_pos int32 and acc fp32 CUDA [B][H_kv][L], updated in place: a written row's position,
+    and 0 for its accumulated weight (the table of dak_attn_acc). Returns q_out, bf16, shaped as q (None
+    without q)."""
+    if stream is not None:
+        _torch or _t()
+        with _current(stream):
+            return _append_rope(KV, rope, 0, q, k_new, v_new, slots, positions, n_new, q_out, slot_pos, acc)
+    return _append_rope(KV, rope, 0, q, k_new, v_new, slots, positions, n_new, q_out, slot_pos, acc)
+
+
+def dak_rope_axes_make(rope: dak_rope_plan, axis=None, n_axes: int = None) -> dak_rope_axes_plan:
+    """The rotation of dak_kv_append_rope_axes: the pairs and frequencies of rope, pair i turned by a
+    token's position on axis[i] (one per pair of rope; None: axis 0 for all). n_axes: positions of
+    a token, 1..4 (None: as many as axis names)."""
+    a = None if axis is None else [int(x) for x in axis]
+    if a is not None and len(a) != rope.rot_dim // 2:
+        raise ValueError(f"axis must name one axis for each of the {rope.rot_dim // 2} pairs")
+    n = int(n_axes) if n_axes is not None else 1 if a is None else max(a) + 1
+    out = dak_rope_axes_plan()
+    _check(lib.dak_rope_axes_make(ctypes.byref(rope), n, None if a is None else (ctypes.c_int * len(a))(*a),
+                                  ctypes.byref(out)), "dak_rope_axes_make")
+    return out
+
+
+def dak_kv_append_rope_axes(KV: Placement, rope: dak_rope_axes_plan, q, k_new, v_new, slots, positions, n_new=None,
+                            q_out=None, slot_pos=None, acc=None, stream=None):
+    """dak_kv_append_rope for tokens with positions of their own (dak.h): positions int32 CUDA
+    [B][T][rope.n_axes]. Rows are slots[b] + t; slot_pos takes a token's position on axis 0."""
+    if positions is None:
+        raise ValueError("positions int32 [B][T][n_axes] are required")
+    if stream is not None:
+        _torch or _t()
+        with _current(stream):
+            return _append_rope(KV, rope, rope.n_axes, q, k_new, v_new, slots, positions, n_new, q_out, slot_pos, acc)
+    return _append_rope(KV, rope, rope.n_axes, q, k_new, v_new, slots, positions, n_new, q_out, slot_pos, acc)
 
 
 def dak_kv_evict_workspace_bytes(KV: Placement) -> int:
@@ -793,6 +838,139 @@ def dak_kv_evict(KV: Placement, seq_lens, n_keep: int, n_recent: int, acc, slot_
     finally:
         _free(ws)
     return lens_out, src_out
+
+
+# ------------------------------------------------------------------------------- drafted trees, forked caches
+
+MAX_TREE = 256  # DAK_MAX_TREE in dak.h
+
+
+def dak_tree_mask(parents, device="cuda"):
+    """The masks and depths of trees of drafted tokens: parents [B][T] (or [T]: one tree), each token's
+    parent among the tokens before it, or -1 for one that continues the text itself. Returns (mask
+    int64 [B][T][ceil(T / 64)], bit s % 64 of word s // 64 for draft s: a token's ancestors and
+    itself; depths int32 [B][T], 0 for a token without parent: what to add to a request's length for
+    its position). Host arithmetic, copied to device."""
+    import torch
+    p = np.asarray(parents.cpu() if isinstance(parents, torch.Tensor) else parents, dtype=np.int64)
+    p = p[None] if p.ndim == 1 else p
+    if p.ndim != 2 or p.shape[1] < 1:
+        raise ValueError("parents must be [B][T] or [T]")
+    B, T = p.shape
+    if ((p < -1) | (p >= np.arange(T))).any():
+        raise ValueError("a token's parent must be -1 or one of the tokens before it")
+    mask, depth = np.zeros((B, T, -(-T // 64)), np.uint64), np.zeros((B, T), np.int32)
+    b = np.arange(B)
+    for t in range(T):
+        has, at = p[:, t] >= 0, np.maximum(p[:, t], 0)
+        mask[:, t] = np.where(has[:, None], mask[b, at], np.uint64(0))
+        mask[:, t, t // 64] |= np.uint64(1) << np.uint64(t % 64)
+        depth[:, t] = np.where(has, depth[b, at] + 1, 0)
+    return torch.from_numpy(mask.view(np.int64)).to(device), torch.from_numpy(depth).to(device)
+
+
+def dak_attn_tree_workspace_bytes(KV: Placement, T: int, H_q: int) -> int:
+    return int(lib.dak_attn_tree_workspace_bytes(KV.handle, int(T), int(H_q)))
+
+
+def dak_attn_tree(Q, KV: Placement, seq_lens, mask=None, n_new=None, scale: float = 0.0, O=None, o_fp32: bool = False,
+                  workspace=None, tuning=None, stream=None):
+    """Decode attention of T drafted tokens per request (dak.h): Q bf16 CUDA [B][T][H_q][D]; seq_lens
+    int32 CUDA [B], the cached rows before the drafted ones, which lie behind them; mask int64 CUDA
+    [B][T][ceil(T / 64)], or [1][T][ceil(T / 64)] for one tree for all (dak_tree_mask), None: a chain;
+    n_new int32 CUDA [B], drafted tokens of each request (None: T). Returns O, shaped as Q; the
+    rows of tokens t >= n_new[b] of a given O are left as they were (of a new one: anything)."""
+    torch = _torch or _t()
+    if stream is not None:
+        with _current(stream):
+            return dak_attn_tree(Q, KV, seq_lens, mask, n_new, scale, O, o_fp32, workspace, tuning)
+    dev = _get_device()
+    B, Hkv, D, L = _kv_shape(KV)
+    shape = Q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != D:
+        raise ValueError("Q must be [B][T][H_q][D] of the KV placement's B and D")
+    _, T, Hq, _ = shape
+    words = -(-T // 64)
+    dtype = torch.float32 if o_fp32 else torch.bfloat16
+    qa = _arg(Q, "Q", torch.bfloat16, shape, dev)
+    pitch = 0
+    if mask is not None and mask.shape[0] != 1:
+        pitch = T * words
+    ma = _arg(mask, "mask", torch.int64, (B if pitch else 1, T, words), dev)
+    if O is None:
+        O = _empty((B, T, Hq, D), (T * Hq * D, Hq * D, D, 1), dtype)
+    la, na = _arg(seq_lens, "seq_lens", torch.int32, (B,), dev), _arg(n_new, "n_new", torch.int32, (B,), dev)
+    args = (qa, KV.handle, la, T, ma, pitch, na, Hq, float(scale), _arg(O, "O", dtype, shape, dev), bool(o_fp32))
+    st, tun = _get_stream(dev), _tuning(tuning)
+    if workspace is not None:
+        _check(lib.dak_attn_tree(*args, *_given(workspace, dev), tun, st), "dak_attn_tree")
+        return O
+    n = KV.cached(("tree", T, Hq), lambda: dak_attn_tree_workspace_bytes(KV, T, Hq))
+    ws = _alloc(n, st)
+    try:
+        _check(lib.dak_attn_tree(*args, ws, n, tun, st), "dak_attn_tree")
+    finally:
+        _free(ws)
+    return O
+
+
+def dak_kv_commit(KV: Placement, seq_lens, path, n_path, T: int, n_new=None, lens_out=None, slot_pos=None, acc=None,
+                  stream=None):
+    """Keep the accepted drafts of a tree whose T rows lie behind each request's own (dak.h): row
+    seq_lens[b] + path[b][i] becomes row seq_lens[b] + i for i < n_path[b]. path int32 CUDA [B][P], ascending
+    draft numbers; seq_lens, n_path, n_new (None: T) int32 CUDA [B]; slot_pos int32 and acc fp32 CUDA
+    [B][H_kv][L], updated in place. Returns lens_out int32 [B], the new lengths."""
+    torch = _torch or _t()
+    if stream is not None:
+        with _current(stream):
+            return dak_kv_commit(KV, seq_lens, path, n_path, T, n_new, lens_out, slot_pos, acc)
+    B, Hkv, _, L = _kv_shape(KV)
+    i32, per_request, table, dev = torch.int32, (B,), (B, Hkv, L), _get_device()
+    if path.ndim != 2:
+        raise ValueError("path must be [B][P]")
+    P = path.shape[1]
+    if lens_out is None:
+        lens_out = _empty(per_request, (1,), i32)
+    _check(lib.dak_kv_commit(KV.handle, _arg(seq_lens, "seq_lens", i32, per_request, dev), int(T),
+                             _arg(n_new, "n_new", i32, per_request, dev), _arg(path, "path", i32, (B, P), dev), P,
+                             _arg(n_path, "n_path", i32, per_request, dev), _arg(lens_out, "lens_out", i32, per_request, dev),
+                             _arg(slot_pos, "slot_pos", i32, table, dev), _arg(acc, "acc", torch.float32, table, dev),
+                             _get_stream(dev)), "dak_kv_commit")
+    return lens_out
+
+
+def dak_kv_fork(KV: Placement, src_of, seq_lens, first=None, source: Placement = None, lens_out=None, slot_pos=None,
+                acc=None, source_slot_pos=None, source_acc=None, stream=None):
+    """Let request b of a placed cache take over rows first[b] .. n - 1 of request src_of[b] (dak.h), of the
+    same cache, all at once, or of another placement source; n is that request's seq_lens. src_of
+    (negative: b stays) and first (None: 0) int32 CUDA [B], seq_lens int32 CUDA of the source's requests;
+    slot_pos int32 and acc fp32 CUDA [B][H_kv][L], updated in place, with source_slot_pos and source_acc
+    the source's (with source). Returns lens_out int32 [B], the new lengths; with source, the entries
+    of requests that stay are left as they are, so that lens_out has to be given."""
+    torch = _torch or _t()
+    if stream is not None:
+        with _current(stream):
+            return dak_kv_fork(KV, src_of, seq_lens, first, source, lens_out, slot_pos, acc, source_slot_pos, source_acc)
+    B, Hkv, _, L = _kv_shape(KV)
+    i32, f32, per_request, table, dev = torch.int32, torch.float32, (B,), (B, Hkv, L), _get_device()
+    if source is None:
+        if source_slot_pos is not None or source_acc is not None:
+            raise ValueError("source_slot_pos and source_acc need a source")
+        source, source_slot_pos, source_acc, n, from_table = KV, slot_pos, acc, B, table
+    else:
+        n, shkv, _, sl = _kv_shape(source, "source")
+        from_table = (n, shkv, sl)
+        if lens_out is None:
+            raise ValueError("a fork from another placement needs lens_out")
+    if lens_out is None:
+        lens_out = _empty(per_request, (1,), i32)
+    _check(lib.dak_kv_fork(KV.handle, source.handle, _arg(src_of, "src_of", i32, per_request, dev),
+                           _arg(seq_lens, "seq_lens", i32, (n,), dev), _arg(first, "first", i32, per_request, dev),
+                           _arg(lens_out, "lens_out", i32, per_request, dev),
+                           _arg(source_slot_pos, "source_slot_pos", i32, from_table, dev),
+                           _arg(slot_pos, "slot_pos", i32, table, dev), _arg(source_acc, "source_acc", f32, from_table, dev),
+                           _arg(acc, "acc", f32, table, dev), _get_stream(dev)), "dak_kv_fork")
+    return lens_out
 
 
 # ------------------------------------------------------------------------------- attention for serving

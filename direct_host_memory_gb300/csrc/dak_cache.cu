@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "dak_device.cuh"
 
@@ -31,6 +32,14 @@ struct RopeParams {
     int T, Hq, Hkv, L, h_s;
     DevStatus* st;
 };
+
+// Every token's own positions (dak_kv_append_rope_axes).
+struct RopeAxes {
+    const int* positions;  // [B][T][n]
+    int n;
+    unsigned char axis[64];
+};
+struct NoAxes {};
 
 constexpr int kRopeThreads = 128;
 
@@ -86,8 +95,10 @@ __device__ __forceinline__ uint4 pack8(const float* y) {
 // launch (1 token 2.9 us, 256 tokens fp32 4.5 us).
 enum { kRopeSplit = 0, kRopeInterleaved = 1, kRopePart = 2 };  // PART: halves of a part of the head
 
-template <int D, bool F32, int KIND>
-__global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8) append_rope_kernel(const __grid_constant__ RopeParams p) {
+template <int D, bool F32, int KIND, class Axes>
+__global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8)
+    append_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ Axes axes) {
+    constexpr bool AXES = !std::is_same<Axes, NoAxes>::value;
     constexpr int PAIRS = D / 16;  // units of a head
     constexpr int PER = 3;         // units in flight per thread (a token of the 8B shape: all of them)
     __shared__ float2 cs[D / 2];
@@ -96,7 +107,7 @@ __global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8) append_rope_kernel(
     const int R = p.rope.rot_dim, half = R / 2;
     const int heads = p.Hq + 2 * p.Hkv, n_units = heads * PAIRS, stride = gridDim.y * kRopeThreads;
     grid_dep_wait();  // launched while the previous kernel ends
-    const int n_new = p.n_new ? p.n_new[b] : p.T, slot = p.slots[b], first = p.positions ? p.positions[b] : slot;
+    const int n_new = p.n_new ? p.n_new[b] : p.T, slot = p.slots[b], first = !AXES && p.positions ? p.positions[b] : slot;
     bool ready = false, in_range = false;
     long long row = 0, pos = 0;
     for (int u0 = blockIdx.y * kRopeThreads + threadIdx.x; u0 - static_cast<int>(threadIdx.x) < n_units; u0 += PER * stride) {
@@ -128,9 +139,15 @@ __global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8) append_rope_kernel(
             if (t >= n_new) return;
             row = static_cast<long long>(slot) + t;
             pos = static_cast<long long>(first) + t;
+            long long turning = pos;  // the position that this thread's pair turns by
+            if constexpr (AXES) {
+                const int* own = axes.positions + token * axes.n;
+                pos = own[0];
+                if (static_cast<int>(threadIdx.x) < half) turning = own[axes.axis[threadIdx.x]];
+            }
             in_range = row >= 0 && row < p.L;
             if (static_cast<int>(threadIdx.x) < half) {
-                const uint64_t turn = static_cast<uint64_t>(pos) * p.rope.turns[threadIdx.x];
+                const uint64_t turn = static_cast<uint64_t>(turning) * p.rope.turns[threadIdx.x];
                 const float a = static_cast<float>(static_cast<int>(static_cast<uint32_t>(turn >> 32))) * 0x1p-31f;
                 float s, c;
                 sincospif(a, &s, &c);
@@ -205,8 +222,8 @@ __global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8) append_rope_kernel(
     }
 }
 
-template <int D, bool F32>
-static cudaError_t launch_append_rope(const RopeParams& p, dim3 grid, cudaStream_t s) {
+template <int D, bool F32, class Axes>
+static cudaError_t launch_append_rope(const RopeParams& p, const Axes& axes, dim3 grid, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -216,9 +233,9 @@ static cudaError_t launch_append_rope(const RopeParams& p, dim3 grid, cudaStream
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (p.rope.interleaved) return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopeInterleaved>, p);
-    if (p.rope.rot_dim == D) return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopeSplit>, p);
-    return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopePart>, p);
+    if (p.rope.interleaved) return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopeInterleaved, Axes>, p, axes);
+    if (p.rope.rot_dim == D) return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopeSplit, Axes>, p, axes);
+    return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopePart, Axes>, p, axes);
 }
 
 // ------------------------------------------------------------------------------------
@@ -894,10 +911,13 @@ extern "C" dak_status dak_rope_make(int head_dim, const dak_rope_config* cfg, da
     return dak_rope_from_freqs(head_dim, inv, R / 2, cfg->interleaved, cfg->attn_scale, out);
 }
 
-extern "C" dak_status dak_kv_append_rope_acc(const dak_placement* KV, const dak_rope_plan* rope, const void* q,
-                                             const void* k, const void* v, int in_fp32, int T, int H_q, int64_t q_pitch,
-                                             int64_t k_pitch, int64_t v_pitch, const int* slots, const int* positions,
-                                             const int* n_new, void* q_out, int* slot_pos, float* acc, void* stream) {
+namespace dak {
+
+// dak_kv_append_rope_acc (axes null) and dak_kv_append_rope_axes.
+static dak_status append_rope(const dak_placement* KV, const dak_rope_plan* rope, const dak_rope_axes_plan* axes,
+                              const void* q, const void* k, const void* v, int in_fp32, int T, int H_q, int64_t q_pitch,
+                              int64_t k_pitch, int64_t v_pitch, const int* slots, const int* positions, const int* n_new,
+                              void* q_out, int* slot_pos, float* acc, void* stream) {
     if (!KV || KV->kind != 1 || !rope || !k || !v || !slots || T < 1 || H_q < 0) return DAK_ERR_INVALID;
     if (H_q > 0 && (!q || !q_out)) return DAK_ERR_INVALID;
     const int D = KV->D;
@@ -952,8 +972,60 @@ extern "C" dak_status dak_kv_append_rope_acc(const dak_placement* KV, const dak_
     const int64_t room = std::max<int64_t>(1, 8ll * device_sm_count() / tokens);
     const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(std::min<int64_t>(std::min(blocks, 16), room)));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return cuda_status(D == 128 ? (in_fp32 ? launch_append_rope<128, true>(p, grid, s) : launch_append_rope<128, false>(p, grid, s))
-                                : (in_fp32 ? launch_append_rope<64, true>(p, grid, s) : launch_append_rope<64, false>(p, grid, s)));
+    const auto launch = [&](const auto& a) {
+        if (D == 128) return in_fp32 ? launch_append_rope<128, true>(p, a, grid, s) : launch_append_rope<128, false>(p, a, grid, s);
+        return in_fp32 ? launch_append_rope<64, true>(p, a, grid, s) : launch_append_rope<64, false>(p, a, grid, s);
+    };
+    if (!axes) return cuda_status(launch(NoAxes{}));
+    RopeAxes a{};
+    a.positions = positions;
+    a.n = axes->n_axes;
+    std::copy(axes->axis, axes->axis + 64, a.axis);
+    return cuda_status(launch(a));
+}
+
+// What dak_rope_axes_make makes, whose axes lie inside a token's positions.
+static bool good_axes(const dak_rope_axes_plan* r) {
+    if (!r || r->n_axes < 1 || r->n_axes > DAK_ROPE_MAX_AXES) return false;
+    for (const unsigned char a : r->axis) {
+        if (a >= r->n_axes) return false;
+    }
+    return true;
+}
+
+}  // namespace dak
+
+extern "C" dak_status dak_rope_axes_make(const dak_rope_plan* rope, int n_axes, const int* axis, dak_rope_axes_plan* out) {
+    if (!rope || !out || n_axes < 1 || n_axes > DAK_ROPE_MAX_AXES) return DAK_ERR_INVALID;
+    if ((rope->head_dim != 64 && rope->head_dim != 128) || rope->rot_dim < 2 || rope->rot_dim > rope->head_dim || rope->rot_dim % 2) {
+        return DAK_ERR_INVALID;
+    }
+    dak_rope_axes_plan r{};
+    r.rope = *rope;
+    r.n_axes = n_axes;
+    for (int i = 0; axis && i < rope->rot_dim / 2; ++i) {
+        if (axis[i] < 0 || axis[i] >= n_axes) return DAK_ERR_INVALID;
+        r.axis[i] = static_cast<unsigned char>(axis[i]);
+    }
+    *out = r;
+    return DAK_OK;
+}
+
+extern "C" dak_status dak_kv_append_rope_axes(const dak_placement* KV, const dak_rope_axes_plan* rope, const void* q,
+                                              const void* k, const void* v, int in_fp32, int T, int H_q, int64_t q_pitch,
+                                              int64_t k_pitch, int64_t v_pitch, const int* slots, const int* positions,
+                                              const int* n_new, void* q_out, int* slot_pos, float* acc, void* stream) {
+    if (!good_axes(rope) || !positions) return DAK_ERR_INVALID;
+    return append_rope(KV, &rope->rope, rope, q, k, v, in_fp32, T, H_q, q_pitch, k_pitch, v_pitch, slots, positions, n_new,
+                       q_out, slot_pos, acc, stream);
+}
+
+extern "C" dak_status dak_kv_append_rope_acc(const dak_placement* KV, const dak_rope_plan* rope, const void* q,
+                                             const void* k, const void* v, int in_fp32, int T, int H_q, int64_t q_pitch,
+                                             int64_t k_pitch, int64_t v_pitch, const int* slots, const int* positions,
+                                             const int* n_new, void* q_out, int* slot_pos, float* acc, void* stream) {
+    return append_rope(KV, rope, nullptr, q, k, v, in_fp32, T, H_q, q_pitch, k_pitch, v_pitch, slots, positions, n_new, q_out,
+                       slot_pos, acc, stream);
 }
 
 extern "C" dak_status dak_kv_append_rope(const dak_placement* KV, const dak_rope_plan* rope, const void* q,

@@ -1,0 +1,408 @@
+// Rows of a placed KV cache moved as a whole: the accepted path of a tree of drafted tokens
+// (dak_kv_commit) and requests that take over the rows of others (dak_kv_fork). Layout and tiers:
+// dak_attn.cu.
+#include <algorithm>
+#include <climits>
+
+#include "dak_device.cuh"
+
+namespace dak {
+
+// A slab's address in whichever tier holds it.
+struct Tiers {
+    uint8_t* host;
+    uint8_t* hbm;
+    long long head_bytes;
+    int h_s;
+    __device__ __forceinline__ uint8_t* slab(long long s) const {
+        return s < h_s ? host + s * head_bytes : hbm + (s - h_s) * head_bytes;
+    }
+};
+
+static Tiers tiers_of(const dak_placement* p) {
+    return {static_cast<uint8_t*>(p->host_dev), static_cast<uint8_t*>(p->hbm_ptr), p->head_bytes, p->h_s};
+}
+
+// ------------------------------------------------------------------------------------
+// commit
+// ------------------------------------------------------------------------------------
+struct CommitParams {
+    Tiers kv;
+    const int* lens;
+    const int* n_new;
+    const int* path;
+    const int* n_path;
+    int* lens_out;
+    int* slot_pos;
+    float* acc;
+    int T, P, Hkv, L;
+    DevStatus* st;
+};
+
+constexpr int kCommitThreads = 256;
+
+// One block per slab, a thread per 16-byte piece of up to eight rows of K or V. A path ascends, so that
+// path[i] >= i: no row is written before the rows after it in the path have been read, if every
+// group of rows is read whole before it is written, and groups are taken in order.
+template <int D>
+__global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitParams p) {
+    constexpr int PIECES = 2 * (D / 8);                // of a row's K and V
+    constexpr int LANES = kCommitThreads / PIECES;     // rows side by side
+    constexpr int PER = 8;
+    __shared__ int path[DAK_MAX_TREE];
+    const int tid = threadIdx.x, b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv;
+    const long long slab = blockIdx.x;
+    grid_dep_wait();  // launched while the previous kernel ends
+    const int base = min(max(p.lens[b], 0), p.L), n_new = p.n_new ? min(max(p.n_new[b], 0), p.T) : p.T;
+    int n = min(max(p.n_path[b], 0), p.P);
+    const int* in = p.path + static_cast<long long>(b) * p.P;
+    bool good = true;
+    if (tid < n) {
+        const int v = in[tid];
+        path[tid] = v;
+        good = v >= (tid ? in[tid - 1] + 1 : 0) && v < n_new && v < p.L - base;
+    }
+    if (!__syncthreads_and(good)) {
+        if (g == 0 && tid == 0) report(p.st, DAK_ERR_BOUNDS, (0xC0113ull << 32) | static_cast<unsigned>(b));
+        n = 0;
+    }
+    if (g == 0 && tid == 0) p.lens_out[b] = base + n;
+    uint4* rows = reinterpret_cast<uint4*>(p.kv.slab(slab));
+    const int piece = tid % PIECES, kv = piece / (D / 8), c = piece % (D / 8), r0 = tid / PIECES;
+    const auto at = [&](int j) -> uint4& {
+        return rows[(static_cast<long long>(j >> 6) * 2 + kv) * (8 * D) + (j & 63) * (D / 8) + (c ^ (j & 7))];
+    };
+    for (int i0 = 0; i0 < n; i0 += LANES * PER) {
+        uint4 v[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = i0 + k * LANES + r0;
+            if (i < n && path[i] != i) v[k] = at(base + path[i]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = i0 + k * LANES + r0;
+            if (i < n && path[i] != i) at(base + i) = v[k];
+        }
+    }
+    if (!p.slot_pos && !p.acc) return;
+    int* pos = p.slot_pos ? p.slot_pos + slab * p.L + base : nullptr;
+    float* acc = p.acc ? p.acc + slab * p.L + base : nullptr;
+    int pv = -1;
+    float av = 0.f;
+    if (tid < n) {
+        if (pos) pv = pos[path[tid]];
+        if (acc) av = acc[path[tid]];
+    }
+    __syncthreads();
+    if (tid < min(n_new, p.L - base)) {
+        if (pos) pos[tid] = pv;
+        if (acc) acc[tid] = av;
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// fork
+// ------------------------------------------------------------------------------------
+struct ForkParams {
+    Tiers to, from;
+    const int* src_of;
+    const int* lens;
+    const int* first;
+    int* lens_out;
+    const int* src_pos;
+    int* pos;
+    const float* src_acc;
+    float* acc;
+    int B, L, src_B, src_L, Hkv;
+    int same;   // src is KV
+    int stage;  // bytes of one of the two staging buffers
+    DevStatus* st;
+};
+
+constexpr int kForkThreads = 256;
+constexpr int kForkMax = DAK_MAX_FORK;
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// Every request that others go on from is a source, with a place in the staging buffers. A unit is the
+// same stretch of bytes (a power of two, at most 64 rows of K or V, as many as fit in a buffer
+// for all sources) of one chunk and kv head: it is read from every source, and once all have arrived
+// written to every taker. No other unit reads or writes these bytes of any request, so that any map can
+// be taken in place, and a source is read once however many take from it. Two buffers: a unit's bytes
+// are on their way while the one before is written.
+template <int D>
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int n_src, n_take, lowest, highest;
+    uint8_t* buffer = smem;
+    int* slot_of = reinterpret_cast<int*>(smem + 2 * p.stage);
+    int* src_f = slot_of + p.src_B;    // of each source: request, rows wanted
+    int* src_lo = src_f + p.src_B;
+    int* src_n = src_lo + p.src_B;
+    int* take_b = src_n + p.src_B;     // of each taker: request, its source's place, first row
+    int* take_slot = take_b + p.B;
+    int* take_lo = take_slot + p.B;
+    const int tid = threadIdx.x;
+    if (tid == 0) n_src = n_take = 0, lowest = INT_MAX, highest = 0;
+    for (int f = tid; f < p.src_B; f += kForkThreads) src_lo[f] = INT_MAX;  // for now by request
+    grid_dep_wait();  // launched while the previous kernel ends
+    __syncthreads();
+    for (int b = tid; b < p.B; b += kForkThreads) {
+        const int f = p.src_of[b];
+        const bool known = f >= 0 && f < p.src_B, takes = known && !(p.same && f == b);
+        int n = 0, lo = 0;
+        if (known) {
+            n = min(max(p.lens[f], 0), p.src_L);
+            if (n > p.L) {
+                if (blockIdx.x == 0) report(p.st, DAK_ERR_BOUNDS, (0xF02Cull << 32) | static_cast<unsigned>(b));
+                n = p.L;
+            }
+            lo = p.first ? min(max(p.first[b], 0), n) : 0;
+        } else if (f >= p.src_B && blockIdx.x == 0) {
+            report(p.st, DAK_ERR_BOUNDS, (0xF02Dull << 32) | static_cast<unsigned>(b));
+        }
+        if (blockIdx.x == 0) {
+            if (takes) p.lens_out[b] = n;
+            else if (p.same) p.lens_out[b] = min(max(p.lens[b], 0), p.L);
+        }
+        if (takes && lo < n) {
+            const int k = atomicAdd(&n_take, 1);
+            take_b[k] = b;
+            take_slot[k] = f;  // for now the request
+            take_lo[k] = lo;
+            atomicMin(&src_lo[f], lo);
+            atomicMin(&lowest, lo);
+            atomicMax(&highest, n);
+        }
+    }
+    __syncthreads();
+    const int takers = n_take;
+    if (takers == 0) return;
+    for (int f = tid; f < p.src_B; f += kForkThreads) {
+        slot_of[f] = src_lo[f] < INT_MAX ? atomicAdd(&n_src, 1) : -1;
+    }
+    __syncthreads();
+    const int sources = n_src;
+    // the lists by place; src_lo is read by request before it is written by place
+    for (int f0 = 0; f0 < p.src_B; f0 += kForkThreads) {
+        const int f = f0 + tid;
+        const bool in = f < p.src_B && slot_of[f] >= 0;
+        if (in) {
+            src_f[slot_of[f]] = f;
+            src_n[slot_of[f]] = min(min(max(p.lens[f], 0), p.src_L), p.L);
+        }
+    }
+    for (int k = tid; k < takers; k += kForkThreads) take_slot[k] = slot_of[take_slot[k]];
+    __syncthreads();
+    for (int s = tid; s < sources; s += kForkThreads) slot_of[s] = src_lo[src_f[s]];
+    __syncthreads();
+    const int* lo_of = slot_of;  // by place from here on
+
+    constexpr int kRow = 2 * D;          // bytes of a row of K or V
+    constexpr int kHalf = 64 * kRow;     // of a chunk's K or V
+    int unit = kHalf;
+    while (unit > 16 && unit * sources > p.stage) unit >>= 1;
+    const int shift = 31 - __clz(unit >> 4);  // pieces of 16 bytes of a unit: 1 << shift
+    const int subs = kHalf / unit, c0 = lowest >> 6, chunks = ((highest + 63) >> 6) - c0;
+    const long long n_units = static_cast<long long>(chunks) * 2 * subs * p.Hkv;
+    // unit x: kv head, chunk, byte offset in the slab and in the chunk's K or V
+    const auto place = [&](long long x, int& g, long long& at, int& row0, int& in_half) {
+        g = static_cast<int>(x % p.Hkv);
+        long long r = x / p.Hkv;
+        in_half = static_cast<int>(r % subs) * unit;
+        r /= subs;
+        const int kv = static_cast<int>(r & 1), c = c0 + static_cast<int>(r >> 1);
+        at = (static_cast<long long>(c) * 2 + kv) * kHalf + in_half;
+        row0 = c * 64;
+    };
+    const auto read = [&](long long x, uint8_t* to) {
+        int g, row0, in_half;
+        long long at;
+        place(x, g, at, row0, in_half);
+        for (int e = tid; e < sources << shift; e += kForkThreads) {
+            const int s = e >> shift, off = (e & ((1 << shift) - 1)) << 4, row = row0 + (in_half + off) / kRow;
+            if (row < lo_of[s] || row >= src_n[s]) continue;
+            copy_async16(to + (static_cast<long long>(e) << 4), p.from.slab(static_cast<long long>(src_f[s]) * p.Hkv + g) + at + off);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    long long x = blockIdx.x;
+    int k = 0;
+    if (x < n_units) read(x, buffer);
+    for (; x < n_units; x += gridDim.x, k ^= 1) {
+        if (x + gridDim.x < n_units) read(x + gridDim.x, buffer + (k ^ 1) * p.stage);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        int g, row0, in_half;
+        long long at;
+        place(x, g, at, row0, in_half);
+        const uint8_t* from = buffer + k * p.stage;
+        for (int e = tid; e < takers << shift; e += kForkThreads) {
+            const int t = e >> shift, off = (e & ((1 << shift) - 1)) << 4, row = row0 + (in_half + off) / kRow, s = take_slot[t];
+            if (row < take_lo[t] || row >= src_n[s]) continue;
+            *reinterpret_cast<uint4*>(p.to.slab(static_cast<long long>(take_b[t]) * p.Hkv + g) + at + off) =
+                *reinterpret_cast<const uint4*>(from + static_cast<long long>(s) * unit + off);
+        }
+        __syncthreads();  // the buffer is free
+    }
+    if (!p.pos && !p.acc) return;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // the tables likewise, a word of each a row
+    int rows = 1024;
+    while (rows > 1 && rows * sources * 8 > 2 * p.stage) rows >>= 1;
+    const int lg = 31 - __clz(rows), blocks = (highest - lowest + rows - 1) / rows;
+    int* hold_pos = reinterpret_cast<int*>(buffer);
+    float* hold_acc = reinterpret_cast<float*>(hold_pos + rows * sources);
+    const long long from_x = (blockIdx.x + gridDim.x - n_units % gridDim.x) % gridDim.x;  // on where the units ended
+    for (long long y = from_x; y < static_cast<long long>(blocks) * p.Hkv; y += gridDim.x) {
+        const int g = static_cast<int>(y % p.Hkv), j0 = lowest + static_cast<int>(y / p.Hkv) * rows;
+        for (int e = tid; e < sources << lg; e += kForkThreads) {
+            const int s = e >> lg, j = j0 + (e & (rows - 1));
+            if (j < lo_of[s] || j >= src_n[s]) continue;
+            const long long at = (static_cast<long long>(src_f[s]) * p.Hkv + g) * p.src_L + j;
+            if (p.pos) hold_pos[e] = p.src_pos[at];
+            if (p.acc) hold_acc[e] = p.src_acc[at];
+        }
+        __syncthreads();
+        for (int e = tid; e < takers << lg; e += kForkThreads) {
+            const int t = e >> lg, r = e & (rows - 1), j = j0 + r, s = take_slot[t];
+            if (j < take_lo[t] || j >= src_n[s]) continue;
+            const long long at = (static_cast<long long>(take_b[t]) * p.Hkv + g) * p.L + j;
+            if (p.pos) p.pos[at] = hold_pos[(s << lg) + r];
+            if (p.acc) p.acc[at] = hold_acc[(s << lg) + r];
+        }
+        __syncthreads();
+    }
+}
+
+static int fork_plan_bytes(int B, int src_B) { return (4 * src_B + 3 * B) * static_cast<int>(sizeof(int)); }
+
+template <int D>
+static cudaError_t launch_fork(ForkParams& p, cudaStream_t s) {
+    // two CTAs an SM, or one where the lists take more room
+    constexpr int kTwo = 110 * 1024, kOne = 220 * 1024;
+    const int plan = fork_plan_bytes(p.B, p.src_B);
+    const int least = std::max(16 * 1024, 16 * p.src_B);
+    const int per_sm = plan + 2 * least <= kTwo ? 2 : 1;
+    p.stage = ((per_sm == 2 ? kTwo : kOne) - plan) / 2 / 128 * 128;
+    const int smem = 2 * p.stage + plan;
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(fork_kernel<D>), kOne);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(per_sm * device_sm_count()));
+    cfg.blockDim = dim3(kForkThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fork_kernel<D>, p);
+}
+
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+static bool off(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+}  // namespace dak
+
+using namespace dak;
+
+extern "C" dak_status dak_kv_commit(const dak_placement* KV, const int* seq_lens, int T, const int* n_new, const int* path,
+                                    int P, const int* n_path, int* lens_out, int* slot_pos, float* acc, void* stream) {
+    if (!KV || KV->kind != 1 || !seq_lens || !path || !n_path || !lens_out || T < 1 || P < 1 || P > T) return DAK_ERR_INVALID;
+    if (T > DAK_MAX_TREE) return DAK_ERR_UNSUPPORTED;
+    if (off(seq_lens, 4) || off(n_new, 4) || off(path, 4) || off(n_path, 4) || off(lens_out, 4) || off(slot_pos, 4) || off(acc, 4)) {
+        return DAK_ERR_ALIGN;
+    }
+    const size_t lens = static_cast<size_t>(KV->B) * 4;
+    if (overlap(lens_out, lens, seq_lens, lens) || overlap(lens_out, lens, n_new, lens) || overlap(lens_out, lens, n_path, lens) ||
+        overlap(lens_out, lens, path, lens * P)) {
+        return DAK_ERR_INVALID;
+    }
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DAK_ERR_CUDA;
+    if (dev != KV->device) return DAK_ERR_INVALID;
+    CommitParams p{};
+    p.kv = tiers_of(KV);
+    p.lens = seq_lens;
+    p.n_new = n_new;
+    p.path = path;
+    p.n_path = n_path;
+    p.lens_out = lens_out;
+    p.slot_pos = slot_pos;
+    p.acc = acc;
+    p.T = T;
+    p.P = P;
+    p.Hkv = KV->H_kv;
+    p.L = KV->L;
+    p.st = status_ptr();
+    if (!p.st) return DAK_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(KV->B) * KV->H_kv);
+    cfg.blockDim = dim3(kCommitThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(KV->D == 128 ? cudaLaunchKernelEx(&cfg, commit_kernel<128>, p) : cudaLaunchKernelEx(&cfg, commit_kernel<64>, p));
+}
+
+extern "C" dak_status dak_kv_fork(const dak_placement* KV, const dak_placement* src, const int* src_of, const int* seq_lens,
+                                  const int* first, int* lens_out, const int* src_slot_pos, int* slot_pos,
+                                  const float* src_acc, float* acc, void* stream) {
+    if (!KV || KV->kind != 1 || !src || src->kind != 1 || !src_of || !seq_lens || !lens_out) return DAK_ERR_INVALID;
+    if (src->H_kv != KV->H_kv || src->D != KV->D || src->device != KV->device) return DAK_ERR_INVALID;
+    if (KV->B > kForkMax || src->B > kForkMax) return DAK_ERR_UNSUPPORTED;
+    if (!slot_pos != !src_slot_pos || !acc != !src_acc) return DAK_ERR_INVALID;
+    if (off(src_of, 4) || off(seq_lens, 4) || off(first, 4) || off(lens_out, 4) || off(src_slot_pos, 4) || off(slot_pos, 4) ||
+        off(src_acc, 4) || off(acc, 4)) {
+        return DAK_ERR_ALIGN;
+    }
+    const size_t lens = static_cast<size_t>(KV->B) * 4, src_lens = static_cast<size_t>(src->B) * 4;
+    if (overlap(lens_out, lens, src_of, lens) || overlap(lens_out, lens, first, lens) || overlap(lens_out, lens, seq_lens, src_lens)) {
+        return DAK_ERR_INVALID;
+    }
+    if (src == KV) {
+        if (slot_pos != src_slot_pos || acc != src_acc) return DAK_ERR_INVALID;
+    } else {
+        const size_t to = lens * KV->H_kv * KV->L, from = src_lens * src->H_kv * src->L;
+        if (overlap(slot_pos, to, src_slot_pos, from) || overlap(acc, to, src_acc, from)) return DAK_ERR_INVALID;
+    }
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DAK_ERR_CUDA;
+    if (dev != KV->device) return DAK_ERR_INVALID;
+    ForkParams p{};
+    p.to = tiers_of(KV);
+    p.from = tiers_of(src);
+    p.src_of = src_of;
+    p.lens = seq_lens;
+    p.first = first;
+    p.lens_out = lens_out;
+    p.src_pos = src_slot_pos;
+    p.pos = slot_pos;
+    p.src_acc = src_acc;
+    p.acc = acc;
+    p.B = KV->B;
+    p.L = KV->L;
+    p.src_B = src->B;
+    p.src_L = src->L;
+    p.Hkv = KV->H_kv;
+    p.same = src == KV;
+    p.st = status_ptr();
+    if (!p.st) return DAK_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(KV->D == 128 ? launch_fork<128>(p, s) : launch_fork<64>(p, s));
+}

@@ -266,6 +266,33 @@ dak_status dak_kv_append_rope_acc(const dak_placement* KV, const dak_rope_plan* 
                                   int64_t v_pitch, const int* slots, const int* positions, const int* n_new,
                                   void* q_out, int* slot_pos, float* acc, void* stream);
 
+/* A rotation whose tokens have a position on each of several axes (time, height and width of a
+ * picture's patches), or one of their own (drafted tokens, of which siblings share a position):
+ * pair i turns by the token's position on axis[i] times f_i. Plain data made by
+ * dak_rope_axes_make, kept by the caller.
+ *   rope  : the pairs and their frequencies, by dak_rope_make or dak_rope_from_freqs (a scheme
+ *           whose frequencies start anew on each axis is one of dak_rope_from_freqs).
+ *   n_axes: 1..DAK_ROPE_MAX_AXES. */
+#define DAK_ROPE_MAX_AXES 4
+typedef struct {
+    dak_rope_plan rope;
+    int n_axes;
+    unsigned char axis[64];
+} dak_rope_axes_plan;
+
+/* axis: [rope->rot_dim / 2], the axis of each pair, 0 <= axis[i] < n_axes; NULL = axis 0 for all.
+ * Host arithmetic only. DAK_ERR_INVALID: null pointers, a plan that dak_rope_make does not
+ * make, n_axes or an axis out of range. */
+dak_status dak_rope_axes_make(const dak_rope_plan* rope, int n_axes, const int* axis, dak_rope_axes_plan* out);
+
+/* dak_kv_append_rope_acc with a position of its own for every token: positions is int32
+ * [B][T][n_axes] (device, required). Rows are slots[b] + t as there; slot_pos takes a token's
+ * position on axis 0. Everything else as dak_kv_append_rope_acc. */
+dak_status dak_kv_append_rope_axes(const dak_placement* KV, const dak_rope_axes_plan* rope, const void* q,
+                                   const void* k, const void* v, int in_fp32, int T, int H_q, int64_t q_pitch,
+                                   int64_t k_pitch, int64_t v_pitch, const int* slots, const int* positions,
+                                   const int* n_new, void* q_out, int* slot_pos, float* acc, void* stream);
+
 /* Evict the least attended tokens of a placed KV cache, each (request, kv head) for itself.
  * Where a request holds L_b = seq_lens[b] (clamped to [0, L]) > n_keep tokens, n_keep slots
  * stay:
@@ -293,6 +320,51 @@ size_t dak_kv_evict_workspace_bytes(const dak_placement* KV);
 dak_status dak_kv_evict(const dak_placement* KV, const int* seq_lens, int n_keep, int n_recent, const float* acc,
                         float* acc_out, const int* slot_pos, int* slot_pos_out, int* lens_out, int* src_out,
                         void* workspace, size_t ws_bytes, void* stream);
+
+/* Keep the accepted path of a tree of drafted tokens, whose rows lie behind each request's own:
+ * row L_b + path[b][i] moves to L_b + i for i < n_path[b], in every kv head, within the tier
+ * that holds it; L_b = seq_lens[b], clamped to [0, L].
+ *   T       : drafted rows of a request, 1..DAK_MAX_TREE. n_new: int32 [B], how many of them were
+ *             drafted, clamped to [0, T], or NULL = T.
+ *   path    : int32 [B][P] (device), 1 <= P <= T: drafts in ascending order, below n_new[b], whose
+ *             rows lie inside the cache. n_path: int32 [B], clamped to [0, P].
+ *             A path that breaks these rules is reported by dak_last_error (DAK_ERR_BOUNDS), and
+ *             the request is treated as one that accepted nothing.
+ *   lens_out: int32 [B], L_b + n_path[b]; must not overlap seq_lens, n_new, path or n_path
+ *             (DAK_ERR_INVALID).
+ *   slot_pos, acc: int32 and fp32 [B][H_kv][L] (device) or NULL, updated in place: entries follow
+ *             their rows, those of the drafts that are not kept (from the new length to L_b +
+ *             n_new[b]) become -1 and 0.
+ * Rows behind the new length are left as they were. Stream-ordered; a following attention is
+ * launched without programmatic launch. DAK_ERR_UNSUPPORTED: T above DAK_MAX_TREE. */
+#define DAK_MAX_TREE 256
+dak_status dak_kv_commit(const dak_placement* KV, const int* seq_lens, int T, const int* n_new, const int* path,
+                         int P, const int* n_path, int* lens_out, int* slot_pos, float* acc, void* stream);
+
+/* Let requests take over the rows of others: request b of KV goes on from request f = src_of[b] of
+ * the placement src, whose rows first[b] .. n - 1 become b's rows, n = seq_lens[f] clamped to
+ * [0, L] of src. src may be KV itself: src_of may then be any map (beams that swap, several from
+ * one), as if all requests were read before any is written. Otherwise src has KV's H_kv, D and
+ * device, and a B, an L and a split between the tiers of its own. Where KV's L is smaller than n,
+ * n is that L (reported by dak_last_error as DAK_ERR_BOUNDS).
+ *   src_of  : int32 [KV's B] (device). Negative: the request stays as it is, as does b = src_of[b]
+ *             where src is KV. A value >= src's B counts as negative and is reported by dak_last_error
+ *             (DAK_ERR_BOUNDS).
+ *   seq_lens: int32 [src's B] (device).
+ *   first   : int32 [KV's B] (device), clamped to [0, n], or NULL = 0: rows below it are taken to be
+ *             the same already (beams behind one prompt).
+ *   lens_out: int32 [KV's B]: n for a request that takes over; for the others seq_lens[b] (clamped)
+ *             where src is KV, and else left as it was. Must not overlap src_of, seq_lens or first
+ *             (DAK_ERR_INVALID).
+ *   src_slot_pos, slot_pos, src_acc, acc: int32 and fp32 tables, [src's B][H_kv][src's L] and [KV's
+ *             B][H_kv][L] (device), of which each pair may be NULL: entries follow their rows. With
+ *             src = KV each table is its source (DAK_ERR_INVALID otherwise).
+ * Rows outside first[b] .. n - 1 are left as they were. Stream-ordered; a following attention is launched
+ * without programmatic launch. At most DAK_MAX_FORK requests in KV and in src (DAK_ERR_UNSUPPORTED). */
+#define DAK_MAX_FORK 2048
+dak_status dak_kv_fork(const dak_placement* KV, const dak_placement* src, const int* src_of, const int* seq_lens,
+                       const int* first, int* lens_out, const int* src_slot_pos, int* slot_pos, const float* src_acc,
+                       float* acc, void* stream);
 
 /* Release a placement (host and HBM parts). NULL is accepted. */
 dak_status dak_free(dak_placement* p);
@@ -523,6 +595,36 @@ dak_status dak_attn_prefix(const void* Q, const dak_placement* KV, const int* se
                            const int* prefix_lens, const int* prefix_of, int H_q, float scale, void* O, int o_fp32,
                            const float* acc_in, float* acc_out, void* workspace, size_t ws_bytes,
                            const dak_tuning* tuning, void* stream);
+
+/* Decode attention of several drafted tokens per request, a tree or a chain of them: token t of
+ * request b attends over the L_b = seq_lens[b] rows of the cache and over those drafted rows,
+ * L_b + s for s < n_new[b], that its mask names (dak_kv_append_rope or dak_kv_append_rope_axes
+ * wrote them from row L_b on),
+ *     o[b,t,h] = softmax over j of scale * q[b,t,h] . k[b,g,j], applied to v[b,g,j],
+ *     j < L_b, and j = L_b + s with bit s of mask[b][t] set.
+ * The cache is read once for all T tokens.
+ *   Q         : bf16 [B][T][H_q][D] (device), as dak_kv_append_rope leaves it. O: the same shape,
+ *               bf16 or (o_fp32) fp32; rows of tokens t >= n_new[b] are left as they were. Must not
+ *               overlap Q (DAK_ERR_INVALID).
+ *   seq_lens  : int32 [B] (device, required), clamped to [0, L]: rows before the drafted ones.
+ *   T         : 1..DAK_MAX_TREE drafted tokens a request (DAK_ERR_UNSUPPORTED above). n_new: int32
+ *               [B], clamped to [0, T], or NULL = T. Drafted rows that would lie at L or behind do not
+ *               exist, which is reported by dak_last_error (DAK_ERR_BOUNDS).
+ *   mask      : uint64 words (device, 8-byte aligned), ceil(T / 64) a token, bit s % 64 of word s / 64
+ *               for draft s; tokens side by side, requests mask_pitch words apart (0: one mask for
+ *               all). Usually a token's ancestors and itself, but any mask is taken. NULL: a chain,
+ *               token t sees the drafts 0..t.
+ *   workspace : dak_attn_tree_workspace_bytes(KV, T, H_q) bytes of device memory, 16-byte aligned,
+ *               contents on entry do not matter; calls that share one must not overlap.
+ *   tuning    : host_ctas, window and hbm_window; the others are not taken.
+ * A token that sees no row at all gives O = 0. What lies in rows that a token does not see, infinities
+ * and NaN too, does not reach its output; a score of NaN or +infinity gives NaN, as its softmax is.
+ * The probabilities enter P.V as two bf16 parts (three with o_fp32). The result does not depend on the
+ * offload ratio. Requires H_q / H_kv <= 16, as dak_attn. */
+size_t dak_attn_tree_workspace_bytes(const dak_placement* KV, int T, int H_q);
+dak_status dak_attn_tree(const void* Q, const dak_placement* KV, const int* seq_lens, int T, const uint64_t* mask,
+                         int64_t mask_pitch, const int* n_new, int H_q, float scale, void* O, int o_fp32,
+                         void* workspace, size_t ws_bytes, const dak_tuning* tuning, void* stream);
 
 /* The n_split dak_attn uses for a placement when tuning->n_split <= 0. */
 int dak_attn_default_split(const dak_placement* KV);
