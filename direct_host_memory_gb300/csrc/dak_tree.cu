@@ -1,8 +1,8 @@
 // Decode attention of a tree (or chain) of drafted tokens per request over a placed KV cache,
 // dak_attn_tree: o[b,t,h] = softmax(scale q[b,t,h] K^T) V over the rows before the drafts and those
-// drafts that the token's mask names. The tokens' query heads of one kv head are the rows of a tile
-// (row t * G + h), so that the cache, which dak_attn streams once per token, is streamed once
-// for all of them; 64 keys a step on the tcgen05 tensor cores, as in the prefix pass, whose
+// drafts that the token's mask names. The tokens' query heads of one kv head are the rows of a tile, as many whole tokens as fit in
+// each 128-row half of it, so that the cache, which dak_attn streams once per token, is streamed
+// once for all of them; 64 keys a step on the tcgen05 tensor cores, as in the prefix pass, whose
 // comment says how (dak_prefix.cu; what both use: dak_umma_attn.cuh).
 //
 // Work is cut on the device from the lengths, so that a captured call follows them: the chunks of
@@ -13,8 +13,9 @@
 // count alone, so that results do not depend on the tiers: the host's slabs are the line's beginning,
 // and where its ranges are more CTAs than may read the host at once, those take several each.
 //
-// A range goes through its tiles without the CTA's warps meeting: copies run ahead over the
-// tile's end, up to what the ring holds.
+// Nothing waits at a tile's end but for what it needs: copies run ahead, up to what the ring holds; the
+// next tile's Q is fetched when the last product that reads the old one is done, and its first scores are
+// computed while the results, straight from TMEM, are on their way out.
 #include <algorithm>
 #include <cmath>
 
@@ -22,9 +23,8 @@
 
 namespace dak {
 
-constexpr int kTreeSoftmax = 2 * 128;             // two streams, a thread a row
+constexpr int kTreeSoftmax = 2 * 2 * 128;         // two streams, two threads a row: of a step's keys and of O's columns a half each
 constexpr int kTreeThreads = kTreeSoftmax + 3 * 32;  // and copies, each stream's products
-constexpr int kTreeRows = 256;                    // of a tile
 // Cost of a chunk for a tile of one or two 128-row halves, and of a tile by itself (its rows' way in, the
 // first chunk's latency, the results' way out).
 constexpr unsigned kTreeTwoCost = 3, kTreeOneCost = 2, kTreeTileCost = 6;
@@ -35,10 +35,12 @@ constexpr int kTreeMergeRows = 8;                 // a warp each
 
 struct TreeMaps {
     CUtensorMap tier[2];  // host, HBM
+    CUtensorMap q;        // (64 elements, head, token, half of a row), 128-byte swizzle
 };
 
 struct TreeHead {  // of range r, the partials of the tile that begins in it and ends in a later one
-    int b, g, row0, pieces;  // pieces 0: there is no such tile
+    int b, g, tile, pieces;  // pieces 0: there is no such tile
+    int n, len, keys, unused;  // TreeRequest's
 };
 
 struct TreeParams {
@@ -55,31 +57,35 @@ struct TreeParams {
     const uint8_t* kv[2];  // host tier (device-visible), HBM tier
     long long head_bytes;
     int B, T, W, Hq, Hkv, G, L, h_s;  // W: mask words of a token
-    int inv_G;      // 2^16 / G rounded up: (r * inv_G) >> 16 is r / G for r < 4096
-    int part_rows;  // rows of a tile, at most
+    int host_requests;  // h_s / Hkv
+    int mpt;        // tokens of a 128-row half: 128 / G
+    int inv_G, inv_mpt;  // 2^16 / G and 2^16 / mpt rounded up: (r * inv) >> 16 is the quotient for any r here
+    int q_tokens;   // tokens that a copy of Q brings: min(mpt, T)
+    int part_rows;  // of a tile's partials: half * 128 + row in it, at most
+    int wide;       // O is 32-byte aligned
     int ranges, host_ctas, slab_chunks;
     int in_flight[2];  // copies of a CTA that have not landed, by tier
     float scale_log2;
     DevStatus* st;
 };
 
-enum : uint32_t { T_PROD_EMPTY = 0x71, T_PROD_FULL, T_MMA_FULL, T_MMA_P, T_MMA_PV, T_SM_S, T_SM_O, T_DRAIN };
+enum : uint32_t { T_PROD_EMPTY = 0x71, T_PROD_FULL, T_MMA_FULL, T_MMA_P, T_MMA_PV, T_SM_S, T_SM_O, T_Q_FREE, T_Q_FULL, T_DRAIN };
 
 // A request as the plan sees it.
 struct TreeRequest {
-    int len, keys, rows, chunks;  // cached rows; with the drafts; query rows a kv head; chunks of 64 keys
+    int len, n;                   // cached rows, drafted tokens
+    int keys, chunks;             // rows with the drafts, chunks of 64 keys
     int tiles, twos;              // tiles, those of two halves
     unsigned two, one, slab;      // cost of a tile of two halves, of one, of all tiles of a kv head
 };
 
-__device__ __forceinline__ TreeRequest tree_request(const TreeParams& p, int b) {
+__device__ __forceinline__ TreeRequest tree_request(const TreeParams& p, int len, int n) {
     TreeRequest q;
-    const int n = p.n_new ? min(max(p.n_new[b], 0), p.T) : p.T;
-    q.len = min(max(p.lens[b], 0), p.L);
+    q.len = len;
+    q.n = n;
     q.keys = min(q.len + n, p.L);
-    q.rows = n * p.G;
     q.chunks = (q.keys + 63) >> 6;
-    const int halves = (q.rows + 127) >> 7;
+    const int halves = ((n + p.mpt - 1) * p.inv_mpt) >> 16;
     q.twos = halves >> 1;
     q.tiles = (halves + 1) >> 1;
     q.two = kTreeTileCost + kTreeTwoCost * q.chunks;
@@ -87,30 +93,45 @@ __device__ __forceinline__ TreeRequest tree_request(const TreeParams& p, int b) 
     q.slab = q.twos * q.two + (halves & 1) * q.one;
     return q;
 }
+__device__ __forceinline__ TreeRequest tree_request(const TreeParams& p, int b) {
+    const int n = p.n_new ? p.n_new[b] : p.T;
+    return tree_request(p, min(max(p.lens[b], 0), p.L), min(max(n, 0), p.T));
+}
+
+// n / d for quotients below 2^21 (the float quotient is off by less than one, which the remainder puts
+// right): an integer division is dozens of instructions that run for the first time.
+__device__ __forceinline__ unsigned tree_quotient(unsigned n, unsigned d) {
+    const unsigned q = static_cast<unsigned>(static_cast<float>(n) * __fdividef(1.f, static_cast<float>(d)));
+    const int r = static_cast<int>(n - q * d);
+    return q + (r >= static_cast<int>(d)) - (r < 0);
+}
 
 struct TreePlan {
     unsigned len;                // of a range
     int ranges, host_ranges;     // host_ranges: those that touch the host's slabs
+    TreeRequest own;             // request `lane`, of which the lanes of a warp find theirs without loads
 };
 
-// By one warp.
+// By one warp, as are the functions of TreeWalk.
 __device__ __forceinline__ TreePlan tree_plan(const TreeParams& p) {
     constexpr unsigned all = 0xffffffffu;
-    const int lane = threadIdx.x & 31, bh = p.h_s / p.Hkv;
+    const int lane = threadIdx.x & 31, bh = p.host_requests;
+    TreePlan x;
+    x.own.slab = 0;
+    if (lane < p.B) x.own = tree_request(p, lane);
     unsigned total = 0, host = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
-        const unsigned slab = b < p.B ? tree_request(p, b).slab : 0u;
+        const unsigned slab = b0 == 0 ? x.own.slab : b < p.B ? tree_request(p, b).slab : 0u;
         total += slab * p.Hkv;
         if (b <= bh) host += slab * (b < bh ? p.Hkv : p.h_s - bh * p.Hkv);
     }
     total = __reduce_add_sync(all, total);
     host = __reduce_add_sync(all, host);
-    TreePlan x;
-    x.len = max((total + p.ranges - 1) / p.ranges, kTreeMinRange);
-    x.ranges = static_cast<int>((total + x.len - 1) / x.len);
-    x.host_ranges = static_cast<int>((host + x.len - 1) / x.len);
+    x.len = max(tree_quotient(total + p.ranges - 1, p.ranges), kTreeMinRange);
+    x.ranges = static_cast<int>(tree_quotient(total + x.len - 1, x.len));
+    x.host_ranges = static_cast<int>(tree_quotient(host + x.len - 1, x.len));
     return x;
 }
 
@@ -122,15 +143,17 @@ struct TreeWalk {
 
     __device__ __forceinline__ bool two() const { return tile < q.twos; }
     __device__ __forceinline__ unsigned end() const { return at + (two() ? q.two : q.one); }
-    // The tile at position x, which lies on the line; by one warp.
-    __device__ __forceinline__ void find(const TreeParams& p, unsigned x) {
+    // The tile at position x, which lies on the line.
+    __device__ __forceinline__ void find(const TreeParams& p, const TreePlan& plan, unsigned x) {
         constexpr unsigned all = 0xffffffffu;
         const int lane = threadIdx.x & 31;
         unsigned base = 0;
         b = 0;
 #pragma unroll 1
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const unsigned cost = b0 + lane < p.B ? tree_request(p, b0 + lane).slab * p.Hkv : 0u;
+            if (b0 > 0) q.slab = b0 + lane < p.B ? tree_request(p, b0 + lane).slab : 0u;
+            else q.slab = plan.own.slab;
+            const unsigned cost = q.slab * p.Hkv;
             unsigned incl = cost;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -146,21 +169,29 @@ struct TreeWalk {
             }
             base += __shfl_sync(all, incl, 31);
         }
-        q = tree_request(p, b);
-        g = static_cast<int>((x - base) / q.slab);
+        load(p, plan);
+        g = static_cast<int>(tree_quotient(x - base, q.slab));
         at = base + g * q.slab;
-        tile = min(static_cast<int>((x - at) / q.two), q.twos);
+        tile = min(static_cast<int>(tree_quotient(x - at, q.two)), q.twos);
         at += tile * q.two;
     }
+    __device__ __forceinline__ void load(const TreeParams& p, const TreePlan& plan) {
+        if (b < 32) {
+            const int n = __shfl_sync(0xffffffffu, plan.own.n, b);
+            q = tree_request(p, __shfl_sync(0xffffffffu, plan.own.len, b), n);
+        } else {
+            q = tree_request(p, b);
+        }
+    }
     // The next tile; past the line's end b is B.
-    __device__ __forceinline__ void next(const TreeParams& p) {
+    __device__ __forceinline__ void next(const TreeParams& p, const TreePlan& plan) {
         at = end();
         if (++tile < q.tiles) return;
         tile = 0;
         if (++g < p.Hkv) return;
         g = 0;
         while (++b < p.B) {
-            q = tree_request(p, b);
+            load(p, plan);
             if (q.tiles > 0) break;
         }
     }
@@ -205,15 +236,127 @@ __device__ __forceinline__ bool tree_sees(const TreeParams& p, const TreeRequest
 }
 
 struct KeysUnset {
-    uint32_t lo, hi;
-    __device__ __forceinline__ bool any() const { return (lo & hi) != 0xffffffffu; }
-    __device__ __forceinline__ bool operator()(int k) const { return !((k < 32 ? lo >> k : hi >> (k - 32)) & 1u); }
+    uint32_t bits;
+    __device__ __forceinline__ bool any() const { return bits != 0xffffffffu; }
+    __device__ __forceinline__ bool operator()(int k) const { return !(bits >> k & 1u); }
 };
+
+// OR of a predicate over the two warps that share rows (barrier `id`).
+__device__ __forceinline__ bool pair_any(int id, bool mine) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(r)
+                 : "r"(static_cast<uint32_t>(mine)), "r"(id)
+                 : "memory");
+    return r != 0;
+}
+
+// softmax_step (dak_umma_attn.cuh) for the 32 of a row's 64 scores that begin at column 32 * half of s_addr;
+// another warp has the others. (counts: the row is one; what else lies in a tile must not move references.)
+// Both go by one reference: where a row outgrows it in either, which
+// pair_any finds, they tell each other their maxima (`other`, from its maximum the partner's).
+template <int PARTS, class Hidden, class Other, class Grown>
+__device__ __forceinline__ void softmax_half(uint32_t s_addr, int half, int pair, const Hidden& hidden, float scale_log2,
+                                             float& m_ref, float& l, bool first, bool counts, const Other& other,
+                                             const Grown& grown) {
+    // with three parts O is in registers too, which leaves none for all scores: they are read twice
+    constexpr bool TWICE = PARTS == 3;
+    float v[TWICE ? 1 : 2][16];
+    const auto mask = [&](int q) {
+        if (hidden.any()) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                if (hidden(q * 16 + k)) v[TWICE ? 0 : q][k] = -INFINITY;
+            }
+        }
+    };
+    const auto read_again = [&](int q) {
+        tmem_ld16(s_addr + half * 32 + q * 16, v[0]);
+        tmem_wait(v[0]);
+        mask(q);
+    };
+    if (!TWICE) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) tmem_ld16(s_addr + half * 32 + q * 16, v[TWICE ? 0 : q]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) tmem_wait(v[TWICE ? 0 : q]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) mask(q);
+    }
+    float mx[2][2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        if (TWICE) read_again(q);
+        const float(&x)[16] = v[TWICE ? 0 : q];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            mx[q][e] = fmaxf(x[8 * e], x[8 * e + 1]);
+#pragma unroll
+            for (int k = 2; k < 8; k += 2) mx[q][e] = max3(mx[q][e], x[8 * e + k], x[8 * e + k + 1]);
+        }
+    }
+    float m_new = fmaxf(max3(mx[0][0], mx[0][1], mx[1][0]), mx[1][1]) * scale_log2;
+    // the reference only moves when a row's maximum outgrows it by 2^8: until then the sums just
+    // grow, which fp32 holds
+    if (first) {
+        m_ref = fmaxf(m_new, other(m_new));
+    } else if (pair_any(pair, counts && m_new > m_ref + 8.f)) {
+        const float m2 = fmaxf(m_ref, fmaxf(m_new, other(m_new)));
+        const float f = m2 == -INFINITY ? 1.f : exp2_ftz(m_ref - m2);
+        m_ref = m2;
+        l *= f;
+        grown(f);
+    }
+    const float base = m_ref == -INFINITY ? 0.f : m_ref;
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    const float2 scale2 = make_float2(scale_log2, scale_log2), base2 = make_float2(-base, -base);
+    const float2 minus = make_float2(-1.f, -1.f);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint32_t part[PARTS][8];
+        if (TWICE) read_again(q);
+        const float(&x)[16] = v[TWICE ? 0 : q];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float2 e = fma2(make_float2(x[2 * k], x[2 * k + 1]), scale2, base2);
+            float2 w = make_float2(exp2_ftz(e.x), exp2_ftz(e.y));
+            sum[k & 1] = add2(sum[k & 1], w);
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+                part[i][k] = pack_bf16(w.x, w.y);
+                if (i + 1 < PARTS) w = fma2(make_float2(bf_lo(part[i][k]), bf_hi(part[i][k])), minus, w);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) tmem_st8(s_addr + p_column(2 * half + q, i), part[i]);
+    }
+    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
 
 // Whether one of eight bf16 values is infinite or NaN.
 __device__ __forceinline__ bool not_finite(const uint4& v) {
     const auto bad = [](uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; };
     return bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
+}
+
+__device__ __forceinline__ void tma_load_q(void* dst, const CUtensorMap* map, int head, int token, int half, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(0), "r"(head), "r"(token), "r"(half), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// 32 bytes of a thread's own row: a whole sector, where the address allows it in one instruction.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&r)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                     "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(to)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        static_cast<uint4*>(to)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
 }
 
 __device__ __forceinline__ uint4 ld_shared_ordered(const void* p) {
@@ -225,22 +368,27 @@ __device__ __forceinline__ void clear_shared_ordered(void* p) {
     asm volatile("st.volatile.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(smem_u32(p)), "r"(0) : "memory");
 }
 
+template <int D>
+constexpr int kTreeSmem = 2 * ChunkCfg<D>::kTileBytes + ChunkCfg<D>::kStages * ChunkCfg<D>::kStage;
+
 template <int D, bool F32>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeMaps maps) {
     using C = ChunkCfg<D>;
     constexpr int NS = C::kStages;
     constexpr int SB = F32 ? 1 : 2;  // buffers of S
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    constexpr int kCopies = kTreeSoftmax / 32, kProducts = kCopies + 1;  // warps
+    extern __shared__ __align__(1024) uint8_t smem[];  // as the swizzle wants it; there is no room for a margin
     uint8_t* ring = smem + 2 * C::kTileBytes;
-    __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_ready[2][2], pv_done[2][2];
+    __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_ready[2][2], pv_done[2][2], q_full, q_ready, q_free;
     __shared__ uint32_t tmem_sh;
-    __shared__ int abort_flag, stop[2];
+    __shared__ int abort_flag, any_bad;
     __shared__ unsigned bad[DAK_MAX_TREE / 32];  // drafts with infinities or NaN in V, of the tile at work
+    __shared__ float maxima[2][2][128];          // by stream, half, row: what threads tell each other
     volatile int* abort = &abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 32) {
         abort_flag = 0;
+        any_bad = 0;
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 2);
@@ -248,39 +396,46 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         for (int s = 0; s < 2; ++s) {
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&s_full[s][b], 1);
-                mbar_init(&p_ready[s][b], 4);
+                mbar_init(&p_ready[s][b], 8);
                 mbar_init(&pv_done[s][b], 1);
             }
         }
+        mbar_init(&q_full, 1);
+        mbar_init(&q_ready, 1);
+        mbar_init(&q_free, 1);
         fence_mbar_init();
     }
-    if (warp == 9) {
+    if (threadIdx.x < DAK_MAX_TREE / 32) bad[threadIdx.x] = 0;
+    if (warp == kCopies && lane < 2) prefetch_tmap(&maps.tier[lane]);
+    if (warp == kProducts) {
         tmem_alloc(&tmem_sh, 512);
         tmem_relinquish();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_sh;
     grid_dep_wait();  // launched while the previous kernel ends
     grid_dep_launch();
     const TreePlan plan = tree_plan(p);
+    if (threadIdx.x == 0 && static_cast<int>(blockIdx.x) >= plan.ranges) p.heads[blockIdx.x].pieces = 0;
     // this CTA's ranges: the one of its number, unless more ranges touch the host than CTAs may
     const bool many = plan.host_ranges > p.host_ctas, takes_host = many && static_cast<int>(blockIdx.x) < p.host_ctas;
     const int r0 = !many || takes_host ? blockIdx.x : plan.host_ranges + blockIdx.x - p.host_ctas;
     const int r_end = takes_host ? plan.host_ranges : plan.ranges, r_step = takes_host ? p.host_ctas : p.ranges;
+    TreeWalk w;
+    if (r0 < r_end) w.find(p, plan, r0 * plan.len);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_sh;
     // TMEM columns: stream s has S at 128 s + 64 b (buffer b) with P over it, and O at 256 + D s
 
-    if (warp == 8) {
+    if (warp == kCopies) {
         // ---------------------------------------------------------------- copies
         RingPos<NS> pos(0), landed(0);
         int sent = 0, behind = 0;  // copies issued, and of these seen to have landed
         bool ok = true;
         for (int r = r0; r < r_end && ok; r += r_step) {
             const unsigned xs = r * plan.len, xe = xs + plan.len;
-            TreeWalk w;
-            w.find(p, xs);
-            for (; w.b < p.B && w.at < xe && ok; w.next(p)) {
+            if (r > r0) w.find(p, plan, xs);
+            for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
                 const int c0 = w.cut(xs, plan.len), c1 = w.cut(xe, plan.len);
                 if (lane == 0) {
                     const long long slab = static_cast<long long>(w.b) * p.Hkv + w.g;
@@ -312,37 +467,57 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             }
         }
         __syncwarp();
-    } else if (warp >= 9) {
+    } else if (warp >= kProducts) {
         // ---------------------------------------------------------------- products, a warp per stream
-        const int st = warp - 9;
+        // Stream 0's also brings Q for both, and hands it to stream 1's (q_ready), which says when its last
+        // product has read it (q_free): one after the other for every tile in which stream 1 has steps.
+        const int st = warp - kProducts;
         const bool leader = elect_one();
         const uint32_t ring_addr = smem_u32(ring);
         const uint32_t s_tmem = tmem + st * 128, o_tmem = tmem + 256 + st * D;
-        int n = 0;           // steps of this stream before this tile
-        int stage = 0, u = 0;  // stages used and tiles taken before it
-        bool ok = true;
+        int n = 0;      // steps of this stream before this tile
+        int stage = 0;  // stages used before it
+        int brought = 0, shared = 0;  // tiles whose Q was brought before it, those in which stream 1 had steps
+        bool ok = true, in_flight = false;
         for (int r = r0; r < r_end && ok; r += r_step) {
             const unsigned xs = r * plan.len, xe = xs + plan.len;
-            TreeWalk w;
-            w.find(p, xs);
-            for (; w.b < p.B && w.at < xe; w.next(p)) {
+            if (r > r0) w.find(p, plan, xs);
+            for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
                 const int steps = w.cut(xe, plan.len) - w.cut(xs, plan.len);
                 if (steps <= 0) continue;
-                const bool two = w.two();
-                named_bar<2, kTreeSoftmax + 64>();  // Q lies in shared memory
-                if (stop[u & 1]) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t q_addr = smem_u32(smem) + (two ? st * C::kTileBytes : 0);
+                const bool two = w.two(), with_1 = two || steps > 1;
                 const int stride = two ? 1 : 2, first = two ? 0 : st, mine = first < steps ? (steps - first + stride - 1) / stride : 0;
-                RingPos<NS> kpos(stage + first), vpos(stage + first);
                 // S buffer of this stream's step i of the tile, and the parity of its barriers' phase: a
                 // wait by parity is right only where the phase before is known to be over and the one after
                 // not to be, and steps i and i + SB of a buffer wait for each other.
                 const auto buf = [&](int i) { return (n + i) & (SB - 1); };
                 const auto par = [&](int i) { return static_cast<uint32_t>((n + i) / SB) & 1u; };
+                if (st == 0) {
+                    if (n > 0) ok = wait_phase(&s_full[0][buf(-1)], par(-1), abort, p.st, T_Q_FREE);
+                    if (ok && shared > 0) ok = wait_phase(&q_free, static_cast<uint32_t>(shared - 1) & 1u, abort, p.st, T_Q_FREE);
+                    if (!ok) break;
+                    if (leader) {
+                        const int halves = two ? 2 : 1, bytes = p.q_tokens * p.G * 128;
+                        mbar_arrive_expect_tx(&q_full, halves * (D / 64) * bytes);
+                        for (int h = 0; h < halves; ++h) {
+                            for (int k = 0; k < D / 64; ++k) {
+                                tma_load_q(smem + h * C::kTileBytes + k * 16384, &maps.q, w.g * p.G,
+                                           w.b * p.T + (2 * w.tile + h) * p.mpt, k, &q_full);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    in_flight = !wait_phase(&q_full, static_cast<uint32_t>(brought) & 1u, abort, p.st, T_Q_FULL);
+                    ok = !in_flight;
+                    if (ok && with_1 && leader) mbar_arrive(&q_ready);
+                    __syncwarp();
+                } else if (with_1) {
+                    ok = wait_phase(&q_ready, static_cast<uint32_t>(shared) & 1u, abort, p.st, T_Q_FULL);
+                }
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t q_addr = smem_u32(smem) + (two ? st * C::kTileBytes : 0);
+                RingPos<NS> kpos(stage + first), vpos(stage + first);
                 const auto qk = [&](int i) {
                     if (!wait_phase(&full[kpos.slot], kpos.phase, abort, p.st, T_MMA_FULL)) return false;
                     if (n + i >= SB && !wait_phase(&pv_done[st][buf(i)], par(i) ^ 1u, abort, p.st, T_MMA_PV)) return false;
@@ -350,15 +525,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     if (leader) {
                         issue_qk<D>(s_tmem + buf(i) * 64, q_addr, ring_addr + kpos.slot * C::kStage);
                         umma_commit(&s_full[st][buf(i)]);
+                        if (st == 1 && i + 1 == mine) umma_commit(&q_free);
                     }
                     __syncwarp();
                     kpos.advance(stride);
                     return true;
                 };
-                bool go = mine == 0 || qk(0);
-                for (int i = 0; i < mine && go; ++i) {
-                    if (!F32 && i + 1 < mine && !qk(i + 1)) break;
-                    if (!wait_phase(&p_ready[st][buf(i)], par(i), abort, p.st, T_MMA_P)) break;
+                ok = mine == 0 || qk(0);
+                for (int i = 0; i < mine && ok; ++i) {
+                    if (!F32 && i + 1 < mine) ok = qk(i + 1);
+                    ok = ok && wait_phase(&p_ready[st][buf(i)], par(i), abort, p.st, T_MMA_P);
+                    if (!ok) break;
                     tc_fence_after();
                     if (leader) {
                         const uint32_t p_tmem = s_tmem + buf(i) * 64, v = ring_addr + vpos.slot * C::kStage + C::kV;
@@ -371,77 +548,73 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     }
                     __syncwarp();
                     vpos.advance(stride);
-                    if (F32 && i + 1 < mine) go = qk(i + 1);
+                    if (F32 && i + 1 < mine) ok = qk(i + 1);
                 }
                 n += mine;
                 stage += steps;
-                ++u;
+                ++brought;
+                shared += with_1;
             }
         }
+        if (in_flight) {  // Q lands before the CTA may leave
+            volatile int dummy = 0;
+            wait_phase(&q_full, static_cast<uint32_t>(brought) & 1u, &dummy, p.st, T_DRAIN);
+        }
     } else {
-        // ---------------------------------------------------------------- softmax, a thread a row
-        const int st = warp >> 2, quad = warp & 3, r_in = quad * 32 + lane;
+        // ---------------------------------------------------------------- softmax, two threads a row
+        // A wait that ran out ends the waiting, not the loops: the warps go on meeting each other.
+        const int st = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, r_in = quad * 32 + lane, pair = 8 + st * 4 + quad;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t s_addr = tmem + lanes + st * 128, o_addr = tmem + lanes + 256 + st * D;
-        int n = 0, stage = 0, u = 0;
-        bool go = true;
-        for (int r = r0; r < r_end && go; r += r_step) {
+        const uint32_t s_addr = tmem + lanes + st * 128;
+        constexpr int HALF = D / 2, QUARTER = D / 4;  // columns of O
+        const uint32_t o_addr = tmem + lanes + 256 + st * D + half * HALF;  // this thread's
+        const auto other = [&](float m) {
+            maxima[st][half][r_in] = m;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+            return maxima[st][half ^ 1][r_in];
+        };
+        const int token_in = (r_in * p.inv_G) >> 16, head_in = r_in - token_in * p.G;  // of a half tile
+        int n = 0, stage = 0;
+        bool failed = false;
+        for (int r = r0; r < r_end; r += r_step) {
             const unsigned xs = r * plan.len, xe = xs + plan.len;
             if (threadIdx.x == 0) p.heads[r].pieces = 0;
-            TreeWalk w;
-            w.find(p, xs);
-            for (; w.b < p.B && w.at < xe; w.next(p)) {
+            if (r > r0) w.find(p, plan, xs);
+            for (; w.b < p.B && w.at < xe; w.next(p, plan)) {
                 const int c0 = w.cut(xs, plan.len), c1 = w.cut(xe, plan.len), steps = c1 - c0;
                 if (steps <= 0) continue;
                 const bool two = w.two();
-                const int row0 = w.tile * kTreeRows;
-                const auto source = [&](int row) {  // a query row of the request, in Q and O
-                    const int t = (row * p.inv_G) >> 16;
-                    return ((static_cast<long long>(w.b) * p.T + t) * p.Hq + w.g * p.G + row - t * p.G) * D;
-                };
-                {   // Q rows into the 128-byte swizzled K-major layout, rows that are none zero
-                    constexpr int PIECES = D / 8;  // 16-byte pieces of a row
-                    const int count = (two ? 256 : 128) * PIECES;
-#pragma unroll 4
-                    for (int e = threadIdx.x; e < count; e += kTreeSoftmax) {
-                        const int rr = e / PIECES, c = e % PIECES;
-                        const bool there = row0 + rr < w.q.rows;
-                        cp_async16(smem + (rr >> 7) * C::kTileBytes + (c >> 3) * 16384 + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4),
-                                   p.Q + (there ? source(row0 + rr) + c * 8 : 0), there ? 16 : 0);
+                if (threadIdx.x == 0) {
+                    if (c0 == 0 && c1 < w.q.chunks) {
+                        // ranges up to the one with the tile's last chunk
+                        int last = static_cast<int>(tree_quotient(w.end() - 1, plan.len));
+                        while (w.cut(last * plan.len, plan.len) == w.q.chunks) --last;
+                        p.heads[r] = TreeHead{w.b, w.g, w.tile, last - r + 1, w.q.n, w.q.len, w.q.keys, 0};
                     }
-                    if (threadIdx.x < DAK_MAX_TREE / 32) bad[threadIdx.x] = 0;
-                    if (threadIdx.x == 0) {
-                        stop[u & 1] = abort_flag;
-                        if (c0 == 0 && c1 < w.q.chunks) {
-                            // ranges up to the one with the tile's last chunk
-                            int last = static_cast<int>((w.end() - 1) / plan.len);
-                            while (w.cut(last * plan.len, plan.len) == w.q.chunks) --last;
-                            p.heads[r] = TreeHead{w.b, w.g, row0, last - r + 1};
-                        }
-                        if (w.g == 0 && w.tile == 0 && c0 == 0 && w.q.keys - w.q.len < (p.n_new ? min(max(p.n_new[w.b], 0), p.T) : p.T)) {
-                            report(p.st, DAK_ERR_BOUNDS, (0x7EEEull << 32) | static_cast<unsigned>(w.b));
-                        }
-                    }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    fence_proxy_async_smem();
-                    named_bar<2, kTreeSoftmax + 64>();
-                    if (stop[u & 1]) {
-                        go = false;
-                        break;
+                    if (w.g == 0 && w.tile == 0 && c0 == 0 && w.q.keys - w.q.len < w.q.n) {
+                        report(p.st, DAK_ERR_BOUNDS, (0x7EEEull << 32) | static_cast<unsigned>(w.b));
                     }
                 }
-                const int row = row0 + (two ? st * 128 : 0) + r_in, t = (row * p.inv_G) >> 16;
-                const bool valid_row = row < w.q.rows, warp_has_rows = row - lane < w.q.rows;
+                const int token0 = (2 * w.tile + (two ? st : 0)) * p.mpt, t = token0 + token_in;
+                const bool valid_row = token_in < p.mpt && t < w.q.n;
+                const bool warp_has_rows = quad * 32 < min(w.q.n - token0, p.mpt) * p.G;
+                // this row in Q and O
+                const long long at = ((static_cast<long long>(w.b) * p.T + t) * p.Hq + w.g * p.G + head_in) * D;
                 const int stride = two ? 1 : 2;
                 const auto buf = [&](int i) { return (n + i) & (SB - 1); };
                 const auto par = [&](int i) { return static_cast<uint32_t>((n + i) / SB) & 1u; };
+                const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t where) {
+                    if (!failed) failed = !mbar_wait(bar, parity, abort, p.st, DAK_ERR_TIMEOUT, where);
+                    __syncwarp();
+                    tc_fence_after();
+                };
                 float m_ref = -INFINITY, l = 0.f;
                 // An fp32 output's O is summed here, a step's product at a time: the tensor cores cut off what
                 // they add to a sum.
-                float sum[F32 ? D / 16 : 1][16] = {};
+                float sum[F32 ? HALF / 16 : 1][16] = {};
                 const auto add_product = [&] {
 #pragma unroll
-                    for (int q = 0; q < (F32 ? D / 16 : 0); ++q) {
+                    for (int q = 0; q < (F32 ? HALF / 16 : 0); ++q) {
                         float o[16];
                         tmem_ld16(o_addr + q * 16, o);
                         tmem_wait(o);
@@ -449,19 +622,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         for (int k = 0; k < 16; ++k) sum[q][k] += o[k];
                     }
                 };
-                bool ok = true;
                 int i = 0;
                 for (int j = two ? 0 : st; j < steps; j += stride, ++i) {
                     const int key0 = (c0 + j) * 64;
-                    unsigned long long bits = ~0ull;
+                    uint32_t bits = 0xffffffffu;  // of this thread's keys
                     const bool drafts = key0 + 64 > w.q.len;
-                    if (drafts && valid_row) bits = tree_bits(p, w.q, w.b, t, key0);
-                    ok = mbar_wait(&s_full[st][buf(i)], par(i), abort, p.st, DAK_ERR_TIMEOUT, T_SM_S);
-                    if (!__all_sync(0xffffffffu, ok)) {  // a wait ran out: the whole warp stops
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                    if (drafts && valid_row) bits = static_cast<uint32_t>(tree_bits(p, w.q, w.b, t, key0) >> (32 * half));
+                    wait(&s_full[st][buf(i)], par(i), T_SM_S);
                     if (drafts) {
                         // Drafted rows' V may hold infinities and NaN, which the probability of zero of a token
                         // that does not see the row would not cancel, and rows behind the drafts anything at all.
@@ -471,13 +638,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         // (The scores say that the chunk is there.)
                         uint8_t* rows = ring + RingPos<NS>(stage + j).slot * C::kStage + C::kV;
                         const int begin = max(0, w.q.len - key0), end = w.q.keys - key0;
-                        for (int e = begin * (D / 8) + r_in; e < 64 * (D / 8); e += 128) {
+                        for (int e = begin * (D / 8) + half * 128 + r_in; e < 64 * (D / 8); e += 256) {
                             const int kr = e / (D / 8), c = e % (D / 8);
                             uint8_t* piece = rows + (c >> 3) * 16384 + kr * 128 + ((c & 7) << 4);
                             if (kr < end) {
                                 if (!not_finite(ld_shared_ordered(piece))) continue;
                                 const int s = key0 + kr - w.q.len;
                                 atomicOr(&bad[s >> 5], 1u << (s & 31));
+                                any_bad = 1;
                                 __threadfence_block();
                             }
                             clear_shared_ordered(piece);
@@ -485,21 +653,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
-                    // O so far, its last product done, to the new reference
+                    // O so far, its last product done, to the new reference: this thread's columns
                     const auto grown = [&](float f) {
                         if (F32) {
 #pragma unroll
-                            for (int q = 0; q < (F32 ? D / 16 : 0); ++q) {
+                            for (int q = 0; q < (F32 ? HALF / 16 : 0); ++q) {
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) sum[q][k] *= f;
                             }
                             return;
                         }
-                        mbar_wait(&pv_done[st][buf(i - 1)], par(i - 1), abort, p.st, DAK_ERR_TIMEOUT, T_SM_O);
-                        __syncwarp();
-                        tc_fence_after();
+                        wait(&pv_done[st][buf(i - 1)], par(i - 1), T_SM_O);
 #pragma unroll 1
-                        for (int q = 0; q < D / 16; ++q) {
+                        for (int q = 0; q < HALF / 16; ++q) {
                             float o[16];
                             tmem_ld16(o_addr + q * 16, o);
                             tmem_wait(o);
@@ -508,32 +674,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                             tmem_st16(o_addr + q * 16, o);
                         }
                     };
-                    const uint32_t at_s = s_addr + buf(i) * 64;
                     if (warp_has_rows) {  // lanes without rows share a warp's work, warps without any do none
-                        const KeysUnset hidden{static_cast<uint32_t>(bits), static_cast<uint32_t>(bits >> 32)};
                         if (F32 && i > 0) add_product();  // the last step's: its scores' columns are these
-                        if (F32) softmax_step<3>(at_s, hidden, p.scale_log2, m_ref, l, i == 0, grown);
-                        else softmax_step<2>(at_s, hidden, p.scale_log2, m_ref, l, i == 0, grown);
+                        softmax_half<F32 ? 3 : 2>(s_addr + buf(i) * 64, half, pair, KeysUnset{bits}, p.scale_log2, m_ref, l, i == 0,
+                                                  valid_row, other, grown);
                         tmem_wait_st();
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_ready[st][buf(i)]);
                 }
-                for (int k = max(0, i - SB); ok && k < i; ++k) {  // one phase of each buffer's
-                    ok = mbar_wait(&pv_done[st][buf(k)], par(k), abort, p.st, DAK_ERR_TIMEOUT, T_SM_O);
-                }
-                __syncwarp();
+                for (int k = max(0, i - SB); k < i; ++k) wait(&pv_done[st][buf(k)], par(k), T_SM_O);  // one phase of each buffer's
                 if (F32) {  // back to where the results are read from
-                    tc_fence_after();
                     if (i > 0) add_product();
 #pragma unroll
-                    for (int q = 0; q < (F32 ? D / 16 : 0); ++q) tmem_st16(o_addr + q * 16, sum[q]);
+                    for (int q = 0; q < (F32 ? HALF / 16 : 0); ++q) tmem_st16(o_addr + q * 16, sum[q]);
                     tmem_wait_st();
                 }
                 // what tokens see of cleared pieces
+                const bool repair = __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&any_bad) != 0);
 #pragma unroll 1
-                for (int word = 0; word < DAK_MAX_TREE / 32; ++word) {
+                for (int word = 0; repair && word < DAK_MAX_TREE / 32; ++word) {
                     unsigned set = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile unsigned*>(&bad[word]), 0);
 #pragma unroll 1
                     for (; set; set &= set - 1) {
@@ -551,7 +712,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         };
                         float x = 0.f;
                         if (sees) {
-                            const uint4* q_row = reinterpret_cast<const uint4*>(p.Q + source(row));
+                            const uint4* q_row = reinterpret_cast<const uint4*>(p.Q + at);
 #pragma unroll 1
                             for (int c = 0; c < D / 8; ++c) x += products(q_row[c], k_row[c ^ (key & 7)]);
                         }
@@ -559,19 +720,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         const float weight = fmaxf(exp2f(x * p.scale_log2 - (m_ref == -INFINITY ? 0.f : m_ref)), 1e-37f);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int q = 0; q < D / 16; ++q) {
+                        for (int q = 0; q < HALF / 16; ++q) {
                             float o[16];
                             tmem_ld16(o_addr + q * 16, o);
                             tmem_wait(o);
 #pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const uint4 v = v_row[(2 * q + half) ^ (key & 7)];
+                            for (int e = 0; e < 2; ++e) {
+                                const uint4 v = v_row[(half * (HALF / 8) + 2 * q + e) ^ (key & 7)];
                                 if (!sees || !not_finite(v)) continue;
-                                const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+                                const uint32_t pairs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
-                                    o[half * 8 + 2 * k] += weight * bf_lo(e[k]);
-                                    o[half * 8 + 2 * k + 1] += weight * bf_hi(e[k]);
+                                    o[e * 8 + 2 * k] += weight * bf_lo(pairs[k]);
+                                    o[e * 8 + 2 * k + 1] += weight * bf_hi(pairs[k]);
                                 }
                             }
                             tmem_st16(o_addr + q * 16, o);
@@ -579,83 +740,74 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         tmem_wait_st();
                     }
                 }
-                // ---- results
-                // Q's memory, no longer read, takes the streams' (m, l) where they share a tile, and then, half
-                // a row's columns at a time, the results on their way out.
-                constexpr int COLS = D / 2;
-                float M = m_ref, total = l, w0 = 1.f, w1 = 0.f;
+                // ---- results: the halves' sums, and where the streams share a tile what the other one has
                 const bool both = !two && steps > 1;  // the streams' rows are the same and both had a step
+                l += other(l);
                 tc_fence_before();
+                named_bar<3, kTreeSoftmax>();
+                if (threadIdx.x < DAK_MAX_TREE / 32) bad[threadIdx.x] = 0;
+                if (threadIdx.x == 32) any_bad = 0;
+                float m_other = -INFINITY, l_other = 0.f;
                 if (!two) {
-                    float2(*ex)[128] = reinterpret_cast<float2(*)[128]>(smem + C::kTileBytes);
-                    ex[st][r_in] = make_float2(m_ref, l);
+                    maxima[st][half][r_in] = half ? l : m_ref;
                     named_bar<3, kTreeSoftmax>();
-                    const float2 e0 = ex[0][r_in], e1 = ex[1][r_in];
-                    named_bar<3, kTreeSoftmax>();  // ex lies in what is written next
-                    M = fmaxf(e0.x, e1.x);
-                    const float base = M == -INFINITY ? 0.f : M;
-                    w0 = exp2_ftz(e0.x - base);
-                    w1 = both ? exp2_ftz(e1.x - base) : 0.f;
-                    total = w0 * e0.y + (both ? w1 * e1.y : 0.f);
+                    if (both || st == 1) m_other = maxima[st ^ 1][0][r_in], l_other = maxima[st ^ 1][1][r_in];
                 }
                 tc_fence_after();
+                const float M = fmaxf(m_ref, m_other), base = M == -INFINITY ? 0.f : M;
+                const float w_own = both || two || st == 0 ? exp2_ftz(m_ref - base) : 0.f, w_other = exp2_ftz(m_other - base);
+                const float total = w_own * l + w_other * l_other;
                 const bool whole = c0 == 0 && c1 == w.q.chunks;
-                if (whole && valid_row && !tree_sees(p, w.q, w.b, t)) total = INFINITY;  // O is zero: it becomes zeros
-                const float inv = whole ? 1.f / total : 1.f;
-                const long long slot = 2ll * r + (c0 == 0);
-                if (!whole && valid_row && (two || st == 0)) p.ml_part[slot * p.part_rows + row - row0] = make_float2(M, total);
-                float4* staged = reinterpret_cast<float4*>(smem + st * C::kTileBytes + quad * 32 * COLS * 4);
-                const int first = row - lane;  // the warp's rows
+                // a token that sees nothing has zeros in O, which stay
+                const float inv = !whole || (valid_row && !tree_sees(p, w.q, w.b, t)) ? 1.f : 1.f / total;
+                const long long local = (2ll * r + (c0 == 0)) * p.part_rows + (two ? st * 128 : 0) + r_in;  // among the partials
+                if (!whole && valid_row && half == 0 && (two || st == 0)) p.ml_part[local] = make_float2(M, total);
+                // stream 0's O, or the only one; the other's where both have one
+                const uint32_t o0 = tmem + lanes + 256 + (two ? st * D : 0), o1 = tmem + lanes + 256 + D;
+                const float w0 = (st == 0 || two ? w_own : w_other) * inv, w1 = (st == 0 ? w_other : w_own) * inv;
+                const int col0 = two ? half * HALF : (2 * st + half) * QUARTER, cols = two ? HALF : QUARTER;
 #pragma unroll 1
-                for (int col = two ? 0 : st * COLS; warp_has_rows && col < (two ? D : (st + 1) * COLS); col += COLS) {
-#pragma unroll 1
-                    for (int q = 0; q < COLS / 16; ++q) {
-                        float o[16];
-                        tmem_ld16(tmem + lanes + 256 + (two ? st * D : 0) + col + q * 16, o);
-                        tmem_wait(o);
-                        if (!two) {
-                            float b[16];
-                            tmem_ld16(tmem + lanes + 256 + D + col + q * 16, b);
-                            tmem_wait(b);
+                for (int col = col0; warp_has_rows && col < col0 + cols; col += 16) {
+                    float o[16];
+                    tmem_ld16(o0 + col, o);
+                    tmem_wait(o);
+                    if (both) {
+                        float b[16];
+                        tmem_ld16(o1 + col, b);
+                        tmem_wait(b);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = both ? o[k] * w0 + b[k] * w1 : o[k] * w0;
-                        }
+                        for (int k = 0; k < 16; ++k) o[k] = o[k] * w0 + b[k] * w1;
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            staged[stage_piece<COLS>(lane, q * 4 + k)] =
-                                make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
-                        }
+                        for (int k = 0; k < 16; ++k) o[k] *= w0;
                     }
-                    __syncwarp();
-                    constexpr int PIECES = COLS / 4;
-#pragma unroll 4
-                    for (int e = lane; e < 32 * PIECES; e += 32) {
-                        const int rr = e / PIECES, c = e % PIECES;
-                        if (first + rr >= w.q.rows) break;
-                        const float4 v = staged[stage_piece<COLS>(rr, c)];
-                        if (!whole) {
-                            *reinterpret_cast<float4*>(p.o_part + (slot * p.part_rows + first + rr - row0) * D + col + c * 4) = v;
-                        } else if (p.o_fp32) {
-                            *reinterpret_cast<float4*>(static_cast<float*>(p.O) + source(first + rr) + col + c * 4) = v;
-                        } else {
-                            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + source(first + rr) + col + c * 4) =
-                                make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+                    uint32_t out[8];
+                    if (valid_row && whole && !F32) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) out[k] = pack_bf16(o[2 * k], o[2 * k + 1]);
+                        store32(static_cast<__nv_bfloat16*>(p.O) + at + col, out, p.wide);
+                    } else if (valid_row) {
+                        float* to = whole ? static_cast<float*>(p.O) + at + col : p.o_part + local * D + col;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) out[k] = __float_as_uint(o[8 * e + k]);
+                            store32(to + 8 * e, out, whole ? p.wide : true);
                         }
                     }
                     __syncwarp();
                 }
                 n += two ? steps : (steps + 1 - st) / 2;
                 stage += steps;
-                ++u;
                 tc_fence_before();
-                named_bar<3, kTreeSoftmax>();  // Q's memory and O are free
+                named_bar<3, kTreeSoftmax>();  // O is free, and what the threads told each other
                 tc_fence_after();
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kProducts) {
         tc_fence_after();
         tmem_dealloc(tmem_sh, 512);
     }
@@ -671,46 +823,55 @@ __global__ void __launch_bounds__(32 * kTreeMergeRows) tree_merge_kernel(const _
     constexpr int LANES = D / 4, AT_ONCE = 32 / LANES;  // pieces that a warp reads at once
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.x;
     grid_dep_wait();
-    const TreePlan plan = tree_plan(p);
-    if (r >= plan.ranges) return;
     const TreeHead head = p.heads[r];
-    const int local = blockIdx.y * kTreeMergeRows + warp;
     // the limits: where a wait ran out, a range's entry may never have been written
-    if (head.pieces <= 0 || head.b < 0 || head.b >= p.B || head.g < 0 || head.g >= p.Hkv || head.row0 < 0) return;
-    const int n = min(head.pieces, plan.ranges - r);
-    const TreeRequest q = tree_request(p, head.b);
-    const int row = head.row0 + local;
-    if (row >= q.rows || local >= p.part_rows) return;
+    if (head.pieces <= 0 || head.b < 0 || head.b >= p.B || head.g < 0 || head.g >= p.Hkv || head.tile < 0) return;
+    const int local = blockIdx.y * kTreeMergeRows + warp, r_in = local & 127, n = min(head.pieces, p.ranges - r);
+    const int token_in = (r_in * p.inv_G) >> 16, t = (2 * head.tile + (local >> 7)) * p.mpt + token_in;
+    if (token_in >= p.mpt || t >= min(head.n, p.T) || local >= p.part_rows) return;
     const auto slot = [&](int s) { return (2ll * (r + s) + (s == 0)) * p.part_rows + local; };
     const int c = lane % LANES, grp = lane / LANES;
     const auto part = [&](int s) { return *reinterpret_cast<const float4*>(p.o_part + slot(s) * D + c * 4); };
-    float4 early[4];
+    constexpr int EARLY = 4;  // of a lane's pieces asked for before the maxima are known
+    float4 early[EARLY];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < EARLY; ++k) {
         if (grp + k * AT_ONCE < n) early[k] = part(grp + k * AT_ONCE);
     }
-    float M = -INFINITY;
-    for (int s = lane; s < n; s += 32) M = fmaxf(M, p.ml_part[slot(s)].x);
+    const float2 first = lane < n ? p.ml_part[slot(lane)] : make_float2(-INFINITY, 0.f);
+    float M = first.x;
+    for (int s = lane + 32; s < n; s += 32) M = fmaxf(M, p.ml_part[slot(s)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float base = M == -INFINITY ? 0.f : M;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    for (int s0 = 0; s0 < n; s0 += 32) {
-        const float2 v = s0 + lane < n ? p.ml_part[slot(s0 + lane)] : make_float2(-INFINITY, 0.f);
-        const float f = exp2f(v.x - base);
-        l += f * v.y;
-#pragma unroll 4
-        for (int k = 0; k < 32; k += AT_ONCE) {
-            if (s0 + k >= n) break;
-            const float w = __shfl_sync(0xffffffffu, f, k + grp);
-            const int s = s0 + k + grp;
-            if (s >= n) continue;
-            const float4 x = s0 == 0 && k / AT_ONCE < 4 ? early[k / AT_ONCE] : part(s);
-            acc.x += w * x.x;
-            acc.y += w * x.y;
-            acc.z += w * x.z;
-            acc.w += w * x.w;
+    const auto add = [&](float w, const float4& x) {
+        acc.x += w * x.x;
+        acc.y += w * x.y;
+        acc.z += w * x.z;
+        acc.w += w * x.w;
+    };
+    float f = exp2f(first.x - base), l = f * first.y;
+#pragma unroll
+    for (int k = 0; k < EARLY; ++k) {
+        const float w = __shfl_sync(0xffffffffu, f, k * AT_ONCE + grp);
+        if (grp + k * AT_ONCE < n) add(w, early[k]);
+    }
+    for (int s0 = EARLY * AT_ONCE; s0 < n; s0 += 4 * AT_ONCE) {
+        if ((s0 & 31) == 0) {
+            const float2 v = s0 + lane < n ? p.ml_part[slot(s0 + lane)] : make_float2(-INFINITY, 0.f);
+            f = exp2f(v.x - base);
+            l += f * v.y;
+        }
+        float4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (s0 + k * AT_ONCE + grp < n) x[k] = part(s0 + k * AT_ONCE + grp);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float w = __shfl_sync(0xffffffffu, f, (s0 + k * AT_ONCE + grp) & 31);
+            if (s0 + k * AT_ONCE + grp < n) add(w, x[k]);
         }
     }
 #pragma unroll
@@ -723,9 +884,11 @@ __global__ void __launch_bounds__(32 * kTreeMergeRows) tree_merge_kernel(const _
         acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
     }
     if (grp != 0) return;
-    const int t = row / p.G;
+    TreeRequest q;
+    q.len = head.len;
+    q.keys = head.keys;
     if (tree_sees(p, q, head.b, t)) acc.x /= l, acc.y /= l, acc.z /= l, acc.w /= l;
-    const long long at = ((static_cast<long long>(head.b) * p.T + t) * p.Hq + head.g * p.G + row - t * p.G) * D + c * 4;
+    const long long at = ((static_cast<long long>(head.b) * p.T + t) * p.Hq + head.g * p.G + r_in - token_in * p.G) * D + c * 4;
     if (p.o_fp32) {
         *reinterpret_cast<float4*>(static_cast<float*>(p.O) + at) = acc;
     } else {
@@ -739,20 +902,20 @@ __global__ void __launch_bounds__(32 * kTreeMergeRows) tree_merge_kernel(const _
 struct TreeLayout {
     int ranges, part_rows;
     size_t o_part, ml_part, heads;
-    size_t total() const { return o_part + ml_part + heads; }
+    size_t total() const { return 16 + o_part + ml_part + heads; }  // the partials begin on 32 bytes
 };
 
 static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // As many ranges as SMs; fewer where the cache, full, would not give each the least there may be.
 static TreeLayout tree_layout(const dak_placement* KV, int T, int H_q) {
-    const int G = H_q / KV->H_kv, rows = T * G;
-    const int64_t chunks = (KV->L + 63) / 64, halves = (rows + 127) / 128;
+    const int G = H_q / KV->H_kv, mpt = 128 / G;
+    const int64_t chunks = (KV->L + 63) / 64, halves = (T + mpt - 1) / mpt;
     const int64_t slab = (halves / 2) * (kTreeTileCost + kTreeTwoCost * chunks) + halves % 2 * (kTreeTileCost + kTreeOneCost * chunks);
     const int64_t least = (slab * KV->B * KV->H_kv + kTreeMinRange - 1) / kTreeMinRange;
     TreeLayout x{};
     x.ranges = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(device_sm_count(), least)));
-    x.part_rows = std::min(rows, kTreeRows);
+    x.part_rows = T <= mpt ? T * G : std::min(256, 128 + (T - mpt) * G);
     x.o_part = round256(sizeof(float) * 2 * x.ranges * x.part_rows * KV->D);
     x.ml_part = round256(sizeof(float2) * 2 * x.ranges * x.part_rows);
     x.heads = round256(sizeof(TreeHead) * x.ranges);
@@ -761,16 +924,30 @@ static TreeLayout tree_layout(const dak_placement* KV, int T, int H_q) {
 
 // The whole line's cost, with every cache full, fits an int.
 static bool line_fits(const dak_placement* KV, int T, int H_q) {
-    const int64_t chunks = (KV->L + 63) / 64, halves = (T * (H_q / KV->H_kv) + 127) / 128;
+    const int mpt = 128 / (H_q / KV->H_kv);
+    const int64_t chunks = (KV->L + 63) / 64, halves = (T + mpt - 1) / mpt;
     return (kTreeTileCost + kTreeOneCost * chunks) * halves * KV->B * KV->H_kv < 0x7FFFFFFF - (1 << 24) &&
-           static_cast<int64_t>(KV->B) * KV->H_kv * chunks <= 0x7FFFFFFF;
+           static_cast<int64_t>(KV->B) * KV->H_kv * chunks <= 0x7FFFFFFF && static_cast<int64_t>(KV->B) * T <= 0x7FFFFFFF;
+}
+
+// Q's rows as a copy brings them: whole tokens of a kv head's query heads, half a row (64 elements) at a time.
+static bool make_query_map(CUtensorMap* map, const void* Q, int64_t tokens, int H_q, int D, int G, int q_tokens) {
+    const auto enc = encode_fn();
+    if (!enc || fault_due(DAK_FAULT_TENSOR_MAP)) return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(H_q), static_cast<cuuint64_t>(tokens), static_cast<cuuint64_t>(D / 64)};
+    const cuuint64_t strides[3] = {row, row * H_q, 128};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(q_tokens), 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(Q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, bool F32>
 static cudaError_t launch_tree(const TreeParams& p, const TreeMaps& maps, cudaStream_t s) {
     auto k = tree_kernel<D, F32>;
     static SmemLimit limit;
-    cudaError_t e = limit.raise(reinterpret_cast<const void*>(k), ChunkCfg<D>::kSmem);
+    cudaError_t e = limit.raise(reinterpret_cast<const void*>(k), kTreeSmem<D>);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -778,7 +955,7 @@ static cudaError_t launch_tree(const TreeParams& p, const TreeMaps& maps, cudaSt
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(p.ranges));
     cfg.blockDim = dim3(kTreeThreads);
-    cfg.dynamicSmemBytes = ChunkCfg<D>::kSmem;
+    cfg.dynamicSmemBytes = kTreeSmem<D>;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -829,7 +1006,7 @@ extern "C" dak_status dak_attn_tree(const void* Q, const dak_placement* KV, cons
     p.mask_pitch = mask_pitch;
     p.O = O;
     p.o_fp32 = o_fp32 ? 1 : 0;
-    uint8_t* w = static_cast<uint8_t*>(workspace);
+    uint8_t* w = static_cast<uint8_t*>(workspace) + (off(workspace, 32) ? 16 : 0);
     p.o_part = reinterpret_cast<float*>(w);
     p.ml_part = reinterpret_cast<float2*>(w + x.o_part);
     p.heads = reinterpret_cast<TreeHead*>(w + x.o_part + x.ml_part);
@@ -842,9 +1019,14 @@ extern "C" dak_status dak_attn_tree(const void* Q, const dak_placement* KV, cons
     p.Hq = H_q;
     p.Hkv = KV->H_kv;
     p.G = G;
+    p.mpt = 128 / G;
     p.inv_G = (65536 + G - 1) / G;
+    p.inv_mpt = (65536 + p.mpt - 1) / p.mpt;
+    p.q_tokens = std::min(p.mpt, T);
+    p.wide = !off(O, 32);
     p.L = KV->L;
     p.h_s = KV->h_s;
+    p.host_requests = KV->h_s / KV->H_kv;
     p.part_rows = x.part_rows;
     p.ranges = x.ranges;
     p.slab_chunks = (KV->L + 63) / 64;
@@ -862,6 +1044,7 @@ extern "C" dak_status dak_attn_tree(const void* Q, const dak_placement* KV, cons
         const int64_t n = tier ? slabs - KV->h_s : KV->h_s;
         if (n > 0 && !make_chunk_map(&maps.tier[tier], p.kv[tier], n * p.slab_chunks, D)) return DAK_ERR_CUDA;
     }
+    if (!make_query_map(&maps.q, Q, static_cast<int64_t>(KV->B) * T, H_q, D, G, p.q_tokens)) return DAK_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(D == 128 ? (o_fp32 ? launch_tree<128, true>(p, maps, s) : launch_tree<128, false>(p, maps, s))
                                 : (o_fp32 ? launch_tree<64, true>(p, maps, s) : launch_tree<64, false>(p, maps, s)));
