@@ -4,14 +4,7 @@
 // each 128-row half of it, so that the cache, which dak_attn streams once per token, is streamed
 // once for all of them; 64 keys a step on the tcgen05 tensor cores, as in the prefix pass, whose
 // comment says how (dak_prefix.cu; what both use: dak_umma_attn.cuh).
-//
-// Work is cut on the device from the lengths, so that a captured call follows them: the chunks of
-// all (request, kv head, 256-row tile) lie on one line, request-major, each with its cost, and
-// the line is cut into as many equal ranges as there are SMs, a CTA each. A tile cut by no range's
-// end is finished where it is; the others leave partial results (at most two a range, whatever the
-// batch) to a second kernel, which merges those of a tile in order. The cuts go by lengths and SM
-// count alone, so that results do not depend on the tiers: the host's slabs are the line's beginning,
-// and where its ranges are more CTAs than may read the host at once, those take several each.
+// How work is cut: dak_tree.cuh.
 //
 // Nothing waits at a tile's end but for what it needs: copies run ahead, up to what the ring holds; the
 // next tile's Q is fetched when the last product that reads the old one is done, and its first scores are
@@ -19,17 +12,13 @@
 #include <algorithm>
 #include <cmath>
 
+#include "dak_tree.cuh"
 #include "dak_umma_attn.cuh"
 
 namespace dak {
 
 constexpr int kTreeSoftmax = 2 * 2 * 128;         // two streams, two threads a row: of a step's keys and of O's columns a half each
 constexpr int kTreeThreads = kTreeSoftmax + 3 * 32;  // and copies, each stream's products
-// Cost of a chunk for a tile of one or two 128-row halves, and of a tile by itself (its rows' way in, the
-// first chunk's latency, the results' way out).
-constexpr unsigned kTreeTwoCost = 3, kTreeOneCost = 2, kTreeTileCost = 6;
-constexpr unsigned kTreeMinRange = 6;             // cost of a range, at least
-constexpr unsigned kTreeSnapRange = 24;           // from here on no tile's first or last chunk is cut off alone
 constexpr int kTreeHostCtas = 32;
 constexpr int kTreeMergeRows = 8;                 // a warp each
 
@@ -38,202 +27,7 @@ struct TreeMaps {
     CUtensorMap q;        // (64 elements, head, token, half of a row), 128-byte swizzle
 };
 
-struct TreeHead {  // of range r, the partials of the tile that begins in it and ends in a later one
-    int b, g, tile, pieces;  // pieces 0: there is no such tile
-    int n, len, keys, unused;  // TreeRequest's
-};
-
-struct TreeParams {
-    const __nv_bfloat16* Q;  // [B][T][Hq][D]
-    const int* lens;
-    const int* n_new;                // or null
-    const unsigned long long* mask;  // or null: a chain
-    long long mask_pitch;
-    void* O;
-    int o_fp32;
-    float* o_part;    // [2 * ranges][part_rows][D]: range r's piece of a tile that began before it, then of one that ends after it
-    float2* ml_part;  // [2 * ranges][part_rows]: reference (log2 domain), sum
-    TreeHead* heads;  // [ranges]
-    const uint8_t* kv[2];  // host tier (device-visible), HBM tier
-    long long head_bytes;
-    int B, T, W, Hq, Hkv, G, L, h_s;  // W: mask words of a token
-    int host_requests;  // h_s / Hkv
-    int mpt;        // tokens of a 128-row half: 128 / G
-    int inv_G, inv_mpt;  // 2^16 / G and 2^16 / mpt rounded up: (r * inv) >> 16 is the quotient for any r here
-    int q_tokens;   // tokens that a copy of Q brings: min(mpt, T)
-    int part_rows;  // of a tile's partials: half * 128 + row in it, at most
-    int wide;       // O is 32-byte aligned
-    int ranges, host_ctas, slab_chunks;
-    int in_flight[2];  // copies of a CTA that have not landed, by tier
-    float scale_log2;
-    DevStatus* st;
-};
-
 enum : uint32_t { T_PROD_EMPTY = 0x71, T_PROD_FULL, T_MMA_FULL, T_MMA_P, T_MMA_PV, T_SM_S, T_SM_O, T_Q_FREE, T_Q_FULL, T_DRAIN };
-
-// A request as the plan sees it.
-struct TreeRequest {
-    int len, n;                   // cached rows, drafted tokens
-    int keys, chunks;             // rows with the drafts, chunks of 64 keys
-    int tiles, twos;              // tiles, those of two halves
-    unsigned two, one, slab;      // cost of a tile of two halves, of one, of all tiles of a kv head
-};
-
-__device__ __forceinline__ TreeRequest tree_request(const TreeParams& p, int len, int n) {
-    TreeRequest q;
-    q.len = len;
-    q.n = n;
-    q.keys = min(q.len + n, p.L);
-    q.chunks = (q.keys + 63) >> 6;
-    const int halves = ((n + p.mpt - 1) * p.inv_mpt) >> 16;
-    q.twos = halves >> 1;
-    q.tiles = (halves + 1) >> 1;
-    q.two = kTreeTileCost + kTreeTwoCost * q.chunks;
-    q.one = kTreeTileCost + kTreeOneCost * q.chunks;
-    q.slab = q.twos * q.two + (halves & 1) * q.one;
-    return q;
-}
-__device__ __forceinline__ TreeRequest tree_request(const TreeParams& p, int b) {
-    const int n = p.n_new ? p.n_new[b] : p.T;
-    return tree_request(p, min(max(p.lens[b], 0), p.L), min(max(n, 0), p.T));
-}
-
-// n / d for quotients below 2^21 (the float quotient is off by less than one, which the remainder puts
-// right): an integer division is dozens of instructions that run for the first time.
-__device__ __forceinline__ unsigned tree_quotient(unsigned n, unsigned d) {
-    const unsigned q = static_cast<unsigned>(static_cast<float>(n) * __fdividef(1.f, static_cast<float>(d)));
-    const int r = static_cast<int>(n - q * d);
-    return q + (r >= static_cast<int>(d)) - (r < 0);
-}
-
-struct TreePlan {
-    unsigned len;                // of a range
-    int ranges, host_ranges;     // host_ranges: those that touch the host's slabs
-    TreeRequest own;             // request `lane`, of which the lanes of a warp find theirs without loads
-};
-
-// By one warp, as are the functions of TreeWalk.
-__device__ __forceinline__ TreePlan tree_plan(const TreeParams& p) {
-    constexpr unsigned all = 0xffffffffu;
-    const int lane = threadIdx.x & 31, bh = p.host_requests;
-    TreePlan x;
-    x.own.slab = 0;
-    if (lane < p.B) x.own = tree_request(p, lane);
-    unsigned total = 0, host = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
-        const unsigned slab = b0 == 0 ? x.own.slab : b < p.B ? tree_request(p, b).slab : 0u;
-        total += slab * p.Hkv;
-        if (b <= bh) host += slab * (b < bh ? p.Hkv : p.h_s - bh * p.Hkv);
-    }
-    total = __reduce_add_sync(all, total);
-    host = __reduce_add_sync(all, host);
-    x.len = max(tree_quotient(total + p.ranges - 1, p.ranges), kTreeMinRange);
-    x.ranges = static_cast<int>(tree_quotient(total + x.len - 1, x.len));
-    x.host_ranges = static_cast<int>(tree_quotient(host + x.len - 1, x.len));
-    return x;
-}
-
-// A tile on the line, and the part of it that a range takes.
-struct TreeWalk {
-    int b, g, tile;
-    unsigned at;  // where the tile begins
-    TreeRequest q;
-
-    __device__ __forceinline__ bool two() const { return tile < q.twos; }
-    __device__ __forceinline__ unsigned end() const { return at + (two() ? q.two : q.one); }
-    // The tile at position x, which lies on the line.
-    __device__ __forceinline__ void find(const TreeParams& p, const TreePlan& plan, unsigned x) {
-        constexpr unsigned all = 0xffffffffu;
-        const int lane = threadIdx.x & 31;
-        unsigned base = 0;
-        b = 0;
-#pragma unroll 1
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            if (b0 > 0) q.slab = b0 + lane < p.B ? tree_request(p, b0 + lane).slab : 0u;
-            else q.slab = plan.own.slab;
-            const unsigned cost = q.slab * p.Hkv;
-            unsigned incl = cost;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned v = __shfl_up_sync(all, incl, o);
-                if (lane >= o) incl += v;
-            }
-            const unsigned hit = __ballot_sync(all, x < base + incl);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                b = b0 + l;
-                base += __shfl_sync(all, incl - cost, l);
-                break;
-            }
-            base += __shfl_sync(all, incl, 31);
-        }
-        load(p, plan);
-        g = static_cast<int>(tree_quotient(x - base, q.slab));
-        at = base + g * q.slab;
-        tile = min(static_cast<int>(tree_quotient(x - at, q.two)), q.twos);
-        at += tile * q.two;
-    }
-    __device__ __forceinline__ void load(const TreeParams& p, const TreePlan& plan) {
-        if (b < 32) {
-            const int n = __shfl_sync(0xffffffffu, plan.own.n, b);
-            q = tree_request(p, __shfl_sync(0xffffffffu, plan.own.len, b), n);
-        } else {
-            q = tree_request(p, b);
-        }
-    }
-    // The next tile; past the line's end b is B.
-    __device__ __forceinline__ void next(const TreeParams& p, const TreePlan& plan) {
-        at = end();
-        if (++tile < q.tiles) return;
-        tile = 0;
-        if (++g < p.Hkv) return;
-        g = 0;
-        while (++b < p.B) {
-            load(p, plan);
-            if (q.tiles > 0) break;
-        }
-    }
-    // The first chunk that does not belong to the ranges before position x.
-    __device__ __forceinline__ int cut(unsigned x, unsigned range_len) const {
-        if (x <= at) return 0;
-        if (x >= end()) return q.chunks;
-        const unsigned k = two() ? kTreeTwoCost : kTreeOneCost, in = x - at;
-        const int t = in <= kTreeTileCost ? 0 : static_cast<int>((in - kTreeTileCost + k - 1) / k);
-        const int least = range_len >= kTreeSnapRange ? 2 : 1;
-        return t < least ? 0 : q.chunks - t < least ? q.chunks : t;
-    }
-};
-
-// Draft s of the request is seen by token t, for the 64 keys from key0 on.
-__device__ __forceinline__ unsigned long long tree_bits(const TreeParams& p, const TreeRequest& q, int b, int t, int key0) {
-    const int d0 = key0 - q.len;  // draft of the first key
-    const int n = min(q.keys - q.len, p.mask ? p.T : t + 1);  // drafts that may be seen
-    unsigned long long v = ~0ull;
-    if (p.mask) {
-        const unsigned long long* w = p.mask + b * p.mask_pitch + static_cast<long long>(t) * p.W;
-        if (d0 < 0) {
-            v = d0 > -64 ? w[0] << -d0 : 0;
-        } else {
-            const int i = d0 >> 6, sh = d0 & 63;
-            v = i < p.W ? w[i] >> sh : 0;
-            if (sh && i + 1 < p.W) v |= w[i + 1] << (64 - sh);
-        }
-    }
-    const int valid = n - d0;  // keys before the drafts that may not be seen
-    if (valid < 64) v &= valid > 0 ? (1ull << valid) - 1 : 0;
-    if (d0 < 0) v |= d0 > -64 ? (1ull << -d0) - 1 : ~0ull;
-    return v;
-}
-
-// Whether a token sees any row at all.
-__device__ __forceinline__ bool tree_sees(const TreeParams& p, const TreeRequest& q, int b, int t) {
-    if (q.len > 0) return true;
-    unsigned long long any = 0;
-    for (int k = 0; k < q.keys; k += 64) any |= tree_bits(p, q, b, t, k);
-    return any != 0;
-}
 
 struct KeysUnset {
     uint32_t bits;
@@ -415,12 +209,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     grid_dep_launch();
     const TreePlan plan = tree_plan(p);
     if (threadIdx.x == 0 && static_cast<int>(blockIdx.x) >= plan.ranges) p.heads[blockIdx.x].pieces = 0;
-    // this CTA's ranges: the one of its number, unless more ranges touch the host than CTAs may
-    const bool many = plan.host_ranges > p.host_ctas, takes_host = many && static_cast<int>(blockIdx.x) < p.host_ctas;
-    const int r0 = !many || takes_host ? blockIdx.x : plan.host_ranges + blockIdx.x - p.host_ctas;
-    const int r_end = takes_host ? plan.host_ranges : plan.ranges, r_step = takes_host ? p.host_ctas : p.ranges;
+    const TreeTurn turn = tree_turn(p, plan);
     TreeWalk w;
-    if (r0 < r_end) w.find(p, plan, r0 * plan.len);
+    if (turn.first < turn.end) w.find(p, plan, turn.first * plan.len);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -432,11 +223,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         RingPos<NS> pos(0), landed(0);
         int sent = 0, behind = 0;  // copies issued, and of these seen to have landed
         bool ok = true;
-        for (int r = r0; r < r_end && ok; r += r_step) {
+        for (int r = turn.first; r < turn.end && ok; r += turn.step) {
             const unsigned xs = r * plan.len, xe = xs + plan.len;
-            if (r > r0) w.find(p, plan, xs);
+            if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
-                const int c0 = w.cut(xs, plan.len), c1 = w.cut(xe, plan.len);
+                const int c0 = w.cut(p, xs, plan.len), c1 = w.cut(p, xe, plan.len);
                 if (lane == 0) {
                     const long long slab = static_cast<long long>(w.b) * p.Hkv + w.g;
                     const int tier = slab < p.h_s ? 0 : 1, window = p.in_flight[tier];
@@ -479,11 +270,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         int stage = 0;  // stages used before it
         int brought = 0, shared = 0;  // tiles whose Q was brought before it, those in which stream 1 had steps
         bool ok = true, in_flight = false;
-        for (int r = r0; r < r_end && ok; r += r_step) {
+        for (int r = turn.first; r < turn.end && ok; r += turn.step) {
             const unsigned xs = r * plan.len, xe = xs + plan.len;
-            if (r > r0) w.find(p, plan, xs);
+            if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
-                const int steps = w.cut(xe, plan.len) - w.cut(xs, plan.len);
+                const int steps = w.cut(p, xe, plan.len) - w.cut(p, xs, plan.len);
                 if (steps <= 0) continue;
                 const bool two = w.two(), with_1 = two || steps > 1;
                 const int stride = two ? 1 : 2, first = two ? 0 : st, mine = first < steps ? (steps - first + stride - 1) / stride : 0;
@@ -576,24 +367,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         const int token_in = (r_in * p.inv_G) >> 16, head_in = r_in - token_in * p.G;  // of a half tile
         int n = 0, stage = 0;
         bool failed = false;
-        for (int r = r0; r < r_end; r += r_step) {
+        for (int r = turn.first; r < turn.end; r += turn.step) {
             const unsigned xs = r * plan.len, xe = xs + plan.len;
             if (threadIdx.x == 0) p.heads[r].pieces = 0;
-            if (r > r0) w.find(p, plan, xs);
+            if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe; w.next(p, plan)) {
-                const int c0 = w.cut(xs, plan.len), c1 = w.cut(xe, plan.len), steps = c1 - c0;
+                const int c0 = w.cut(p, xs, plan.len), c1 = w.cut(p, xe, plan.len), steps = c1 - c0;
                 if (steps <= 0) continue;
                 const bool two = w.two();
                 if (threadIdx.x == 0) {
-                    if (c0 == 0 && c1 < w.q.chunks) {
-                        // ranges up to the one with the tile's last chunk
-                        int last = static_cast<int>(tree_quotient(w.end() - 1, plan.len));
-                        while (w.cut(last * plan.len, plan.len) == w.q.chunks) --last;
-                        p.heads[r] = TreeHead{w.b, w.g, w.tile, last - r + 1, w.q.n, w.q.len, w.q.keys, 0};
-                    }
-                    if (w.g == 0 && w.tile == 0 && c0 == 0 && w.q.keys - w.q.len < w.q.n) {
-                        report(p.st, DAK_ERR_BOUNDS, (0x7EEEull << 32) | static_cast<unsigned>(w.b));
-                    }
+                    tree_head(p, plan, w, r, c0, c1);
+                    tree_report(p, w, c0);
                 }
                 const int token0 = (2 * w.tile + (two ? st : 0)) * p.mpt, t = token0 + token_in;
                 const bool valid_row = token_in < p.mpt && t < w.q.n;
@@ -899,22 +683,31 @@ __global__ void __launch_bounds__(32 * kTreeMergeRows) tree_merge_kernel(const _
 // ------------------------------------------------------------------------------------
 // host side
 // ------------------------------------------------------------------------------------
+constexpr unsigned kTreeTileCost = 6, kTreeMinRange = 6;        // of tree_kernel
+constexpr unsigned kTreeFewTileCost = 2, kTreeFewMinRange = 6;  // of tree_few_kernel
+
 struct TreeLayout {
+    bool few;
     int ranges, part_rows;
+    unsigned tile_cost, min_range;
     size_t o_part, ml_part, heads;
     size_t total() const { return 16 + o_part + ml_part + heads; }  // the partials begin on 32 bytes
 };
 
 static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// As many ranges as SMs; fewer where the cache, full, would not give each the least there may be.
+// As many ranges as CTAs run at once; fewer where the cache, full, would not give each the least there may be.
 static TreeLayout tree_layout(const dak_placement* KV, int T, int H_q) {
     const int G = H_q / KV->H_kv, mpt = 128 / G;
-    const int64_t chunks = (KV->L + 63) / 64, halves = (T + mpt - 1) / mpt;
-    const int64_t slab = (halves / 2) * (kTreeTileCost + kTreeTwoCost * chunks) + halves % 2 * (kTreeTileCost + kTreeOneCost * chunks);
-    const int64_t least = (slab * KV->B * KV->H_kv + kTreeMinRange - 1) / kTreeMinRange;
     TreeLayout x{};
-    x.ranges = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(device_sm_count(), least)));
+    x.few = T * G <= kTreeFewRows;
+    x.tile_cost = x.few ? kTreeFewTileCost : kTreeTileCost;
+    x.min_range = x.few ? kTreeFewMinRange : kTreeMinRange;
+    const int64_t chunks = (KV->L + 63) / 64, halves = (T + mpt - 1) / mpt;
+    const int64_t slab = (halves / 2) * (x.tile_cost + kTreeTwoCost * chunks) + halves % 2 * (x.tile_cost + kTreeOneCost * chunks);
+    const int64_t least = (slab * KV->B * KV->H_kv + x.min_range - 1) / x.min_range;
+    const int ctas = x.few ? tree_few_ctas(T * G, KV->D) : device_sm_count();
+    x.ranges = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ctas, least)));
     x.part_rows = T <= mpt ? T * G : std::min(256, 128 + (T - mpt) * G);
     x.o_part = round256(sizeof(float) * 2 * x.ranges * x.part_rows * KV->D);
     x.ml_part = round256(sizeof(float2) * 2 * x.ranges * x.part_rows);
@@ -947,7 +740,7 @@ template <int D, bool F32>
 static cudaError_t launch_tree(const TreeParams& p, const TreeMaps& maps, cudaStream_t s) {
     auto k = tree_kernel<D, F32>;
     static SmemLimit limit;
-    cudaError_t e = limit.raise(reinterpret_cast<const void*>(k), kTreeSmem<D>);
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(k), kTreeSmem<D>);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -959,12 +752,21 @@ static cudaError_t launch_tree(const TreeParams& p, const TreeMaps& maps, cudaSt
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k, p, maps);
-    if (e != cudaSuccess || p.ranges == 1) return e;
+    return cudaLaunchKernelEx(&cfg, k, p, maps);
+}
+
+static cudaError_t launch_tree_merge(const TreeParams& p, int D, cudaStream_t s) {
+    if (p.ranges == 1) return cudaSuccess;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(p.ranges - 1), static_cast<unsigned>((p.part_rows + kTreeMergeRows - 1) / kTreeMergeRows));
     cfg.blockDim = dim3(32 * kTreeMergeRows);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return D == 128 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<128>, p) : cudaLaunchKernelEx(&cfg, tree_merge_kernel<64>, p);
 }
 
 static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -1029,23 +831,33 @@ extern "C" dak_status dak_attn_tree(const void* Q, const dak_placement* KV, cons
     p.host_requests = KV->h_s / KV->H_kv;
     p.part_rows = x.part_rows;
     p.ranges = x.ranges;
+    p.tile_cost = x.tile_cost;
+    p.min_range = x.min_range;
     p.slab_chunks = (KV->L + 63) / 64;
     p.host_ctas = std::min(x.ranges, tuning && tuning->host_ctas > 0 ? tuning->host_ctas : kTreeHostCtas);
-    const int window = D == 128 ? ChunkCfg<128>::kInFlight : ChunkCfg<64>::kInFlight;
-    const int most = D == 128 ? ChunkCfg<128>::kStages : ChunkCfg<64>::kStages;
-    p.in_flight[0] = std::min(most, tuning && tuning->window > 0 ? tuning->window : window);
-    p.in_flight[1] = std::min(most, tuning && tuning->hbm_window > 0 ? tuning->hbm_window : window);
     p.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D))) * 1.4426950408889634f;
     p.st = status_ptr();
     if (!p.st) return DAK_ERR_CUDA;
-    const int64_t slabs = static_cast<int64_t>(KV->B) * KV->H_kv;
-    TreeMaps maps{};
-    for (int tier = 0; tier < 2; ++tier) {
-        const int64_t n = tier ? slabs - KV->h_s : KV->h_s;
-        if (n > 0 && !make_chunk_map(&maps.tier[tier], p.kv[tier], n * p.slab_chunks, D)) return DAK_ERR_CUDA;
-    }
-    if (!make_query_map(&maps.q, Q, static_cast<int64_t>(KV->B) * T, H_q, D, G, p.q_tokens)) return DAK_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return cuda_status(D == 128 ? (o_fp32 ? launch_tree<128, true>(p, maps, s) : launch_tree<128, false>(p, maps, s))
-                                : (o_fp32 ? launch_tree<64, true>(p, maps, s) : launch_tree<64, false>(p, maps, s)));
+    cudaError_t e;
+    if (x.few) {
+        p.in_flight[0] = tuning ? tuning->window : 0;
+        p.in_flight[1] = tuning ? tuning->hbm_window : 0;
+        e = launch_tree_few(p, T * G, D, s);
+    } else {
+        const int window = D == 128 ? ChunkCfg<128>::kInFlight : ChunkCfg<64>::kInFlight;
+        const int most = D == 128 ? ChunkCfg<128>::kStages : ChunkCfg<64>::kStages;
+        p.in_flight[0] = std::min(most, tuning && tuning->window > 0 ? tuning->window : window);
+        p.in_flight[1] = std::min(most, tuning && tuning->hbm_window > 0 ? tuning->hbm_window : window);
+        const int64_t slabs = static_cast<int64_t>(KV->B) * KV->H_kv;
+        TreeMaps maps{};
+        for (int tier = 0; tier < 2; ++tier) {
+            const int64_t n = tier ? slabs - KV->h_s : KV->h_s;
+            if (n > 0 && !make_chunk_map(&maps.tier[tier], p.kv[tier], n * p.slab_chunks, D)) return DAK_ERR_CUDA;
+        }
+        if (!make_query_map(&maps.q, Q, static_cast<int64_t>(KV->B) * T, H_q, D, G, p.q_tokens)) return DAK_ERR_CUDA;
+        e = D == 128 ? (o_fp32 ? launch_tree<128, true>(p, maps, s) : launch_tree<128, false>(p, maps, s))
+                     : (o_fp32 ? launch_tree<64, true>(p, maps, s) : launch_tree<64, false>(p, maps, s));
+    }
+    return cuda_status(e == cudaSuccess ? launch_tree_merge(p, D, s) : e);
 }
