@@ -18,7 +18,7 @@
 namespace dak {
 
 constexpr int kTreeSoftmax = 2 * 2 * 128;         // two streams, two threads a row: of a step's keys and of O's columns a half each
-constexpr int kTreeThreads = kTreeSoftmax + 3 * 32;  // and copies, each stream's products
+constexpr int kTreeThreads = kTreeSoftmax + 4 * 32;  // and copies, scores, each stream's P.V
 constexpr int kTreeHostCtas = 32;
 constexpr int kTreeMergeRows = 8;                 // a warp each
 
@@ -170,10 +170,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     using C = ChunkCfg<D>;
     constexpr int NS = C::kStages;
     constexpr int SB = F32 ? 1 : 2;  // buffers of S
-    constexpr int kCopies = kTreeSoftmax / 32, kProducts = kCopies + 1;  // warps
+    constexpr int kCopies = kTreeSoftmax / 32, kScores = kCopies + 1, kProducts = kScores + 1;  // warps
     extern __shared__ __align__(1024) uint8_t smem[];  // as the swizzle wants it; there is no room for a margin
     uint8_t* ring = smem + 2 * C::kTileBytes;
-    __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_ready[2][2], pv_done[2][2], q_full, q_ready, q_free;
+    __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_ready[2][2], pv_done[2][2], q_full;
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_flag, any_bad;
     __shared__ unsigned bad[DAK_MAX_TREE / 32];  // drafts with infinities or NaN in V, of the tile at work
@@ -195,8 +195,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             }
         }
         mbar_init(&q_full, 1);
-        mbar_init(&q_ready, 1);
-        mbar_init(&q_free, 1);
         fence_mbar_init();
     }
     if (threadIdx.x < DAK_MAX_TREE / 32) bad[threadIdx.x] = 0;
@@ -258,98 +256,106 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             }
         }
         __syncwarp();
-    } else if (warp >= kProducts) {
-        // ---------------------------------------------------------------- products, a warp per stream
-        // Stream 0's also brings Q for both, and hands it to stream 1's (q_ready), which says when its last
-        // product has read it (q_free): one after the other for every tile in which stream 1 has steps.
-        const int st = warp - kProducts;
+    } else if (warp == kScores) {
+        // ---------------------------------------------------------------- Q, and the scores of both streams
+        // A product's issue takes its warp some 40 cycles whatever its size, and a wait 100: one warp for a stream's
+        // scores and P.V took 2000 a step, more than the products themselves.
         const bool leader = elect_one();
         const uint32_t ring_addr = smem_u32(ring);
-        const uint32_t s_tmem = tmem + st * 128, o_tmem = tmem + 256 + st * D;
-        int n = 0;      // steps of this stream before this tile
-        int stage = 0;  // stages used before it
-        int brought = 0, shared = 0;  // tiles whose Q was brought before it, those in which stream 1 had steps
+        RingPos<NS> pos(0);
+        int n[2] = {0, 0};  // steps of the streams so far
+        int tiles = 0;
         bool ok = true, in_flight = false;
+        // S buffer of a stream's step i, and the parity of its barriers' phase: a wait by parity is right only
+        // where the phase before is known to be over and the one after not to be, and steps i and i + SB of a
+        // buffer wait for each other.
+        const auto buf = [](int i) { return i & (SB - 1); };
+        const auto par = [](int i) { return static_cast<uint32_t>(i / SB) & 1u; };
         for (int r = turn.first; r < turn.end && ok; r += turn.step) {
             const unsigned xs = r * plan.len, xe = xs + plan.len;
             if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
                 const int steps = w.cut(p, xe, plan.len) - w.cut(p, xs, plan.len);
                 if (steps <= 0) continue;
-                const bool two = w.two(), with_1 = two || steps > 1;
-                const int stride = two ? 1 : 2, first = two ? 0 : st, mine = first < steps ? (steps - first + stride - 1) / stride : 0;
-                // S buffer of this stream's step i of the tile, and the parity of its barriers' phase: a
-                // wait by parity is right only where the phase before is known to be over and the one after
-                // not to be, and steps i and i + SB of a buffer wait for each other.
-                const auto buf = [&](int i) { return (n + i) & (SB - 1); };
-                const auto par = [&](int i) { return static_cast<uint32_t>((n + i) / SB) & 1u; };
-                if (st == 0) {
-                    if (n > 0) ok = wait_phase(&s_full[0][buf(-1)], par(-1), abort, p.st, T_Q_FREE);
-                    if (ok && shared > 0) ok = wait_phase(&q_free, static_cast<uint32_t>(shared - 1) & 1u, abort, p.st, T_Q_FREE);
-                    if (!ok) break;
-                    if (leader) {
-                        const int halves = two ? 2 : 1, bytes = p.q_tokens * p.G * 128;
-                        mbar_arrive_expect_tx(&q_full, halves * (D / 64) * bytes);
-                        for (int h = 0; h < halves; ++h) {
-                            for (int k = 0; k < D / 64; ++k) {
-                                tma_load_q(smem + h * C::kTileBytes + k * 16384, &maps.q, w.g * p.G,
-                                           w.b * p.T + (2 * w.tile + h) * p.mpt, k, &q_full);
-                            }
-                        }
-                    }
-                    __syncwarp();
-                    in_flight = !wait_phase(&q_full, static_cast<uint32_t>(brought) & 1u, abort, p.st, T_Q_FULL);
-                    ok = !in_flight;
-                    if (ok && with_1 && leader) mbar_arrive(&q_ready);
-                    __syncwarp();
-                } else if (with_1) {
-                    ok = wait_phase(&q_ready, static_cast<uint32_t>(shared) & 1u, abort, p.st, T_Q_FULL);
+                const bool two = w.two();
+                // Q, when the scores that read the last tile's are there
+                for (int st = 0; st < 2; ++st) {
+                    if (n[st] > 0) ok = ok && wait_phase(&s_full[st][buf(n[st] - 1)], par(n[st] - 1), abort, p.st, T_Q_FREE);
                 }
                 if (!ok) break;
-                tc_fence_after();
-                const uint32_t q_addr = smem_u32(smem) + (two ? st * C::kTileBytes : 0);
-                RingPos<NS> kpos(stage + first), vpos(stage + first);
-                const auto qk = [&](int i) {
-                    if (!wait_phase(&full[kpos.slot], kpos.phase, abort, p.st, T_MMA_FULL)) return false;
-                    if (n + i >= SB && !wait_phase(&pv_done[st][buf(i)], par(i) ^ 1u, abort, p.st, T_MMA_PV)) return false;
-                    tc_fence_after();
-                    if (leader) {
-                        issue_qk<D>(s_tmem + buf(i) * 64, q_addr, ring_addr + kpos.slot * C::kStage);
-                        umma_commit(&s_full[st][buf(i)]);
-                        if (st == 1 && i + 1 == mine) umma_commit(&q_free);
+                if (leader) {
+                    const int halves = two ? 2 : 1, bytes = p.q_tokens * p.G * 128;
+                    mbar_arrive_expect_tx(&q_full, halves * (D / 64) * bytes);
+                    for (int h = 0; h < halves; ++h) {
+                        for (int k = 0; k < D / 64; ++k) {
+                            tma_load_q(smem + h * C::kTileBytes + k * 16384, &maps.q, w.g * p.G, w.b * p.T + (2 * w.tile + h) * p.mpt, k,
+                                       &q_full);
+                        }
                     }
-                    __syncwarp();
-                    kpos.advance(stride);
-                    return true;
-                };
-                ok = mine == 0 || qk(0);
-                for (int i = 0; i < mine && ok; ++i) {
-                    if (!F32 && i + 1 < mine) ok = qk(i + 1);
-                    ok = ok && wait_phase(&p_ready[st][buf(i)], par(i), abort, p.st, T_MMA_P);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (leader) {
-                        const uint32_t p_tmem = s_tmem + buf(i) * 64, v = ring_addr + vpos.slot * C::kStage + C::kV;
-                        if (F32) issue_pv<D, 3>(o_tmem, p_tmem, v, false);
-                        else issue_pv<D, 2>(o_tmem, p_tmem, v, i > 0);
-                        umma_commit(&pv_done[st][buf(i)]);
-                        // a stage is free when both streams have used it, or the one that does has said so twice
-                        umma_commit(&empty[vpos.slot]);
-                        if (!two) umma_commit(&empty[vpos.slot]);
-                    }
-                    __syncwarp();
-                    vpos.advance(stride);
-                    if (F32 && i + 1 < mine) ok = qk(i + 1);
                 }
-                n += mine;
-                stage += steps;
-                ++brought;
-                shared += with_1;
+                __syncwarp();
+                in_flight = !wait_phase(&q_full, static_cast<uint32_t>(tiles) & 1u, abort, p.st, T_Q_FULL);
+                ok = !in_flight;
+                for (int j = 0; j < steps && ok; ++j) {
+                    ok = wait_phase(&full[pos.slot], pos.phase, abort, p.st, T_MMA_FULL);
+                    const uint32_t k_addr = ring_addr + pos.slot * C::kStage;
+                    // two tiles: both streams take every step; one: they take turns
+                    for (int st = two ? 0 : j & 1; ok && st <= (two ? 1 : j & 1); ++st) {
+                        const int i = n[st];
+                        if (i >= SB) ok = wait_phase(&pv_done[st][buf(i)], par(i) ^ 1u, abort, p.st, T_MMA_PV);  // P in these columns is read
+                        tc_fence_after();
+                        if (ok && leader) {
+                            issue_qk<D>(tmem + st * 128 + buf(i) * 64, smem_u32(smem) + (two ? st * C::kTileBytes : 0), k_addr);
+                            umma_commit(&s_full[st][buf(i)]);
+                        }
+                        __syncwarp();
+                        n[st] += 1;
+                    }
+                    pos.advance(1);
+                }
+                tiles += ok;
             }
         }
         if (in_flight) {  // Q lands before the CTA may leave
             volatile int dummy = 0;
-            wait_phase(&q_full, static_cast<uint32_t>(brought) & 1u, &dummy, p.st, T_DRAIN);
+            wait_phase(&q_full, static_cast<uint32_t>(tiles) & 1u, &dummy, p.st, T_DRAIN);
+        }
+    } else if (warp >= kProducts) {
+        // ---------------------------------------------------------------- P.V, a warp per stream
+        const int st = warp - kProducts;
+        const bool leader = elect_one();
+        const uint32_t ring_addr = smem_u32(ring), s_tmem = tmem + st * 128, o_tmem = tmem + 256 + st * D;
+        int n = 0, stage = 0;  // steps of this stream so far, stages used before this tile
+        bool ok = true;
+        for (int r = turn.first; r < turn.end && ok; r += turn.step) {
+            const unsigned xs = r * plan.len, xe = xs + plan.len;
+            if (r > turn.first) w.find(p, plan, xs);
+            for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
+                const int steps = w.cut(p, xe, plan.len) - w.cut(p, xs, plan.len);
+                if (steps <= 0) continue;
+                const bool two = w.two();
+                const int stride = two ? 1 : 2, first = two ? 0 : st;
+                RingPos<NS> pos(stage + first);
+                for (int j = first; j < steps && ok; j += stride, ++n) {
+                    const int b = n & (SB - 1);
+                    ok = wait_phase(&full[pos.slot], pos.phase, abort, p.st, T_MMA_FULL) &&
+                         wait_phase(&p_ready[st][b], static_cast<uint32_t>(n / SB) & 1u, abort, p.st, T_MMA_P);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t p_tmem = s_tmem + b * 64, v = ring_addr + pos.slot * C::kStage + C::kV;
+                        if (F32) issue_pv<D, 3>(o_tmem, p_tmem, v, false);
+                        else issue_pv<D, 2>(o_tmem, p_tmem, v, j > first);
+                        umma_commit(&pv_done[st][b]);
+                        // a stage is free when both streams have used it, or the one that does has said so twice
+                        umma_commit(&empty[pos.slot]);
+                        if (!two) umma_commit(&empty[pos.slot]);
+                    }
+                    __syncwarp();
+                    pos.advance(stride);
+                }
+                stage += steps;
+            }
         }
     } else {
         // ---------------------------------------------------------------- softmax, two threads a row
