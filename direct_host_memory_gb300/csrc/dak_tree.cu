@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     constexpr int kCopies = kTreeSoftmax / 32, kScores = kCopies + 1, kProducts = kScores + 1;  // warps
     extern __shared__ __align__(1024) uint8_t smem[];  // as the swizzle wants it; there is no room for a margin
     uint8_t* ring = smem + 2 * C::kTileBytes;
-    __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_ready[2][2], pv_done[2][2], q_full;
+    __shared__ uint64_t full[NS], empty[NS], s_full[2][2], p_ready[2][2], pv_done[2][2], q_full, q_ready, q_free;
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_flag, any_bad;
     __shared__ unsigned bad[DAK_MAX_TREE / 32];  // drafts with infinities or NaN in V, of the tile at work
@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             }
         }
         mbar_init(&q_full, 1);
+        mbar_init(&q_ready, 1);
+        mbar_init(&q_free, 2);
         fence_mbar_init();
     }
     if (threadIdx.x < DAK_MAX_TREE / 32) bad[threadIdx.x] = 0;
@@ -214,7 +216,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_sh;
-    // TMEM columns: stream s has S at 128 s + 64 b (buffer b) with P over it, and O at 256 + D s
+    // TMEM columns: stream s has S at 128 s + 64 b (buffer b) with P over it, and O at 256 + D s.
+    // S buffer of a stream's n-th step, and the parity of its barriers' phase: a wait by parity is right only
+    // where the phase before is known to be over and the one after not to be, and steps n and n + SB of a
+    // buffer wait for each other.
+    const auto buf = [](int n) { return n & (SB - 1); };
+    const auto par = [](int n) { return static_cast<uint32_t>(n / SB) & 1u; };
+    // Issuing a product takes a warp some 40 cycles whatever the product's size, and a wait 100. Where the streams
+    // share a tile, two steps at once have to keep up with the arrival of two chunks: scores and each stream's P.V
+    // have warps of their own (32 chats of 16 drafts over 8K: 172 us with a warp for each stream's scores and P.V,
+    // 158 so). With a tile each the products take most of the time, and a warp for both streams' scores
+    // holds them up (48 of 64 drafts and 64 heads over 2K: 230 and 242 us).
 
     if (warp == kCopies) {
         // ---------------------------------------------------------------- copies
@@ -257,20 +269,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         }
         __syncwarp();
     } else if (warp == kScores) {
-        // ---------------------------------------------------------------- Q, and the scores of both streams
-        // A product's issue takes its warp some 40 cycles whatever its size, and a wait 100: one warp for a stream's
-        // scores and P.V took 2000 a step, more than the products themselves.
+        // ---------------------------------------------------------------- Q, and the scores of a tile that both streams share
         const bool leader = elect_one();
-        const uint32_t ring_addr = smem_u32(ring);
         RingPos<NS> pos(0);
         int n[2] = {0, 0};  // steps of the streams so far
-        int tiles = 0;
-        bool ok = true, in_flight = false;
-        // S buffer of a stream's step i, and the parity of its barriers' phase: a wait by parity is right only
-        // where the phase before is known to be over and the one after not to be, and steps i and i + SB of a
-        // buffer wait for each other.
-        const auto buf = [](int i) { return i & (SB - 1); };
-        const auto par = [](int i) { return static_cast<uint32_t>(i / SB) & 1u; };
+        int tiles = 0, twos = 0;  // tiles so far, those of two halves
+        bool ok = true, in_flight = false, was_two = false;
         for (int r = turn.first; r < turn.end && ok; r += turn.step) {
             const unsigned xs = r * plan.len, xe = xs + plan.len;
             if (r > turn.first) w.find(p, plan, xs);
@@ -278,11 +282,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 const int steps = w.cut(p, xe, plan.len) - w.cut(p, xs, plan.len);
                 if (steps <= 0) continue;
                 const bool two = w.two();
-                // Q, when the scores that read the last tile's are there
-                for (int st = 0; st < 2; ++st) {
-                    if (n[st] > 0) ok = ok && wait_phase(&s_full[st][buf(n[st] - 1)], par(n[st] - 1), abort, p.st, T_Q_FREE);
+                // Q, when the scores that read the last tile's are there: those of a tile of two halves are the
+                // streams' own warps' products, whose phases this one has not followed
+                if (was_two) {
+                    ok = wait_phase(&q_free, static_cast<uint32_t>(twos - 1) & 1u, abort, p.st, T_Q_FREE);
+                } else {
+                    for (int st = 0; st < 2; ++st) {
+                        if (n[st] > 0) ok = ok && wait_phase(&s_full[st][buf(n[st] - 1)], par(n[st] - 1), abort, p.st, T_Q_FREE);
+                    }
                 }
                 if (!ok) break;
+                was_two = two;
                 if (leader) {
                     const int halves = two ? 2 : 1, bytes = p.q_tokens * p.G * 128;
                     mbar_arrive_expect_tx(&q_full, halves * (D / 64) * bytes);
@@ -296,21 +306,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 __syncwarp();
                 in_flight = !wait_phase(&q_full, static_cast<uint32_t>(tiles) & 1u, abort, p.st, T_Q_FULL);
                 ok = !in_flight;
-                for (int j = 0; j < steps && ok; ++j) {
-                    ok = wait_phase(&full[pos.slot], pos.phase, abort, p.st, T_MMA_FULL);
-                    const uint32_t k_addr = ring_addr + pos.slot * C::kStage;
-                    // two tiles: both streams take every step; one: they take turns
-                    for (int st = two ? 0 : j & 1; ok && st <= (two ? 1 : j & 1); ++st) {
-                        const int i = n[st];
-                        if (i >= SB) ok = wait_phase(&pv_done[st][buf(i)], par(i) ^ 1u, abort, p.st, T_MMA_PV);  // P in these columns is read
-                        tc_fence_after();
-                        if (ok && leader) {
-                            issue_qk<D>(tmem + st * 128 + buf(i) * 64, smem_u32(smem) + (two ? st * C::kTileBytes : 0), k_addr);
-                            umma_commit(&s_full[st][buf(i)]);
-                        }
-                        __syncwarp();
-                        n[st] += 1;
+                if (two) {
+                    if (ok && leader) mbar_arrive(&q_ready);  // the streams' own warps issue the products
+                    __syncwarp();
+                    n[0] += steps;
+                    n[1] += steps;
+                    pos.skip(steps);
+                    ++twos;
+                }
+                for (int j = 0; !two && j < steps && ok; ++j) {
+                    const int st = j & 1, i = n[st];
+                    ok = wait_phase(&full[pos.slot], pos.phase, abort, p.st, T_MMA_FULL) &&
+                         (i < SB || wait_phase(&pv_done[st][buf(i)], par(i) ^ 1u, abort, p.st, T_MMA_PV));  // P in these columns is read
+                    tc_fence_after();
+                    if (ok && leader) {
+                        issue_qk<D>(tmem + st * 128 + buf(i) * 64, smem_u32(smem), smem_u32(ring) + pos.slot * C::kStage);
+                        umma_commit(&s_full[st][buf(i)]);
                     }
+                    __syncwarp();
+                    n[st] += 1;
                     pos.advance(1);
                 }
                 tiles += ok;
@@ -321,11 +335,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             wait_phase(&q_full, static_cast<uint32_t>(tiles) & 1u, &dummy, p.st, T_DRAIN);
         }
     } else if (warp >= kProducts) {
-        // ---------------------------------------------------------------- P.V, a warp per stream
+        // ---------------------------------------------------------------- P.V, a warp per stream, and its scores if it has a tile of its own
         const int st = warp - kProducts;
         const bool leader = elect_one();
         const uint32_t ring_addr = smem_u32(ring), s_tmem = tmem + st * 128, o_tmem = tmem + 256 + st * D;
-        int n = 0, stage = 0;  // steps of this stream so far, stages used before this tile
+        int n = 0, stage = 0;  // steps of this stream and stages used before this tile
+        int twos = 0;          // tiles of two halves before it
         bool ok = true;
         for (int r = turn.first; r < turn.end && ok; r += turn.step) {
             const unsigned xs = r * plan.len, xe = xs + plan.len;
@@ -334,26 +349,46 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 const int steps = w.cut(p, xe, plan.len) - w.cut(p, xs, plan.len);
                 if (steps <= 0) continue;
                 const bool two = w.two();
-                const int stride = two ? 1 : 2, first = two ? 0 : st;
-                RingPos<NS> pos(stage + first);
-                for (int j = first; j < steps && ok; j += stride, ++n) {
-                    const int b = n & (SB - 1);
-                    ok = wait_phase(&full[pos.slot], pos.phase, abort, p.st, T_MMA_FULL) &&
-                         wait_phase(&p_ready[st][b], static_cast<uint32_t>(n / SB) & 1u, abort, p.st, T_MMA_P);
+                const int stride = two ? 1 : 2, first = two ? 0 : st, mine = first < steps ? (steps - first + stride - 1) / stride : 0;
+                RingPos<NS> kpos(stage), vpos(stage + first);
+                const auto qk = [&](int i) {
+                    if (!wait_phase(&full[kpos.slot], kpos.phase, abort, p.st, T_MMA_FULL)) return false;
+                    if (n + i >= SB && !wait_phase(&pv_done[st][buf(n + i)], par(n + i) ^ 1u, abort, p.st, T_MMA_PV)) return false;
+                    tc_fence_after();
+                    if (leader) {
+                        issue_qk<D>(s_tmem + buf(n + i) * 64, smem_u32(smem) + st * C::kTileBytes, ring_addr + kpos.slot * C::kStage);
+                        umma_commit(&s_full[st][buf(n + i)]);
+                        if (i + 1 == mine) umma_commit(&q_free);
+                    }
+                    __syncwarp();
+                    kpos.advance(1);
+                    return true;
+                };
+                if (two) {
+                    ok = wait_phase(&q_ready, static_cast<uint32_t>(twos) & 1u, abort, p.st, T_Q_FULL) && qk(0);
+                    ++twos;
+                }
+                for (int i = 0; i < mine && ok; ++i) {
+                    const int b = buf(n + i);
+                    if (two) ok = F32 || i + 1 >= mine || qk(i + 1);
+                    else ok = wait_phase(&full[vpos.slot], vpos.phase, abort, p.st, T_MMA_FULL);
+                    ok = ok && wait_phase(&p_ready[st][b], par(n + i), abort, p.st, T_MMA_P);
                     if (!ok) break;
                     tc_fence_after();
                     if (leader) {
-                        const uint32_t p_tmem = s_tmem + b * 64, v = ring_addr + pos.slot * C::kStage + C::kV;
+                        const uint32_t p_tmem = s_tmem + b * 64, v = ring_addr + vpos.slot * C::kStage + C::kV;
                         if (F32) issue_pv<D, 3>(o_tmem, p_tmem, v, false);
-                        else issue_pv<D, 2>(o_tmem, p_tmem, v, j > first);
+                        else issue_pv<D, 2>(o_tmem, p_tmem, v, i > 0);
                         umma_commit(&pv_done[st][b]);
                         // a stage is free when both streams have used it, or the one that does has said so twice
-                        umma_commit(&empty[pos.slot]);
-                        if (!two) umma_commit(&empty[pos.slot]);
+                        umma_commit(&empty[vpos.slot]);
+                        if (!two) umma_commit(&empty[vpos.slot]);
                     }
                     __syncwarp();
-                    pos.advance(stride);
+                    vpos.advance(stride);
+                    if (F32 && two && i + 1 < mine) ok = qk(i + 1);
                 }
+                n += mine;
                 stage += steps;
             }
         }
@@ -391,8 +426,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 // this row in Q and O
                 const long long at = ((static_cast<long long>(w.b) * p.T + t) * p.Hq + w.g * p.G + head_in) * D;
                 const int stride = two ? 1 : 2;
-                const auto buf = [&](int i) { return (n + i) & (SB - 1); };
-                const auto par = [&](int i) { return static_cast<uint32_t>((n + i) / SB) & 1u; };
                 const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t where) {
                     if (!failed) failed = !mbar_wait(bar, parity, abort, p.st, DAK_ERR_TIMEOUT, where);
                     __syncwarp();
@@ -418,7 +451,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     uint32_t bits = 0xffffffffu;  // of this thread's keys
                     const bool drafts = key0 + 64 > w.q.len;
                     if (drafts && valid_row) bits = static_cast<uint32_t>(tree_bits(p, w.q, w.b, t, key0) >> (32 * half));
-                    wait(&s_full[st][buf(i)], par(i), T_SM_S);
+                    wait(&s_full[st][buf(n + i)], par(n + i), T_SM_S);
                     if (drafts) {
                         // Drafted rows' V may hold infinities and NaN, which the probability of zero of a token
                         // that does not see the row would not cancel, and rows behind the drafts anything at all.
@@ -453,7 +486,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                             }
                             return;
                         }
-                        wait(&pv_done[st][buf(i - 1)], par(i - 1), T_SM_O);
+                        wait(&pv_done[st][buf(n + i - 1)], par(n + i - 1), T_SM_O);
 #pragma unroll 1
                         for (int q = 0; q < HALF / 16; ++q) {
                             float o[16];
@@ -466,15 +499,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     };
                     if (warp_has_rows) {  // lanes without rows share a warp's work, warps without any do none
                         if (F32 && i > 0) add_product();  // the last step's: its scores' columns are these
-                        softmax_half<F32 ? 3 : 2>(s_addr + buf(i) * 64, half, pair, KeysUnset{bits}, p.scale_log2, m_ref, l, i == 0,
+                        softmax_half<F32 ? 3 : 2>(s_addr + buf(n + i) * 64, half, pair, KeysUnset{bits}, p.scale_log2, m_ref, l, i == 0,
                                                   valid_row, other, grown);
                         tmem_wait_st();
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_ready[st][buf(i)]);
+                    if (lane == 0) mbar_arrive(&p_ready[st][buf(n + i)]);
                 }
-                for (int k = max(0, i - SB); k < i; ++k) wait(&pv_done[st][buf(k)], par(k), T_SM_O);  // one phase of each buffer's
+                for (int k = max(0, i - SB); k < i; ++k) wait(&pv_done[st][buf(n + k)], par(n + k), T_SM_O);  // one phase of each buffer's
                 if (F32) {  // back to where the results are read from
                     if (i > 0) add_product();
 #pragma unroll
@@ -706,7 +739,7 @@ static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 static TreeLayout tree_layout(const dak_placement* KV, int T, int H_q) {
     const int G = H_q / KV->H_kv, mpt = 128 / G;
     TreeLayout x{};
-    x.few = T * G <= kTreeFewRows;
+    x.few = T * G <= (KV->D == 128 ? 16 : 32);
     x.tile_cost = x.few ? kTreeFewTileCost : kTreeTileCost;
     x.min_range = x.few ? kTreeFewMinRange : kTreeMinRange;
     const int64_t chunks = (KV->L + 63) / 64, halves = (T + mpt - 1) / mpt;

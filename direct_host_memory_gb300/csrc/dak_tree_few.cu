@@ -39,9 +39,11 @@ constexpr int few_stage_bytes() { return 2 * 64 * D * 2; }
 // CTAs an SM by registers: O^T and Q of more rows leave room for two.
 constexpr int few_ctas_per_sm(int NB) { return NB == 1 ? 3 : 2; }
 
+constexpr bool few_q_shared(int D, int NB) { return D * NB > 256; }
+
 template <int D, int NB>
 constexpr int few_fixed_bytes() {  // the four warps' merge, and Q where it does not fit into registers
-    return 2 * 8 * NB * (D + 2) * 4 + (NB > 2 ? 8 * NB * D * 2 : 0);
+    return 2 * 8 * NB * (D + 2) * 4 + (few_q_shared(D, NB) ? 8 * NB * D * 2 : 0);
 }
 template <int D, int NB>
 constexpr int few_stages() {  // as many as the CTAs of an SM have room for
@@ -55,7 +57,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
     constexpr int CHUNK_BYTES = 64 * D * 2;   // K (or V) of a chunk
     constexpr int STAGE = 2 * CHUNK_BYTES, W = few_stages<D, NB>();
     constexpr int ROWS = 8 * NB;
-    constexpr bool Q_SHARED = NB > 2;
+    constexpr bool Q_SHARED = few_q_shared(D, NB);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[W], empty[W];
     __shared__ int abort_flag;

@@ -263,6 +263,11 @@ struct RingPos {
     int slot;
     uint32_t phase;
     __device__ __forceinline__ explicit RingPos(int n) : slot(n % NS), phase(static_cast<uint32_t>(n / NS) & 1u) {}
+    __device__ __forceinline__ void skip(int by) {
+        const int to = slot + by;
+        phase ^= static_cast<uint32_t>(to / NS) & 1u;
+        slot = to % NS;
+    }
     __device__ __forceinline__ void advance(int by) {  // by < NS
         slot += by;
         if (slot >= NS) {

@@ -70,6 +70,11 @@ TREE_CASES = [
     (40, 2, 4, 2, 64, 130, [3 * i for i in range(40)], None, "chain", False, 11),
     (1, 4, 8, 2, 128, 20000, [19990], None, "tree", False, 0),
     (5, 12, 9, 1, 128, 900, [888, 0, 300, 64, 711], [12, 12, 1, 0, 6], "any", False, 2),
+    # several tiles of two halves, of one and of both kinds one after the other in a CTA
+    (80, 32, 64, 8, 128, 200, [(37 * i) % 168 for i in range(80)], None, "one", False, 100),
+    (40, 48, 32, 8, 64, 300, [(61 * i) % 252 for i in range(40)], [48 - i for i in range(40)], "chain", False, 0),
+    (60, 32, 32, 4, 64, 150, [(29 * i) % 118 for i in range(60)], [(i % 3) * 16 for i in range(60)], "one", True, 7),
+    (300, 6, 8, 2, 64, 100, [(13 * i) % 94 for i in range(300)], None, "one", False, 0),
 ]
 
 
