@@ -39,66 +39,85 @@ struct CommitParams {
     DevStatus* st;
 };
 
-constexpr int kCommitThreads = 256;
+constexpr int kCommitThreads = 128;
 
 // One block per slab, a thread per 16-byte piece of up to eight rows of K or V. A path ascends, so that
 // path[i] >= i: no row is written before the rows after it in the path have been read, if every
-// group of rows is read whole before it is written, and groups are taken in order.
+// group of rows is read whole before it is written, and groups are taken in order. What a block waits
+// for are two loads one after the other, the path and the rows; with 128 threads all slabs of a wide
+// batch are there at once (256 requests of 8 kv heads, up to 48 of 64 drafts, tables: 17.4 us with
+// blocks of 256 and the tables behind the rows).
 template <int D>
 __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitParams p) {
     constexpr int PIECES = 2 * (D / 8);                // of a row's K and V
     constexpr int LANES = kCommitThreads / PIECES;     // rows side by side
     constexpr int PER = 8;
+    constexpr int MORE = (DAK_MAX_TREE + kCommitThreads - 1) / kCommitThreads;  // drafts of a thread
     __shared__ int path[DAK_MAX_TREE];
     const int tid = threadIdx.x, b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv;
     const long long slab = blockIdx.x;
     grid_dep_wait();  // launched while the previous kernel ends
-    const int base = min(max(p.lens[b], 0), p.L), n_new = p.n_new ? min(max(p.n_new[b], 0), p.T) : p.T;
-    int n = min(max(p.n_path[b], 0), p.P);
     const int* in = p.path + static_cast<long long>(b) * p.P;
+    int v[MORE], before[MORE];
+#pragma unroll
+    for (int k = 0; k < MORE; ++k) {
+        const int i = tid + k * kCommitThreads;
+        v[k] = i < p.P ? in[i] : 0;
+        before[k] = i > 0 && i < p.P ? in[i - 1] : -1;
+    }
+    const int base = min(max(p.lens[b], 0), p.L), n_new = p.n_new ? min(max(p.n_new[b], 0), p.T) : p.T;
+    const int drafts = min(n_new, p.L - base);
+    int n = min(max(p.n_path[b], 0), p.P);
     bool good = true;
-    if (tid < n) {
-        const int v = in[tid];
-        path[tid] = v;
-        good = v >= (tid ? in[tid - 1] + 1 : 0) && v < n_new && v < p.L - base;
+#pragma unroll
+    for (int k = 0; k < MORE; ++k) {
+        const int i = tid + k * kCommitThreads;
+        if (i >= n) continue;
+        path[i] = v[k];
+        good = good && v[k] >= 0 && v[k] > before[k] && v[k] < drafts;
     }
     if (!__syncthreads_and(good)) {
         if (g == 0 && tid == 0) report(p.st, DAK_ERR_BOUNDS, (0xC0113ull << 32) | static_cast<unsigned>(b));
         n = 0;
     }
     if (g == 0 && tid == 0) p.lens_out[b] = base + n;
+    int* pos = p.slot_pos ? p.slot_pos + slab * p.L + base : nullptr;
+    float* acc = p.acc ? p.acc + slab * p.L + base : nullptr;
+    int pv[MORE];
+    float av[MORE];
+#pragma unroll
+    for (int k = 0; k < MORE; ++k) {
+        const int i = tid + k * kCommitThreads;
+        pv[k] = pos && i < n ? pos[path[i]] : -1;
+        av[k] = acc && i < n ? acc[path[i]] : 0.f;
+    }
     uint4* rows = reinterpret_cast<uint4*>(p.kv.slab(slab));
     const int piece = tid % PIECES, kv = piece / (D / 8), c = piece % (D / 8), r0 = tid / PIECES;
     const auto at = [&](int j) -> uint4& {
         return rows[(static_cast<long long>(j >> 6) * 2 + kv) * (8 * D) + (j & 63) * (D / 8) + (c ^ (j & 7))];
     };
     for (int i0 = 0; i0 < n; i0 += LANES * PER) {
-        uint4 v[PER];
+        uint4 x[PER];
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int i = i0 + k * LANES + r0;
-            if (i < n && path[i] != i) v[k] = at(base + path[i]);
+            if (i < n && path[i] != i) x[k] = at(base + path[i]);
         }
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int i = i0 + k * LANES + r0;
-            if (i < n && path[i] != i) at(base + i) = v[k];
+            if (i < n && path[i] != i) at(base + i) = x[k];
         }
     }
-    if (!p.slot_pos && !p.acc) return;
-    int* pos = p.slot_pos ? p.slot_pos + slab * p.L + base : nullptr;
-    float* acc = p.acc ? p.acc + slab * p.L + base : nullptr;
-    int pv = -1;
-    float av = 0.f;
-    if (tid < n) {
-        if (pos) pv = pos[path[tid]];
-        if (acc) av = acc[path[tid]];
-    }
-    __syncthreads();
-    if (tid < min(n_new, p.L - base)) {
-        if (pos) pos[tid] = pv;
-        if (acc) acc[tid] = av;
+    if (!pos && !acc) return;
+    __syncthreads();  // entries are all read
+#pragma unroll
+    for (int k = 0; k < MORE; ++k) {
+        const int i = tid + k * kCommitThreads;
+        if (i >= drafts) continue;
+        if (pos) pos[i] = pv[k];
+        if (acc) acc[i] = av[k];
     }
 }
 
@@ -124,9 +143,20 @@ struct ForkParams {
 constexpr int kForkThreads = 256;
 constexpr int kForkMax = DAK_MAX_FORK;
 
+__device__ __forceinline__ void copy_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+
+// A unit's stretch in one request: where it begins, which of its 16-byte pieces are wanted, and (of a
+// taker) where in the staging buffer its source's stretch lies.
+struct __align__(16) ForkStretch {
+    uint8_t* at;
+    int pieces;  // first | end << 16
+    int from;
+};
 
 // Every request that others go on from is a source, with a place in the staging buffers. A unit is the
 // same stretch of bytes (a power of two, at most 64 rows of K or V, as many as fit in a buffer
@@ -139,7 +169,9 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int n_src, n_take, lowest, highest;
     uint8_t* buffer = smem;
-    int* slot_of = reinterpret_cast<int*>(smem + 2 * p.stage);
+    ForkStretch* read_at = reinterpret_cast<ForkStretch*>(smem + 2 * p.stage);  // of each source, of the next unit
+    ForkStretch* write_at = read_at + p.src_B;                                  // of each taker, of this unit
+    int* slot_of = reinterpret_cast<int*>(write_at + p.B);
     int* src_f = slot_of + p.src_B;    // of each source: request, rows wanted
     int* src_lo = src_f + p.src_B;
     int* src_n = src_lo + p.src_B;
@@ -207,53 +239,65 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
     int unit = kHalf;
     while (unit > 16 && unit * sources > p.stage) unit >>= 1;
     const int shift = 31 - __clz(unit >> 4);  // pieces of 16 bytes of a unit: 1 << shift
-    const int subs = kHalf / unit, c0 = lowest >> 6, chunks = ((highest + 63) >> 6) - c0;
-    const long long n_units = static_cast<long long>(chunks) * 2 * subs * p.Hkv;
-    // unit x: kv head, chunk, byte offset in the slab and in the chunk's K or V
-    const auto place = [&](long long x, int& g, long long& at, int& row0, int& in_half) {
-        g = static_cast<int>(x % p.Hkv);
-        long long r = x / p.Hkv;
-        in_half = static_cast<int>(r % subs) * unit;
-        r /= subs;
-        const int kv = static_cast<int>(r & 1), c = c0 + static_cast<int>(r >> 1);
-        at = (static_cast<long long>(c) * 2 + kv) * kHalf + in_half;
-        row0 = c * 64;
+    const int subs = kHalf / unit, sub_shift = 31 - __clz(subs), c0 = lowest >> 6, chunks = ((highest + 63) >> 6) - c0;
+    const long long n_units = (static_cast<long long>(chunks) * p.Hkv << sub_shift) * 2;
+    // Unit x, stretches of one slab side by side: kv head, offset in the slab, and the rows lo .. n - 1 of
+    // one request as pieces of it.
+    const auto stretch = [&](long long x, const Tiers& tiers, int request, int lo, int n, int from) {
+        const int in_half = static_cast<int>(x & (subs - 1)) * unit, kv = static_cast<int>(x >> sub_shift) & 1;
+        const int y = static_cast<int>(x >> (sub_shift + 1)), c = y / p.Hkv, g = y - c * p.Hkv, row0 = (c0 + c) * 64;
+        // of the half's pieces, and of this stretch's
+        const int first = max(min(max(lo - row0, 0) * (kRow / 16) - in_half / 16, 1 << shift), 0);
+        const int end = max(min(min(n - row0, 64) * (kRow / 16) - in_half / 16, 1 << shift), 0);
+        ForkStretch at;
+        at.at = tiers.slab(static_cast<long long>(request) * p.Hkv + g) + (static_cast<long long>(c0 + c) * 2 + kv) * kHalf + in_half;
+        at.pieces = first | end << 16;
+        at.from = from;
+        return at;
     };
-    const auto read = [&](long long x, uint8_t* to) {
-        int g, row0, in_half;
-        long long at;
-        place(x, g, at, row0, in_half);
+    const auto sources_of = [&](long long x) {
+        for (int s = tid; s < sources; s += kForkThreads) read_at[s] = stretch(x, p.from, src_f[s], lo_of[s], src_n[s], s * unit);
+    };
+    const auto read = [&](uint8_t* to) {
         for (int e = tid; e < sources << shift; e += kForkThreads) {
-            const int s = e >> shift, off = (e & ((1 << shift) - 1)) << 4, row = row0 + (in_half + off) / kRow;
-            if (row < lo_of[s] || row >= src_n[s]) continue;
-            copy_async16(to + (static_cast<long long>(e) << 4), p.from.slab(static_cast<long long>(src_f[s]) * p.Hkv + g) + at + off);
+            const ForkStretch from = read_at[e >> shift];
+            const int k = e & ((1 << shift) - 1);
+            if (k >= (from.pieces & 0xFFFF) && k < from.pieces >> 16) copy_async16(to + from.from + (k << 4), from.at + (k << 4));
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     long long x = blockIdx.x;
-    int k = 0;
-    if (x < n_units) read(x, buffer);
-    for (; x < n_units; x += gridDim.x, k ^= 1) {
-        if (x + gridDim.x < n_units) read(x + gridDim.x, buffer + (k ^ 1) * p.stage);
+    if (x < n_units) sources_of(x);
+    __syncthreads();
+    if (x < n_units) read(buffer);
+    __syncthreads();
+    if (x + gridDim.x < n_units) sources_of(x + gridDim.x);
+    for (int k = 0; x < n_units; x += gridDim.x, k ^= 1) {
+        __syncthreads();  // the other buffer is free, the next stretches are known
+        if (x + gridDim.x < n_units) read(buffer + (k ^ 1) * p.stage);
         else asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int t = tid; t < takers; t += kForkThreads) {
+            write_at[t] = stretch(x, p.to, take_b[t], take_lo[t], src_n[take_slot[t]], take_slot[t] * unit);
+        }
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-        int g, row0, in_half;
-        long long at;
-        place(x, g, at, row0, in_half);
         const uint8_t* from = buffer + k * p.stage;
+#pragma unroll 4
         for (int e = tid; e < takers << shift; e += kForkThreads) {
-            const int t = e >> shift, off = (e & ((1 << shift) - 1)) << 4, row = row0 + (in_half + off) / kRow, s = take_slot[t];
-            if (row < take_lo[t] || row >= src_n[s]) continue;
-            *reinterpret_cast<uint4*>(p.to.slab(static_cast<long long>(take_b[t]) * p.Hkv + g) + at + off) =
-                *reinterpret_cast<const uint4*>(from + static_cast<long long>(s) * unit + off);
+            const ForkStretch to = write_at[e >> shift];
+            const int i = e & ((1 << shift) - 1);
+            if (i >= (to.pieces & 0xFFFF) && i < to.pieces >> 16) {
+                *reinterpret_cast<uint4*>(to.at + (i << 4)) = *reinterpret_cast<const uint4*>(from + to.from + (i << 4));
+            }
         }
-        __syncthreads();  // the buffer is free
+        if (x + 2ll * gridDim.x < n_units) sources_of(x + 2ll * gridDim.x);
     }
+    __syncthreads();
     if (!p.pos && !p.acc) return;
     asm volatile("cp.async.wait_all;" ::: "memory");
-    // the tables likewise, a word of each a row
-    int rows = 1024;
+    // the tables likewise, a word of each a row; short stretches, so that every CTA has some
+    int rows = 256;
+    while (rows > 32 && (rows * sources * 8 > 2 * p.stage || (highest - lowest) / rows * p.Hkv < static_cast<int>(gridDim.x))) rows >>= 1;
     while (rows > 1 && rows * sources * 8 > 2 * p.stage) rows >>= 1;
     const int lg = 31 - __clz(rows), blocks = (highest - lowest + rows - 1) / rows;
     int* hold_pos = reinterpret_cast<int*>(buffer);
@@ -265,10 +309,12 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
             const int s = e >> lg, j = j0 + (e & (rows - 1));
             if (j < lo_of[s] || j >= src_n[s]) continue;
             const long long at = (static_cast<long long>(src_f[s]) * p.Hkv + g) * p.src_L + j;
-            if (p.pos) hold_pos[e] = p.src_pos[at];
-            if (p.acc) hold_acc[e] = p.src_acc[at];
+            if (p.pos) copy_async4(&hold_pos[e], &p.src_pos[at]);
+            if (p.acc) copy_async4(&hold_acc[e], &p.src_acc[at]);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
+#pragma unroll 4
         for (int e = tid; e < takers << lg; e += kForkThreads) {
             const int t = e >> lg, r = e & (rows - 1), j = j0 + r, s = take_slot[t];
             if (j < take_lo[t] || j >= src_n[s]) continue;
@@ -280,7 +326,9 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
     }
 }
 
-static int fork_plan_bytes(int B, int src_B) { return (4 * src_B + 3 * B) * static_cast<int>(sizeof(int)); }
+static int fork_plan_bytes(int B, int src_B) {
+    return (src_B + B) * static_cast<int>(sizeof(ForkStretch)) + (4 * src_B + 3 * B) * static_cast<int>(sizeof(int));
+}
 
 template <int D>
 static cudaError_t launch_fork(ForkParams& p, cudaStream_t s) {

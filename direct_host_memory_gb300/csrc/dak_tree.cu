@@ -739,13 +739,13 @@ static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 static TreeLayout tree_layout(const dak_placement* KV, int T, int H_q) {
     const int G = H_q / KV->H_kv, mpt = 128 / G;
     TreeLayout x{};
-    x.few = T * G <= (KV->D == 128 ? 16 : 32);
+    x.few = T * G <= kTreeFewRows;
     x.tile_cost = x.few ? kTreeFewTileCost : kTreeTileCost;
     x.min_range = x.few ? kTreeFewMinRange : kTreeMinRange;
     const int64_t chunks = (KV->L + 63) / 64, halves = (T + mpt - 1) / mpt;
     const int64_t slab = (halves / 2) * (x.tile_cost + kTreeTwoCost * chunks) + halves % 2 * (x.tile_cost + kTreeOneCost * chunks);
     const int64_t least = (slab * KV->B * KV->H_kv + x.min_range - 1) / x.min_range;
-    const int ctas = x.few ? tree_few_ctas(T * G, KV->D) : device_sm_count();
+    const int ctas = x.few ? tree_few_ctas(T * G) : device_sm_count();
     x.ranges = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ctas, least)));
     x.part_rows = T <= mpt ? T * G : std::min(256, 128 + (T - mpt) * G);
     x.o_part = round256(sizeof(float) * 2 * x.ranges * x.part_rows * KV->D);

@@ -237,9 +237,11 @@ __device__ __forceinline__ void tree_report(const TreeParams& p, const TreeWalk&
     }
 }
 
-constexpr int kTreeFewRows = 32;  // query rows a kv head that tree_few_kernel takes, at most
+// Query rows a kv head that tree_few_kernel takes, at most (32 chats over 7K to 8K, 8 kv heads of 128: 16 rows
+// 150 us there, 48 155 by tree_kernel; 24 or 32 there 330, their O^T out of registers).
+constexpr int kTreeFewRows = 16;
 // Ranges (CTAs) of tree_few_kernel on this device, and its launch; the merge is the caller's.
-int tree_few_ctas(int rows, int D);
+int tree_few_ctas(int rows);
 cudaError_t launch_tree_few(const TreeParams& p, int rows, int D, cudaStream_t s);
 
 }  // namespace dak

@@ -39,11 +39,9 @@ constexpr int few_stage_bytes() { return 2 * 64 * D * 2; }
 // CTAs an SM by registers: O^T and Q of more rows leave room for two.
 constexpr int few_ctas_per_sm(int NB) { return NB == 1 ? 3 : 2; }
 
-constexpr bool few_q_shared(int D, int NB) { return D * NB > 256; }
-
 template <int D, int NB>
-constexpr int few_fixed_bytes() {  // the four warps' merge, and Q where it does not fit into registers
-    return 2 * 8 * NB * (D + 2) * 4 + (few_q_shared(D, NB) ? 8 * NB * D * 2 : 0);
+constexpr int few_fixed_bytes() {  // the four warps' merge
+    return 2 * 8 * NB * (D + 2) * 4;
 }
 template <int D, int NB>
 constexpr int few_stages() {  // as many as the CTAs of an SM have room for
@@ -57,13 +55,11 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
     constexpr int CHUNK_BYTES = 64 * D * 2;   // K (or V) of a chunk
     constexpr int STAGE = 2 * CHUNK_BYTES, W = few_stages<D, NB>();
     constexpr int ROWS = 8 * NB;
-    constexpr bool Q_SHARED = few_q_shared(D, NB);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[W], empty[W];
     __shared__ int abort_flag;
     volatile int* abort = &abort_flag;
     float* comb = reinterpret_cast<float*>(smem + W * STAGE);  // [2][ROWS][D + 2]
-    uint8_t* q_smem = reinterpret_cast<uint8_t*>(comb + 2 * ROWS * (D + 2));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -143,25 +139,16 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
                 const int t = (row * p.inv_G) >> 16;
                 return ((static_cast<long long>(w.b) * p.T + t) * p.Hq + w.g * p.G + row - t * p.G) * D;
             };
-            uint32_t q[Q_SHARED ? 1 : NB][Q_SHARED ? 1 : KS][2];  // rows nb * 8 + ra, elements ks * 16 + 2 q4 (+ 8)
-            if (Q_SHARED) {
-                for (int e = threadIdx.x - 32; e < ROWS * (D / 8); e += 32 * kFewConsumers) {
-                    const int row = e / (D / 8), c = e % (D / 8);
-                    const uint4 v = row < rows ? *reinterpret_cast<const uint4*>(p.Q + row_at(row) + c * 8) : make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(q_smem + row * D * 2 + ((c ^ (row & 7)) << 4)) = v;
-                }
-                bar();
-            } else {
+            uint32_t q[NB][KS][2];  // rows nb * 8 + ra, elements ks * 16 + 2 q4 (+ 8)
 #pragma unroll
-                for (int nb = 0; nb < (Q_SHARED ? 0 : NB); ++nb) {
-                    const int row = nb * 8 + ra;
-                    const __nv_bfloat16* from = p.Q + (row < rows ? row_at(row) : 0);
+            for (int nb = 0; nb < NB; ++nb) {
+                const int row = nb * 8 + ra;
+                const __nv_bfloat16* from = p.Q + (row < rows ? row_at(row) : 0);
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
+                for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            q[nb][ks][j] = row < rows ? *reinterpret_cast<const uint32_t*>(from + ks * 16 + 2 * q4 + 8 * j) : 0u;
-                        }
+                    for (int j = 0; j < 2; ++j) {
+                        q[nb][ks][j] = row < rows ? *reinterpret_cast<const uint32_t*>(from + ks * 16 + 2 * q4 + 8 * j) : 0u;
                     }
                 }
             }
@@ -205,21 +192,8 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
                             const int cc = ks * 2 + (mi >> 1);
                             uint32_t a0, a1, a2, a3;
                             ldsm_x4(ks_base + static_cast<uint32_t>(tok * D * 2 + ((cc ^ (tok & 7)) << 4)), a0, a1, a2, a3);
-                            if (Q_SHARED) {
 #pragma unroll
-                                for (int nb = 0; nb < NB; nb += 2) {  // two blocks of 8 rows at once
-                                    const int row = nb * 8 + (mi >> 1) * 8 + rr, qc = ks * 2 + (mi & 1);
-                                    uint32_t b0, b1, b2, b3;
-                                    ldsm_x4(smem_u32(q_smem) + static_cast<uint32_t>(row * D * 2 + ((qc ^ (row & 7)) << 4)), b0, b1, b2, b3);
-                                    mma_bf16_16816(sc[nb], a0, a1, a2, a3, b0, b1);
-                                    mma_bf16_16816(sc[nb + 1 < NB ? nb + 1 : nb], a0, a1, a2, a3, b2, b3);
-                                }
-                            } else {
-#pragma unroll
-                                for (int nb = 0; nb < (Q_SHARED ? 0 : NB); ++nb) {
-                                    mma_bf16_16816(sc[nb], a0, a1, a2, a3, q[nb][ks][0], q[nb][ks][1]);
-                                }
-                            }
+                            for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(sc[nb], a0, a1, a2, a3, q[nb][ks][0], q[nb][ks][1]);
                         }
                     }
                     bool grown = false;
@@ -418,7 +392,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
                 if (PARTS == 3) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + at) = make_float4(v[0], v[1], v[2], v[3]);
                 else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + at) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
             }
-            bar();  // comb and Q are rewritten by the next tile
+            bar();  // comb is rewritten by the next tile
         }
     }
 }
@@ -448,11 +422,10 @@ static cudaError_t launch_few(const TreeParams& given, cudaStream_t s) {
 template <int D>
 static cudaError_t launch_few_d(const TreeParams& p, int rows, cudaStream_t s) {
     if (rows <= 8) return p.o_fp32 ? launch_few<D, 1, 3>(p, s) : launch_few<D, 1, 2>(p, s);
-    if (rows <= 16) return p.o_fp32 ? launch_few<D, 2, 3>(p, s) : launch_few<D, 2, 2>(p, s);
-    return p.o_fp32 ? launch_few<D, 4, 3>(p, s) : launch_few<D, 4, 2>(p, s);
+    return p.o_fp32 ? launch_few<D, 2, 3>(p, s) : launch_few<D, 2, 2>(p, s);
 }
 
-int tree_few_ctas(int rows, int) { return few_ctas_per_sm(rows <= 8 ? 1 : 2) * device_sm_count(); }
+int tree_few_ctas(int rows) { return few_ctas_per_sm(rows <= 8 ? 1 : 2) * device_sm_count(); }
 
 cudaError_t launch_tree_few(const TreeParams& p, int rows, int D, cudaStream_t s) {
     return D == 128 ? launch_few_d<128>(p, rows, s) : launch_few_d<64>(p, rows, s);
