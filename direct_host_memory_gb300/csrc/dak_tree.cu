@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         int sent = 0, behind = 0;  // copies issued, and of these seen to have landed
         bool ok = true;
         for (int r = turn.first; r < turn.end && ok; r += turn.step) {
+            if (lane == 0) p.heads[r].pieces = 0;
             const unsigned xs = r * plan.len, xe = xs + plan.len;
             if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
@@ -255,6 +256,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         tma_load_chunk(ring + pos.slot * C::kStage, &maps.tier[tier], chunk0 + c, &full[pos.slot], policy);
                         pos.advance(1);
                         ++sent;
+                    }
+                    if (c0 < c1) {
+                        tree_head(p, plan, w, r, c0, c1);
+                        tree_report(p, w, c0);
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -410,16 +415,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         bool failed = false;
         for (int r = turn.first; r < turn.end; r += turn.step) {
             const unsigned xs = r * plan.len, xe = xs + plan.len;
-            if (threadIdx.x == 0) p.heads[r].pieces = 0;
             if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe; w.next(p, plan)) {
                 const int c0 = w.cut(p, xs, plan.len), c1 = w.cut(p, xe, plan.len), steps = c1 - c0;
                 if (steps <= 0) continue;
                 const bool two = w.two();
-                if (threadIdx.x == 0) {
-                    tree_head(p, plan, w, r, c0, c1);
-                    tree_report(p, w, c0);
-                }
                 const int token0 = (2 * w.tile + (two ? st : 0)) * p.mpt, t = token0 + token_in;
                 const bool valid_row = token_in < p.mpt && t < w.q.n;
                 const bool warp_has_rows = quad * 32 < min(w.q.n - token0, p.mpt) * p.G;
@@ -641,27 +641,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
 // ------------------------------------------------------------------------------------
 // Block (r, y): eight rows, a warp each, of the tile that begins in range r and ends in a later one:
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over its pieces, in order.
+// What it waits for are loads: the first pieces, which every such tile has, are asked for before it is known
+// whether there is one.
 template <int D>
 __global__ void __launch_bounds__(32 * kTreeMergeRows) tree_merge_kernel(const __grid_constant__ TreeParams p) {
     constexpr int LANES = D / 4, AT_ONCE = 32 / LANES;  // pieces that a warp reads at once
+    constexpr int EARLY = 2 / AT_ONCE;                  // of a lane's, asked for first
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.x;
-    grid_dep_wait();
-    const TreeHead head = p.heads[r];
-    // the limits: where a wait ran out, a range's entry may never have been written
-    if (head.pieces <= 0 || head.b < 0 || head.b >= p.B || head.g < 0 || head.g >= p.Hkv || head.tile < 0) return;
-    const int local = blockIdx.y * kTreeMergeRows + warp, r_in = local & 127, n = min(head.pieces, p.ranges - r);
-    const int token_in = (r_in * p.inv_G) >> 16, t = (2 * head.tile + (local >> 7)) * p.mpt + token_in;
-    if (token_in >= p.mpt || t >= min(head.n, p.T) || local >= p.part_rows) return;
+    const int local = blockIdx.y * kTreeMergeRows + warp, r_in = local & 127, token_in = (r_in * p.inv_G) >> 16;
+    if (local >= p.part_rows || token_in >= p.mpt) return;
     const auto slot = [&](int s) { return (2ll * (r + s) + (s == 0)) * p.part_rows + local; };
     const int c = lane % LANES, grp = lane / LANES;
     const auto part = [&](int s) { return *reinterpret_cast<const float4*>(p.o_part + slot(s) * D + c * 4); };
-    constexpr int EARLY = 4;  // of a lane's pieces asked for before the maxima are known
-    float4 early[EARLY];
+    grid_dep_wait();
+    const TreeHead head = p.heads[r];
+    float4 early[EARLY];  // range r is not the last
 #pragma unroll
-    for (int k = 0; k < EARLY; ++k) {
-        if (grp + k * AT_ONCE < n) early[k] = part(grp + k * AT_ONCE);
-    }
-    const float2 first = lane < n ? p.ml_part[slot(lane)] : make_float2(-INFINITY, 0.f);
+    for (int k = 0; k < EARLY; ++k) early[k] = part(grp + k * AT_ONCE);
+    float2 first = lane < p.ranges - r ? p.ml_part[slot(lane)] : make_float2(-INFINITY, 0.f);
+    // the limits: where a wait ran out, a range's entry may never have been written
+    if (head.pieces <= 0 || head.b < 0 || head.b >= p.B || head.g < 0 || head.g >= p.Hkv || head.tile < 0) return;
+    const int n = min(head.pieces, p.ranges - r), t = (2 * head.tile + (local >> 7)) * p.mpt + token_in;
+    if (t >= min(head.n, p.T)) return;
+    if (lane >= n) first = make_float2(-INFINITY, 0.f);
     float M = first.x;
     for (int s = lane + 32; s < n; s += 32) M = fmaxf(M, p.ml_part[slot(s)].x);
 #pragma unroll
@@ -680,21 +682,25 @@ __global__ void __launch_bounds__(32 * kTreeMergeRows) tree_merge_kernel(const _
         const float w = __shfl_sync(0xffffffffu, f, k * AT_ONCE + grp);
         if (grp + k * AT_ONCE < n) add(w, early[k]);
     }
-    for (int s0 = EARLY * AT_ONCE; s0 < n; s0 += 4 * AT_ONCE) {
-        if ((s0 & 31) == 0) {
-            const float2 v = s0 + lane < n ? p.ml_part[slot(s0 + lane)] : make_float2(-INFINITY, 0.f);
+    for (int at = 0; at < n; at += 32) {  // 32 pieces' factors on the lanes
+        if (at > 0) {
+            const float2 v = at + lane < n ? p.ml_part[slot(at + lane)] : make_float2(-INFINITY, 0.f);
             f = exp2f(v.x - base);
             l += f * v.y;
         }
-        float4 x[4];
+        for (int s0 = at > 0 ? 0 : EARLY * AT_ONCE; s0 < min(32, n - at); s0 += 6 * AT_ONCE) {
+            float4 x[6];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (s0 + k * AT_ONCE + grp < n) x[k] = part(s0 + k * AT_ONCE + grp);
-        }
+            for (int k = 0; k < 6; ++k) {
+                const int s = s0 + k * AT_ONCE + grp;
+                if (s < 32 && at + s < n) x[k] = part(at + s);
+            }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float w = __shfl_sync(0xffffffffu, f, (s0 + k * AT_ONCE + grp) & 31);
-            if (s0 + k * AT_ONCE + grp < n) add(w, x[k]);
+            for (int k = 0; k < 6; ++k) {
+                const int s = s0 + k * AT_ONCE + grp;
+                const float w = __shfl_sync(0xffffffffu, f, s & 31);
+                if (s < 32 && at + s < n) add(w, x[k]);
+            }
         }
     }
 #pragma unroll
@@ -722,8 +728,12 @@ __global__ void __launch_bounds__(32 * kTreeMergeRows) tree_merge_kernel(const _
 // ------------------------------------------------------------------------------------
 // host side
 // ------------------------------------------------------------------------------------
-constexpr unsigned kTreeTileCost = 6, kTreeMinRange = 6;        // of tree_kernel
-constexpr unsigned kTreeFewTileCost = 2, kTreeFewMinRange = 6;  // of tree_few_kernel
+// A tile by itself costs about as much as three and two chunks. Short ranges make more partials to merge than
+// they save: one chat of 4K, 8 drafts of 32 heads 13.3 us with ranges of 9, 14.9 of 4, 15.3 of 20; four drafts (few)
+// 14.0 with 8, 16.9 with 4, 16.3 with 16. 12 chats of up to 2.5K, fp32 heads of 64 (few): 16.5 with a tile's cost of
+// 4, 20.4 of 2.
+constexpr unsigned kTreeTileCost = 6, kTreeMinRange = 9;        // of tree_kernel
+constexpr unsigned kTreeFewTileCost = 4, kTreeFewMinRange = 8;  // of tree_few_kernel
 
 struct TreeLayout {
     bool few;

@@ -85,7 +85,9 @@ __device__ __forceinline__ unsigned tree_quotient(unsigned n, unsigned d) {
 struct TreePlan {
     unsigned len;                // of a range
     int ranges, host_ranges;     // host_ranges: those that touch the host's slabs
-    TreeRequest own;             // request `lane`, of which the lanes of a warp find theirs without loads
+    // the first 32 requests, a lane each, which a warp finds without loads:
+    TreeRequest own;
+    unsigned own_end;            // where its tiles end on the line
 };
 
 // By one warp, as are the functions of TreeWalk.
@@ -95,16 +97,26 @@ __device__ __forceinline__ TreePlan tree_plan(const TreeParams& p) {
     TreePlan x;
     x.own.slab = 0;
     if (lane < p.B) x.own = tree_request(p, lane);
-    unsigned total = 0, host = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
-        const unsigned slab = b0 == 0 ? x.own.slab : b < p.B ? tree_request(p, b).slab : 0u;
-        total += slab * p.Hkv;
-        if (b <= bh) host += slab * (b < bh ? p.Hkv : p.h_s - bh * p.Hkv);
+    x.own_end = x.own.slab * p.Hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned v = __shfl_up_sync(all, x.own_end, o);
+        if (lane >= o) x.own_end += v;
     }
-    total = __reduce_add_sync(all, total);
-    host = __reduce_add_sync(all, host);
+    unsigned total = __shfl_sync(all, x.own_end, 31), host = 0;
+    const auto host_part = [&](int b, unsigned slab) { return b < bh ? slab * p.Hkv : b == bh ? slab * (p.h_s - bh * p.Hkv) : 0u; };
+    if (p.h_s > 0) host = host_part(lane, x.own.slab);
+    if (p.B > 32) {
+        unsigned more = 0;
+#pragma unroll 1
+        for (int b = 32 + lane; b < p.B; b += 32) {
+            const unsigned slab = tree_request(p, b).slab;
+            more += slab * p.Hkv;
+            host += host_part(b, slab);
+        }
+        total += __reduce_add_sync(all, more);
+    }
+    if (p.h_s > 0) host = __reduce_add_sync(all, host);
     x.len = max(tree_quotient(total + p.ranges - 1, p.ranges), p.min_range);
     x.ranges = static_cast<int>(tree_quotient(total + x.len - 1, x.len));
     x.host_ranges = static_cast<int>(tree_quotient(host + x.len - 1, x.len));
@@ -123,27 +135,32 @@ struct TreeWalk {
     __device__ __forceinline__ void find(const TreeParams& p, const TreePlan& plan, unsigned x) {
         constexpr unsigned all = 0xffffffffu;
         const int lane = threadIdx.x & 31;
-        unsigned base = 0;
-        b = 0;
+        unsigned base = 0;  // where the request's tiles begin
+        unsigned hit = __ballot_sync(all, x < plan.own_end);
+        if (hit) {
+            b = __ffs(hit) - 1;
+            base = __shfl_sync(all, plan.own_end - plan.own.slab * p.Hkv, b);
+        } else {
+            base = __shfl_sync(all, plan.own_end, 31);
+            b = 32;
 #pragma unroll 1
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            if (b0 > 0) q.slab = b0 + lane < p.B ? tree_request(p, b0 + lane).slab : 0u;
-            else q.slab = plan.own.slab;
-            const unsigned cost = q.slab * p.Hkv;
-            unsigned incl = cost;
+            for (int b0 = 32; b0 < p.B; b0 += 32) {
+                const unsigned cost = b0 + lane < p.B ? tree_request(p, b0 + lane).slab * p.Hkv : 0u;
+                unsigned incl = cost;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned v = __shfl_up_sync(all, incl, o);
-                if (lane >= o) incl += v;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned v = __shfl_up_sync(all, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                hit = __ballot_sync(all, x < base + incl);
+                if (hit) {
+                    const int l = __ffs(hit) - 1;
+                    b = b0 + l;
+                    base += __shfl_sync(all, incl - cost, l);
+                    break;
+                }
+                base += __shfl_sync(all, incl, 31);
             }
-            const unsigned hit = __ballot_sync(all, x < base + incl);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                b = b0 + l;
-                base += __shfl_sync(all, incl - cost, l);
-                break;
-            }
-            base += __shfl_sync(all, incl, 31);
         }
         load(p, plan);
         g = static_cast<int>(tree_quotient(x - base, q.slab));
@@ -175,8 +192,8 @@ struct TreeWalk {
     __device__ __forceinline__ int cut(const TreeParams& p, unsigned x, unsigned range_len) const {
         if (x <= at) return 0;
         if (x >= end()) return q.chunks;
-        const unsigned k = two() ? kTreeTwoCost : kTreeOneCost, in = x - at;
-        const int t = in <= p.tile_cost ? 0 : static_cast<int>((in - p.tile_cost + k - 1) / k);
+        const unsigned in = max(x - at, p.tile_cost) - p.tile_cost;
+        const int t = static_cast<int>(two() ? (in + kTreeTwoCost - 1) / kTreeTwoCost : (in + kTreeOneCost - 1) / kTreeOneCost);
         const int least = range_len >= kTreeSnapRange ? 2 : 1;
         return t < least ? 0 : q.chunks - t < least ? q.chunks : t;
     }

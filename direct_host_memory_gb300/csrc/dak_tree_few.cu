@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
         uint32_t phase = 0;
         bool ok = true;
         for (int r = turn.first; r < turn.end && ok; r += turn.step) {
+            if (lane == 0) p.heads[r].pieces = 0;
             const unsigned xs = r * plan.len, xe = xs + plan.len;
             if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
@@ -101,6 +102,10 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
                         mbar_arrive_expect_tx(&full[s], STAGE);
                         bulk_g2s(smem + s * STAGE, base + static_cast<long long>(c) * STAGE, STAGE, &full[s], policy);
                         if (++s == W) s = 0, phase ^= 1u;
+                    }
+                    if (c0 < c1) {
+                        tree_head(p, plan, w, r, c0, c1);
+                        tree_report(p, w, c0);
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -125,15 +130,10 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
     bool failed = false;  // a wait ran out: skip the work but keep meeting the named barriers
     for (int r = turn.first; r < turn.end; r += turn.step) {
         const unsigned xs = r * plan.len, xe = xs + plan.len;
-        if (threadIdx.x == 32) p.heads[r].pieces = 0;
         if (r > turn.first) w.find(p, plan, xs);
         for (; w.b < p.B && w.at < xe; w.next(p, plan)) {
             const int c0 = w.cut(p, xs, plan.len), c1 = w.cut(p, xe, plan.len), rows = w.q.n * p.G;
             if (c0 >= c1) continue;
-            if (threadIdx.x == 32) {
-                tree_head(p, plan, w, r, c0, c1);
-                tree_report(p, w, c0);
-            }
             // row r of this kv head: token r / G, head r % G of the request
             const auto row_at = [&](int row) {
                 const int t = (row * p.inv_G) >> 16;

@@ -69,7 +69,11 @@ class SplitK_FlashAttn(torch.nn.Module):
     For chats that outgrow the cache, track() keeps every token's accumulated attention weight
     (self.weights, fp32 [B][H_kv][L]) and position (self.slot_pos, int32 of the same shape),
     which evict(...) goes by. For requests that share prefixes, forward takes the KV placement
-    that holds those."""
+    that holds those.
+    For drafted tokens, append_rope writes a tree of them behind each request's rows (with a rotation
+    by dak_rope_axes_make, which gives every token a position of its own), forward_tree attends for
+    all of them at once and commit(...) keeps the accepted path. fork(...) lets requests go on
+    from others' rows."""
 
     def __init__(self, k_cache, v_cache, offload_ratio: float = 0.0, n_host_heads: int = None,
                  n_split: int = 0, fp32_out: bool = False, tuning=None):
@@ -118,7 +122,8 @@ class SplitK_FlashAttn(torch.nn.Module):
     def append_rope(self, rope, q, k_new, v_new, slots, positions=None, n_new=None):
         """Rotate new tokens and write them from row slots[b] on (dak_kv_append_rope): q
         [B][T][H_q][D] or None, k_new and v_new [B][T][H_kv][D], bf16 or fp32 CUDA (T = 1: the
-        axis may be absent), rope by dak_rope_make; rope None: as they are. In a tracked cache a
+        axis may be absent), rope by dak_rope_make; rope None: as they are; rope by dak_rope_axes_make:
+        positions int32 [B][T][n_axes], each token's own (dak_kv_append_rope_axes). In a tracked cache a
         row's new token starts with its own position and no weight, whatever the row held before
         (a draft taken back, a chat that ended). Returns the rotated q in bf16. Where the module's
         tuning sets pdl, a single token is the newest one of seq_lens at the next forward, as after
@@ -127,6 +132,9 @@ class SplitK_FlashAttn(torch.nn.Module):
             rope = _lib.dak_rope_from_freqs(self.head_dim, [0.0])
         if k_new.ndim == 4 and k_new.shape[1] > 1:
             self._several_new = True
+        if isinstance(rope, _lib.dak_rope_axes_plan):
+            return _lib.dak_kv_append_rope_axes(self.placement, rope, q, k_new, v_new, slots, positions, n_new=n_new,
+                                                slot_pos=self.slot_pos, acc=self.weights)
         return _lib.dak_kv_append_rope(self.placement, rope, q, k_new, v_new, slots, positions=positions, n_new=n_new,
                                        slot_pos=self.slot_pos, acc=self.weights)
 
@@ -136,6 +144,43 @@ class SplitK_FlashAttn(torch.nn.Module):
         if self.slot_pos is None:
             raise ValueError("evict needs a tracked cache: call track() first")
         return _lib.dak_kv_evict(self.placement, seq_lens, n_keep, n_recent, self.weights, self.slot_pos)[0]
+
+    def forward_tree(self, query, seq_lens, mask=None, n_new=None, scale: float = None):
+        """Attention of T drafted tokens per request, whose rows append_rope wrote from row seq_lens[b] on:
+        query [B][T][H_q][D], mask int64 [B or 1][T][ceil(T / 64)] by dak_tree_mask (None: a chain), n_new
+        int32 [B] drafted tokens of each request (dak_attn_tree). Returns the same shape, bf16 (or fp32
+        with fp32_out); rows of tokens that were not drafted may hold anything. In a tracked cache no
+        weights come from it: which drafts are kept is not known yet, so an eviction goes by what
+        forward has seen."""
+        tun = {k: v for k, v in self.tuning.items() if k not in ("pdl", "link")}
+        return _lib.dak_attn_tree(query, self.placement, seq_lens, mask=mask, n_new=n_new, scale=float(scale or 0.0),
+                                  o_fp32=self.fp32_out, tuning=tun or None)
+
+    def commit(self, seq_lens, path, n_path, n_drafts: int, n_new=None):
+        """Keep the accepted drafts path[b][: n_path[b]] (int32 [B][P], ascending) of the n_drafts rows behind
+        each request's own (dak_kv_commit). Returns the new seq_lens."""
+        self._several_new = True
+        return _lib.dak_kv_commit(self.placement, seq_lens, path, n_path, n_drafts, n_new=n_new, slot_pos=self.slot_pos,
+                                  acc=self.weights)
+
+    def fork(self, src_of, seq_lens, first=None, source: "SplitK_FlashAttn" = None, lens=None):
+        """Request b goes on from rows first[b] (None: 0) on of request src_of[b] (negative: b stays as it is), of
+        this cache or of another module's (dak_kv_fork); seq_lens are the lengths there. With source,
+        lens are this cache's. A tracked cache takes positions and weights too. Returns the new lengths
+        of this cache."""
+        self._several_new = True
+        kw = dict(first=first, slot_pos=self.slot_pos, acc=self.weights)
+        if source is None:
+            if lens is not None:
+                raise ValueError("lens is for a fork from another module")
+            return _lib.dak_kv_fork(self.placement, src_of, seq_lens, **kw)
+        if lens is None:
+            raise ValueError("a fork from another module needs this cache's lens")
+        if self.slot_pos is not None:
+            if source.slot_pos is None:
+                raise ValueError("a tracked cache forks from a tracked one")
+            kw.update(source_slot_pos=source.slot_pos, source_acc=source.weights)
+        return _lib.dak_kv_fork(self.placement, src_of, seq_lens, source=source.placement, lens_out=lens.clone(), **kw)
 
     def _serve(self, q, seq_lens, scale, prefix, prefix_of, prefix_lens):
         # whether the kernel before writes the cache is not known here: no programmatic launch
