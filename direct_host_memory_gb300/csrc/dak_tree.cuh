@@ -74,10 +74,13 @@ __device__ __forceinline__ TreeRequest tree_request(const TreeParams& p, int b) 
     return tree_request(p, min(max(p.lens[b], 0), p.L), min(max(n, 0), p.T));
 }
 
-// n / d for quotients below 2^21 (the float quotient is off by less than one, which the remainder puts
-// right): an integer division is dozens of instructions that run for the first time.
+// n / d for n below 2^31: the float quotient is off by at most 2^-22 of itself, 2^9; what the remainder says of
+// that (off by less than one) is added, and the remainder then puts the last step right. (An integer
+// division is dozens of instructions that run for the first time.)
 __device__ __forceinline__ unsigned tree_quotient(unsigned n, unsigned d) {
-    const unsigned q = static_cast<unsigned>(static_cast<float>(n) * __fdividef(1.f, static_cast<float>(d)));
+    const float inv = __fdividef(1.f, static_cast<float>(d));
+    unsigned q = static_cast<unsigned>(static_cast<float>(n) * inv);
+    q += static_cast<int>(static_cast<float>(static_cast<int>(n - q * d)) * inv);
     const int r = static_cast<int>(n - q * d);
     return q + (r >= static_cast<int>(d)) - (r < 0);
 }

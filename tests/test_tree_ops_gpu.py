@@ -177,17 +177,18 @@ def test_attn_tree_nan_in_the_cache_is_kept(dak):
             assert torch.isnan(o[:, :, :2]).all() and torch.isfinite(o[:, :, 2:]).all()
 
 
-def test_attn_tree_does_not_depend_on_the_tiers(dak):
+@pytest.mark.parametrize("T,fp32", [(11, False), (11, True), (3, False), (8, True), (140, False)])
+def test_attn_tree_does_not_depend_on_the_tiers(dak, T, fp32):
     import torch
-    B, T, Hq, Hkv, D, L = 6, 11, 8, 4, 128, 1500
+    B, Hq, Hkv, D, L = 6, 8, 4, 128, 1500
     q, k, v = _inputs(9, B, T, Hq, Hkv, D, L)
-    lens = _i32([1489, 3, 800, 0, 64, 1111])
+    lens = _i32([L - T, 3, 800, 0, 64, 1111])
     mask = _mask_dev(_bits(np.random.default_rng(2), "tree", B, T))
     want = None
     for host in (0, 1, 7, 13, 24):
         for tun in (None, dict(host_ctas=3, window=2, hbm_window=1), dict(host_ctas=1)):
             kv = dak.dak_place_kv_heads(k, v, host)
-            o = dak.dak_attn_tree(to_dev(q), kv, lens, mask=mask, tuning=tun)
+            o = dak.dak_attn_tree(to_dev(q), kv, lens, mask=mask, tuning=tun, o_fp32=fp32)
             _ok(dak)
             want = o if want is None else want
             assert torch.equal(o, want), (host, tun)
@@ -242,6 +243,49 @@ def test_attn_tree_captured_on_another_stream(dak):
         ref, spread, reach = ot.attention(q, k, v, new, mask.cpu().numpy())
         for o in outs:
             _check_attn(o, ref, spread, reach, D, L, False)
+
+
+def test_attn_tree_alignment_and_unused_rows(dak):
+    """An O that is 16-byte aligned but not 32, and a workspace likewise; nothing around them is written."""
+    import torch
+    for T, Hq, Hkv, fp32 in ((20, 8, 2, False), (20, 8, 2, True), (3, 4, 2, False), (40, 16, 2, False)):
+        B, D, L = 3, 64, 1700
+        q, k, v = _inputs(T, B, T, Hq, Hkv, D, L)
+        lens, n_new = _i32([L - T, 900, 0]), _i32([T, T - 2, 1])
+        kv = dak.dak_place_kv_heads(k, v, 2)
+        dtype, item = (torch.float32, 4) if fp32 else (torch.bfloat16, 2)
+        need = dak.dak_attn_tree_workspace_bytes(kv, T, Hq)
+        n = B * T * Hq * D
+        got = []
+        for shift in (0, 16):
+            buf = torch.full((n + 64,), 7.0, dtype=dtype, device="cuda")
+            ws = torch.full((need + 64,), 3, dtype=torch.uint8, device="cuda")
+            o = buf[shift // item:shift // item + n].view(B, T, Hq, D)
+            dak.dak_attn_tree(to_dev(q), kv, lens, n_new=n_new, O=o, o_fp32=fp32, workspace=ws[shift:shift + need])
+            _ok(dak)
+            assert (buf[:shift // item] == 7).all() and (buf[shift // item + n:] == 7).all()
+            assert (ws[:shift] == 3).all() and (ws[shift + need:] == 3).all()
+            assert (o[1, T - 2:] == 7).all() and (o[2, 1:] == 7).all()
+            got.append(o.clone())
+        assert torch.equal(got[0], got[1])
+
+
+def test_attn_tree_without_a_tensor_map(dak):
+    """A tensor map that cannot be encoded is an error, and nothing is written."""
+    import torch
+    kv = dak.dak_place_kv_heads(*_inputs(1, 2, 9, 4, 2, 64, 50)[1:], 0)
+    q, lens = torch.ones(2, 9, 4, 64, dtype=torch.bfloat16, device="cuda"), _i32([1, 2])
+    o = torch.full_like(q, 7.0)
+    for skip in (0, 1):
+        dak.dak_inject_fault(dak.FAULT_TENSOR_MAP, 1, skip)
+        with pytest.raises(dak.DakError) as e:
+            dak.dak_attn_tree(q, kv, lens, O=o)
+        assert e.value.status == 5 and dak.dak_fault_pending(dak.FAULT_TENSOR_MAP) == 0
+    torch.cuda.synchronize()
+    assert (o == 7).all()
+    dak.dak_attn_tree(q, kv, lens, O=o)
+    _ok(dak)
+    assert not (o == 7).any()
 
 
 def test_attn_tree_arguments(dak):
