@@ -39,14 +39,15 @@ struct CommitParams {
     DevStatus* st;
 };
 
-constexpr int kCommitThreads = 128;
+constexpr int kCommitThreads = 64;
 
 // One block per slab, a thread per 16-byte piece of up to eight rows of K or V. A path ascends, so that
 // path[i] >= i: no row is written before the rows after it in the path have been read, if every
 // group of rows is read whole before it is written, and groups are taken in order. What a block waits
-// for are two loads one after the other, the path and the rows; with 128 threads all slabs of a wide
-// batch are there at once (256 requests of 8 kv heads, up to 48 of 64 drafts, tables: 17.4 us with
-// blocks of 256 and the tables behind the rows).
+// for are loads one after the other, the path and then the rows, which more slabs at once cover: with 64
+// threads 18 blocks fit an SM (256 requests of 8 kv heads, up to 48 of 64 drafts, tables: 12.1 us, 50 MB
+// of rows read and written in 7.4 at the copy rate; 13.3 with 128 threads, 17.4 with 256 and the tables behind
+// the rows; four rows a thread 13.4).
 template <int D>
 __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitParams p) {
     constexpr int PIECES = 2 * (D / 8);                // of a row's K and V
