@@ -333,15 +333,18 @@ static int fork_plan_bytes(int B, int src_B) {
 
 template <int D>
 static cudaError_t launch_fork(ForkParams& p, cudaStream_t s) {
-    // two CTAs an SM, or one where the lists take more room
-    constexpr int kTwo = 110 * 1024, kOne = 220 * 1024;
+    // Three CTAs an SM, or two or one where the lists take more room (16 beams of 8 kv heads over 850 rows 7.4 us with
+    // three, 8.6 with two; 16 samples of two prompts over 7K 91, 95, with four 98; any of 61 requests over up
+    // to 3000 tracked rows 34.8, 35.5, 34.5).
+    constexpr int kMost = 3, kRoom[kMost] = {220 * 1024, 110 * 1024, 73 * 1024};  // by CTAs an SM, from one on
     const int plan = fork_plan_bytes(p.B, p.src_B);
     const int least = std::max(16 * 1024, 16 * p.src_B);
-    const int per_sm = plan + 2 * least <= kTwo ? 2 : 1;
-    p.stage = ((per_sm == 2 ? kTwo : kOne) - plan) / 2 / 128 * 128;
+    int per_sm = kMost;
+    while (per_sm > 1 && plan + 2 * least > kRoom[per_sm - 1]) --per_sm;
+    p.stage = (kRoom[per_sm - 1] - plan) / 2 / 128 * 128;
     const int smem = 2 * p.stage + plan;
     static SmemLimit limit;
-    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(fork_kernel<D>), kOne);
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(fork_kernel<D>), kRoom[0]);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
