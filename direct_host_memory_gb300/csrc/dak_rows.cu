@@ -164,7 +164,10 @@ struct __align__(16) ForkStretch {
 // for all sources) of one chunk and kv head: it is read from every source, and once all have arrived
 // written to every taker. No other unit reads or writes these bytes of any request, so that any map can
 // be taken in place, and a source is read once however many take from it. Two buffers: a unit's bytes
-// are on their way while the one before is written.
+// are on their way while the one before is written. What bounds it: bytes (16 samples of two prompts over 7K:
+// 560 MB, 92.5 us, 81 at the copy rate); with many requests of many lengths the lists (about 4 us) and
+// units of few pieces (any of 61 over up to 3000 tracked rows 34.8 us, 22 at the copy rate, 3 of them for
+// the tables; all of 3001 rows 57.5, 45); a few beams the lists, one unit's way in and out: 7.2 us.
 template <int D>
 __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) {
     extern __shared__ __align__(128) uint8_t smem[];

@@ -1,14 +1,24 @@
 // Decode attention of a tree (or chain) of drafted tokens per request over a placed KV cache,
 // dak_attn_tree: o[b,t,h] = softmax(scale q[b,t,h] K^T) V over the rows before the drafts and those
-// drafts that the token's mask names. The tokens' query heads of one kv head are the rows of a tile, as many whole tokens as fit in
-// each 128-row half of it, so that the cache, which dak_attn streams once per token, is streamed
-// once for all of them; 64 keys a step on the tcgen05 tensor cores, as in the prefix pass, whose
-// comment says how (dak_prefix.cu; what both use: dak_umma_attn.cuh).
-// How work is cut: dak_tree.cuh.
+// drafts that the token's mask names. The tokens' query heads of one kv head are the rows of a tile, as
+// many whole tokens as fit in each 128-row half of it, so that the cache, which dak_attn streams once
+// per token, is streamed once for all of them; 64 keys a step on the tcgen05 tensor cores, as in the
+// prefix pass, whose comment says how (dak_prefix.cu; what both use: dak_umma_attn.cuh).
+// How work is cut: dak_tree.cuh. Up to 16 rows a kv head go to dak_tree_few.cu.
 //
-// Nothing waits at a tile's end but for what it needs: copies run ahead, up to what the ring holds; the
-// next tile's Q is fetched when the last product that reads the old one is done, and its first scores are
-// computed while the results, straight from TMEM, are on their way out.
+// A row is two threads', of a step's keys and of O's columns a half each, so that a sub-partition has four
+// softmax warps to cover the latencies of S, exp2 and P. Nothing waits at a tile's end but for what it
+// needs: copies run ahead, up to what the ring holds; the next tile's Q is fetched when the last product that
+// reads the old one is done, and its first scores are computed while the results, straight from TMEM, are
+// on their way out. (48 requests of 64 drafts and 64 heads over 2K 230 us with both, 250 with a thread a row
+// and Q, scores and results one after the other.)
+//
+// What bounds it: with a half tile the cache's bytes (32 requests of 16 drafts and 32/8 heads over 7K to 8K:
+// 157 us, 148 at the copy rate; 32 rows 151, 128 rows 169). With two halves the tensor cores, which P in two
+// bf16 parts keeps busy for half as long again: those 48 requests 224 us, of which 13 are the merge, the
+// two products 85 at the rate of a large matrix product, 127 with the second part; the pipe is active 60% of
+// the time, and the rest is the chain from S to P.V that two streams do not cover. Small calls the start, the
+// first chunks and the merge's launch (one request of 8 drafts over 4K: 13.5 us, the merge 4.4 of them).
 #include <algorithm>
 #include <cmath>
 
@@ -17,7 +27,7 @@
 
 namespace dak {
 
-constexpr int kTreeSoftmax = 2 * 2 * 128;         // two streams, two threads a row: of a step's keys and of O's columns a half each
+constexpr int kTreeSoftmax = 2 * 2 * 128;            // two streams, two threads a row
 constexpr int kTreeThreads = kTreeSoftmax + 4 * 32;  // and copies, scores, each stream's P.V
 constexpr int kTreeHostCtas = 32;
 constexpr int kTreeMergeRows = 8;                 // a warp each
@@ -47,8 +57,8 @@ __device__ __forceinline__ bool pair_any(int id, bool mine) {
 
 // softmax_step (dak_umma_attn.cuh) for the 32 of a row's 64 scores that begin at column 32 * half of s_addr;
 // another warp has the others. (counts: the row is one; what else lies in a tile must not move references.)
-// Both go by one reference: where a row outgrows it in either, which
-// pair_any finds, they tell each other their maxima (`other`, from its maximum the partner's).
+// Both go by one reference: where a row outgrows it in either, which pair_any finds, they tell each other
+// their maxima (`other`, from its maximum the partner's).
 template <int PARTS, class Hidden, class Other, class Grown>
 __device__ __forceinline__ void softmax_half(uint32_t s_addr, int half, int pair, const Hidden& hidden, float scale_log2,
                                              float& m_ref, float& l, bool first, bool counts, const Other& other,
@@ -642,7 +652,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
 // Block (r, y): eight rows, a warp each, of the tile that begins in range r and ends in a later one:
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over its pieces, in order.
 // What it waits for are loads: the first pieces, which every such tile has, are asked for before it is known
-// whether there is one.
+// whether there is one. 4.4 us of one request's 13.5, most of them the launch and two loads one after the
+// other; 5 of 157 for 32 rows a kv head of 32 requests, 13 of 224 for 512 rows of 48 (31 MB of partials).
 template <int D>
 __global__ void __launch_bounds__(32 * kTreeMergeRows) tree_merge_kernel(const __grid_constant__ TreeParams p) {
     constexpr int LANES = D / 4, AT_ONCE = 32 / LANES;  // pieces that a warp reads at once

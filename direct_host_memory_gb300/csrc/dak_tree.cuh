@@ -257,8 +257,9 @@ __device__ __forceinline__ void tree_report(const TreeParams& p, const TreeWalk&
     }
 }
 
-// Query rows a kv head that tree_few_kernel takes, at most (32 chats over 7K to 8K, 8 kv heads of 128: 16 rows
-// 150 us there, 48 155 by tree_kernel; 24 or 32 there 330, their O^T out of registers).
+// Query rows a kv head that tree_few_kernel takes, at most (32 requests over 7K to 8K, 8 kv heads of 128: 16 rows
+// 150 us there, 32 rows 149 by tree_kernel; 24 or 32 there 330, their O^T out of registers; one request over 4K,
+// heads of 64: 16 rows 10.2 us there, 32 12.2 by tree_kernel).
 constexpr int kTreeFewRows = 16;
 // Ranges (CTAs) of tree_few_kernel on this device, and its launch; the merge is the caller's.
 int tree_few_ctas(int rows);
