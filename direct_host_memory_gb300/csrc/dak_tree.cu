@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             const unsigned xs = r * plan.len, xe = xs + plan.len;
             if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
-                const int c0 = w.cut(p, xs, plan.len), c1 = w.cut(p, xe, plan.len);
+                const int c0 = w.cut(p, plan, xs), c1 = w.cut(p, plan, xe);
                 if (lane == 0) {
                     const long long slab = static_cast<long long>(w.b) * p.Hkv + w.g;
                     const int tier = slab < p.h_s ? 0 : 1, window = p.in_flight[tier];
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             const unsigned xs = r * plan.len, xe = xs + plan.len;
             if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
-                const int steps = w.cut(p, xe, plan.len) - w.cut(p, xs, plan.len);
+                const int steps = w.cut(p, plan, xe) - w.cut(p, plan, xs);
                 if (steps <= 0) continue;
                 const bool two = w.two();
                 // Q, when the scores that read the last tile's are there: those of a tile of two halves are the
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             const unsigned xs = r * plan.len, xe = xs + plan.len;
             if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
-                const int steps = w.cut(p, xe, plan.len) - w.cut(p, xs, plan.len);
+                const int steps = w.cut(p, plan, xe) - w.cut(p, plan, xs);
                 if (steps <= 0) continue;
                 const bool two = w.two();
                 const int stride = two ? 1 : 2, first = two ? 0 : st, mine = first < steps ? (steps - first + stride - 1) / stride : 0;
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             const unsigned xs = r * plan.len, xe = xs + plan.len;
             if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe; w.next(p, plan)) {
-                const int c0 = w.cut(p, xs, plan.len), c1 = w.cut(p, xe, plan.len), steps = c1 - c0;
+                const int c0 = w.cut(p, plan, xs), c1 = w.cut(p, plan, xe), steps = c1 - c0;
                 if (steps <= 0) continue;
                 const bool two = w.two();
                 const int token0 = (2 * w.tile + (two ? st : 0)) * p.mpt, t = token0 + token_in;
@@ -745,11 +745,19 @@ __global__ void __launch_bounds__(32 * kTreeMergeRows) tree_merge_kernel(const _
 // 4, 20.4 of 2.
 constexpr unsigned kTreeTileCost = 6, kTreeMinRange = 9;        // of tree_kernel
 constexpr unsigned kTreeFewTileCost = 4, kTreeFewMinRange = 8;  // of tree_few_kernel
+// Tiles that cost no more than this when the cache is full are never cut, and there is no merge (32 drafts of 4
+// heads and 4 kv heads, 16 requests over 380 rows: 13.3 us, 19.6 cut; one request of 8 drafts over 380 rows 10.3 and 12.4, over
+// 510 11.5 and 11.6; few: one of 4 drafts over 250 rows 10.4 and 12.0, over 380 12.2 and 11.3).
+constexpr unsigned kTreeWhole = 24, kTreeFewWhole = 15;
+// Larger ones stay whole where that makes the longest range no more than this longer (32 requests of 64 drafts,
+// 32/8 heads, 760 rows: 52.9 us, 63.4 cut; few, 64 of 4 over 380 rows 30.8, 33.3 cut).
+constexpr unsigned kTreeSlack = 16, kTreeFewSlack = 6;
 
 struct TreeLayout {
     bool few;
     int ranges, part_rows;
-    unsigned tile_cost, min_range;
+    unsigned tile_cost, min_range, slack;
+    bool whole;  // no tile is ever cut
     size_t o_part, ml_part, heads;
     size_t total() const { return 16 + o_part + ml_part + heads; }  // the partials begin on 32 bytes
 };
@@ -764,6 +772,9 @@ static TreeLayout tree_layout(const dak_placement* KV, int T, int H_q) {
     x.tile_cost = x.few ? kTreeFewTileCost : kTreeTileCost;
     x.min_range = x.few ? kTreeFewMinRange : kTreeMinRange;
     const int64_t chunks = (KV->L + 63) / 64, halves = (T + mpt - 1) / mpt;
+    x.whole = x.tile_cost + (halves > 1 ? kTreeTwoCost : kTreeOneCost) * chunks <= (x.few ? kTreeFewWhole : kTreeWhole);
+    if (x.whole) x.min_range = x.tile_cost + kTreeOneCost;  // of one chunk: a range each
+    x.slack = x.whole ? 0x40000000u : x.few ? kTreeFewSlack : kTreeSlack;
     const int64_t slab = (halves / 2) * (x.tile_cost + kTreeTwoCost * chunks) + halves % 2 * (x.tile_cost + kTreeOneCost * chunks);
     const int64_t least = (slab * KV->B * KV->H_kv + x.min_range - 1) / x.min_range;
     const int ctas = x.few ? tree_few_ctas(T * G) : device_sm_count();
@@ -816,7 +827,6 @@ static cudaError_t launch_tree(const TreeParams& p, const TreeMaps& maps, cudaSt
 }
 
 static cudaError_t launch_tree_merge(const TreeParams& p, int D, cudaStream_t s) {
-    if (p.ranges == 1) return cudaSuccess;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -893,6 +903,7 @@ extern "C" dak_status dak_attn_tree(const void* Q, const dak_placement* KV, cons
     p.ranges = x.ranges;
     p.tile_cost = x.tile_cost;
     p.min_range = x.min_range;
+    p.slack = x.slack;
     p.slab_chunks = (KV->L + 63) / 64;
     p.host_ctas = std::min(x.ranges, tuning && tuning->host_ctas > 0 ? tuning->host_ctas : kTreeHostCtas);
     p.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D))) * 1.4426950408889634f;
@@ -919,5 +930,6 @@ extern "C" dak_status dak_attn_tree(const void* Q, const dak_placement* KV, cons
         e = D == 128 ? (o_fp32 ? launch_tree<128, true>(p, maps, s) : launch_tree<128, false>(p, maps, s))
                      : (o_fp32 ? launch_tree<64, true>(p, maps, s) : launch_tree<64, false>(p, maps, s));
     }
+    if (x.whole || x.ranges == 1) return cuda_status(e);
     return cuda_status(e == cudaSuccess ? launch_tree_merge(p, D, s) : e);
 }

@@ -3,9 +3,10 @@
 // captured call follows them: the chunks of all (request, kv head, 256-row tile) lie on one line,
 // request-major, each with its cost, and the line is cut into equal ranges, a CTA each. A tile cut by
 // no range's end is finished where it is; the others leave partial results (at most two a range, whatever
-// the batch) to a merge (dak_tree.cu), which takes those of a tile in order. The cuts go by lengths and SM
-// count alone, so that results do not depend on the tiers: the host's slabs are the line's beginning,
-// and where its ranges are more CTAs than may read the host at once, those take several each.
+// the batch) to a merge (dak_tree.cu), which takes those of a tile in order. Where tiles are short they are
+// not cut, but belong to the range with their middle. The cuts go by lengths and SM count alone, so that
+// results do not depend on the tiers: the host's slabs are the line's beginning, and where its ranges are
+// more CTAs than may read the host at once, those take several each.
 #pragma once
 #include "dak_device.cuh"
 
@@ -41,6 +42,7 @@ struct TreeParams {
     int part_rows;  // of a tile's partials: half * 128 + row in it, at most
     int wide;       // O is 32-byte aligned
     int ranges, host_ctas, slab_chunks;
+    unsigned slack;  // how much longer the longest range may be for whole tiles (tree_plan)
     unsigned tile_cost, min_range;  // of a tile by itself (rows' way in, first chunk's latency, results' way out); of a range, at least
     int in_flight[2];  // copies of a CTA that have not landed, by tier
     float scale_log2;
@@ -87,6 +89,7 @@ __device__ __forceinline__ unsigned tree_quotient(unsigned n, unsigned d) {
 
 struct TreePlan {
     unsigned len;                // of a range
+    bool whole;                  // ranges take whole tiles, those whose middles lie in them
     int ranges, host_ranges;     // host_ranges: those that touch the host's slabs
     // the first 32 requests, a lane each, which a warp finds without loads:
     TreeRequest own;
@@ -107,21 +110,30 @@ __device__ __forceinline__ TreePlan tree_plan(const TreeParams& p) {
         if (lane >= o) x.own_end += v;
     }
     unsigned total = __shfl_sync(all, x.own_end, 31), host = 0;
+    const auto largest = [](const TreeRequest& q) { return q.tiles == 0 ? 0u : q.twos > 0 ? q.two : q.one; };  // of its tiles
+    unsigned tile = lane < p.B ? largest(x.own) : 0u;
     const auto host_part = [&](int b, unsigned slab) { return b < bh ? slab * p.Hkv : b == bh ? slab * (p.h_s - bh * p.Hkv) : 0u; };
     if (p.h_s > 0) host = host_part(lane, x.own.slab);
     if (p.B > 32) {
         unsigned more = 0;
 #pragma unroll 1
         for (int b = 32 + lane; b < p.B; b += 32) {
-            const unsigned slab = tree_request(p, b).slab;
-            more += slab * p.Hkv;
-            host += host_part(b, slab);
+            const TreeRequest q = tree_request(p, b);
+            more += q.slab * p.Hkv;
+            host += host_part(b, q.slab);
+            tile = max(tile, largest(q));
         }
         total += __reduce_add_sync(all, more);
     }
     if (p.h_s > 0) host = __reduce_add_sync(all, host);
-    x.len = max(tree_quotient(total + p.ranges - 1, p.ranges), p.min_range);
+    tile = max(__reduce_max_sync(all, tile), 1u);
+    x.len = max(tree_quotient(total + p.ranges - 1, p.ranges), min(p.min_range, tile));
     x.ranges = static_cast<int>(tree_quotient(total + x.len - 1, x.len));
+    // The longest range of whole tiles is about len rounded up to largest ones: where that costs less than what
+    // cutting does (a cut tile's second start, its partial results, the merge), no tile is cut.
+    unsigned most = tree_quotient(x.len, tile) * tile;
+    if (most < x.len) most += tile;
+    x.whole = most <= x.len + p.slack;
     x.host_ranges = static_cast<int>(tree_quotient(host + x.len - 1, x.len));
     return x;
 }
@@ -192,12 +204,13 @@ struct TreeWalk {
         }
     }
     // The first chunk that does not belong to the ranges before position x.
-    __device__ __forceinline__ int cut(const TreeParams& p, unsigned x, unsigned range_len) const {
+    __device__ __forceinline__ int cut(const TreeParams& p, const TreePlan& plan, unsigned x) const {
         if (x <= at) return 0;
         if (x >= end()) return q.chunks;
+        if (plan.whole) return 2 * (x - at) <= end() - at ? 0 : q.chunks;
         const unsigned in = max(x - at, p.tile_cost) - p.tile_cost;
         const int t = static_cast<int>(two() ? (in + kTreeTwoCost - 1) / kTreeTwoCost : (in + kTreeOneCost - 1) / kTreeOneCost);
-        const int least = range_len >= kTreeSnapRange ? 2 : 1;
+        const int least = plan.len >= kTreeSnapRange ? 2 : 1;
         return t < least ? 0 : q.chunks - t < least ? q.chunks : t;
     }
 };
@@ -246,7 +259,7 @@ __device__ __forceinline__ TreeTurn tree_turn(const TreeParams& p, const TreePla
 __device__ __forceinline__ void tree_head(const TreeParams& p, const TreePlan& plan, const TreeWalk& w, int r, int c0, int c1) {
     if (c0 > 0 || c1 == w.q.chunks) return;
     int last = static_cast<int>(tree_quotient(w.end() - 1, plan.len));  // the range with the tile's last chunk
-    while (w.cut(p, last * plan.len, plan.len) == w.q.chunks) --last;
+    while (w.cut(p, plan, last * plan.len) == w.q.chunks) --last;
     p.heads[r] = TreeHead{w.b, w.g, w.tile, last - r + 1, w.q.n, w.q.len, w.q.keys, 0};
 }
 

@@ -8,7 +8,7 @@
 //
 // What bounds it: the cache's bytes (32 requests of 4 drafts and 32/8 heads of 128 over 7K to 8K 150 us, 145 at
 // the copy rate; heads of 64 81 us, 73). Small calls the latency of the start, the first chunks, the warps' merge
-// and the pieces': one request over 4K 14 us, 12 of 16/16 heads of 64 over up to 2.5K, fp32 output, 17 us (8.6). More
+// and the pieces': one request over 4K 14 us, over 5 rows 7, 12 of 16/16 heads of 64 over up to 2.5K, fp32 output, 17 us (8.6). More
 // rows than 16 spill O^T and Q, of which five warps and two CTAs an SM leave 168 registers a thread: 24 rows of
 // heads of 64 102 us in that batch and 13.5 for one request (121 and 12.2 by tree_kernel), 32 rows 157 and 17.6.
 #include <algorithm>
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
             const unsigned xs = r * plan.len, xe = xs + plan.len;
             if (r > turn.first) w.find(p, plan, xs);
             for (; w.b < p.B && w.at < xe && ok; w.next(p, plan)) {
-                const int c0 = w.cut(p, xs, plan.len), c1 = w.cut(p, xe, plan.len);
+                const int c0 = w.cut(p, plan, xs), c1 = w.cut(p, plan, xe);
                 if (lane == 0) {
                     const long long slab = static_cast<long long>(w.b) * p.Hkv + w.g;
                     const int tier = slab < p.h_s ? 0 : 1, window = p.in_flight[tier];
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
         const unsigned xs = r * plan.len, xe = xs + plan.len;
         if (r > turn.first) w.find(p, plan, xs);
         for (; w.b < p.B && w.at < xe; w.next(p, plan)) {
-            const int c0 = w.cut(p, xs, plan.len), c1 = w.cut(p, xe, plan.len), rows = w.q.n * p.G;
+            const int c0 = w.cut(p, plan, xs), c1 = w.cut(p, plan, xe), rows = w.q.n * p.G;
             if (c0 >= c1) continue;
             // row r of this kv head: token r / G, head r % G of the request
             const auto row_at = [&](int row) {
