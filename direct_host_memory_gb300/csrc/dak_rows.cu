@@ -39,7 +39,6 @@ struct CommitParams {
     DevStatus* st;
 };
 
-constexpr int kCommitThreads = 64;
 
 // One block per slab, a thread per 16-byte piece of up to eight rows of K or V. A path ascends, so that
 // path[i] >= i: no row is written before the rows after it in the path have been read, if every
@@ -47,13 +46,15 @@ constexpr int kCommitThreads = 64;
 // for are loads one after the other, the path and then the rows, which more slabs at once cover: with 64
 // threads 18 blocks fit an SM (256 requests of 8 kv heads, up to 48 of 64 drafts, tables: 12.1 us, 50 MB
 // of rows read and written in 7.4 at the copy rate; 13.3 with 128 threads, 17.4 with 256 and the tables behind
-// the rows; four rows a thread 13.4).
-template <int D>
-__global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitParams p) {
+// the rows; four rows a thread 13.4). Where slabs are few enough for blocks of 256 to be there at once, and
+// paths long, those have fewer groups to take one after the other (up to 83 of 88 drafts of one request and 2 kv
+// heads 3.1 us, 7.9 with 64 threads).
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) commit_kernel(const CommitParams p) {
     constexpr int PIECES = 2 * (D / 8);                // of a row's K and V
-    constexpr int LANES = kCommitThreads / PIECES;     // rows side by side
+    constexpr int LANES = THREADS / PIECES;     // rows side by side
     constexpr int PER = 8;
-    constexpr int MORE = (DAK_MAX_TREE + kCommitThreads - 1) / kCommitThreads;  // drafts of a thread
+    constexpr int MORE = (DAK_MAX_TREE + THREADS - 1) / THREADS;  // drafts of a thread
     __shared__ int path[DAK_MAX_TREE];
     const int tid = threadIdx.x, b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv;
     const long long slab = blockIdx.x;
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitPara
     int v[MORE], before[MORE];
 #pragma unroll
     for (int k = 0; k < MORE; ++k) {
-        const int i = tid + k * kCommitThreads;
+        const int i = tid + k * THREADS;
         v[k] = i < p.P ? in[i] : 0;
         before[k] = i > 0 && i < p.P ? in[i - 1] : -1;
     }
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitPara
     bool good = true;
 #pragma unroll
     for (int k = 0; k < MORE; ++k) {
-        const int i = tid + k * kCommitThreads;
+        const int i = tid + k * THREADS;
         if (i >= n) continue;
         path[i] = v[k];
         good = good && v[k] >= 0 && v[k] > before[k] && v[k] < drafts;
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitPara
     float av[MORE];
 #pragma unroll
     for (int k = 0; k < MORE; ++k) {
-        const int i = tid + k * kCommitThreads;
+        const int i = tid + k * THREADS;
         pv[k] = pos && i < n ? pos[path[i]] : -1;
         av[k] = acc && i < n ? acc[path[i]] : 0.f;
     }
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitPara
     __syncthreads();  // entries are all read
 #pragma unroll
     for (int k = 0; k < MORE; ++k) {
-        const int i = tid + k * kCommitThreads;
+        const int i = tid + k * THREADS;
         if (i >= drafts) continue;
         if (pos) pos[i] = pv[k];
         if (acc) acc[i] = av[k];
@@ -242,9 +243,12 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
     constexpr int kHalf = 64 * kRow;     // of a chunk's K or V
     int unit = kHalf;
     while (unit > 16 && unit * sources > p.stage) unit >>= 1;
+    const long long halves = (((highest + 63) >> 6) - (lowest >> 6)) * 2ll * p.Hkv;
+    // smaller ones where the SMs would not all have one (62 requests from one of 560 rows, 2 kv heads: 9.6 us, 24.2)
+    while (unit > 512 && halves * (kHalf / unit) < gridDim.x) unit >>= 1;
     const int shift = 31 - __clz(unit >> 4);  // pieces of 16 bytes of a unit: 1 << shift
-    const int subs = kHalf / unit, sub_shift = 31 - __clz(subs), c0 = lowest >> 6, chunks = ((highest + 63) >> 6) - c0;
-    const long long n_units = (static_cast<long long>(chunks) * p.Hkv << sub_shift) * 2;
+    const int subs = kHalf / unit, sub_shift = 31 - __clz(subs), c0 = lowest >> 6;
+    const long long n_units = halves << sub_shift;
     // Unit x, stretches of one slab side by side: kv head, offset in the slab, and the rows lo .. n - 1 of
     // one request as pieces of it.
     const auto stretch = [&](long long x, const Tiers& tiers, int request, int lo, int n, int from) {
@@ -403,16 +407,23 @@ extern "C" dak_status dak_kv_commit(const dak_placement* KV, const int* seq_lens
     p.L = KV->L;
     p.st = status_ptr();
     if (!p.st) return DAK_ERR_CUDA;
+    const int64_t slabs = static_cast<int64_t>(KV->B) * KV->H_kv;
+    const bool wide = P > 16 && slabs <= 4 * device_sm_count();  // wide blocks of all slabs are there at once
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(KV->B) * KV->H_kv);
-    cfg.blockDim = dim3(kCommitThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(slabs));
+    cfg.blockDim = dim3(wide ? 256 : 64);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cuda_status(KV->D == 128 ? cudaLaunchKernelEx(&cfg, commit_kernel<128>, p) : cudaLaunchKernelEx(&cfg, commit_kernel<64>, p));
+    if (wide) {
+        return cuda_status(KV->D == 128 ? cudaLaunchKernelEx(&cfg, commit_kernel<128, 256>, p)
+                                        : cudaLaunchKernelEx(&cfg, commit_kernel<64, 256>, p));
+    }
+    return cuda_status(KV->D == 128 ? cudaLaunchKernelEx(&cfg, commit_kernel<128, 64>, p)
+                                    : cudaLaunchKernelEx(&cfg, commit_kernel<64, 64>, p));
 }
 
 extern "C" dak_status dak_kv_fork(const dak_placement* KV, const dak_placement* src, const int* src_of, const int* seq_lens,
