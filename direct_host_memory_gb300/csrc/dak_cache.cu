@@ -42,6 +42,7 @@ struct RopeAxes {
 struct NoAxes {};
 
 constexpr int kRopeThreads = 128;
+constexpr int kRopeFewUnits = 96;  // three a thread of a warp
 
 template <bool F32>
 __device__ __forceinline__ float load_elem(const void* p, long long i) {
@@ -89,30 +90,35 @@ __device__ __forceinline__ uint4 pack8(const float* y) {
 // value heads two pieces side by side. Its inputs are asked for first; the position, its angles and
 // the table of cos and sin come under those loads. Position x turns modulo 2^64 is the angle as a
 // binary fraction of a turn, without a rounding (turns itself is good to f_i * 2^-55, so the angle to
-// 2^-35 turns at position 10^6 and 2^-24 at 2^31); its upper 32 bits, signed, are half-turns * 2^-31. Products and sums in fp32, one rounding to bf16 at the store. Memory bound: every element is
-// read and written once (8192 tokens of 32 query and 8 kv heads, D 128, bf16: 33.7 us, 5.4 TB/s; with a
-// thread a piece, and its pair's other half by a load of its own, 48 us); a few tokens are bound by the
-// launch (1 token 2.9 us, 256 tokens fp32 4.5 us). With positions of each token's own, on up to four axes
+// 2^-35 turns at position 10^6 and 2^-24 at 2^31); its upper 32 bits, signed, are half-turns * 2^-31.
+// Products and sums in fp32, one rounding to bf16 at the store. Memory bound: every element is read
+// and written once (8192 tokens of 32 query and 8 kv heads, D 128, bf16: 33.7 us, 5.4 TB/s; with a thread
+// a piece, and its pair's other half by a load of its own, 48 us); a few tokens are bound by the launch
+// (1 token 2.9 us, 256 tokens fp32 4.5 us). With positions of each token's own, on up to four axes
 // (Axes), a pair's position is a load by its axis, under the inputs' too: 8192 tokens of three axes 35.0 us,
-// 512 drafted tokens fp32 5.6.
-enum { kRopeSplit = 0, kRopeInterleaved = 1, kRopePart = 2 };  // PART: halves of a part of the head
+// 512 drafted tokens fp32 5.6. Many such tokens of few heads are blocks' latencies one after the other, of which
+// one-warp blocks have more at a time: 8000 tokens of 2 query heads and a kv head 12.2 us, 15.8 with 128 threads
+// (D 64: 8.4 and 14.6). Half a head that turns, 8 and 4 heads: 17.0 us by pieces, 31.1 element by element.
+enum { kRopeSplit = 0, kRopeInterleaved = 1, kRopePart = 2, kRopePieces = 3 };
+// Halves of a part of the head: PIECES where they are whole pieces, else PART.
 
-template <int D, bool F32, int KIND, class Axes>
-__global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8)
+template <int D, bool F32, int KIND, class Axes, int THREADS>
+__global__ void __launch_bounds__(THREADS, (F32 ? 6 : 8) * kRopeThreads / THREADS)
     append_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ Axes axes) {
     constexpr bool AXES = !std::is_same<Axes, NoAxes>::value;
     constexpr int PAIRS = D / 16;  // units of a head
+    constexpr int PAIRS_EACH = (D / 2 + THREADS - 1) / THREADS;  // entries of the table by a thread
     constexpr int PER = 3;         // units in flight per thread (a token of the 8B shape: all of them)
     __shared__ float2 cs[D / 2];
     const int b = blockIdx.x / p.T, t = blockIdx.x - b * p.T;
     const long long token = blockIdx.x;
     const int R = p.rope.rot_dim, half = R / 2;
-    const int heads = p.Hq + 2 * p.Hkv, n_units = heads * PAIRS, stride = gridDim.y * kRopeThreads;
+    const int heads = p.Hq + 2 * p.Hkv, n_units = heads * PAIRS, stride = gridDim.y * THREADS;
     grid_dep_wait();  // launched while the previous kernel ends
     const int n_new = p.n_new ? p.n_new[b] : p.T, slot = p.slots[b], first = !AXES && p.positions ? p.positions[b] : slot;
     bool ready = false, in_range = false;
     long long row = 0, pos = 0;
-    for (int u0 = blockIdx.y * kRopeThreads + threadIdx.x; u0 - static_cast<int>(threadIdx.x) < n_units; u0 += PER * stride) {
+    for (int u0 = blockIdx.y * THREADS + threadIdx.x; u0 - static_cast<int>(threadIdx.x) < n_units; u0 += PER * stride) {
         Piece<F32> raw[PER][2];
         // unit u: its head, where its pieces begin in it
         const auto place = [&](int u, int& h, int& e0, int& e1, bool& is_q, bool& is_v, int& g) {
@@ -121,9 +127,9 @@ __global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8)
             is_v = h >= p.Hq + p.Hkv;
             g = is_q ? h : is_v ? h - p.Hq - p.Hkv : h - p.Hq;
             const int c = u - h * PAIRS;
-            const bool apart = KIND == kRopeSplit && !is_v;
+            const bool apart = !is_v && (KIND == kRopeSplit || (KIND == kRopePieces && c * 8 < half));
             e0 = apart ? c * 8 : c * 16;
-            e1 = apart ? e0 + D / 2 : e0 + 8;
+            e1 = !apart ? e0 + 8 : e0 + (KIND == kRopeSplit ? D / 2 : half);
         };
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
@@ -141,19 +147,28 @@ __global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8)
             if (t >= n_new) return;
             row = static_cast<long long>(slot) + t;
             pos = static_cast<long long>(first) + t;
-            long long turning = pos;  // the position that this thread's pair turns by
+            long long turning[PAIRS_EACH];  // the positions that this thread's pairs turn by
+#pragma unroll
+            for (int k = 0; k < PAIRS_EACH; ++k) turning[k] = pos;
             if constexpr (AXES) {
                 const int* own = axes.positions + token * axes.n;
                 pos = own[0];
-                if (static_cast<int>(threadIdx.x) < half) turning = own[axes.axis[threadIdx.x]];
+#pragma unroll
+                for (int k = 0; k < PAIRS_EACH; ++k) {
+                    const int i = threadIdx.x + k * THREADS;
+                    if (i < half) turning[k] = own[axes.axis[i]];
+                }
             }
             in_range = row >= 0 && row < p.L;
-            if (static_cast<int>(threadIdx.x) < half) {
-                const uint64_t turn = static_cast<uint64_t>(turning) * p.rope.turns[threadIdx.x];
+#pragma unroll
+            for (int k = 0; k < PAIRS_EACH; ++k) {
+                const int i = threadIdx.x + k * THREADS;
+                if (i >= half) continue;
+                const uint64_t turn = static_cast<uint64_t>(turning[k]) * p.rope.turns[i];
                 const float a = static_cast<float>(static_cast<int>(static_cast<uint32_t>(turn >> 32))) * 0x1p-31f;
                 float s, c;
                 sincospif(a, &s, &c);
-                cs[threadIdx.x] = make_float2(c * p.rope.scale, s * p.rope.scale);
+                cs[i] = make_float2(c * p.rope.scale, s * p.rope.scale);
             }
             if (!in_range && blockIdx.y == 0 && threadIdx.x == 0) {
                 report(p.st, DAK_ERR_BOUNDS, 0xA9901000ull << 32 | static_cast<unsigned>(b));
@@ -180,6 +195,15 @@ __global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8)
                         const float a = x[i], c = x[8 + i];
                         x[i] = a * f.x - c * f.y;
                         x[8 + i] = c * f.x + a * f.y;
+                    }
+                } else if (KIND == kRopePieces) {  // rounded as in PART
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (e0 >= half) continue;
+                        const float2 f = cs[e0 + i];
+                        const float a = x[i], c = x[8 + i];
+                        x[i] = __fmaf_rn(a, f.x, __fmul_rn(-c, f.y));
+                        x[8 + i] = __fmaf_rn(c, f.x, __fmul_rn(a, f.y));
                     }
                 } else if (KIND == kRopeInterleaved) {
 #pragma unroll
@@ -224,20 +248,27 @@ __global__ void __launch_bounds__(kRopeThreads, F32 ? 6 : 8)
     }
 }
 
-template <int D, bool F32, class Axes>
+template <int D, bool F32, int THREADS, class Axes>
 static cudaError_t launch_append_rope(const RopeParams& p, const Axes& axes, dim3 grid, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kRopeThreads);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (p.rope.interleaved) return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopeInterleaved, Axes>, p, axes);
-    if (p.rope.rot_dim == D) return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopeSplit, Axes>, p, axes);
-    return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopePart, Axes>, p, axes);
+    if (p.rope.interleaved) return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopeInterleaved, Axes, THREADS>, p, axes);
+    if (p.rope.rot_dim == D) return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopeSplit, Axes, THREADS>, p, axes);
+    if (p.rope.rot_dim % 16 == 0) return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopePieces, Axes, THREADS>, p, axes);
+    return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, F32, kRopePart, Axes, THREADS>, p, axes);
+}
+
+template <int THREADS, class Axes>
+static cudaError_t launch_rope(const RopeParams& p, const Axes& a, int D, bool in_fp32, dim3 grid, cudaStream_t s) {
+    if (D == 128) return in_fp32 ? launch_append_rope<128, true, THREADS>(p, a, grid, s) : launch_append_rope<128, false, THREADS>(p, a, grid, s);
+    return in_fp32 ? launch_append_rope<64, true, THREADS>(p, a, grid, s) : launch_append_rope<64, false, THREADS>(p, a, grid, s);
 }
 
 // ------------------------------------------------------------------------------------
@@ -974,16 +1005,14 @@ static dak_status append_rope(const dak_placement* KV, const dak_rope_plan* rope
     const int64_t room = std::max<int64_t>(1, 8ll * device_sm_count() / tokens);
     const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(std::min<int64_t>(std::min(blocks, 16), room)));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const auto launch = [&](const auto& a) {
-        if (D == 128) return in_fp32 ? launch_append_rope<128, true>(p, a, grid, s) : launch_append_rope<128, false>(p, a, grid, s);
-        return in_fp32 ? launch_append_rope<64, true>(p, a, grid, s) : launch_append_rope<64, false>(p, a, grid, s);
-    };
-    if (!axes) return cuda_status(launch(NoAxes{}));
+    if (!axes) return cuda_status(launch_rope<kRopeThreads>(p, NoAxes{}, D, in_fp32, grid, s));
     RopeAxes a{};
     a.positions = positions;
     a.n = axes->n_axes;
     std::copy(axes->axis, axes->axis + 64, a.axis);
-    return cuda_status(launch(a));
+    // many tokens of few heads: one warp each
+    if (room == 1 && units <= kRopeFewUnits) return cuda_status(launch_rope<32>(p, a, D, in_fp32, grid, s));
+    return cuda_status(launch_rope<kRopeThreads>(p, a, D, in_fp32, grid, s));
 }
 
 // What dak_rope_axes_make makes, whose axes lie inside a token's positions.
