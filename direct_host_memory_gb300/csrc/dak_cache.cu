@@ -44,12 +44,6 @@ struct NoAxes {};
 constexpr int kRopeThreads = 128;
 constexpr int kRopeFewUnits = 96;  // three a thread of a warp
 
-template <bool F32>
-__device__ __forceinline__ float load_elem(const void* p, long long i) {
-    if (F32) return static_cast<const float*>(p)[i];
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
 // Eight consecutive elements at i as they lie in memory (16-byte aligned), and as fp32.
 template <bool F32>
 struct Piece;
@@ -63,6 +57,7 @@ struct Piece<false> {
         x[0] = bf_lo(v.x), x[1] = bf_hi(v.x), x[2] = bf_lo(v.y), x[3] = bf_hi(v.y);
         x[4] = bf_lo(v.z), x[5] = bf_hi(v.z), x[6] = bf_lo(v.w), x[7] = bf_hi(v.w);
     }
+    __device__ __forceinline__ void hold(uint32_t* to) const { to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w; }
 };
 template <>
 struct Piece<true> {
@@ -77,6 +72,10 @@ struct Piece<true> {
             x[4 * k] = __uint_as_float(v[k].x), x[4 * k + 1] = __uint_as_float(v[k].y);
             x[4 * k + 2] = __uint_as_float(v[k].z), x[4 * k + 3] = __uint_as_float(v[k].w);
         }
+    }
+    __device__ __forceinline__ void hold(uint32_t* to) const {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) to[4 * k] = v[k].x, to[4 * k + 1] = v[k].y, to[4 * k + 2] = v[k].z, to[4 * k + 3] = v[k].w;
     }
 };
 
@@ -98,7 +97,9 @@ __device__ __forceinline__ uint4 pack8(const float* y) {
 // (Axes), a pair's position is a load by its axis, under the inputs' too: 8192 tokens of three axes 35.0 us,
 // 512 drafted tokens fp32 5.6. Many such tokens of few heads are blocks' latencies one after the other, of which
 // one-warp blocks have more at a time: 8000 tokens of 2 query heads and a kv head 12.2 us, 15.8 with 128 threads
-// (D 64: 8.4 and 14.6). Half a head that turns, 8 and 4 heads: 17.0 us by pieces, 31.1 element by element.
+// (D 64: 8.4 and 14.6). Half a head that turns, 8 and 4 heads: 17.0 us by pieces, 31.1 element by element. What is
+// left to single elements (halves that are not whole pieces) is bound by their instructions: 8192 tokens of 32 and 8
+// heads, 120 of 128 elements, 68.6 us with the other halves from shared memory, 81 with loads of their own.
 enum { kRopeSplit = 0, kRopeInterleaved = 1, kRopePart = 2, kRopePieces = 3 };
 // Halves of a part of the head: PIECES where they are whole pieces, else PART.
 
@@ -110,6 +111,9 @@ __global__ void __launch_bounds__(THREADS, (F32 ? 6 : 8) * kRopeThreads / THREAD
     constexpr int PAIRS_EACH = (D / 2 + THREADS - 1) / THREADS;  // entries of the table by a thread
     constexpr int PER = 3;         // units in flight per thread (a token of the 8B shape: all of them)
     __shared__ float2 cs[D / 2];
+    // PART: a warp's units, for the pairs' other halves; an odd number of words apart, so that lanes meet different banks
+    constexpr int UNIT = F32 ? 17 : 9;
+    __shared__ uint32_t held[KIND == kRopePart ? THREADS * UNIT : 1];
     const int b = blockIdx.x / p.T, t = blockIdx.x - b * p.T;
     const long long token = blockIdx.x;
     const int R = p.rope.rot_dim, half = R / 2;
@@ -179,6 +183,14 @@ __global__ void __launch_bounds__(THREADS, (F32 ? 6 : 8) * kRopeThreads / THREAD
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int u = u0 + k * stride;
+            if (KIND == kRopePart) {  // a head's units lie in one warp
+                __syncwarp();
+                if (u < n_units) {
+                    raw[k][0].hold(held + threadIdx.x * UNIT);
+                    raw[k][1].hold(held + threadIdx.x * UNIT + UNIT / 2);
+                }
+                __syncwarp();
+            }
             if (u >= n_units) continue;
             int h, e0, e1, g;
             bool is_q, is_v;
@@ -214,15 +226,16 @@ __global__ void __launch_bounds__(THREADS, (F32 ? 6 : 8) * kRopeThreads / THREAD
                         x[i] = a * f.x - c * f.y;
                         x[i + 1] = c * f.x + a * f.y;
                     }
-                } else {  // a pair's other half by a load of its own
-                    const void* src = is_q ? p.q : p.k;
-                    const long long at = token * (is_q ? p.q_pitch : p.k_pitch) + static_cast<long long>(g) * D;
+                } else {  // a pair's other half from where the warp's units are held
+                    const uint32_t* head = held + (threadIdx.x & ~(PAIRS - 1)) * UNIT;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int e = e0 + i;
                         if (e >= R) continue;
                         const float2 f = cs[e < half ? e : e - half];
-                        const float o = load_elem<F32>(src, at + (e < half ? e + half : e - half));
+                        const int other = e < half ? e + half : e - half;
+                        const uint32_t w = head[(other >> 4) * UNIT + (F32 ? other & 15 : (other & 15) >> 1)];
+                        const float o = F32 ? __uint_as_float(w) : other & 1 ? bf_hi(w) : bf_lo(w);
                         x[i] = x[i] * f.x + (e < half ? -o : o) * f.y;
                     }
                 }
