@@ -98,8 +98,8 @@ __device__ __forceinline__ uint4 pack8(const float* y) {
 // 512 drafted tokens fp32 5.6. Many such tokens of few heads are blocks' latencies one after the other, of which
 // one-warp blocks have more at a time: 8000 tokens of 2 query heads and a kv head 12.2 us, 15.8 with 128 threads
 // (D 64: 8.4 and 14.6). Half a head that turns, 8 and 4 heads: 17.0 us by pieces, 31.1 element by element. What is
-// left to single elements (halves that are not whole pieces) is bound by their instructions: 8192 tokens of 32 and 8
-// heads, 120 of 128 elements, 68.6 us with the other halves from shared memory, 81 with loads of their own.
+// left to PART (halves that are not whole pieces) is bound by its instructions: 8192 tokens of 32 and 8 heads, 120 of 128
+// elements, 61.9 us with the other halves two at a time from shared memory, 68.6 one at a time, 81 with loads of their own.
 enum { kRopeSplit = 0, kRopeInterleaved = 1, kRopePart = 2, kRopePieces = 3 };
 // Halves of a part of the head: PIECES where they are whole pieces, else PART.
 
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(THREADS, (F32 ? 6 : 8) * kRopeThreads / THREAD
     constexpr int PAIRS = D / 16;  // units of a head
     constexpr int PAIRS_EACH = (D / 2 + THREADS - 1) / THREADS;  // entries of the table by a thread
     constexpr int PER = 3;         // units in flight per thread (a token of the 8B shape: all of them)
-    __shared__ float2 cs[D / 2];
+    __shared__ __align__(16) float2 cs[D / 2];
     // PART: a warp's units, for the pairs' other halves; an odd number of words apart, so that lanes meet different banks
     constexpr int UNIT = F32 ? 17 : 9;
     __shared__ uint32_t held[KIND == kRopePart ? THREADS * UNIT : 1];
@@ -228,15 +228,33 @@ __global__ void __launch_bounds__(THREADS, (F32 ? 6 : 8) * kRopeThreads / THREAD
                     }
                 } else {  // a pair's other half from where the warp's units are held
                     const uint32_t* head = held + (threadIdx.x & ~(PAIRS - 1)) * UNIT;
+                    const auto word = [&](int e) { return head[(e >> 4) * UNIT + (F32 ? e & 15 : (e & 15) >> 1)]; };
+                    const auto turned = [](float own, float other, bool first, float2 f) {
+                        return __fmaf_rn(own, f.x, __fmul_rn(first ? -other : other, f.y));
+                    };
+                    if (half % 2 == 0) {  // two elements of one word side by side have theirs side by side
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int e = e0 + i;
-                        if (e >= R) continue;
-                        const float2 f = cs[e < half ? e : e - half];
-                        const int other = e < half ? e + half : e - half;
-                        const uint32_t w = head[(other >> 4) * UNIT + (F32 ? other & 15 : (other & 15) >> 1)];
-                        const float o = F32 ? __uint_as_float(w) : other & 1 ? bf_hi(w) : bf_lo(w);
-                        x[i] = x[i] * f.x + (e < half ? -o : o) * f.y;
+                        for (int i = 0; i < 16; i += 2) {
+                            const int e = e0 + i;
+                            if (e >= R) continue;
+                            const bool first = e < half;
+                            const int other = first ? e + half : e - half;
+                            const float4 f = *reinterpret_cast<const float4*>(&cs[first ? e : other]);
+                            const uint32_t w = word(other);
+                            const float o0 = F32 ? __uint_as_float(w) : bf_lo(w), o1 = F32 ? __uint_as_float(word(other + 1)) : bf_hi(w);
+                            x[i] = turned(x[i], o0, first, make_float2(f.x, f.y));
+                            x[i + 1] = turned(x[i + 1], o1, first, make_float2(f.z, f.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int e = e0 + i;
+                            if (e >= R) continue;
+                            const bool first = e < half;
+                            const int other = first ? e + half : e - half;
+                            const uint32_t w = word(other);
+                            x[i] = turned(x[i], F32 ? __uint_as_float(w) : other & 1 ? bf_hi(w) : bf_lo(w), first, cs[first ? e : other]);
+                        }
                     }
                 }
             }
