@@ -85,8 +85,8 @@ __device__ __forceinline__ uint4 pack8(const float* y) {
 
 // One block per token (or a share of its heads, where tokens are few). A thread's unit is a pair of
 // 16-byte output pieces: of a query or key head the two that hold the same pairs' halves, or where
-// pairs do not lie so (interleaved, a share of pieces that turn, halves not of whole pieces) and in
-// value heads two pieces side by side. Its inputs are asked for first; the position, its angles and
+// pairs do not lie so (interleaved, halves not of whole pieces), in what does not turn and in value
+// heads two pieces side by side. Its inputs are asked for first; the position, its angles and
 // the table of cos and sin come under those loads. Position x turns modulo 2^64 is the angle as a
 // binary fraction of a turn, without a rounding (turns itself is good to f_i * 2^-55, so the angle to
 // 2^-35 turns at position 10^6 and 2^-24 at 2^31); its upper 32 bits, signed, are half-turns * 2^-31.

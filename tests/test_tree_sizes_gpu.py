@@ -81,3 +81,37 @@ def test_fork_of_one_request_in_place(dak):
 ], ids=lambda c: str(c[:6]))
 def test_append_rope_axes_many_tokens(dak, case):
     ops.test_append_rope_axes(dak, case, 0)
+
+
+@pytest.mark.parametrize("case", [
+    (2, 50, 5, 1, 128, 42, False, 2, True, 0),
+    (1, 3, 4, 2, 64, 22, False, 1, False, 1),
+    (2, 9, 3, 3, 128, 126, False, 3, False, 2),
+], ids=str)
+@pytest.mark.parametrize("far", [0, 1000000000])
+def test_append_rope_axes_odd_halves(dak, case, far):
+    ops.test_append_rope_axes(dak, case, far)
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("rot", [128, 120, 112, 64, 42, 16, 12, 2])
+@pytest.mark.parametrize("B,T,Hq,Hkv", [(3, 7, 8, 2), (2, 700, 4, 1)])
+def test_axes_of_a_run_are_append_rope(dak, B, T, Hq, Hkv, rot, fp32):
+    """Positions one after the other on every axis: the same bits as one position a request, in blocks of either size."""
+    import torch
+    D, L = 128, T + 9
+    g = torch.Generator(device="cuda").manual_seed(rot)
+    x = torch.randn(B, T, Hq + 2 * Hkv, D, generator=g, device="cuda", dtype=torch.float32 if fp32 else torch.bfloat16)
+    parts = x[:, :, :Hq], x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:]
+    rope = dak.dak_rope_make(D, rot_dim=rot, theta=10000.0)
+    start, slots = _i32([4000 + b for b in range(B)]), _i32([b for b in range(B)])
+    zero = torch.zeros(B, Hkv, L, D, dtype=torch.bfloat16, device="cuda")
+    one, many = dak.dak_place_kv_heads(zero, zero, 1), dak.dak_place_kv_heads(zero, zero, 0)
+    q = dak.dak_kv_append_rope(one, rope, *parts, slots, positions=start)
+    at = (start[:, None] + torch.arange(T, device="cuda", dtype=torch.int32))[:, :, None].expand(B, T, 3).contiguous()
+    axes = dak.dak_rope_axes_make(rope, [i % 3 for i in range(rot // 2)], n_axes=3)
+    assert torch.equal(dak.dak_kv_append_rope_axes(many, axes, *parts, slots, at), q)
+    _ok(dak)
+    host, hbm = one.slabs()
+    torch.cuda.synchronize()
+    assert torch.equal(torch.cat([host.cuda(), hbm]), many.slabs()[1])
