@@ -142,6 +142,10 @@ __device__ __forceinline__ bool not_finite(const uint4& v) {
     const auto bad = [](uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; };
     return bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
 }
+// The values without those.
+__device__ __forceinline__ uint4 finite_part(const uint4& v) {
+    return make_uint4(v.x & ~tree_not_finite(v.x), v.y & ~tree_not_finite(v.y), v.z & ~tree_not_finite(v.z), v.w & ~tree_not_finite(v.w));
+}
 
 __device__ __forceinline__ void tma_load_q(void* dst, const CUtensorMap* map, int head, int token, int half, uint64_t* bar) {
     asm volatile(
@@ -168,8 +172,49 @@ __device__ __forceinline__ uint4 ld_shared_ordered(const void* p) {
     asm volatile("ld.volatile.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem_u32(p)) : "memory");
     return v;
 }
-__device__ __forceinline__ void clear_shared_ordered(void* p) {
-    asm volatile("st.volatile.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(smem_u32(p)), "r"(0) : "memory");
+__device__ __forceinline__ void st_shared_ordered(void* p, const uint4& v) {
+    asm volatile("st.volatile.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(smem_u32(p)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// An infinity or NaN in V of a row before the drafts is in the sum of every token: in a row's stored results (columns col0
+// to col0 + cols - 1, fp32 or bf16) it becomes what it is, where a weight in parts (infinity times a part of zero) or a
+// factor of zero has made NaN of it. Those of the drafts in `bad`, which the products did not meet, are put in where the
+// token sees them. By a warp, whose rows' columns are the same; a row that is none, or whose scores are, stays (sound: false).
+template <int D>
+__device__ __forceinline__ void odd_values(const TreeParams& p, const TreeRequest& q, int b, int g, int c0, int c1, int t,
+                                           bool valid_row, bool sound, const unsigned* bad, int col0, int cols, uint8_t* row, bool as_bf16) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int col = col0; col < col0 + cols; col += 8) {
+        float x[8] = {};
+        for (int key = c0 * 64 + lane; key < min(c1 * 64, q.len); key += 32) add_not_finite(x, tree_v_piece(p, b, g, D, key, col / 8));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) x[k] += __shfl_xor_sync(0xffffffffu, x[k], o);
+        }
+        if (!valid_row || !sound) continue;
+        for (int word = 0; bad && word < DAK_MAX_TREE / 32; ++word) {
+            for (unsigned set = bad[word]; set; set &= set - 1) {
+                const int key = q.len + word * 32 + __ffs(set) - 1;
+                if (tree_bits(p, q, b, t, key) & 1) add_not_finite(x, tree_v_piece(p, b, g, D, key, col / 8));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (x[k] == 0.f) continue;
+            if (as_bf16) reinterpret_cast<__nv_bfloat16*>(row)[col + k] = __float2bfloat16_rn(x[k]);
+            else reinterpret_cast<float*>(row)[col + k] = x[k];
+        }
+    }
+}
+// Out of line for a bf16 output (32 requests of 64 drafts over 760 rows 53.1 us, 54.4 inlined), inline for fp32, whose
+// registers a call disturbs (32 requests of 64 rows over 8K 315 us, 344 with a call).
+template <int D>
+__device__ __noinline__ void odd_values_apart(const TreeParams& p, TreeRequest q, int b, int g, int c0, int c1, int t,
+                                              bool valid_row, bool sound, const unsigned* bad, int col0, int cols, uint8_t* row,
+                                              bool as_bf16) {
+    odd_values<D>(p, q, b, g, c0, c1, t, valid_row, sound, bad, col0, cols, row, as_bf16);
 }
 
 template <int D>
@@ -433,8 +478,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 const int token0 = (2 * w.tile + (two ? st : 0)) * p.mpt, t = token0 + token_in;
                 const bool valid_row = token_in < p.mpt && t < w.q.n;
                 const bool warp_has_rows = quad * 32 < min(w.q.n - token0, p.mpt) * p.G;
-                // this row in Q and O
-                const long long at = ((static_cast<long long>(w.b) * p.T + t) * p.Hq + w.g * p.G + head_in) * D;
                 const int stride = two ? 1 : 2;
                 const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t where) {
                     if (!failed) failed = !mbar_wait(bar, parity, abort, p.st, DAK_ERR_TIMEOUT, where);
@@ -465,24 +508,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     if (drafts) {
                         // Drafted rows' V may hold infinities and NaN, which the probability of zero of a token
                         // that does not see the row would not cancel, and rows behind the drafts anything at all.
-                        // Such pieces become zeros for the product; what a token sees of them is added at the end.
+                        // They become zeros for the product; what a token sees of them is put in at the end.
                         // Both streams of a step go through them, as either one's product may be first, and a
                         // piece that the other has cleared already is in this one's fence like its own.
                         // (The scores say that the chunk is there.)
                         uint8_t* rows = ring + RingPos<NS>(stage + j).slot * C::kStage + C::kV;
-                        const int begin = max(0, w.q.len - key0), end = w.q.keys - key0;
-                        for (int e = begin * (D / 8) + half * 128 + r_in; e < 64 * (D / 8); e += 256) {
+                        const int begin = max(0, w.q.len - key0), end = min(w.q.keys - key0, 64), first = half * 128 + r_in;
+                        const auto piece = [&](int e) {
                             const int kr = e / (D / 8), c = e % (D / 8);
-                            uint8_t* piece = rows + (c >> 3) * 16384 + kr * 128 + ((c & 7) << 4);
-                            if (kr < end) {
-                                if (!not_finite(ld_shared_ordered(piece))) continue;
-                                const int s = key0 + kr - w.q.len;
-                                atomicOr(&bad[s >> 5], 1u << (s & 31));
-                                any_bad = 1;
-                                __threadfence_block();
-                            }
-                            clear_shared_ordered(piece);
+                            return rows + (c >> 3) * 16384 + kr * 128 + ((c & 7) << 4);
+                        };
+                        for (int e = begin * (D / 8) + first; e < end * (D / 8); e += 256) {
+                            const uint4 v = ld_shared_ordered(piece(e));
+                            if (!not_finite(v)) continue;
+                            const int s = key0 + e / (D / 8) - w.q.len;
+                            atomicOr(&bad[s >> 5], 1u << (s & 31));
+                            any_bad = 1;
+                            __threadfence_block();
+                            st_shared_ordered(piece(e), finite_part(v));
                         }
+                        for (int e = end * (D / 8) + first; e < 64 * (D / 8); e += 256) st_shared_ordered(piece(e), make_uint4(0, 0, 0, 0));
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
@@ -524,62 +569,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     for (int q = 0; q < (F32 ? HALF / 16 : 0); ++q) tmem_st16(o_addr + q * 16, sum[q]);
                     tmem_wait_st();
                 }
-                // what tokens see of cleared pieces
-                const bool repair = __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&any_bad) != 0);
-#pragma unroll 1
-                for (int word = 0; repair && word < DAK_MAX_TREE / 32; ++word) {
-                    unsigned set = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile unsigned*>(&bad[word]), 0);
-#pragma unroll 1
-                    for (; set; set &= set - 1) {
-                        const int s = word * 32 + __ffs(set) - 1, key = w.q.len + s, j = (key >> 6) - c0;
-                        if (j < 0 || j >= steps || (!two && (j & 1) != st)) continue;
-                        const bool sees = valid_row && (tree_bits(p, w.q, w.b, t, key) & 1);
-                        if (!__any_sync(0xffffffffu, sees)) continue;
-                        const long long slab = static_cast<long long>(w.b) * p.Hkv + w.g;
-                        const uint8_t* base = slab < p.h_s ? p.kv[0] + slab * p.head_bytes : p.kv[1] + (slab - p.h_s) * p.head_bytes;
-                        const uint4* k_row = reinterpret_cast<const uint4*>(base) + (static_cast<long long>(key >> 6) * 2 * 64 + (key & 63)) * (D / 8);
-                        const uint4* v_row = k_row + 64 * (D / 8);
-                        const auto products = [](const uint4& a, const uint4& b) {
-                            return bf_lo(a.x) * bf_lo(b.x) + bf_hi(a.x) * bf_hi(b.x) + bf_lo(a.y) * bf_lo(b.y) + bf_hi(a.y) * bf_hi(b.y) +
-                                   bf_lo(a.z) * bf_lo(b.z) + bf_hi(a.z) * bf_hi(b.z) + bf_lo(a.w) * bf_lo(b.w) + bf_hi(a.w) * bf_hi(b.w);
-                        };
-                        float x = 0.f;
-                        if (sees) {
-                            const uint4* q_row = reinterpret_cast<const uint4*>(p.Q + at);
-#pragma unroll 1
-                            for (int c = 0; c < D / 8; ++c) x += products(q_row[c], k_row[c ^ (key & 7)]);
-                        }
-                        // a weight that is too small for its type is none the less more than zero
-                        const float weight = fmaxf(exp2f(x * p.scale_log2 - (m_ref == -INFINITY ? 0.f : m_ref)), 1e-37f);
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int q = 0; q < HALF / 16; ++q) {
-                            float o[16];
-                            tmem_ld16(o_addr + q * 16, o);
-                            tmem_wait(o);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint4 v = v_row[(half * (HALF / 8) + 2 * q + e) ^ (key & 7)];
-                                if (!sees || !not_finite(v)) continue;
-                                const uint32_t pairs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    o[e * 8 + 2 * k] += weight * bf_lo(pairs[k]);
-                                    o[e * 8 + 2 * k + 1] += weight * bf_hi(pairs[k]);
-                                }
-                            }
-                            tmem_st16(o_addr + q * 16, o);
-                        }
-                        tmem_wait_st();
-                    }
-                }
                 // ---- results: the halves' sums, and where the streams share a tile what the other one has
                 const bool both = !two && steps > 1;  // the streams' rows are the same and both had a step
                 l += other(l);
                 tc_fence_before();
                 named_bar<3, kTreeSoftmax>();
-                if (threadIdx.x < DAK_MAX_TREE / 32) bad[threadIdx.x] = 0;
-                if (threadIdx.x == 32) any_bad = 0;
                 float m_other = -INFINITY, l_other = 0.f;
                 if (!two) {
                     maxima[st][half][r_in] = half ? l : m_ref;
@@ -595,10 +589,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 const float inv = !whole || (valid_row && !tree_sees(p, w.q, w.b, t)) ? 1.f : 1.f / total;
                 const long long local = (2ll * r + (c0 == 0)) * p.part_rows + (two ? st * 128 : 0) + r_in;  // among the partials
                 if (!whole && valid_row && half == 0 && (two || st == 0)) p.ml_part[local] = make_float2(M, total);
+                const long long at = ((static_cast<long long>(w.b) * p.T + t) * p.Hq + w.g * p.G + head_in) * D;  // this row in O
                 // stream 0's O, or the only one; the other's where both have one
                 const uint32_t o0 = tmem + lanes + 256 + (two ? st * D : 0), o1 = tmem + lanes + 256 + D;
                 const float w0 = (st == 0 || two ? w_own : w_other) * inv, w1 = (st == 0 ? w_other : w_own) * inv;
                 const int col0 = two ? half * HALF : (2 * st + half) * QUARTER, cols = two ? HALF : QUARTER;
+                float2 odd[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // NaN where a result is none or infinite
 #pragma unroll 1
                 for (int col = col0; warp_has_rows && col < col0 + cols; col += 16) {
                     float o[16];
@@ -614,6 +610,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
 #pragma unroll
                         for (int k = 0; k < 16; ++k) o[k] *= w0;
                     }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) odd[k & 1] = fma2(make_float2(o[2 * k], o[2 * k + 1]), make_float2(0.f, 0.f), odd[k & 1]);
                     uint32_t out[8];
                     if (valid_row && whole && !F32) {
 #pragma unroll
@@ -629,6 +627,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         }
                     }
                     __syncwarp();
+                }
+                const bool repair = *reinterpret_cast<volatile int*>(&any_bad) != 0;
+                const float none = (odd[0].x + odd[0].y) + (odd[1].x + odd[1].y);
+                if (__any_sync(0xffffffffu, valid_row && (repair || (none != 0.f && fabsf(total) < INFINITY)))) {
+                    const bool sound = fabsf(total) < INFINITY;  // a row whose own sum is none has scores that are none
+                    uint8_t* row = whole ? static_cast<uint8_t*>(p.O) + at * (F32 ? 4 : 2) : reinterpret_cast<uint8_t*>(p.o_part + local * D);
+                    const unsigned* drafts = repair ? bad : nullptr;
+                    if constexpr (F32) odd_values<D>(p, w.q, w.b, w.g, c0, c1, t, valid_row, sound, drafts, col0, cols, row, false);
+                    else odd_values_apart<D>(p, w.q, w.b, w.g, c0, c1, t, valid_row, sound, drafts, col0, cols, row, whole);
+                }
+                if (repair) {
+                    named_bar<3, kTreeSoftmax>();  // all have been through the list
+                    if (threadIdx.x < DAK_MAX_TREE / 32) bad[threadIdx.x] = 0;
+                    if (threadIdx.x == 32) any_bad = 0;
                 }
                 n += two ? steps : (steps + 1 - st) / 2;
                 stage += steps;
@@ -651,6 +663,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
 // ------------------------------------------------------------------------------------
 // Block (r, y): eight rows, a warp each, of the tile that begins in range r and ends in a later one:
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over its pieces, in order.
+// (No factor is below 1e-37: zero would make NaN of an infinity that V had.)
 // What it waits for are loads: the first pieces, which every such tile has, are asked for before it is known
 // whether there is one. 4.4 us of one request's 13.5, most of them the launch and two loads one after the
 // other; 5 of 157 for 32 rows a kv head of 32 requests, 13 of 224 for 512 rows of 48 (31 MB of partials).
@@ -687,7 +700,8 @@ __global__ void __launch_bounds__(32 * kTreeMergeRows) tree_merge_kernel(const _
         acc.z += w * x.z;
         acc.w += w * x.w;
     };
-    float f = exp2f(first.x - base), l = f * first.y;
+    const auto factor = [&](float m) { return fmaxf(exp2f(m - base), 1e-37f); };
+    float f = factor(first.x), l = f * first.y;
 #pragma unroll
     for (int k = 0; k < EARLY; ++k) {
         const float w = __shfl_sync(0xffffffffu, f, k * AT_ONCE + grp);
@@ -696,7 +710,7 @@ __global__ void __launch_bounds__(32 * kTreeMergeRows) tree_merge_kernel(const _
     for (int at = 0; at < n; at += 32) {  // 32 pieces' factors on the lanes
         if (at > 0) {
             const float2 v = at + lane < n ? p.ml_part[slot(at + lane)] : make_float2(-INFINITY, 0.f);
-            f = exp2f(v.x - base);
+            f = factor(v.x);
             l += f * v.y;
         }
         for (int s0 = at > 0 ? 0 : EARLY * AT_ONCE; s0 < min(32, n - at); s0 += 6 * AT_ONCE) {

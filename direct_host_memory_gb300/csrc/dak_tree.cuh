@@ -244,6 +244,33 @@ __device__ __forceinline__ bool tree_sees(const TreeParams& p, const TreeRequest
     return any != 0;
 }
 
+// Of a bf16 pair the elements that are infinite or NaN.
+__device__ __forceinline__ uint32_t tree_not_finite(uint32_t a) {
+    return ((a & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((a & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
+// Elements 8 c to 8 c + 7 of a row of V.
+__device__ __forceinline__ const uint4* tree_v_piece(const TreeParams& p, int b, int g, int D, int key, int c) {
+    const long long slab = static_cast<long long>(b) * p.Hkv + g;
+    const uint8_t* base = slab < p.h_s ? p.kv[0] + slab * p.head_bytes : p.kv[1] + (slab - p.h_s) * p.head_bytes;
+    return reinterpret_cast<const uint4*>(base) + (static_cast<long long>(key >> 6) * 2 * 64 + 64 + (key & 63)) * (D / 8) + (c ^ (key & 7));
+}
+
+// What is infinite or NaN in N consecutive bf16 values, added to `to`: the result of an element that a token sees,
+// whatever the weights (with infinities of both signs NaN), where its sum with weights would be NaN as soon as one
+// of them, or a part of one, is rounded to zero.
+template <class Words>
+__device__ __forceinline__ void add_not_finite(float* to, const Words* at) {
+    const Words v = *at;
+    const uint32_t* word = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+    for (int k = 0; k < static_cast<int>(sizeof(Words) / 4); ++k) {
+        const uint32_t odd = tree_not_finite(word[k]);
+        if (odd & 0xFFFFu) to[2 * k] += bf_lo(word[k]);
+        if (odd >> 16) to[2 * k + 1] += bf_hi(word[k]);
+    }
+}
+
 // The ranges that a CTA takes: the one of its number, unless more ranges touch the host than CTAs may.
 struct TreeTurn {
     int first, end, step;

@@ -34,11 +34,6 @@ __device__ __forceinline__ uint32_t few_movmatrix(uint32_t a) {
 // Mask of a bf16 pair of which the first n elements count.
 __device__ __forceinline__ uint32_t few_pair_mask(int n) { return n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u; }
 
-// Of a bf16 pair the elements that are infinite or NaN.
-__device__ __forceinline__ uint32_t few_not_finite(uint32_t a) {
-    return ((a & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((a & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-}
-
 template <int D>
 constexpr int few_stage_bytes() { return 2 * 64 * D * 2; }
 
@@ -63,12 +58,12 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
     constexpr int ROWS = 8 * NB;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[W], empty[W];
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, any_left_out;  // of the tile at work's drafts, of the product
     volatile int* abort = &abort_flag;
     float* comb = reinterpret_cast<float*>(smem + W * STAGE);  // [2][ROWS][D + 2]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        abort_flag = 0;
+        abort_flag = any_left_out = 0;
         for (int s = 0; s < W; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kFewConsumers);
@@ -257,7 +252,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
                     }
                     // Rows behind the last may hold anything, also infinities and NaN, which a probability of zero
                     // would not cancel; drafted rows likewise for a row that does not see them: their infinities and
-                    // NaN are left out of the product and added after it where they are seen.
+                    // NaN are left out of the product and put in at the end where they are seen.
                     const int tok = 16 * wk + (mi >> 1) * 8 + rr;
                     const uint32_t lo = few_pair_mask(valid - 2 * q4), hi = few_pair_mask(valid - 8 - 2 * q4);
                     const uint32_t committed_lo = few_pair_mask(w.q.len - key0 - 2 * q4), committed_hi = few_pair_mask(w.q.len - key0 - 8 - 2 * q4);
@@ -268,8 +263,8 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
                         uint32_t a0, a1, a2, a3;
                         ldsm_x4_t(vs_base + static_cast<uint32_t>(tok * D * 2 + ((cc ^ (tok & 7)) << 4)), a0, a1, a2, a3);
                         if (drafts) {
-                            const uint32_t x0 = few_not_finite(a0) & ~committed_lo & lo, x1 = few_not_finite(a1) & ~committed_lo & lo;
-                            const uint32_t x2 = few_not_finite(a2) & ~committed_hi & hi, x3 = few_not_finite(a3) & ~committed_hi & hi;
+                            const uint32_t x0 = tree_not_finite(a0) & ~committed_lo & lo, x1 = tree_not_finite(a1) & ~committed_lo & lo;
+                            const uint32_t x2 = tree_not_finite(a2) & ~committed_hi & hi, x3 = tree_not_finite(a3) & ~committed_hi & hi;
                             left_out |= x0 | x1 | x2 | x3;
                             a0 &= lo & ~x0;
                             a1 &= lo & ~x1;
@@ -289,32 +284,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
                             }
                         }
                     }
-                    if (__any_sync(0xffffffffu, left_out != 0)) {
-#pragma unroll 1
-                        for (int j = max(0, w.q.len - key0); j < min(16, valid); ++j) {
-                            const uint8_t* v_row = smem + s * STAGE + CHUNK_BYTES + (16 * wk + j) * D * 2;
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    // a weight that is too small for its type is none the less more than zero
-                                    const float x = __shfl_sync(0xffffffffu, j < 8 ? sc[nb][e] : sc[nb][2 + e], (j & 7) * 4 + q4);
-                                    const float weight = fmaxf(x, 1e-37f);
-                                    if (!(seen[nb][e] >> j & 1u)) continue;
-#pragma unroll
-                                    for (int tt = 0; tt < KS; ++tt) {
-#pragma unroll
-                                        for (int h = 0; h < 2; ++h) {
-                                            const int cc = 2 * tt + h;
-                                            const unsigned short v = *reinterpret_cast<const unsigned short*>(v_row + ((cc ^ (j & 7)) << 4) + ra * 2);
-                                            if ((v & 0x7F80u) == 0x7F80u) o[tt][nb][2 * h + e] += weight * __uint_as_float(static_cast<uint32_t>(v) << 16);
-                                        }
-                                    }
-                                }
-                            }
-                        }
-                        __syncwarp();
-                    }
+                    if (left_out) any_left_out = 1;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[s]);
@@ -376,27 +346,68 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
                 put();
             }
             bar();
-            const bool whole = c0 == 0 && c1 == w.q.chunks;
-            for (int e = threadIdx.x - 32; e < rows * (D / 4); e += 32 * kFewConsumers) {
-                const int h = e / (D / 4), d = e % (D / 4) * 4;
+            const bool whole = c0 == 0 && c1 == w.q.chunks, repair = *reinterpret_cast<volatile int*>(&any_left_out) != 0;
+            bool odd = false;
+            const auto combined = [&](int h, int d, float(&v)[4]) {  // of two warps each
                 const float* ca = comb + h * (D + 2);
                 const float* cb = ca + ROWS * (D + 2);
                 const float M = fmaxf(ca[D], cb[D]), base = M == -INFINITY ? 0.f : M;
-                const float fa = exp2_ftz(ca[D] - base), fb = exp2_ftz(cb[D] - base), total = fa * ca[D + 1] + fb * cb[D + 1];
-                float v[4];
+                const float fa = exp2_ftz(ca[D] - base), fb = exp2_ftz(cb[D] - base);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] = fa * ca[d + k] + fb * cb[d + k];
+                return make_float2(M, fa * ca[D + 1] + fb * cb[D + 1]);
+            };
+            const auto store = [&](int h, int d, const float2& ml, float(&v)[4]) {
                 if (!whole) {
                     const long long at = (2ll * r + (c0 == 0)) * p.part_rows + h;
                     *reinterpret_cast<float4*>(p.o_part + at * D + d) = make_float4(v[0], v[1], v[2], v[3]);
-                    if (d == 0) p.ml_part[at] = make_float2(M, total);
-                    continue;
+                    if (d == 0) p.ml_part[at] = ml;
+                    return;
                 }
                 // a token that sees nothing has zeros, which stay
-                if (tree_sees(p, w.q, w.b, (h * p.inv_G) >> 16)) v[0] /= total, v[1] /= total, v[2] /= total, v[3] /= total;
+                if (tree_sees(p, w.q, w.b, (h * p.inv_G) >> 16)) v[0] /= ml.y, v[1] /= ml.y, v[2] /= ml.y, v[3] /= ml.y;
                 const long long at = row_at(h) + d;
                 if (PARTS == 3) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + at) = make_float4(v[0], v[1], v[2], v[3]);
                 else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + at) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            };
+            for (int e = threadIdx.x - 32; e < rows * (D / 4); e += 32 * kFewConsumers) {
+                const int h = e / (D / 4), d = e % (D / 4) * 4;
+                float v[4];
+                const float2 ml = combined(h, d, v);
+                // (a row whose own sum is none has scores that are none)
+                odd |= fmaf(v[0], 0.f, v[1] * 0.f) + fmaf(v[2], 0.f, v[3] * 0.f) != 0.f && fabsf(ml.y) < INFINITY;
+                store(h, d, ml, v);
+            }
+            // An infinity or NaN in V of a row before the drafts is in the sum of every token: here it becomes what it
+            // is, where a weight in parts (infinity times a part of zero) or a factor of zero has made NaN of it. Those of
+            // the drafts, which the products did not meet, are put in where the token sees them.
+            if (odd || repair) {
+                const int d = (threadIdx.x - 32) % (D / 4) * 4;  // the same in all of a thread's rows
+                const auto v_at = [&](int key) {
+                    return reinterpret_cast<const uint2*>(tree_v_piece(p, w.b, w.g, D, key, d >> 3)) + (d >> 2 & 1);
+                };
+                float cached[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                for (int key = c0 * 64; key < min(c1 * 64, w.q.len); ++key) add_not_finite(cached, v_at(key));
+#pragma unroll 1
+                for (int h = (threadIdx.x - 32) / (D / 4); h < rows; h += 32 * kFewConsumers / (D / 4)) {
+                    float v[4], x[4] = {cached[0], cached[1], cached[2], cached[3]};
+                    const float2 ml = combined(h, d, v);
+#pragma unroll 1
+                    for (int key = max(c0 * 64, w.q.len); key < min(c1 * 64, w.q.keys); ++key) {
+                        if (tree_bits(p, w.q, w.b, (h * p.inv_G) >> 16, key) & 1) add_not_finite(x, v_at(key));
+                    }
+                    if (!(fabsf(ml.y) < INFINITY)) continue;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (x[k] != 0.f) v[k] = x[k];
+                    }
+                    store(h, d, ml, v);
+                }
+            }
+            if (repair) {
+                bar();  // all have read it
+                if (threadIdx.x == 32) any_left_out = 0;
             }
             bar();  // comb is rewritten by the next tile
         }

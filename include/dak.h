@@ -619,6 +619,8 @@ dak_status dak_attn_prefix(const void* Q, const dak_placement* KV, const int* se
  *   tuning    : host_ctas, window and hbm_window; the others are not taken.
  * A token that sees no row at all gives O = 0. What lies in rows that a token does not see, infinities
  * and NaN too, does not reach its output; a score of NaN or +infinity gives NaN, as its softmax is.
+ * An infinity or NaN in V of a row that a token sees, cached or drafted, is what its output has there,
+ * however small the row's weight (NaN with infinities of both signs).
  * The probabilities enter P.V as two bf16 parts (three with o_fp32). The result does not depend on the
  * offload ratio. Requires H_q / H_kv <= 16, as dak_attn. */
 size_t dak_attn_tree_workspace_bytes(const dak_placement* KV, int T, int H_q);
