@@ -533,7 +533,8 @@ size_t dak_attn_workspace_bytes(int B, int H_q, int D, int n_split);
  *   Q        : bf16 [B][H_q][D] (device).
  *   seq_lens : int32 [B] (device) with 1 <= L_b <= L, or NULL for all L.
  *   scale    : softmax scale; <= 0 means 1/sqrt(D).
- *   O        : bf16 [B][H_q][D] (device).
+ *   O        : bf16 [B][H_q][D] (device). An infinity or NaN in V of a row j < L_b makes that
+ *              element infinite or NaN (NaN where the row's probability rounds to zero).
  *   workspace: device scratch of dak_attn_workspace_bytes(B, H_q, D, n_split) bytes,
  *              8-byte aligned (DAK_ERR_ALIGN otherwise; NULL allowed when that size is
  *              0), caller-owned; its contents on entry do not matter.
@@ -558,7 +559,9 @@ dak_status dak_attn_f32(const void* Q, const dak_placement* KV, const int* seq_l
  *             clamped to [0, L].
  *   O       : [B][H_q][D], bf16 or (o_fp32) fp32. The probabilities enter P.V as two bf16 parts
  *             (three with o_fp32). A score of NaN or +infinity makes its head's O and its kv
- *             head's weights NaN, as the softmax of such a row is.
+ *             head's weights NaN, as the softmax of such a row is. An infinity or NaN in V of a
+ *             counted row makes that element of O infinite or NaN (NaN where a part of the row's
+ *             probability is zero), and no other.
  *   acc_in  : fp32 [B][H_kv][L] (device), or NULL = zeros. acc_out: the same shape; it may be
  *             acc_in (in place) but must not overlap it otherwise.
  *   workspace: dak_attn_acc_workspace_bytes(KV, H_q, n_split) bytes (n_split <= 0: the default),
@@ -587,7 +590,8 @@ dak_status dak_attn_acc(const void* Q, const dak_placement* KV, const int* seq_l
  *   tuning     : applies to the pass over the own caches; pdl and link are not taken.
  * The prefixes are read by tcgen05 tensor-core tiles of up to 256 query rows (requests x H_q /
  * H_kv); a prefix with more rows than that is streamed once per 256. The probabilities enter P.V
- * as two bf16 parts (three with o_fp32), however many requests share a prefix.
+ * as two bf16 parts (three with o_fp32), however many requests share a prefix. Infinities and NaN
+ * as in dak_attn_acc.
  * Requires H_q / H_kv <= 16, as dak_attn, and at most 1024 prefixes (DAK_ERR_UNSUPPORTED). */
 size_t dak_attn_prefix_workspace_bytes(const dak_placement* KV, const dak_placement* P, int H_q, int n_split,
                                        int with_acc);
