@@ -69,16 +69,6 @@ __device__ __forceinline__ ServeUnit serve_unit(const ServeParams& p, unsigned u
     return x;
 }
 
-// Mask of a bf16 pair of which the first n elements count.
-__device__ __forceinline__ uint32_t pair_mask(int n) { return n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u; }
-
-// 8x8 16-bit matrix across the warp, transposed.
-__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
-    uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
-
 // The query heads of a kv head are the narrow side of both products, so that they are the 8-wide N
 // of the warp MMAs (NB blocks of 8 heads) and tokens or head elements the 16-high M:
 //   S^T (16 tokens x heads) = K (16 x D) . Q^T (D x heads)

@@ -24,16 +24,6 @@ constexpr int kFewMaxStages = 6;
 
 enum : uint32_t { W_PROD_EMPTY = 0x81, W_CONS_FULL, W_DRAIN };
 
-// 8x8 16-bit matrix across the warp, transposed.
-__device__ __forceinline__ uint32_t few_movmatrix(uint32_t a) {
-    uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
-
-// Mask of a bf16 pair of which the first n elements count.
-__device__ __forceinline__ uint32_t few_pair_mask(int n) { return n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u; }
-
 template <int D>
 constexpr int few_stage_bytes() { return 2 * 64 * D * 2; }
 
@@ -244,7 +234,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const uint32_t v = pack_bf16(x[2 * h], x[2 * h + 1]);
-                                pb[nb][k][h] = few_movmatrix(v);
+                                pb[nb][k][h] = movmatrix(v);
                                 x[2 * h] -= bf_lo(v);
                                 x[2 * h + 1] -= bf_hi(v);
                             }
@@ -254,8 +244,8 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas_per_sm(NB)) tree_few_ker
                     // would not cancel; drafted rows likewise for a row that does not see them: their infinities and
                     // NaN are left out of the product and put in at the end where they are seen.
                     const int tok = 16 * wk + (mi >> 1) * 8 + rr;
-                    const uint32_t lo = few_pair_mask(valid - 2 * q4), hi = few_pair_mask(valid - 8 - 2 * q4);
-                    const uint32_t committed_lo = few_pair_mask(w.q.len - key0 - 2 * q4), committed_hi = few_pair_mask(w.q.len - key0 - 8 - 2 * q4);
+                    const uint32_t lo = pair_mask(valid - 2 * q4), hi = pair_mask(valid - 8 - 2 * q4);
+                    const uint32_t committed_lo = pair_mask(w.q.len - key0 - 2 * q4), committed_hi = pair_mask(w.q.len - key0 - 8 - 2 * q4);
                     uint32_t left_out = 0;
 #pragma unroll
                     for (int tt = 0; tt < KS; ++tt) {
