@@ -865,7 +865,7 @@ static bool off(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>
 using namespace dak;
 
 extern "C" size_t dak_attn_tree_workspace_bytes(const dak_placement* KV, int T, int H_q) {
-    if (!KV || KV->kind != 1 || T < 1 || T > DAK_MAX_TREE || H_q < 1 || H_q % KV->H_kv || H_q / KV->H_kv > 16) return 0;
+    if (!KV || KV->kind != 1 || T < 1 || T > DAK_MAX_TREE || H_q < 1 || H_q % KV->H_kv || H_q / KV->H_kv > 16 || !line_fits(KV, T, H_q)) return 0;
     return tree_layout(KV, T, H_q).total();
 }
 

@@ -626,7 +626,11 @@ dak_status dak_attn_prefix(const void* Q, const dak_placement* KV, const int* se
  * An infinity or NaN in V of a row that a token sees, cached or drafted, is what its output has there,
  * however small the row's weight (NaN with infinities of both signs).
  * The probabilities enter P.V as two bf16 parts (three with o_fp32). The result does not depend on the
- * offload ratio. Requires H_q / H_kv <= 16, as dak_attn. */
+ * offload ratio.
+ * DAK_ERR_UNSUPPORTED, and a workspace of 0 bytes: H_q / H_kv above 16, as dak_attn; T above
+ * DAK_MAX_TREE; work that 31 bits do not count, with G = H_q / H_kv:
+ *     (6 + 2 ceil(L / 64)) ceil(T / floor(128 / G)) B H_kv >= 2^31 - 2^24,
+ *     B H_kv ceil(L / 64) >= 2^31 or B T >= 2^31. */
 size_t dak_attn_tree_workspace_bytes(const dak_placement* KV, int T, int H_q);
 dak_status dak_attn_tree(const void* Q, const dak_placement* KV, const int* seq_lens, int T, const uint64_t* mask,
                          int64_t mask_pitch, const int* n_new, int H_q, float scale, void* O, int o_fp32,
