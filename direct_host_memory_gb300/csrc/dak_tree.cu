@@ -804,7 +804,7 @@ static TreeLayout tree_layout(const dak_placement* KV, int T, int H_q) {
 static bool line_fits(const dak_placement* KV, int T, int H_q) {
     const int mpt = 128 / (H_q / KV->H_kv);
     const int64_t chunks = (KV->L + 63) / 64, halves = (T + mpt - 1) / mpt;
-    return (kTreeTileCost + kTreeOneCost * chunks) * halves * KV->B * KV->H_kv < 0x7FFFFFFF - (1 << 24) &&
+    return (kTreeTileCost + kTreeOneCost * chunks) * halves * KV->B * KV->H_kv < (1ll << 31) - (1 << 24) &&
            static_cast<int64_t>(KV->B) * KV->H_kv * chunks <= 0x7FFFFFFF && static_cast<int64_t>(KV->B) * T <= 0x7FFFFFFF;
 }
 
