@@ -297,7 +297,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 if (lane == 0) {
                     const long long slab = static_cast<long long>(w.b) * p.Hkv + w.g;
                     const int tier = slab < p.h_s ? 0 : 1, window = p.in_flight[tier];
-                    const uint64_t policy = w.q.tiles > 1 ? policy_evict_last() : policy_evict_first();
+                    // also where another tile reads the chunks again: with evict_last 4 requests of 64 drafts and 64 heads
+                    // over 27K took 274 us, 267 so, 32 of heads of 64 over 3.6K 250 and 247, the 48 above 232 and 233
+                    const uint64_t policy = policy_evict_first();
                     const int chunk0 = static_cast<int>((tier ? slab - p.h_s : slab) * p.slab_chunks);
                     for (int c = c0; c < c1; ++c) {
                         if (sent >= NS) ok = wait_phase(&empty[pos.slot], pos.phase ^ 1u, abort, p.st, T_PROD_EMPTY);
