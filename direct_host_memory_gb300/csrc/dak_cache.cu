@@ -886,13 +886,6 @@ static cudaError_t launch_evict_d(const EvictParams& p, unsigned slabs, cudaStre
     return cudaLaunchKernelEx(&cfg, evict_move_kernel<D>, p);
 }
 
-static bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + nb && y < x + na;
-}
-
-static bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
-
 static dak_status device_matches(const dak_placement* p) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DAK_ERR_CUDA;

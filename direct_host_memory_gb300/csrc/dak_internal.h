@@ -34,6 +34,13 @@ namespace dak {
 
 constexpr int kTileM = 64;
 
+// Checks of arguments: ranges of bytes that share one (null: none), an address that is no multiple of n.
+inline bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+inline bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
 // Device status block: first failure code and where it happened.
 struct DevStatus {
     int code;

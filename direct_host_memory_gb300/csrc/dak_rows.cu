@@ -366,13 +366,6 @@ static cudaError_t launch_fork(ForkParams& p, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, fork_kernel<D>, p);
 }
 
-static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + nb && y < x + na;
-}
-
-static bool off(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
-
 }  // namespace dak
 
 using namespace dak;
@@ -381,12 +374,12 @@ extern "C" dak_status dak_kv_commit(const dak_placement* KV, const int* seq_lens
                                     int P, const int* n_path, int* lens_out, int* slot_pos, float* acc, void* stream) {
     if (!KV || KV->kind != 1 || !seq_lens || !path || !n_path || !lens_out || T < 1 || P < 1 || P > T) return DAK_ERR_INVALID;
     if (T > DAK_MAX_TREE) return DAK_ERR_UNSUPPORTED;
-    if (off(seq_lens, 4) || off(n_new, 4) || off(path, 4) || off(n_path, 4) || off(lens_out, 4) || off(slot_pos, 4) || off(acc, 4)) {
+    if (misaligned(seq_lens, 4) || misaligned(n_new, 4) || misaligned(path, 4) || misaligned(n_path, 4) || misaligned(lens_out, 4) || misaligned(slot_pos, 4) || misaligned(acc, 4)) {
         return DAK_ERR_ALIGN;
     }
     const size_t lens = static_cast<size_t>(KV->B) * 4;
-    if (overlap(lens_out, lens, seq_lens, lens) || overlap(lens_out, lens, n_new, lens) || overlap(lens_out, lens, n_path, lens) ||
-        overlap(lens_out, lens, path, lens * P)) {
+    if (ranges_overlap(lens_out, lens, seq_lens, lens) || ranges_overlap(lens_out, lens, n_new, lens) || ranges_overlap(lens_out, lens, n_path, lens) ||
+        ranges_overlap(lens_out, lens, path, lens * P)) {
         return DAK_ERR_INVALID;
     }
     int dev = 0;
@@ -433,19 +426,19 @@ extern "C" dak_status dak_kv_fork(const dak_placement* KV, const dak_placement* 
     if (src->H_kv != KV->H_kv || src->D != KV->D || src->device != KV->device) return DAK_ERR_INVALID;
     if (KV->B > kForkMax || src->B > kForkMax) return DAK_ERR_UNSUPPORTED;
     if (!slot_pos != !src_slot_pos || !acc != !src_acc) return DAK_ERR_INVALID;
-    if (off(src_of, 4) || off(seq_lens, 4) || off(first, 4) || off(lens_out, 4) || off(src_slot_pos, 4) || off(slot_pos, 4) ||
-        off(src_acc, 4) || off(acc, 4)) {
+    if (misaligned(src_of, 4) || misaligned(seq_lens, 4) || misaligned(first, 4) || misaligned(lens_out, 4) || misaligned(src_slot_pos, 4) || misaligned(slot_pos, 4) ||
+        misaligned(src_acc, 4) || misaligned(acc, 4)) {
         return DAK_ERR_ALIGN;
     }
     const size_t lens = static_cast<size_t>(KV->B) * 4, src_lens = static_cast<size_t>(src->B) * 4;
-    if (overlap(lens_out, lens, src_of, lens) || overlap(lens_out, lens, first, lens) || overlap(lens_out, lens, seq_lens, src_lens)) {
+    if (ranges_overlap(lens_out, lens, src_of, lens) || ranges_overlap(lens_out, lens, first, lens) || ranges_overlap(lens_out, lens, seq_lens, src_lens)) {
         return DAK_ERR_INVALID;
     }
     if (src == KV) {
         if (slot_pos != src_slot_pos || acc != src_acc) return DAK_ERR_INVALID;
     } else {
         const size_t to = lens * KV->H_kv * KV->L, from = src_lens * src->H_kv * src->L;
-        if (overlap(slot_pos, to, src_slot_pos, from) || overlap(acc, to, src_acc, from)) return DAK_ERR_INVALID;
+        if (ranges_overlap(slot_pos, to, src_slot_pos, from) || ranges_overlap(acc, to, src_acc, from)) return DAK_ERR_INVALID;
     }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DAK_ERR_CUDA;

@@ -713,8 +713,6 @@ static bool partly_overlaps(const void* a, const void* b, size_t bytes) {
     return x != y && x < y + bytes && y < x + bytes;
 }
 
-static bool low_bits(const void* p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
-
 static dak_status serve_attention(const void* Q, const dak_placement* KV, const int* seq_lens, const dak_placement* P,
                                   const int* prefix_lens, const int* prefix_of, int H_q, float scale, void* O,
                                   int o_fp32, const float* acc_in, float* acc_out, void* ws, size_t ws_bytes,
@@ -730,8 +728,8 @@ static dak_status serve_attention(const void* Q, const dak_placement* KV, const 
     if (acc_out && acc_in && partly_overlaps(acc_in, acc_out, static_cast<size_t>(slabs) * KV->L * sizeof(float))) {
         return DAK_ERR_INVALID;
     }
-    if (low_bits(Q, 15) || low_bits(O, 15) || low_bits(ws, 15) || low_bits(acc_in, 3) || low_bits(acc_out, 3) ||
-        low_bits(seq_lens, 3) || low_bits(prefix_lens, 3) || low_bits(prefix_of, 3)) {
+    if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(ws, 16) || misaligned(acc_in, 4) || misaligned(acc_out, 4) ||
+        misaligned(seq_lens, 4) || misaligned(prefix_lens, 4) || misaligned(prefix_of, 4)) {
         return DAK_ERR_ALIGN;
     }
     const ServeLayout x = serve_layout(KV, P, H_q, t ? t->n_split : 0, acc_out != nullptr);

@@ -855,13 +855,6 @@ static cudaError_t launch_tree_merge(const TreeParams& p, int D, cudaStream_t s)
     return D == 128 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<128>, p) : cudaLaunchKernelEx(&cfg, tree_merge_kernel<64>, p);
 }
 
-static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
-static bool off(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
-
 }  // namespace dak
 
 using namespace dak;
@@ -879,8 +872,8 @@ extern "C" dak_status dak_attn_tree(const void* Q, const dak_placement* KV, cons
     if (T > DAK_MAX_TREE || G > 16 || !line_fits(KV, T, H_q)) return DAK_ERR_UNSUPPORTED;
     if (mask && mask_pitch != 0 && mask_pitch < static_cast<int64_t>(T) * W) return DAK_ERR_INVALID;
     const size_t elems = static_cast<size_t>(KV->B) * T * H_q * D;
-    if (overlap(Q, elems * 2, O, elems * (o_fp32 ? 4 : 2))) return DAK_ERR_INVALID;
-    if (off(Q, 16) || off(O, 16) || off(workspace, 16) || off(seq_lens, 4) || off(n_new, 4) || off(mask, 8)) return DAK_ERR_ALIGN;
+    if (ranges_overlap(Q, elems * 2, O, elems * (o_fp32 ? 4 : 2))) return DAK_ERR_INVALID;
+    if (misaligned(Q, 16) || misaligned(O, 16) || misaligned(workspace, 16) || misaligned(seq_lens, 4) || misaligned(n_new, 4) || misaligned(mask, 8)) return DAK_ERR_ALIGN;
     const TreeLayout x = tree_layout(KV, T, H_q);
     if (!workspace || ws_bytes < x.total()) return DAK_ERR_INVALID;
     int dev = 0;
@@ -894,7 +887,7 @@ extern "C" dak_status dak_attn_tree(const void* Q, const dak_placement* KV, cons
     p.mask_pitch = mask_pitch;
     p.O = O;
     p.o_fp32 = o_fp32 ? 1 : 0;
-    uint8_t* w = static_cast<uint8_t*>(workspace) + (off(workspace, 32) ? 16 : 0);
+    uint8_t* w = static_cast<uint8_t*>(workspace) + (misaligned(workspace, 32) ? 16 : 0);
     p.o_part = reinterpret_cast<float*>(w);
     p.ml_part = reinterpret_cast<float2*>(w + x.o_part);
     p.heads = reinterpret_cast<TreeHead*>(w + x.o_part + x.ml_part);
@@ -911,7 +904,7 @@ extern "C" dak_status dak_attn_tree(const void* Q, const dak_placement* KV, cons
     p.inv_G = (65536 + G - 1) / G;
     p.inv_mpt = (65536 + p.mpt - 1) / p.mpt;
     p.q_tokens = std::min(p.mpt, T);
-    p.wide = !off(O, 32);
+    p.wide = !misaligned(O, 32);
     p.L = KV->L;
     p.h_s = KV->h_s;
     p.host_requests = KV->h_s / KV->H_kv;
