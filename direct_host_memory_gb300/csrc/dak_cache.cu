@@ -97,7 +97,7 @@ __device__ __forceinline__ uint4 pack8(const float* y) {
 // (Axes), a pair's position is a load by its axis, under the inputs' too: 8192 tokens of three axes 35.0 us,
 // 512 drafted tokens fp32 5.6. Many such tokens of few heads are blocks' latencies one after the other, of which
 // one-warp blocks have more at a time: 8000 tokens of 2 query heads and a kv head 12.2 us, 15.8 with 128 threads
-// (D 64: 8.4 and 14.6). Half a head that turns, 8 and 4 heads: 17.0 us by pieces, 31.1 element by element. What is
+// (D 64: 8.4 and 14.6), where the bytes take 2.4 (1.2). Half a head that turns, 8 and 4 heads: 17.0 us by pieces, 31.1 element by element. What is
 // left to PART (halves that are not whole pieces) is bound by its instructions: 8192 tokens of 32 and 8 heads, 120 of 128
 // elements, 61.9 us with the other halves two at a time from shared memory, 68.6 one at a time, 81 with loads of their own.
 enum { kRopeSplit = 0, kRopeInterleaved = 1, kRopePart = 2, kRopePieces = 3 };
@@ -1034,7 +1034,8 @@ static dak_status append_rope(const dak_placement* KV, const dak_rope_plan* rope
     a.positions = positions;
     a.n = axes->n_axes;
     std::copy(axes->axis, axes->axis + 64, a.axis);
-    // many tokens of few heads: one warp each
+    // many tokens of few heads: one warp each (measured for positions of their own; one position a request keeps the
+    // blocks that it had)
     if (room == 1 && units <= kRopeFewUnits) return cuda_status(launch_rope<32>(p, a, D, in_fp32, grid, s));
     return cuda_status(launch_rope<kRopeThreads>(p, a, D, in_fp32, grid, s));
 }

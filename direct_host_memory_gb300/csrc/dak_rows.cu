@@ -44,8 +44,8 @@ struct CommitParams {
 // path[i] >= i: no row is written before the rows after it in the path have been read, if every
 // group of rows is read whole before it is written, and groups are taken in order. What a block waits
 // for are loads one after the other, the path and then the rows, which more slabs at once cover: with 64
-// threads 18 blocks fit an SM (256 requests of 8 kv heads, up to 48 of 64 drafts, tables: 12.1 us, 50 MB
-// of rows read and written in 7.4 at the copy rate; 13.3 with 128 threads, 17.4 with 256 and the tables behind
+// threads 18 blocks fit an SM (256 requests of 8 kv heads, up to 48 of 64 drafts, tables: 12.1 us, 55 MB
+// of rows read and written in 8.2 at the copy rate; 13.3 with 128 threads, 17.4 with 256 and the tables behind
 // the rows; four rows a thread 13.4). Where slabs are few enough for blocks of 256 to be there at once, and
 // paths long, those have fewer groups to take one after the other (up to 83 of 88 drafts of one request and 2 kv
 // heads 3.1 us, 7.9 with 64 threads).
@@ -168,7 +168,7 @@ struct __align__(16) ForkStretch {
 // are on their way while the one before is written. What bounds it: bytes (16 samples of two prompts over 7K:
 // 560 MB, 92.5 us, 81 at the copy rate); with many requests of many lengths the lists (about 4 us) and
 // units of few pieces (any of 61 over up to 3000 tracked rows 34.8 us, 22 at the copy rate, 3 of them for
-// the tables; all of 3001 rows 57.5, 45); a few beams the lists, one unit's way in and out: 7.2 us.
+// the tables; all of 3001 rows 57.5, 45); a few beams the lists, one unit's way in and out: 7.5 us.
 template <int D>
 __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -340,7 +340,7 @@ static int fork_plan_bytes(int B, int src_B) {
 
 template <int D>
 static cudaError_t launch_fork(ForkParams& p, cudaStream_t s) {
-    // Three CTAs an SM, or two or one where the lists take more room (16 beams of 8 kv heads over 850 rows 7.4 us with
+    // Three CTAs an SM, or two or one where the lists take more room (16 beams of 8 kv heads over 850 rows 7.5 us with
     // three, 8.6 with two; 16 samples of two prompts over 7K 91, 95, with four 98; any of 61 requests over up
     // to 3000 tracked rows 34.8, 35.5, 34.5).
     constexpr int kMost = 3, kRoom[kMost] = {220 * 1024, 110 * 1024, 73 * 1024};  // by CTAs an SM, from one on

@@ -1,8 +1,9 @@
 // Decode attention of a tree (or chain) of drafted tokens per request over a placed KV cache,
 // dak_attn_tree: o[b,t,h] = softmax(scale q[b,t,h] K^T) V over the rows before the drafts and those
 // drafts that the token's mask names. The tokens' query heads of one kv head are the rows of a tile, as
-// many whole tokens as fit in each 128-row half of it, so that the cache, which dak_attn streams once
-// per token, is streamed once for all of them; 64 keys a step on the tcgen05 tensor cores, as in the
+// many whole tokens as fit in each of its two 128-row halves, so that the cache, which dak_attn streams once
+// per token, is streamed once per tile: once for up to 256 rows a kv head, again for every further 256 (by the
+// memory that holds it, which for the host's slabs is the link); 64 keys a step on the tcgen05 tensor cores, as in the
 // prefix pass, whose comment says how (dak_prefix.cu; what both use: dak_umma_attn.cuh).
 // How work is cut: dak_tree.cuh. Up to 16 rows a kv head go to dak_tree_few.cu.
 //
@@ -14,11 +15,14 @@
 // and Q, scores and results one after the other.)
 //
 // What bounds it: with a half tile the cache's bytes (32 requests of 16 drafts and 32/8 heads over 7K to 8K:
-// 157 us, 148 at the copy rate; 32 rows 151, 128 rows 169). With two halves the tensor cores, which P in two
-// bf16 parts keeps busy for half as long again: those 48 requests 224 us, of which 13 are the merge, the
+// 158 to 161 us on several boxes, 148 at the copy rate; 32 rows 154, 128 rows 182). With two halves the tensor cores, which P in two
+// bf16 parts keeps busy for half as long again: those 48 requests 230 us, of which 13 are the merge, the
 // two products 85 at the rate of a large matrix product, 127 with the second part; the pipe is active 60% of
 // the time, and the rest is the chain from S to P.V that two streams do not cover. Small calls the start, the
-// first chunks and the merge's launch (one request of 8 drafts over 4K: 13.5 us, the merge 4.4 of them).
+// first chunks and the merge's launch (one request of 8 drafts over 4K: 13.8 us, the merge 4.4 of them). An fp32
+// output's sums, in registers, do not fit beside a step's scores: of heads of 128 594 bytes of a thread are spilled and
+// 840 read again (of heads of 64 152 and 216), and every step adds a whole product: in that batch 273 us with 32 rows, 311
+// with 64, 342 with 128. Host slabs are bound by the link (kTreeHostCtas).
 #include <algorithm>
 #include <cmath>
 
@@ -29,6 +33,11 @@ namespace dak {
 
 constexpr int kTreeSoftmax = 2 * 2 * 128;            // two streams, two threads a row
 constexpr int kTreeThreads = kTreeSoftmax + 4 * 32;  // and copies, scores, each stream's P.V
+// CTAs that read the host's slabs, by dak_attn's number. 32 requests over 7K to 8K, a quarter of the slabs on the host (249
+// MB): 4 drafts 1196 us with 16, 32, 64 and 152, 16 drafts 1200, 208 GB/s of the link, where one token by dak_attn takes
+// 1190; with 8 CTAs 1243 and 1202. With 3% there 16 drafts take 165, as with 8 to 152. What more rows a step cost shows
+// in fewer CTAs: 32 drafts of 8 heads a kv head over 2K 480 us, with 64 451; 64 of them, two tiles and so two passes over the
+// link, 942 and 894. Copies under way: two a CTA are enough (windows of 2 to 6 are within 1%, 1 is up to twice as slow).
 constexpr int kTreeHostCtas = 32;
 constexpr int kTreeMergeRows = 8;                 // a warp each
 

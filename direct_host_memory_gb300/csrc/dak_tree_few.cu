@@ -8,9 +8,10 @@
 //
 // What bounds it: the cache's bytes (32 requests of 4 drafts and 32/8 heads of 128 over 7K to 8K 150 us, 145 at
 // the copy rate; heads of 64 81 us, 73). Small calls the latency of the start, the first chunks, the warps' merge
-// and the pieces': one request over 4K 14 us, over 5 rows 7, 12 of 16/16 heads of 64 over up to 2.5K, fp32 output, 17 us (8.6). More
-// rows than 16 spill O^T and Q, of which five warps and two CTAs an SM leave 168 registers a thread: 24 rows of
-// heads of 64 102 us in that batch and 13.5 for one request (121 and 12.2 by tree_kernel), 32 rows 157 and 17.6.
+// and the pieces': one request over 4K 14 us, over 5 rows 7, 12 of 16/16 heads of 64 over up to 2.5K, fp32 output, 17 us (8.6). Five
+// warps and two CTAs an SM leave 168 registers a thread, of which 9 to 16 rows of heads of 128 spill a little (about 105
+// bytes; 152 us in that batch, fp32 output 165; heads of 64 do not, 81 and 94) and more rows O^T and Q: 24 rows of heads of
+// 64 102 us and 13.5 for one request (121 and 12.2 by tree_kernel), 32 rows 157 and 17.6.
 #include <algorithm>
 #include <atomic>
 

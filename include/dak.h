@@ -531,7 +531,8 @@ size_t dak_attn_workspace_bytes(int B, int H_q, int D, int n_split);
  * section 5). SDPA semantics for one query token per request, no mask:
  *   o[b,h] = softmax_j(scale * q[b,h] . k[b,g,j]) v[b,g,j],  g = h / (H_q / H_kv), j < L_b
  *   Q        : bf16 [B][H_q][D] (device).
- *   seq_lens : int32 [B] (device) with 1 <= L_b <= L, or NULL for all L.
+ *   seq_lens : int32 [B] (device) with 1 <= L_b <= L, or NULL for all L. Rows behind L_b may hold
+ *              anything.
  *   scale    : softmax scale; <= 0 means 1/sqrt(D).
  *   O        : bf16 [B][H_q][D] (device). An infinity or NaN in V of a row j < L_b makes that
  *              element infinite or NaN (NaN where the row's probability rounds to zero).
@@ -606,7 +607,9 @@ dak_status dak_attn_prefix(const void* Q, const dak_placement* KV, const int* se
  * wrote them from row L_b on),
  *     o[b,t,h] = softmax over j of scale * q[b,t,h] . k[b,g,j], applied to v[b,g,j],
  *     j < L_b, and j = L_b + s with bit s of mask[b][t] set.
- * The cache is read once for all T tokens.
+ * The token-heads of a kv head are the rows of tiles of two halves of 128, whole tokens in each, and a
+ * tile streams its kv head's rows: with G = H_q / H_kv every row is read once for up to
+ * 2 floor(128 / G) tokens, and ceil(T / (2 floor(128 / G))) times for T (T = 64, G = 8: twice).
  *   Q         : bf16 [B][T][H_q][D] (device), as dak_kv_append_rope leaves it. O: the same shape,
  *               bf16 or (o_fp32) fp32; rows of tokens t >= n_new[b] are left as they were. Must not
  *               overlap Q (DAK_ERR_INVALID).
