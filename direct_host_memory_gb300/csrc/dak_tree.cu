@@ -15,7 +15,7 @@
 // and Q, scores and results one after the other.)
 //
 // What bounds it: with a half tile the cache's bytes (32 requests of 16 drafts and 32/8 heads over 7K to 8K:
-// 158 to 161 us on several boxes, 148 at the copy rate; 32 rows 154, 128 rows 182). With two halves the tensor cores, which P in two
+// 158 to 161 us, 148 at the copy rate; 32 rows 154, 128 rows 182). With two halves the tensor cores, which P in two
 // bf16 parts keeps busy for half as long again: those 48 requests 230 us, of which 13 are the merge, the
 // two products 85 at the rate of a large matrix product, 127 with the second part; the pipe is active 60% of
 // the time, and the rest is the chain from S to P.V that two streams do not cover. Small calls the start, the
